@@ -10,7 +10,10 @@ Functions carry the C names: ``attn_fwd``, ``attn_fwd_partial``,
 ``attn_merge_states``, ``attn_fwd_splitkv``, ``attn_blocklist_normalize``,
 ``attn_blocklist_stats``, ``attn_fwd_blocksparse``, ``attn_select_blocks``,
 ``attn_bwd``, ``attn_bwd_blocksparse``, ``attn_bwd_noalloc``, ``attn_poll_status``,
-``attn_bwd_time_main``, ``attn_watchdog_selftest``, ``attn_probe_ex2_rate``.  Each
+``attn_bwd_time_main``, ``attn_watchdog_selftest``, ``attn_probe_ex2_rate``; with a sliding
+window and sinks ``attn_fwd_window``, ``attn_bwd_window``; over a paged cache
+``attn_decode_paged``, ``attn_kv_reserve``, ``attn_kv_write``, ``attn_kv_fork``,
+``attn_kv_free``, ``attn_kv_evict``, ``attn_kv_compact``, ``attn_kv_copy_pages``.  Each
 call runs on the
 device of its tensors and on that device's current stream.
 """
@@ -31,6 +34,9 @@ __all__ = [
     "attn_select_blocks_nnz", "attn_bwd", "attn_bwd_workspace_bytes", "attn_bwd_blocksparse",
     "attn_bwd_blocksparse_workspace_bytes", "attn_bwd_noalloc", "attn_poll_status",
     "attn_bwd_time_main", "attn_watchdog_selftest", "attn_probe_ex2_rate", "library",
+    "attn_fwd_window", "attn_bwd_window", "attn_bwd_window_workspace_bytes",
+    "attn_decode_paged", "attn_decode_paged_workspace_bytes", "attn_kv_reserve", "attn_kv_write",
+    "attn_kv_fork", "attn_kv_free", "attn_kv_evict", "attn_kv_compact", "attn_kv_copy_pages",
 ]
 
 OK = 0
@@ -40,6 +46,8 @@ ERR_BAD_BLOCKLIST = 3
 ERR_CUDA = 4
 ERR_TIMEOUT = 5
 ERR_WORKSPACE = 6
+ERR_BAD_PAGES = 7
+ERR_NO_PAGES = 8
 
 
 class AttnError(RuntimeError):
@@ -427,3 +435,10 @@ def attn_probe_ex2_rate(blocks: int, iters: int, sink: Optional[torch.Tensor] = 
 def attn_watchdog_selftest(timeout_cycles: int = 1 << 20, device=None) -> None:
     stream = torch.cuda.current_stream(device).cuda_stream
     _check(_lib.load().attn_watchdog_selftest(int(timeout_cycles), stream), "attn_watchdog_selftest")
+
+
+from ._window import (attn_bwd_window, attn_bwd_window_workspace_bytes,  # noqa: E402
+                      attn_fwd_window)
+from ._paged import (attn_decode_paged, attn_decode_paged_workspace_bytes,  # noqa: E402
+                     attn_kv_compact, attn_kv_copy_pages, attn_kv_evict, attn_kv_fork,
+                     attn_kv_free, attn_kv_reserve, attn_kv_write)

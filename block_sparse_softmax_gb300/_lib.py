@@ -64,6 +64,44 @@ _SIGNATURES = {
                                     _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
                                     _C.c_void_p, _C.c_void_p, _C.c_int, _C.c_int, _C.c_int,
                                     _C.c_int, _C.c_int, _C.c_float, _C.c_int, _C.c_void_p]),
+    "attn_fwd_window": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                   _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                   _C.c_float, _C.c_int64, _C.c_int64, _C.c_int64, _C.c_int64,
+                                   _C.c_void_p]),
+    "attn_bwd_window_workspace_bytes": (_C.c_size_t, [_C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                                      _C.c_int, _C.c_int, _C.c_int64, _C.c_int64,
+                                                      _C.c_int64, _C.c_int64]),
+    "attn_bwd_window": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                   _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                   _C.c_void_p, _C.c_size_t, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                   _C.c_int, _C.c_int, _C.c_float, _C.c_int64, _C.c_int64,
+                                   _C.c_int64, _C.c_int64, _C.c_void_p]),
+    "attn_decode_paged_workspace_bytes": (_C.c_size_t, [_C.c_int, _C.c_int, _C.c_int, _C.c_int]),
+    "attn_decode_paged": (_C.c_int, [_C.c_void_p, _C.c_int64, _C.c_void_p, _C.c_void_p, _C.c_int64,
+                                     _C.c_int64, _C.c_int, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                     _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                     _C.c_size_t, _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                     _C.c_int, _C.c_int, _C.c_float, _C.c_int64, _C.c_int64,
+                                     _C.c_void_p]),
+    "attn_kv_reserve": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                   _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_void_p]),
+    "attn_kv_write": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_int64, _C.c_int64, _C.c_void_p,
+                                 _C.c_void_p, _C.c_int64, _C.c_int64, _C.c_int, _C.c_void_p,
+                                 _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_int,
+                                 _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                 _C.c_void_p]),
+    "attn_kv_fork": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                _C.c_int, _C.c_void_p, _C.c_void_p, _C.c_int, _C.c_int, _C.c_int,
+                                _C.c_int, _C.c_void_p]),
+    "attn_kv_free": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_int,
+                                _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_void_p]),
+    "attn_kv_evict": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_int64, _C.c_int64,
+                                 _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_void_p]),
+    "attn_kv_compact": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                   _C.c_int, _C.c_int, _C.c_int, _C.c_void_p]),
+    "attn_kv_copy_pages": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_int64, _C.c_int64, _C.c_int,
+                                      _C.c_void_p, _C.c_void_p, _C.c_int, _C.c_void_p, _C.c_int,
+                                      _C.c_int, _C.c_int, _C.c_int, _C.c_void_p]),
     "attn_poll_status": (_C.c_int, [_C.c_void_p]),
     "attn_bwd_time_main": (_C.c_int, [_C.c_void_p, _C.c_void_p]),
     "attn_watchdog_selftest": (_C.c_int, [_C.c_ulonglong, _C.c_void_p]),

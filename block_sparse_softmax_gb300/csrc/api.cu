@@ -9,7 +9,7 @@
 #include <mutex>
 #include <vector>
 
-#include "common.cuh"
+#include "host.cuh"
 
 namespace bss {
 namespace {
@@ -41,6 +41,8 @@ int g_trace_cta = 0;
 void set_error(const char* where, cudaError_t e) {
   snprintf(g_last_error, sizeof(g_last_error), "%s: %s", where, cudaGetErrorString(e));
 }
+
+}  // namespace
 
 // Device address of the status word for the current device.
 attn_status_t status_word(int** out) {
@@ -130,9 +132,6 @@ attn_status_t make_map_f32(CUtensorMap* map, void* ptr, int B, int H, long long 
   return ATTN_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 // K/V heads: 1 <= Hkv <= H and Hkv divides H (query head h reads K/V head
 // h / (H / Hkv)).
 bool valid_kv_heads(int H, int Hkv) { return Hkv >= 1 && Hkv <= H && H % Hkv == 0; }
@@ -151,6 +150,13 @@ attn_status_t cuda_status(const char* where, cudaError_t e) {
   set_error(where, e);
   return ATTN_ERR_CUDA;
 }
+
+void bwd_main_events(cudaEvent_t* begin, cudaEvent_t* end) {
+  *begin = g_bwd_main_ev[0];
+  *end = g_bwd_main_ev[1];
+}
+
+namespace {
 
 attn_status_t fwd_common(const void* q, const void* k, const void* v, int B, int H, int Hkv,
                          int Lq, int Lk, int d, float scale, int causal, long long q_offset,
@@ -366,6 +372,8 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_CUDA: return "ATTN_ERR_CUDA";
     case ATTN_ERR_TIMEOUT: return "ATTN_ERR_TIMEOUT";
     case ATTN_ERR_WORKSPACE: return "ATTN_ERR_WORKSPACE";
+    case ATTN_ERR_BAD_PAGES: return "ATTN_ERR_BAD_PAGES";
+    case ATTN_ERR_NO_PAGES: return "ATTN_ERR_NO_PAGES";
     default: return "ATTN_ERR_UNKNOWN";
   }
 }

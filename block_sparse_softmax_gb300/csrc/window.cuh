@@ -1,0 +1,63 @@
+// The mask of the sliding window with sinks, shared by its forward and
+// backward kernels, and their launch parameters.
+//
+// With i a query row and k a key row of the launch and sh = q_offset - k_offset,
+// the pair's distance is t = i + sh - k, and the pair is allowed when
+//     t >= 0   and   (t < window   or   k < snk),
+// where snk counts the keys of this launch among the sequence's first `sinks`
+// positions (sinks - k_offset, clamped to [0, Lk]).
+#pragma once
+#include "common.cuh"
+
+namespace bss {
+
+struct WindowMask {
+  long long sh;        // q_offset - k_offset
+  long long window;    // >= 1
+  int snk;             // sink keys of this launch
+};
+
+struct WindowFwdParams {
+  int B, H, Hkv, Lq, Lk;
+  float scale_log2;
+  WindowMask w;
+  __nv_bfloat16* o;    // [B,H,Lq,d]
+  float* lse;          // [B,H,Lq]
+  int n_items;         // 128-row query tiles of every (b, h)
+  int* err;
+};
+
+// The key blocks (of 128) a query tile reads: the sink blocks [0, nsb) and the
+// window's blocks [wb0, wb0 + nwb), disjoint and in ascending order.
+struct WindowBlocks {
+  int nsb, wb0, nwb;
+  __device__ __forceinline__ int count() const { return nsb + nwb; }
+  __device__ __forceinline__ int at(int n) const { return n < nsb ? n : wb0 + (n - nsb); }
+};
+
+__device__ __forceinline__ WindowBlocks window_blocks(const WindowMask& w, int r0, int Lq, int Lk) {
+  WindowBlocks b{0, 0, 0};
+  if (r0 >= Lq || Lk <= 0) return b;
+  const long long last = static_cast<long long>(min(r0 + kTileM, Lq) - 1) + w.sh;   // last row's own key
+  if (last < 0) return b;
+  const int kmax = static_cast<int>(min(last, static_cast<long long>(Lk) - 1));
+  const long long lo = max(0ll, static_cast<long long>(r0) + w.sh - w.window + 1);
+  const int s_end = min(w.snk, kmax + 1);
+  const int sink_blocks = (s_end + kTileN - 1) / kTileN;
+  if (lo > kmax) {               // the window lies past the last key: sinks alone
+    b.nsb = sink_blocks;
+    return b;
+  }
+  b.wb0 = static_cast<int>(lo / kTileN);
+  b.nwb = kmax / kTileN - b.wb0 + 1;
+  b.nsb = min(sink_blocks, b.wb0);
+  return b;
+}
+
+}  // namespace bss
+
+namespace bss {
+// The mask of a launch with Lk keys; false for window < 1 or a negative argument (window_fwd.cu).
+bool window_mask(WindowMask* w, int Lk, int64_t window, int64_t sinks, int64_t q_offset,
+                 int64_t k_offset);
+}  // namespace bss

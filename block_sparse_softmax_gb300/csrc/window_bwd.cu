@@ -1,0 +1,1005 @@
+// attn_bwd_window: gradients of attn_fwd_window by recomputation.
+//
+// Mathematics (window.cuh has the mask; sums run over the allowed pairs):
+//   D_i  = dO_i . O_i
+//   P_ij = exp(scale q_i . k_j - LSE_i)
+//   dV_j = sum_i P_ij dO_i
+//   dS_ij = scale P_ij (dO_i . V_j - D_i)
+//   dK_j = sum_i dS_ij q_i,   dQ_i = sum_j dS_ij k_j
+//
+// The main kernel is the KV-owned traversal of the dense backward (one CTA per
+// 128-key tile, scores transposed so that a thread owns a key row, dK and dV
+// in tensor memory, dQ added into an fp32 accumulator by bulk reduce-adds)
+// over the query tiles that the window lets the key tile meet.
+//
+// A tile with a sink key meets every later query tile, window / 128 + 1 tiles
+// would be its neighbours' share: its walk is cut into segments of about that
+// share, each a CTA of its own that leaves fp32 parts of dK and dV in the
+// workspace; a last kernel adds the parts in segment order and rounds once.
+// The other tiles' walks are cut the same way when there are too few tiles to
+// fill the GPU.  dK and dV come out the same in every run; dQ's fp32 additions
+// come in the order the CTAs reach them, so its last bit may differ.
+#include <algorithm>
+
+#include "host.cuh"
+#include "window.cuh"
+
+namespace bss {
+namespace {
+
+struct WindowBwdParams {
+  int B, H, Hkv, Lq, Lk;
+  float scale, scale_log2;
+  WindowMask w;
+  const __nv_bfloat16* o;
+  const __nv_bfloat16* dout;
+  const float* lse;
+  float* delta;
+  float* dq_acc;        // fp32 [B,H,Lq,d]
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  float* part;          // fp32 [slot][dK, dV][128][d]: parts of the cut walks
+  int nk;               // key tiles
+  int nst;              // the first of them, which hold a sink key
+  int seg_s, seg_w;     // segments of a sink tile's walk and of another tile's
+  int head_group;       // K/V heads whose key tiles are launched together
+  int* err;
+};
+
+template <int D>
+struct WinBwdCfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kChunkBytes = kTileM * 128;
+  static constexpr int kTileBytes = kTileM * D * 2;
+  static constexpr int kStagesQ = 2;                     // Q_i ring depth (S^T(i+1) and dK(i) overlap)
+  static constexpr int kStagesDO = (D == 128) ? 1 : 2;    // dO_i ring depth (room for dQ staging)
+  static constexpr int kKOff = 0;
+  static constexpr int kVOff = kKOff + kTileBytes;
+  static constexpr int kQOff = kVOff + kTileBytes;
+  static constexpr int kDOOff = kQOff + kStagesQ * kTileBytes;
+  static constexpr int kDSOff = kDOOff + kStagesDO * kTileBytes;  // dS, 128 keys x 128 queries bf16
+  static constexpr int kDSBytes = kTileM * kTileN * 2;
+  static constexpr int kStageOff = kDSOff + kDSBytes;    // dQ staging: 128 rows x 64 fp32
+  static constexpr int kStageBytes = kTileM * 64 * 4;
+  static constexpr int kStatOff = kStageOff + kStageBytes;   // 2 x (lse2[128], delta[128])
+  static constexpr int kBarOff = kStatOff + 2 * 2 * 128 * 4;
+  static constexpr int kBarKV = 0;
+  static constexpr int kBarQFull = 1;
+  static constexpr int kBarQEmpty = kBarQFull + kStagesQ;
+  static constexpr int kBarDOFull = kBarQEmpty + kStagesQ;
+  static constexpr int kBarDOEmpty = kBarDOFull + kStagesDO;
+  static constexpr int kBarSFull = kBarDOEmpty + kStagesDO;   // S^T of a query tile in TMEM
+  static constexpr int kBarDPFull = kBarSFull + 1;            // [2]: dP^T query half h in TMEM
+  static constexpr int kBarPReady = kBarDPFull + 2;           // P^T written (S^T read)
+  static constexpr int kBarDSReady = kBarPReady + 1;          // dS in shared memory (dP^T read)
+  static constexpr int kBarDQFull = kBarDSReady + 1;
+  static constexpr int kBarDQFree = kBarDQFull + 1;           // [2]: dQ d-columns [64r, 64r+64) read
+  static constexpr int kBarDKVFull = kBarDQFree + 2;
+  static constexpr int kBarMmaDone = kBarDKVFull + 1;
+  static constexpr int kBarStat = kBarMmaDone + 1;     // [2]: LSE/D of a query tile staged
+  static constexpr int kBarStaged = kBarStat + 2;      // dQ round staged (CTA-wide drain)
+  static constexpr int kBarStageFree = kBarStaged + 1; // staging read by the reduce (CTA-wide drain)
+  static constexpr int kNumBars = kBarStageFree + 1;
+  // dQ drain: at d=128 each drain warp reduces its own 32 rows (no barrier
+  // among the four warps, which frees dQ's columns for dP^T sooner); at d=64,
+  // with one round per tile and a shorter period, one thread reduces all 128
+  // rows in two larger boxes after a CTA-wide barrier (measured faster there).
+  static constexpr bool kDrainPerWarp = (D == 128);
+  static constexpr int kDrainBoxRows = kDrainPerWarp ? 32 : 128;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  // Alignment slack for the 1024-byte aligned layout.  At d=128 the layout
+  // leaves less than 1024 bytes: the kernel then relies on the dynamic shared
+  // memory base being 1024-aligned and checks that before touching it.
+  static constexpr int kPayload = kMiscOff + 16;
+  static constexpr int kSlack = (kPayload + 1024 <= 232448) ? 1024 : 232448 - kPayload;
+  static constexpr int kSmemBytes = kPayload + kSlack;
+  static_assert(kPayload <= 232448, "backward shared memory exceeds the 227 KB a CTA may use");
+  static constexpr uint32_t kTmemCols = 512;
+  // TMEM columns: S^T (fp32) at [0,128) and dP^T at [128,256).  Half X of the
+  // P^T/dS warpgroups (query columns [64X, 64X+64)) writes its P^T (bf16
+  // pairs, 32 columns) to S^T columns [64X, 64X+32), inside the range it has
+  // itself already read.  dV and dK follow.  dQ of a query tile takes dP^T's
+  // columns at d=128 and columns of its own, [384,448), at d=64.
+  static constexpr uint32_t kColST = 0;
+  static constexpr uint32_t kColDPT = 128;
+  static constexpr uint32_t kColDV = 256;
+  static constexpr uint32_t kColDK = 256 + D;
+  static constexpr uint32_t kColDQ = (D == 128) ? kColDPT : 384;
+  static constexpr bool kDQOverDP = (kColDQ == kColDPT);
+  // A operand address of query k-step kk (16 queries) inside P^T
+  static __device__ __forceinline__ uint32_t pcol(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }
+  static constexpr int kThreads = 512;
+};
+
+// Register split per warpgroup (setmaxnreg): warpgroup 0 (TMA, MMA, two idle
+// warps) kLow, the P/dS warpgroups 1-2 kMid (each thread keeps 64 fp32 P
+// values between its two phases), the dQ warpgroup 3 kHigh.  96/160/160/96
+// compiles every instantiation without register spills (88/160/160/104
+// spilled a few bytes at d=128 and measured 1.9 % slower there).  Each SM
+// sub-partition holds one warp of every warpgroup: kLow + 2 kMid + kHigh <= 512
+// registers a lane, and the split fits the 512 * 128 registers the launch
+// holds (launch_main refuses to launch if ptxas gave the kernel fewer than 128
+// a thread).
+template <int D>
+struct WinBwdRegs {
+  static constexpr uint32_t kLow = 96;
+  static constexpr uint32_t kMid = 160;
+  static constexpr uint32_t kHigh = 96;
+  static constexpr uint32_t kLaunchRegs = 128;
+  static_assert(kLow + 2 * kMid + kHigh <= 512, "register split exceeds an SM sub-partition");
+  static_assert(128 * (kLow + 2 * kMid + kHigh) <= 512 * kLaunchRegs, "register split exceeds the launch");
+};
+
+
+// CTA x: the sink tiles' segments first (each at least as long as any other
+// walk), then the other key tiles in groups of K/V heads, tile-major inside a
+// group, so that the running CTAs' Q, dO and dQ accumulator stay in L2.
+struct WindowBwdCta {
+  int bh, j, seg, nseg, slot;
+};
+__device__ __forceinline__ WindowBwdCta window_bwd_cta(int x, const WindowBwdParams& p) {
+  WindowBwdCta c;
+  const int BH = p.B * p.Hkv;
+  const int n_sink = BH * p.nst * p.seg_s;
+  if (x < n_sink) {
+    c.nseg = p.seg_s;
+    c.slot = x;
+    c.seg = x % p.seg_s;
+    const int t = x / p.seg_s;
+    c.bh = t / p.nst;
+    c.j = t - c.bh * p.nst;
+    return c;
+  }
+  const int y = x - n_sink;
+  const int n = p.nk - p.nst;
+  c.nseg = p.seg_w;
+  c.seg = y % p.seg_w;
+  const int z = y / p.seg_w;
+  const int grp = z / (p.head_group * n);
+  const int gsz = min(p.head_group, BH - grp * p.head_group);
+  const int within = z - grp * p.head_group * n;
+  const int jj = within / gsz;
+  c.bh = grp * p.head_group + (within - jj * gsz);
+  c.j = p.nst + jj;
+  c.slot = (p.seg_s > 1 ? n_sink : 0) + (c.bh * n + jj) * p.seg_w + c.seg;
+  return c;
+}
+
+// The (query head of the group, query tile) pairs of a CTA's walk: its segment
+// of the tiles first .. first + nt - 1 of every query head, head by head.
+struct WindowQWalk {
+  int first, nt, n_it;
+  int g0, i0;
+  __device__ __forceinline__ void start(int& g, int& i) const {
+    g = g0;
+    i = i0;
+  }
+  __device__ __forceinline__ void advance(int& g, int& i) const {
+    if (++i == first + nt) {
+      i = first;
+      ++g;
+    }
+  }
+};
+__device__ __forceinline__ WindowQWalk window_bwd_walk(const WindowBwdCta& c, const WindowBwdParams& p) {
+  WindowQWalk w{0, 0, 0, 0, 0};
+  const int k0 = c.j * kTileN;
+  const int k1 = min(k0 + kTileN, p.Lk) - 1;
+  const long long lo = max(0ll, static_cast<long long>(k0) - p.w.sh);
+  long long hi = p.Lq - 1;
+  if (c.j >= p.nst) hi = min(hi, static_cast<long long>(k1) - p.w.sh + p.w.window - 1);
+  if (lo > hi) return w;
+  w.first = static_cast<int>(lo / kTileM);
+  w.nt = static_cast<int>(hi / kTileM) - w.first + 1;
+  const long long total = static_cast<long long>(w.nt) * (p.H / p.Hkv);
+  const long long x0 = total * c.seg / c.nseg;
+  const long long x1 = total * (c.seg + 1) / c.nseg;
+  w.n_it = static_cast<int>(x1 - x0);
+  w.g0 = static_cast<int>(x0 / w.nt);
+  w.i0 = w.first + static_cast<int>(x0 - static_cast<long long>(w.g0) * w.nt);
+  return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
+    attn_bwd_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                         const __grid_constant__ CUtensorMap tmDQ, const WindowBwdParams p) {
+  using C = WinBwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  {
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+    if (pad > static_cast<uint32_t>(C::kSlack)) {     // layout would not fit: report, touch nothing
+      if (threadIdx.x == 0) record_error(p.err, ATTN_ERR_UNSUPPORTED);
+      return;
+    }
+  }
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::kBarOff + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+  float* stats = reinterpret_cast<float*>(smem + C::kStatOff);
+
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  const int tid = static_cast<int>(threadIdx.x);
+  if (*reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
+
+  const int Lk = p.Lk, Lq = p.Lq;
+  const WindowBwdCta cta = window_bwd_cta(static_cast<int>(blockIdx.x), p);
+  const int j = cta.j;                            // key tile owned by this CTA
+  const int bh = cta.bh;                          // (b, K/V head)
+  const int G = p.H / p.Hkv;
+  const int b = bh / p.Hkv;
+  const int h = bh - b * p.Hkv;                   // K/V head
+  const int hq0 = h * G;                          // first query head of the group
+  const int bhq0 = b * p.H + hq0;
+  const WindowQWalk walk = window_bwd_walk(cta, p);
+  const int n_it = walk.n_it;                     // query tiles met, over the group's heads
+
+  if (tid == 0) {
+    mbar_init(bar(C::kBarKV), 1);
+    for (int s = 0; s < C::kStagesQ; ++s) {
+      mbar_init(bar(C::kBarQFull + s), 1);
+      mbar_init(bar(C::kBarQEmpty + s), 1);
+    }
+    for (int s = 0; s < C::kStagesDO; ++s) {
+      mbar_init(bar(C::kBarDOFull + s), 1);
+      mbar_init(bar(C::kBarDOEmpty + s), 1);
+    }
+    mbar_init(bar(C::kBarSFull), 1);
+    mbar_init(bar(C::kBarDPFull), 1);
+    mbar_init(bar(C::kBarDPFull + 1), 1);
+    mbar_init(bar(C::kBarPReady), 256);
+    mbar_init(bar(C::kBarDSReady), 256);
+    mbar_init(bar(C::kBarDQFull), 1);
+    mbar_init(bar(C::kBarDQFree), 128);
+    mbar_init(bar(C::kBarDQFree + 1), 128);
+    mbar_init(bar(C::kBarStaged), 128);
+    mbar_init(bar(C::kBarStageFree), 1);
+    mbar_init(bar(C::kBarDKVFull), 1);
+    mbar_init(bar(C::kBarMmaDone), 1);
+    mbar_init(bar(C::kBarStat + 0), 128);
+    mbar_init(bar(C::kBarStat + 1), 128);
+    *abort_flag = 0;
+    fence_barrier_init();
+    // K_j and V_j go out at once: their load overlaps the rest of the set-up
+    mbar_arrive_expect_tx(bar(C::kBarKV), 2 * C::kTileBytes);
+    for (int c = 0; c < C::kChunks; ++c) {
+      tma_load_4d(sbase + C::kKOff + c * C::kChunkBytes, &tmK, bar(C::kBarKV), c * 64, j * kTileN, h, b);
+      tma_load_4d(sbase + C::kVOff + c * C::kChunkBytes, &tmV, bar(C::kBarKV), c * 64, j * kTileN, h, b);
+    }
+  }
+  if (warp == 0) {
+    tmem_alloc(sbase + C::kMiscOff, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 4) {
+  regs_set<WinBwdRegs<D>::kLow, WinBwdRegs<D>::kLaunchRegs>();
+  if (warp == 0) {
+    // =================== TMA producer ===================
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmDO);
+      int nq_ld = 0, ndo_ld = 0;
+      int g, i;
+      walk.start(g, i);
+      for (int it = 0; it < n_it; walk.advance(g, i), ++it) {
+        const int row = i * kTileM;
+        const int hq = hq0 + g;
+        const int sq = it % C::kStagesQ;
+        if (it >= C::kStagesQ &&
+            !wait_bar(bar(C::kBarQEmpty + sq), ((it / C::kStagesQ) & 1) ^ 1, abort_flag, p.err))
+          break;
+        mbar_arrive_expect_tx(bar(C::kBarQFull + sq), C::kTileBytes);
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_4d(sbase + C::kQOff + sq * C::kTileBytes + c * C::kChunkBytes, &tmQ,
+                      bar(C::kBarQFull + sq), c * 64, row, hq, b);
+        ++nq_ld;
+        const int sd = it % C::kStagesDO;
+        if (it >= C::kStagesDO &&
+            !wait_bar(bar(C::kBarDOEmpty + sd), ((it / C::kStagesDO) & 1) ^ 1, abort_flag, p.err))
+          break;
+        mbar_arrive_expect_tx(bar(C::kBarDOFull + sd), C::kTileBytes);
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_4d(sbase + C::kDOOff + sd * C::kTileBytes + c * C::kChunkBytes, &tmDO,
+                      bar(C::kBarDOFull + sd), c * 64, row, hq, b);
+        ++ndo_ld;
+      }
+      // Drain: every load issued has landed before the CTA may exit.
+      drain_bar(bar(C::kBarKV), 0);
+      for (int x = max(0, nq_ld - C::kStagesQ); x < nq_ld; ++x)
+        drain_bar(bar(C::kBarQFull + x % C::kStagesQ), (x / C::kStagesQ) & 1);
+      for (int x = max(0, ndo_ld - C::kStagesDO); x < ndo_ld; ++x)
+        drain_bar(bar(C::kBarDOFull + x % C::kStagesDO), (x / C::kStagesDO) & 1);
+    }
+  } else if (warp == 1) {
+    // =================== MMA issuer (one thread) ===================
+    // Issue order per query tile i: dV(i), S^T(i+1), dQ(i), dK(i), dP^T(i+1).
+    // Every overwrite of TMEM or shared memory is ordered behind the MMAs that
+    // read the old contents by issue order (the tensor core executes one
+    // thread's MMAs in order) or by the barrier it waits on:
+    //   S^T(i+1) over P^T(i): after dV(i);  P^T(i+1) written after S^T(i+1)
+    //   completes; dQ(i) over dP^T(i): after ds_ready(i) (dP^T read);
+    //   dP^T(i+1) over dQ(i): after dq_free(i); dS(i+1) written after
+    //   dP^T(i+1) completes, so after dQ(i) and dK(i) read dS(i).
+    if (lane == 0) {
+      constexpr uint32_t kIdescT = idesc_bf16_f32(kTileM, kTileN, false, false);  // S^T, dP^T
+      constexpr uint32_t kIdescKV = idesc_bf16_f32(kTileM, D, false, true);       // dV, dK
+      constexpr uint32_t kIdescQ = idesc_bf16_f32(kTileM, D, true, true);         // dQ
+      const uint32_t ka = sbase + C::kKOff, va = sbase + C::kVOff, dsa = sbase + C::kDSOff;
+      auto qaddr = [&](int it) { return sbase + C::kQOff + (it % C::kStagesQ) * C::kTileBytes; };
+      auto doaddr = [&](int it) { return sbase + C::kDOOff + (it % C::kStagesDO) * C::kTileBytes; };
+      // S^T(it) = K_j Q^T
+      auto issue_s = [&](int it) -> bool {
+        if (!wait_bar(bar(C::kBarQFull + it % C::kStagesQ), (it / C::kStagesQ) & 1, abort_flag, p.err))
+          return false;
+        tc_fence_after();
+        const uint32_t qa = qaddr(it);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+          mma_ss(tmem + C::kColST, sdesc_sw128(ka + off, 16, 1024), sdesc_sw128(qa + off, 16, 1024),
+                 kIdescT, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(C::kBarSFull));
+        return true;
+      };
+      // dP^T(it) = V_j dO^T, in two halves of 64 queries (N = 64) when dQ
+      // shares dP^T's columns: half h overwrites dQ's d-columns [64h, 64h+64),
+      // which round h of the drain frees, and feeds P/dS half X = h alone.
+      constexpr uint32_t kIdescTHalf = idesc_bf16_f32(kTileM, kTileN / 2, false, false);
+      auto issue_dp_half = [&](int it, int h) -> bool {
+        if (h == 0) {
+          if (!wait_bar(bar(C::kBarDOFull + it % C::kStagesDO), (it / C::kStagesDO) & 1, abort_flag,
+                        p.err))
+            return false;
+        }
+        tc_fence_after();
+        const uint32_t doa = doaddr(it) + h * (kTileN / 2) * 128;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+          mma_ss(tmem + C::kColDPT + h * (kTileN / 2), sdesc_sw128(va + off, 16, 1024),
+                 sdesc_sw128(doa + off, 16, 1024), kIdescTHalf, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(C::kBarDPFull + h));
+        return true;
+      };
+      constexpr bool kDPHalves = C::kDQOverDP;
+      auto issue_dp = [&](int it) -> bool {
+        if (kDPHalves) return issue_dp_half(it, 0) && issue_dp_half(it, 1);
+        if (!wait_bar(bar(C::kBarDOFull + it % C::kStagesDO), (it / C::kStagesDO) & 1, abort_flag, p.err))
+          return false;
+        tc_fence_after();
+        const uint32_t doa = doaddr(it);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+          mma_ss(tmem + C::kColDPT, sdesc_sw128(va + off, 16, 1024), sdesc_sw128(doa + off, 16, 1024),
+                 kIdescT, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(C::kBarDPFull));
+        mma_commit(bar(C::kBarDPFull + 1));
+        return true;
+      };
+      bool ok = wait_bar(bar(C::kBarKV), 0, abort_flag, p.err);
+      if (ok && n_it > 0) ok = issue_s(0) && issue_dp(0);
+      int g, i;
+      walk.start(g, i);
+      for (int it = 0; it < n_it && ok; walk.advance(g, i), ++it) {
+        const bool more = it + 1 < n_it;               // another query tile follows
+        // dV += P^T dO_i  (K dimension = the 128 queries)
+        if (!wait_bar(bar(C::kBarPReady), it & 1, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint32_t doa = doaddr(it);
+#pragma unroll
+        for (int kk = 0; kk < kTileM / 16; ++kk) {
+          mma_ts(tmem + C::kColDV, tmem + C::kColST + C::pcol(kk),
+                 sdesc_sw128(doa + kk * 2048, C::kChunkBytes, 1024), kIdescKV,
+                 (it > 0 || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(bar(C::kBarDOEmpty + it % C::kStagesDO));   // dP^T(it) and dV(it) read dO_i
+        if (more && !issue_s(it + 1)) break;
+        // the P/dS warps run for a while: poll gently so that the issue slots
+        // they share with this warp stay theirs
+        if (!wait_bar_relaxed(bar(C::kBarDSReady), it & 1, abort_flag, p.err)) break;
+        tc_fence_after();
+        // dQ_i = dS K_j  (M = queries, N = d, K dimension = the 128 keys); with
+        // columns of its own, only after the previous dQ has been read
+        if (!C::kDQOverDP && it > 0 && !wait_bar(bar(C::kBarDQFree), (it - 1) & 1, abort_flag, p.err))
+          break;
+#pragma unroll
+        for (int kk = 0; kk < kTileN / 16; ++kk) {
+          mma_ss(tmem + C::kColDQ, sdesc_sw128(dsa + kk * 2048, C::kChunkBytes, 1024),
+                 sdesc_sw128(ka + kk * 2048, C::kChunkBytes, 1024), kIdescQ, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(C::kBarDQFull));
+        // dK += dS^T Q_i  (dS^T: the same tile read K-major; K dimension = queries)
+        const uint32_t qa = qaddr(it);
+#pragma unroll
+        for (int kk = 0; kk < kTileM / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+          mma_ss(tmem + C::kColDK, sdesc_sw128(dsa + off, 16, 1024),
+                 sdesc_sw128(qa + kk * 2048, C::kChunkBytes, 1024), kIdescKV,
+                 (it > 0 || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(bar(C::kBarQEmpty + it % C::kStagesQ));
+        if (more) {
+          if (kDPHalves) {
+            // dP^T(i+1) over dQ(i): each half once its columns have been read out
+            if (!wait_bar(bar(C::kBarDQFree), it & 1, abort_flag, p.err)) break;
+            if (!issue_dp_half(it + 1, 0)) break;
+            if (!wait_bar(bar(C::kBarDQFree + 1), it & 1, abort_flag, p.err)) break;
+            if (!issue_dp_half(it + 1, 1)) break;
+          } else if (C::kDQOverDP) {
+            // one N=128 group once both halves of dQ's columns are read out
+            if (!wait_bar(bar(C::kBarDQFree), it & 1, abort_flag, p.err)) break;
+            if (!wait_bar(bar(C::kBarDQFree + 1), it & 1, abort_flag, p.err)) break;
+            if (!issue_dp(it + 1)) break;
+          } else {
+            if (!issue_dp(it + 1)) break;
+          }
+        }
+      }
+      mma_commit(bar(C::kBarDKVFull));
+      mma_commit(bar(C::kBarMmaDone));
+      drain_bar(bar(C::kBarMmaDone), 0);   // every MMA issued has completed
+    }
+  }
+  } else if (warp < 12) {
+    regs_set<WinBwdRegs<D>::kMid, WinBwdRegs<D>::kLaunchRegs>();
+    // =================== P^T / dS: two warpgroups, thread = key row ===================
+    // Warpgroup X (warps 4-7: X = 0, warps 8-11: X = 1) handles query columns
+    // [64X, 64X + 64), 16 at a time.  Phase 1 turns S^T into P (kept in fp32
+    // registers) and writes P^T (bf16) to columns [64X + 8c, 64X + 8c + 8) of
+    // chunk c, which this half has already read; phase 2 forms dS from P and
+    // dP^T and stores it in shared memory.
+    const int X = (warp - 4) >> 2;
+    const int wq = warp & 3;
+    const int kr = wq * 32 + lane;
+    const int key = j * kTileN + kr;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tST = tmem + lane_base + C::kColST;
+    const uint32_t tDPT = tmem + lane_base + C::kColDPT;
+    const float sl2 = p.scale_log2;
+    const float scale = p.scale;
+    const float INF = __int_as_float(0x7f800000);
+    uint8_t* ds_row = smem + C::kDSOff + X * C::kChunkBytes + kr * 128;   // this key's dS row
+    // statistics of query tile i of query head hq0 + g, negated so that
+    // P = ex2(S sl2 + nl2) and dP - D = dP scale + ndl are single FMAs
+    auto load_stats = [&](int g, int i, float& nl2, float& ndl) {
+      const int q = i * kTileM + kr;
+      if (q < Lq) {
+        const size_t stat = static_cast<size_t>(bhq0 + g) * Lq + q;
+        const float lse = __ldg(p.lse + stat);
+        nl2 = (lse == -INF) ? -INF : -(lse * kLog2e);  // an empty row contributes nothing
+        ndl = -(__ldg(p.delta + stat) * scale);
+      } else {
+        nl2 = -INF;
+        ndl = 0.f;
+      }
+    };
+    if (X == 0) {
+      float l2 = -INF, dl = 0.f;
+      int gf, tf;
+      walk.start(gf, tf);
+      if (n_it > 0) load_stats(gf, tf, l2, dl);
+      stats[kr] = l2;
+      stats[128 + kr] = dl;
+      mbar_arrive(bar(C::kBarStat + 0));
+    }
+    // Buffer (it & 1) holds the statistics of the it-th query tile met (minus
+    // the LSE in log2 units, minus scale * D).  It is rewritten (for tile it + 2) at the end of tile
+    // it + 1 by half 0; by then dP^T(it + 1) has been issued, which waited for
+    // dS(it) of both halves, so nobody reads it for tile it any more.
+    bool ok = true;
+    int g, i;
+    walk.start(g, i);
+    for (int it = 0; it < n_it; walk.advance(g, i), ++it) {
+      const float* lse2 = stats + (it & 1) * 256 + 64 * X;
+      const float* dlt = lse2 + 128;
+      float l2n = 0.f, dln = 0.f;
+      if (X == 0 && it + 1 < n_it) {
+        int gn = g, in = i;
+        walk.advance(gn, in);
+        load_stats(gn, in, l2n, dln);
+      }
+      if (!wait_bar(bar(C::kBarSFull), it & 1, abort_flag, p.err) ||
+          !wait_bar(bar(C::kBarStat + (it & 1)), (it >> 1) & 1, abort_flag, p.err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // element mask, in query index c of the tile: allowed are qlo <= c <= qhi
+      // (a sink key has no upper limit, a key past the last one nothing); the
+      // ragged tail (query >= Lq) has -lse2 = -inf, so P is 0 there already
+      const long long own = static_cast<long long>(key) - p.w.sh - static_cast<long long>(i) * kTileM;
+      const int qlo = key < Lk ? static_cast<int>(max(0ll, min(128ll, own))) : 128;
+      const int qhi = key < p.w.snk ? 127 : static_cast<int>(max(-1ll, min(127ll, own + p.w.window - 1)));
+      const bool need_mask = __any_sync(0xFFFFFFFFu, qlo > 0 || qhi < 127);
+      // ---- phase 1: P (four chunks of 16 queries; chunk c+1's TMEM load is in
+      // flight while chunk c is computed) ----
+      float pf[4][16];
+      {
+        uint32_t sv[2][16];
+        tmem_ld16(tST + 64 * X, sv[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int cur = c & 1;
+          const int col = 64 * X + 16 * c;                 // first query of the chunk
+          tmem_ld_wait16(sv[cur]);
+          if (c + 1 < 4) tmem_ld16(tST + col + 16, sv[cur ^ 1]);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(lse2 + 16 * c + e);
+            float x[4];
+            ffma2(x[0], x[1], __uint_as_float(sv[cur][e]), __uint_as_float(sv[cur][e + 1]), sl2,
+                  sl2, l4.x, l4.y);
+            ffma2(x[2], x[3], __uint_as_float(sv[cur][e + 2]), __uint_as_float(sv[cur][e + 3]),
+                  sl2, sl2, l4.z, l4.w);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) pf[c][e + u] = ex2(x[u]);
+          }
+          if (need_mask) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (col + e < qlo || col + e > qhi) pf[c][e] = 0.f;
+          }
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(pf[c][2 * e], pf[c][2 * e + 1]);
+          tmem_st8(tST + 64 * X + 8 * c, pk);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bar(C::kBarPReady));
+      // ---- phase 2: dS = P o (dP - D), into shared memory ----
+      if (!wait_bar(bar(C::kBarDPFull + X), it & 1, abort_flag, p.err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      {
+        uint32_t dv[2][16];
+        tmem_ld16(tDPT + 64 * X, dv[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int cur = c & 1;
+          const int col = 64 * X + 16 * c;
+          tmem_ld_wait16(dv[cur]);
+          if (c + 1 < 4) tmem_ld16(tDPT + col + 16, dv[cur ^ 1]);
+          uint32_t dk[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 d4 = *reinterpret_cast<const float4*>(dlt + 16 * c + e);
+            float ds[4];
+            ffma2(ds[0], ds[1], __uint_as_float(dv[cur][e]), __uint_as_float(dv[cur][e + 1]), scale,
+                  scale, d4.x, d4.y);
+            ffma2(ds[2], ds[3], __uint_as_float(dv[cur][e + 2]), __uint_as_float(dv[cur][e + 3]),
+                  scale, scale, d4.z, d4.w);
+            fmul2(ds[0], ds[1], pf[c][e], pf[c][e + 1], ds[0], ds[1]);
+            fmul2(ds[2], ds[3], pf[c][e + 2], pf[c][e + 3], ds[2], ds[3]);
+            if (need_mask) {          // a masked pair sends nothing, whatever dP and D hold
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (col + e + u < qlo || col + e + u > qhi) ds[u] = 0.f;
+            }
+            dk[e / 2] = pack_bf16(ds[0], ds[1]);
+            dk[e / 2 + 1] = pack_bf16(ds[2], ds[3]);
+          }
+          // one 128-byte row per key (queries 64X .. 64X+63), 16-byte units of
+          // 8 queries swizzled by the row index: the K-major tile layout
+#pragma unroll
+          for (int u2 = 0; u2 < 2; ++u2) {
+            const int unit = 2 * c + u2;
+            *reinterpret_cast<uint4*>(ds_row + ((unit ^ (kr & 7)) * 16)) =
+                make_uint4(dk[4 * u2 + 0], dk[4 * u2 + 1], dk[4 * u2 + 2], dk[4 * u2 + 3]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(bar(C::kBarDSReady));
+      if (X == 0) {
+        // statistics of the next query tile
+        float* nxt = stats + ((it + 1) & 1) * 256;
+        nxt[kr] = l2n;
+        nxt[128 + kr] = dln;
+        mbar_arrive(bar(C::kBarStat + ((it + 1) & 1)));
+      }
+    }
+    // ---- epilogue: half 0 stores dK rows, half 1 stores dV rows ----
+    if (ok) ok = wait_bar(bar(C::kBarDKVFull), 0, abort_flag, p.err);
+    tc_fence_after();
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (ok) {
+      // one 128-byte line (64 columns as bf16 pairs) of this thread's key row
+      // at a time; after the octet transpose every store writes whole lines
+      const uint32_t tsrc = tmem + lane_base + (X == 0 ? C::kColDK : C::kColDV);
+      const int wrow0 = j * kTileN + wq * 32;          // this warp's first key row
+      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, key < Lk);
+      uint8_t* base = reinterpret_cast<uint8_t*>((X == 0 ? p.dk : p.dv) +
+                                                 (static_cast<size_t>(bh) * Lk + wrow0) * D);
+      // a cut walk leaves its fp32 part [128][D] of dK and of dV in the workspace
+      uint8_t* part = reinterpret_cast<uint8_t*>(
+          p.part + ((static_cast<size_t>(cta.slot) * 2 + X) * kTileN + wq * 32) * D);
+#pragma unroll 1
+      for (int g2 = 0; g2 < D / 64; ++g2) {
+        uint32_t a[32], c[32];
+        if (n_it > 0) {
+          tmem_ld32(tsrc + g2 * 64, a);
+          tmem_ld32(tsrc + g2 * 64 + 32, c);
+          tmem_ld_wait(a);
+          tmem_ld_wait(c);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = c[e] = 0u;
+        }
+        if (cta.nseg > 1) {
+          transpose_octets(a, lane);
+          store_octet_lines(a, part + g2 * 256, D * 4, 0xFFFFFFFFu, lane);
+          transpose_octets(c, lane);
+          store_octet_lines(c, part + g2 * 256 + 128, D * 4, 0xFFFFFFFFu, lane);
+        } else {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            w[k] = pack_bf16(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1]));
+            w[16 + k] = pack_bf16(__uint_as_float(c[2 * k]), __uint_as_float(c[2 * k + 1]));
+          }
+          transpose_octets(w, lane);
+          store_octet_lines(w, base + g2 * 128, D * 2, valid, lane);
+        }
+      }
+    }
+  } else {
+    regs_set<WinBwdRegs<D>::kHigh, WinBwdRegs<D>::kLaunchRegs>();
+    // =================== dQ: warps 12-15, thread = query row ===================
+    // Each round moves 64 d-columns of the tile's dQ from TMEM to a
+    // 128-byte-swizzled fp32 staging buffer, from which bulk tensor
+    // reduce-adds (boxes of 32 columns) add it into the fp32 accumulator in
+    // global memory; dQ's TMEM columns of a round are handed back right after
+    // their reads.  Per-warp drain (d=128): each warp reduces its own 32 rows
+    // and reuses its staging rows once its own previous reduces have read them
+    // (bulk groups are per thread).  CTA-wide drain (d=64): one thread reduces
+    // the 128 rows after all four warps have staged them.  (On the bench
+    // shapes, vector red.global from registers, for all of dQ or for one
+    // round, measured slower: the reduce stream sets the pace.)
+    constexpr bool kPerWarp = C::kDrainPerWarp;
+    const int wq = warp & 3;
+    const int qr = wq * 32 + lane;
+    const uint32_t tDQ = tmem + (static_cast<uint32_t>(wq * 32) << 16) + C::kColDQ;
+    constexpr int kRounds = D / 64;
+    constexpr int kBoxBytes = kTileM * 32 * 4;    // 128 rows x 32 fp32: one box column
+    static_assert(2 * kBoxBytes == C::kStageBytes, "two box columns fill the staging buffer");
+    const uint32_t stage = sbase + C::kStageOff + (kPerWarp ? wq * 32 * 128 : 0);
+    uint8_t* stage_ptr = smem + C::kStageOff;
+    bool ok = true;
+    int g = 0;                                    // staged rounds (CTA-wide drain)
+    int gq, i;                                    // query head of the group, query tile
+    walk.start(gq, i);
+    for (int it = 0; it < n_it && ok; walk.advance(gq, i), ++it) {
+      if (!wait_bar_relaxed(bar(C::kBarDQFull), it & 1, abort_flag, p.err)) break;
+      tc_fence_after();
+      for (int r = 0; r < kRounds; ++r, ++g) {
+        uint32_t v0[32], v1[32];
+        tmem_ld32(tDQ + 64 * r, v0);
+        tmem_ld32(tDQ + 64 * r + 32, v1);
+        tmem_ld_wait(v0);
+        tmem_ld_wait(v1);
+        // d-columns [64r, 64r + 64) of this tile are read (at d=128 dP^T's
+        // half r may overwrite them; at d=64 the next dQ may)
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarDQFree + r));
+        // the staging rows must have been read by the reduces that used them
+        if constexpr (kPerWarp) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+        } else if (g > 0) {
+          if (qr == 0) {
+            bulk_wait_read_all();
+            mbar_arrive(bar(C::kBarStageFree));
+          }
+          if (!wait_bar(bar(C::kBarStageFree), (g - 1) & 1, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {               // box column 0: columns 0..31 of the round
+          *reinterpret_cast<uint4*>(stage_ptr + qr * 128 + ((u ^ (qr & 7)) * 16)) =
+              make_uint4(v0[4 * u], v0[4 * u + 1], v0[4 * u + 2], v0[4 * u + 3]);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {               // box column 1: columns 32..63
+          *reinterpret_cast<uint4*>(stage_ptr + kBoxBytes + qr * 128 + ((u ^ (qr & 7)) * 16)) =
+              make_uint4(v1[4 * u], v1[4 * u + 1], v1[4 * u + 2], v1[4 * u + 3]);
+        }
+        fence_proxy_async_smem();
+        if constexpr (kPerWarp) {
+          __syncwarp();
+          if (lane == 0) {
+            const int row = i * kTileM + wq * 32;
+            tma_reduce_add_4d(&tmDQ, stage, 64 * r, row, hq0 + gq, b);
+            tma_reduce_add_4d(&tmDQ, stage + kBoxBytes, 64 * r + 32, row, hq0 + gq, b);
+            bulk_commit_group();
+          }
+        } else {
+          mbar_arrive(bar(C::kBarStaged));
+          if (qr == 0) {
+            if (!wait_bar(bar(C::kBarStaged), g & 1, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
+            const int row = i * kTileM;
+            tma_reduce_add_4d(&tmDQ, stage, 64 * r, row, hq0 + gq, b);
+            tma_reduce_add_4d(&tmDQ, stage + kBoxBytes, 64 * r + 32, row, hq0 + gq, b);
+            bulk_commit_group();
+          }
+        }
+        __syncwarp();                               // reconverge before the next TMEM load
+      }
+    }
+    if (kPerWarp ? lane == 0 : qr == 0) bulk_wait_all();   // every reduction has landed
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// D_i = dO_i . O_i for every row, and the fp32 dQ accumulator cleared.
+template <int D>
+__global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBwdParams p) {
+  constexpr int G = D / 8;                           // threads per row, 16 bytes each
+  const long long rows = static_cast<long long>(p.B) * p.H * p.Lq;
+  const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long nthreads = static_cast<long long>(gridDim.x) * blockDim.x;
+  const int g = static_cast<int>(threadIdx.x % G);
+  for (long long r = tid / G;; r += nthreads / G) {
+    const bool active = r < rows;
+    if (__all_sync(0xFFFFFFFFu, !active)) break;     // every lane of the warp is done
+    uint4 o = make_uint4(0u, 0u, 0u, 0u), d = o;
+    if (active) {
+      o = __ldg(reinterpret_cast<const uint4*>(p.o + r * D) + g);
+      d = __ldg(reinterpret_cast<const uint4*>(p.dout + r * D) + g);
+    }
+    float s = bf16lo(o.x) * bf16lo(d.x) + bf16hi(o.x) * bf16hi(d.x);
+    s = fmaf(bf16lo(o.y), bf16lo(d.y), s);
+    s = fmaf(bf16hi(o.y), bf16hi(d.y), s);
+    s = fmaf(bf16lo(o.z), bf16lo(d.z), s);
+    s = fmaf(bf16hi(o.z), bf16hi(d.z), s);
+    s = fmaf(bf16lo(o.w), bf16lo(d.w), s);
+    s = fmaf(bf16hi(o.w), bf16hi(d.w), s);
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off, G);
+    if (active && g == 0) p.delta[r] = s;
+  }
+  float4* acc = reinterpret_cast<float4*>(p.dq_acc);
+  const long long n4 = rows * D / 4;
+  for (long long x = tid; x < n4; x += nthreads) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// dQ (bf16) from the fp32 accumulator (the scale was applied to dS already),
+// and dK, dV of the cut walks: their parts added in segment order.
+template <int D>
+__global__ void __launch_bounds__(256) attn_bwd_window_post_kernel(const WindowBwdParams p) {
+  const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long nthreads = static_cast<long long>(gridDim.x) * blockDim.x;
+  const long long n8 = static_cast<long long>(p.B) * p.H * p.Lq * D / 8;
+  for (long long x = tid; x < n8; x += nthreads) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p.dq_acc) + 2 * x);
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p.dq_acc) + 2 * x + 1);
+    uint4 w;
+    w.x = pack_bf16(a.x, a.y);
+    w.y = pack_bf16(a.z, a.w);
+    w.z = pack_bf16(b.x, b.y);
+    w.w = pack_bf16(b.z, b.w);
+    reinterpret_cast<uint4*>(p.dq)[x] = w;
+  }
+  // one thread per 4 columns of a row of dK or dV of a cut tile
+  const int BH = p.B * p.Hkv;
+  const int cut_s = p.seg_s > 1 ? p.nst : 0;                 // cut tiles per K/V head
+  const int cut_w = p.seg_w > 1 ? p.nk - p.nst : 0;
+  const long long per_tile = 2ll * kTileN * D / 4;
+  const long long n = static_cast<long long>(BH) * (cut_s + cut_w) * per_tile;
+  for (long long x = tid; x < n; x += nthreads) {
+    const long long t = x / per_tile;
+    const int e = static_cast<int>(x - t * per_tile);
+    int bh, j, nseg;
+    long long slot;
+    if (t < static_cast<long long>(BH) * cut_s) {
+      bh = static_cast<int>(t / p.nst);
+      j = static_cast<int>(t - static_cast<long long>(bh) * p.nst);
+      nseg = p.seg_s;
+      slot = t * nseg;
+    } else {
+      const long long u = t - static_cast<long long>(BH) * cut_s;
+      const int nn = p.nk - p.nst;
+      bh = static_cast<int>(u / nn);
+      j = p.nst + static_cast<int>(u - static_cast<long long>(bh) * nn);
+      nseg = p.seg_w;
+      slot = static_cast<long long>(BH) * cut_s * p.seg_s + u * nseg;
+    }
+    const int which = e / (kTileN * D / 4);                  // 0: dK, 1: dV
+    const int rest = e - which * (kTileN * D / 4);
+    const int r = rest / (D / 4);
+    const int c4 = rest - r * (D / 4);
+    const int key = j * kTileN + r;
+    if (key >= p.Lk) continue;
+    const float4* src = reinterpret_cast<const float4*>(p.part) +
+                        (static_cast<size_t>(slot) * 2 + which) * (kTileN * D / 4) + rest;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < nseg; ++i) {
+      const float4 a = __ldg(src + static_cast<size_t>(i) * 2 * (kTileN * D / 4));
+      s.x += a.x;
+      s.y += a.y;
+      s.z += a.z;
+      s.w += a.w;
+    }
+    uint2 w;
+    w.x = pack_bf16(s.x, s.y);
+    w.y = pack_bf16(s.z, s.w);
+    *(reinterpret_cast<uint2*>((which ? p.dv : p.dk) + (static_cast<size_t>(bh) * p.Lk + key) * D) + c4) = w;
+  }
+}
+
+// How the walks are cut, and where the parts go.
+struct WindowBwdPlan {
+  int nk, nst, seg_s, seg_w;
+  long long slots, n_cta;
+  size_t part_off, bytes;
+};
+WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, const WindowMask& w) {
+  WindowBwdPlan pl{};
+  const long long nq = (static_cast<long long>(Lq) + kTileM - 1) / kTileM;
+  const long long G = H / Hkv, BH = static_cast<long long>(B) * Hkv;
+  pl.nk = static_cast<int>((static_cast<long long>(Lk) + kTileN - 1) / kTileN);
+  pl.nst = (w.snk + kTileN - 1) / kTileN;
+  // query tiles that a tile without sinks meets at most, over its heads
+  const long long share = std::min(nq, std::min<long long>(w.window, 1ll << 40) / kTileM + 2) * G;
+  const long long rest = pl.nk - pl.nst;
+  pl.seg_w = 1;
+  // too few key tiles for the 152 SMs: cut every walk so that the CTAs make a wave
+  const long long tiles = BH * (rest > 0 ? rest : 1);
+  if (tiles < 152) pl.seg_w = static_cast<int>(std::max(1ll, std::min(share, 152 / tiles)));
+  // a sink tile meets up to nq tiles a head: segments as long as the others'
+  // walks, but of at least 8 tiles (a part costs as much memory as 2 tiles)
+  const long long each = std::max(8ll, (share + pl.seg_w - 1) / pl.seg_w);
+  pl.seg_s = static_cast<int>(std::max(1ll, (nq * G + each - 1) / each));
+  if (pl.nst == 0) pl.seg_s = 1;
+  pl.n_cta = BH * (static_cast<long long>(pl.nst) * pl.seg_s + rest * pl.seg_w);
+  pl.slots = BH * ((pl.seg_s > 1 ? static_cast<long long>(pl.nst) * pl.seg_s : 0) +
+                   (pl.seg_w > 1 ? rest * pl.seg_w : 0));
+  pl.part_off = (static_cast<size_t>(B) * H * Lq * d * 4 + 255) & ~static_cast<size_t>(255);
+  pl.bytes = pl.part_off + static_cast<size_t>(pl.slots) * 2 * kTileN * d * 4;
+  return pl;
+}
+
+unsigned window_grid(long long work) {
+  return static_cast<unsigned>(std::max(1ll, std::min(152ll * 16, (work + 255) / 256)));
+}
+
+template <int D>
+cudaError_t launch_window_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tdo, const CUtensorMap& tdq, const WindowBwdParams& p,
+                              long long n_cta, cudaStream_t st) {
+  using C = WinBwdCfg<D>;
+  auto kern = attn_bwd_window_kernel<D>;
+  constexpr int kMaxDev = 64;
+  static bool configured[kMaxDev] = {};  // the attribute is per device and function
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs < static_cast<int>(WinBwdRegs<D>::kLaunchRegs)) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  const long long rows = static_cast<long long>(p.B) * p.H * p.Lq;
+  attn_bwd_window_pre_kernel<D><<<window_grid(rows * (D / 8)), 256, 0, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // optional timing of the main kernel alone (attn_bwd_time_main)
+  cudaEvent_t begin, end;
+  bwd_main_events(&begin, &end);
+  if (begin && (e = cudaEventRecord(begin, st)) != cudaSuccess) return e;
+  if (n_cta > 0) {
+    kern<<<static_cast<unsigned>(n_cta), C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, tdo, tdq, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (end && (e = cudaEventRecord(end, st)) != cudaSuccess) return e;
+  attn_bwd_window_post_kernel<D><<<window_grid(rows * D / 8), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace bss
+
+using namespace bss;
+
+extern "C" size_t attn_bwd_window_workspace_bytes(int B, int H, int H_kv, int Lq, int Lk, int d,
+                                                  int64_t window, int64_t sinks, int64_t q_offset,
+                                                  int64_t k_offset) {
+  WindowMask w;
+  if (check_common(B, H, Lq, Lk, d, 1.f) != ATTN_OK || !valid_kv_heads(H, H_kv)) return 0;
+  if (!window_mask(&w, Lk, window, sinks, q_offset, k_offset)) return 0;
+  return window_bwd_plan(B, H, H_kv, Lq, Lk, d, w).bytes;
+}
+
+extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const void* v, const void* o,
+                                         const float* lse, const void* dout, void* dq, void* dk,
+                                         void* dv, float* delta, void* workspace,
+                                         size_t workspace_bytes, int B, int H, int H_kv, int Lq,
+                                         int Lk, int d, float scale, int64_t window, int64_t sinks,
+                                         int64_t q_offset, int64_t k_offset, void* stream) {
+  attn_status_t s = check_common(B, H, Lq, Lk, d, scale);
+  if (s != ATTN_OK) return s;
+  if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
+  const void* ptrs16[] = {q, k, v, o, dout, dq, dk, dv, workspace};
+  for (const void* ptr : ptrs16)
+    if (!ptr || !aligned16(ptr)) return ATTN_ERR_INVALID_ARG;
+  if (!lse || !delta || !aligned4(lse) || !aligned4(delta)) return ATTN_ERR_INVALID_ARG;
+  WindowBwdParams p{};
+  if (!window_mask(&p.w, Lk, window, sinks, q_offset, k_offset)) return ATTN_ERR_INVALID_ARG;
+  const WindowBwdPlan pl = window_bwd_plan(B, H, H_kv, Lq, Lk, d, p.w);
+  if (workspace_bytes < pl.bytes) return ATTN_ERR_WORKSPACE;
+  if (pl.n_cta > 0x7FFFFFFFll || pl.slots > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (Lq == 0) {                 // no query sends anything
+    const size_t bytes = static_cast<size_t>(B) * H_kv * Lk * d * 2;
+    if (bytes == 0) return ATTN_OK;
+    s = cuda_status("attn_bwd_window clear", cudaMemsetAsync(dk, 0, bytes, st));
+    return s != ATTN_OK ? s : cuda_status("attn_bwd_window clear", cudaMemsetAsync(dv, 0, bytes, st));
+  }
+  if ((s = get_encoder()) != ATTN_OK) return s;
+  if ((s = status_word(&p.err)) != ATTN_OK) return s;
+  CUtensorMap tq, tk, tv, tdo, tdq;
+  if ((s = make_map(&tq, q, B, H, Lq, d)) != ATTN_OK) return s;
+  if ((s = make_map(&tk, k, B, H_kv, Lk, d)) != ATTN_OK) return s;
+  if ((s = make_map(&tv, v, B, H_kv, Lk, d)) != ATTN_OK) return s;
+  if ((s = make_map(&tdo, dout, B, H, Lq, d)) != ATTN_OK) return s;
+  const int box = d == 128 ? WinBwdCfg<128>::kDrainBoxRows : WinBwdCfg<64>::kDrainBoxRows;
+  if ((s = make_map_f32(&tdq, workspace, B, H, Lq, d, box)) != ATTN_OK) return s;
+  p.B = B;
+  p.H = H;
+  p.Hkv = H_kv;
+  p.Lq = Lq;
+  p.Lk = Lk;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.o = static_cast<const __nv_bfloat16*>(o);
+  p.dout = static_cast<const __nv_bfloat16*>(dout);
+  p.lse = lse;
+  p.delta = delta;
+  p.dq_acc = static_cast<float*>(workspace);
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.part_off);
+  p.nk = pl.nk;
+  p.nst = pl.nst;
+  p.seg_s = pl.seg_s;
+  p.seg_w = pl.seg_w;
+  p.head_group = B * H_kv;
+  return cuda_status("attn_bwd_window launch",
+                     d == 64 ? launch_window_bwd<64>(tq, tk, tv, tdo, tdq, p, pl.n_cta, st)
+                             : launch_window_bwd<128>(tq, tk, tv, tdo, tdq, p, pl.n_cta, st));
+}

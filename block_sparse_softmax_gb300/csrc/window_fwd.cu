@@ -1,0 +1,710 @@
+// attn_fwd_window: softmax attention in which a query sees the last `window`
+// positions up to its own and the sequence's first `sinks` positions.
+//
+// Mathematics (window.cuh has the mask): O_i = sum_j P_ij V_j with
+// P_ij = exp(scale q_i . k_j - LSE_i) over the allowed keys j, LSE_i the log
+// of their sum; a row that sees no key gets O = 0, LSE = -inf.
+//
+// One work item is a 128-row query tile.  Its keys are the sink blocks and the
+// window's blocks (128 keys each), disjoint and ascending, taken two at a time
+// with the pipeline of the dense forward with 256-key score tiles: TMA
+// producer, one MMA thread, two softmax warpgroups that take one block of each
+// pair, S (256 columns) | P | O in tensor memory, items handed out by cluster
+// launch control.  An odd last block is scored alone.  The element mask is
+// applied in the blocks that the diagonal, the window's lower edge or the last
+// sink crosses; all others run without it.
+#include <algorithm>
+
+#include "host.cuh"
+#include "window.cuh"
+
+namespace bss {
+namespace {
+
+template <int D>
+struct WinCfg {
+  static constexpr int kChunks = D / 64;                   // 128-byte swizzle atoms across d
+  static constexpr int kChunkBytes = kTileM * 128;         // 128 rows x 64 d
+  static constexpr int kTileBytes = kTileM * D * 2;        // one 128-row tile
+  static constexpr int kPairBytes = 2 * kTileBytes;        // two key blocks
+  // 224 KB of tiles at d=128; at d=64 every ring has a stage more
+  static constexpr int kStagesQ = D == 64 ? 2 : 1;
+  static constexpr int kStagesK = D == 64 ? 3 : 2;         // key-block pairs
+  static constexpr int kStagesV = D == 64 ? 4 : 2;         // V tiles
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kQOff + kStagesQ * kTileBytes;
+  static constexpr int kVOff = kKOff + kStagesK * kPairBytes;
+  static constexpr int kBarOff = kVOff + kStagesV * kTileBytes;
+  static constexpr int kBarQFull = 0;
+  static constexpr int kBarQEmpty = kBarQFull + kStagesQ;
+  static constexpr int kBarKFull = kBarQEmpty + kStagesQ;
+  static constexpr int kBarKEmpty = kBarKFull + kStagesK;
+  static constexpr int kBarVFull = kBarKEmpty + kStagesK;
+  static constexpr int kBarVEmpty = kBarVFull + kStagesV;
+  static constexpr int kBarSFull = kBarVEmpty + kStagesV;  // a pair's S in TMEM
+  static constexpr int kBarSFree = kBarSFull + 1;          // ... read into registers by both warpgroups
+  // [2] P of key block X written by warpgroup X; block 0's also waits for
+  // warpgroup 1's rescale of its half of O
+  static constexpr int kBarPFull = kBarSFree + 1;
+  static constexpr int kBarPvDone = kBarPFull + 2;         // [2] a pair's P V of block X completed
+  static constexpr int kBarXch = kBarPvDone + 2;           // [2] row values exchanged, by parity
+  static constexpr int kBarOFull = kBarXch + 2;
+  static constexpr int kBarOEmpty = kBarOFull + 1;
+  static constexpr int kBarItemFull = kBarOEmpty + 1;      // [2]
+  static constexpr int kBarItemEmpty = kBarItemFull + 2;   // [2]
+  static constexpr int kBarClc = kBarItemEmpty + 2;
+  static constexpr int kBarMmaDone = kBarClc + 1;
+  static constexpr int kNumBars = kBarMmaDone + 1;
+  // cancel answer (16) | TMEM base | abort flag | next item [2]
+  static constexpr int kMiscOff = kBarOff + ((kNumBars + 1) / 2) * 16;
+  static constexpr int kClcOff = kMiscOff;
+  static constexpr int kTmemSlotOff = kMiscOff + 16;
+  static constexpr int kAbortOff = kMiscOff + 20;
+  static constexpr int kNextItemOff = kMiscOff + 24;
+  // exchanged row values: [parity][warpgroup][128 rows] fp32
+  static constexpr int kXchOff = kMiscOff + 32;
+  static constexpr int kPayload = kXchOff + 2 * 2 * kTileM * 4;
+  // alignment slack: at d=128 less than 1024 bytes are left, and the kernel
+  // checks that the dynamic shared memory base leaves room
+  static constexpr int kSlack = kPayload + 1024 <= 232448 ? 1024 : 232448 - kPayload;
+  static constexpr int kSmemBytes = kPayload + kSlack;
+  static_assert(kSlack >= 256, "too little alignment slack");
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS = 0;      // S: 256 fp32 columns (key block X at 128 X)
+  static constexpr uint32_t kColP = 256;    // P: 256 keys, bf16 pairs (block X at 256 + 64 X)
+  static constexpr uint32_t kColO = 384;    // O: D fp32 columns
+  static constexpr int kThreads = 384;
+  static constexpr int kItemReaders = 1 + 8;   // the MMA thread and one lane of each softmax warp
+};
+
+// Register split per warpgroup: warpgroup 0 (TMA, MMA, two idle warps) 136
+// registers a thread, the two softmax warpgroups 184; the launch holds 168.
+constexpr uint32_t kWinLow = 136;
+constexpr uint32_t kWinHigh = 184;
+constexpr uint32_t kWinLaunchRegs = 168;
+static_assert(128 * kWinLow + 256 * kWinHigh <= 384 * kWinLaunchRegs, "register split exceeds the launch");
+
+// Item -> query tile: tile-major with the heads side by side, so that the CTAs
+// running at any moment share the window's K and V tiles in L2; the last tiles
+// first (the first tiles of a sequence have shorter windows and fill the tail).
+struct WindowItem {
+  int b, h, bh, hkv, r0;
+  WindowBlocks kb;
+};
+__device__ __forceinline__ WindowItem window_item(int item, const WindowFwdParams& p, int n_tiles) {
+  WindowItem it;
+  const int BH = p.B * p.H;
+  const int rank = item / BH;
+  it.bh = item - rank * BH;
+  it.b = it.bh / p.H;
+  it.h = it.bh - it.b * p.H;
+  it.hkv = it.h / (p.H / p.Hkv);
+  it.r0 = (n_tiles - 1 - rank) * kTileM;
+  it.kb = window_blocks(p.w, it.r0, p.Lq, p.Lk);
+  return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    attn_fwd_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const WindowFwdParams p) {
+  using C = WinCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  {
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+    if (pad > static_cast<uint32_t>(C::kSlack)) {   // layout would not fit: report, touch nothing
+      if (threadIdx.x == 0) record_error(p.err, ATTN_ERR_UNSUPPORTED);
+      return;
+    }
+  }
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::kBarOff + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kTmemSlotOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbortOff);
+  volatile int* next_item = reinterpret_cast<volatile int*>(smem + C::kNextItemOff);
+
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  const int tid = static_cast<int>(threadIdx.x);
+  // A launch whose earlier CTAs already timed out stops at once.
+  if (*reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
+  const int n_tiles = (p.Lq + kTileM - 1) / kTileM;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStagesQ; ++s) {
+      mbar_init(bar(C::kBarQFull + s), 1);
+      mbar_init(bar(C::kBarQEmpty + s), 1);
+    }
+    for (int s = 0; s < C::kStagesK; ++s) {
+      mbar_init(bar(C::kBarKFull + s), 1);
+      mbar_init(bar(C::kBarKEmpty + s), 1);
+    }
+    for (int s = 0; s < C::kStagesV; ++s) {
+      mbar_init(bar(C::kBarVFull + s), 1);
+      mbar_init(bar(C::kBarVEmpty + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(C::kBarXch + s), 2 * 4 * 32);
+      mbar_init(bar(C::kBarItemFull + s), 1);
+      mbar_init(bar(C::kBarItemEmpty + s), C::kItemReaders);
+    }
+    mbar_init(bar(C::kBarSFull), 1);
+    mbar_init(bar(C::kBarSFree), 2 * 4 * 32);
+    mbar_init(bar(C::kBarPFull + 0), 2 * 4 * 32);
+    mbar_init(bar(C::kBarPFull + 1), 4 * 32);
+    mbar_init(bar(C::kBarPvDone + 0), 1);
+    mbar_init(bar(C::kBarPvDone + 1), 1);
+    mbar_init(bar(C::kBarOFull), 1);
+    mbar_init(bar(C::kBarOEmpty), 2 * 4 * 32);
+    mbar_init(bar(C::kBarClc), 1);
+    mbar_init(bar(C::kBarMmaDone), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(sbase + C::kTmemSlotOff, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 4) {
+    regs_set<kWinLow, kWinLaunchRegs>();
+    if (warp == 0) {
+      // =================== TMA producer and item scheduler ===================
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        int item = static_cast<int>(blockIdx.x);
+        int n = 0;              // items finished
+        int ik = 0, iv = 0;     // pair stages and V tiles loaded (over all items)
+        int qn = 0;             // Q tiles loaded
+        int clc_k = 0;          // cancel requests answered
+        bool clc_live = true;
+        bool clc_out = false;   // a cancel request is in flight
+        bool ok = true;
+        auto request_item = [&]() {
+          fence_proxy_async_smem();
+          mbar_arrive_expect_tx(bar(C::kBarClc), 16);
+          clc_try_cancel(sbase + C::kClcOff, bar(C::kBarClc));
+          clc_out = true;
+        };
+        // key blocks b0 and b1 (b1 = -1: b0 alone); a block that reaches past
+        // the last key reads the zero fill there
+        auto load_k = [&](const WindowItem& it, int b0, int b1) -> bool {
+          const int s = ik % C::kStagesK;
+          if (ik >= C::kStagesK &&
+              !wait_bar(bar(C::kBarKEmpty + s), ((ik / C::kStagesK) & 1) ^ 1, abort_flag, p.err))
+            return false;
+          const uint32_t ks = sbase + C::kKOff + s * C::kPairBytes;
+          mbar_arrive_expect_tx(bar(C::kBarKFull + s), b1 >= 0 ? C::kPairBytes : C::kTileBytes);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t == 1 && b1 < 0) break;
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_4d(ks + c * 2 * C::kChunkBytes + t * C::kChunkBytes, &tmK, bar(C::kBarKFull + s),
+                          c * 64, (t ? b1 : b0) * kTileN, it.hkv, it.b);
+          }
+          ++ik;
+          return true;
+        };
+        auto load_v = [&](const WindowItem& it, int kb) -> bool {
+          const int s = iv % C::kStagesV;
+          if (iv >= C::kStagesV &&
+              !wait_bar(bar(C::kBarVEmpty + s), ((iv / C::kStagesV) & 1) ^ 1, abort_flag, p.err))
+            return false;
+          const uint32_t vs = sbase + C::kVOff + s * C::kTileBytes;
+          mbar_arrive_expect_tx(bar(C::kBarVFull + s), C::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_4d(vs + c * C::kChunkBytes, &tmV, bar(C::kBarVFull + s), c * 64, kb * kTileN, it.hkv,
+                        it.b);
+          ++iv;
+          return true;
+        };
+        while (ok) {
+          const WindowItem it = window_item(item, p, n_tiles);
+          const int nb = it.kb.count();
+          const int ns = (nb + 1) / 2;
+          auto second = [&](int k) { return 2 * k + 1 < nb ? it.kb.at(2 * k + 1) : -1; };
+          if (ns > 0) {
+            const int s = qn % C::kStagesQ;
+            // the last S that read this Q buffer must have completed
+            if (qn >= C::kStagesQ &&
+                !wait_bar(bar(C::kBarQEmpty + s), ((qn / C::kStagesQ) & 1) ^ 1, abort_flag, p.err))
+              break;
+            mbar_arrive_expect_tx(bar(C::kBarQFull + s), C::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_4d(sbase + C::kQOff + s * C::kTileBytes + c * C::kChunkBytes, &tmQ,
+                          bar(C::kBarQFull + s), c * 64, it.r0, it.h, it.b);
+            ++qn;
+            // K runs one step ahead of V
+            ok = load_k(it, it.kb.at(0), second(0));
+            for (int k = 0; k < ns && ok; ++k) {
+              if (k == ns - 1 && clc_live) request_item();   // the next item, as this one's last loads go
+              if (k + 1 < ns) ok = load_k(it, it.kb.at(2 * k + 2), second(k + 1));
+              if (ok) ok = load_v(it, it.kb.at(2 * k)) && (second(k) < 0 || load_v(it, second(k)));
+            }
+            if (!ok) break;
+          }
+          if (clc_live && !clc_out) request_item();   // an item without keys
+          int next = -1;
+          if (clc_out) {
+            if (!wait_bar(bar(C::kBarClc), clc_k & 1, abort_flag, p.err)) break;
+            clc_out = false;
+            ++clc_k;
+            int x = -1;
+            if (clc_query(sbase + C::kClcOff, x)) {
+              if (x >= 0 && x < p.n_items) {
+                next = x;
+              } else {
+                record_error(p.err, ATTN_ERR_CUDA);   // not an index of this grid
+                clc_live = false;
+              }
+            } else {
+              clc_live = false;                        // nothing left to take
+            }
+          }
+          const int s = n & 1;
+          if (n >= 2 && !wait_bar(bar(C::kBarItemEmpty + s), ((n >> 1) & 1) ^ 1, abort_flag, p.err))
+            break;
+          next_item[s] = next;
+          mbar_arrive(bar(C::kBarItemFull + s));
+          ++n;
+          if (next < 0) break;
+          item = next;
+        }
+        // every copy issued has landed before the CTA may exit
+        for (int j = max(0, ik - C::kStagesK); j < ik; ++j)
+          drain_bar(bar(C::kBarKFull + j % C::kStagesK), (j / C::kStagesK) & 1);
+        for (int j = max(0, iv - C::kStagesV); j < iv; ++j)
+          drain_bar(bar(C::kBarVFull + j % C::kStagesV), (j / C::kStagesV) & 1);
+        for (int j = max(0, qn - C::kStagesQ); j < qn; ++j)
+          drain_bar(bar(C::kBarQFull + j % C::kStagesQ), (j / C::kStagesQ) & 1);
+        if (clc_out) drain_bar(bar(C::kBarClc), clc_k & 1);
+      }
+    } else if (warp == 1) {
+      // =================== MMA issuer (one thread) ===================
+      // Per item: S_0, then for every step k: S_{k+1} (as soon as both
+      // softmax warpgroups hold S_k in registers) and P_k V_k.
+      if (lane == 0) {
+        constexpr uint32_t kIdescS = idesc_bf16_f32(kTileM, 2 * kTileN, false, false);
+        constexpr uint32_t kIdescS1 = idesc_bf16_f32(kTileM, kTileN, false, false);   // a block alone
+        constexpr uint32_t kIdescPV = idesc_bf16_f32(kTileM, D, false, true);
+        int item = static_cast<int>(blockIdx.x);
+        int n = 0;              // items finished
+        int ik = 0, iv = 0;     // pair stages and V tiles consumed
+        int qn = 0;             // Q tiles consumed
+        int sn = 0;             // S tiles issued
+        int pn = 0;             // P tiles consumed
+        int on = 0;             // O results handed to the epilogue
+        bool ok = true;
+        auto issue_s = [&](bool last, bool alone) -> bool {
+          if (sn > 0 && !wait_bar(bar(C::kBarSFree), (sn - 1) & 1, abort_flag, p.err)) return false;
+          const int s = ik % C::kStagesK;
+          if (!wait_bar(bar(C::kBarKFull + s), (ik / C::kStagesK) & 1, abort_flag, p.err)) return false;
+          tc_fence_after();
+          const int qs = (qn - 1) % C::kStagesQ;
+          const uint64_t dq = sdesc_sw128(sbase + C::kQOff + qs * C::kTileBytes, 16, 1024);
+          const uint64_t dk = sdesc_sw128(sbase + C::kKOff + s * C::kPairBytes, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qoff = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+            const uint32_t koff = (kk >> 2) * 2 * C::kChunkBytes + (kk & 3) * 32;
+            mma_ss(tmem + C::kColS, sdesc_add(dq, qoff), sdesc_add(dk, koff), alone ? kIdescS1 : kIdescS,
+                   kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(C::kBarSFull));
+          mma_commit(bar(C::kBarKEmpty + s));
+          if (last) mma_commit(bar(C::kBarQEmpty + qs));   // Q's buffer is free for a later item
+          ++ik;
+          ++sn;
+          return true;
+        };
+        // P V block by block: block X's MMAs go as soon as warpgroup X has
+        // written its P, and their completion frees that block's P columns
+        auto issue_pv = [&](bool first, bool alone) -> bool {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!wait_bar(bar(C::kBarPFull + t), pn & 1, abort_flag, p.err)) return false;
+            tc_fence_after();
+            if (t == 0 && first && on > 0) {
+              // O still holds the previous item's result until its epilogue read it
+              if (!wait_bar(bar(C::kBarOEmpty), (on - 1) & 1, abort_flag, p.err)) return false;
+              tc_fence_after();
+            }
+            if (!(alone && t == 1)) {
+              const int s = iv % C::kStagesV;
+              if (!wait_bar(bar(C::kBarVFull + s), (iv / C::kStagesV) & 1, abort_flag, p.err)) return false;
+              tc_fence_after();
+              const uint64_t dv = sdesc_sw128(sbase + C::kVOff + s * C::kTileBytes, C::kChunkBytes, 1024);
+#pragma unroll
+              for (int kk = 0; kk < kTileN / 16; ++kk)
+                mma_ts(tmem + C::kColO, tmem + C::kColP + (t * 8 + kk) * 8, sdesc_add(dv, kk * 16 * 128),
+                       kIdescPV, (!first || t > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(bar(C::kBarVEmpty + s));
+              ++iv;
+            }
+            mma_commit(bar(C::kBarPvDone + t));
+          }
+          ++pn;
+          return true;
+        };
+        while (ok) {
+          const WindowItem it = window_item(item, p, n_tiles);
+          const int nb = it.kb.count();
+          const int ns = (nb + 1) / 2;
+          const bool odd = (nb & 1) != 0;     // the last pair is one block
+          if (ns > 0) {
+            if (!wait_bar(bar(C::kBarQFull + qn % C::kStagesQ), (qn / C::kStagesQ) & 1, abort_flag, p.err))
+              break;
+            ++qn;
+            ok = issue_s(ns == 1, odd && ns == 1);
+            for (int k = 0; k < ns && ok; ++k) {
+              if (k + 1 < ns) ok = issue_s(k + 1 == ns - 1, odd && k + 1 == ns - 1);
+              if (ok) ok = issue_pv(k == 0, odd && k == ns - 1);
+            }
+            if (!ok) break;
+            mma_commit(bar(C::kBarOFull));
+            ++on;
+          }
+          const int s = n & 1;
+          if (!wait_bar(bar(C::kBarItemFull + s), (n >> 1) & 1, abort_flag, p.err)) break;
+          const int next = next_item[s];
+          mbar_arrive(bar(C::kBarItemEmpty + s));
+          ++n;
+          if (next < 0) break;
+          item = next;
+        }
+        // every MMA issued has completed before tensor memory is released
+        mma_commit(bar(C::kBarMmaDone));
+        drain_bar(bar(C::kBarMmaDone), 0);
+      }
+    }
+  } else {
+    regs_set<kWinHigh, kWinLaunchRegs>();
+    // =================== softmax warpgroups: X = 0 (warps 4-7), 1 (warps 8-11) ===================
+    const int X = (warp - 4) >> 2;                // key block X of every pair
+    const int wq = warp & 3;                      // TMEM lane quarter of this warp
+    const int row_in_tile = wq * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_base + C::kColS + X * 128;
+    const uint32_t tP = tmem + lane_base + C::kColP + X * 64;
+    const uint32_t tO = tmem + lane_base + C::kColO + X * (D / 2);
+    // the 64 columns this warpgroup's epilogue reads (at d=64 both read all)
+    const uint32_t tO0 = tmem + lane_base + C::kColO + (D == 128 ? X * 64 : 0);
+    const float sl2 = p.scale_log2;
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    float* xch = reinterpret_cast<float*>(smem + C::kXchOff);
+
+    int item = static_cast<int>(blockIdx.x);
+    int n = 0;          // items finished
+    int cnt = 0;        // S tiles consumed (over all items)
+    int nx = 0;         // row values exchanged
+    int on = 0;         // O results read
+    bool ok = true;
+    // hand this row's value to the other warpgroup and take its value back
+    auto exchange = [&](float v, float& other) -> bool {
+      float* xb = xch + (nx & 1) * 2 * kTileM;
+      xb[X * kTileM + row_in_tile] = v;
+      mbar_arrive(bar(C::kBarXch + (nx & 1)));
+      const bool w = __all_sync(0xFFFFFFFFu,
+                                wait_bar(bar(C::kBarXch + (nx & 1)), (nx >> 1) & 1, abort_flag, p.err));
+      other = xb[(1 - X) * kTileM + row_in_tile];
+      ++nx;
+      return w;
+    };
+    while (ok) {
+      const WindowItem it = window_item(item, p, n_tiles);
+      const int row = it.r0 + row_in_tile;
+      const int nb = it.kb.count();
+      const int ns = (nb + 1) / 2;
+      float m2 = NEG_INF;     // reference max (log2 units), moved only by > 8
+      float l = 0.f;          // this warpgroup's part of the row sum
+      for (int k = 0; k < ns; ++k) {
+        const bool none = 2 * k + X >= nb;        // the pair's second block is missing
+        const int kstart = none ? 0 : it.kb.at(2 * k + X) * kTileN;
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarSFull), cnt & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
+        // S is in registers: the next pair's S may overwrite its columns
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarSFree));
+
+        // element mask: in key index j of the block, allowed are j <= jhi
+        // (diagonal, last key) with j >= jlo (window) or j < js (sinks)
+        const long long diag0 = static_cast<long long>(it.r0) + p.w.sh - kstart;   // first row's own key
+        const bool edge = none || kstart + kTileN > p.Lk || kTileN - 1 > diag0 ||
+                          (diag0 + kTileM - 1 - p.w.window + 1 > 0 && kstart + kTileN > p.w.snk);
+        if (edge) {
+          const long long dg = diag0 + row_in_tile;
+          const int jhi = none ? -1 : static_cast<int>(max(-1ll, min(dg, static_cast<long long>(p.Lk) - 1 - kstart)));
+          const int jlo = static_cast<int>(max(0ll, min(128ll, dg - p.w.window + 1)));
+          const int js = p.w.snk - kstart;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int e = c * 32 + j;
+              if (e > jhi || (e < jlo && e >= js)) s[c][j] = __float_as_uint(NEG_INF);
+            }
+        }
+        // row max of this block over 8 chains of three-input max
+        float mx[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mx[u] = __uint_as_float(s[0][u]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = (c == 0 ? 8 : 0); j < 32; j += 16)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (j + 8 + u < 32)
+                mx[u] = fmax3(mx[u], __uint_as_float(s[c][j + u]), __uint_as_float(s[c][j + 8 + u]));
+              else
+                mx[u] = fmaxf(mx[u], __uint_as_float(s[c][j + u]));
+        const float mmine = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
+        // the pair's row max: both warpgroups take the same decisions below
+        float mothr;
+        if (!exchange(mmine, mothr)) {
+          ok = false;
+          break;
+        }
+        const float mblk = fmaxf(mmine, mothr);
+        float alpha = 1.f;
+        bool moved = false;
+        if (mblk > m2 + 8.f) {
+          alpha = ex2(m2 - mblk);
+          m2 = mblk;
+          moved = true;
+        }
+        const float mu = (m2 == NEG_INF) ? 0.f : m2;
+        // Where the reference max moved, this warpgroup's half of O is
+        // rescaled: after the previous pair's whole P V (both blocks write
+        // all of O).  Warpgroup 1 does it first and then releases block 0's
+        // P V; warpgroup 0 after writing its P, before releasing it.
+        const bool fix = moved && k > 0;
+        const bool any_fix = __any_sync(0xFFFFFFFFu, fix);
+        auto rescale_o = [&]() -> bool {
+          if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarPvDone + 1), (cnt - 1) & 1, abort_flag, p.err)))
+            return false;
+          tc_fence_after();
+          const float a = fix ? alpha : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+            tmem_st32(tO + c * 32, o);
+          }
+          return true;
+        };
+        if (X == 1) {
+          if (any_fix && !rescale_o()) {
+            ok = false;
+            break;
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar(C::kBarPFull + 0));
+        }
+        // P block X is written below: the previous pair's P V of block X
+        // (which reads it) must have completed
+        if (cnt > 0 &&
+            !__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarPvDone + X), (cnt - 1) & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float rs[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) rs[u] = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            const int c = half * 2 + c2;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float x0, x1;
+              ffma2(x0, x1, __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]), sl2, sl2, -mu,
+                    -mu);
+              const float p0 = ex2(x0);
+              const float p1 = ex2(x1);
+              const int u = (j >> 1) & 3;
+              fadd2(rs[2 * u], rs[2 * u + 1], rs[2 * u], rs[2 * u + 1], p0, p1);
+              pk[c2 * 16 + j / 2] = pack_bf16(p0, p1);
+            }
+          }
+          tmem_st32(tP + half * 32, pk);
+        }
+        l = l * alpha + (((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7])));
+        if (X == 0 && any_fix && !rescale_o()) {
+          ok = false;
+          break;
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarPFull + X));
+        ++cnt;
+      }
+      if (!ok) break;
+
+      // ---- epilogue: the row sum is the two warpgroups' parts.  At d=128
+      // each writes its half of the row's columns (one 128-byte line); at
+      // d=64 a row is one line, and warpgroup 0 writes it ----
+      constexpr bool kSplit = D == 128;
+      uint32_t o[2][32];
+      float lt = 0.f;
+      if (ns > 0) {
+        float lo;
+        if (!exchange(l, lo)) break;
+        lt = l + lo;
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarOFull), on & 1, abort_flag, p.err))) break;
+        tc_fence_after();
+        tmem_ld32(tO0, o[0]);
+        tmem_ld32(tO0 + 32, o[1]);
+        tmem_ld_wait(o[0]);
+        tmem_ld_wait(o[1]);
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarOEmpty));
+        ++on;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[c][j] = 0u;
+      }
+      if (kSplit || X == 0) {
+        const bool inb = row < p.Lq;
+        const size_t rows0 = static_cast<size_t>(it.bh) * p.Lq;
+        // a row that saw no key has lt = 0 (its O is 0, whatever the masked
+        // keys held); a NaN score makes lt NaN and goes through
+        const bool empty = lt == 0.f;
+        const float inv = empty ? 0.f : 1.f / lt;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, inb);
+        uint8_t* base =
+            reinterpret_cast<uint8_t*>(p.o + (rows0 + it.r0 + wq * 32) * D) + (kSplit ? X * 128 : 0);
+        uint32_t w[32];
+#pragma unroll
+        for (int kq = 0; kq < 32; ++kq) {
+          const int c = kq / 16;
+          const int j = (2 * kq) % 32;
+          w[kq] = empty ? 0u : pack_bf16(__uint_as_float(o[c][j]) * inv, __uint_as_float(o[c][j + 1]) * inv);
+        }
+        transpose_octets(w, lane);
+        store_octet_lines(w, base, D * 2, valid, lane);
+        if (X == 0 && inb) p.lse[rows0 + row] = empty ? NEG_INF : (m2 + __log2f(lt)) * kLn2;
+      }
+      // ---- next item ----
+      const int s = n & 1;
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarItemFull + s), (n >> 1) & 1, abort_flag, p.err)))
+        break;
+      const int next = next_item[s];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kBarItemEmpty + s));
+      ++n;
+      if (next < 0) break;
+      item = next;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_window_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const WindowFwdParams& p, cudaStream_t st) {
+  using C = WinCfg<D>;
+  auto kern = attn_fwd_window_kernel<D>;
+  constexpr int kMaxDev = 64;
+  static bool configured[kMaxDev] = {};  // the attribute is per device and function
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs < static_cast<int>(kWinLaunchRegs)) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  kern<<<p.n_items, C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool window_mask(WindowMask* w, int Lk, int64_t window, int64_t sinks, int64_t q_offset,
+                 int64_t k_offset) {
+  if (window < 1 || sinks < 0 || q_offset < 0 || k_offset < 0) return false;
+  // positions are compared as differences: bounded so that no sum wraps
+  constexpr int64_t kMost = int64_t(1) << 60;
+  w->sh = std::min(q_offset, kMost) - std::min(k_offset, kMost);
+  w->window = std::min(window, kMost);
+  w->snk = static_cast<int>(
+      std::max<int64_t>(0, std::min<int64_t>(std::min(sinks, kMost) - std::min(k_offset, kMost), Lk)));
+  return true;
+}
+
+}  // namespace bss
+
+using namespace bss;
+
+extern "C" attn_status_t attn_fwd_window(const void* q, const void* k, const void* v, void* o,
+                                         float* lse, int B, int H, int H_kv, int Lq, int Lk, int d,
+                                         float scale, int64_t window, int64_t sinks,
+                                         int64_t q_offset, int64_t k_offset, void* stream) {
+  if (!o || !lse || !aligned16(o) || !aligned4(lse)) return ATTN_ERR_INVALID_ARG;
+  attn_status_t s = check_common(B, H, Lq, Lk, d, scale);
+  if (s != ATTN_OK) return s;
+  if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
+  if (!q || !k || !v || !aligned16(q) || !aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID_ARG;
+  WindowFwdParams p{};
+  if (!window_mask(&p.w, Lk, window, sinks, q_offset, k_offset)) return ATTN_ERR_INVALID_ARG;
+  if (Lq == 0) return ATTN_OK;
+  if ((s = get_encoder()) != ATTN_OK) return s;
+  if ((s = status_word(&p.err)) != ATTN_OK) return s;
+  CUtensorMap tq, tk, tv;
+  if ((s = make_map(&tq, q, B, H, Lq, d)) != ATTN_OK) return s;
+  if ((s = make_map(&tk, k, B, H_kv, Lk, d)) != ATTN_OK) return s;
+  if ((s = make_map(&tv, v, B, H_kv, Lk, d)) != ATTN_OK) return s;
+  p.B = B;
+  p.H = H;
+  p.Hkv = H_kv;
+  p.Lq = Lq;
+  p.Lk = Lk;
+  p.scale_log2 = scale * kLog2e;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.n_items = B * H * ((Lq + kTileM - 1) / kTileM);   // checked by check_common
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status("attn_fwd_window launch", d == 64 ? launch_window_fwd<64>(tq, tk, tv, p, st)
+                                                       : launch_window_fwd<128>(tq, tk, tv, p, st));
+}

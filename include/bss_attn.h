@@ -52,7 +52,9 @@ typedef enum {
   ATTN_ERR_BAD_BLOCKLIST = 3, /* malformed CSR: row_ptr not monotone, index out of range, nnz mismatch */
   ATTN_ERR_CUDA = 4,          /* a CUDA runtime/driver call or kernel launch failed */
   ATTN_ERR_TIMEOUT = 5,       /* a kernel's bounded wait expired (watchdog); the kernel returned early */
-  ATTN_ERR_WORKSPACE = 6      /* workspace missing or smaller than attn_bwd_workspace_bytes() */
+  ATTN_ERR_WORKSPACE = 6,     /* workspace missing or smaller than attn_bwd_workspace_bytes() */
+  ATTN_ERR_BAD_PAGES = 7,     /* paged cache: a page, sequence, length or position out of range */
+  ATTN_ERR_NO_PAGES = 8       /* paged cache: fewer free pages than asked for; nothing was changed */
 } attn_status_t;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -331,6 +333,184 @@ attn_status_t attn_bwd_noalloc(const void* q, const void* k, const void* v, cons
                                float* delta, int B, int H, int H_kv, int L, int d, float scale,
                                int causal,
                                void* stream);
+
+/*
+ * attn_fwd_window - attention forward with a sliding window and sinks: query
+ * i sees key j when 0 <= t and (t < window or j + k_offset < sinks), with t =
+ * (i + q_offset) - (j + k_offset): the last `window` positions up to its own,
+ * and the sequence's first `sinks` positions that are not in its future.
+ * "Exact Blocks, Rings, and Sparsity", section 5 (a mandatory local window
+ * united with a few global blocks) at the granularity of single keys; the
+ * block-sparse attention patterns page, 'Block-sparse attention' (local +
+ * global patterns).
+ *   q [B,H,Lq,d], k/v [B,H_kv,Lk,d] bf16 in; o [B,H,Lq,d] bf16 out; lse
+ *   [B,H,Lq] fp32 out; window >= 1, sinks >= 0, offsets >= 0.  A query that
+ *   sees no key gets O = 0, LSE = -inf.  window >= every distance gives the
+ *   causal attn_fwd (within rounding).
+ *   Work is proportional to the visible 128-key blocks: the blocks that meet a
+ *   128-query tile's window, and the sink blocks.
+ *   Keys and values are taken as finite: a NaN or infinity in v reaches the
+ *   queries of every 128-query tile that reads its block.
+ */
+attn_status_t attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse,
+                              int B, int H, int H_kv, int Lq, int Lk, int d, float scale,
+                              int64_t window, int64_t sinks, int64_t q_offset, int64_t k_offset,
+                              void* stream);
+
+/*
+ * attn_bwd_window - gradients of attn_fwd_window by recomputation from the
+ * saved LSE ("Exact Blocks, Rings, and Sparsity", section 3, over the
+ * window's allowed pairs).
+ *   q, o, dout [B,H,Lq,d], k, v [B,H_kv,Lk,d] bf16, lse fp32 [B,H,Lq] from
+ *   attn_fwd_window with the same window, sinks, offsets and scale.  Out: dq
+ *   [B,H,Lq,d], dk, dv [B,H_kv,Lk,d] bf16 (dk and dv summed over the query
+ *   heads of their group), delta fp32 [B,H,Lq].  A query that sees no key gets
+ *   dq = 0; a key that no query sees gets dk = dv = 0.
+ *   dk and dv are the same in every run.  dq is accumulated in fp32 in the
+ *   order the key tiles finish, so its last bit may differ from run to run.
+ *   workspace: device, 16-byte aligned, >= attn_bwd_window_workspace_bytes
+ *   bytes (0 for invalid arguments): the fp32 dQ accumulator, and fp32 parts
+ *   of dK and dV of key tiles whose queries several CTAs share; contents on
+ *   entry irrelevant.  Calls that can overlap need a workspace each.
+ */
+size_t attn_bwd_window_workspace_bytes(int B, int H, int H_kv, int Lq, int Lk, int d,
+                                       int64_t window, int64_t sinks, int64_t q_offset,
+                                       int64_t k_offset);
+attn_status_t attn_bwd_window(const void* q, const void* k, const void* v, const void* o,
+                              const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                              float* delta, void* workspace, size_t workspace_bytes, int B, int H,
+                              int H_kv, int Lq, int Lk, int d, float scale, int64_t window,
+                              int64_t sinks, int64_t q_offset, int64_t k_offset, void* stream);
+
+/*
+ * Paged key/value caches (attn_decode_paged and the attn_kv_ calls).
+ *   - k_cache, v_cache [n_pages][H_kv][page_size][d], bf16 (ATTN_KV_BF16) or
+ *     e4m3 (ATTN_KV_E4M3); a page is contiguous, pages lie k_page_stride /
+ *     v_page_stride elements apart (a multiple of 16 bytes, at least a page).
+ *     page_size: a power of two in [16, 1024].  An e4m3 element x of K/V head
+ *     h stands for x * k_scale[h] (v_scale[h]), fp32 device arrays [H_kv] of
+ *     positive scales; both are NULL for bf16 caches.
+ *   - page_table [S][max_pages] int32: entry m of row s is the page of tokens
+ *     m * page_size .. of sequence s, -1 where it holds none.  seq_lens [S]
+ *     int32: tokens.  refs [n_pages] int32: table entries holding the page
+ *     (0: free).  S <= 65536.  A fresh cache has every entry -1, every length
+ *     and every count 0.
+ *   - The attn_kv_ calls keep these consistent: a page that is not full is
+ *     held once, pages are taken from the lowest free index up, in order of
+ *     the sequences (or forks), and a call that cannot be met changes nothing.
+ *   - What is wrong in the arrays (a page, sequence, length or position out of
+ *     range) is skipped and reported as ATTN_ERR_BAD_PAGES by
+ *     attn_poll_status; too few free pages as ATTN_ERR_NO_PAGES.
+ */
+enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1 };
+
+/*
+ * attn_decode_paged - attention of one new token per sequence over a paged
+ * cache, split over its length and joined ("Exact Blocks, Rings, and
+ * Sparsity", section 4: partial states over key chunks and their associative
+ * merge).
+ *   q [S][H][d] bf16, rows q_stride elements apart (a multiple of 8, at least
+ *   H*d); o [S][H][d] bf16 and lse [S][H] fp32 out, contiguous.  The query of
+ *   sequence s stands at position seq_lens[s] - 1 (its key is in the cache)
+ *   and sees the keys j < seq_lens[s], with window > 0 only those with j >=
+ *   seq_lens[s] - window or j < sinks; window = 0: every key (sinks must be
+ *   0).  H_kv divides H; query head h reads K/V head h / (H / H_kv).  A
+ *   sequence of length 0 gets O = 0, LSE = -inf.
+ *   Table entries of keys that are not seen are not read, and neither are the
+ *   rows of the last page past the length: they may hold anything.  A seen
+ *   page outside [0, n_pages) is skipped and reported, a length past
+ *   max_pages * page_size is cut to it and reported.
+ *   workspace: device, 16-byte aligned, >= attn_decode_paged_workspace_bytes
+ *   (0 for invalid arguments; it does not depend on the lengths), contents on
+ *   entry irrelevant.  Calls that can overlap need a workspace each.
+ *   The same lengths give the same bits in every run.
+ */
+size_t attn_decode_paged_workspace_bytes(int S, int H, int H_kv, int d);
+attn_status_t attn_decode_paged(const void* q, int64_t q_stride, const void* k_cache,
+                                const void* v_cache, int64_t k_page_stride, int64_t v_page_stride,
+                                int kv_dtype, const float* k_scale, const float* v_scale,
+                                const int32_t* page_table, const int32_t* seq_lens, void* o,
+                                float* lse, void* workspace, size_t workspace_bytes, int S, int H,
+                                int H_kv, int d, int max_pages, int n_pages, int page_size,
+                                float scale, int64_t window, int64_t sinks, void* stream);
+
+/*
+ * attn_kv_reserve - room for n_new[s] >= 0 more tokens in every sequence: new
+ * pages enter the table, seq_lens grows.  start [S] out: the position of the
+ * first new token, or -1 for every sequence when the call was refused (too
+ * few free pages, or a sequence past max_pages * page_size).
+ */
+attn_status_t attn_kv_reserve(int32_t* page_table, int32_t* seq_lens, int32_t* refs,
+                              const int32_t* n_new, int32_t* start, int S, int max_pages,
+                              int n_pages, int page_size, void* stream);
+
+/*
+ * attn_kv_write - keys and values of new tokens into their pages.  k_new,
+ * v_new [T][H_kv][d] bf16, rows k_new_stride / v_new_stride elements apart (a
+ * multiple of 8, at least H_kv*d).  Rows cu_new[s] .. cu_new[s+1]-1 (cu_new
+ * [S+1] int32, ascending) are sequence s's tokens start[s], start[s]+1, ...;
+ * rows before cu_new[0] or from cu_new[S] on are left out, and so are
+ * sequences with start[s] < 0.  An e4m3 cache gets round(x / scale[h]),
+ * saturated at 448.
+ */
+attn_status_t attn_kv_write(const void* k_new, const void* v_new, int64_t k_new_stride,
+                            int64_t v_new_stride, void* k_cache, void* v_cache,
+                            int64_t k_page_stride, int64_t v_page_stride, int kv_dtype,
+                            const float* k_scale, const float* v_scale, const int32_t* page_table,
+                            const int32_t* start, const int32_t* cu_new, int T, int S,
+                            int max_pages, int n_pages, int H_kv, int d, int page_size,
+                            void* stream);
+
+/*
+ * attn_kv_fork - sequence children[f] becomes a copy of parents[f].  Full
+ * pages are shared; of a last page that is not full the child takes a page of
+ * its own, and copy_src[f], copy_dst[f] name the copy to make (-1: none) with
+ * attn_kv_copy_pages, once per layer's cache.  A child must be empty, occur
+ * once and not be a parent too; a parent may occur often.
+ */
+attn_status_t attn_kv_fork(int32_t* page_table, int32_t* seq_lens, int32_t* refs,
+                           const int32_t* parents, const int32_t* children, int n_forks,
+                           int32_t* copy_src, int32_t* copy_dst, int S, int max_pages, int n_pages,
+                           int page_size, void* stream);
+
+/*
+ * attn_kv_free - the listed sequences give back their pages and become empty
+ * (listed twice: freed once).
+ */
+attn_status_t attn_kv_free(int32_t* page_table, int32_t* seq_lens, int32_t* refs,
+                           const int32_t* seqs, int n_seqs, int S, int max_pages, int n_pages,
+                           int page_size, void* stream);
+
+/*
+ * attn_kv_evict - every sequence gives back the pages that attn_decode_paged
+ * with this window and sinks no longer reads, now or at a greater length.
+ */
+attn_status_t attn_kv_evict(int32_t* page_table, const int32_t* seq_lens, int32_t* refs,
+                            int64_t window, int64_t sinks, int S, int max_pages, int n_pages,
+                            int page_size, void* stream);
+
+/*
+ * attn_kv_compact - the pages in use move to the lowest indices: with n in
+ * use, those at n or past it take, in ascending order, the free pages below n.
+ * The table and refs follow; copy_src, copy_dst [n_pages] list the copies to
+ * make (ascending, then -1) and count [1] their number, for
+ * attn_kv_copy_pages.
+ */
+attn_status_t attn_kv_compact(int32_t* page_table, int32_t* refs, int32_t* copy_src,
+                              int32_t* copy_dst, int32_t* count, int S, int max_pages, int n_pages,
+                              void* stream);
+
+/*
+ * attn_kv_copy_pages - page copy_src[i] of both caches to page copy_dst[i],
+ * for i < n_copies, or i < min(n_copies, *count) when count (device) is not
+ * NULL.  A pair of two negative entries is left out.  The copies run in any
+ * order: no page may be both a source and a destination, and a destination
+ * may occur once.
+ */
+attn_status_t attn_kv_copy_pages(void* k_cache, void* v_cache, int64_t k_page_stride,
+                                 int64_t v_page_stride, int kv_dtype, const int32_t* copy_src,
+                                 const int32_t* copy_dst, int n_copies, const int32_t* count,
+                                 int n_pages, int H_kv, int d, int page_size, void* stream);
 
 /*
  * attn_poll_status - synchronise `stream`, then return and clear the first

@@ -1,0 +1,341 @@
+"""The paged key/value cache on the GPU: attention of one new token per sequence against its
+definition in 64 bits (bounds of `oracle/window.py`), and the pages' bookkeeping, writes and copies
+against `oracle/pages.py`, number by number."""
+import math
+import random
+
+import pytest
+import torch
+
+from oracle import window as ref
+from oracle.pages import Pages
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def bss():
+    import block_sparse_softmax_gb300 as m
+    m.library()
+    return m
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Cache:
+    """A filled cache: lengths as given, pages in a random order, garbage (NaN) wherever no token
+    lies.  `inter`: K and V pages interleaved in one tensor."""
+
+    def __init__(self, lens, Hkv, d, page, seed, e4m3=False, inter=False, extra=3, window=0, sinks=0):
+        g = torch.Generator("cuda").manual_seed(seed)
+        S = len(lens)
+        held = [-(-max(0, n) // page) for n in lens]
+        P, M = sum(held) + extra, max(1, max(held)) + 1
+        order = torch.randperm(P, generator=g, device="cuda").tolist()
+        both = torch.full((P, 2, Hkv, page, d), float("nan"), device="cuda")
+        self.k64 = [torch.randn(Hkv, n, d, generator=g, device="cuda") for n in lens]
+        self.v64 = [torch.randn(Hkv, n, d, generator=g, device="cuda") for n in lens]
+        self.k_scale = self.v_scale = None
+        if e4m3:
+            self.k_scale = 0.01 + 0.02 * torch.rand(Hkv, generator=g, device="cuda")
+            self.v_scale = 0.01 + 0.02 * torch.rand(Hkv, generator=g, device="cuda")
+
+        def held_as(x, scale):          # the values the cache holds, and what they stand for
+            if scale is None:
+                return x.bfloat16().float(), x.bfloat16().double()
+            y = (x / scale[:, None, None]).clamp(-448, 448).to(E4M3).float()
+            return y, y.double() * scale.double()[:, None, None]
+
+        self.table = torch.full((S, M), -1, dtype=torch.int32, device="cuda")
+        for s, n in enumerate(lens):
+            kx, self.k64[s] = held_as(self.k64[s], self.k_scale)
+            vx, self.v64[s] = held_as(self.v64[s], self.v_scale)
+            for m in range(held[s]):
+                x = order.pop()
+                a, e = m * page, min(n, (m + 1) * page)
+                # a page that nobody sees any more is not even in the table
+                if window and e <= n - window and a >= sinks:
+                    continue
+                self.table[s, m] = x
+                both[x, 0, :, :e - a] = kx[:, a:e]
+                both[x, 1, :, :e - a] = vx[:, a:e]
+                for j in range(a, e):
+                    if window and j < n - window and j >= sinks:
+                        both[x, :, :, j - a] = float("nan")
+        kind = E4M3 if e4m3 else torch.bfloat16
+        if inter:
+            both = both.to(kind)
+            self.k, self.v = both[:, 0], both[:, 1]
+        else:
+            self.k, self.v = both[:, 0].to(kind).contiguous(), both[:, 1].to(kind).contiguous()
+        self.lens = ints(lens)
+
+
+def check_decode(bss, c, q, lens, window, sinks, **kw):
+    S, H, d = q.shape
+    scale = 1.0 / math.sqrt(d)
+    o, lse = bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens, window=window, sinks=sinks,
+                                   k_scale=c.k_scale, v_scale=c.v_scale, **kw)
+    torch.cuda.synchronize()
+    assert bss.attn_poll_status() == 0
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert torch.all(o[s] == 0) and torch.all(torch.isneginf(lse[s]))
+            continue
+        mask = ref.window_mask(1, n, window or n, sinks, n - 1, 0, "cuda")
+        args = q[s].reshape(1, H, 1, d), c.k64[s][None], c.v64[s][None], mask, scale
+        O, L, _ = ref.forward(*args)
+        bo, bl = ref.forward_bounds(*args)
+        off = (o[s].double() - O[0, :, 0]).abs()
+        assert (off <= bo[0, :, 0]).all(), (s, n, (off / bo[0, :, 0]).max())
+        off = (lse[s].double() - L[0, :, 0]).abs()
+        assert (off <= bl[0, :, 0]).all(), (s, n, (off / bl[0, :, 0]).max())
+    return o, lse
+
+
+CASES = [
+    # lens, H, Hkv, d, page, window, sinks
+    ([1], 1, 1, 128, 16, 0, 0),
+    ([300], 16, 4, 128, 16, 0, 0),
+    ([0, 1, 15, 16, 17, 63, 64, 65, 0, 128, 200], 8, 2, 128, 16, 0, 0),
+    ([0, 0, 0], 4, 4, 64, 32, 0, 0),
+    ([5, 1000, 33, 257, 0, 64], 6, 2, 64, 64, 0, 0),
+    ([777, 12, 2049], 16, 1, 128, 128, 0, 0),      # 16 query heads on one K/V head
+    ([500, 31, 1025], 20, 1, 64, 32, 0, 0),        # ... 20: two groups of rows
+    ([130, 70], 66, 2, 128, 16, 0, 0),             # ... 33
+    ([4000, 1, 2600], 8, 8, 64, 1024, 0, 0),
+    ([20011], 2, 1, 128, 32, 0, 0),                # one sequence over every CTA
+    ([1000, 40, 3, 0, 999], 8, 2, 128, 16, 100, 4),
+    ([1000, 40, 3, 0, 999], 8, 2, 64, 64, 1, 0),   # each token sees itself
+    ([1000, 40, 3, 0, 999], 16, 2, 128, 32, 37, 70),   # sinks past a page
+    ([600, 601, 615, 616], 4, 4, 64, 16, 600, 1),  # the window just falls behind
+    ([900, 17], 9, 3, 128, 64, 10 ** 12, 10 ** 12),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens,H,Hkv,d,page,window,sinks", CASES)
+def test_decode(bss, lens, H, Hkv, d, page, window, sinks, e4m3):
+    c = Cache(lens, Hkv, d, page, sum(lens) + H + page, e4m3, window=window, sinks=sinks)
+    g = torch.Generator("cuda").manual_seed(H + len(lens))
+    q = torch.randn(len(lens), H, d, generator=g, device="cuda").bfloat16()
+    a = check_decode(bss, c, q, lens, window, sinks)
+    b = check_decode(bss, c, q, lens, window, sinks)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_of_many_sequences(bss):
+    rng = random.Random(5)
+    lens = [rng.choice([0, 1, 7, 64, rng.randint(1, 500)]) for _ in range(300)]
+    c = Cache(lens, 2, 64, 16, 9)
+    q = torch.randn(300, 4, 64, device="cuda").bfloat16()
+    check_decode(bss, c, q, lens, 0, 0)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_takes_strided_queries_and_interleaved_caches(bss, e4m3):
+    lens = [70, 0, 333, 18]
+    c = Cache(lens, 2, 128, 32, 3, e4m3, inter=True)
+    qkv = torch.randn(4, 8 + 2 + 2, 128, device="cuda").bfloat16()
+    check_decode(bss, c, qkv[:, :8], lens, 0, 0)
+
+
+def random_pages(rng, S, M, P, page, steps=12):
+    """A state that calls have led to, with shared and evicted pages, beside its host double."""
+    h = Pages(S, M, P, page)
+    for _ in range(steps):
+        x = rng.random()
+        if x < 0.6:
+            h.reserve([rng.choice([0, 1, rng.randint(0, 2 * page)]) for _ in range(S)])
+        elif x < 0.75:
+            empty = [s for s in range(S) if h.lens[s] == 0]
+            full = [s for s in range(S) if h.lens[s]]
+            if empty and full:
+                children = rng.sample(empty, min(len(empty), 3))
+                h.fork([rng.choice(full) for _ in children], children)
+        elif x < 0.9:
+            h.free([rng.randrange(S)])
+        else:
+            h.evict(2 * page, 1)
+    return h
+
+
+def on_gpu(h):
+    return ints(h.table), ints(h.lens), ints(h.refs)
+
+
+def same(h, table, lens, refs):
+    assert table.tolist() == h.table
+    assert lens.tolist() == h.lens
+    assert refs.tolist() == h.refs
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_bookkeeping_follows_the_host(bss, seed):
+    rng = random.Random(seed)
+    S, M, page = rng.choice([(1, 4, 16), (9, 20, 16), (40, 33, 32)])
+    P = rng.choice([S * 3, S * 6, 1500])
+    h = random_pages(rng, S, M, P, page)
+    t, n, r = on_gpu(h)
+    for _ in range(25):
+        x = rng.random()
+        if x < 0.45:
+            new = [rng.choice([0, 1, rng.randint(0, 3 * page)]) for _ in range(S)]
+            want = h.reserve(new)
+            start = bss.attn_kv_reserve(t, n, r, ints(new), page)
+            assert start.tolist() == (want if want is not None else [-1] * S)
+            assert (bss.attn_poll_status() == 0) == (want is not None)
+        elif x < 0.65:
+            empty = [s for s in range(S) if h.lens[s] == 0]
+            rest = [s for s in range(S) if h.lens[s]] or [s for s in range(S) if s not in empty[:1]]
+            children = rng.sample(empty, min(len(empty), rng.randint(1, 4)))
+            rest = [s for s in rest if s not in children]
+            if not children or not rest:
+                continue
+            parents = [rng.choice(rest) for _ in children]
+            want = h.fork(parents, children)
+            src, dst = bss.attn_kv_fork(t, n, r, ints(parents), ints(children), page)
+            none = [-1] * len(children)
+            assert (src.tolist(), dst.tolist()) == (want if want is not None else (none, none))
+            assert bss.attn_poll_status() == (0 if want is not None else bss.ERR_NO_PAGES)
+        elif x < 0.8:
+            seqs = [rng.randrange(S) for _ in range(rng.randint(1, 4))]
+            seqs.append(seqs[0])                       # listed twice: freed once
+            h.free(seqs)
+            bss.attn_kv_free(t, n, r, ints(seqs), page)
+            assert bss.attn_poll_status() == 0
+        elif x < 0.9:
+            w, k = rng.randint(1, 4 * page), rng.choice([0, 1, 4, page + 1])
+            h.evict(w, k)
+            bss.attn_kv_evict(t, n, r, w, k, page)
+            assert bss.attn_poll_status() == 0
+        else:
+            src, dst = h.compact()
+            a, b, count = bss.attn_kv_compact(t, r)
+            assert count.tolist() == [len(src)]
+            tail = [-1] * (P - len(src))
+            assert a.tolist() == src + tail and b.tolist() == dst + tail
+            assert bss.attn_poll_status() == 0
+        same(h, t, n, r)
+
+
+@pytest.mark.parametrize("e4m3,Hkv,d,page", [(False, 2, 128, 16), (False, 3, 64, 64),
+                                             (True, 2, 64, 16), (True, 1, 128, 128)])
+def test_write_and_copy(bss, e4m3, Hkv, d, page):
+    rng = random.Random(page + d)
+    h = random_pages(rng, 7, 12, 60, page)
+    t, n, r = on_gpu(h)
+    kind, word = (E4M3, torch.uint8) if e4m3 else (torch.bfloat16, torch.int16)
+    both = torch.randint(-100, 100, (60, 2, Hkv, page, d), device="cuda").to(kind)
+    scales = [0.01 + torch.rand(Hkv, device="cuda") for _ in range(2)] if e4m3 else [None, None]
+    new = [rng.choice([0, 1, rng.randint(0, page)]) for _ in range(7)]
+    start = bss.attn_kv_reserve(t, n, r, ints(new), page)
+    assert h.reserve(new) == start.tolist()
+    cu = [2]                                           # rows before and behind them are left out
+    for x in new:
+        cu.append(cu[-1] + x)
+    total = cu[-1] + 5
+    qkv = 30 * torch.randn(total, 3 * Hkv, d, device="cuda").bfloat16()
+    qkv[cu[0], Hkv:] = float("nan")                    # a NaN stays one, and
+    qkv[cu[0] + 1:cu[0] + 2, Hkv:] = float("inf")      # in e4m3 infinity is 448
+    k_new, v_new = qkv[:, Hkv:2 * Hkv], qkv[:, 2 * Hkv:]
+    want = both.clone()
+    for s, x in enumerate(new):
+        for i in range(x):
+            pos = start.tolist()[s] + i
+            at = h.table[s][pos // page]
+            for j, (src, scale) in enumerate(zip((k_new, v_new), scales)):
+                row = src[cu[s] + i]
+                if e4m3:
+                    row = (row.float() / scale[:, None]).clamp(-448, 448).to(E4M3)
+                want.view(word)[at, j, :, pos % page] = row.contiguous().view(word)
+    bss.attn_kv_write(k_new, v_new, both[:, 0], both[:, 1], t, start, ints(cu), k_scale=scales[0],
+                      v_scale=scales[1])
+    assert bss.attn_poll_status() == 0
+    assert torch.equal(both.view(word), want.view(word))
+    # copies: pairs, none, and a count that cuts the list
+    src, dst = [3, -1, 7, 3, 9], [50, -1, 51, 52, 53]
+    for count in (None, 4):
+        for a, b in list(zip(src, dst))[:count]:
+            if a >= 0:
+                want.view(word)[b] = want.view(word)[a]
+        bss.attn_kv_copy_pages(both[:, 0], both[:, 1], ints(src), ints(dst),
+                               None if count is None else ints([count]))
+        assert bss.attn_poll_status() == 0
+        assert torch.equal(both.view(word), want.view(word))
+        both.view(word)[53] = 0
+        want.view(word)[53] = 0
+
+
+def test_serving_run(bss):
+    """Prompts through the windowed forward, then decoding steps over pages with eviction, forks
+    and a compaction in between: every token's output as the windowed forward gives it for the
+    whole sequence."""
+    g = torch.Generator("cuda").manual_seed(11)
+    H, Hkv, d, page, window, sinks, rows = 4, 2, 64, 16, 40, 3, 6
+    prompts, steps = [70, 5, 33], 60
+    P, M = 60, 12
+    table, lens, refs = ints([[-1] * M] * rows), ints([0] * rows), ints([0] * P)
+    kc, vc = (torch.full((P, Hkv, page, d), float("nan"), device="cuda").bfloat16() for _ in range(2))
+    seqs = {}                                          # row -> (q, k, v) of its tokens so far
+
+    def draw(n):
+        return [torch.randn(x, n, d, generator=g, device="cuda").bfloat16() for x in (H, Hkv, Hkv)]
+
+    for s, n in enumerate(prompts):
+        seqs[s] = draw(n)
+
+    def put(news):
+        """The newest news[s] tokens of every row into the cache."""
+        cu = [0]
+        for x in news:
+            cu.append(cu[-1] + x)
+        k_new = torch.cat([seqs[s][1][:, -x:].transpose(0, 1) for s, x in enumerate(news) if x])
+        v_new = torch.cat([seqs[s][2][:, -x:].transpose(0, 1) for s, x in enumerate(news) if x])
+        start = bss.attn_kv_reserve(table, lens, refs, ints(news), page)
+        bss.attn_kv_write(k_new.contiguous(), v_new.contiguous(), kc, vc, table, start, ints(cu))
+
+    put(prompts + [0] * (rows - 3))
+    for step in range(steps):
+        if step == 20:
+            src, dst = bss.attn_kv_fork(table, lens, refs, ints([0, 0]), ints([3, 5]), page)
+            bss.attn_kv_copy_pages(kc, vc, src, dst)
+            seqs[3], seqs[5] = [x.clone() for x in seqs[0]], [x.clone() for x in seqs[0]]
+        if step == 30:
+            bss.attn_kv_free(table, lens, refs, ints([0]), page)
+            del seqs[0]
+        if step in (35, 50):
+            src, dst, count = bss.attn_kv_compact(table, refs)
+            bss.attn_kv_copy_pages(kc, vc, src, dst, count)
+            live = int((refs > 0).sum())
+            assert torch.all(refs[:live] > 0)
+        bss.attn_kv_evict(table, lens, refs, window, sinks, page)
+        for s in seqs:
+            seqs[s] = [torch.cat([a, b], 1) for a, b in zip(seqs[s], draw(1))]
+        put([1 if s in seqs else 0 for s in range(rows)])
+        q = torch.zeros(rows, H, d, device="cuda").bfloat16()
+        for s in seqs:
+            q[s] = seqs[s][0][:, -1]
+        o, lse = bss.attn_decode_paged(q, kc, vc, table, lens, window=window, sinks=sinks)
+        assert bss.attn_poll_status() == 0
+        for s in range(rows):
+            if s not in seqs:
+                assert torch.all(o[s] == 0)
+                continue
+            n = seqs[s][0].shape[1]
+            assert int(lens[s]) == n
+            args = [x[None] for x in seqs[s]]
+            mask = ref.window_mask(1, n, window, sinks, n - 1, 0, "cuda")
+            O, L, _ = ref.forward(args[0][:, :, -1:], *args[1:], mask, d ** -0.5)
+            bo, bl = ref.forward_bounds(args[0][:, :, -1:], *args[1:], mask, d ** -0.5)
+            assert ((o[s].double() - O[0, :, 0]).abs() <= bo[0, :, 0]).all(), (step, s)
+            assert ((lse[s].double() - L[0, :, 0]).abs() <= bl[0, :, 0]).all()
+            if step == steps - 1:
+                whole, _ = bss.attn_fwd_window(*[x.contiguous() for x in args], window, sinks=sinks)
+                assert ((whole[0, :, -1].double() - O[0, :, 0]).abs() <= bo[0, :, 0]).all()
+    held = sum(len({int(x) for x in table[s] if x >= 0}) for s in seqs)
+    assert held <= 5 * (-(-window // page) + 2)        # memory stays bounded by window and sinks

@@ -13,74 +13,77 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _lib, _need, _scale, _stream_of
-from ._window import _same_device
+from . import _lib, _need, _scale
+from ._window import _is, _run, _workspace
 
 KV_BF16 = 0
 KV_E4M3 = 1
-_KV_DTYPES = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3}
+_INT, _BF16, _FP32, _E4M3 = torch.int32, torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
-def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale, v_scale, scales: bool = True):
-    """(n_pages, H_kv, page_size, d, dtype code, page strides) of a checked cache."""
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int):
+    """(k address, v address, k page stride, v page stride, dtype code) of a checked cache."""
+    kind, shape = k_cache.dtype, k_cache.shape
+    if kind is not _BF16 and kind is not _E4M3:
+        raise ValueError(f"k_cache must be torch.bfloat16 or torch.float8_e4m3fn, got {kind}")
+    if len(shape) != 4:
+        raise ValueError("k_cache must have 4 dimensions [n_pages, H_kv, page_size, d]")
+    if v_cache.dtype is not kind or v_cache.shape != shape:
+        raise ValueError(f"v_cache must be {kind} of shape {tuple(shape)}, got {v_cache.dtype} of "
+                         f"{tuple(v_cache.shape)}")
+    P, Hkv, page, d = shape
+    strides = []
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype not in _KV_DTYPES:
-            raise ValueError(f"{name} must be torch.bfloat16 or torch.float8_e4m3fn, got {t.dtype}")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must have 4 dimensions [n_pages, H_kv, page_size, d]")
-        if t.shape[0] > 0 and not t[0].is_contiguous():
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{name} must be a CUDA tensor on the call's device, got {t.device}")
+        if t.is_contiguous():
+            strides.append(Hkv * page * d)
+        elif P > 1 and t[0].is_contiguous():
+            strides.append(t.stride(0))
+        else:
             raise ValueError(f"a page of {name} must be contiguous")
-    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
-        raise ValueError(f"v_cache must be {k_cache.dtype} of shape {tuple(k_cache.shape)}, got "
-                         f"{v_cache.dtype} of {tuple(v_cache.shape)}")
-    P, Hkv, page, d = k_cache.shape
-    if scales:
-        if (k_cache.dtype == torch.float8_e4m3fn) != (k_scale is not None) or (
-                k_scale is None) != (v_scale is None):
-            raise ValueError("k_scale and v_scale belong to e4m3 caches, and to no others")
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is not None:
-                _need(t, name, torch.float32, (Hkv,))
-    _same_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    # a single page has no distance to the next
-    ks = k_cache.stride(0) if P > 1 else Hkv * page * d
-    vs = v_cache.stride(0) if P > 1 else Hkv * page * d
-    return P, Hkv, page, d, _KV_DTYPES[k_cache.dtype], ks, vs
+    return (k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1],
+            KV_BF16 if kind is _BF16 else KV_E4M3)
+
+
+def _scales(code: int, k_scale, v_scale, Hkv: int, dev: int):
+    """The scales' addresses: both for an e4m3 cache, none for a bf16 one."""
+    if code == KV_BF16:
+        if k_scale is None and v_scale is None:
+            return None, None
+    elif k_scale is not None and v_scale is not None:
+        return (_is(k_scale, "k_scale", _FP32, (Hkv,), dev),
+                _is(v_scale, "v_scale", _FP32, (Hkv,), dev))
+    raise ValueError("k_scale and v_scale belong to e4m3 caches, both of them, and to no others")
+
+
+def _table(page_table: torch.Tensor, dev: int):
+    """(address, rows, max_pages) of a checked page table."""
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have 2 dimensions [S, max_pages]")
+    shape = page_table.shape
+    return _is(page_table, "page_table", _INT, shape, dev), shape[0], shape[1]
 
 
 def _state(page_table, seq_lens, refs):
-    """(S, max_pages, n_pages) of a checked page table, lengths (or None) and counts (or None)."""
-    if page_table.dim() != 2:
-        raise ValueError("page_table must have 2 dimensions [S, max_pages]")
-    S, M = page_table.shape
-    _need(page_table, "page_table", torch.int32, (S, M))
-    if seq_lens is not None:
-        _need(seq_lens, "seq_lens", torch.int32, (S,))
-    P = 0
-    if refs is not None:
-        P = refs.numel()
-        _need(refs, "refs", torch.int32, (P,))
-    _same_device(page_table.device, seq_lens=seq_lens, refs=refs)
-    return S, M, P
+    """(device, table, lengths and counts addresses, S, max_pages, n_pages) of a checked state."""
+    dev = page_table.get_device()
+    tp, S, M = _table(page_table, dev)
+    P = refs.numel()
+    return (dev, tp, _is(seq_lens, "seq_lens", _INT, (S,), dev), _is(refs, "refs", _INT, (P,), dev),
+            S, M, P)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _rows(t: torch.Tensor, name: str, shape: Tuple[int, int, int]) -> int:
+def _rows(t: torch.Tensor, name: str, shape: Tuple[int, int, int], dev: int) -> int:
     """The row stride of a bf16 [n, heads, d] tensor whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if shape[0] > 0 and not t[0].is_contiguous():
+    if t.get_device() == dev and t.dtype is _BF16 and t.shape == shape:
+        if t.is_contiguous() or shape[0] == 0:
+            return shape[1] * shape[2]
+        if t[0].is_contiguous():
+            return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
         raise ValueError(f"a row of {name} must be contiguous")
-    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+    _need(t, name, _BF16, shape)
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
 def attn_decode_paged_workspace_bytes(S: int, H: int, H_kv: int, d: int) -> int:
@@ -96,33 +99,26 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int 
     ``window`` positions and the first ``sinks`` ones, with 0 every one.  A sequence of length 0
     gets O = 0, LSE = -inf.  The table may have more rows than q has sequences: they are ignored,
     and so are the lengths past the S-th."""
-    P, Hkv, page, d, code, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale)
+    dev = q.get_device()
+    kp, vp, ks, vs, code = _cache(k_cache, v_cache, dev)
+    P, Hkv, page, d = k_cache.shape
     if q.dim() != 3:
         raise ValueError("q must have 3 dimensions [S, H, d]")
     S, H = q.shape[0], q.shape[1]
-    q_stride = _rows(q, "q", (S, H, d))
-    rows, M, _ = _state(page_table, seq_lens, None)
+    q_stride = _rows(q, "q", (S, H, d), dev)
+    ksp, vsp = _scales(code, k_scale, v_scale, Hkv, dev)
+    tp, rows, M = _table(page_table, dev)
     if rows < S:
         raise ValueError(f"page_table has {rows} rows for {S} sequences")
-    out = torch.empty((S, H, d), device=q.device, dtype=torch.bfloat16) if out is None else out
-    lse = torch.empty((S, H), device=q.device, dtype=torch.float32) if lse is None else lse
-    _need(out, "out", torch.bfloat16, (S, H, d))
-    _need(lse, "lse", torch.float32, (S, H))
-    if workspace is None:
-        nbytes = attn_decode_paged_workspace_bytes(S, H, Hkv, d)
-        workspace = torch.empty(max(16, nbytes), device=q.device, dtype=torch.uint8)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _same_device(q.device, k_cache=k_cache, page_table=page_table, out=out, lse=lse,
-                 workspace=workspace)
-    with torch.cuda.device(q.device):
-        st = _lib.load().attn_decode_paged(
-            q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, code,
-            _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), seq_lens.data_ptr(),
-            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), S, H, Hkv, d, M, P, page,
-            _scale(scale, d), int(window), int(sinks), _stream_of(q))
-    _check(st, "attn_decode_paged")
+    lp = _is(seq_lens, "seq_lens", _INT, (rows,), dev)
+    out = torch.empty((S, H, d), dtype=_BF16, device=q.device) if out is None else out
+    lse = torch.empty((S, H), dtype=_FP32, device=q.device) if lse is None else lse
+    ws = _workspace(workspace, 0 if workspace is not None else attn_decode_paged_workspace_bytes(
+        S, H, Hkv, d), q)
+    _run("attn_decode_paged", dev, q.data_ptr(), q_stride, kp, vp, ks, vs, code, ksp, vsp, tp, lp,
+         _is(out, "out", _BF16, (S, H, d), dev), _is(lse, "lse", _FP32, (S, H), dev), ws.data_ptr(),
+         ws.numel() * ws.element_size(), S, H, Hkv, d, M, P, page, _scale(scale, d), int(window),
+         int(sinks))
     return out, lse
 
 
@@ -131,19 +127,14 @@ def attn_kv_reserve(page_table, seq_lens, refs, n_new, page_size: int, *, start=
     of each sequence's first new token, or -1 throughout when the call was refused (then nothing
     changed, and attn_poll_status says why).  n_new may be shorter than the table: the other
     sequences get none."""
-    S, M, P = _state(page_table, seq_lens, refs)
+    dev, tp, lp, rp, S, M, P = _state(page_table, seq_lens, refs)
     n = n_new.numel()
-    _need(n_new, "n_new", torch.int32, (n,))
+    np_ = _is(n_new, "n_new", _INT, (n,), dev)
     if n > S:
         raise ValueError(f"n_new has {n} entries for {S} sequences")
-    start = torch.empty((n,), device=page_table.device, dtype=torch.int32) if start is None else start
-    _need(start, "start", torch.int32, (n,))
-    _same_device(page_table.device, n_new=n_new, start=start)
-    with torch.cuda.device(page_table.device):
-        st = _lib.load().attn_kv_reserve(page_table.data_ptr(), seq_lens.data_ptr(),
-                                         refs.data_ptr(), n_new.data_ptr(), start.data_ptr(), n, M,
-                                         P, int(page_size), _stream_of(page_table))
-    _check(st, "attn_kv_reserve")
+    start = torch.empty_like(n_new) if start is None else start
+    _run("attn_kv_reserve", dev, tp, lp, rp, np_, _is(start, "start", _INT, (n,), dev), n, M, P,
+         int(page_size))
     return start
 
 
@@ -153,24 +144,20 @@ def attn_kv_write(k_new, v_new, k_cache, v_cache, page_table, start, cu_new, *, 
     and v_new [T,H_kv,d] bf16 (rows may be strided) become sequence s's tokens start[s], ...;
     rows from cu_new[S] on are left out.  An e4m3 cache gets round(x / scale[h]), saturated at
     448."""
-    P, Hkv, page, d, code, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.get_device()
+    kp, vp, ks, vs, code = _cache(k_cache, v_cache, dev)
+    P, Hkv, page, d = k_cache.shape
     T = k_new.shape[0]
-    k_row = _rows(k_new, "k_new", (T, Hkv, d))
-    v_row = _rows(v_new, "v_new", (T, Hkv, d))
-    rows, M, _ = _state(page_table, None, None)
+    k_row = _rows(k_new, "k_new", (T, Hkv, d), dev)
+    v_row = _rows(v_new, "v_new", (T, Hkv, d), dev)
+    ksp, vsp = _scales(code, k_scale, v_scale, Hkv, dev)
+    tp, rows, M = _table(page_table, dev)
     S = start.numel()
     if rows < S:
         raise ValueError(f"page_table has {rows} rows for {S} sequences")
-    _need(start, "start", torch.int32, (S,))
-    _need(cu_new, "cu_new", torch.int32, (S + 1,))
-    _same_device(k_cache.device, k_new=k_new, v_new=v_new, page_table=page_table, start=start,
-                 cu_new=cu_new)
-    with torch.cuda.device(k_cache.device):
-        st = _lib.load().attn_kv_write(
-            k_new.data_ptr(), v_new.data_ptr(), k_row, v_row, k_cache.data_ptr(),
-            v_cache.data_ptr(), ks, vs, code, _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(),
-            start.data_ptr(), cu_new.data_ptr(), T, S, M, P, Hkv, d, page, _stream_of(k_cache))
-    _check(st, "attn_kv_write")
+    _run("attn_kv_write", dev, k_new.data_ptr(), v_new.data_ptr(), k_row, v_row, kp, vp, ks, vs, code,
+         ksp, vsp, tp, _is(start, "start", _INT, (S,), dev),
+         _is(cu_new, "cu_new", _INT, (S + 1,), dev), T, S, M, P, Hkv, d, page)
 
 
 def attn_kv_fork(page_table, seq_lens, refs, parents, children, page_size: int, *, copy_src=None,
@@ -179,67 +166,46 @@ def attn_kv_fork(page_table, seq_lens, refs, parents, children, page_size: int, 
     that is not full the child takes its own: returns (copy_src, copy_dst) [F] int32, the copies
     to make with attn_kv_copy_pages in every layer's cache (-1: none).  A child must be empty,
     occur once and not be a parent too."""
-    S, M, P = _state(page_table, seq_lens, refs)
+    dev, tp, lp, rp, S, M, P = _state(page_table, seq_lens, refs)
     F = parents.numel()
-    dev = page_table.device
-    copy_src = torch.empty((F,), device=dev, dtype=torch.int32) if copy_src is None else copy_src
-    copy_dst = torch.empty((F,), device=dev, dtype=torch.int32) if copy_dst is None else copy_dst
-    for name, t in (("parents", parents), ("children", children), ("copy_src", copy_src),
-                    ("copy_dst", copy_dst)):
-        _need(t, name, torch.int32, (F,))
-    _same_device(dev, parents=parents, children=children, copy_src=copy_src, copy_dst=copy_dst)
-    with torch.cuda.device(dev):
-        st = _lib.load().attn_kv_fork(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
-                                      parents.data_ptr(), children.data_ptr(), F,
-                                      copy_src.data_ptr(), copy_dst.data_ptr(), S, M, P,
-                                      int(page_size), _stream_of(page_table))
-    _check(st, "attn_kv_fork")
+    pp = _is(parents, "parents", _INT, (F,), dev)
+    cp = _is(children, "children", _INT, (F,), dev)
+    copy_src = torch.empty_like(parents) if copy_src is None else copy_src
+    copy_dst = torch.empty_like(parents) if copy_dst is None else copy_dst
+    _run("attn_kv_fork", dev, tp, lp, rp, pp, cp, F, _is(copy_src, "copy_src", _INT, (F,), dev),
+         _is(copy_dst, "copy_dst", _INT, (F,), dev), S, M, P, int(page_size))
     return copy_src, copy_dst
 
 
 def attn_kv_free(page_table, seq_lens, refs, seqs, page_size: int) -> None:
     """The listed sequences (int32) give back their pages and become empty; one that is listed
     twice is freed once."""
-    S, M, P = _state(page_table, seq_lens, refs)
+    dev, tp, lp, rp, S, M, P = _state(page_table, seq_lens, refs)
     n = seqs.numel()
-    _need(seqs, "seqs", torch.int32, (n,))
-    _same_device(page_table.device, seqs=seqs)
-    with torch.cuda.device(page_table.device):
-        st = _lib.load().attn_kv_free(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
-                                      seqs.data_ptr(), n, S, M, P, int(page_size),
-                                      _stream_of(page_table))
-    _check(st, "attn_kv_free")
+    _run("attn_kv_free", dev, tp, lp, rp, _is(seqs, "seqs", _INT, (n,), dev), n, S, M, P,
+         int(page_size))
 
 
 def attn_kv_evict(page_table, seq_lens, refs, window: int, sinks: int, page_size: int) -> None:
     """Every sequence gives back the pages that attn_decode_paged with this window and sinks no
     longer reads, now or at a greater length."""
-    S, M, P = _state(page_table, seq_lens, refs)
-    with torch.cuda.device(page_table.device):
-        st = _lib.load().attn_kv_evict(page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
-                                       int(window), int(sinks), S, M, P, int(page_size),
-                                       _stream_of(page_table))
-    _check(st, "attn_kv_evict")
+    dev, tp, lp, rp, S, M, P = _state(page_table, seq_lens, refs)
+    _run("attn_kv_evict", dev, tp, lp, rp, int(window), int(sinks), S, M, P, int(page_size))
 
 
 def attn_kv_compact(page_table, refs, *, copy_src=None, copy_dst=None, count=None):
     """The pages in use move to the lowest indices; table and counts follow.  Returns (copy_src,
     copy_dst [n_pages], count [1]) int32: the copies to make with attn_kv_copy_pages in every
     layer's cache."""
-    S, M, P = _state(page_table, None, refs)
-    dev = page_table.device
-    copy_src = torch.empty((P,), device=dev, dtype=torch.int32) if copy_src is None else copy_src
-    copy_dst = torch.empty((P,), device=dev, dtype=torch.int32) if copy_dst is None else copy_dst
-    count = torch.empty((1,), device=dev, dtype=torch.int32) if count is None else count
-    _need(copy_src, "copy_src", torch.int32, (P,))
-    _need(copy_dst, "copy_dst", torch.int32, (P,))
-    _need(count, "count", torch.int32, (1,))
-    _same_device(dev, copy_src=copy_src, copy_dst=copy_dst, count=count)
-    with torch.cuda.device(dev):
-        st = _lib.load().attn_kv_compact(page_table.data_ptr(), refs.data_ptr(),
-                                         copy_src.data_ptr(), copy_dst.data_ptr(),
-                                         count.data_ptr(), S, M, P, _stream_of(page_table))
-    _check(st, "attn_kv_compact")
+    dev = page_table.get_device()
+    tp, S, M = _table(page_table, dev)
+    P = refs.numel()
+    rp = _is(refs, "refs", _INT, (P,), dev)
+    copy_src = torch.empty_like(refs) if copy_src is None else copy_src
+    copy_dst = torch.empty_like(refs) if copy_dst is None else copy_dst
+    count = torch.empty((1,), dtype=_INT, device=refs.device) if count is None else count
+    _run("attn_kv_compact", dev, tp, rp, _is(copy_src, "copy_src", _INT, (P,), dev),
+         _is(copy_dst, "copy_dst", _INT, (P,), dev), _is(count, "count", _INT, (1,), dev), S, M, P)
     return copy_src, copy_dst, count
 
 
@@ -247,15 +213,11 @@ def attn_kv_copy_pages(k_cache, v_cache, copy_src, copy_dst, count=None) -> None
     """Page copy_src[i] of both caches to page copy_dst[i], for every i (the first ``count[0]`` of
     them when ``count``, int32 on the device, is given); a pair of two negative entries is left
     out.  No page may be both a source and a destination, and a destination may occur once."""
-    P, Hkv, page, d, code, ks, vs = _cache(k_cache, v_cache, None, None, scales=False)
+    dev = k_cache.get_device()
+    kp, vp, ks, vs, code = _cache(k_cache, v_cache, dev)
+    P, Hkv, page, d = k_cache.shape
     n = copy_src.numel()
-    _need(copy_src, "copy_src", torch.int32, (n,))
-    _need(copy_dst, "copy_dst", torch.int32, (n,))
-    if count is not None:
-        _need(count, "count", torch.int32, (1,))
-    _same_device(k_cache.device, copy_src=copy_src, copy_dst=copy_dst, count=count)
-    with torch.cuda.device(k_cache.device):
-        st = _lib.load().attn_kv_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, code,
-                                            copy_src.data_ptr(), copy_dst.data_ptr(), n,
-                                            _ptr(count), P, Hkv, d, page, _stream_of(k_cache))
-    _check(st, "attn_kv_copy_pages")
+    cp = None if count is None else _is(count, "count", _INT, (1,), dev)
+    _run("attn_kv_copy_pages", dev, kp, vp, ks, vs, code,
+         _is(copy_src, "copy_src", _INT, (n,), dev), _is(copy_dst, "copy_dst", _INT, (n,), dev), n,
+         cp, P, Hkv, d, page)

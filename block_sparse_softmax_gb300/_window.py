@@ -5,13 +5,42 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _lib, _need, _scale, _stream_of
+from . import OK, AttnError, _lib, _need, _scale
+
+# These calls serve single tokens, where the host's share of a call counts: the checks below cost
+# a few attribute reads per tensor where all is well, and look for what is wrong only where it is
+# not.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _same_device(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _is(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
+    """The address of a contiguous CUDA tensor of this type and shape on this device."""
+    if (t.get_device() != device or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _run(name: str, device: int, *args) -> None:
+    """One library call on the device's current stream; raises on a status other than OK."""
+    fn = getattr(_lib.load(), name)
+    if device == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(device))
+    if st != OK:
+        raise AttnError(st, name)
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> torch.Tensor:
+    """The caller's workspace, checked, or a new one of ``nbytes``."""
+    if workspace is None:
+        return torch.empty(max(16, nbytes), dtype=torch.uint8, device=like.device)
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace
 
 
 def attn_fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, *,
@@ -23,22 +52,17 @@ def attn_fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: i
     last ``window`` positions up to its own and the sequence's first ``sinks`` positions.
     k and v may have fewer heads than q (grouped query heads).  A query that sees no key gets
     O = 0, LSE = -inf."""
-    B, H, Lq, d = q.shape
+    B, H, Lq, d = q_shape = q.shape
     Hkv, Lk = k.shape[1], k.shape[2]
-    _need(q, "q", torch.bfloat16, (B, H, Lq, d))
-    _need(k, "k", torch.bfloat16, (B, Hkv, Lk, d))
-    _need(v, "v", torch.bfloat16, (B, Hkv, Lk, d))
+    dev, bf16, fp32 = q.get_device(), torch.bfloat16, torch.float32
+    qp = _is(q, "q", bf16, q_shape, dev)
+    kp = _is(k, "k", bf16, (B, Hkv, Lk, d), dev)
+    vp = _is(v, "v", bf16, (B, Hkv, Lk, d), dev)
     out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, H, Lq), device=q.device, dtype=torch.float32) if lse is None else lse
-    _need(out, "out", torch.bfloat16, (B, H, Lq, d))
-    _need(lse, "lse", torch.float32, (B, H, Lq))
-    _same_device(q.device, k=k, v=v, out=out, lse=lse)
-    with torch.cuda.device(q.device):
-        st = _lib.load().attn_fwd_window(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv,
-            Lq, Lk, d, _scale(scale, d), int(window), int(sinks), int(q_offset), int(k_offset),
-            _stream_of(q))
-    _check(st, "attn_fwd_window")
+    lse = torch.empty((B, H, Lq), dtype=fp32, device=q.device) if lse is None else lse
+    _run("attn_fwd_window", dev, qp, kp, vp, _is(out, "out", bf16, q_shape, dev),
+         _is(lse, "lse", fp32, (B, H, Lq), dev), B, H, Hkv, Lq, Lk, d, _scale(scale, d), int(window),
+         int(sinks), int(q_offset), int(k_offset))
     return out, lse
 
 
@@ -57,33 +81,23 @@ def attn_bwd_window(q, k, v, o, lse, dout, window: int, *, sinks: int = 0,
     """Gradients (dq, dk, dv) bf16 of attn_fwd_window with the same window, sinks, offsets and
     scale, and delta = rowsum(dO * O) fp32, by recomputation.  dk and dv are the same in every
     run; dq's last bit may differ (fp32 additions in the order the key tiles finish)."""
-    B, H, Lq, d = q.shape
+    B, H, Lq, d = q_shape = q.shape
     Hkv, Lk = k.shape[1], k.shape[2]
-    for name, t in (("q", q), ("o", o), ("dout", dout)):
-        _need(t, name, torch.bfloat16, (B, H, Lq, d))
-    for name, t in (("k", k), ("v", v)):
-        _need(t, name, torch.bfloat16, (B, Hkv, Lk, d))
-    _need(lse, "lse", torch.float32, (B, H, Lq))
+    k_shape, rows = (B, Hkv, Lk, d), (B, H, Lq)
+    dev, bf16, fp32 = q.get_device(), torch.bfloat16, torch.float32
+    qp, op = _is(q, "q", bf16, q_shape, dev), _is(o, "o", bf16, q_shape, dev)
+    dop = _is(dout, "dout", bf16, q_shape, dev)
+    kp, vp = _is(k, "k", bf16, k_shape, dev), _is(v, "v", bf16, k_shape, dev)
+    lp = _is(lse, "lse", fp32, rows, dev)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    delta = torch.empty((B, H, Lq), device=q.device, dtype=torch.float32) if delta is None else delta
-    _need(dq, "dq", torch.bfloat16, (B, H, Lq, d))
-    _need(dk, "dk", torch.bfloat16, (B, Hkv, Lk, d))
-    _need(dv, "dv", torch.bfloat16, (B, Hkv, Lk, d))
-    _need(delta, "delta", torch.float32, (B, H, Lq))
-    nbytes = attn_bwd_window_workspace_bytes(B, H, Hkv, Lq, Lk, d, window, sinks, q_offset, k_offset)
-    if workspace is None:
-        workspace = torch.empty(max(16, nbytes), device=q.device, dtype=torch.uint8)
-    _same_device(q.device, k=k, v=v, o=o, lse=lse, dout=dout, dq=dq, dk=dk, dv=dv, delta=delta,
-                 workspace=workspace)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    with torch.cuda.device(q.device):
-        st = _lib.load().attn_bwd_window(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
-            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), delta.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), B, H, Hkv, Lq, Lk, d, _scale(scale, d),
-            int(window), int(sinks), int(q_offset), int(k_offset), _stream_of(q))
-    _check(st, "attn_bwd_window")
+    delta = torch.empty_like(lse) if delta is None else delta
+    window, sinks, q_offset, k_offset = int(window), int(sinks), int(q_offset), int(k_offset)
+    ws = _workspace(workspace, 0 if workspace is not None else attn_bwd_window_workspace_bytes(
+        B, H, Hkv, Lq, Lk, d, window, sinks, q_offset, k_offset), q)
+    _run("attn_bwd_window", dev, qp, kp, vp, op, lp, dop, _is(dq, "dq", bf16, q_shape, dev),
+         _is(dk, "dk", bf16, k_shape, dev), _is(dv, "dv", bf16, k_shape, dev),
+         _is(delta, "delta", fp32, rows, dev), ws.data_ptr(), ws.numel() * ws.element_size(), B, H,
+         Hkv, Lq, Lk, d, _scale(scale, d), window, sinks, q_offset, k_offset)
     return dq, dk, dv, delta

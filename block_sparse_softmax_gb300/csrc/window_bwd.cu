@@ -1,7 +1,7 @@
 // attn_bwd_window: gradients of attn_fwd_window by recomputation.
 //
 // Mathematics (window.cuh has the mask; sums run over the allowed pairs):
-//   D_i  = dO_i . O_i
+//   D_i  = dO_i . O_i  (= sum_j P_ij dO_i . V_j)
 //   P_ij = exp(scale q_i . k_j - LSE_i)
 //   dV_j = sum_i P_ij dO_i
 //   dS_ij = scale P_ij (dO_i . V_j - D_i)
@@ -27,7 +27,13 @@
 namespace bss {
 namespace {
 
+// Rows that see at most this many keys get D from its definition (below).
+constexpr int kFewKeys = 16;
+
 struct WindowBwdParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
   int B, H, Hkv, Lq, Lk;
   float scale, scale_log2;
   WindowMask w;
@@ -762,7 +768,43 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
   }
 }
 
-// D_i = dO_i . O_i for every row, and the fp32 dQ accumulator cleared.
+// The keys query row i sees: the sinks below the window, [0, nsk), and the
+// window's [lo, lo + nw).
+struct RowKeys {
+  int nsk, lo, nw;
+};
+__device__ __forceinline__ RowKeys window_row_keys(const WindowBwdParams& p, int i) {
+  const long long own = static_cast<long long>(i) + p.w.sh;          // the row's own key
+  const long long hi = min(own, static_cast<long long>(p.Lk) - 1);
+  const long long lo = max(0ll, min(own - p.w.window + 1, static_cast<long long>(p.Lk)));
+  RowKeys r;
+  r.lo = static_cast<int>(lo);
+  r.nw = static_cast<int>(max(0ll, hi - lo + 1));
+  r.nsk = own < 0 ? 0 : static_cast<int>(min(static_cast<long long>(p.w.snk), min(lo, own + 1)));
+  return r;
+}
+
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float s) {
+  s = fmaf(bf16lo(a.x), bf16lo(b.x), s);
+  s = fmaf(bf16hi(a.x), bf16hi(b.x), s);
+  s = fmaf(bf16lo(a.y), bf16lo(b.y), s);
+  s = fmaf(bf16hi(a.y), bf16hi(b.y), s);
+  s = fmaf(bf16lo(a.z), bf16lo(b.z), s);
+  s = fmaf(bf16hi(a.z), bf16hi(b.z), s);
+  s = fmaf(bf16lo(a.w), bf16lo(b.w), s);
+  return fmaf(bf16hi(a.w), bf16hi(b.w), s);
+}
+
+// D_i for every row, and the fp32 dQ accumulator cleared.
+//
+// D_i = dO_i . O_i uses the saved O, rounded to bf16, so it is off by up to
+// 2^-8 |dO_i| . |O_i|.  Over many keys O averages out and that is small beside
+// the dP_ij = dO_i . V_j it is subtracted from; over a few keys it is as large
+// as dQ's own rounding, and more where one key has nearly all of the weight
+// (with 3 keys dQ came out 6.9e-3 off, with exact D 2.9e-3).  Rows that see at
+// most 16 keys therefore take the definition, D_i = sum_j P_ij dP_ij, in fp32:
+// a warp a row, two lanes a key.  They are the first rows of a sequence, or
+// all of them when window and sinks together are that few.
 template <int D>
 __global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBwdParams p) {
   constexpr int G = D / 8;                           // threads per row, 16 bytes each
@@ -774,20 +816,59 @@ __global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBw
     const bool active = r < rows;
     if (__all_sync(0xFFFFFFFFu, !active)) break;     // every lane of the warp is done
     uint4 o = make_uint4(0u, 0u, 0u, 0u), d = o;
+    bool few = false;
     if (active) {
       o = __ldg(reinterpret_cast<const uint4*>(p.o + r * D) + g);
       d = __ldg(reinterpret_cast<const uint4*>(p.dout + r * D) + g);
+      const RowKeys rk = window_row_keys(p, static_cast<int>(r % p.Lq));
+      few = rk.nsk + rk.nw <= kFewKeys;
     }
-    float s = bf16lo(o.x) * bf16lo(d.x) + bf16hi(o.x) * bf16hi(d.x);
-    s = fmaf(bf16lo(o.y), bf16lo(d.y), s);
-    s = fmaf(bf16hi(o.y), bf16hi(d.y), s);
-    s = fmaf(bf16lo(o.z), bf16lo(d.z), s);
-    s = fmaf(bf16hi(o.z), bf16hi(d.z), s);
-    s = fmaf(bf16lo(o.w), bf16lo(d.w), s);
-    s = fmaf(bf16hi(o.w), bf16hi(d.w), s);
+    float s = dot8(o, d, 0.f);
 #pragma unroll
     for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off, G);
-    if (active && g == 0) p.delta[r] = s;
+    if (active && g == 0 && !few) p.delta[r] = s;
+  }
+  // the rows with few keys: those near the first key, those near the last one
+  // of a launch whose queries run past it, or all of them
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const bool every = p.w.window + p.w.snk <= kFewKeys || p.Lk <= kFewKeys;
+  const long long first_end = every ? p.Lq : max(0ll, min(static_cast<long long>(p.Lq), kFewKeys - p.w.sh));
+  const long long late = every ? p.Lq
+                               : max(first_end, min(static_cast<long long>(p.Lq),
+                                                    p.Lk - kFewKeys - 1 - p.w.sh + p.w.window));
+  const long long per = first_end + (p.Lq - late);
+  const long long n = per * p.B * p.H;
+  for (long long x = tid / 32; x < n; x += nthreads / 32) {
+    const long long bhq = x / per;
+    long long i = x - bhq * per;
+    if (i >= first_end) i += late - first_end;
+    const RowKeys rk = window_row_keys(p, static_cast<int>(i));
+    const int nk = rk.nsk + rk.nw;
+    if (nk > kFewKeys) continue;
+    const long long r = bhq * p.Lq + i;
+    const int b = static_cast<int>(bhq / p.H);
+    const int h = static_cast<int>(bhq - static_cast<long long>(b) * p.H);
+    const size_t kv = (static_cast<size_t>(b) * p.Hkv + h / (p.H / p.Hkv)) * p.Lk;
+    const int t = lane >> 1, half = lane & 1;
+    float sqk = 0.f, dov = 0.f;
+    if (t < nk) {
+      const int key = t < rk.nsk ? t : rk.lo + (t - rk.nsk);
+      const uint4* qr = reinterpret_cast<const uint4*>(p.q + r * D) + half * (D / 16);
+      const uint4* dr = reinterpret_cast<const uint4*>(p.dout + r * D) + half * (D / 16);
+      const uint4* kr = reinterpret_cast<const uint4*>(p.k + (kv + key) * D) + half * (D / 16);
+      const uint4* vr = reinterpret_cast<const uint4*>(p.v + (kv + key) * D) + half * (D / 16);
+#pragma unroll 4
+      for (int e = 0; e < D / 16; ++e) {
+        sqk = dot8(__ldg(qr + e), __ldg(kr + e), sqk);
+        dov = dot8(__ldg(dr + e), __ldg(vr + e), dov);
+      }
+    }
+    sqk += __shfl_xor_sync(0xFFFFFFFFu, sqk, 1);
+    dov += __shfl_xor_sync(0xFFFFFFFFu, dov, 1);
+    float s = t < nk ? ex2(sqk * p.scale_log2 - __ldg(p.lse + r) * kLog2e) * dov : 0.f;
+#pragma unroll
+    for (int off = 2; off < 32; off <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    if (lane == 0) p.delta[r] = nk > 0 ? s : 0.f;
   }
   float4* acc = reinterpret_cast<float4*>(p.dq_acc);
   const long long n4 = rows * D / 4;
@@ -953,15 +1034,15 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   attn_status_t s = check_common(B, H, Lq, Lk, d, scale);
   if (s != ATTN_OK) return s;
   if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
-  const void* ptrs16[] = {q, k, v, o, dout, dq, dk, dv, workspace};
-  for (const void* ptr : ptrs16)
-    if (!ptr || !aligned16(ptr)) return ATTN_ERR_INVALID_ARG;
-  if (!lse || !delta || !aligned4(lse) || !aligned4(delta)) return ATTN_ERR_INVALID_ARG;
   WindowBwdParams p{};
   if (!window_mask(&p.w, Lk, window, sinks, q_offset, k_offset)) return ATTN_ERR_INVALID_ARG;
   const WindowBwdPlan pl = window_bwd_plan(B, H, H_kv, Lq, Lk, d, p.w);
   if (workspace_bytes < pl.bytes) return ATTN_ERR_WORKSPACE;
   if (pl.n_cta > 0x7FFFFFFFll || pl.slots > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  // empty tensors may have no address
+  const void* of_keys[] = {k, v, dk, dv};
+  for (const void* ptr : of_keys)
+    if (Lk > 0 && (!ptr || !aligned16(ptr))) return ATTN_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (Lq == 0) {                 // no query sends anything
     const size_t bytes = static_cast<size_t>(B) * H_kv * Lk * d * 2;
@@ -969,6 +1050,11 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
     s = cuda_status("attn_bwd_window clear", cudaMemsetAsync(dk, 0, bytes, st));
     return s != ATTN_OK ? s : cuda_status("attn_bwd_window clear", cudaMemsetAsync(dv, 0, bytes, st));
   }
+  const void* of_queries[] = {q, o, dout, dq, workspace};
+  for (const void* ptr : of_queries)
+    if (!ptr || !aligned16(ptr)) return ATTN_ERR_INVALID_ARG;
+  if (!lse || !delta || !aligned4(lse) || !aligned4(delta)) return ATTN_ERR_INVALID_ARG;
+  if (Lk == 0) k = v = q;        // no key is read
   if ((s = get_encoder()) != ATTN_OK) return s;
   if ((s = status_word(&p.err)) != ATTN_OK) return s;
   CUtensorMap tq, tk, tv, tdo, tdq;
@@ -985,6 +1071,9 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   p.Lk = Lk;
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
   p.o = static_cast<const __nv_bfloat16*>(o);
   p.dout = static_cast<const __nv_bfloat16*>(dout);
   p.lse = lse;

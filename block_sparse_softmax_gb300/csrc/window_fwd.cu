@@ -681,14 +681,17 @@ extern "C" attn_status_t attn_fwd_window(const void* q, const void* k, const voi
                                          float* lse, int B, int H, int H_kv, int Lq, int Lk, int d,
                                          float scale, int64_t window, int64_t sinks,
                                          int64_t q_offset, int64_t k_offset, void* stream) {
-  if (!o || !lse || !aligned16(o) || !aligned4(lse)) return ATTN_ERR_INVALID_ARG;
   attn_status_t s = check_common(B, H, Lq, Lk, d, scale);
   if (s != ATTN_OK) return s;
   if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
-  if (!q || !k || !v || !aligned16(q) || !aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID_ARG;
   WindowFwdParams p{};
   if (!window_mask(&p.w, Lk, window, sinks, q_offset, k_offset)) return ATTN_ERR_INVALID_ARG;
   if (Lq == 0) return ATTN_OK;
+  if (Lk == 0) k = v = q;        // empty tensors may have no address; no key is read
+  const void* ptrs16[] = {q, k, v, o};
+  for (const void* ptr : ptrs16)
+    if (!ptr || !aligned16(ptr)) return ATTN_ERR_INVALID_ARG;
+  if (!lse || !aligned4(lse)) return ATTN_ERR_INVALID_ARG;
   if ((s = get_encoder()) != ATTN_OK) return s;
   if ((s = status_word(&p.err)) != ATTN_OK) return s;
   CUtensorMap tq, tk, tv;

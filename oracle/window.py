@@ -15,7 +15,8 @@ The bounds count the roundings that such a kernel makes, each by at most half a 
           the logarithm's own error, and the fp32 sum of the row), and 2^-8 as an operand of P V
           or P^T dO.
   O       sum P |v| times P's error, + 2^-8 |O| for its own rounding.
-  D       dO . O with the rounded O: sum |dO| (O's error), + fp32.
+  D       dO . O with the rounded O: sum |dO| (O's error), + fp32; for rows of at most 16 keys
+          sum_j P_ij dP_ij in fp32: P's error before any rounding to bf16.
   dS      scale P (dP - D): P's error on |dS|, 2^-8 |dS| as an operand, scale P (D's error + dP's).
   dQ, dK  sums of dS's error times |k|, |q|, + 2^-8 of the result.
 """
@@ -95,6 +96,9 @@ def backward_bounds(q, k, v, do, mask, scale):
     D = (do.double() * O).sum(-1, keepdim=True)
     D_err = (doa * bound_o).sum(-1, keepdim=True) + (doa * (O.abs() + bound_o)).sum(
         -1, keepdim=True) * d * 2.0 ** -23
+    few = (P * (1 + p_rel) * (dP.abs() * p_rel + dP_size * d * 2.0 ** -23)).sum(-1, keepdim=True)
+    D_err = torch.where(mask.sum(-1, keepdim=True) <= 16, few + (P * dP.abs()).sum(
+        -1, keepdim=True) * 2.0 ** -19, D_err)
     dS = (scale * P * (dP - D)).abs()
     dS_err = scale * P * (1 + p_rel) * (D_err + dP_size * d * 2.0 ** -23 + (dP.abs() + D.abs()) * 2.0 ** -22)
     dS_err = dS_err + dS * p_rel

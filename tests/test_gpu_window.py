@@ -58,6 +58,13 @@ SHAPES = [
     (1, 2, 1, 300, 200, 64, 64, 160, 0, 150),    # a chunk with the last of the sinks
     (1, 2, 1, 130, 260, 128, 64, 4, 2 ** 40, 2 ** 40 - 130),  # far positions
     (1, 1, 1, 64, 64, 64, 8, 2, 2 ** 40, 0),     # nothing but sinks is near
+    (2, 4, 2, 3, 3, 128, 50, 4, 0, 0),           # three tokens
+    (1, 2, 1, 9, 9, 64, 5, 1, 0, 0),
+    (1, 2, 2, 200, 200, 64, 9, 7, 0, 0),         # every row sees at most 16 keys
+    (1, 2, 2, 200, 200, 128, 10, 7, 0, 0),       # ... 17
+    (1, 2, 2, 100, 12, 128, 50, 0, 0, 0),        # 12 keys, queries run past them
+    (1, 2, 2, 100, 40, 64, 50, 3, 5, 0),
+    (1, 2, 1, 0, 70, 64, 5, 0, 0, 0),            # no query
 ]
 
 
@@ -81,3 +88,13 @@ def test_forward_and_backward(bss, B, H, Hkv, Lq, Lk, d, window, sinks, qo, ko):
     unseen = ~mask.any(0)
     assert torch.all(got[1][:, :, unseen] == 0) and torch.all(got[2][:, :, unseen] == 0)
     assert torch.all(got[0][:, :, ~mask.any(1)] == 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_no_key(bss, d):
+    q, k, v, do = inputs(1, 2, 1, 70, 0, d, 1)
+    o, lse = bss.attn_fwd_window(q, k, v, 5)
+    dq, dk, dv, delta = bss.attn_bwd_window(q, k, v, o, lse, do, 5)
+    assert bss.attn_poll_status() == 0
+    assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
+    assert torch.all(dq == 0) and torch.all(delta == 0) and dk.numel() == dv.numel() == 0

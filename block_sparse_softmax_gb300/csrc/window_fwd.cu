@@ -7,12 +7,29 @@
 //
 // One work item is a 128-row query tile.  Its keys are the sink blocks and the
 // window's blocks (128 keys each), disjoint and ascending, taken two at a time
-// with the pipeline of the dense forward with 256-key score tiles: TMA
-// producer, one MMA thread, two softmax warpgroups that take one block of each
-// pair, S (256 columns) | P | O in tensor memory, items handed out by cluster
-// launch control.  An odd last block is scored alone.  The element mask is
-// applied in the blocks that the diagonal, the window's lower edge or the last
-// sink crosses; all others run without it.
+// (an odd last block alone): S of a pair by M128 N256 MMAs (about 170 cycles
+// each against 105 for an N=128 one, with every SM issuing), S (256 columns) |
+// P | O in tensor memory, P V block by block.
+//
+// Items are short (a window of 1024 keys is 5 pairs), so what decides is that
+// nothing stops between them.  The CTAs are persistent and take items by a
+// fixed stride (the items of a window are alike), so every role knows the next
+// item; four kinds of warps each run ahead over the items:
+//   TMA     K of the next pair, at an item's end the next item's first pair
+//           and its Q tile (prefetched into L2 an item earlier), then V;
+//   MMA     S of the next pair, or of the next item's first one, before P V of
+//           this one;
+//   softmax two warpgroups, one per block of the pair, which exchange their
+//           rows' maxima through shared memory; they go on to the next item's
+//           S as soon as P is written;
+//   output  a warpgroup that waits for the item's last P V, scales and stores
+//           O while the softmax works on the next item.
+// With the softmax warps writing O themselves an item of one pair took 12000
+// cycles and every further pair 3100: 410 us for B2 H16(4) L16384 d128, window
+// 1024, sinks 4; as described here it is MEASURED.
+//
+// The element mask is applied in the blocks that the diagonal, the window's
+// lower edge or the last sink crosses; all others run without it.
 #include <algorithm>
 
 #include "host.cuh"
@@ -48,22 +65,19 @@ struct WinCfg {
   static constexpr int kBarPFull = kBarSFree + 1;
   static constexpr int kBarPvDone = kBarPFull + 2;         // [2] a pair's P V of block X completed
   static constexpr int kBarXch = kBarPvDone + 2;           // [2] row values exchanged, by parity
-  static constexpr int kBarOFull = kBarXch + 2;
-  static constexpr int kBarOEmpty = kBarOFull + 1;
-  static constexpr int kBarItemFull = kBarOEmpty + 1;      // [2]
-  static constexpr int kBarItemEmpty = kBarItemFull + 2;   // [2]
-  static constexpr int kBarClc = kBarItemEmpty + 2;
-  static constexpr int kBarMmaDone = kBarClc + 1;
+  static constexpr int kBarOFull = kBarXch + 2;            // an item's last P V completed
+  static constexpr int kBarOEmpty = kBarOFull + 1;         // ... O and the row factors read
+  static constexpr int kBarLFull = kBarOEmpty + 1;         // an item's row factors 1 / l written
+  static constexpr int kBarMmaDone = kBarLFull + 1;
   static constexpr int kNumBars = kBarMmaDone + 1;
-  // cancel answer (16) | TMEM base | abort flag | next item [2]
+  // TMEM base | abort flag
   static constexpr int kMiscOff = kBarOff + ((kNumBars + 1) / 2) * 16;
-  static constexpr int kClcOff = kMiscOff;
-  static constexpr int kTmemSlotOff = kMiscOff + 16;
-  static constexpr int kAbortOff = kMiscOff + 20;
-  static constexpr int kNextItemOff = kMiscOff + 24;
+  static constexpr int kTmemSlotOff = kMiscOff;
+  static constexpr int kAbortOff = kMiscOff + 4;
   // exchanged row values: [parity][warpgroup][128 rows] fp32
-  static constexpr int kXchOff = kMiscOff + 32;
-  static constexpr int kPayload = kXchOff + 2 * 2 * kTileM * 4;
+  static constexpr int kXchOff = kMiscOff + 16;
+  static constexpr int kInvOff = kXchOff + 2 * 2 * kTileM * 4;   // 1 / l of an item's rows
+  static constexpr int kPayload = kInvOff + kTileM * 4;
   // alignment slack: at d=128 less than 1024 bytes are left, and the kernel
   // checks that the dynamic shared memory base leaves room
   static constexpr int kSlack = kPayload + 1024 <= 232448 ? 1024 : 232448 - kPayload;
@@ -73,16 +87,17 @@ struct WinCfg {
   static constexpr uint32_t kColS = 0;      // S: 256 fp32 columns (key block X at 128 X)
   static constexpr uint32_t kColP = 256;    // P: 256 keys, bf16 pairs (block X at 256 + 64 X)
   static constexpr uint32_t kColO = 384;    // O: D fp32 columns
-  static constexpr int kThreads = 384;
-  static constexpr int kItemReaders = 1 + 8;   // the MMA thread and one lane of each softmax warp
+  static constexpr int kThreads = 512;
 };
 
-// Register split per warpgroup: warpgroup 0 (TMA, MMA, two idle warps) 136
-// registers a thread, the two softmax warpgroups 184; the launch holds 168.
-constexpr uint32_t kWinLow = 136;
-constexpr uint32_t kWinHigh = 184;
-constexpr uint32_t kWinLaunchRegs = 168;
-static_assert(128 * kWinLow + 256 * kWinHigh <= 384 * kWinLaunchRegs, "register split exceeds the launch");
+// Register split per warpgroup (setmaxnreg): output (warps 0-3), softmax
+// (4-7, 8-11), TMA and MMA (12, 13; two idle warps).  The launch holds 128 a
+// thread; each SM sub-partition has one warp of every warpgroup.
+constexpr uint32_t kWinOut = 48;
+constexpr uint32_t kWinSoft = 192;
+constexpr uint32_t kWinLow = 80;
+constexpr uint32_t kWinLaunchRegs = 128;
+static_assert(kWinOut + 2 * kWinSoft + kWinLow <= 4 * kWinLaunchRegs, "register split exceeds the launch");
 
 // Item -> query tile: tile-major with the heads side by side, so that the CTAs
 // running at any moment share the window's K and V tiles in L2; the last tiles
@@ -104,8 +119,23 @@ __device__ __forceinline__ WindowItem window_item(int item, const WindowFwdParam
   return it;
 }
 
+// The first item from `item` on in this CTA's stride that has a key block
+// (p.n_items or more: none).
+__device__ __forceinline__ int window_next(int item, const WindowFwdParams& p, int n_tiles, WindowItem& it) {
+  for (; item < p.n_items; item += static_cast<int>(gridDim.x)) {
+    it = window_item(item, p, n_tiles);
+    if (it.kb.count() > 0) break;
+  }
+  return item;
+}
+
+// The lowest n bits (n may lie outside [0, 32]).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
 template <int D>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(512, 1)
     attn_fwd_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const WindowFwdParams p) {
   using C = WinCfg<D>;
@@ -123,7 +153,6 @@ __global__ void __launch_bounds__(384, 1)
   auto bar = [&](int i) { return sbase + C::kBarOff + 8u * static_cast<uint32_t>(i); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kTmemSlotOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbortOff);
-  volatile int* next_item = reinterpret_cast<volatile int*>(smem + C::kNextItemOff);
 
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
@@ -145,11 +174,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(bar(C::kBarVFull + s), 1);
       mbar_init(bar(C::kBarVEmpty + s), 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(C::kBarXch + s), 2 * 4 * 32);
-      mbar_init(bar(C::kBarItemFull + s), 1);
-      mbar_init(bar(C::kBarItemEmpty + s), C::kItemReaders);
-    }
+    for (int s = 0; s < 2; ++s) mbar_init(bar(C::kBarXch + s), 2 * 4 * 32);
     mbar_init(bar(C::kBarSFull), 1);
     mbar_init(bar(C::kBarSFree), 2 * 4 * 32);
     mbar_init(bar(C::kBarPFull + 0), 2 * 4 * 32);
@@ -157,8 +182,8 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(bar(C::kBarPvDone + 0), 1);
     mbar_init(bar(C::kBarPvDone + 1), 1);
     mbar_init(bar(C::kBarOFull), 1);
-    mbar_init(bar(C::kBarOEmpty), 2 * 4 * 32);
-    mbar_init(bar(C::kBarClc), 1);
+    mbar_init(bar(C::kBarOEmpty), 4 * 32);
+    mbar_init(bar(C::kBarLFull), 4 * 32);
     mbar_init(bar(C::kBarMmaDone), 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -172,49 +197,41 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp < 4) {
+  if (warp >= 12) {
     regs_set<kWinLow, kWinLaunchRegs>();
-    if (warp == 0) {
-      // =================== TMA producer and item scheduler ===================
+    if (warp == 12) {
+      // =================== TMA producer ===================
       if (lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
-        int item = static_cast<int>(blockIdx.x);
-        int n = 0;              // items finished
         int ik = 0, iv = 0;     // pair stages and V tiles loaded (over all items)
         int qn = 0;             // Q tiles loaded
-        int clc_k = 0;          // cancel requests answered
-        bool clc_live = true;
-        bool clc_out = false;   // a cancel request is in flight
-        bool ok = true;
-        auto request_item = [&]() {
-          fence_proxy_async_smem();
-          mbar_arrive_expect_tx(bar(C::kBarClc), 16);
-          clc_try_cancel(sbase + C::kClcOff, bar(C::kBarClc));
-          clc_out = true;
-        };
-        // key blocks b0 and b1 (b1 = -1: b0 alone); a block that reaches past
-        // the last key reads the zero fill there
-        auto load_k = [&](const WindowItem& it, int b0, int b1) -> bool {
+        // the item's pair k: key blocks 2 k and 2 k + 1 of its list (the second
+        // may be missing); a block that reaches past the last key reads the
+        // zero fill there
+        auto load_k = [&](const WindowItem& it, int k) -> bool {
           const int s = ik % C::kStagesK;
           if (ik >= C::kStagesK &&
               !wait_bar(bar(C::kBarKEmpty + s), ((ik / C::kStagesK) & 1) ^ 1, abort_flag, p.err))
             return false;
+          const bool two = 2 * k + 1 < it.kb.count();
           const uint32_t ks = sbase + C::kKOff + s * C::kPairBytes;
-          mbar_arrive_expect_tx(bar(C::kBarKFull + s), b1 >= 0 ? C::kPairBytes : C::kTileBytes);
+          mbar_arrive_expect_tx(bar(C::kBarKFull + s), two ? C::kPairBytes : C::kTileBytes);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (t == 1 && b1 < 0) break;
+            if (t == 1 && !two) break;
+            const int row = it.kb.at(2 * k + t) * kTileN;
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
               tma_load_4d(ks + c * 2 * C::kChunkBytes + t * C::kChunkBytes, &tmK, bar(C::kBarKFull + s),
-                          c * 64, (t ? b1 : b0) * kTileN, it.hkv, it.b);
+                          c * 64, row, it.hkv, it.b);
           }
           ++ik;
           return true;
         };
-        auto load_v = [&](const WindowItem& it, int kb) -> bool {
+        auto load_v = [&](int row, int hkv, int b) -> bool {
+          if (row < 0) return true;        // no such block
           const int s = iv % C::kStagesV;
           if (iv >= C::kStagesV &&
               !wait_bar(bar(C::kBarVEmpty + s), ((iv / C::kStagesV) & 1) ^ 1, abort_flag, p.err))
@@ -223,63 +240,43 @@ __global__ void __launch_bounds__(384, 1)
           mbar_arrive_expect_tx(bar(C::kBarVFull + s), C::kTileBytes);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d(vs + c * C::kChunkBytes, &tmV, bar(C::kBarVFull + s), c * 64, kb * kTileN, it.hkv,
-                        it.b);
+            tma_load_4d(vs + c * C::kChunkBytes, &tmV, bar(C::kBarVFull + s), c * 64, row, hkv, b);
           ++iv;
           return true;
         };
-        while (ok) {
-          const WindowItem it = window_item(item, p, n_tiles);
-          const int nb = it.kb.count();
-          const int ns = (nb + 1) / 2;
-          auto second = [&](int k) { return 2 * k + 1 < nb ? it.kb.at(2 * k + 1) : -1; };
-          if (ns > 0) {
-            const int s = qn % C::kStagesQ;
-            // the last S that read this Q buffer must have completed
-            if (qn >= C::kStagesQ &&
-                !wait_bar(bar(C::kBarQEmpty + s), ((qn / C::kStagesQ) & 1) ^ 1, abort_flag, p.err))
-              break;
-            mbar_arrive_expect_tx(bar(C::kBarQFull + s), C::kTileBytes);
+        auto load_q = [&](const WindowItem& it) -> bool {
+          const int s = qn % C::kStagesQ;
+          // the last S that read this Q buffer must have completed
+          if (qn >= C::kStagesQ &&
+              !wait_bar(bar(C::kBarQEmpty + s), ((qn / C::kStagesQ) & 1) ^ 1, abort_flag, p.err))
+            return false;
+          mbar_arrive_expect_tx(bar(C::kBarQFull + s), C::kTileBytes);
 #pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-              tma_load_4d(sbase + C::kQOff + s * C::kTileBytes + c * C::kChunkBytes, &tmQ,
-                          bar(C::kBarQFull + s), c * 64, it.r0, it.h, it.b);
-            ++qn;
-            // K runs one step ahead of V
-            ok = load_k(it, it.kb.at(0), second(0));
-            for (int k = 0; k < ns && ok; ++k) {
-              if (k == ns - 1 && clc_live) request_item();   // the next item, as this one's last loads go
-              if (k + 1 < ns) ok = load_k(it, it.kb.at(2 * k + 2), second(k + 1));
-              if (ok) ok = load_v(it, it.kb.at(2 * k)) && (second(k) < 0 || load_v(it, second(k)));
-            }
-            if (!ok) break;
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_4d(sbase + C::kQOff + s * C::kTileBytes + c * C::kChunkBytes, &tmQ,
+                        bar(C::kBarQFull + s), c * 64, it.r0, it.h, it.b);
+          ++qn;
+          return true;
+        };
+        WindowItem it;
+        int item = window_next(static_cast<int>(blockIdx.x), p, n_tiles, it);
+        bool ok = true;
+        if (item < p.n_items) ok = load_k(it, 0) && load_q(it);
+        int k = 0;
+        while (ok && item < p.n_items) {
+          // V of this pair goes after K of the next one
+          const int nb = it.kb.count();
+          const int hkv = it.hkv, b = it.b;
+          const int v0 = it.kb.at(2 * k) * kTileN;
+          const int v1 = 2 * k + 1 < nb ? it.kb.at(2 * k + 1) * kTileN : -1;
+          if (2 * k + 2 < nb) {
+            ok = load_k(it, ++k);
+          } else {
+            k = 0;
+            item = window_next(item + static_cast<int>(gridDim.x), p, n_tiles, it);
+            if (item < p.n_items) ok = load_k(it, 0) && load_q(it);
           }
-          if (clc_live && !clc_out) request_item();   // an item without keys
-          int next = -1;
-          if (clc_out) {
-            if (!wait_bar(bar(C::kBarClc), clc_k & 1, abort_flag, p.err)) break;
-            clc_out = false;
-            ++clc_k;
-            int x = -1;
-            if (clc_query(sbase + C::kClcOff, x)) {
-              if (x >= 0 && x < p.n_items) {
-                next = x;
-              } else {
-                record_error(p.err, ATTN_ERR_CUDA);   // not an index of this grid
-                clc_live = false;
-              }
-            } else {
-              clc_live = false;                        // nothing left to take
-            }
-          }
-          const int s = n & 1;
-          if (n >= 2 && !wait_bar(bar(C::kBarItemEmpty + s), ((n >> 1) & 1) ^ 1, abort_flag, p.err))
-            break;
-          next_item[s] = next;
-          mbar_arrive(bar(C::kBarItemFull + s));
-          ++n;
-          if (next < 0) break;
-          item = next;
+          ok = ok && load_v(v0, hkv, b) && load_v(v1, hkv, b);
         }
         // every copy issued has landed before the CTA may exit
         for (int j = max(0, ik - C::kStagesK); j < ik; ++j)
@@ -288,25 +285,28 @@ __global__ void __launch_bounds__(384, 1)
           drain_bar(bar(C::kBarVFull + j % C::kStagesV), (j / C::kStagesV) & 1);
         for (int j = max(0, qn - C::kStagesQ); j < qn; ++j)
           drain_bar(bar(C::kBarQFull + j % C::kStagesQ), (j / C::kStagesQ) & 1);
-        if (clc_out) drain_bar(bar(C::kBarClc), clc_k & 1);
       }
-    } else if (warp == 1) {
+    } else if (warp == 13) {
       // =================== MMA issuer (one thread) ===================
-      // Per item: S_0, then for every step k: S_{k+1} (as soon as both
-      // softmax warpgroups hold S_k in registers) and P_k V_k.
+      // For every pair: S of the next pair (of the next item at an item's
+      // end), as soon as both softmax warpgroups hold this pair's S in
+      // registers, then this pair's P V.
       if (lane == 0) {
         constexpr uint32_t kIdescS = idesc_bf16_f32(kTileM, 2 * kTileN, false, false);
         constexpr uint32_t kIdescS1 = idesc_bf16_f32(kTileM, kTileN, false, false);   // a block alone
         constexpr uint32_t kIdescPV = idesc_bf16_f32(kTileM, D, false, true);
-        int item = static_cast<int>(blockIdx.x);
-        int n = 0;              // items finished
         int ik = 0, iv = 0;     // pair stages and V tiles consumed
         int qn = 0;             // Q tiles consumed
         int sn = 0;             // S tiles issued
         int pn = 0;             // P tiles consumed
-        int on = 0;             // O results handed to the epilogue
-        bool ok = true;
-        auto issue_s = [&](bool last, bool alone) -> bool {
+        int on = 0;             // O results handed to the output warps
+        // S of pair k of an item with nb blocks
+        auto issue_s = [&](int k, int nb) -> bool {
+          if (k == 0) {
+            if (!wait_bar(bar(C::kBarQFull + qn % C::kStagesQ), (qn / C::kStagesQ) & 1, abort_flag, p.err))
+              return false;
+            ++qn;
+          }
           if (sn > 0 && !wait_bar(bar(C::kBarSFree), (sn - 1) & 1, abort_flag, p.err)) return false;
           const int s = ik % C::kStagesK;
           if (!wait_bar(bar(C::kBarKFull + s), (ik / C::kStagesK) & 1, abort_flag, p.err)) return false;
@@ -314,33 +314,33 @@ __global__ void __launch_bounds__(384, 1)
           const int qs = (qn - 1) % C::kStagesQ;
           const uint64_t dq = sdesc_sw128(sbase + C::kQOff + qs * C::kTileBytes, 16, 1024);
           const uint64_t dk = sdesc_sw128(sbase + C::kKOff + s * C::kPairBytes, 16, 1024);
+          const uint32_t idesc = 2 * k + 1 < nb ? kIdescS : kIdescS1;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t qoff = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
             const uint32_t koff = (kk >> 2) * 2 * C::kChunkBytes + (kk & 3) * 32;
-            mma_ss(tmem + C::kColS, sdesc_add(dq, qoff), sdesc_add(dk, koff), alone ? kIdescS1 : kIdescS,
-                   kk > 0 ? 1u : 0u);
+            mma_ss(tmem + C::kColS, sdesc_add(dq, qoff), sdesc_add(dk, koff), idesc, kk > 0 ? 1u : 0u);
           }
           mma_commit(bar(C::kBarSFull));
           mma_commit(bar(C::kBarKEmpty + s));
-          if (last) mma_commit(bar(C::kBarQEmpty + qs));   // Q's buffer is free for a later item
+          if (2 * k + 2 >= nb) mma_commit(bar(C::kBarQEmpty + qs));   // Q's buffer is free for a later item
           ++ik;
           ++sn;
           return true;
         };
         // P V block by block: block X's MMAs go as soon as warpgroup X has
         // written its P, and their completion frees that block's P columns
-        auto issue_pv = [&](bool first, bool alone) -> bool {
+        auto issue_pv = [&](int k, int nb) -> bool {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!wait_bar(bar(C::kBarPFull + t), pn & 1, abort_flag, p.err)) return false;
             tc_fence_after();
-            if (t == 0 && first && on > 0) {
-              // O still holds the previous item's result until its epilogue read it
+            if (t == 0 && k == 0 && on > 0) {
+              // O still holds the previous item's result until the output warps read it
               if (!wait_bar(bar(C::kBarOEmpty), (on - 1) & 1, abort_flag, p.err)) return false;
               tc_fence_after();
             }
-            if (!(alone && t == 1)) {
+            if (2 * k + t < nb) {
               const int s = iv % C::kStagesV;
               if (!wait_bar(bar(C::kBarVFull + s), (iv / C::kStagesV) & 1, abort_flag, p.err)) return false;
               tc_fence_after();
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
               for (int kk = 0; kk < kTileN / 16; ++kk)
                 mma_ts(tmem + C::kColO, tmem + C::kColP + (t * 8 + kk) * 8, sdesc_add(dv, kk * 16 * 128),
-                       kIdescPV, (!first || t > 0 || kk > 0) ? 1u : 0u);
+                       kIdescPV, (k > 0 || t > 0 || kk > 0) ? 1u : 0u);
               mma_commit(bar(C::kBarVEmpty + s));
               ++iv;
             }
@@ -357,39 +357,78 @@ __global__ void __launch_bounds__(384, 1)
           ++pn;
           return true;
         };
-        while (ok) {
-          const WindowItem it = window_item(item, p, n_tiles);
-          const int nb = it.kb.count();
+        WindowItem it;
+        int item = window_next(static_cast<int>(blockIdx.x), p, n_tiles, it);
+        int nb = it.kb.count();
+        bool ok = item >= p.n_items || issue_s(0, nb);
+        while (ok && item < p.n_items) {
+          item = window_next(item + static_cast<int>(gridDim.x), p, n_tiles, it);
+          const int nb2 = item < p.n_items ? it.kb.count() : 0;
           const int ns = (nb + 1) / 2;
-          const bool odd = (nb & 1) != 0;     // the last pair is one block
-          if (ns > 0) {
-            if (!wait_bar(bar(C::kBarQFull + qn % C::kStagesQ), (qn / C::kStagesQ) & 1, abort_flag, p.err))
-              break;
-            ++qn;
-            ok = issue_s(ns == 1, odd && ns == 1);
-            for (int k = 0; k < ns && ok; ++k) {
-              if (k + 1 < ns) ok = issue_s(k + 1 == ns - 1, odd && k + 1 == ns - 1);
-              if (ok) ok = issue_pv(k == 0, odd && k == ns - 1);
-            }
-            if (!ok) break;
-            mma_commit(bar(C::kBarOFull));
-            ++on;
+          for (int k = 0; k < ns && ok; ++k) {
+            if (k + 1 < ns) ok = issue_s(k + 1, nb);
+            else if (nb2 > 0) ok = issue_s(0, nb2);
+            if (ok) ok = issue_pv(k, nb);
           }
-          const int s = n & 1;
-          if (!wait_bar(bar(C::kBarItemFull + s), (n >> 1) & 1, abort_flag, p.err)) break;
-          const int next = next_item[s];
-          mbar_arrive(bar(C::kBarItemEmpty + s));
-          ++n;
-          if (next < 0) break;
-          item = next;
+          if (!ok) break;
+          mma_commit(bar(C::kBarOFull));
+          ++on;
+          nb = nb2;
         }
         // every MMA issued has completed before tensor memory is released
         mma_commit(bar(C::kBarMmaDone));
         drain_bar(bar(C::kBarMmaDone), 0);
       }
     }
+  } else if (warp < 4) {
+    regs_set<kWinOut, kWinLaunchRegs>();
+    // =================== output: thread = query row ===================
+    const int row_in_tile = warp * 32 + lane;
+    const uint32_t tO = tmem + (static_cast<uint32_t>(warp * 32) << 16) + C::kColO;
+    const volatile float* inv_s = reinterpret_cast<const volatile float*>(smem + C::kInvOff);
+    int on = 0;             // O results read
+    for (int item = static_cast<int>(blockIdx.x); item < p.n_items; item += static_cast<int>(gridDim.x)) {
+      const WindowItem it = window_item(item, p, n_tiles);
+      const size_t rows0 = static_cast<size_t>(it.bh) * p.Lq;
+      const bool inb = it.r0 + row_in_tile < p.Lq;
+      uint4* dst = reinterpret_cast<uint4*>(p.o + (rows0 + it.r0 + row_in_tile) * D);
+      const bool any = it.kb.count() > 0;
+      float inv = 0.f;
+      if (any) {
+        if (!__all_sync(0xFFFFFFFFu, wait_bar_relaxed(bar(C::kBarLFull), on & 1, abort_flag, p.err))) break;
+        inv = inv_s[row_in_tile];
+        if (!__all_sync(0xFFFFFFFFu, wait_bar_relaxed(bar(C::kBarOFull), on & 1, abort_flag, p.err))) break;
+        tc_fence_after();
+      } else if (inb) {
+        p.lse[rows0 + it.r0 + row_in_tile] = -__int_as_float(0x7f800000);
+      }
+      // 16 columns at a time, 32 bytes of the row (the warpgroup has few
+      // registers); a row without a key (inv = 0) is 0 whatever the masked
+      // keys held
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
+        if (any) {
+          tmem_ld16(tO + c * 16, o);
+          tmem_ld_wait16(o);
+          if (c == D / 16 - 1) {
+            tc_fence_before();
+            mbar_arrive(bar(C::kBarOEmpty));      // the next item's P V may overwrite O
+          }
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w[e] = inv == 0.f ? 0u : pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        if (inb) {
+          dst[2 * c] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[2 * c + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      if (any) ++on;
+    }
   } else {
-    regs_set<kWinHigh, kWinLaunchRegs>();
+    regs_set<kWinSoft, kWinLaunchRegs>();
     // =================== softmax warpgroups: X = 0 (warps 4-7), 1 (warps 8-11) ===================
     const int X = (warp - 4) >> 2;                // key block X of every pair
     const int wq = warp & 3;                      // TMEM lane quarter of this warp
@@ -398,17 +437,15 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tS = tmem + lane_base + C::kColS + X * 128;
     const uint32_t tP = tmem + lane_base + C::kColP + X * 64;
     const uint32_t tO = tmem + lane_base + C::kColO + X * (D / 2);
-    // the 64 columns this warpgroup's epilogue reads (at d=64 both read all)
-    const uint32_t tO0 = tmem + lane_base + C::kColO + (D == 128 ? X * 64 : 0);
     const float sl2 = p.scale_log2;
     const float NEG_INF = -__int_as_float(0x7f800000);
     float* xch = reinterpret_cast<float*>(smem + C::kXchOff);
 
-    int item = static_cast<int>(blockIdx.x);
-    int n = 0;          // items finished
+    float* inv_s = reinterpret_cast<float*>(smem + C::kInvOff);
+
     int cnt = 0;        // S tiles consumed (over all items)
     int nx = 0;         // row values exchanged
-    int on = 0;         // O results read
+    int on = 0;         // items finished
     bool ok = true;
     // hand this row's value to the other warpgroup and take its value back
     auto exchange = [&](float v, float& other) -> bool {
@@ -421,16 +458,19 @@ __global__ void __launch_bounds__(384, 1)
       ++nx;
       return w;
     };
-    while (ok) {
-      const WindowItem it = window_item(item, p, n_tiles);
-      const int row = it.r0 + row_in_tile;
-      const int nb = it.kb.count();
+    for (int item = static_cast<int>(blockIdx.x); item < p.n_items; item += static_cast<int>(gridDim.x)) {
+      // few registers are left beside the scores: of the item only its first
+      // row and its blocks are kept
+      const int r0 = (n_tiles - 1 - item / (p.B * p.H)) * kTileM;
+      const WindowBlocks kb = window_blocks(p.w, r0, p.Lq, p.Lk);
+      const int nb = kb.count();
+      if (nb == 0) continue;
       const int ns = (nb + 1) / 2;
       float m2 = NEG_INF;     // reference max (log2 units), moved only by > 8
       float l = 0.f;          // this warpgroup's part of the row sum
       for (int k = 0; k < ns; ++k) {
         const bool none = 2 * k + X >= nb;        // the pair's second block is missing
-        const int kstart = none ? 0 : it.kb.at(2 * k + X) * kTileN;
+        const int kstart = none ? 0 : kb.at(2 * k + X) * kTileN;
         if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarSFull), cnt & 1, abort_flag, p.err))) {
           ok = false;
           break;
@@ -445,23 +485,27 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_before();
         mbar_arrive(bar(C::kBarSFree));
 
-        // element mask: in key index j of the block, allowed are j <= jhi
-        // (diagonal, last key) with j >= jlo (window) or j < js (sinks)
-        const long long diag0 = static_cast<long long>(it.r0) + p.w.sh - kstart;   // first row's own key
+        // element mask, 32 columns at a time: a bit for each allowed key of this
+        // row (j <= jhi: diagonal and last key; j >= jlo: window; j < js:
+        // sinks).  Most groups of an edge block are allowed or masked as a
+        // whole for the warp's 32 rows; only the others go element by element
+        const long long diag0 = static_cast<long long>(r0) + p.w.sh - kstart;   // first row's own key
         const bool edge = none || kstart + kTileN > p.Lk || kTileN - 1 > diag0 ||
                           (diag0 + kTileM - 1 - p.w.window + 1 > 0 && kstart + kTileN > p.w.snk);
         if (edge) {
           const long long dg = diag0 + row_in_tile;
           const int jhi = none ? -1 : static_cast<int>(max(-1ll, min(dg, static_cast<long long>(p.Lk) - 1 - kstart)));
           const int jlo = static_cast<int>(max(0ll, min(128ll, dg - p.w.window + 1)));
-          const int js = p.w.snk - kstart;
+          const int js = max(0, p.w.snk - kstart);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = bits_below(jhi + 1 - 32 * c) & (~bits_below(jlo - 32 * c) | bits_below(js - 32 * c));
+            if (!__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int e = c * 32 + j;
-              if (e > jhi || (e < jlo && e >= js)) s[c][j] = __float_as_uint(NEG_INF);
+              for (int j = 0; j < 32; ++j)
+                if (!((bits >> j) & 1u)) s[c][j] = __float_as_uint(NEG_INF);
             }
+          }
         }
         // row max of this block over 8 chains of three-input max
         float mx[8];
@@ -568,62 +612,26 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) break;
 
-      // ---- epilogue: the row sum is the two warpgroups' parts.  At d=128
-      // each writes its half of the row's columns (one 128-byte line); at
-      // d=64 a row is one line, and warpgroup 0 writes it ----
-      constexpr bool kSplit = D == 128;
-      uint32_t o[2][32];
-      float lt = 0.f;
-      if (ns > 0) {
-        float lo;
-        if (!exchange(l, lo)) break;
-        lt = l + lo;
-        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarOFull), on & 1, abort_flag, p.err))) break;
-        tc_fence_after();
-        tmem_ld32(tO0, o[0]);
-        tmem_ld32(tO0 + 32, o[1]);
-        tmem_ld_wait(o[0]);
-        tmem_ld_wait(o[1]);
-        tc_fence_before();
-        mbar_arrive(bar(C::kBarOEmpty));
-        ++on;
-      } else {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[c][j] = 0u;
+      // ---- the row sum is the two warpgroups' parts; warpgroup 0 hands its
+      // inverse to the output warps, which must have read the previous item's
+      float lo;
+      if (!exchange(l, lo)) break;
+      if (X == 0) {
+        if (on > 0 &&
+            !__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarOEmpty), (on - 1) & 1, abort_flag, p.err)))
+          break;
+        // a row that saw no key has l = 0; a NaN score makes l NaN and goes through
+        const float lt = l + lo;
+        inv_s[row_in_tile] = lt == 0.f ? 0.f : 1.f / lt;
+        mbar_arrive(bar(C::kBarLFull));
+        const int row = r0 + row_in_tile;
+        int it = item;
+        asm volatile("" : "+r"(it));        // the head again from the item, rather than kept
+        if (row < p.Lq)
+          p.lse[static_cast<size_t>(it % (p.B * p.H)) * p.Lq + row] =
+              lt == 0.f ? NEG_INF : (m2 + __log2f(lt)) * kLn2;
       }
-      if (kSplit || X == 0) {
-        const bool inb = row < p.Lq;
-        const size_t rows0 = static_cast<size_t>(it.bh) * p.Lq;
-        // a row that saw no key has lt = 0 (its O is 0, whatever the masked
-        // keys held); a NaN score makes lt NaN and goes through
-        const bool empty = lt == 0.f;
-        const float inv = empty ? 0.f : 1.f / lt;
-        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, inb);
-        uint8_t* base =
-            reinterpret_cast<uint8_t*>(p.o + (rows0 + it.r0 + wq * 32) * D) + (kSplit ? X * 128 : 0);
-        uint32_t w[32];
-#pragma unroll
-        for (int kq = 0; kq < 32; ++kq) {
-          const int c = kq / 16;
-          const int j = (2 * kq) % 32;
-          w[kq] = empty ? 0u : pack_bf16(__uint_as_float(o[c][j]) * inv, __uint_as_float(o[c][j + 1]) * inv);
-        }
-        transpose_octets(w, lane);
-        store_octet_lines(w, base, D * 2, valid, lane);
-        if (X == 0 && inb) p.lse[rows0 + row] = empty ? NEG_INF : (m2 + __log2f(lt)) * kLn2;
-      }
-      // ---- next item ----
-      const int s = n & 1;
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarItemFull + s), (n >> 1) & 1, abort_flag, p.err)))
-        break;
-      const int next = next_item[s];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kBarItemEmpty + s));
-      ++n;
-      if (next < 0) break;
-      item = next;
+      ++on;
     }
   }
 
@@ -655,7 +663,9 @@ cudaError_t launch_window_fwd(const CUtensorMap& tq, const CUtensorMap& tk, cons
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  kern<<<p.n_items, C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, p);
+  int sms = 0;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  kern<<<std::min(p.n_items, sms), C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 

@@ -132,6 +132,28 @@ attn_status_t make_map_f32(CUtensorMap* map, void* ptr, int B, int H, long long 
   return ATTN_OK;
 }
 
+attn_status_t make_map_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ptr,
+                             const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                             CUtensorMapSwizzle swizzle) {
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], e[5];
+  if (rank < 1 || rank > 5) return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    e[i] = 1;
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  CUresult r = g_encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(ptr), d, s, b, e,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return ATTN_ERR_CUDA;
+  }
+  return ATTN_OK;
+}
+
 // K/V heads: 1 <= Hkv <= H and Hkv divides H (query head h reads K/V head
 // h / (H / Hkv)).
 bool valid_kv_heads(int H, int Hkv) { return Hkv >= 1 && Hkv <= H && H % Hkv == 0; }

@@ -15,6 +15,10 @@ attn_status_t make_map(CUtensorMap* map, const void* ptr, int B, int H, long lon
 // The fp32 dQ accumulator [B, H, L, d] with boxes of 32 x box_rows.
 attn_status_t make_map_f32(CUtensorMap* map, void* ptr, int B, int H, long long L, int d,
                            int box_rows);
+// A tiled tensor map of any rank with unit element strides and zero fill.
+attn_status_t make_map_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ptr,
+                             const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                             CUtensorMapSwizzle swizzle);
 attn_status_t check_common(int B, int H, long long Lq, long long Lk, int d, float scale);
 attn_status_t cuda_status(const char* where, cudaError_t e);
 // K/V heads: 1 <= Hkv <= H and Hkv divides H.

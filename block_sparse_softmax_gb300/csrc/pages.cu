@@ -65,36 +65,60 @@ __device__ __forceinline__ T block_scan(T v, T* warp_sums, T* total) {
   return before;
 }
 
+// A thread's 32 entries of `refs` from 32 * t on as a mask of the pages in use
+// (bits past the last page are clear); all eight loads are in flight at once.
+constexpr int kSpan = 32 * kBookThreads;          // entries the block looks at in one turn
+__device__ __forceinline__ uint32_t used_mask(const int* refs, int P, long long first) {
+  uint32_t mask = 0;
+  if (first + 32 <= P && (reinterpret_cast<uintptr_t>(refs) & 15u) == 0) {
+    int4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const int4*>(refs + first + 4 * u);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      mask |= (v[u].x > 0 ? 1u : 0u) << (4 * u) | (v[u].y > 0 ? 2u : 0u) << (4 * u) |
+              (v[u].z > 0 ? 4u : 0u) << (4 * u) | (v[u].w > 0 ? 8u : 0u) << (4 * u);
+  } else {
+    for (int u = 0; u < 32 && first + u < P; ++u) mask |= (refs[first + u] > 0 ? 1u : 0u) << u;
+  }
+  return mask;
+}
+// ... of the pages that exist.
+__device__ __forceinline__ uint32_t page_mask(int P, long long first) {
+  return first >= P ? 0u : first + 32 <= P ? 0xFFFFFFFFu : (1u << (P - first)) - 1u;
+}
+
 // Calls take(rank, page) for the `want` lowest free pages in ascending order,
-// or returns false without a call when there are fewer.
+// or returns false without a call when there are fewer.  Free pages often lie
+// side by side, in few threads' masks: up to kPageList of them are listed in
+// shared memory and given out by all threads.
+constexpr int kPageList = 4096;
 template <class Take>
 __device__ bool take_free_pages(const int* refs, int P, int want, int* warp_sums, const Take& take) {
+  __shared__ int list[kPageList];
   if (want == 0) return true;
-  for (int pass = 0; pass < 2; ++pass) {
+  const bool once = P <= kSpan;                   // one turn: counted and given out at a time
+  for (int pass = once ? 1 : 0; pass < 2; ++pass) {
     int found = 0;
-    for (long long x0 = 0; x0 < P && found < want; x0 += 4 * kBookThreads) {
-      const long long x = x0 + 4 * static_cast<int>(threadIdx.x);
-      int f[4];
-      int n = 0;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        f[u] = x + u < P && refs[x + u] == 0;
-        n += f[u];
-      }
+    for (long long x0 = 0; x0 < P && found < want; x0 += kSpan) {
+      const long long x = x0 + 32ll * threadIdx.x;
+      uint32_t free = page_mask(P, x) & ~used_mask(refs, P, x);
       int total;
-      int rank = found + block_scan(n, warp_sums, &total);
-      if (pass == 1) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (f[u]) {
-            if (rank < want) take(rank, static_cast<int>(x + u));
-            ++rank;
-          }
-      }
+      int rank = found + block_scan(__popc(free), warp_sums, &total);
+      if (once && total < want) return false;
+      if (pass == 1)
+        for (; free != 0 && rank < want; free &= free - 1, ++rank) {
+          const int page = static_cast<int>(x) + __ffs(free) - 1;
+          if (want <= kPageList) list[rank] = page;
+          else take(rank, page);
+        }
       found += total;
     }
     if (pass == 0 && found < want) return false;
   }
+  __syncthreads();
+  if (want <= kPageList)
+    for (int r = static_cast<int>(threadIdx.x); r < want; r += kBookThreads) take(r, list[r]);
   __syncthreads();
   return true;
 }
@@ -296,44 +320,69 @@ __global__ void __launch_bounds__(256) kv_evict_kernel(const PageState st, long 
   }
 }
 
-// attn_kv_compact, first half: the pages in use at or past the number of pages
-// in use move, in ascending order, to the free pages below it.
+// attn_kv_compact: the pages in use at or past the number of pages in use move,
+// in ascending order, to the free pages below it.  Where pages and table are
+// small enough the block also rewrites the table, by a map in shared memory.
+constexpr int kSmallTable = 1 << 16;
 __global__ void __launch_bounds__(kBookThreads) kv_compact_kernel(int* refs, int P, int* copy_src,
-                                                                  int* copy_dst, int* count) {
+                                                                  int* copy_dst, int* count, int* table,
+                                                                  int entries, int* err) {
   __shared__ int warp_sums[32];
+  __shared__ unsigned pair_sums[32];
+  extern __shared__ int to[];                     // [P]: a moved page's place, else -1 (entries > 0)
+  const int tid = static_cast<int>(threadIdx.x);
+  const bool once = P <= kSpan;
+  if (entries > 0)
+    for (int i = tid; i < P; i += kBookThreads) to[i] = -1;
   int live = 0;
-  for (int x0 = 0; x0 < P; x0 += kBookThreads) {
-    const int x = x0 + static_cast<int>(threadIdx.x);
-    live += __syncthreads_count(x < P && refs[x] > 0);
+  uint32_t kept = 0;
+  for (long long x0 = 0; x0 < P; x0 += kSpan) {
+    kept = used_mask(refs, P, x0 + 32ll * tid);
+    int total;
+    block_scan(__popc(kept), warp_sums, &total);
+    live += total;
   }
   int n_src = 0, n_dst = 0;
-  for (int x0 = 0; x0 < P; x0 += kBookThreads) {
-    const int x = x0 + static_cast<int>(threadIdx.x);
-    const bool used = x < P && refs[x] > 0;
-    const int src = used && x >= live;
-    const int dst = !used && x < live;
-    int total;
-    const int rank = block_scan(src ? 1 << 16 : dst, warp_sums, &total);
-    if (src) copy_src[n_src + (rank >> 16)] = x;
-    if (dst) copy_dst[n_dst + (rank & 0xFFFF)] = x;
-    n_src += total >> 16;
-    n_dst += total & 0xFFFF;
+  for (long long x0 = 0; x0 < P; x0 += kSpan) {
+    const long long x = x0 + 32ll * tid;
+    const uint32_t used = once ? kept : used_mask(refs, P, x);
+    const uint32_t low = page_mask(live, x);      // the places below the number in use
+    uint32_t src = used & ~low;
+    uint32_t dst = ~used & low;
+    unsigned total;
+    const unsigned rank = block_scan((static_cast<unsigned>(__popc(src)) << 16) + __popc(dst), pair_sums, &total);
+    for (int r = n_src + static_cast<int>(rank >> 16); src != 0; src &= src - 1)
+      copy_src[r++] = static_cast<int>(x) + __ffs(src) - 1;
+    for (int r = n_dst + static_cast<int>(rank & 0xFFFFu); dst != 0; dst &= dst - 1)
+      copy_dst[r++] = static_cast<int>(x) + __ffs(dst) - 1;
+    n_src += static_cast<int>(total >> 16);
+    n_dst += static_cast<int>(total & 0xFFFFu);
   }
   __syncthreads();
-  for (int i = static_cast<int>(threadIdx.x); i < P; i += kBookThreads) {
+#pragma unroll 4
+  for (int i = tid; i < P; i += kBookThreads) {
     if (i < n_src) {
       const int a = copy_src[i], b = copy_dst[i];
       refs[b] = refs[a];
       refs[a] = 0;
+      if (entries > 0) to[a] = b;
     } else {
       copy_src[i] = -1;
       copy_dst[i] = -1;
     }
   }
-  if (threadIdx.x == 0) *count = n_src;
+  if (tid == 0) *count = n_src;
+  if (entries == 0) return;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = tid; i < entries; i += kBookThreads) {
+    const int e = table[i];
+    if (e >= P) record_error(err, ATTN_ERR_BAD_PAGES);
+    else if (e >= 0 && to[e] >= 0) table[i] = to[e];
+  }
 }
 
-// Second half: the table's entries follow (copy_src ascends).
+// A larger table's entries follow in a launch of their own (copy_src ascends).
 __global__ void __launch_bounds__(256) kv_remap_kernel(int* table, long long entries, int P,
                                                        const int* copy_src, const int* copy_dst,
                                                        const int* count, int* err) {
@@ -477,6 +526,22 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const WriteParams p) {
 unsigned grid_256(long long work) {
   long long b = (work + 255) / 256;
   return static_cast<unsigned>(b < 1 ? 1 : (b > 152ll * 16 ? 152ll * 16 : b));
+}
+
+// Dynamic shared memory past 48 KB, once a device.
+attn_status_t allow_smem(const void* kernel, int bytes) {
+  constexpr int kMaxDev = 64;
+  static bool configured[kMaxDev] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status("cudaGetDevice", e);
+  if (dev < 0 || dev >= kMaxDev) return ATTN_ERR_UNSUPPORTED;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_status("cudaFuncSetAttribute", e);
+    configured[dev] = true;
+  }
+  return ATTN_OK;
 }
 
 bool valid_page_size(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
@@ -630,9 +695,13 @@ attn_status_t attn_kv_compact(int32_t* page_table, int32_t* refs, int32_t* copy_
   attn_status_t s = status_word(&err);
   if (s != ATTN_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  kv_compact_kernel<<<1, kBookThreads, 0, st>>>(refs, n_pages, copy_src, copy_dst, count);
-  if ((s = cuda_status("attn_kv_compact launch", cudaGetLastError())) != ATTN_OK) return s;
   const long long entries = static_cast<long long>(S) * max_pages;
+  const bool inside = entries <= kSmallTable && n_pages <= kSpan;
+  const int smem = inside ? n_pages * 4 : 0;
+  if ((s = allow_smem(reinterpret_cast<const void*>(kv_compact_kernel), kSpan * 4)) != ATTN_OK) return s;
+  kv_compact_kernel<<<1, kBookThreads, smem, st>>>(refs, n_pages, copy_src, copy_dst, count, page_table,
+                                                   inside ? static_cast<int>(entries) : 0, err);
+  if ((s = cuda_status("attn_kv_compact launch", cudaGetLastError())) != ATTN_OK || inside) return s;
   kv_remap_kernel<<<grid_256(entries), 256, 0, st>>>(page_table, entries, n_pages, copy_src, copy_dst,
                                                      count, err);
   return cuda_status("attn_kv_compact launch", cudaGetLastError());

@@ -54,9 +54,11 @@ __device__ __forceinline__ WindowBlocks window_blocks(const WindowMask& w, int r
   return b;
 }
 
-}  // namespace bss
+// The lowest n bits (n may lie outside [0, 32]).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
 
-namespace bss {
 // The mask of a launch with Lk keys; false for window < 1 or a negative argument (window_fwd.cu).
 bool window_mask(WindowMask* w, int Lk, int64_t window, int64_t sinks, int64_t q_offset,
                  int64_t k_offset);

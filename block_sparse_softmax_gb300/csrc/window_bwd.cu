@@ -129,8 +129,8 @@ struct WinBwdCfg {
 // a thread).
 template <int D>
 struct WinBwdRegs {
-  static constexpr uint32_t kLow = 96;
-  static constexpr uint32_t kMid = 160;
+  static constexpr uint32_t kLow = 80;
+  static constexpr uint32_t kMid = 168;
   static constexpr uint32_t kHigh = 96;
   static constexpr uint32_t kLaunchRegs = 128;
   static_assert(kLow + 2 * kMid + kHigh <= 512, "register split exceeds an SM sub-partition");
@@ -525,13 +525,19 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
         break;
       }
       tc_fence_after();
-      // element mask, in query index c of the tile: allowed are qlo <= c <= qhi
-      // (a sink key has no upper limit, a key past the last one nothing); the
-      // ragged tail (query >= Lq) has -lse2 = -inf, so P is 0 there already
-      const long long own = static_cast<long long>(key) - p.w.sh - static_cast<long long>(i) * kTileM;
-      const int qlo = key < Lk ? static_cast<int>(max(0ll, min(128ll, own))) : 128;
-      const int qhi = key < p.w.snk ? 127 : static_cast<int>(max(-1ll, min(127ll, own + p.w.window - 1)));
-      const bool need_mask = __any_sync(0xFFFFFFFFu, qlo > 0 || qhi < 127);
+      // element mask: a bit for each of this half's 64 queries that sees the
+      // key (those from its own position on, up to the window's end unless
+      // the key is a sink; none for a key past the last one).  The ragged tail
+      // (query >= Lq) has -lse2 = -inf, so P is 0 there already
+      uint32_t seen[2];
+      {
+        const long long own = static_cast<long long>(key) - p.w.sh - static_cast<long long>(i) * kTileM - 64 * X;
+        const int qlo = key < Lk ? static_cast<int>(max(0ll, min(64ll, own))) : 64;
+        const int end = key < p.w.snk ? 64 : static_cast<int>(max(0ll, min(64ll, own + p.w.window)));
+        seen[0] = bits_below(end) & ~bits_below(qlo);
+        seen[1] = bits_below(end - 32) & ~bits_below(qlo - 32);
+      }
+      const bool need_mask = __any_sync(0xFFFFFFFFu, (seen[0] & seen[1]) != 0xFFFFFFFFu);
       // ---- phase 1: P (four chunks of 16 queries; chunk c+1's TMEM load is in
       // flight while chunk c is computed) ----
       float pf[4][16];
@@ -558,7 +564,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
           if (need_mask) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (col + e < qlo || col + e > qhi) pf[c][e] = 0.f;
+              if (!((seen[c >> 1] >> (16 * (c & 1) + e)) & 1u)) pf[c][e] = 0.f;
           }
           uint32_t pk[8];
 #pragma unroll
@@ -598,7 +604,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
             if (need_mask) {          // a masked pair sends nothing, whatever dP and D hold
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                if (col + e + u < qlo || col + e + u > qhi) ds[u] = 0.f;
+                if (!((seen[c >> 1] >> (16 * (c & 1) + e + u)) & 1u)) ds[u] = 0.f;
             }
             dk[e / 2] = pack_bf16(ds[0], ds[1]);
             dk[e / 2 + 1] = pack_bf16(ds[2], ds[3]);

@@ -129,11 +129,6 @@ __device__ __forceinline__ int window_next(int item, const WindowFwdParams& p, i
   return item;
 }
 
-// The lowest n bits (n may lie outside [0, 32]).
-__device__ __forceinline__ uint32_t bits_below(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
-}
-
 template <int D>
 __global__ void __launch_bounds__(512, 1)
     attn_fwd_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

@@ -7,8 +7,8 @@
 //   dS_ij = scale P_ij (dO_i . V_j - D_i)
 //   dK_j = sum_i dS_ij q_i,   dQ_i = sum_j dS_ij k_j
 //
-// The main kernel is the KV-owned traversal of the dense backward (one CTA per
-// 128-key tile, scores transposed so that a thread owns a key row, dK and dV
+// The main kernel is the KV-owned traversal of the dense backward (an item is a
+// 128-key tile; scores transposed so that a thread owns a key row, dK and dV
 // in tensor memory, dQ added into an fp32 accumulator by bulk reduce-adds)
 // over the query tiles that the window lets the key tile meet.
 //
@@ -49,7 +49,8 @@ struct WindowBwdParams {
   int nk;               // key tiles
   int nst;              // the first of them, which hold a sink key
   int seg_s, seg_w;     // segments of a sink tile's walk and of another tile's
-  int head_group;       // K/V heads whose key tiles are launched together
+  int head_group;       // K/V heads whose key tiles come together
+  int n_items;          // key tiles, or segments of them, over all heads
   int* err;
 };
 
@@ -86,7 +87,9 @@ struct WinBwdCfg {
   static constexpr int kBarStat = kBarMmaDone + 1;     // [2]: LSE/D of a query tile staged
   static constexpr int kBarStaged = kBarStat + 2;      // dQ round staged (CTA-wide drain)
   static constexpr int kBarStageFree = kBarStaged + 1; // staging read by the reduce (CTA-wide drain)
-  static constexpr int kNumBars = kBarStageFree + 1;
+  static constexpr int kBarKVEmpty = kBarStageFree + 1;  // an item's last MMA that reads K or V completed
+  static constexpr int kBarDKVEmpty = kBarKVEmpty + 1;   // its dK and dV read out of TMEM
+  static constexpr int kNumBars = kBarDKVEmpty + 1;
   // dQ drain: at d=128 each drain warp reduces its own 32 rows (no barrier
   // among the four warps, which frees dQ's columns for dP^T sooner); at d=64,
   // with one round per tile and a shorter period, one thread reduces all 128
@@ -120,25 +123,27 @@ struct WinBwdCfg {
 
 // Register split per warpgroup (setmaxnreg): warpgroup 0 (TMA, MMA, two idle
 // warps) kLow, the P/dS warpgroups 1-2 kMid (each thread keeps 64 fp32 P
-// values between its two phases), the dQ warpgroup 3 kHigh.  96/160/160/96
-// compiles every instantiation without register spills (88/160/160/104
-// spilled a few bytes at d=128 and measured 1.9 % slower there).  Each SM
+// values between its two phases), the dQ warpgroup 3 kHigh.  This split
+// compiles without spills, which matter more than their bytes say: the tiles
+// leave L1 next to nothing, so each spilled value comes back from L2 (with 20
+// values spilled and the mask compared element by element the main kernel of
+// B1 H16(4) L16384 d128, window 1024, sinks 4 took 437 us, now 395).  Each SM
 // sub-partition holds one warp of every warpgroup: kLow + 2 kMid + kHigh <= 512
 // registers a lane, and the split fits the 512 * 128 registers the launch
-// holds (launch_main refuses to launch if ptxas gave the kernel fewer than 128
-// a thread).
+// holds (the launcher refuses to launch if ptxas gave the kernel fewer than
+// 128 a thread).
 template <int D>
 struct WinBwdRegs {
-  static constexpr uint32_t kLow = 80;
+  static constexpr uint32_t kLow = 72;
   static constexpr uint32_t kMid = 168;
-  static constexpr uint32_t kHigh = 96;
+  static constexpr uint32_t kHigh = 104;
   static constexpr uint32_t kLaunchRegs = 128;
   static_assert(kLow + 2 * kMid + kHigh <= 512, "register split exceeds an SM sub-partition");
   static_assert(128 * (kLow + 2 * kMid + kHigh) <= 512 * kLaunchRegs, "register split exceeds the launch");
 };
 
 
-// CTA x: the sink tiles' segments first (each at least as long as any other
+// Item x: the sink tiles' segments first (each at least as long as any other
 // walk), then the other key tiles in groups of K/V heads, tile-major inside a
 // group, so that the running CTAs' Q, dO and dQ accumulator stay in L2.
 struct WindowBwdCta {
@@ -235,16 +240,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
   if (*reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
 
   const int Lk = p.Lk, Lq = p.Lq;
-  const WindowBwdCta cta = window_bwd_cta(static_cast<int>(blockIdx.x), p);
-  const int j = cta.j;                            // key tile owned by this CTA
-  const int bh = cta.bh;                          // (b, K/V head)
   const int G = p.H / p.Hkv;
-  const int b = bh / p.Hkv;
-  const int h = bh - b * p.Hkv;                   // K/V head
-  const int hq0 = h * G;                          // first query head of the group
-  const int bhq0 = b * p.H + hq0;
-  const WindowQWalk walk = window_bwd_walk(cta, p);
-  const int n_it = walk.n_it;                     // query tiles met, over the group's heads
 
   if (tid == 0) {
     mbar_init(bar(C::kBarKV), 1);
@@ -267,17 +263,13 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     mbar_init(bar(C::kBarStaged), 128);
     mbar_init(bar(C::kBarStageFree), 1);
     mbar_init(bar(C::kBarDKVFull), 1);
+    mbar_init(bar(C::kBarDKVEmpty), 256);
+    mbar_init(bar(C::kBarKVEmpty), 1);
     mbar_init(bar(C::kBarMmaDone), 1);
     mbar_init(bar(C::kBarStat + 0), 128);
     mbar_init(bar(C::kBarStat + 1), 128);
     *abort_flag = 0;
     fence_barrier_init();
-    // K_j and V_j go out at once: their load overlaps the rest of the set-up
-    mbar_arrive_expect_tx(bar(C::kBarKV), 2 * C::kTileBytes);
-    for (int c = 0; c < C::kChunks; ++c) {
-      tma_load_4d(sbase + C::kKOff + c * C::kChunkBytes, &tmK, bar(C::kBarKV), c * 64, j * kTileN, h, b);
-      tma_load_4d(sbase + C::kVOff + c * C::kChunkBytes, &tmV, bar(C::kBarKV), c * 64, j * kTileN, h, b);
-    }
   }
   if (warp == 0) {
     tmem_alloc(sbase + C::kMiscOff, C::kTmemCols);
@@ -295,33 +287,53 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmDO);
-      int nq_ld = 0, ndo_ld = 0;
-      int g, i;
-      walk.start(g, i);
-      for (int it = 0; it < n_it; walk.advance(g, i), ++it) {
-        const int row = i * kTileM;
-        const int hq = hq0 + g;
-        const int sq = it % C::kStagesQ;
-        if (it >= C::kStagesQ &&
-            !wait_bar(bar(C::kBarQEmpty + sq), ((it / C::kStagesQ) & 1) ^ 1, abort_flag, p.err))
-          break;
-        mbar_arrive_expect_tx(bar(C::kBarQFull + sq), C::kTileBytes);
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_4d(sbase + C::kQOff + sq * C::kTileBytes + c * C::kChunkBytes, &tmQ,
-                      bar(C::kBarQFull + sq), c * 64, row, hq, b);
-        ++nq_ld;
-        const int sd = it % C::kStagesDO;
-        if (it >= C::kStagesDO &&
-            !wait_bar(bar(C::kBarDOEmpty + sd), ((it / C::kStagesDO) & 1) ^ 1, abort_flag, p.err))
-          break;
-        mbar_arrive_expect_tx(bar(C::kBarDOFull + sd), C::kTileBytes);
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_4d(sbase + C::kDOOff + sd * C::kTileBytes + c * C::kChunkBytes, &tmDO,
-                      bar(C::kBarDOFull + sd), c * 64, row, hq, b);
-        ++ndo_ld;
+      int nq_ld = 0, ndo_ld = 0;   // query tiles' Q and dO loaded (over all items)
+      int kv = 0;                  // items' K and V loaded
+      bool ok = true;
+      for (int x = static_cast<int>(blockIdx.x); x < p.n_items && ok; x += static_cast<int>(gridDim.x)) {
+        const WindowBwdCta cta = window_bwd_cta(x, p);
+        const WindowQWalk walk = window_bwd_walk(cta, p);
+        if (walk.n_it == 0) continue;
+        const int b = cta.bh / p.Hkv;
+        const int h = cta.bh - b * p.Hkv;
+        if (kv > 0 && !wait_bar(bar(C::kBarKVEmpty), (kv - 1) & 1, abort_flag, p.err)) break;
+        mbar_arrive_expect_tx(bar(C::kBarKV), 2 * C::kTileBytes);
+        for (int c = 0; c < C::kChunks; ++c) {
+          tma_load_4d(sbase + C::kKOff + c * C::kChunkBytes, &tmK, bar(C::kBarKV), c * 64, cta.j * kTileN, h, b);
+          tma_load_4d(sbase + C::kVOff + c * C::kChunkBytes, &tmV, bar(C::kBarKV), c * 64, cta.j * kTileN, h, b);
+        }
+        ++kv;
+        int g, i;
+        walk.start(g, i);
+        for (int it = 0; it < walk.n_it; walk.advance(g, i), ++it) {
+          const int row = i * kTileM;
+          const int hq = h * G + g;
+          const int sq = nq_ld % C::kStagesQ;
+          if (nq_ld >= C::kStagesQ &&
+              !wait_bar(bar(C::kBarQEmpty + sq), ((nq_ld / C::kStagesQ) & 1) ^ 1, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(C::kBarQFull + sq), C::kTileBytes);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_4d(sbase + C::kQOff + sq * C::kTileBytes + c * C::kChunkBytes, &tmQ,
+                        bar(C::kBarQFull + sq), c * 64, row, hq, b);
+          ++nq_ld;
+          const int sd = ndo_ld % C::kStagesDO;
+          if (ndo_ld >= C::kStagesDO &&
+              !wait_bar(bar(C::kBarDOEmpty + sd), ((ndo_ld / C::kStagesDO) & 1) ^ 1, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(C::kBarDOFull + sd), C::kTileBytes);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_4d(sbase + C::kDOOff + sd * C::kTileBytes + c * C::kChunkBytes, &tmDO,
+                        bar(C::kBarDOFull + sd), c * 64, row, hq, b);
+          ++ndo_ld;
+        }
       }
       // Drain: every load issued has landed before the CTA may exit.
-      drain_bar(bar(C::kBarKV), 0);
+      if (kv > 0) drain_bar(bar(C::kBarKV), (kv - 1) & 1);
       for (int x = max(0, nq_ld - C::kStagesQ); x < nq_ld; ++x)
         drain_bar(bar(C::kBarQFull + x % C::kStagesQ), (x / C::kStagesQ) & 1);
       for (int x = max(0, ndo_ld - C::kStagesDO); x < ndo_ld; ++x)
@@ -337,11 +349,28 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     //   completes; dQ(i) over dP^T(i): after ds_ready(i) (dP^T read);
     //   dP^T(i+1) over dQ(i): after dq_free(i); dS(i+1) written after
     //   dP^T(i+1) completes, so after dQ(i) and dK(i) read dS(i).
+    // Tiles are counted over all items (n).  An item's S^T and dP^T wait for
+    // its K and V, whose buffers are free once the last item's dQ has
+    // completed, and its first dV for the last item's dK and dV to be read out.
     if (lane == 0) {
       constexpr uint32_t kIdescT = idesc_bf16_f32(kTileM, kTileN, false, false);  // S^T, dP^T
       constexpr uint32_t kIdescKV = idesc_bf16_f32(kTileM, D, false, true);       // dV, dK
       constexpr uint32_t kIdescQ = idesc_bf16_f32(kTileM, D, true, true);         // dQ
       const uint32_t ka = sbase + C::kKOff, va = sbase + C::kVOff, dsa = sbase + C::kDSOff;
+      // K-major and M-/N-major descriptors of a tile, built once per group of
+      // MMAs, each of which adds its offset.  They go through an empty asm so
+      // that the compiler does not keep every group's in registers across the
+      // loop and spill them, to an L1 that the tiles leave almost nothing of.
+      auto desc_k = [](uint32_t addr) -> uint64_t {
+        uint64_t d = sdesc_sw128(addr, 16, 1024);
+        asm volatile("" : "+l"(d));
+        return d;
+      };
+      auto desc_mn = [](uint32_t addr) -> uint64_t {
+        uint64_t d = sdesc_sw128(addr, C::kChunkBytes, 1024);
+        asm volatile("" : "+l"(d));
+        return d;
+      };
       auto qaddr = [&](int it) { return sbase + C::kQOff + (it % C::kStagesQ) * C::kTileBytes; };
       auto doaddr = [&](int it) { return sbase + C::kDOOff + (it % C::kStagesDO) * C::kTileBytes; };
       // S^T(it) = K_j Q^T
@@ -349,11 +378,11 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
         if (!wait_bar(bar(C::kBarQFull + it % C::kStagesQ), (it / C::kStagesQ) & 1, abort_flag, p.err))
           return false;
         tc_fence_after();
-        const uint32_t qa = qaddr(it);
+        const uint64_t dq = desc_k(qaddr(it)), dk = desc_k(ka);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
-          mma_ss(tmem + C::kColST, sdesc_sw128(ka + off, 16, 1024), sdesc_sw128(qa + off, 16, 1024),
+          mma_ss(tmem + C::kColST, sdesc_add(dk, off), sdesc_add(dq, off),
                  kIdescT, kk > 0 ? 1u : 0u);
         }
         mma_commit(bar(C::kBarSFull));
@@ -370,12 +399,12 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
             return false;
         }
         tc_fence_after();
-        const uint32_t doa = doaddr(it) + h * (kTileN / 2) * 128;
+        const uint64_t ddo = desc_k(doaddr(it) + h * (kTileN / 2) * 128), dv = desc_k(va);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
-          mma_ss(tmem + C::kColDPT + h * (kTileN / 2), sdesc_sw128(va + off, 16, 1024),
-                 sdesc_sw128(doa + off, 16, 1024), kIdescTHalf, kk > 0 ? 1u : 0u);
+          mma_ss(tmem + C::kColDPT + h * (kTileN / 2), sdesc_add(dv, off),
+                 sdesc_add(ddo, off), kIdescTHalf, kk > 0 ? 1u : 0u);
         }
         mma_commit(bar(C::kBarDPFull + h));
         return true;
@@ -386,77 +415,83 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
         if (!wait_bar(bar(C::kBarDOFull + it % C::kStagesDO), (it / C::kStagesDO) & 1, abort_flag, p.err))
           return false;
         tc_fence_after();
-        const uint32_t doa = doaddr(it);
+        const uint64_t ddo = desc_k(doaddr(it)), dv = desc_k(va);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
-          mma_ss(tmem + C::kColDPT, sdesc_sw128(va + off, 16, 1024), sdesc_sw128(doa + off, 16, 1024),
+          mma_ss(tmem + C::kColDPT, sdesc_add(dv, off), sdesc_add(ddo, off),
                  kIdescT, kk > 0 ? 1u : 0u);
         }
         mma_commit(bar(C::kBarDPFull));
         mma_commit(bar(C::kBarDPFull + 1));
         return true;
       };
-      bool ok = wait_bar(bar(C::kBarKV), 0, abort_flag, p.err);
-      if (ok && n_it > 0) ok = issue_s(0) && issue_dp(0);
-      int g, i;
-      walk.start(g, i);
-      for (int it = 0; it < n_it && ok; walk.advance(g, i), ++it) {
-        const bool more = it + 1 < n_it;               // another query tile follows
-        // dV += P^T dO_i  (K dimension = the 128 queries)
-        if (!wait_bar(bar(C::kBarPReady), it & 1, abort_flag, p.err)) break;
-        tc_fence_after();
-        const uint32_t doa = doaddr(it);
-#pragma unroll
-        for (int kk = 0; kk < kTileM / 16; ++kk) {
-          mma_ts(tmem + C::kColDV, tmem + C::kColST + C::pcol(kk),
-                 sdesc_sw128(doa + kk * 2048, C::kChunkBytes, 1024), kIdescKV,
-                 (it > 0 || kk > 0) ? 1u : 0u);
+      // dP^T(n), over dQ(n - 1) where it shares dQ's columns: each half once
+      // its columns have been read out
+      auto issue_dp_over = [&](int n) -> bool {
+        if (kDPHalves) {
+          if (n > 0 && !wait_bar(bar(C::kBarDQFree), (n - 1) & 1, abort_flag, p.err)) return false;
+          if (!issue_dp_half(n, 0)) return false;
+          if (n > 0 && !wait_bar(bar(C::kBarDQFree + 1), (n - 1) & 1, abort_flag, p.err)) return false;
+          return issue_dp_half(n, 1);
         }
-        mma_commit(bar(C::kBarDOEmpty + it % C::kStagesDO));   // dP^T(it) and dV(it) read dO_i
-        if (more && !issue_s(it + 1)) break;
-        // the P/dS warps run for a while: poll gently so that the issue slots
-        // they share with this warp stay theirs
-        if (!wait_bar_relaxed(bar(C::kBarDSReady), it & 1, abort_flag, p.err)) break;
-        tc_fence_after();
-        // dQ_i = dS K_j  (M = queries, N = d, K dimension = the 128 keys); with
-        // columns of its own, only after the previous dQ has been read
-        if (!C::kDQOverDP && it > 0 && !wait_bar(bar(C::kBarDQFree), (it - 1) & 1, abort_flag, p.err))
-          break;
+        return issue_dp(n);
+      };
+      bool ok = true;
+      int n = 0;               // query tiles done
+      int kv = 0;              // items done
+      for (int x = static_cast<int>(blockIdx.x); x < p.n_items && ok; x += static_cast<int>(gridDim.x)) {
+        const int n_it = window_bwd_walk(window_bwd_cta(x, p), p).n_it;
+        if (n_it == 0) continue;
+        ok = wait_bar(bar(C::kBarKV), kv & 1, abort_flag, p.err) && issue_s(n) && issue_dp_over(n);
+        for (int it = 0; it < n_it && ok; ++it, ++n) {
+          const bool more = it + 1 < n_it;               // another query tile follows
+          ok = false;
+          // dV += P^T dO_i  (K dimension = the 128 queries)
+          if (!wait_bar(bar(C::kBarPReady), n & 1, abort_flag, p.err)) break;
+          if (it == 0 && kv > 0 && !wait_bar(bar(C::kBarDKVEmpty), (kv - 1) & 1, abort_flag, p.err)) break;
+          tc_fence_after();
+          const uint64_t ddo = desc_mn(doaddr(n));
 #pragma unroll
-        for (int kk = 0; kk < kTileN / 16; ++kk) {
-          mma_ss(tmem + C::kColDQ, sdesc_sw128(dsa + kk * 2048, C::kChunkBytes, 1024),
-                 sdesc_sw128(ka + kk * 2048, C::kChunkBytes, 1024), kIdescQ, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(bar(C::kBarDQFull));
-        // dK += dS^T Q_i  (dS^T: the same tile read K-major; K dimension = queries)
-        const uint32_t qa = qaddr(it);
-#pragma unroll
-        for (int kk = 0; kk < kTileM / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
-          mma_ss(tmem + C::kColDK, sdesc_sw128(dsa + off, 16, 1024),
-                 sdesc_sw128(qa + kk * 2048, C::kChunkBytes, 1024), kIdescKV,
-                 (it > 0 || kk > 0) ? 1u : 0u);
-        }
-        mma_commit(bar(C::kBarQEmpty + it % C::kStagesQ));
-        if (more) {
-          if (kDPHalves) {
-            // dP^T(i+1) over dQ(i): each half once its columns have been read out
-            if (!wait_bar(bar(C::kBarDQFree), it & 1, abort_flag, p.err)) break;
-            if (!issue_dp_half(it + 1, 0)) break;
-            if (!wait_bar(bar(C::kBarDQFree + 1), it & 1, abort_flag, p.err)) break;
-            if (!issue_dp_half(it + 1, 1)) break;
-          } else if (C::kDQOverDP) {
-            // one N=128 group once both halves of dQ's columns are read out
-            if (!wait_bar(bar(C::kBarDQFree), it & 1, abort_flag, p.err)) break;
-            if (!wait_bar(bar(C::kBarDQFree + 1), it & 1, abort_flag, p.err)) break;
-            if (!issue_dp(it + 1)) break;
-          } else {
-            if (!issue_dp(it + 1)) break;
+          for (int kk = 0; kk < kTileM / 16; ++kk) {
+            mma_ts(tmem + C::kColDV, tmem + C::kColST + C::pcol(kk),
+                   sdesc_add(ddo, kk * 2048), kIdescKV,
+                   (it > 0 || kk > 0) ? 1u : 0u);
           }
+          mma_commit(bar(C::kBarDOEmpty + n % C::kStagesDO));   // dP^T(n) and dV(n) read dO_i
+          if (more && !issue_s(n + 1)) break;
+          // the P/dS warps run for a while: poll gently so that the issue slots
+          // they share with this warp stay theirs
+          if (!wait_bar_relaxed(bar(C::kBarDSReady), n & 1, abort_flag, p.err)) break;
+          tc_fence_after();
+          // dQ_i = dS K_j  (M = queries, N = d, K dimension = the 128 keys); with
+          // columns of its own, only after the previous dQ has been read
+          if (!C::kDQOverDP && n > 0 && !wait_bar(bar(C::kBarDQFree), (n - 1) & 1, abort_flag, p.err))
+            break;
+          const uint64_t dds = desc_mn(dsa), dk = desc_mn(ka);
+#pragma unroll
+          for (int kk = 0; kk < kTileN / 16; ++kk) {
+            mma_ss(tmem + C::kColDQ, sdesc_add(dds, kk * 2048),
+                   sdesc_add(dk, kk * 2048), kIdescQ, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(C::kBarDQFull));
+          if (!more) mma_commit(bar(C::kBarKVEmpty));
+          // dK += dS^T Q_i  (dS^T: the same tile read K-major; K dimension = queries)
+          const uint64_t dq = desc_mn(qaddr(n)), dds2 = desc_k(dsa);
+#pragma unroll
+          for (int kk = 0; kk < kTileM / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+            mma_ss(tmem + C::kColDK, sdesc_add(dds2, off),
+                   sdesc_add(dq, kk * 2048), kIdescKV,
+                   (it > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(bar(C::kBarQEmpty + n % C::kStagesQ));
+          ok = !more || issue_dp_over(n + 1);
         }
+        if (!ok) break;
+        mma_commit(bar(C::kBarDKVFull));
+        ++kv;
       }
-      mma_commit(bar(C::kBarDKVFull));
       mma_commit(bar(C::kBarMmaDone));
       drain_bar(bar(C::kBarMmaDone), 0);   // every MMA issued has completed
     }
@@ -472,7 +507,6 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     const int X = (warp - 4) >> 2;
     const int wq = warp & 3;
     const int kr = wq * 32 + lane;
-    const int key = j * kTileN + kr;
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tST = tmem + lane_base + C::kColST;
     const uint32_t tDPT = tmem + lane_base + C::kColDPT;
@@ -482,10 +516,10 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     uint8_t* ds_row = smem + C::kDSOff + X * C::kChunkBytes + kr * 128;   // this key's dS row
     // statistics of query tile i of query head hq0 + g, negated so that
     // P = ex2(S sl2 + nl2) and dP - D = dP scale + ndl are single FMAs
-    auto load_stats = [&](int g, int i, float& nl2, float& ndl) {
+    auto load_stats = [&](int bhq, int i, float& nl2, float& ndl) {
       const int q = i * kTileM + kr;
       if (q < Lq) {
-        const size_t stat = static_cast<size_t>(bhq0 + g) * Lq + q;
+        const size_t stat = static_cast<size_t>(bhq) * Lq + q;
         const float lse = __ldg(p.lse + stat);
         nl2 = (lse == -INF) ? -INF : -(lse * kLog2e);  // an empty row contributes nothing
         ndl = -(__ldg(p.delta + stat) * scale);
@@ -494,33 +528,45 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
         ndl = 0.f;
       }
     };
-    if (X == 0) {
-      float l2 = -INF, dl = 0.f;
-      int gf, tf;
-      walk.start(gf, tf);
-      if (n_it > 0) load_stats(gf, tf, l2, dl);
-      stats[kr] = l2;
-      stats[128 + kr] = dl;
-      mbar_arrive(bar(C::kBarStat + 0));
-    }
-    // Buffer (it & 1) holds the statistics of the it-th query tile met (minus
-    // the LSE in log2 units, minus scale * D).  It is rewritten (for tile it + 2) at the end of tile
-    // it + 1 by half 0; by then dP^T(it + 1) has been issued, which waited for
-    // dS(it) of both halves, so nobody reads it for tile it any more.
+    auto store_stats = [&](int n, float nl2, float ndl) {
+      float* to = stats + (n & 1) * 256;
+      to[kr] = nl2;
+      to[128 + kr] = ndl;
+      mbar_arrive(bar(C::kBarStat + (n & 1)));
+    };
+    // Buffer (n & 1) holds the statistics of the n-th query tile met (minus
+    // the LSE in log2 units, minus scale * D).  It is rewritten (for tile n + 2)
+    // by half 0 after its tile n + 1; by then dP^T(n + 1) has been issued, which
+    // waited for dS(n) of both halves, so nobody reads it for tile n any more.
     bool ok = true;
+    int n = 0;                 // query tiles done (over all items)
+    int kv = 0;                // items with query tiles done
+    for (int x = static_cast<int>(blockIdx.x); x < p.n_items && ok; x += static_cast<int>(gridDim.x)) {
+    int key, n_it;
+    {
+    const WindowBwdCta cta = window_bwd_cta(x, p);
+    const WindowQWalk walk = window_bwd_walk(cta, p);
+    key = cta.j * kTileN + kr;
+    n_it = walk.n_it;
+    const int bhq0 = (cta.bh / p.Hkv) * p.H + (cta.bh % p.Hkv) * G;   // first query head of the group
     int g, i;
     walk.start(g, i);
-    for (int it = 0; it < n_it; walk.advance(g, i), ++it) {
-      const float* lse2 = stats + (it & 1) * 256 + 64 * X;
+    if (X == 0 && n_it > 0) {
+      float l2, dl;
+      load_stats(bhq0 + g, i, l2, dl);
+      store_stats(n, l2, dl);
+    }
+    for (int it = 0; it < n_it; walk.advance(g, i), ++it, ++n) {
+      const float* lse2 = stats + (n & 1) * 256 + 64 * X;
       const float* dlt = lse2 + 128;
       float l2n = 0.f, dln = 0.f;
       if (X == 0 && it + 1 < n_it) {
         int gn = g, in = i;
         walk.advance(gn, in);
-        load_stats(gn, in, l2n, dln);
+        load_stats(bhq0 + gn, in, l2n, dln);
       }
-      if (!wait_bar(bar(C::kBarSFull), it & 1, abort_flag, p.err) ||
-          !wait_bar(bar(C::kBarStat + (it & 1)), (it >> 1) & 1, abort_flag, p.err)) {
+      if (!wait_bar(bar(C::kBarSFull), n & 1, abort_flag, p.err) ||
+          !wait_bar(bar(C::kBarStat + (n & 1)), (n >> 1) & 1, abort_flag, p.err)) {
         ok = false;
         break;
       }
@@ -576,7 +622,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(bar(C::kBarPReady));
       // ---- phase 2: dS = P o (dP - D), into shared memory ----
-      if (!wait_bar(bar(C::kBarDPFull + X), it & 1, abort_flag, p.err)) {
+      if (!wait_bar(bar(C::kBarDPFull + X), n & 1, abort_flag, p.err)) {
         ok = false;
         break;
       }
@@ -622,26 +668,24 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(bar(C::kBarDSReady));
-      if (X == 0) {
-        // statistics of the next query tile
-        float* nxt = stats + ((it + 1) & 1) * 256;
-        nxt[kr] = l2n;
-        nxt[128 + kr] = dln;
-        mbar_arrive(bar(C::kBarStat + ((it + 1) & 1)));
-      }
+      if (X == 0 && it + 1 < n_it) store_stats(n + 1, l2n, dln);
     }
-    // ---- epilogue: half 0 stores dK rows, half 1 stores dV rows ----
-    if (ok) ok = wait_bar(bar(C::kBarDKVFull), 0, abort_flag, p.err);
+    }
+    // ---- an item's end: half 0 stores dK rows, half 1 stores dV rows ----
+    if (ok && n_it > 0) ok = wait_bar(bar(C::kBarDKVFull), kv & 1, abort_flag, p.err);
     tc_fence_after();
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (ok) {
+      int xx = x;
+      asm volatile("" : "+r"(xx));            // the item again, rather than kept in registers
+      const WindowBwdCta cta = window_bwd_cta(xx, p);
       // one 128-byte line (64 columns as bf16 pairs) of this thread's key row
       // at a time; after the octet transpose every store writes whole lines
       const uint32_t tsrc = tmem + lane_base + (X == 0 ? C::kColDK : C::kColDV);
-      const int wrow0 = j * kTileN + wq * 32;          // this warp's first key row
+      const int wrow0 = cta.j * kTileN + wq * 32;      // this warp's first key row
       const uint32_t valid = __ballot_sync(0xFFFFFFFFu, key < Lk);
       uint8_t* base = reinterpret_cast<uint8_t*>((X == 0 ? p.dk : p.dv) +
-                                                 (static_cast<size_t>(bh) * Lk + wrow0) * D);
+                                                 (static_cast<size_t>(cta.bh) * Lk + wrow0) * D);
       // a cut walk leaves its fp32 part [128][D] of dK and of dV in the workspace
       uint8_t* part = reinterpret_cast<uint8_t*>(
           p.part + ((static_cast<size_t>(cta.slot) * 2 + X) * kTileN + wq * 32) * D);
@@ -674,6 +718,12 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
         }
       }
     }
+    if (n_it > 0) {
+      tc_fence_before();
+      mbar_arrive(bar(C::kBarDKVEmpty));
+      ++kv;
+    }
+    }
   } else {
     regs_set<WinBwdRegs<D>::kHigh, WinBwdRegs<D>::kLaunchRegs>();
     // =================== dQ: warps 12-15, thread = query row ===================
@@ -698,10 +748,19 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     uint8_t* stage_ptr = smem + C::kStageOff;
     bool ok = true;
     int g = 0;                                    // staged rounds (CTA-wide drain)
+    int n = 0;                                    // query tiles done (over all items)
+    for (int x = static_cast<int>(blockIdx.x); x < p.n_items && ok; x += static_cast<int>(gridDim.x)) {
+    const WindowBwdCta cta = window_bwd_cta(x, p);
+    const WindowQWalk walk = window_bwd_walk(cta, p);
+    const int b = cta.bh / p.Hkv;
+    const int hq0 = (cta.bh - b * p.Hkv) * G;
     int gq, i;                                    // query head of the group, query tile
     walk.start(gq, i);
-    for (int it = 0; it < n_it && ok; walk.advance(gq, i), ++it) {
-      if (!wait_bar_relaxed(bar(C::kBarDQFull), it & 1, abort_flag, p.err)) break;
+    for (int it = 0; it < walk.n_it && ok; walk.advance(gq, i), ++it, ++n) {
+      if (!wait_bar_relaxed(bar(C::kBarDQFull), n & 1, abort_flag, p.err)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       for (int r = 0; r < kRounds; ++r, ++g) {
         uint32_t v0[32], v1[32];
@@ -761,6 +820,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
         }
         __syncwarp();                               // reconverge before the next TMEM load
       }
+    }
     }
     if (kPerWarp ? lane == 0 : qr == 0) bulk_wait_all();   // every reduction has landed
   }
@@ -949,6 +1009,7 @@ __global__ void __launch_bounds__(256) attn_bwd_window_post_kernel(const WindowB
 struct WindowBwdPlan {
   int nk, nst, seg_s, seg_w;
   long long slots, n_cta;
+  bool persistent;
   size_t part_off, bytes;
 };
 WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, const WindowMask& w) {
@@ -969,6 +1030,11 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   const long long each = std::max(8ll, (share + pl.seg_w - 1) / pl.seg_w);
   pl.seg_s = static_cast<int>(std::max(1ll, (nq * G + each - 1) / each));
   if (pl.nst == 0) pl.seg_s = 1;
+  // A CTA an SM that takes items by a fixed stride saves an item's set-up
+  // (5-8 % over walks of up to 12 tiles); over longer walks, whose lengths
+  // differ more, a CTA an item is balanced better by the hardware (equal at 17
+  // to 36 tiles, 10 % better at 68: B2 H16(4) L8192, windows of 64 to 8192).
+  pl.persistent = share <= 20ll * pl.seg_w;
   pl.n_cta = BH * (static_cast<long long>(pl.nst) * pl.seg_s + rest * pl.seg_w);
   pl.slots = BH * ((pl.seg_s > 1 ? static_cast<long long>(pl.nst) * pl.seg_s : 0) +
                    (pl.seg_w > 1 ? rest * pl.seg_w : 0));
@@ -984,7 +1050,7 @@ unsigned window_grid(long long work) {
 template <int D>
 cudaError_t launch_window_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const CUtensorMap& tdq, const WindowBwdParams& p,
-                              long long n_cta, cudaStream_t st) {
+                              long long n_cta, bool persistent, cudaStream_t st) {
   using C = WinBwdCfg<D>;
   auto kern = attn_bwd_window_kernel<D>;
   constexpr int kMaxDev = 64;
@@ -1009,7 +1075,10 @@ cudaError_t launch_window_bwd(const CUtensorMap& tq, const CUtensorMap& tk, cons
   bwd_main_events(&begin, &end);
   if (begin && (e = cudaEventRecord(begin, st)) != cudaSuccess) return e;
   if (n_cta > 0) {
-    kern<<<static_cast<unsigned>(n_cta), C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, tdo, tdq, p);
+    int sms = 0;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(persistent ? std::min<long long>(n_cta, sms) : n_cta);
+    kern<<<grid, C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, tdo, tdq, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (end && (e = cudaEventRecord(end, st)) != cudaSuccess) return e;
@@ -1094,7 +1163,8 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   p.seg_s = pl.seg_s;
   p.seg_w = pl.seg_w;
   p.head_group = B * H_kv;
+  p.n_items = static_cast<int>(pl.n_cta);
   return cuda_status("attn_bwd_window launch",
-                     d == 64 ? launch_window_bwd<64>(tq, tk, tv, tdo, tdq, p, pl.n_cta, st)
-                             : launch_window_bwd<128>(tq, tk, tv, tdo, tdq, p, pl.n_cta, st));
+                     d == 64 ? launch_window_bwd<64>(tq, tk, tv, tdo, tdq, p, pl.n_cta, pl.persistent, st)
+                             : launch_window_bwd<128>(tq, tk, tv, tdo, tdq, p, pl.n_cta, pl.persistent, st));
 }

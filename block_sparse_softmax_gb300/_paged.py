@@ -76,7 +76,7 @@ def _state(page_table, seq_lens, refs):
 
 def _rows(t: torch.Tensor, name: str, shape: Tuple[int, int, int], dev: int) -> int:
     """The row stride of a bf16 [n, heads, d] tensor whose rows are contiguous."""
-    if t.get_device() == dev and t.dtype is _BF16 and t.shape == shape:
+    if dev >= 0 and t.get_device() == dev and t.dtype is _BF16 and t.shape == shape:
         if t.is_contiguous() or shape[0] == 0:
             return shape[1] * shape[2]
         if t[0].is_contiguous():

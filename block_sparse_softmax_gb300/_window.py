@@ -15,7 +15,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _is(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
     """The address of a contiguous CUDA tensor of this type and shape on this device."""
-    if (t.get_device() != device or t.dtype is not dtype or t.shape != shape
+    if (device < 0 or t.get_device() != device or t.dtype is not dtype or t.shape != shape
             or not t.is_contiguous()):
         _need(t, name, dtype, shape)
         raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")

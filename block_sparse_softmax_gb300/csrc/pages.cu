@@ -23,6 +23,7 @@ namespace bss {
 namespace {
 
 constexpr int kMaxSeqs = 65536;      // rows of a page table (the fork kernel keeps a bit for each)
+constexpr int kMaxPages = 1 << 30;   // pages of a cache
 constexpr int kBookThreads = 1024;
 
 struct PageState {
@@ -551,9 +552,9 @@ attn_status_t page_state(PageState* st, int32_t* table, int32_t* lens, int32_t* 
   if (!table || !lens || !refs || !aligned4(table) || !aligned4(lens) || !aligned4(refs))
     return ATTN_ERR_INVALID_ARG;
   if (S < 1 || M < 1 || P < 1) return ATTN_ERR_INVALID_ARG;
-  if (S > kMaxSeqs || !valid_page_size(page)) return ATTN_ERR_UNSUPPORTED;
+  if (S > kMaxSeqs || P > kMaxPages || !valid_page_size(page)) return ATTN_ERR_UNSUPPORTED;
   *st = PageState{table, lens, refs, S, M, P, page, nullptr};
-  return status_word(&st->err);
+  return ATTN_OK;
 }
 
 attn_status_t check_cache(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int P,
@@ -583,6 +584,7 @@ attn_status_t attn_kv_reserve(int32_t* page_table, int32_t* seq_lens, int32_t* r
   attn_status_t s = page_state(&st, page_table, seq_lens, refs, S, max_pages, n_pages, page_size);
   if (s != ATTN_OK) return s;
   if (!n_new || !start || !aligned4(n_new) || !aligned4(start)) return ATTN_ERR_INVALID_ARG;
+  if ((s = status_word(&st.err)) != ATTN_OK) return s;
   kv_reserve_kernel<<<1, kBookThreads, 0, static_cast<cudaStream_t>(stream)>>>(st, n_new, start);
   return cuda_status("attn_kv_reserve launch", cudaGetLastError());
 }
@@ -650,6 +652,7 @@ attn_status_t attn_kv_fork(int32_t* page_table, int32_t* seq_lens, int32_t* refs
   const void* ptrs[] = {parents, children, copy_src, copy_dst};
   for (const void* x : ptrs)
     if (!x || !aligned4(x)) return ATTN_ERR_INVALID_ARG;
+  if ((s = status_word(&st.err)) != ATTN_OK) return s;
   kv_fork_kernel<<<1, kBookThreads, (S + 31) / 32 * 4, static_cast<cudaStream_t>(stream)>>>(
       st, parents, children, n_forks, copy_src, copy_dst);
   return cuda_status("attn_kv_fork launch", cudaGetLastError());
@@ -664,6 +667,7 @@ attn_status_t attn_kv_free(int32_t* page_table, int32_t* seq_lens, int32_t* refs
   if (n_seqs < 0) return ATTN_ERR_INVALID_ARG;
   if (n_seqs == 0) return ATTN_OK;
   if (!seqs || !aligned4(seqs)) return ATTN_ERR_INVALID_ARG;
+  if ((s = status_word(&st.err)) != ATTN_OK) return s;
   kv_free_kernel<<<grid_256(static_cast<long long>(n_seqs) * max_pages), 256, 0,
                    static_cast<cudaStream_t>(stream)>>>(st, seqs, n_seqs);
   return cuda_status("attn_kv_free launch", cudaGetLastError());
@@ -678,6 +682,7 @@ attn_status_t attn_kv_evict(int32_t* page_table, const int32_t* seq_lens, int32_
   if (s != ATTN_OK) return s;
   if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
   constexpr int64_t kMost = int64_t(1) << 60;
+  if ((s = status_word(&st.err)) != ATTN_OK) return s;
   kv_evict_kernel<<<grid_256(static_cast<long long>(S) * max_pages), 256, 0,
                     static_cast<cudaStream_t>(stream)>>>(st, window < kMost ? window : kMost, sinks);
   return cuda_status("attn_kv_evict launch", cudaGetLastError());
@@ -690,7 +695,7 @@ attn_status_t attn_kv_compact(int32_t* page_table, int32_t* refs, int32_t* copy_
   for (const void* x : ptrs)
     if (!x || !aligned4(x)) return ATTN_ERR_INVALID_ARG;
   if (S < 1 || max_pages < 1 || n_pages < 1) return ATTN_ERR_INVALID_ARG;
-  if (S > kMaxSeqs) return ATTN_ERR_UNSUPPORTED;
+  if (S > kMaxSeqs || n_pages > kMaxPages) return ATTN_ERR_UNSUPPORTED;
   int* err = nullptr;
   attn_status_t s = status_word(&err);
   if (s != ATTN_OK) return s;

@@ -1113,7 +1113,7 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   if (!window_mask(&p.w, Lk, window, sinks, q_offset, k_offset)) return ATTN_ERR_INVALID_ARG;
   const WindowBwdPlan pl = window_bwd_plan(B, H, H_kv, Lq, Lk, d, p.w);
   if (workspace_bytes < pl.bytes) return ATTN_ERR_WORKSPACE;
-  if (pl.n_cta > 0x7FFFFFFFll || pl.slots > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  if (pl.n_cta > 0x7FFF0000ll || pl.slots > 0x7FFF0000ll) return ATTN_ERR_UNSUPPORTED;
   // empty tensors may have no address
   const void* of_keys[] = {k, v, dk, dv};
   for (const void* ptr : of_keys)

@@ -711,7 +711,9 @@ extern "C" attn_status_t attn_fwd_window(const void* q, const void* k, const voi
   p.scale_log2 = scale * kLog2e;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.n_items = B * H * ((Lq + kTileM - 1) / kTileM);   // checked by check_common
+  const long long items = static_cast<long long>(B) * H * ((static_cast<long long>(Lq) + kTileM - 1) / kTileM);
+  if (items > 0x7FFF0000ll) return ATTN_ERR_UNSUPPORTED;   // counted in an int, a grid's stride past the last
+  p.n_items = static_cast<int>(items);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_status("attn_fwd_window launch", d == 64 ? launch_window_fwd<64>(tq, tk, tv, p, st)
                                                        : launch_window_fwd<128>(tq, tk, tv, p, st));

@@ -394,7 +394,7 @@ attn_status_t attn_bwd_window(const void* q, const void* k, const void* v, const
  *   - page_table [S][max_pages] int32: entry m of row s is the page of tokens
  *     m * page_size .. of sequence s, -1 where it holds none.  seq_lens [S]
  *     int32: tokens.  refs [n_pages] int32: table entries holding the page
- *     (0: free).  S <= 65536.  A fresh cache has every entry -1, every length
+ *     (0: free).  S <= 65536, n_pages <= 2^30.  A fresh cache has every entry -1, every length
  *     and every count 0.
  *   - The attn_kv_ calls keep these consistent: a page that is not full is
  *     held once, pages are taken from the lowest free index up, in order of

@@ -339,3 +339,215 @@ def test_serving_run(bss):
                 assert ((whole[0, :, -1].double() - O[0, :, 0]).abs() <= bo[0, :, 0]).all()
     held = sum(len({int(x) for x in table[s] if x >= 0}) for s in seqs)
     assert held <= 5 * (-(-window // page) + 2)        # memory stays bounded by window and sinks
+
+
+def test_decode_leaves_out_bad_pages(bss):
+    """A page out of range and a length past the table are reported, and nothing is read there."""
+    lens = [100, 40, 64]
+    c = Cache(lens, 2, 64, 16, 21)
+    q = torch.randn(3, 4, 64, device="cuda").bfloat16()
+    good, _ = bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens)
+    assert bss.attn_poll_status() == 0
+    c.table[0, 2] = c.k.shape[0] + 5                 # tokens 32 .. 47 of sequence 0
+    o, lse = bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens)
+    assert bss.attn_poll_status() == bss.ERR_BAD_PAGES
+    assert torch.equal(o[1:], good[1:])
+    mask = torch.ones(1, 100, dtype=torch.bool, device="cuda")
+    mask[:, 32:48] = False
+    args = q[0].reshape(1, 4, 1, 64), c.k64[0][None], c.v64[0][None], mask, 0.125
+    assert ((o[0].double() - ref.forward(*args)[0][0, :, 0]).abs() <= ref.forward_bounds(*args)[0][0, :, 0]).all()
+    c.table[0, 2] = -7
+    bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens)
+    assert bss.attn_poll_status() == bss.ERR_BAD_PAGES
+    c = Cache(lens, 2, 64, 16, 21)
+    c.lens[1] = 10 ** 6
+    o, _ = bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens)
+    assert bss.attn_poll_status() == bss.ERR_BAD_PAGES
+    assert torch.equal(o[0], good[0]) and torch.equal(o[2], good[2])
+    c.lens[1] = -3
+    o, lse = bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens)
+    assert bss.attn_poll_status() == bss.ERR_BAD_PAGES
+    assert torch.all(o[1] == 0) and torch.all(torch.isneginf(lse[1]))
+
+
+def test_decode_of_the_most_sequences(bss):
+    """65536 rows, one in nine with tokens; the answer of each is its own."""
+    S = 65536
+    lens = torch.zeros(S, dtype=torch.int32)
+    lens[::9] = torch.arange(len(range(0, S, 9)), dtype=torch.int32) % 40
+    held = (lens + 15) // 16
+    table = torch.full((S, 3), -1, dtype=torch.int32)
+    at = 0
+    base = torch.cumsum(held, 0) - held
+    for m in range(3):
+        table[:, m] = torch.where(held > m, base + m, -1)
+    at = int(held.sum())
+    k, v = (torch.randn(at, 1, 16, 64, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(S, 1, 64, device="cuda").bfloat16()
+    o, lse = bss.attn_decode_paged(q, k, v, table.cuda(), lens.cuda())
+    assert bss.attn_poll_status() == 0
+    empty = lens.cuda() == 0
+    assert torch.all(o[empty] == 0) and torch.all(torch.isneginf(lse[empty]))
+    for s in list(range(0, 900, 9)) + [S - 7, S // 2 // 9 * 9]:
+        n = int(lens[s])
+        if n == 0:
+            continue
+        kk, vv = (x[table[s, :int(held[s])].long().cuda()].transpose(0, 1).reshape(1, -1, 64)[:, :n] for x in (k, v))
+        mask = torch.ones(1, n, dtype=torch.bool, device="cuda")
+        args = q[s].reshape(1, 1, 1, 64), kk[None], vv[None], mask, 0.125
+        assert ((o[s].double() - ref.forward(*args)[0][0, :, 0]).abs() <= ref.forward_bounds(*args)[0][0, :, 0]).all(), s
+
+
+def test_decode_with_far_pages(bss):
+    """Offsets past 32 bits: a cache of over 2^32 elements whose last pages are in use."""
+    page, Hkv, d = 1024, 8, 128
+    P = (1 << 32) // (page * Hkv * d) + 3
+    k = torch.empty(P, Hkv, page, d, device="cuda", dtype=torch.bfloat16)
+    v = torch.empty_like(k)
+    last = [P - 1, 0, P - 2]
+    for t in (k, v):
+        t[last] = torch.randn(3, Hkv, page, d, device="cuda").bfloat16()
+    table, lens = ints([[P - 1, 0, P - 2]]), ints([2900])
+    q = torch.randn(1, 8, d, device="cuda").bfloat16()
+    o, _ = bss.attn_decode_paged(q, k, v, table, lens)
+    bss.attn_kv_copy_pages(k, v, ints([P - 1]), ints([P - 3]))
+    new = torch.randn(1, Hkv, d, device="cuda").bfloat16()
+    bss.attn_kv_write(new, new, k, v, table, ints([2900]), ints([0, 1]))
+    assert bss.attn_poll_status() == 0
+    assert torch.equal(k[P - 3], k[P - 1]) and torch.equal(v[P - 3], v[P - 1])
+    assert torch.equal(k[P - 2, :, 2900 - 2048], new[0])
+    kk, vv = (t[last].transpose(0, 1).reshape(Hkv, -1, d)[:, :2900][None] for t in (k, v))
+    mask = torch.ones(1, 2900, dtype=torch.bool, device="cuda")
+    kk = kk.clone()
+    args = q.reshape(1, 8, 1, d), kk, vv, mask, d ** -0.5
+    assert ((o[0].double() - ref.forward(*args)[0][0, :, 0]).abs() <= ref.forward_bounds(*args)[0][0, :, 0]).all()
+
+
+def test_refused_bookkeeping_changes_nothing(bss):
+    h = random_pages(random.Random(3), 6, 5, 40, 16, steps=4)
+    h.free([5])
+    h.free([4])
+    t, n, r = on_gpu(h)
+    full = [s for s in range(4) if h.lens[s]][0]
+    cases = [
+        lambda: bss.attn_kv_reserve(t, n, r, ints([0, -1, 0, 0, 0, 0]), 16),
+        lambda: bss.attn_kv_reserve(t, n, r, ints([10 ** 9, 0, 0, 0, 0, 0]), 16),
+        lambda: bss.attn_kv_reserve(t, n, r, ints([81, 0, 0, 0, 0, 0]), 16),           # past max_pages
+        lambda: bss.attn_kv_fork(t, n, r, ints([full, full]), ints([5, 5]), 16)[0],    # a child twice
+        lambda: bss.attn_kv_fork(t, n, r, ints([full]), ints([full]), 16)[0],
+        lambda: bss.attn_kv_fork(t, n, r, ints([5]), ints([5]), 16)[0],                # its own parent
+        lambda: bss.attn_kv_fork(t, n, r, ints([full, 4]), ints([4, 5]), 16)[0],       # a child as parent
+        lambda: bss.attn_kv_fork(t, n, r, ints([9]), ints([5]), 16)[0],
+        lambda: bss.attn_kv_fork(t, n, r, ints([full]), ints([-1]), 16)[0],
+    ]
+    for i, call in enumerate(cases):
+        got = call()
+        assert bss.attn_poll_status() == bss.ERR_BAD_PAGES, i
+        assert torch.all(got == -1), i
+        same(h, t, n, r)
+    # too few pages
+    small = Pages(3, 8, 4, 16)
+    t, n, r = on_gpu(small)
+    assert torch.all(bss.attn_kv_reserve(t, n, r, ints([40, 20, 1]), 16) == -1)
+    assert bss.attn_poll_status() == bss.ERR_NO_PAGES
+    same(small, t, n, r)
+    bss.attn_kv_free(t, n, r, ints([7, -2, 1]), 16)      # sequences that do not exist
+    assert bss.attn_poll_status() == bss.ERR_BAD_PAGES
+    same(small, t, n, r)
+    # fewer entries than rows: the others get nothing
+    assert bss.attn_kv_reserve(t, n, r, ints([17]), 16).tolist() == [0]
+    small.reserve([17, 0, 0])
+    same(small, t, n, r)
+
+
+def test_bookkeeping_of_many_pages(bss):
+    """More pages than one turn of the scan takes, and tables that a second launch rewrites."""
+    P, S, M, page = 70001, 700, 120, 16
+    g = torch.Generator().manual_seed(1)
+    held = torch.randperm(P, generator=g)[:60000]
+    table = torch.full((S * M,), -1, dtype=torch.int64)
+    table[:60000] = held
+    table = table[torch.randperm(S * M, generator=g)].reshape(S, M)
+    refs = torch.zeros(P, dtype=torch.int32)
+    refs[held] = 1
+    t, r = table.int().cuda(), refs.cuda()
+    src, dst, count = bss.attn_kv_compact(t, r)
+    assert bss.attn_poll_status() == 0
+    at = torch.arange(P)
+    want_src, want_dst = at[(refs > 0) & (at >= 60000)], at[(refs == 0) & (at < 60000)]
+    assert int(count) == len(want_src)
+    assert torch.equal(src.cpu().long()[:len(want_src)], want_src) and torch.all(src[len(want_src):] == -1)
+    assert torch.equal(dst.cpu().long()[:len(want_src)], want_dst)
+    to = at.clone()
+    to[want_src] = want_dst
+    assert torch.equal(t.cpu().long(), torch.where(table >= 0, to[table.clamp_min(0)], -1))
+    assert torch.equal(r.cpu(), (at < 60000).int())
+    # 9000 pages at once, past the list in shared memory; the lowest first
+    n = torch.zeros(S, dtype=torch.int32, device="cuda")
+    t2 = torch.full((S, M), -1, dtype=torch.int32, device="cuda")
+    r2 = (torch.arange(P) % 3 > 0).int().cuda()
+    new = torch.full((S,), 13 * page - 3, dtype=torch.int32, device="cuda")
+    start = bss.attn_kv_reserve(t2, n, r2, new, page)
+    assert bss.attn_poll_status() == 0 and torch.all(start == 0)
+    assert torch.equal(t2[:, :13].cpu().long().flatten(), 3 * torch.arange(13 * S))
+    assert torch.all(t2[:, 13:] == -1)
+
+
+def test_two_graphs_and_streams(bss):
+    """Two captured decodings that share a workspace, replayed one after the other on new contents,
+    and two eager ones at once on streams and workspaces of their own."""
+    lens = [[300, 0, 77, 1024], [64, 500, 3]]
+    caches = [Cache(l, 2, 128, 32, 31 + i) for i, l in enumerate(lens)]
+    qs = [torch.randn(len(l), 8, 128, device="cuda").bfloat16() for l in lens]
+    ws = torch.empty(bss.attn_decode_paged_workspace_bytes(4, 8, 2, 128), device="cuda", dtype=torch.uint8)
+    ws.fill_(255)
+    run = lambda i, **kw: bss.attn_decode_paged(qs[i], caches[i].k, caches[i].v, caches[i].table,  # noqa: E731
+                                                caches[i].lens, **kw)
+    for i in range(2):
+        run(i)
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(run(i, workspace=ws))
+        graphs.append(g)
+    for turn in range(3):
+        for i in (0, 1):
+            qs[i].copy_(torch.randn_like(qs[i]))
+        caches[0].lens.copy_(ints([300 - 50 * turn, 0, 77, 1024 - turn]))
+        want = [run(i) for i in range(2)]
+        for i in (1, 0, 1):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for w, x in zip(want, held):
+            assert torch.equal(w[0], x[0]) and torch.equal(w[1], x[1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append(run(i))
+        torch.cuda.synchronize()
+        for w, x in zip(want, got):
+            assert torch.equal(w[0], x[0]) and torch.equal(w[1], x[1])
+    assert bss.attn_poll_status() == 0
+
+
+def test_paged_refusals(bss):
+    c = Cache([40], 2, 64, 16, 1)
+    q = torch.randn(1, 4, 64, device="cuda").bfloat16()
+    for bad in (dict(k_cache=c.k.transpose(1, 2).contiguous().transpose(1, 2)), dict(v_cache=c.v[:-1]),
+                dict(k_cache=c.k.half()), dict(q=q.float()), dict(q=q[:, ::2]), dict(page_table=c.table.long()),
+                dict(seq_lens=c.lens.repeat(2)), dict(k_scale=torch.ones(2, device="cuda")),
+                dict(k_cache=c.k.to(E4M3), v_cache=c.v.to(E4M3))):
+        args = dict(q=q, k_cache=c.k, v_cache=c.v, page_table=c.table, seq_lens=c.lens) | bad
+        with pytest.raises(ValueError):
+            bss.attn_decode_paged(**args)
+    with pytest.raises(bss.AttnError, match="INVALID_ARG"):
+        bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens, sinks=3)
+    with pytest.raises(bss.AttnError, match="WORKSPACE"):
+        bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens, workspace=torch.empty(64, device="cuda"))
+    with pytest.raises(bss.AttnError, match="UNSUPPORTED"):
+        bss.attn_kv_reserve(c.table, c.lens, ints([0] * c.k.shape[0]), ints([1]), 24)

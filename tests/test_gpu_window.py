@@ -98,3 +98,104 @@ def test_no_key(bss, d):
     assert bss.attn_poll_status() == 0
     assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
     assert torch.all(dq == 0) and torch.all(delta == 0) and dk.numel() == dv.numel() == 0
+
+
+def test_same_bits_every_run(bss):
+    """O, LSE, dK and dV come out the same in every run; dQ is summed in fp32 in the order the key
+    tiles finish, so two runs differ by at most a rounding of the sum (2^-8) and of the terms."""
+    q, k, v, do = inputs(1, 4, 2, 1500, 1500, 128, 3, 4)
+    o, lse = bss.attn_fwd_window(q, k, v, 300, sinks=4)
+    first = bss.attn_bwd_window(q, k, v, o, lse, do, 300, sinks=4)
+    for _ in range(3):
+        o2, lse2 = bss.attn_fwd_window(q, k, v, 300, sinks=4)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        again = bss.attn_bwd_window(q, k, v, o, lse, do, 300, sinks=4)
+        assert torch.equal(first[1], again[1]) and torch.equal(first[2], again[2])
+        assert torch.equal(first[3], again[3])
+        mask = ref.window_mask(1500, 1500, 300, 4, device="cuda")
+        bound = ref.backward_bounds(q, k, v, do, mask, 128 ** -0.5)[0]
+        assert ((first[0].double() - again[0].double()).abs() <= bound).all()
+
+
+def test_two_streams_at_once(bss):
+    """Two calls at a time on streams of their own, with workspaces of their own."""
+    a = inputs(1, 8, 2, 900, 900, 64, 1)
+    b = inputs(1, 4, 4, 1200, 1200, 128, 2)
+    want = []
+    for (q, k, v, do), w in ((a, 100), (b, 333)):
+        o, lse = bss.attn_fwd_window(q, k, v, w, sinks=2)
+        want.append((o, lse) + bss.attn_bwd_window(q, k, v, o, lse, do, w, sinks=2)[1:3])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for st, (q, k, v, do), w in zip(streams, (a, b), (100, 333)):
+            with torch.cuda.stream(st):
+                o, lse = bss.attn_fwd_window(q, k, v, w, sinks=2)
+                got.append((o, lse) + bss.attn_bwd_window(q, k, v, o, lse, do, w, sinks=2)[1:3])
+        torch.cuda.synchronize()
+        for x, y in zip(want, got):
+            assert all(torch.equal(s, t) for s, t in zip(x, y))
+    assert bss.attn_poll_status() == 0
+
+
+def test_captured_and_replayed(bss):
+    """A training step captured in a graph gives, on new contents of its inputs, what the eager
+    calls give, also while eager calls on the same tensors run in between."""
+    q, k, v, do = inputs(1, 4, 2, 700, 700, 128, 4)
+    run = lambda: (lambda o, l: (o, l) + bss.attn_bwd_window(q, k, v, o, l, do, 130, sinks=3))(  # noqa: E731
+        *bss.attn_fwd_window(q, k, v, 130, sinks=3))
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for seed in (5, 6):
+        for t, new in zip((q, k, v, do), inputs(1, 4, 2, 700, 700, 128, seed)):
+            t.copy_(new)
+        eager = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in (0, 1, 3, 4, 5):                   # dQ is compared below
+            assert torch.equal(held[n], eager[n])
+        mask = ref.window_mask(700, 700, 130, 3, device="cuda")
+        off = (held[2].double() - ref.backward(q, k, v, do, mask, 128 ** -0.5)[0]).abs()
+        assert (off <= ref.backward_bounds(q, k, v, do, mask, 128 ** -0.5)[0]).all()
+    assert bss.attn_poll_status() == 0
+
+
+def test_writes_nothing_else(bss):
+    """Outputs inside larger buffers: what lies before and behind them stays."""
+    q, k, v, do = inputs(1, 2, 1, 200, 333, 64, 8)
+    bufs = {}
+
+    def inside(name, like):
+        big = torch.full((like.numel() + 512,), 7.0, device="cuda", dtype=like.dtype)
+        bufs[name] = big
+        return big[256:256 + like.numel()].view(like.shape)
+
+    lse = torch.empty(1, 2, 200, device="cuda")
+    o, l = bss.attn_fwd_window(q, k, v, 50, sinks=1, q_offset=133, out=inside("o", q), lse=inside("l", lse))
+    bss.attn_bwd_window(q, k, v, o, l, do, 50, sinks=1, q_offset=133, dq=inside("dq", q),
+                        dk=inside("dk", k), dv=inside("dv", v), delta=inside("delta", lse),
+                        workspace=inside("ws", torch.empty(bss.attn_bwd_window_workspace_bytes(
+                            1, 2, 1, 200, 333, 64, 50, 1, 133) // 4, device="cuda")))
+    torch.cuda.synchronize()
+    assert bss.attn_poll_status() == 0
+    for name, big in bufs.items():
+        assert torch.all(big[:256] == 7) and torch.all(big[-256:] == 7), name
+
+
+def test_refuses_what_it_cannot_take(bss):
+    q, k, v, do = inputs(1, 2, 1, 64, 64, 64, 9)
+    with pytest.raises(ValueError, match="contiguous"):
+        bss.attn_fwd_window(q.transpose(1, 2).contiguous().transpose(1, 2), k, v, 4)
+    with pytest.raises(ValueError, match="bfloat16"):
+        bss.attn_fwd_window(q.half(), k.half(), v.half(), 4)
+    with pytest.raises(ValueError, match="shape"):
+        bss.attn_fwd_window(q, k, v[:, :, :32], 4)
+    with pytest.raises(bss.AttnError, match="INVALID_ARG"):
+        bss.attn_fwd_window(q, k, v, 0)
+    o, lse = bss.attn_fwd_window(q, k, v, 4)
+    with pytest.raises(bss.AttnError, match="WORKSPACE"):
+        bss.attn_bwd_window(q, k, v, o, lse, do, 4, workspace=torch.empty(64, device="cuda"))

@@ -27,8 +27,11 @@
 namespace bss {
 namespace {
 
-// Rows that see at most this many keys get D from its definition (below).
-constexpr int kFewKeys = 16;
+// Which rows get D from its definition (below): those of at most kFewKeys keys
+// near the first or past the last key, and all of them where window and sinks
+// together are at most kFewWindow keys.
+constexpr int kFewKeys = 64;
+constexpr int kFewWindow = 32;
 
 struct WindowBwdParams {
   const __nv_bfloat16* q;
@@ -861,24 +864,94 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float s) {
   return fmaf(bf16hi(a.w), bf16hi(b.w), s);
 }
 
+// The rows whose D comes from its definition: below first, and from late on, as
+// far as they see at most kFewKeys keys.
+struct FewRows {
+  long long first, late;
+  __device__ __forceinline__ bool has(const RowKeys& rk, long long i) const {
+    return (i < first || i >= late) && rk.nsk + rk.nw <= kFewKeys;
+  }
+};
+FewRows window_few_rows(const WindowBwdParams& p) {
+  FewRows f;
+  const long long Lq = p.Lq;
+  if (p.w.window + p.w.snk <= kFewWindow || p.Lk <= kFewKeys) {
+    f.first = f.late = Lq;
+  } else {
+    f.first = std::max(0ll, std::min(Lq, kFewKeys - p.w.sh));
+    f.late = std::max(f.first, std::min(Lq, p.Lk - kFewKeys - 1 - p.w.sh + p.w.window));
+  }
+  return f;
+}
+
 // D_i for every row, and the fp32 dQ accumulator cleared.
 //
 // D_i = dO_i . O_i uses the saved O, rounded to bf16, so it is off by up to
 // 2^-8 |dO_i| . |O_i|.  Over many keys O averages out and that is small beside
 // the dP_ij = dO_i . V_j it is subtracted from; over a few keys it is as large
 // as dQ's own rounding, and more where one key has nearly all of the weight
-// (with 3 keys dQ came out 6.9e-3 off, with exact D 2.9e-3).  Rows that see at
-// most 16 keys therefore take the definition, D_i = sum_j P_ij dP_ij, in fp32:
-// a warp a row, two lanes a key.  They are the first rows of a sequence, or
-// all of them when window and sinks together are that few.
+// (with 3 keys dQ came out 6.9e-3 off, with exact D 2.9e-3; with 63 keys of
+// which one is a heavy sink 5.2e-3 and 3.3e-3).  Rows of few keys therefore
+// take the definition, D_i = sum_j P_ij dP_ij, in fp32: a warp a row, two lanes
+// a key, 16 keys at a time.  Rows of a wide window have few keys only near the
+// first key and past the last; under a window of up to 32 keys every row takes
+// its time (at 16384 rows of 16 heads about as long as the main kernel).
 template <int D>
-__global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBwdParams p) {
+__global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBwdParams p, const FewRows fr,
+                                                                  int few_blocks) {
   constexpr int G = D / 8;                           // threads per row, 16 bytes each
   const long long rows = static_cast<long long>(p.B) * p.H * p.Lq;
-  const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long nthreads = static_cast<long long>(gridDim.x) * blockDim.x;
+  // the first blocks take the rows of few keys, the others stream
+  const bool takes_few = static_cast<int>(blockIdx.x) < few_blocks;
+  const long long block = takes_few ? blockIdx.x : blockIdx.x - few_blocks;
+  const long long tid = block * blockDim.x + threadIdx.x;
+  const long long nthreads = static_cast<long long>(takes_few ? few_blocks : gridDim.x - few_blocks) * blockDim.x;
   const int g = static_cast<int>(threadIdx.x % G);
-  for (long long r = tid / G;; r += nthreads / G) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const long long per = fr.first + (p.Lq - fr.late);
+  const long long n = takes_few ? per * p.B * p.H : 0;
+  for (long long x = tid / 32; x < n; x += nthreads / 32) {
+    const long long bhq = x / per;
+    long long i = x - bhq * per;
+    if (i >= fr.first) i += fr.late - fr.first;
+    const RowKeys rk = window_row_keys(p, static_cast<int>(i));
+    if (!fr.has(rk, i)) continue;
+    const int nk = rk.nsk + rk.nw;
+    const long long r = bhq * p.Lq + i;
+    const int b = static_cast<int>(bhq / p.H);
+    const int h = static_cast<int>(bhq - static_cast<long long>(b) * p.H);
+    const size_t kv = (static_cast<size_t>(b) * p.Hkv + h / (p.H / p.Hkv)) * p.Lk;
+    const int half = lane & 1;
+    const uint4* qr = reinterpret_cast<const uint4*>(p.q + r * D) + half * (D / 16);
+    const uint4* dr = reinterpret_cast<const uint4*>(p.dout + r * D) + half * (D / 16);
+    const float nl2 = nk > 0 ? -(__ldg(p.lse + r) * kLog2e) : 0.f;
+    float s = 0.f;
+    for (int t0 = 0; t0 < nk; t0 += 16) {
+      const int t = t0 + (lane >> 1);
+      float sqk = 0.f, dov = 0.f;
+      if (t < nk) {
+        const int key = t < rk.nsk ? t : rk.lo + (t - rk.nsk);
+        const uint4* kr = reinterpret_cast<const uint4*>(p.k + (kv + key) * D) + half * (D / 16);
+        const uint4* vr = reinterpret_cast<const uint4*>(p.v + (kv + key) * D) + half * (D / 16);
+#pragma unroll 4
+        for (int e = 0; e < D / 16; ++e) {
+          sqk = dot8(__ldg(qr + e), __ldg(kr + e), sqk);
+          dov = dot8(__ldg(dr + e), __ldg(vr + e), dov);
+        }
+      }
+      sqk += __shfl_xor_sync(0xFFFFFFFFu, sqk, 1);
+      dov += __shfl_xor_sync(0xFFFFFFFFu, dov, 1);
+      if (t < nk) s += ex2(fmaf(sqk, p.scale_log2, nl2)) * dov;
+    }
+#pragma unroll
+    for (int off = 2; off < 32; off <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    if (lane == 0) p.delta[r] = s;
+  }
+  if (takes_few) return;
+  const long long step = nthreads / G;
+  const int step_row = static_cast<int>(step % p.Lq);
+  int row = static_cast<int>(tid / G % p.Lq);        // r % Lq, kept beside r
+  for (long long r = tid / G;; r += step) {
     const bool active = r < rows;
     if (__all_sync(0xFFFFFFFFu, !active)) break;     // every lane of the warp is done
     uint4 o = make_uint4(0u, 0u, 0u, 0u), d = o;
@@ -886,55 +959,13 @@ __global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBw
     if (active) {
       o = __ldg(reinterpret_cast<const uint4*>(p.o + r * D) + g);
       d = __ldg(reinterpret_cast<const uint4*>(p.dout + r * D) + g);
-      const RowKeys rk = window_row_keys(p, static_cast<int>(r % p.Lq));
-      few = rk.nsk + rk.nw <= kFewKeys;
+      few = (row < fr.first || row >= fr.late) && fr.has(window_row_keys(p, row), row);
     }
     float s = dot8(o, d, 0.f);
 #pragma unroll
     for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off, G);
     if (active && g == 0 && !few) p.delta[r] = s;
-  }
-  // the rows with few keys: those near the first key, those near the last one
-  // of a launch whose queries run past it, or all of them
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  const bool every = p.w.window + p.w.snk <= kFewKeys || p.Lk <= kFewKeys;
-  const long long first_end = every ? p.Lq : max(0ll, min(static_cast<long long>(p.Lq), kFewKeys - p.w.sh));
-  const long long late = every ? p.Lq
-                               : max(first_end, min(static_cast<long long>(p.Lq),
-                                                    p.Lk - kFewKeys - 1 - p.w.sh + p.w.window));
-  const long long per = first_end + (p.Lq - late);
-  const long long n = per * p.B * p.H;
-  for (long long x = tid / 32; x < n; x += nthreads / 32) {
-    const long long bhq = x / per;
-    long long i = x - bhq * per;
-    if (i >= first_end) i += late - first_end;
-    const RowKeys rk = window_row_keys(p, static_cast<int>(i));
-    const int nk = rk.nsk + rk.nw;
-    if (nk > kFewKeys) continue;
-    const long long r = bhq * p.Lq + i;
-    const int b = static_cast<int>(bhq / p.H);
-    const int h = static_cast<int>(bhq - static_cast<long long>(b) * p.H);
-    const size_t kv = (static_cast<size_t>(b) * p.Hkv + h / (p.H / p.Hkv)) * p.Lk;
-    const int t = lane >> 1, half = lane & 1;
-    float sqk = 0.f, dov = 0.f;
-    if (t < nk) {
-      const int key = t < rk.nsk ? t : rk.lo + (t - rk.nsk);
-      const uint4* qr = reinterpret_cast<const uint4*>(p.q + r * D) + half * (D / 16);
-      const uint4* dr = reinterpret_cast<const uint4*>(p.dout + r * D) + half * (D / 16);
-      const uint4* kr = reinterpret_cast<const uint4*>(p.k + (kv + key) * D) + half * (D / 16);
-      const uint4* vr = reinterpret_cast<const uint4*>(p.v + (kv + key) * D) + half * (D / 16);
-#pragma unroll 4
-      for (int e = 0; e < D / 16; ++e) {
-        sqk = dot8(__ldg(qr + e), __ldg(kr + e), sqk);
-        dov = dot8(__ldg(dr + e), __ldg(vr + e), dov);
-      }
-    }
-    sqk += __shfl_xor_sync(0xFFFFFFFFu, sqk, 1);
-    dov += __shfl_xor_sync(0xFFFFFFFFu, dov, 1);
-    float s = t < nk ? ex2(sqk * p.scale_log2 - __ldg(p.lse + r) * kLog2e) * dov : 0.f;
-#pragma unroll
-    for (int off = 2; off < 32; off <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    if (lane == 0) p.delta[r] = nk > 0 ? s : 0.f;
+    row += step_row - (row >= p.Lq - step_row ? p.Lq : 0);
   }
   float4* acc = reinterpret_cast<float4*>(p.dq_acc);
   const long long n4 = rows * D / 4;
@@ -1068,7 +1099,13 @@ cudaError_t launch_window_bwd(const CUtensorMap& tq, const CUtensorMap& tk, cons
     configured[dev] = true;
   }
   const long long rows = static_cast<long long>(p.B) * p.H * p.Lq;
-  attn_bwd_window_pre_kernel<D><<<window_grid(rows * (D / 8)), 256, 0, st>>>(p);
+  const FewRows few = window_few_rows(p);
+  const long long n_few = (few.first + p.Lq - few.late) * p.B * p.H;
+  const int few_blocks = n_few > 0 ? static_cast<int>(window_grid(n_few * 32)) : 0;
+  // (together no more than the two waves that either takes alone)
+  const int stream_blocks =
+      std::max(1, std::min(static_cast<int>(window_grid(rows * (D / 8))), std::max(152 * 8, 152 * 16 - few_blocks)));
+  attn_bwd_window_pre_kernel<D><<<stream_blocks + few_blocks, 256, 0, st>>>(p, few, few_blocks);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // optional timing of the main kernel alone (attn_bwd_time_main)
   cudaEvent_t begin, end;

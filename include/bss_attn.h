@@ -364,9 +364,10 @@ attn_status_t attn_fwd_window(const void* q, const void* k, const void* v, void*
  *   q, o, dout [B,H,Lq,d], k, v [B,H_kv,Lk,d] bf16, lse fp32 [B,H,Lq] from
  *   attn_fwd_window with the same window, sinks, offsets and scale.  Out: dq
  *   [B,H,Lq,d], dk, dv [B,H_kv,Lk,d] bf16 (dk and dv summed over the query
- *   heads of their group), delta fp32 [B,H,Lq]: dO . O, and for a query that
- *   sees at most 16 keys sum_j P_ij (dO_i . V_j), the same without O's
- *   rounding.  A query that sees no key gets dq = 0; a key that no query sees gets dk = dv = 0.
+ *   heads of their group), delta fp32 [B,H,Lq]: dO . O, and for queries of few
+ *   keys (up to 64 near the first and past the last key; all of them when
+ *   window and sinks are at most 32 keys together) sum_j P_ij (dO_i . V_j),
+ *   the same without O's rounding.  A query that sees no key gets dq = 0; a key that no query sees gets dk = dv = 0.
  *   dk and dv are the same in every run.  dq is accumulated in fp32 in the
  *   order the key tiles finish, so its last bit may differ from run to run.
  *   workspace: device, 16-byte aligned, >= attn_bwd_window_workspace_bytes

@@ -76,7 +76,8 @@ _SIGNATURES = {
                                    _C.c_void_p, _C.c_size_t, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
                                    _C.c_int, _C.c_int, _C.c_float, _C.c_int64, _C.c_int64,
                                    _C.c_int64, _C.c_int64, _C.c_void_p]),
-    "attn_decode_paged_workspace_bytes": (_C.c_size_t, [_C.c_int, _C.c_int, _C.c_int, _C.c_int]),
+    "attn_decode_paged_workspace_bytes": (_C.c_size_t, [_C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                                        _C.c_int, _C.c_int]),
     "attn_decode_paged": (_C.c_int, [_C.c_void_p, _C.c_int64, _C.c_void_p, _C.c_void_p, _C.c_int64,
                                      _C.c_int64, _C.c_int, _C.c_void_p, _C.c_void_p, _C.c_void_p,
                                      _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,

@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib, _need, _scale
-from ._window import _is, _run, _workspace
+from ._window import _is, _out, _run, _workspace
 
 KV_BF16 = 0
 KV_E4M3 = 1
@@ -86,8 +86,9 @@ def _rows(t: torch.Tensor, name: str, shape: Tuple[int, int, int], dev: int) -> 
     raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
-def attn_decode_paged_workspace_bytes(S: int, H: int, H_kv: int, d: int) -> int:
-    return int(_lib.load().attn_decode_paged_workspace_bytes(S, H, H_kv, d))
+def attn_decode_paged_workspace_bytes(S: int, H: int, H_kv: int, d: int, max_pages: int,
+                                      page_size: int) -> int:
+    return int(_lib.load().attn_decode_paged_workspace_bytes(S, H, H_kv, d, max_pages, page_size))
 
 
 def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int = 0,
@@ -111,14 +112,13 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int 
     if rows < S:
         raise ValueError(f"page_table has {rows} rows for {S} sequences")
     lp = _is(seq_lens, "seq_lens", _INT, (rows,), dev)
-    out = torch.empty((S, H, d), dtype=_BF16, device=q.device) if out is None else out
-    lse = torch.empty((S, H), dtype=_FP32, device=q.device) if lse is None else lse
+    out, op = _out(out, "out", _BF16, (S, H, d), q)
+    lse, ep = _out(lse, "lse", _FP32, (S, H), q)
     ws = _workspace(workspace, 0 if workspace is not None else attn_decode_paged_workspace_bytes(
-        S, H, Hkv, d), q)
+        S, H, Hkv, d, M, page), q)
     _run("attn_decode_paged", dev, q.data_ptr(), q_stride, kp, vp, ks, vs, code, ksp, vsp, tp, lp,
-         _is(out, "out", _BF16, (S, H, d), dev), _is(lse, "lse", _FP32, (S, H), dev), ws.data_ptr(),
-         ws.numel() * ws.element_size(), S, H, Hkv, d, M, P, page, _scale(scale, d), int(window),
-         int(sinks))
+         op, ep, ws.data_ptr(), ws.numel() * ws.element_size(), S, H, Hkv, d, M, P, page,
+         _scale(scale, d), int(window), int(sinks))
     return out, lse
 
 
@@ -132,9 +132,8 @@ def attn_kv_reserve(page_table, seq_lens, refs, n_new, page_size: int, *, start=
     np_ = _is(n_new, "n_new", _INT, (n,), dev)
     if n > S:
         raise ValueError(f"n_new has {n} entries for {S} sequences")
-    start = torch.empty_like(n_new) if start is None else start
-    _run("attn_kv_reserve", dev, tp, lp, rp, np_, _is(start, "start", _INT, (n,), dev), n, M, P,
-         int(page_size))
+    start, sp = _out(start, "start", _INT, (n,), n_new)
+    _run("attn_kv_reserve", dev, tp, lp, rp, np_, sp, n, M, P, int(page_size))
     return start
 
 
@@ -170,10 +169,9 @@ def attn_kv_fork(page_table, seq_lens, refs, parents, children, page_size: int, 
     F = parents.numel()
     pp = _is(parents, "parents", _INT, (F,), dev)
     cp = _is(children, "children", _INT, (F,), dev)
-    copy_src = torch.empty_like(parents) if copy_src is None else copy_src
-    copy_dst = torch.empty_like(parents) if copy_dst is None else copy_dst
-    _run("attn_kv_fork", dev, tp, lp, rp, pp, cp, F, _is(copy_src, "copy_src", _INT, (F,), dev),
-         _is(copy_dst, "copy_dst", _INT, (F,), dev), S, M, P, int(page_size))
+    copy_src, csp = _out(copy_src, "copy_src", _INT, (F,), parents)
+    copy_dst, cdp = _out(copy_dst, "copy_dst", _INT, (F,), parents)
+    _run("attn_kv_fork", dev, tp, lp, rp, pp, cp, F, csp, cdp, S, M, P, int(page_size))
     return copy_src, copy_dst
 
 
@@ -201,11 +199,10 @@ def attn_kv_compact(page_table, refs, *, copy_src=None, copy_dst=None, count=Non
     tp, S, M = _table(page_table, dev)
     P = refs.numel()
     rp = _is(refs, "refs", _INT, (P,), dev)
-    copy_src = torch.empty_like(refs) if copy_src is None else copy_src
-    copy_dst = torch.empty_like(refs) if copy_dst is None else copy_dst
-    count = torch.empty((1,), dtype=_INT, device=refs.device) if count is None else count
-    _run("attn_kv_compact", dev, tp, rp, _is(copy_src, "copy_src", _INT, (P,), dev),
-         _is(copy_dst, "copy_dst", _INT, (P,), dev), _is(count, "count", _INT, (1,), dev), S, M, P)
+    copy_src, csp = _out(copy_src, "copy_src", _INT, (P,), refs)
+    copy_dst, cdp = _out(copy_dst, "copy_dst", _INT, (P,), refs)
+    count, cp = _out(count, "count", _INT, (1,), refs)
+    _run("attn_kv_compact", dev, tp, rp, csp, cdp, cp, S, M, P)
     return copy_src, copy_dst, count
 
 

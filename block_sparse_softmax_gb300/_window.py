@@ -15,23 +15,36 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _is(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
     """The address of a contiguous CUDA tensor of this type and shape on this device."""
-    if (device < 0 or t.get_device() != device or t.dtype is not dtype or t.shape != shape
-            or not t.is_contiguous()):
-        _need(t, name, dtype, shape)
-        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
-    return t.data_ptr()
+    if (t.dtype is dtype and t.is_contiguous() and t.get_device() == device and t.shape == shape
+            and device >= 0):
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+
+
+_entry = {}
 
 
 def _run(name: str, device: int, *args) -> None:
     """One library call on the device's current stream; raises on a status other than OK."""
-    fn = getattr(_lib.load(), name)
-    if device == torch.cuda.current_device():
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(_lib.load(), name)
+    if device == torch._C._cuda_getDevice():
         st = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
             st = fn(*args, _raw_stream(device))
     if st != OK:
         raise AttnError(st, name)
+
+
+def _out(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, like: torch.Tensor):
+    """(tensor, address) of an output: the caller's, checked, or a new one on ``like``'s device."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _is(t, name, dtype, shape, like.get_device())
 
 
 def _workspace(workspace: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> torch.Tensor:
@@ -58,11 +71,10 @@ def attn_fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: i
     qp = _is(q, "q", bf16, q_shape, dev)
     kp = _is(k, "k", bf16, (B, Hkv, Lk, d), dev)
     vp = _is(v, "v", bf16, (B, Hkv, Lk, d), dev)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, H, Lq), dtype=fp32, device=q.device) if lse is None else lse
-    _run("attn_fwd_window", dev, qp, kp, vp, _is(out, "out", bf16, q_shape, dev),
-         _is(lse, "lse", fp32, (B, H, Lq), dev), B, H, Hkv, Lq, Lk, d, _scale(scale, d), int(window),
-         int(sinks), int(q_offset), int(k_offset))
+    out, op = _out(out, "out", bf16, q_shape, q)
+    lse, lp = _out(lse, "lse", fp32, (B, H, Lq), q)
+    _run("attn_fwd_window", dev, qp, kp, vp, op, lp, B, H, Hkv, Lq, Lk, d, _scale(scale, d),
+         int(window), int(sinks), int(q_offset), int(k_offset))
     return out, lse
 
 
@@ -89,15 +101,14 @@ def attn_bwd_window(q, k, v, o, lse, dout, window: int, *, sinks: int = 0,
     dop = _is(dout, "dout", bf16, q_shape, dev)
     kp, vp = _is(k, "k", bf16, k_shape, dev), _is(v, "v", bf16, k_shape, dev)
     lp = _is(lse, "lse", fp32, rows, dev)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    delta = torch.empty_like(lse) if delta is None else delta
+    dq, dqp = _out(dq, "dq", bf16, q_shape, q)
+    dk, dkp = _out(dk, "dk", bf16, k_shape, q)
+    dv, dvp = _out(dv, "dv", bf16, k_shape, q)
+    delta, dep = _out(delta, "delta", fp32, rows, q)
     window, sinks, q_offset, k_offset = int(window), int(sinks), int(q_offset), int(k_offset)
     ws = _workspace(workspace, 0 if workspace is not None else attn_bwd_window_workspace_bytes(
         B, H, Hkv, Lq, Lk, d, window, sinks, q_offset, k_offset), q)
-    _run("attn_bwd_window", dev, qp, kp, vp, op, lp, dop, _is(dq, "dq", bf16, q_shape, dev),
-         _is(dk, "dk", bf16, k_shape, dev), _is(dv, "dv", bf16, k_shape, dev),
-         _is(delta, "delta", fp32, rows, dev), ws.data_ptr(), ws.numel() * ws.element_size(), B, H,
-         Hkv, Lq, Lk, d, _scale(scale, d), window, sinks, q_offset, k_offset)
+    _run("attn_bwd_window", dev, qp, kp, vp, op, lp, dop, dqp, dkp, dvp, dep, ws.data_ptr(),
+         ws.numel() * ws.element_size(), B, H, Hkv, Lq, Lk, d, _scale(scale, d), window, sinks,
+         q_offset, k_offset)
     return dq, dk, dv, delta

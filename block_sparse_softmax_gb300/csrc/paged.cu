@@ -854,8 +854,14 @@ constexpr int kDecWorkers = kDecMaxCtas * kDecWarps;
 
 // query heads of a part: what a K/V head's group has, at most 16
 int decode_rows(int G) { return G <= 8 ? 8 : 16; }
-size_t decode_workspace(int d, int G) {
-  return static_cast<size_t>(kDecWorkers) * 8 + static_cast<size_t>(kDecWorkers) * 2 * decode_rows(G) * (d + 2) * 4;
+// 16-key steps that the table's rows have room for, over all units: more
+// workers than that have nothing to do (rounded up to whole CTAs)
+long long decode_workers(int S, int Hkv, int G, int max_pages, int page) {
+  const long long steps = static_cast<long long>(max_pages) * (page / 16) * S * Hkv * ((G + 15) / 16);
+  return std::min<long long>(kDecWorkers, (steps + kDecWarps - 1) / kDecWarps * kDecWarps);
+}
+size_t decode_workspace(int d, int G, long long workers) {
+  return static_cast<size_t>(workers) * 8 + static_cast<size_t>(workers) * 2 * decode_rows(G) * (d + 2) * 4;
 }
 
 // K or V pages as a 3-D tensor (d, H_kv * page_size, pages) with boxes of 16
@@ -905,7 +911,8 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
   return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D>, p);
 }
 
-bool decode_sizes(int S, int H, int Hkv, int d) {
+bool decode_sizes(int S, int H, int Hkv, int d, int max_pages, int page) {
+  if (max_pages < 1 || page < 16 || page > 1024 || (page & (page - 1))) return false;
   if (S < 1 || H < 1 || !valid_kv_heads(H, Hkv) || (d != 64 && d != 128)) return false;
   return S <= kMaxSeqs && static_cast<long long>(S) * H <= 0x7FFFFFFFll;
 }
@@ -915,8 +922,10 @@ bool decode_sizes(int S, int H, int Hkv, int d) {
 
 using namespace bss;
 
-extern "C" size_t attn_decode_paged_workspace_bytes(int S, int H, int H_kv, int d) {
-  return decode_sizes(S, H, H_kv, d) ? decode_workspace(d, H / H_kv) : 0;
+extern "C" size_t attn_decode_paged_workspace_bytes(int S, int H, int H_kv, int d, int max_pages,
+                                                    int page_size) {
+  if (!decode_sizes(S, H, H_kv, d, max_pages, page_size)) return 0;
+  return decode_workspace(d, H / H_kv, decode_workers(S, H_kv, H / H_kv, max_pages, page_size));
 }
 
 extern "C" attn_status_t attn_decode_paged(
@@ -947,7 +956,8 @@ extern "C" attn_status_t attn_decode_paged(
   if (k_page_stride < least || v_page_stride < least || k_page_stride % unit || v_page_stride % unit)
     return ATTN_ERR_INVALID_ARG;
   if (q_stride < static_cast<int64_t>(H) * d || q_stride % 8) return ATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < decode_workspace(d, H / H_kv)) return ATTN_ERR_WORKSPACE;
+  const long long workers = decode_workers(S, H_kv, H / H_kv, max_pages, page_size);
+  if (workspace_bytes < decode_workspace(d, H / H_kv, workers)) return ATTN_ERR_WORKSPACE;
   DecodeParams p{};
   if ((s = status_word(&p.err)) != ATTN_OK) return s;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -963,7 +973,7 @@ extern "C" attn_status_t attn_decode_paged(
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.meta = static_cast<int2*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + static_cast<size_t>(kDecWorkers) * 8);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + static_cast<size_t>(workers) * 8);
   p.rows = decode_rows(H / H_kv);
   p.S = S;
   p.H = H;

@@ -499,7 +499,8 @@ def test_two_graphs_and_streams(bss):
     lens = [[300, 0, 77, 1024], [64, 500, 3]]
     caches = [Cache(l, 2, 128, 32, 31 + i) for i, l in enumerate(lens)]
     qs = [torch.randn(len(l), 8, 128, device="cuda").bfloat16() for l in lens]
-    ws = torch.empty(bss.attn_decode_paged_workspace_bytes(4, 8, 2, 128), device="cuda", dtype=torch.uint8)
+    ws = torch.empty(max(bss.attn_decode_paged_workspace_bytes(len(l), 8, 2, 128, c.table.shape[1], 32)
+                         for l, c in zip(lens, caches)), device="cuda", dtype=torch.uint8)
     ws.fill_(255)
     run = lambda i, **kw: bss.attn_decode_paged(qs[i], caches[i].k, caches[i].v, caches[i].table,  # noqa: E731
                                                 caches[i].lens, **kw)

@@ -54,11 +54,14 @@ def test_window_backward(lib):
 
 
 def test_decode(lib):
-    full = lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128)
+    full = lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 4, 16)
     assert full > 0
-    assert lib.attn_decode_paged_workspace_bytes(3, 8, 3, 128) == 0
-    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 96) == 0
-    assert lib.attn_decode_paged_workspace_bytes(0, 8, 2, 128) == 0
+    assert lib.attn_decode_paged_workspace_bytes(3, 8, 3, 128, 4, 16) == 0
+    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 96, 4, 16) == 0
+    assert lib.attn_decode_paged_workspace_bytes(0, 8, 2, 128, 4, 16) == 0
+    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 4, 24) == 0
+    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 0, 16) == 0
+    assert lib.attn_decode_paged_workspace_bytes(9000, 8, 2, 128, 400, 16) <= 16e6
 
     def call(q=P, qs=8 * 128, ks=2 * 16 * 128, vs=2 * 16 * 128, kind=0, kscale=None, vscale=None,
              table=P, ws=P, nbytes=full, S=3, H=8, Hkv=2, d=128, M=4, n=20, page=16, scale=0.1, window=0,

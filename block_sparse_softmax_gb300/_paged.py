@@ -114,11 +114,14 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int 
     lp = _is(seq_lens, "seq_lens", _INT, (rows,), dev)
     out, op = _out(out, "out", _BF16, (S, H, d), q)
     lse, ep = _out(lse, "lse", _FP32, (S, H), q)
-    ws = _workspace(workspace, 0 if workspace is not None else attn_decode_paged_workspace_bytes(
-        S, H, Hkv, d, M, page), q)
+    wp, nbytes = None, 0
+    if workspace is None:
+        nbytes = attn_decode_paged_workspace_bytes(S, H, Hkv, d, M, page)
+    if workspace is not None or nbytes:       # small calls need none
+        workspace = _workspace(workspace, nbytes, q)
+        wp, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _run("attn_decode_paged", dev, q.data_ptr(), q_stride, kp, vp, ks, vs, code, ksp, vsp, tp, lp,
-         op, ep, ws.data_ptr(), ws.numel() * ws.element_size(), S, H, Hkv, d, M, P, page,
-         _scale(scale, d), int(window), int(sinks))
+         op, ep, wp, nbytes, S, H, Hkv, d, M, P, page, _scale(scale, d), int(window), int(sinks))
     return out, lse
 
 

@@ -10,33 +10,47 @@
 //
 // What bounds it: every key and value is read once and used for the few query
 // heads of its group, so HBM bandwidth.  Hence:
-//   * The work is cut evenly, whatever the lengths: all tiles of 64 keys of
-//     every (sequence, K/V head, group of 16 query heads) form one line, and
-//     each of the resident CTAs takes an equal stretch of it.  A stretch that
-//     covers a whole unit writes its output; the (at most two) units a CTA
-//     has only a part of leave their state in the workspace, two slots a CTA,
-//     and a second kernel joins them in order.
-//   * A warp works by itself on 16 or 32 keys at a time.  TMA brings their K
-//     and V rows (boxes of 16 rows of a page) into the warp's own ring of
-//     stages, swizzled for ldmatrix: one lane's four to eight instructions a
-//     step.  (With cp.async, 16 bytes a lane and copy, the e4m3 kernel spent
-//     most of its issue slots on addresses: 169 us on 128 ragged sequences of
-//     up to 16384 tokens, MEASURED now.)  Only a step with keys that are not
-//     seen (a sequence's end, a window's edge) is copied row by row with
-//     cp.async, which leaves those rows out and fills in zeros.  The next
-//     unit's first stages are on their way before this unit's states merge.
+//   * The work is cut evenly, whatever the lengths: the steps (16 or 32 keys)
+//     of every unit (sequence, K/V head, group of up to 16 query heads) form
+//     one line, and every resident warp takes an equal stretch of it.  A unit
+//     that lies whole in a stretch is written out; the (at most two) units a
+//     warp has only a part of leave their state in the workspace, two slots a
+//     warp, and a second kernel, launched programmatically so that it is set
+//     up beside the first, joins them in order.  The warps of a CTA share
+//     nothing: when they took a unit's tiles in turn and merged at its end,
+//     each end cost its CTA 4 us (32 sequences of up to 8192 tokens: the CTAs
+//     were done after 28 to 44 us, the warps are after 31 to 40).  Where every
+//     unit is short, a CTA a unit in one launch does instead (decode_small).
+//   * TMA brings a step's K and V rows (boxes of 16 rows of a page) into the
+//     warp's own ring of stages, swizzled for ldmatrix: one lane's four to
+//     eight instructions a step.  Only a step with keys that are not seen (a
+//     sequence's end, a window's edge) is copied row by row with cp.async,
+//     which leaves those rows out and fills in zeros.  The next unit's first
+//     steps and its Q are on their way before this unit's state goes out.
 //   * The products run transposed on mma.m16n8k16: S^T = K Q^T has 16 keys as
 //     rows and 8 query heads as columns, A^T = V^T P^T has 16 columns of d as
 //     rows.  A group of up to 8 query heads then costs one tile of N = 8, the
 //     16-row side is always full, and a thread's accumulators belong to the
-//     same two heads as its softmax state.
+//     same two heads as its softmax state.  (tcgen05 tiles have at least 64
+//     rows and would be fed through shared memory twice; these products take a
+//     tenth of the time the bytes do.)
 //   * e4m3 pages are read as they are (half the bytes); a pair of elements
-//     becomes fp16 by one conversion, exactly, on the way into an fp16 MMA
-//     (going on to bf16 takes four instructions).  So that Q and P lose
-//     nothing there that bf16 holds, a head's Q is scaled by a power of two
-//     (largest element in [128, 256)) and P by 2^12: an fp16 step is then at
-//     most 2^-33 of Q's largest element, 2^-37 of P's.  The caches' scales
-//     multiply the score and the output.
+//     becomes fp16 by one conversion, exactly, on the way into an fp16 MMA.
+//     (Going on to bf16 takes four instructions: 128 sequences of up to 16384
+//     tokens took 174 us that way, 148 so.)  So that Q and P lose nothing
+//     there that bf16 holds, a head's Q is scaled by a power of two (largest
+//     element in [128, 256)) and P by 2^12: fp16 then rounds by at most 2^-32
+//     of Q's largest element, 2^-37 of P's.  The caches' scales multiply the
+//     score and the output.
+// Measured (GPU time, d=128, 4 K/V heads of 4 query heads where not said):
+//   2 sequences of 131071 tokens, 8 heads    159 us, 6.7 TB/s (99 % of a copy's)
+//   128 of up to 16384 tokens, e4m3          148 us, 6.2 TB/s (92 %)
+//   32 of up to 8192 tokens                   50 us, 4.7 TB/s (69 %)
+//   64 of up to 16384 tokens, window 1000,
+//     4 sinks, d=64, 16 heads                 46 us, 4.7 TB/s (70 %)
+// What the last two lose is about 6 us until the first keys land (lengths,
+// table and data, one after the other), 4 us between the first and the last
+// warp's end, 5 us for the join and 4 us for the two launches.
 #include <algorithm>
 
 #include "host.cuh"
@@ -209,6 +223,64 @@ struct DecState {
   float m[NT][2], l[NT][2];
 };
 
+// The warps' states of one unit become its output, by way of `merge` in shared
+// memory (the rings, which every warp is done with).
+template <int D, bool FP8, int NT>
+__device__ __forceinline__ void decode_merge(const DecodeParams& p, const DecState<D, NT>& a, float* merge, int s,
+                                             int h0, int nh, int hkv, int warp, int lane) {
+  constexpr int kRow = D + 4;                       // A | m, l; padded against bank conflicts
+  static_assert(kDecWarps * 8 * NT * kRow * 4 <= DecCfg<D, FP8, NT>::kRing, "the states fit the rings");
+  const int g = lane >> 2, c2 = (lane & 3) * 2;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  __syncthreads();
+#pragma unroll
+  for (int n8 = 0; n8 < NT; ++n8) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float l = a.l[n8][u];
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+      float* mr = merge + ((warp * NT + n8) * 8 + c2 + u) * kRow;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        mr[16 * i + (FP8 ? 2 * g : g)] = a.acc[n8][i][u];
+        mr[16 * i + (FP8 ? 2 * g + 1 : g + 8)] = a.acc[n8][i][2 + u];
+      }
+      if (g == 0) {
+        mr[D] = FP8 ? a.m[n8][u] - 12.f : a.m[n8][u];   // l carries P's 2^12
+        mr[D + 1] = l;
+      }
+    }
+  }
+  __syncthreads();
+  const float vs = FP8 ? __ldg(p.v_scale + hkv) : 1.f;
+  for (int e = warp * 32 + lane; e < nh * (D / 2); e += kDecThreads) {
+    const int hh = e / (D / 2);
+    const int d2 = (e - hh * (D / 2)) * 2;
+    const float* mr = merge + hh * kRow;
+    constexpr int kWarp = NT * 8 * kRow;
+    float m = NEG_INF;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w)
+      if (mr[w * kWarp + D + 1] != 0.f) m = fmaxf(m, mr[w * kWarp + D]);
+    float l = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float* x = mr + w * kWarp;
+      if (x[D + 1] == 0.f) continue;                // this warp saw no key
+      const float f = ex2(x[D] - m);
+      l = fmaf(f, x[D + 1], l);
+      y0 = fmaf(f, x[d2], y0);
+      y1 = fmaf(f, x[d2 + 1], y1);
+    }
+    const float inv = l == 0.f ? 0.f : vs / l;
+    const size_t oh = static_cast<size_t>(s) * p.H + h0 + hh;
+    *reinterpret_cast<uint32_t*>(p.o + oh * D + d2) = pack_bf16(y0 * inv, y1 * inv);
+    if (d2 == 0) p.lse[oh] = l == 0.f ? NEG_INF : (m + __log2f(l)) * kLn2;
+  }
+}
+
 // A warp's part of unit (s, r): steps [ta, tb) of the unit's st.total; x0 steps
 // of the line lie before the unit.
 template <int KEYS>
@@ -218,7 +290,9 @@ struct DecUnit {
   SeqSteps<KEYS> st;
 };
 
-template <int D, bool FP8, int NT>
+// SMALL: a CTA a unit, whose steps its warps share and whose states they join in
+// shared memory; no line, no parts.
+template <int D, bool FP8, int NT, bool SMALL>
 __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     attn_decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                              const DecodeParams p) {
@@ -235,14 +309,14 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
   const int units = p.Hkv * p.q_tiles;              // units of a sequence
   const int cta = static_cast<int>(blockIdx.x);
   const int n_cta = static_cast<int>(gridDim.x);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may line up
+  if (!SMALL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may line up
 
   const uint32_t bars = smem_u32(dec_smem) + C::kBarOff + warp * C::kStages * 8;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(dec_smem + C::kAbortOff);
   if (smem_u32(dec_smem) & 1023u) {                 // the swizzle needs it: report, touch nothing
     if (tid == 0) {
       record_error(p.err, ATTN_ERR_UNSUPPORTED);
-      for (int w = 0; w < kDecWarps; ++w) p.meta[cta * kDecWarps + w] = make_int2(-1, -1);
+      for (int w = 0; w < kDecWarps && !SMALL; ++w) p.meta[cta * kDecWarps + w] = make_int2(-1, -1);
     }
     return;
   }
@@ -252,83 +326,99 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     fence_barrier_init();
   }
 
-  // ---- this warp's stretch [x0, x1) of the line of all steps ----
-  long long all = 0;
-  for (int s = tid; s < p.S; s += kDecThreads) all += seq_steps<KEYS>(__ldg(p.lens + s), p).total;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-  if (lane == 0) sums[warp] = all;
-  __syncthreads();
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) all += sums[w];
-  const long long steps = all * units;
+  DecUnit<KEYS> un;
+  int2 meta = make_int2(-1, -1);
   const int worker = cta * kDecWarps + warp;
-  const int active = static_cast<int>(min(static_cast<long long>(n_cta) * kDecWarps, steps));
-  if (tid <= kDecWarps) {
-    const int w = cta * kDecWarps + tid;
-    edge[tid] = w < active ? steps * w / active : steps;
-  }
-  __syncthreads();
-  const long long x0 = edge[warp], x1 = edge[warp + 1];
-  // sequences that see no key, and lengths out of range
-  for (int s = cta; s < p.S; s += n_cta) {
-    const int n = __ldg(p.lens + s);
-    if (tid == 0 && (n < 0 || n > (static_cast<long long>(p.M) << p.page_log2)))
+  long long steps = 0, x1 = 0;                      // the line's steps, and this warp's last one + 1
+  int active = 0;                                   // warps with a stretch of it
+  if constexpr (SMALL) {
+    un.s = cta / units;
+    un.r = cta - un.s * units;
+    const int n = __ldg(p.lens + un.s);
+    if (tid == 0 && un.r == 0 && (n < 0 || n > (static_cast<long long>(p.M) << p.page_log2)))
       record_error(p.err, ATTN_ERR_BAD_PAGES);
-    if (seq_steps<KEYS>(n, p).total > 0) continue;
-    for (int e = tid; e < p.H * D; e += kDecThreads)
-      p.o[static_cast<size_t>(s) * p.H * D + e] = __float2bfloat16(0.f);
-    for (int h = tid; h < p.H; h += kDecThreads) p.lse[static_cast<size_t>(s) * p.H + h] = NEG_INF;
-  }
-  // the sequences that hold its warps' first steps, and the steps before them
-  if (cta * kDecWarps < active) {
-    long long last_x0 = edge[0];
-    for (int w = 1; w < kDecWarps; ++w)
-      if (cta * kDecWarps + w < active) last_x0 = edge[w];
-    long long base = 0;
-    for (int s0 = 0;; s0 += kDecThreads) {
-      const int s = s0 + tid;
-      const long long t = s < p.S ? static_cast<long long>(seq_steps<KEYS>(__ldg(p.lens + s), p).total) * units : 0;
-      long long x = t;
+    un.st = seq_steps<KEYS>(n, p);
+    un.x0 = 0;
+    un.ta = un.st.total * warp / kDecWarps;
+    un.tb = un.st.total * (warp + 1) / kDecWarps;
+    __syncthreads();                                // the abort flag
+  } else {
+    // ---- this warp's stretch [x0, x1) of the line of all steps ----
+    long long all = 0;
+    for (int s = tid; s < p.S; s += kDecThreads) all += seq_steps<KEYS>(__ldg(p.lens + s), p).total;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) sums[warp] = x;
-      __syncthreads();
-      long long before = base + x - t;
-      for (int w = 0; w < warp; ++w) before += sums[w];
-      for (int w = 0; w < kDecWarps; ++w) {
-        const long long xw = edge[w];
-        if (xw >= before && xw < before + t) {
-          found[2 * w] = s;
-          found[2 * w + 1] = before;
-        }
-      }
-      for (int w = 0; w < kDecWarps; ++w) base += sums[w];
-      if (last_x0 < base) break;
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    if (lane == 0) sums[warp] = all;
+    __syncthreads();
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) all += sums[w];
+    steps = all * units;
+    active = static_cast<int>(min(static_cast<long long>(n_cta) * kDecWarps, steps));
+    if (tid <= kDecWarps) {
+      const int w = cta * kDecWarps + tid;
+      edge[tid] = w < active ? steps * w / active : steps;
     }
     __syncthreads();
+    const long long x0 = edge[warp];
+    x1 = edge[warp + 1];
+    // sequences that see no key, and lengths out of range
+    for (int s = cta; s < p.S; s += n_cta) {
+      const int n = __ldg(p.lens + s);
+      if (tid == 0 && (n < 0 || n > (static_cast<long long>(p.M) << p.page_log2)))
+        record_error(p.err, ATTN_ERR_BAD_PAGES);
+      if (seq_steps<KEYS>(n, p).total > 0) continue;
+      for (int e = tid; e < p.H * D; e += kDecThreads)
+        p.o[static_cast<size_t>(s) * p.H * D + e] = __float2bfloat16(0.f);
+      for (int h = tid; h < p.H; h += kDecThreads) p.lse[static_cast<size_t>(s) * p.H + h] = NEG_INF;
+    }
+    // the sequences that hold its warps' first steps, and the steps before them
+    if (cta * kDecWarps < active) {
+      long long last_x0 = edge[0];
+      for (int w = 1; w < kDecWarps; ++w)
+        if (cta * kDecWarps + w < active) last_x0 = edge[w];
+      long long base = 0;
+      for (int s0 = 0;; s0 += kDecThreads) {
+        const int s = s0 + tid;
+        const long long t = s < p.S ? static_cast<long long>(seq_steps<KEYS>(__ldg(p.lens + s), p).total) * units : 0;
+        long long x = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+          if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = x;
+        __syncthreads();
+        long long before = base + x - t;
+        for (int w = 0; w < warp; ++w) before += sums[w];
+        for (int w = 0; w < kDecWarps; ++w) {
+          const long long xw = edge[w];
+          if (xw >= before && xw < before + t) {
+            found[2 * w] = s;
+            found[2 * w + 1] = before;
+          }
+        }
+        for (int w = 0; w < kDecWarps; ++w) base += sums[w];
+        if (last_x0 < base) break;
+      }
+      __syncthreads();
+    }
+    // from here on the warps go their own ways
+    if (x0 >= x1) {
+      if (lane == 0) p.meta[worker] = meta;
+      return;
+    }
+    un.s = static_cast<int>(found[2 * warp]);
+    un.st = seq_steps<KEYS>(__ldg(p.lens + un.s), p);
+    {
+      const long long before = found[2 * warp + 1];
+      un.r = static_cast<int>((x0 - before) / un.st.total);
+      un.x0 = before + static_cast<long long>(un.r) * un.st.total;
+    }
+    un.ta = static_cast<int>(x0 - un.x0);
+    un.tb = static_cast<int>(min(static_cast<long long>(un.st.total), x1 - un.x0));
   }
-  // from here on the warps go their own ways
-  int2 meta = make_int2(-1, -1);
-  if (x0 >= x1) {
-    if (lane == 0) p.meta[worker] = meta;
-    return;
-  }
-  DecUnit<KEYS> un;
-  un.s = static_cast<int>(found[2 * warp]);
-  un.st = seq_steps<KEYS>(__ldg(p.lens + un.s), p);
-  {
-    const long long before = found[2 * warp + 1];
-    un.r = static_cast<int>((x0 - before) / un.st.total);
-    un.x0 = before + static_cast<long long>(un.r) * un.st.total;
-  }
-  un.ta = static_cast<int>(x0 - un.x0);
-  un.tb = static_cast<int>(min(static_cast<long long>(un.st.total), x1 - un.x0));
 
   uint8_t* ring = dec_smem + warp * C::kStages * C::kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
@@ -410,7 +500,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
   // The unit after u in this warp's stretch; false at its end.
   auto next_unit = [&](DecUnit<KEYS>& u) -> bool {
     const long long x = u.x0 + u.tb;
-    if (u.tb != u.st.total || x >= x1) return false;
+    if (SMALL || u.tb != u.st.total || x >= x1) return false;
     u.x0 = x;
     if (++u.r == units) {
       u.r = 0;
@@ -655,7 +745,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
         if (by_tma >> i & 1u) drain_bar(bars + 8 * i, (phases >> i) & 1);
       cp_wait<0>();
       meta = make_int2(-1, -1);
-      break;
+      if (!SMALL) break;
     }
     // the next unit's first steps and its Q, on their way while this one's
     // state goes out
@@ -665,6 +755,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
       load_q(un);
     }
 
+    if constexpr (SMALL) {
+      decode_merge<D, FP8, NT>(p, a, reinterpret_cast<float*>(dec_smem), s, h0, nh, hkv, warp, lane);
+      return;
+    }
     // ---- the state: the output of a unit that is whole, else a part ----
     const bool whole = ta == 0 && tb == st.total;
     const bool head = ta > 0;
@@ -851,6 +945,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join_kernel(const
 constexpr int kDecMaxCtas = 152 * 3;
 
 constexpr int kDecWorkers = kDecMaxCtas * kDecWarps;
+constexpr int kSmallKeys = 1024;
+constexpr int kSmallUnits = 4096;
 
 // query heads of a part: what a K/V head's group has, at most 16
 int decode_rows(int G) { return G <= 8 ? 8 : 16; }
@@ -859,6 +955,18 @@ int decode_rows(int G) { return G <= 8 ? 8 : 16; }
 long long decode_workers(int S, int Hkv, int G, int max_pages, int page) {
   const long long steps = static_cast<long long>(max_pages) * (page / 16) * S * Hkv * ((G + 15) / 16);
   return std::min<long long>(kDecWorkers, (steps + kDecWarps - 1) / kDecWarps * kDecWarps);
+}
+// Whether a CTA a unit does: where a row of the table holds up to 1024 tokens,
+// one launch without a scan of the lengths and without parts is shorter than
+// sharing all steps evenly (us, d=128, 4 K/V heads, 300 tokens: 8.3 against
+// 12.3 for 1 sequence, 10.3 against 14.4 for 64; 1000 tokens: 16.5 and 16.4,
+// 26.6 and 32.6; one K/V head of 16 query heads, 1000 tokens: 22 and 18), and
+// the host has one launch and one allocation less (20 against 25 us).  Over
+// very many units the CTAs' set-up adds up (2048 units of 30 tokens: 18.5
+// against 12.3).
+bool decode_small(int S, int Hkv, int G, int max_pages, int page) {
+  const long long units = static_cast<long long>(S) * Hkv * ((G + 15) / 16);
+  return static_cast<long long>(max_pages) * page <= kSmallKeys && units <= kSmallUnits;
 }
 size_t decode_workspace(int d, int G, long long workers) {
   return static_cast<size_t>(workers) * 8 + static_cast<size_t>(workers) * 2 * decode_rows(G) * (d + 2) * 4;
@@ -877,10 +985,10 @@ attn_status_t cache_map(CUtensorMap* map, const void* ptr, int d, bool fp8, long
                         dims, strides, boxes, box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-template <int D, bool FP8, int NT>
+template <int D, bool FP8, int NT, bool SMALL>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, cudaStream_t st) {
   using C = DecCfg<D, FP8, NT>;
-  auto kern = attn_decode_paged_kernel<D, FP8, NT>;
+  auto kern = attn_decode_paged_kernel<D, FP8, NT, SMALL>;
   constexpr int kMaxDev = 64;
   static bool configured[kMaxDev] = {};  // the attribute is per device and function
   int dev = 0;
@@ -891,6 +999,10 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
+  }
+  if constexpr (SMALL) {
+    kern<<<static_cast<unsigned>(p.S * p.Hkv * p.q_tiles), kDecThreads, C::kSmem, st>>>(tk, tv, p);
+    return cudaGetLastError();
   }
   // no more CTAs than the table's rows can hold steps for
   const long long most = ((static_cast<long long>(p.M) << p.page_log2) + C::kKeys - 1) / C::kKeys * p.S * p.Hkv * p.q_tiles;
@@ -925,6 +1037,7 @@ using namespace bss;
 extern "C" size_t attn_decode_paged_workspace_bytes(int S, int H, int H_kv, int d, int max_pages,
                                                     int page_size) {
   if (!decode_sizes(S, H, H_kv, d, max_pages, page_size)) return 0;
+  if (decode_small(S, H_kv, H / H_kv, max_pages, page_size)) return 0;
   return decode_workspace(d, H / H_kv, decode_workers(S, H_kv, H / H_kv, max_pages, page_size));
 }
 
@@ -942,7 +1055,8 @@ extern "C" attn_status_t attn_decode_paged(
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return ATTN_ERR_UNSUPPORTED;
   if (kv_dtype != ATTN_KV_BF16 && kv_dtype != ATTN_KV_E4M3) return ATTN_ERR_UNSUPPORTED;
   if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return ATTN_ERR_INVALID_ARG;
-  const void* ptrs16[] = {q, k_cache, v_cache, o, workspace};
+  const bool small = decode_small(S, H_kv, H / H_kv, max_pages, page_size);
+  const void* ptrs16[] = {q, k_cache, v_cache, o, small ? o : workspace};
   for (const void* ptr : ptrs16)
     if (!ptr || !aligned16(ptr)) return ATTN_ERR_INVALID_ARG;
   const void* ptrs4[] = {page_table, seq_lens, lse};
@@ -957,7 +1071,7 @@ extern "C" attn_status_t attn_decode_paged(
     return ATTN_ERR_INVALID_ARG;
   if (q_stride < static_cast<int64_t>(H) * d || q_stride % 8) return ATTN_ERR_INVALID_ARG;
   const long long workers = decode_workers(S, H_kv, H / H_kv, max_pages, page_size);
-  if (workspace_bytes < decode_workspace(d, H / H_kv, workers)) return ATTN_ERR_WORKSPACE;
+  if (!small && workspace_bytes < decode_workspace(d, H / H_kv, workers)) return ATTN_ERR_WORKSPACE;
   DecodeParams p{};
   if ((s = status_word(&p.err)) != ATTN_OK) return s;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -993,13 +1107,19 @@ extern "C" attn_status_t attn_decode_paged(
   const long long rows = static_cast<long long>(H_kv) * page_size;
   if ((s = cache_map(&tk, k_cache, d, fp8, rows, n_pages, p.k_stride)) != ATTN_OK) return s;
   if ((s = cache_map(&tv, v_cache, d, fp8, rows, n_pages, p.v_stride)) != ATTN_OK) return s;
-  cudaError_t e;
-  if (d == 64) {
-    e = fp8 ? (one ? launch_decode<64, true, 1>(tk, tv, p, st) : launch_decode<64, true, 2>(tk, tv, p, st))
-            : (one ? launch_decode<64, false, 1>(tk, tv, p, st) : launch_decode<64, false, 2>(tk, tv, p, st));
-  } else {
-    e = fp8 ? (one ? launch_decode<128, true, 1>(tk, tv, p, st) : launch_decode<128, true, 2>(tk, tv, p, st))
-            : (one ? launch_decode<128, false, 1>(tk, tv, p, st) : launch_decode<128, false, 2>(tk, tv, p, st));
-  }
+  cudaError_t e = cudaErrorInvalidValue;
+#define BSS_DECODE_CASE(DD, FP, NN, SM) \
+  if (d == DD && fp8 == FP && one == (NN == 1) && small == SM) e = launch_decode<DD, FP, NN, SM>(tk, tv, p, st);
+#define BSS_DECODE_CASES(DD, FP)    \
+  BSS_DECODE_CASE(DD, FP, 1, false) \
+  BSS_DECODE_CASE(DD, FP, 2, false) \
+  BSS_DECODE_CASE(DD, FP, 1, true)  \
+  BSS_DECODE_CASE(DD, FP, 2, true)
+  BSS_DECODE_CASES(64, false)
+  BSS_DECODE_CASES(64, true)
+  BSS_DECODE_CASES(128, false)
+  BSS_DECODE_CASES(128, true)
+#undef BSS_DECODE_CASES
+#undef BSS_DECODE_CASE
   return cuda_status("attn_decode_paged launch", e);
 }

@@ -423,9 +423,9 @@ enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1 };
  *   page outside [0, n_pages) is skipped and reported, a length past
  *   max_pages * page_size is cut to it and reported.
  *   workspace: device, 16-byte aligned, >= attn_decode_paged_workspace_bytes
- *   (0 for invalid arguments; it does not depend on the lengths, and at most
- *   16 MB for groups of up to 8 query heads, 31 MB for larger ones), contents
- *   on entry irrelevant.  Calls that can overlap need a workspace each.
+ *   (it does not depend on the lengths: 0 for invalid arguments and for small
+ *   calls, which take NULL; at most 16 MB for groups of up to 8 query heads,
+ *   31 MB for larger ones), contents on entry irrelevant.  Calls that can overlap need a workspace each.
  *   The same lengths give the same bits in every run.
  */
 size_t attn_decode_paged_workspace_bytes(int S, int H, int H_kv, int d, int max_pages,

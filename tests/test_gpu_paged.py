@@ -123,9 +123,12 @@ def test_decode(bss, lens, H, Hkv, d, page, window, sinks, e4m3):
     c = Cache(lens, Hkv, d, page, sum(lens) + H + page, e4m3, window=window, sinks=sinks)
     g = torch.Generator("cuda").manual_seed(H + len(lens))
     q = torch.randn(len(lens), H, d, generator=g, device="cuda").bfloat16()
-    a = check_decode(bss, c, q, lens, window, sinks)
-    b = check_decode(bss, c, q, lens, window, sinks)
-    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # a table with little room takes a block per K/V head, a wide one shares all steps evenly
+    for columns in (0, 1100 // page):
+        c.table = torch.cat([c.table, ints([[-1] * columns] * len(lens))], 1)
+        a = check_decode(bss, c, q, lens, window, sinks)
+        b = check_decode(bss, c, q, lens, window, sinks)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_decode_of_many_sequences(bss):
@@ -499,7 +502,7 @@ def test_two_graphs_and_streams(bss):
     lens = [[300, 0, 77, 1024], [64, 500, 3]]
     caches = [Cache(l, 2, 128, 32, 31 + i) for i, l in enumerate(lens)]
     qs = [torch.randn(len(l), 8, 128, device="cuda").bfloat16() for l in lens]
-    ws = torch.empty(max(bss.attn_decode_paged_workspace_bytes(len(l), 8, 2, 128, c.table.shape[1], 32)
+    ws = torch.empty(16 + max(bss.attn_decode_paged_workspace_bytes(len(l), 8, 2, 128, c.table.shape[1], 32)
                          for l, c in zip(lens, caches)), device="cuda", dtype=torch.uint8)
     ws.fill_(255)
     run = lambda i, **kw: bss.attn_decode_paged(qs[i], caches[i].k, caches[i].v, caches[i].table,  # noqa: E731
@@ -549,6 +552,6 @@ def test_paged_refusals(bss):
     with pytest.raises(bss.AttnError, match="INVALID_ARG"):
         bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens, sinks=3)
     with pytest.raises(bss.AttnError, match="WORKSPACE"):
-        bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens, workspace=torch.empty(64, device="cuda"))
+        bss.attn_decode_paged(q, c.k, c.v, c.table.repeat(1, 50), c.lens, workspace=torch.empty(64, device="cuda"))
     with pytest.raises(bss.AttnError, match="UNSUPPORTED"):
         bss.attn_kv_reserve(c.table, c.lens, ints([0] * c.k.shape[0]), ints([1]), 24)

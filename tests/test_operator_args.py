@@ -54,17 +54,18 @@ def test_window_backward(lib):
 
 
 def test_decode(lib):
-    full = lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 4, 16)
+    full = lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 400, 16)
     assert full > 0
-    assert lib.attn_decode_paged_workspace_bytes(3, 8, 3, 128, 4, 16) == 0
-    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 96, 4, 16) == 0
+    assert lib.attn_decode_paged_workspace_bytes(3, 8, 3, 128, 400, 16) == 0
+    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 96, 400, 16) == 0
     assert lib.attn_decode_paged_workspace_bytes(0, 8, 2, 128, 4, 16) == 0
-    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 4, 24) == 0
+    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 4, 16) == 0      # small: none needed
+    assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 400, 24) == 0
     assert lib.attn_decode_paged_workspace_bytes(3, 8, 2, 128, 0, 16) == 0
     assert lib.attn_decode_paged_workspace_bytes(9000, 8, 2, 128, 400, 16) <= 16e6
 
     def call(q=P, qs=8 * 128, ks=2 * 16 * 128, vs=2 * 16 * 128, kind=0, kscale=None, vscale=None,
-             table=P, ws=P, nbytes=full, S=3, H=8, Hkv=2, d=128, M=4, n=20, page=16, scale=0.1, window=0,
+             table=P, ws=P, nbytes=full, S=3, H=8, Hkv=2, d=128, M=400, n=20, page=16, scale=0.1, window=0,
              sinks=0):
         return lib.attn_decode_paged(q, qs, P, P, ks, vs, kind, kscale, vscale, table, P, P, P, ws, nbytes,
                                      S, H, Hkv, d, M, n, page, scale, window, sinks, None)

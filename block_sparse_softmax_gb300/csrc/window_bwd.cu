@@ -52,7 +52,6 @@ struct WindowBwdParams {
   int nk;               // key tiles
   int nst;              // the first of them, which hold a sink key
   int seg_s, seg_w;     // segments of a sink tile's walk and of another tile's
-  int head_group;       // K/V heads whose key tiles come together
   int n_items;          // key tiles, or segments of them, over all heads
   int* err;
 };
@@ -147,8 +146,8 @@ struct WinBwdRegs {
 
 
 // Item x: the sink tiles' segments first (each at least as long as any other
-// walk), then the other key tiles in groups of K/V heads, tile-major inside a
-// group, so that the running CTAs' Q, dO and dQ accumulator stay in L2.
+// walk), then the other key tiles with the K/V heads side by side, so that the
+// running CTAs' Q, dO and dQ accumulator stay in L2.
 struct WindowBwdCta {
   int bh, j, seg, nseg, slot;
 };
@@ -170,11 +169,8 @@ __device__ __forceinline__ WindowBwdCta window_bwd_cta(int x, const WindowBwdPar
   c.nseg = p.seg_w;
   c.seg = y % p.seg_w;
   const int z = y / p.seg_w;
-  const int grp = z / (p.head_group * n);
-  const int gsz = min(p.head_group, BH - grp * p.head_group);
-  const int within = z - grp * p.head_group * n;
-  const int jj = within / gsz;
-  c.bh = grp * p.head_group + (within - jj * gsz);
+  const int jj = z / BH;
+  c.bh = z - jj * BH;
   c.j = p.nst + jj;
   c.slot = (p.seg_s > 1 ? n_sink : 0) + (c.bh * n + jj) * p.seg_w + c.seg;
   return c;
@@ -1060,7 +1056,11 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   // walks, but of at least 8 tiles (a part costs as much memory as 2 tiles)
   const long long each = std::max(8ll, (share + pl.seg_w - 1) / pl.seg_w);
   pl.seg_s = static_cast<int>(std::max(1ll, (nq * G + each - 1) / each));
-  if (pl.nst == 0) pl.seg_s = 1;
+  // ... and no more of them than 8 an SM: many sink tiles fill the GPU uncut,
+  // and their parts would take more memory than everything else (16384 sinks
+  // of 16384 keys, 32 heads, d=128: 8.6 GB)
+  if (pl.nst > 0) pl.seg_s = static_cast<int>(std::max(1ll, std::min<long long>(pl.seg_s, 152 * 8 / (BH * pl.nst))));
+  else pl.seg_s = 1;
   // A CTA an SM that takes items by a fixed stride saves an item's set-up
   // (5-8 % over walks of up to 12 tiles); over longer walks, whose lengths
   // differ more, a CTA an item is balanced better by the hardware (equal at 17
@@ -1199,7 +1199,6 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   p.nst = pl.nst;
   p.seg_s = pl.seg_s;
   p.seg_w = pl.seg_w;
-  p.head_group = B * H_kv;
   p.n_items = static_cast<int>(pl.n_cta);
   return cuda_status("attn_bwd_window launch",
                      d == 64 ? launch_window_bwd<64>(tq, tk, tv, tdo, tdq, p, pl.n_cta, pl.persistent, st)

@@ -65,6 +65,8 @@ SHAPES = [
     (1, 2, 2, 100, 12, 128, 50, 0, 0, 0),        # 12 keys, queries run past them
     (1, 2, 2, 100, 40, 64, 50, 3, 5, 0),
     (1, 2, 1, 0, 70, 64, 5, 0, 0, 0),            # no query
+    (1, 50, 50, 2100, 2100, 64, 100, 1200, 0, 0),  # sink tiles for three waves of CTAs
+    (1, 48, 48, 1100, 1100, 64, 100, 1100, 0, 0),
 ]
 
 

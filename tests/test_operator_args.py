@@ -43,6 +43,11 @@ def test_window_backward(lib):
     assert size(1, 4, 2, 4096, 4096, 64, 0, 4, 0, 0) == 0
     assert size(1, 4, 2, 4096, 4096, 64, 256, -1, 0, 0) == 0
 
+    # however many keys are sinks, the parts of their walks stay within 8 a multiprocessor
+    for sinks in (1, 4, 1000, 16384):
+        assert size(2, 16, 16, 16384, 16384, 128, 1, sinks, 0, 0) <= (
+            2 * 16 * 16384 * 128 * 4 + 152 * 8 * 2 * 128 * 128 * 4)
+
     def call(ws=P, nbytes=full, B=1, H=4, Hkv=2, d=64, window=256, sinks=4, q=P, lse=P):
         return lib.attn_bwd_window(q, P, P, P, lse, P, P, P, P, P, ws, nbytes, B, H, Hkv, 4096, 4096, d,
                                    0.1, window, sinks, 0, 0, None)

@@ -87,6 +87,11 @@ struct DecodeParams {
   int* err;
 };
 
+// The tokens a row of the table has room for.
+__device__ __forceinline__ int most_tokens(const DecodeParams& p) {
+  return static_cast<int>(min(static_cast<long long>(p.M) << p.page_log2, static_cast<long long>(kMaxTokens)));
+}
+
 // The steps of KEYS keys a sequence's query reads: the sinks' steps [0,
 // nsink), then [first, first + rest).
 template <int KEYS>
@@ -105,7 +110,7 @@ struct SeqSteps {
 template <int KEYS>
 __device__ __forceinline__ SeqSteps<KEYS> seq_steps(int n, const DecodeParams& p) {
   SeqSteps<KEYS> q;
-  q.n = min(max(n, 0), static_cast<int>(min(static_cast<long long>(p.M) << p.page_log2, 0x7FFFFF00ll)));
+  q.n = min(max(n, 0), most_tokens(p));
   q.lo = p.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(q.n) - p.window)) : 0;
   q.sk = min(p.sinks, q.lo);
   q.first = q.lo / KEYS;
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     un.s = cta / units;
     un.r = cta - un.s * units;
     const int n = __ldg(p.lens + un.s);
-    if (tid == 0 && un.r == 0 && (n < 0 || n > (static_cast<long long>(p.M) << p.page_log2)))
+    if (tid == 0 && un.r == 0 && (n < 0 || n > most_tokens(p)))
       record_error(p.err, ATTN_ERR_BAD_PAGES);
     un.st = seq_steps<KEYS>(n, p);
     un.x0 = 0;
@@ -365,20 +370,24 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     // sequences that see no key, and lengths out of range
     for (int s = cta; s < p.S; s += n_cta) {
       const int n = __ldg(p.lens + s);
-      if (tid == 0 && (n < 0 || n > (static_cast<long long>(p.M) << p.page_log2)))
+      if (tid == 0 && (n < 0 || n > most_tokens(p)))
         record_error(p.err, ATTN_ERR_BAD_PAGES);
       if (seq_steps<KEYS>(n, p).total > 0) continue;
       for (int e = tid; e < p.H * D; e += kDecThreads)
         p.o[static_cast<size_t>(s) * p.H * D + e] = __float2bfloat16(0.f);
       for (int h = tid; h < p.H; h += kDecThreads) p.lse[static_cast<size_t>(s) * p.H + h] = NEG_INF;
     }
-    // the sequences that hold its warps' first steps, and the steps before them
+    // the sequences that hold its warps' first steps, and the steps before
+    // them.  (The lengths are read again: should somebody change them in the
+    // meantime, the results are lost, but every walk below ends and every
+    // index stays in range.)
     if (cta * kDecWarps < active) {
       long long last_x0 = edge[0];
       for (int w = 1; w < kDecWarps; ++w)
         if (cta * kDecWarps + w < active) last_x0 = edge[w];
       long long base = 0;
-      for (int s0 = 0;; s0 += kDecThreads) {
+      if (tid < kDecWarps) found[2 * tid] = -1;
+      for (int s0 = 0; s0 < p.S; s0 += kDecThreads) {
         const int s = s0 + tid;
         const long long t = s < p.S ? static_cast<long long>(seq_steps<KEYS>(__ldg(p.lens + s), p).total) * units : 0;
         long long x = t;
@@ -405,16 +414,18 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
       __syncthreads();
     }
     // from here on the warps go their own ways
-    if (x0 >= x1) {
+    bool any = x0 < x1 && found[2 * warp] >= 0;
+    if (any) {
+      un.s = static_cast<int>(found[2 * warp]);
+      un.st = seq_steps<KEYS>(__ldg(p.lens + un.s), p);
+      const long long before = found[2 * warp + 1];
+      un.r = un.st.total > 0 ? static_cast<int>((x0 - before) / un.st.total) : units;
+      un.x0 = before + static_cast<long long>(un.r) * un.st.total;
+      any = un.r < units;
+    }
+    if (!any) {
       if (lane == 0) p.meta[worker] = meta;
       return;
-    }
-    un.s = static_cast<int>(found[2 * warp]);
-    un.st = seq_steps<KEYS>(__ldg(p.lens + un.s), p);
-    {
-      const long long before = found[2 * warp + 1];
-      un.r = static_cast<int>((x0 - before) / un.st.total);
-      un.x0 = before + static_cast<long long>(un.r) * un.st.total;
     }
     un.ta = static_cast<int>(x0 - un.x0);
     un.tb = static_cast<int>(min(static_cast<long long>(un.st.total), x1 - un.x0));
@@ -505,7 +516,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     if (++u.r == units) {
       u.r = 0;
       do {
-        u.st = seq_steps<KEYS>(__ldg(p.lens + ++u.s), p);
+        if (++u.s == p.S) return false;
+        u.st = seq_steps<KEYS>(__ldg(p.lens + u.s), p);
       } while (u.st.total == 0);
     }
     u.ta = 0;
@@ -765,7 +777,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     if (!whole && !head) {
       // step y of the line lies in the last warp w with steps w / active <= y
       meta.x = s * units + r;
-      meta.y = static_cast<int>(((unit_x + st.total) * active + steps - 1) / steps) - 1;
+      meta.y = static_cast<int>(min(((unit_x + st.total) * active + steps - 1) / steps, static_cast<long long>(active))) - 1;
     }
     float* part = p.part + (static_cast<size_t>(worker) * 2 + (head ? 0 : 1)) * p.rows * (D + 2);
     const float vs = FP8 ? __ldg(p.v_scale + hkv) : 1.f;
@@ -1105,6 +1117,7 @@ extern "C" attn_status_t attn_decode_paged(
   if ((s = get_encoder()) != ATTN_OK) return s;
   CUtensorMap tk, tv;
   const long long rows = static_cast<long long>(H_kv) * page_size;
+  if (rows > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;     // a copy's row is an int
   if ((s = cache_map(&tk, k_cache, d, fp8, rows, n_pages, p.k_stride)) != ATTN_OK) return s;
   if ((s = cache_map(&tv, v_cache, d, fp8, rows, n_pages, p.v_stride)) != ATTN_OK) return s;
   cudaError_t e = cudaErrorInvalidValue;

@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kBookThreads) kv_reserve_kernel(const PageStat
     long long need = 0;
     if (s < st.S) {
       const int len = st.lens[s], n = n_new[s];
-      if (len < 0 || n < 0 || static_cast<long long>(len) + n > static_cast<long long>(st.M) * st.page)
+      if (len < 0 || n < 0 ||
+          static_cast<long long>(len) + n > min(static_cast<long long>(st.M) * st.page, static_cast<long long>(kMaxTokens)))
         bad = 1;
       else
         need = ceil_div(static_cast<long long>(len) + n, st.page) - ceil_div(len, st.page);

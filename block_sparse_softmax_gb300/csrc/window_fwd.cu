@@ -16,7 +16,7 @@
 // fixed stride (the items of a window are alike), so every role knows the next
 // item; four kinds of warps each run ahead over the items:
 //   TMA     K of the next pair, at an item's end the next item's first pair
-//           and its Q tile (prefetched into L2 an item earlier), then V;
+//           and its Q tile, then V;
 //   MMA     S of the next pair, or of the next item's first one, before P V of
 //           this one;
 //   softmax two warpgroups, one per block of the pair, which exchange their

@@ -367,7 +367,9 @@ attn_status_t attn_fwd_window(const void* q, const void* k, const void* v, void*
  *   heads of their group), delta fp32 [B,H,Lq]: dO . O, and for queries of few
  *   keys (up to 64 near the first and past the last key; all of them when
  *   window and sinks are at most 32 keys together) sum_j P_ij (dO_i . V_j),
- *   the same without O's rounding.  A query that sees no key gets dq = 0; a key that no query sees gets dk = dv = 0.
+ *   the same without O's rounding.  A query that sees no key gets dq = 0; a
+ *   key that no query sees gets dk = dv = 0.  Inputs are taken as finite, as in
+ *   attn_fwd_window.
  *   dk and dv are the same in every run.  dq is accumulated in fp32 in the
  *   order the key tiles finish, so its last bit may differ from run to run.
  *   workspace: device, 16-byte aligned, >= attn_bwd_window_workspace_bytes
@@ -395,8 +397,8 @@ attn_status_t attn_bwd_window(const void* q, const void* k, const void* v, const
  *   - page_table [S][max_pages] int32: entry m of row s is the page of tokens
  *     m * page_size .. of sequence s, -1 where it holds none.  seq_lens [S]
  *     int32: tokens.  refs [n_pages] int32: table entries holding the page
- *     (0: free).  S <= 65536, n_pages <= 2^30.  A fresh cache has every entry -1, every length
- *     and every count 0.
+ *     (0: free).  S <= 65536, n_pages <= 2^30, a length at most 0x7FFFFF00.
+ *     A fresh cache has every entry -1, every length and every count 0.
  *   - The attn_kv_ calls keep these consistent: a page that is not full is
  *     held once, pages are taken from the lowest free index up, in order of
  *     the sequences (or forks), and a call that cannot be met changes nothing.
@@ -421,11 +423,12 @@ enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1 };
  *   Table entries of keys that are not seen are not read, and neither are the
  *   rows of the last page past the length: they may hold anything.  A seen
  *   page outside [0, n_pages) is skipped and reported, a length past
- *   max_pages * page_size is cut to it and reported.
+ *   max_pages * page_size (or 0x7FFFFF00) is cut to it and reported.
  *   workspace: device, 16-byte aligned, >= attn_decode_paged_workspace_bytes
  *   (it does not depend on the lengths: 0 for invalid arguments and for small
  *   calls, which take NULL; at most 16 MB for groups of up to 8 query heads,
- *   31 MB for larger ones), contents on entry irrelevant.  Calls that can overlap need a workspace each.
+ *   31 MB for larger ones), contents on entry irrelevant.  Calls that can
+ *   overlap need a workspace each.
  *   The same lengths give the same bits in every run.
  */
 size_t attn_decode_paged_workspace_bytes(int S, int H, int H_kv, int d, int max_pages,
@@ -442,7 +445,7 @@ attn_status_t attn_decode_paged(const void* q, int64_t q_stride, const void* k_c
  * attn_kv_reserve - room for n_new[s] >= 0 more tokens in every sequence: new
  * pages enter the table, seq_lens grows.  start [S] out: the position of the
  * first new token, or -1 for every sequence when the call was refused (too
- * few free pages, or a sequence past max_pages * page_size).
+ * few free pages, or a sequence past max_pages * page_size or 0x7FFFFF00).
  */
 attn_status_t attn_kv_reserve(int32_t* page_table, int32_t* seq_lens, int32_t* refs,
                               const int32_t* n_new, int32_t* start, int S, int max_pages,

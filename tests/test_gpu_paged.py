@@ -463,6 +463,31 @@ def test_refused_bookkeeping_changes_nothing(bss):
     same(small, t, n, r)
 
 
+def test_the_longest_sequence(bss):
+    """Lengths count in 32 bits: a table with room for more neither grows a sequence past the last
+    length nor decodes past it."""
+    most, page = 0x7FFFFF00, 1024
+    table = torch.zeros(1, 2 ** 21 + 1, dtype=torch.int32, device="cuda")
+    refs = ints([1, 0, 0, 0])
+    lens = ints([most - 256])
+    assert bss.attn_kv_reserve(table, lens, refs, ints([257]), page).tolist() == [-1]
+    assert bss.attn_poll_status() == bss.ERR_BAD_PAGES and lens.tolist() == [most - 256]
+    assert bss.attn_kv_reserve(table, lens, refs, ints([256]), page).tolist() == [most - 256]
+    assert bss.attn_poll_status() == 0 and lens.tolist() == [most]
+    g = torch.Generator("cuda").manual_seed(1)
+    k, v = (torch.randn(1, 1, page, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(1, 2, 64, generator=g, device="cuda").bfloat16()
+    o, lse = bss.attn_decode_paged(q, k, v, table, lens, window=100, sinks=3)
+    assert bss.attn_poll_status() == 0
+    rows = [0, 1, 2] + [(most - 100 + i) % page for i in range(100)]
+    mask = torch.ones(1, 103, dtype=torch.bool, device="cuda")
+    args = q.reshape(1, 2, 1, 64), k[:, :, rows].double(), v[:, :, rows].double(), mask, 0.125
+    assert ((o.double() - ref.forward(*args)[0][:, :, 0]).abs() <= ref.forward_bounds(*args)[0][:, :, 0]).all()
+    lens[0] = 0x7FFFFFFF
+    cut, _ = bss.attn_decode_paged(q, k, v, table, lens, window=100, sinks=3)
+    assert bss.attn_poll_status() == bss.ERR_BAD_PAGES and torch.equal(cut, o)
+
+
 def test_bookkeeping_of_many_pages(bss):
     """More pages than one turn of the scan takes, and tables that a second launch rewrites."""
     P, S, M, page = 70001, 700, 120, 16

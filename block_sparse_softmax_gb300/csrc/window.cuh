@@ -24,19 +24,28 @@ struct WindowFwdParams {
   __nv_bfloat16* o;    // [B,H,Lq,d]
   float* lse;          // [B,H,Lq]
   int n_items;         // 128-row query tiles of every (b, h)
+  int split;           // CTAs of an item (a cluster of them; 1: none)
   int* err;
 };
 
-// The key blocks (of 128) a query tile reads: the sink blocks [0, nsb) and the
-// window's blocks [wb0, wb0 + nwb), disjoint and in ascending order.
+// The key blocks (of 128) a query tile reads: the sink blocks [sb0, sb0 + nsb)
+// and the window's blocks [wb0, wb0 + nwb), disjoint and in ascending order.
 struct WindowBlocks {
   int nsb, wb0, nwb;
+  int sb0;                 // 0, but for a part of a list
   __device__ __forceinline__ int count() const { return nsb + nwb; }
-  __device__ __forceinline__ int at(int n) const { return n < nsb ? n : wb0 + (n - nsb); }
+  __device__ __forceinline__ int at(int n) const { return n < nsb ? sb0 + n : wb0 + (n - nsb); }
+  // Part `rank` of `split` parts of about as many pairs of blocks each.
+  __device__ __forceinline__ WindowBlocks part(int rank, int split) const {
+    const int pairs = (count() + 1) / 2;
+    const int b0 = 2 * (pairs * rank / split), b1 = min(count(), 2 * (pairs * (rank + 1) / split));
+    const int w0 = max(b0 - nsb, 0);
+    return WindowBlocks{max(min(b1, nsb) - b0, 0), wb0 + w0, max(b1 - nsb, 0) - w0, b0};
+  }
 };
 
 __device__ __forceinline__ WindowBlocks window_blocks(const WindowMask& w, int r0, int Lq, int Lk) {
-  WindowBlocks b{0, 0, 0};
+  WindowBlocks b{0, 0, 0, 0};
   if (r0 >= Lq || Lk <= 0) return b;
   const long long last = static_cast<long long>(min(r0 + kTileM, Lq) - 1) + w.sh;   // last row's own key
   if (last < 0) return b;

@@ -33,15 +33,20 @@
 // has freed its buffer (shared memory holds one at d=128; prefetching it into
 // L2 made everything 3 to 5 % slower).
 //
+// Where a launch has few items, a cluster of CTAs shares one (window_split).
+//
 // The element mask is applied in the blocks that the diagonal, the window's
 // lower edge or the last sink crosses; all others run without it.
 #include <algorithm>
+#include <mutex>
 
 #include "host.cuh"
 #include "window.cuh"
 
 namespace bss {
 namespace {
+
+constexpr int kMostSplit = 4;      // CTAs that share an item at most
 
 template <int D>
 struct WinCfg {
@@ -93,6 +98,13 @@ struct WinCfg {
   static constexpr uint32_t kColP = 256;    // P: 256 keys, bf16 pairs (block X at 256 + 64 X)
   static constexpr uint32_t kColO = 384;    // O: D fp32 columns
   static constexpr int kThreads = 512;
+  // Split items: when an item's last S is done, its K ring takes the rows'
+  // statistics (m, l) and then the other CTAs' parts of this CTA's columns of
+  // O, fp32 [CTA][4 columns][128 rows].
+  static constexpr int kStatOff = kKOff;
+  static constexpr int kRecvOff = kKOff + 2 * kTileM * 4;
+  static_assert(kRecvOff + kTileM * D * 4 <= kVOff, "the parts fit the K ring");
+  static_assert(D / kMostSplit >= 16, "16 columns of O at least to a CTA");
 };
 
 // Register split per warpgroup (setmaxnreg): output (warps 0-3), softmax
@@ -111,6 +123,7 @@ struct WindowItem {
   int b, h, bh, hkv, r0;
   WindowBlocks kb;
 };
+template <bool SPLIT>
 __device__ __forceinline__ WindowItem window_item(int item, const WindowFwdParams& p, int n_tiles) {
   WindowItem it;
   const int BH = p.B * p.H;
@@ -121,20 +134,52 @@ __device__ __forceinline__ WindowItem window_item(int item, const WindowFwdParam
   it.hkv = it.h / (p.H / p.Hkv);
   it.r0 = (n_tiles - 1 - rank) * kTileM;
   it.kb = window_blocks(p.w, it.r0, p.Lq, p.Lk);
+  if (SPLIT) it.kb = it.kb.part(static_cast<int>(blockIdx.x) % p.split, p.split);
   return it;
 }
 
+// A CTA's first item, and how far the next one is (a split item is its CTAs' only one).
+template <bool SPLIT>
+__device__ __forceinline__ int window_first(const WindowFwdParams& p) {
+  return SPLIT ? static_cast<int>(blockIdx.x) / p.split : static_cast<int>(blockIdx.x);
+}
+template <bool SPLIT>
+__device__ __forceinline__ int window_stride(const WindowFwdParams& p) {
+  return SPLIT ? p.n_items : static_cast<int>(gridDim.x);
+}
 // The first item from `item` on in this CTA's stride that has a key block
 // (p.n_items or more: none).
+template <bool SPLIT>
 __device__ __forceinline__ int window_next(int item, const WindowFwdParams& p, int n_tiles, WindowItem& it) {
-  for (; item < p.n_items; item += static_cast<int>(gridDim.x)) {
-    it = window_item(item, p, n_tiles);
+  for (; item < p.n_items; item += window_stride<SPLIT>(p)) {
+    it = window_item<SPLIT>(item, p, n_tiles);
     if (it.kb.count() > 0) break;
   }
   return item;
 }
 
-template <int D>
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// The address of this CTA's shared memory `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_store4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+
+// SPLIT: the CTAs of a cluster share one item's blocks, and join their states.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(512, 1)
     attn_fwd_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const WindowFwdParams p) {
@@ -157,8 +202,9 @@ __global__ void __launch_bounds__(512, 1)
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
   const int tid = static_cast<int>(threadIdx.x);
-  // A launch whose earlier CTAs already timed out stops at once.
-  if (*reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
+  // A launch whose earlier CTAs already timed out stops at once (but not a
+  // cluster's CTAs, which would have to agree on it).
+  if (!SPLIT && *reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
   const int n_tiles = (p.Lq + kTileM - 1) / kTileM;
 
   if (tid == 0) {
@@ -259,7 +305,7 @@ __global__ void __launch_bounds__(512, 1)
           return true;
         };
         WindowItem it;
-        int item = window_next(static_cast<int>(blockIdx.x), p, n_tiles, it);
+        int item = window_next<SPLIT>(window_first<SPLIT>(p), p, n_tiles, it);
         bool ok = true;
         if (item < p.n_items) ok = load_k(it, 0) && load_q(it);
         int k = 0;
@@ -273,7 +319,7 @@ __global__ void __launch_bounds__(512, 1)
             ok = load_k(it, ++k);
           } else {
             k = 0;
-            item = window_next(item + static_cast<int>(gridDim.x), p, n_tiles, it);
+            item = window_next<SPLIT>(item + window_stride<SPLIT>(p), p, n_tiles, it);
             if (item < p.n_items) ok = load_k(it, 0) && load_q(it);
           }
           ok = ok && load_v(v0, hkv, b) && load_v(v1, hkv, b);
@@ -358,11 +404,11 @@ __global__ void __launch_bounds__(512, 1)
           return true;
         };
         WindowItem it;
-        int item = window_next(static_cast<int>(blockIdx.x), p, n_tiles, it);
+        int item = window_next<SPLIT>(window_first<SPLIT>(p), p, n_tiles, it);
         int nb = it.kb.count();
         bool ok = item >= p.n_items || issue_s(0, nb);
         while (ok && item < p.n_items) {
-          item = window_next(item + static_cast<int>(gridDim.x), p, n_tiles, it);
+          item = window_next<SPLIT>(item + window_stride<SPLIT>(p), p, n_tiles, it);
           const int nb2 = item < p.n_items ? it.kb.count() : 0;
           const int ns = (nb + 1) / 2;
           for (int k = 0; k < ns && ok; ++k) {
@@ -385,10 +431,84 @@ __global__ void __launch_bounds__(512, 1)
     // =================== output: thread = query row ===================
     const int row_in_tile = warp * 32 + lane;
     const uint32_t tO = tmem + (static_cast<uint32_t>(warp * 32) << 16) + C::kColO;
+    if constexpr (SPLIT) {
+      // Every CTA of the cluster is done with its part of the keys; rank r
+      // joins columns [r D / split, (r + 1) D / split) of O.  A part is scaled
+      // by e^{m_c - m} / l on its way, l = sum_c e^{m_c - m} l_c.
+      cluster_arrive();
+      cluster_wait();
+      tc_fence_after();
+      const int rank = static_cast<int>(blockIdx.x) % p.split;
+      const int cols = D / p.split;
+      const WindowItem it = window_item<SPLIT>(window_first<SPLIT>(p), p, n_tiles);
+      const float NEG_INF = -__int_as_float(0x7f800000);
+      const uint32_t stat = sbase + C::kStatOff + row_in_tile * 4;
+      float m = NEG_INF, l = 0.f, f = 0.f;
+      for (int c = 0; c < p.split; ++c)
+        if (cluster_load(cluster_addr(stat + kTileM * 4, c)) != 0.f)
+          m = fmaxf(m, cluster_load(cluster_addr(stat, c)));
+      for (int c = 0; c < p.split; ++c) {
+        const float lc = cluster_load(cluster_addr(stat + kTileM * 4, c));
+        if (lc == 0.f) continue;                      // this part saw no key
+        const float w = ex2(cluster_load(cluster_addr(stat, c)) - m);
+        l = fmaf(w, lc, l);
+        if (c == rank) f = w;
+      }
+      if (l != 0.f) f /= l;
+      const bool none = it.kb.count() == 0 || f == 0.f;   // O holds nothing, or nothing that counts
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        const int owner = c * 16 / cols;
+        if (owner == rank) continue;
+        uint32_t o[16];
+        tmem_ld16(tO + c * 16, o);
+        tmem_ld_wait16(o);
+        const uint32_t to = cluster_addr(
+            sbase + C::kRecvOff + ((rank * cols + c * 16 - owner * cols) / 4 * kTileM + row_in_tile) * 16, owner);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          cluster_store4(to + e / 4 * kTileM * 16, none ? 0.f : __uint_as_float(o[e]) * f,
+                         none ? 0.f : __uint_as_float(o[e + 1]) * f, none ? 0.f : __uint_as_float(o[e + 2]) * f,
+                         none ? 0.f : __uint_as_float(o[e + 3]) * f);
+      }
+      cluster_arrive();
+      cluster_wait();
+      const int row = it.r0 + row_in_tile;
+      const size_t at = static_cast<size_t>(it.bh) * p.Lq + row;
+#pragma unroll 1
+      for (int c = rank * cols / 16; c < (rank + 1) * cols / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(tO + c * 16, o);
+        tmem_ld_wait16(o);
+        float y[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = none ? 0.f : __uint_as_float(o[e]) * f;
+        for (int s = 0; s < p.split; ++s) {
+          if (s == rank) continue;
+          const float4* from = reinterpret_cast<const float4*>(smem + C::kRecvOff) +
+                               (s * cols + c * 16 - rank * cols) / 4 * kTileM + row_in_tile;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 x = from[e * kTileM];
+            y[4 * e] += x.x;
+            y[4 * e + 1] += x.y;
+            y[4 * e + 2] += x.z;
+            y[4 * e + 3] += x.w;
+          }
+        }
+        if (row < p.Lq) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + at * D) + 2 * c;
+          dst[0] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+          dst[1] = make_uint4(pack_bf16(y[8], y[9]), pack_bf16(y[10], y[11]), pack_bf16(y[12], y[13]),
+                              pack_bf16(y[14], y[15]));
+        }
+      }
+      if (rank == 0 && row < p.Lq) p.lse[at] = l == 0.f ? NEG_INF : (m + __log2f(l)) * kLn2;
+    }
     const volatile float* inv_s = reinterpret_cast<const volatile float*>(smem + C::kInvOff);
     int on = 0;             // O results read
-    for (int item = static_cast<int>(blockIdx.x); item < p.n_items; item += static_cast<int>(gridDim.x)) {
-      const WindowItem it = window_item(item, p, n_tiles);
+    for (int item = static_cast<int>(blockIdx.x); !SPLIT && item < p.n_items; item += static_cast<int>(gridDim.x)) {
+      const WindowItem it = window_item<SPLIT>(item, p, n_tiles);
       const size_t rows0 = static_cast<size_t>(it.bh) * p.Lq;
       const bool inb = it.r0 + row_in_tile < p.Lq;
       uint4* dst = reinterpret_cast<uint4*>(p.o + (rows0 + it.r0 + row_in_tile) * D);
@@ -458,13 +578,20 @@ __global__ void __launch_bounds__(512, 1)
       ++nx;
       return w;
     };
-    for (int item = static_cast<int>(blockIdx.x); item < p.n_items; item += static_cast<int>(gridDim.x)) {
+    for (int item = window_first<SPLIT>(p); item < p.n_items; item += window_stride<SPLIT>(p)) {
       // few registers are left beside the scores: of the item only its first
       // row and its blocks are kept
       const int r0 = (n_tiles - 1 - item / (p.B * p.H)) * kTileM;
-      const WindowBlocks kb = window_blocks(p.w, r0, p.Lq, p.Lk);
+      WindowBlocks kb = window_blocks(p.w, r0, p.Lq, p.Lk);
+      if (SPLIT) kb = kb.part(static_cast<int>(blockIdx.x) % p.split, p.split);
       const int nb = kb.count();
-      if (nb == 0) continue;
+      if (nb == 0) {
+        if (SPLIT && X == 0) {                      // a part without a block
+          reinterpret_cast<float*>(smem + C::kStatOff)[row_in_tile] = NEG_INF;
+          reinterpret_cast<float*>(smem + C::kStatOff)[kTileM + row_in_tile] = 0.f;
+        }
+        continue;
+      }
       const int ns = (nb + 1) / 2;
       float m2 = NEG_INF;     // reference max (log2 units), moved only by > 8
       float l = 0.f;          // this warpgroup's part of the row sum
@@ -616,7 +743,12 @@ __global__ void __launch_bounds__(512, 1)
       // inverse to the output warps, which must have read the previous item's
       float lo;
       if (!exchange(l, lo)) break;
-      if (X == 0) {
+      if (SPLIT) {
+        if (X == 0) {
+          reinterpret_cast<float*>(smem + C::kStatOff)[row_in_tile] = m2;
+          reinterpret_cast<float*>(smem + C::kStatOff)[kTileM + row_in_tile] = l + lo;
+        }
+      } else if (X == 0) {
         if (on > 0 &&
             !__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarOEmpty), (on - 1) & 1, abort_flag, p.err)))
           break;
@@ -636,6 +768,13 @@ __global__ void __launch_bounds__(512, 1)
   }
 
   tc_fence_before();
+  if (SPLIT && warp >= 4) {        // the output warps' two meetings with the cluster's other CTAs
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+  }
   __syncthreads();
   if (warp == 0) {
     __syncwarp();
@@ -644,29 +783,107 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
+// An item's CTAs.  Where a launch has few items, their steps of a pair of key
+// blocks (1.7 us each) follow one another while most SMs idle: a cluster of 2
+// or 4 CTAs then shares the item's pairs and joins its states through
+// distributed shared memory, which costs 3 to 4 us.  Taken where the clusters
+// all run at once (`room` of them) and items have 5 pairs or more, 4 or more
+// for 4 CTAs (us with 1, 2, 4 CTAs an item, d=128, 16 heads: 1 query, window
+// 512 (2 pairs) 9.0, 10.9, 11.3, window 1024 (4) 12.8, 12.3, 11.5, window 4096
+// 33.2, 22.5, 16.4; 500 queries, which leave room for 2, window 1024 (5) 16.0,
+// 16.0, window 2048 (9) 22.8, 19.5).  8 CTAs find room for few clusters (16
+// of them take two turns).
+int window_split(int n_items, int pairs, const int* room) {
+  if (pairs >= 4 && n_items <= room[1]) return 4;
+  return pairs >= 5 && n_items <= room[0] ? 2 : 1;
+}
+
+template <int D, bool SPLIT>
+cudaError_t launch_window_kernel(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const WindowFwdParams& p, int sms, cudaStream_t st) {
+  using C = WinCfg<D>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(SPLIT ? p.n_items * p.split : std::min(p.n_items, sms));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_fwd_window_kernel<D, SPLIT>, tq, tk, tv, p);
+}
+
+// What a launch has to know of the device, and the kernels' attributes, set once a device.
+struct WindowDevice {
+  bool ready;
+  int sms;
+  int room[2];                  // clusters of 2 and of 4 CTAs that run at once
+};
+template <int D>
+cudaError_t window_device(int dev, const WindowDevice** out) {
+  using C = WinCfg<D>;
+  constexpr int kMaxDev = 64;
+  static WindowDevice devices[kMaxDev] = {};
+  static std::mutex mu;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!devices[dev].ready) {
+    WindowDevice w{};
+    const void* kernels[] = {reinterpret_cast<const void*>(attn_fwd_window_kernel<D, false>),
+                             reinterpret_cast<const void*>(attn_fwd_window_kernel<D, true>)};
+    cudaError_t e;
+    for (const void* k : kernels) {
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
+      if (fa.numRegs < static_cast<int>(kWinLaunchRegs)) return cudaErrorInvalidConfiguration;
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+      if (e != cudaSuccess) return e;
+    }
+    if ((e = cudaDeviceGetAttribute(&w.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    for (int i = 0; i < 2; ++i) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(2 << i);
+      cfg.blockDim = dim3(C::kThreads);
+      cfg.dynamicSmemBytes = C::kSmemBytes;
+      cudaLaunchAttribute attr{};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 2 << i;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if ((e = cudaOccupancyMaxActiveClusters(&w.room[i], kernels[1], &cfg)) != cudaSuccess) return e;
+    }
+    w.ready = true;
+    devices[dev] = w;
+  }
+  *out = &devices[dev];
+  return cudaSuccess;
+}
+
+// `pairs`: pairs of key blocks that an item has at most.
 template <int D>
 cudaError_t launch_window_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const WindowFwdParams& p, cudaStream_t st) {
-  using C = WinCfg<D>;
-  auto kern = attn_fwd_window_kernel<D>;
-  constexpr int kMaxDev = 64;
-  static bool configured[kMaxDev] = {};  // the attribute is per device and function
+                              WindowFwdParams& p, int pairs, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-  if (!configured[dev]) {
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-    if (fa.numRegs < static_cast<int>(kWinLaunchRegs)) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
-  int sms = 0;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  kern<<<std::min(p.n_items, sms), C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  const WindowDevice* w;
+  if ((e = window_device<D>(dev, &w)) != cudaSuccess) return e;
+  p.split = window_split(p.n_items, pairs, w->room);
+  return p.split > 1 ? launch_window_kernel<D, true>(tq, tk, tv, p, w->sms, st)
+                     : launch_window_kernel<D, false>(tq, tk, tv, p, w->sms, st);
+}
+
+// Pairs of key blocks of the query tiles that see the most.
+int window_pairs(const WindowFwdParams& p) {
+  const long long last = std::min<long long>(p.Lq - 1 + p.w.sh, p.Lk - 1);      // the last key anyone sees
+  if (last < 0) return 0;
+  const long long span = std::min<long long>(p.w.window + std::min(p.Lq, kTileM) - 1, last + 1);
+  const long long blocks = (span + kTileN - 1) / kTileN + (p.w.snk + kTileN - 1) / kTileN;
+  return static_cast<int>((std::min(blocks, last / kTileN + 1) + 1) / 2);
 }
 
 }  // namespace
@@ -720,6 +937,8 @@ extern "C" attn_status_t attn_fwd_window(const void* q, const void* k, const voi
   if (items > 0x7FFF0000ll) return ATTN_ERR_UNSUPPORTED;   // counted in an int, a grid's stride past the last
   p.n_items = static_cast<int>(items);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_status("attn_fwd_window launch", d == 64 ? launch_window_fwd<64>(tq, tk, tv, p, st)
-                                                       : launch_window_fwd<128>(tq, tk, tv, p, st));
+  const int pairs = window_pairs(p);
+  const cudaError_t e = d == 64 ? launch_window_fwd<64>(tq, tk, tv, p, pairs, st)
+                                : launch_window_fwd<128>(tq, tk, tv, p, pairs, st);
+  return cuda_status("attn_fwd_window launch", e);
 }

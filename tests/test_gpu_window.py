@@ -65,6 +65,14 @@ SHAPES = [
     (1, 2, 2, 100, 12, 128, 50, 0, 0, 0),        # 12 keys, queries run past them
     (1, 2, 2, 100, 40, 64, 50, 3, 5, 0),
     (1, 2, 1, 0, 70, 64, 5, 0, 0, 0),            # no query
+    (1, 2, 1, 1, 2000, 128, 1500, 4, 1999, 0),   # CTAs that share a tile's keys: one query
+    (1, 2, 2, 300, 2500, 64, 2300, 4, 2200, 0),
+    (1, 40, 8, 100, 1300, 64, 1200, 3, 1200, 0),   # ... two CTAs a tile
+    (1, 50, 25, 128, 1500, 128, 1400, 0, 1372, 0),
+    (1, 4, 2, 1100, 1100, 128, 1000, 2, 0, 0),   # ... and the first tiles have too few for all
+    (1, 2, 1, 700, 1500, 64, 900, 300, 1400, 0),  # ... the last queries see sinks alone
+    (1, 2, 2, 700, 1500, 128, 900, 0, 2000, 0),  # ... or nothing
+    (2, 2, 1, 1000, 700, 64, 10 ** 12, 0, 0, 400),  # ... or the first ones do not
     (1, 50, 50, 2100, 2100, 64, 100, 1200, 0, 0),  # sink tiles for three waves of CTAs
     (1, 48, 48, 1100, 1100, 64, 100, 1100, 0, 0),
 ]
@@ -119,19 +127,20 @@ def test_same_bits_every_run(bss):
         assert ((first[0].double() - again[0].double()).abs() <= bound).all()
 
 
-def test_two_streams_at_once(bss):
+@pytest.mark.parametrize("windows", [(100, 333), (800, 1100)])
+def test_two_streams_at_once(bss, windows):
     """Two calls at a time on streams of their own, with workspaces of their own."""
     a = inputs(1, 8, 2, 900, 900, 64, 1)
     b = inputs(1, 4, 4, 1200, 1200, 128, 2)
     want = []
-    for (q, k, v, do), w in ((a, 100), (b, 333)):
+    for (q, k, v, do), w in ((a, windows[0]), (b, windows[1])):
         o, lse = bss.attn_fwd_window(q, k, v, w, sinks=2)
         want.append((o, lse) + bss.attn_bwd_window(q, k, v, o, lse, do, w, sinks=2)[1:3])
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
     for _ in range(5):
         got = []
-        for st, (q, k, v, do), w in zip(streams, (a, b), (100, 333)):
+        for st, (q, k, v, do), w in zip(streams, (a, b), windows):
             with torch.cuda.stream(st):
                 o, lse = bss.attn_fwd_window(q, k, v, w, sinks=2)
                 got.append((o, lse) + bss.attn_bwd_window(q, k, v, o, lse, do, w, sinks=2)[1:3])

@@ -944,28 +944,40 @@ __global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBw
     if (lane == 0) p.delta[r] = s;
   }
   if (takes_few) return;
+  // kRows rows at a time, so that their loads are in flight together; a thread
+  // clears its own 8 columns of the accumulator behind them
+  constexpr int kRows = 2;
   const long long step = nthreads / G;
   const int step_row = static_cast<int>(step % p.Lq);
   int row = static_cast<int>(tid / G % p.Lq);        // r % Lq, kept beside r
-  for (long long r = tid / G;; r += step) {
-    const bool active = r < rows;
-    if (__all_sync(0xFFFFFFFFu, !active)) break;     // every lane of the warp is done
-    uint4 o = make_uint4(0u, 0u, 0u, 0u), d = o;
-    bool few = false;
-    if (active) {
-      o = __ldg(reinterpret_cast<const uint4*>(p.o + r * D) + g);
-      d = __ldg(reinterpret_cast<const uint4*>(p.dout + r * D) + g);
-      few = (row < fr.first || row >= fr.late) && fr.has(window_row_keys(p, row), row);
-    }
-    float s = dot8(o, d, 0.f);
+  for (long long r0 = tid / G;; r0 += kRows * step) {
+    if (__all_sync(0xFFFFFFFFu, r0 >= rows)) break;  // every lane of the warp is done
+    uint4 o[kRows], d[kRows];
 #pragma unroll
-    for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off, G);
-    if (active && g == 0 && !few) p.delta[r] = s;
-    row += step_row - (row >= p.Lq - step_row ? p.Lq : 0);
+    for (int u = 0; u < kRows; ++u) {
+      const long long r = r0 + u * step;
+      o[u] = d[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        o[u] = __ldg(reinterpret_cast<const uint4*>(p.o + r * D) + g);
+        d[u] = __ldg(reinterpret_cast<const uint4*>(p.dout + r * D) + g);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const long long r = r0 + u * step;
+      const bool active = r < rows;
+      if (active) {
+        float4* acc = reinterpret_cast<float4*>(p.dq_acc + r * D + g * 8);
+        acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      const bool few = active && (row < fr.first || row >= fr.late) && fr.has(window_row_keys(p, row), row);
+      float s = dot8(o[u], d[u], 0.f);
+#pragma unroll
+      for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off, G);
+      if (active && g == 0 && !few) p.delta[r] = s;
+      row += step_row - (row >= p.Lq - step_row ? p.Lq : 0);
+    }
   }
-  float4* acc = reinterpret_cast<float4*>(p.dq_acc);
-  const long long n4 = rows * D / 4;
-  for (long long x = tid; x < n4; x += nthreads) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // dQ (bf16) from the fp32 accumulator (the scale was applied to dS already),

@@ -9,6 +9,7 @@ in them is found on the device: ``attn_poll_status`` then returns ``ERR_BAD_PAGE
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -24,6 +25,12 @@ _INT, _BF16, _FP32, _E4M3 = torch.int32, torch.bfloat16, torch.float32, torch.fl
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int):
     """(k address, v address, k page stride, v page stride, dtype code) of a checked cache."""
     kind, shape = k_cache.dtype, k_cache.shape
+    if (v_cache.dtype is kind and v_cache.shape == shape and (kind is _BF16 or kind is _E4M3)
+            and len(shape) == 4 and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_cache.get_device() == dev and v_cache.get_device() == dev and dev >= 0):
+        page = shape[1] * shape[2] * shape[3]
+        return (k_cache.data_ptr(), v_cache.data_ptr(), page, page,
+                KV_BF16 if kind is _BF16 else KV_E4M3)
     if kind is not _BF16 and kind is not _E4M3:
         raise ValueError(f"k_cache must be torch.bfloat16 or torch.float8_e4m3fn, got {kind}")
     if len(shape) != 4:
@@ -59,9 +66,9 @@ def _scales(code: int, k_scale, v_scale, Hkv: int, dev: int):
 
 def _table(page_table: torch.Tensor, dev: int):
     """(address, rows, max_pages) of a checked page table."""
-    if page_table.dim() != 2:
-        raise ValueError("page_table must have 2 dimensions [S, max_pages]")
     shape = page_table.shape
+    if len(shape) != 2:
+        raise ValueError("page_table must have 2 dimensions [S, max_pages]")
     return _is(page_table, "page_table", _INT, shape, dev), shape[0], shape[1]
 
 
@@ -91,6 +98,9 @@ def attn_decode_paged_workspace_bytes(S: int, H: int, H_kv: int, d: int, max_pag
     return int(_lib.load().attn_decode_paged_workspace_bytes(S, H, H_kv, d, max_pages, page_size))
 
 
+_decode_bytes = functools.lru_cache(maxsize=256)(attn_decode_paged_workspace_bytes)
+
+
 def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int = 0,
                       sinks: int = 0, scale: Optional[float] = None, k_scale=None, v_scale=None,
                       workspace: Optional[torch.Tensor] = None, out=None, lse=None):
@@ -103,9 +113,10 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int 
     dev = q.get_device()
     kp, vp, ks, vs, code = _cache(k_cache, v_cache, dev)
     P, Hkv, page, d = k_cache.shape
-    if q.dim() != 3:
+    q_shape = q.shape
+    if len(q_shape) != 3:
         raise ValueError("q must have 3 dimensions [S, H, d]")
-    S, H = q.shape[0], q.shape[1]
+    S, H, _ = q_shape
     q_stride = _rows(q, "q", (S, H, d), dev)
     ksp, vsp = _scales(code, k_scale, v_scale, Hkv, dev)
     tp, rows, M = _table(page_table, dev)
@@ -116,7 +127,7 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int 
     lse, ep = _out(lse, "lse", _FP32, (S, H), q)
     wp, nbytes = None, 0
     if workspace is None:
-        nbytes = attn_decode_paged_workspace_bytes(S, H, Hkv, d, M, page)
+        nbytes = _decode_bytes(S, H, Hkv, d, M, page)
     if workspace is not None or nbytes:       # small calls need none
         workspace = _workspace(workspace, nbytes, q)
         wp, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

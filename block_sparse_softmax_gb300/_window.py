@@ -1,6 +1,7 @@
 """Attention with a sliding window and sinks: ``attn_fwd_window`` and ``attn_bwd_window``."""
 from __future__ import annotations
 
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -11,6 +12,8 @@ from . import OK, AttnError, _lib, _need, _scale
 # a few attribute reads per tensor where all is well, and look for what is wrong only where it is
 # not.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_empty = torch.empty
 
 
 def _is(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: int) -> int:
@@ -30,7 +33,7 @@ def _run(name: str, device: int, *args) -> None:
     fn = _entry.get(name)
     if fn is None:
         fn = _entry[name] = getattr(_lib.load(), name)
-    if device == torch._C._cuda_getDevice():
+    if device == _current_device():
         st = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -42,7 +45,7 @@ def _run(name: str, device: int, *args) -> None:
 def _out(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, like: torch.Tensor):
     """(tensor, address) of an output: the caller's, checked, or a new one on ``like``'s device."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = _empty(shape, dtype=dtype, device=like.device)
         return t, t.data_ptr()
     return t, _is(t, name, dtype, shape, like.get_device())
 
@@ -50,7 +53,7 @@ def _out(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, like: 
 def _workspace(workspace: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> torch.Tensor:
     """The caller's workspace, checked, or a new one of ``nbytes``."""
     if workspace is None:
-        return torch.empty(max(16, nbytes), dtype=torch.uint8, device=like.device)
+        return _empty(max(16, nbytes), dtype=torch.uint8, device=like.device)
     if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
     return workspace
@@ -86,6 +89,9 @@ def attn_bwd_window_workspace_bytes(B: int, H: int, H_kv: int, Lq: int, Lk: int,
                                                            int(k_offset)))
 
 
+_bwd_bytes = functools.lru_cache(maxsize=256)(attn_bwd_window_workspace_bytes)
+
+
 def attn_bwd_window(q, k, v, o, lse, dout, window: int, *, sinks: int = 0,
                     scale: Optional[float] = None, q_offset: int = 0, k_offset: int = 0,
                     workspace: Optional[torch.Tensor] = None, dq=None, dk=None, dv=None,
@@ -106,7 +112,7 @@ def attn_bwd_window(q, k, v, o, lse, dout, window: int, *, sinks: int = 0,
     dv, dvp = _out(dv, "dv", bf16, k_shape, q)
     delta, dep = _out(delta, "delta", fp32, rows, q)
     window, sinks, q_offset, k_offset = int(window), int(sinks), int(q_offset), int(k_offset)
-    ws = _workspace(workspace, 0 if workspace is not None else attn_bwd_window_workspace_bytes(
+    ws = _workspace(workspace, 0 if workspace is not None else _bwd_bytes(
         B, H, Hkv, Lq, Lk, d, window, sinks, q_offset, k_offset), q)
     _run("attn_bwd_window", dev, qp, kp, vp, op, lp, dop, dqp, dkp, dvp, dep, ws.data_ptr(),
          ws.numel() * ws.element_size(), B, H, Hkv, Lq, Lk, d, _scale(scale, d), window, sinks,

@@ -33,6 +33,14 @@ namespace {
 constexpr int kFewKeys = 64;
 constexpr int kFewWindow = 32;
 
+// Key tiles j0 .. j0 + n - 1 of every K/V head, their walks cut into `seg`
+// segments each; their first item, and the workspace slot of its part (cut
+// walks).
+struct WindowTiles {
+  int j0, n, seg;
+  int item0, slot0;
+};
+
 struct WindowBwdParams {
   const __nv_bfloat16* q;
   const __nv_bfloat16* k;
@@ -51,7 +59,7 @@ struct WindowBwdParams {
   float* part;          // fp32 [slot][dK, dV][128][d]: parts of the cut walks
   int nk;               // key tiles
   int nst;              // the first of them, which hold a sink key
-  int seg_s, seg_w;     // segments of a sink tile's walk and of another tile's
+  WindowTiles tiles[2]; // those, and the others, in the order of their items
   int n_items;          // key tiles, or segments of them, over all heads
   int* err;
 };
@@ -145,34 +153,23 @@ struct WinBwdRegs {
 };
 
 
-// Item x: the sink tiles' segments first (each at least as long as any other
-// walk), then the other key tiles with the K/V heads side by side, so that the
-// running CTAs' Q, dO and dQ accumulator stay in L2.
+// Item x: a segment of a key tile's walk; the K/V heads of a tile come side by
+// side, so that the running CTAs' Q, dO and dQ accumulator stay in L2.
 struct WindowBwdCta {
   int bh, j, seg, nseg, slot;
 };
 __device__ __forceinline__ WindowBwdCta window_bwd_cta(int x, const WindowBwdParams& p) {
-  WindowBwdCta c;
+  const WindowTiles& t = x >= p.tiles[1].item0 ? p.tiles[1] : p.tiles[0];
   const int BH = p.B * p.Hkv;
-  const int n_sink = BH * p.nst * p.seg_s;
-  if (x < n_sink) {
-    c.nseg = p.seg_s;
-    c.slot = x;
-    c.seg = x % p.seg_s;
-    const int t = x / p.seg_s;
-    c.bh = t / p.nst;
-    c.j = t - c.bh * p.nst;
-    return c;
-  }
-  const int y = x - n_sink;
-  const int n = p.nk - p.nst;
-  c.nseg = p.seg_w;
-  c.seg = y % p.seg_w;
-  const int z = y / p.seg_w;
+  const int y = x - t.item0;
+  WindowBwdCta c;
+  c.nseg = t.seg;
+  c.slot = t.slot0 + y;
+  const int z = y / t.seg;
+  c.seg = y - z * t.seg;
   const int jj = z / BH;
   c.bh = z - jj * BH;
-  c.j = p.nst + jj;
-  c.slot = (p.seg_s > 1 ? n_sink : 0) + (c.bh * n + jj) * p.seg_w + c.seg;
+  c.j = t.j0 + jj;
   return c;
 }
 
@@ -999,54 +996,47 @@ __global__ void __launch_bounds__(256) attn_bwd_window_post_kernel(const WindowB
   }
   // one thread per 4 columns of a row of dK or dV of a cut tile
   const int BH = p.B * p.Hkv;
-  const int cut_s = p.seg_s > 1 ? p.nst : 0;                 // cut tiles per K/V head
-  const int cut_w = p.seg_w > 1 ? p.nk - p.nst : 0;
   const long long per_tile = 2ll * kTileN * D / 4;
-  const long long n = static_cast<long long>(BH) * (cut_s + cut_w) * per_tile;
-  for (long long x = tid; x < n; x += nthreads) {
-    const long long t = x / per_tile;
-    const int e = static_cast<int>(x - t * per_tile);
-    int bh, j, nseg;
-    long long slot;
-    if (t < static_cast<long long>(BH) * cut_s) {
-      bh = static_cast<int>(t / p.nst);
-      j = static_cast<int>(t - static_cast<long long>(bh) * p.nst);
-      nseg = p.seg_s;
-      slot = t * nseg;
-    } else {
-      const long long u = t - static_cast<long long>(BH) * cut_s;
-      const int nn = p.nk - p.nst;
-      bh = static_cast<int>(u / nn);
-      j = p.nst + static_cast<int>(u - static_cast<long long>(bh) * nn);
-      nseg = p.seg_w;
-      slot = static_cast<long long>(BH) * cut_s * p.seg_s + u * nseg;
+  for (int c = 0; c < 2; ++c) {
+    const WindowTiles t = p.tiles[c];
+    if (t.seg == 1) continue;
+    const long long n = static_cast<long long>(BH) * t.n * per_tile;
+    for (long long x = tid; x < n; x += nthreads) {
+      const int z = static_cast<int>(x / per_tile);            // tile and K/V head, as in the items
+      const int e = static_cast<int>(x - z * per_tile);
+      const int jj = z / BH;
+      const int bh = z - jj * BH;
+      const int j = t.j0 + jj;
+      const int nseg = t.seg;
+      const long long slot = t.slot0 + static_cast<long long>(z) * nseg;
+      const int which = e / (kTileN * D / 4);                  // 0: dK, 1: dV
+      const int rest = e - which * (kTileN * D / 4);
+      const int r = rest / (D / 4);
+      const int c4 = rest - r * (D / 4);
+      const int key = j * kTileN + r;
+      if (key >= p.Lk) continue;
+      const float4* src = reinterpret_cast<const float4*>(p.part) +
+                          (static_cast<size_t>(slot) * 2 + which) * (kTileN * D / 4) + rest;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < nseg; ++i) {
+        const float4 a = __ldg(src + static_cast<size_t>(i) * 2 * (kTileN * D / 4));
+        s.x += a.x;
+        s.y += a.y;
+        s.z += a.z;
+        s.w += a.w;
+      }
+      uint2 w;
+      w.x = pack_bf16(s.x, s.y);
+      w.y = pack_bf16(s.z, s.w);
+      *(reinterpret_cast<uint2*>((which ? p.dv : p.dk) + (static_cast<size_t>(bh) * p.Lk + key) * D) + c4) = w;
     }
-    const int which = e / (kTileN * D / 4);                  // 0: dK, 1: dV
-    const int rest = e - which * (kTileN * D / 4);
-    const int r = rest / (D / 4);
-    const int c4 = rest - r * (D / 4);
-    const int key = j * kTileN + r;
-    if (key >= p.Lk) continue;
-    const float4* src = reinterpret_cast<const float4*>(p.part) +
-                        (static_cast<size_t>(slot) * 2 + which) * (kTileN * D / 4) + rest;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < nseg; ++i) {
-      const float4 a = __ldg(src + static_cast<size_t>(i) * 2 * (kTileN * D / 4));
-      s.x += a.x;
-      s.y += a.y;
-      s.z += a.z;
-      s.w += a.w;
-    }
-    uint2 w;
-    w.x = pack_bf16(s.x, s.y);
-    w.y = pack_bf16(s.z, s.w);
-    *(reinterpret_cast<uint2*>((which ? p.dv : p.dk) + (static_cast<size_t>(bh) * p.Lk + key) * D) + c4) = w;
   }
 }
 
 // How the walks are cut, and where the parts go.
 struct WindowBwdPlan {
-  int nk, nst, seg_s, seg_w;
+  int nk, nst;
+  WindowTiles tiles[2];
   long long slots, n_cta;
   bool persistent;
   size_t part_off, bytes;
@@ -1060,27 +1050,36 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   // query tiles that a tile without sinks meets at most, over its heads
   const long long share = std::min(nq, std::min<long long>(w.window, 1ll << 40) / kTileM + 2) * G;
   const long long rest = pl.nk - pl.nst;
-  pl.seg_w = 1;
+  long long seg_w = 1;
   // too few key tiles for the 152 SMs: cut every walk so that the CTAs make a wave
   const long long tiles = BH * (rest > 0 ? rest : 1);
-  if (tiles < 152) pl.seg_w = static_cast<int>(std::max(1ll, std::min(share, 152 / tiles)));
-  // a sink tile meets up to nq tiles a head: segments as long as the others'
-  // walks, but of at least 8 tiles (a part costs as much memory as 2 tiles)
-  const long long each = std::max(8ll, (share + pl.seg_w - 1) / pl.seg_w);
-  pl.seg_s = static_cast<int>(std::max(1ll, (nq * G + each - 1) / each));
-  // ... and no more of them than 8 an SM: many sink tiles fill the GPU uncut,
-  // and their parts would take more memory than everything else (16384 sinks
-  // of 16384 keys, 32 heads, d=128: 8.6 GB)
-  if (pl.nst > 0) pl.seg_s = static_cast<int>(std::max(1ll, std::min<long long>(pl.seg_s, 152 * 8 / (BH * pl.nst))));
-  else pl.seg_s = 1;
+  if (tiles < 152) seg_w = std::max(1ll, std::min(share, 152 / tiles));
   // A CTA an SM that takes items by a fixed stride saves an item's set-up
   // (5-8 % over walks of up to 12 tiles); over longer walks, whose lengths
   // differ more, a CTA an item is balanced better by the hardware (equal at 17
   // to 36 tiles, 10 % better at 68: B2 H16(4) L8192, windows of 64 to 8192).
-  pl.persistent = share <= 20ll * pl.seg_w;
-  pl.n_cta = BH * (static_cast<long long>(pl.nst) * pl.seg_s + rest * pl.seg_w);
-  pl.slots = BH * ((pl.seg_s > 1 ? static_cast<long long>(pl.nst) * pl.seg_s : 0) +
-                   (pl.seg_w > 1 ? rest * pl.seg_w : 0));
+  pl.persistent = share <= 20 * seg_w;
+  // a sink tile meets up to nq tiles a head: segments as long as the others'
+  // walks, but of at least 8 tiles (a part costs as much memory as 2 tiles)
+  const long long each = std::max(8ll, (share + seg_w - 1) / seg_w);
+  long long seg_s = std::max(1ll, (nq * G + each - 1) / each);
+  // ... and no more of them than 8 an SM: many sink tiles fill the GPU uncut,
+  // and their parts would take more memory than everything else (16384 sinks
+  // of 16384 keys, 32 heads, d=128: 8.6 GB)
+  if (pl.nst > 0) seg_s = std::max(1ll, std::min(seg_s, 152 * 8 / (BH * pl.nst)));
+  // The segments of the sink tiles come first: with the last tiles' whole walks
+  // they would end late (B1 H16(4) L16384 d128, window 1024, sinks 4: 17 us of
+  // 395 more).  Cutting the walks of a last wave that leaves SMs idle into four
+  // cost more than it gave there (104 items of 40 tiles on 152 SMs: 6 us more).
+  pl.tiles[0] = WindowTiles{0, pl.nst, static_cast<int>(seg_s), 0, 0};
+  pl.tiles[1] = WindowTiles{pl.nst, static_cast<int>(rest), static_cast<int>(seg_w), 0, 0};
+  for (WindowTiles& t : pl.tiles) {
+    if (t.n == 0) t.seg = 1;
+    t.item0 = static_cast<int>(std::min(pl.n_cta, 0x7FFFFFFFll));       // (a launch that passes it is refused)
+    t.slot0 = static_cast<int>(std::min(pl.slots, 0x7FFFFFFFll));
+    pl.n_cta += BH * t.n * t.seg;
+    if (t.seg > 1) pl.slots += BH * t.n * t.seg;
+  }
   pl.part_off = (static_cast<size_t>(B) * H * Lq * d * 4 + 255) & ~static_cast<size_t>(255);
   pl.bytes = pl.part_off + static_cast<size_t>(pl.slots) * 2 * kTileN * d * 4;
   return pl;
@@ -1209,8 +1208,7 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.part_off);
   p.nk = pl.nk;
   p.nst = pl.nst;
-  p.seg_s = pl.seg_s;
-  p.seg_w = pl.seg_w;
+  for (int i = 0; i < 2; ++i) p.tiles[i] = pl.tiles[i];
   p.n_items = static_cast<int>(pl.n_cta);
   return cuda_status("attn_bwd_window launch",
                      d == 64 ? launch_window_bwd<64>(tq, tk, tv, tdo, tdq, p, pl.n_cta, pl.persistent, st)

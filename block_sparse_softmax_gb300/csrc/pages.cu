@@ -361,26 +361,42 @@ __global__ void __launch_bounds__(kBookThreads) kv_compact_kernel(int* refs, int
     n_dst += static_cast<int>(total & 0xFFFFu);
   }
   __syncthreads();
-#pragma unroll 4
-  for (int i = tid; i < P; i += kBookThreads) {
-    if (i < n_src) {
-      const int a = copy_src[i], b = copy_dst[i];
-      refs[b] = refs[a];
-      refs[a] = 0;
-      if (entries > 0) to[a] = b;
-    } else {
-      copy_src[i] = -1;
-      copy_dst[i] = -1;
+  // a batch's loads are in flight together (one CTA: latency is what counts)
+  constexpr int kBatch = 8;
+  for (int i0 = tid; i0 < n_src; i0 += kBatch * kBookThreads) {
+    int a[kBatch], b[kBatch], held[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kBookThreads;
+      a[u] = i < n_src ? copy_src[i] : -1;
+      b[u] = i < n_src ? copy_dst[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) held[u] = a[u] >= 0 ? refs[a[u]] : 0;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (a[u] < 0) continue;
+      refs[b[u]] = held[u];
+      refs[a[u]] = 0;
+      if (entries > 0) to[a[u]] = b[u];
     }
   }
+  for (int i = n_src + tid; i < P; i += kBookThreads) copy_src[i] = copy_dst[i] = -1;
   if (tid == 0) *count = n_src;
   if (entries == 0) return;
   __syncthreads();
-#pragma unroll 4
-  for (int i = tid; i < entries; i += kBookThreads) {
-    const int e = table[i];
-    if (e >= P) record_error(err, ATTN_ERR_BAD_PAGES);
-    else if (e >= 0 && to[e] >= 0) table[i] = to[e];
+  for (int i0 = tid; i0 < entries; i0 += kBatch * kBookThreads) {
+    int e[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kBookThreads;
+      e[u] = i < entries ? table[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (e[u] >= P) record_error(err, ATTN_ERR_BAD_PAGES);
+      else if (e[u] >= 0 && to[e[u]] >= 0) table[i0 + u * kBookThreads] = to[e[u]];
+    }
   }
 }
 

@@ -63,9 +63,15 @@ __device__ __forceinline__ WindowBlocks window_blocks(const WindowMask& w, int r
   return b;
 }
 
-// The lowest n bits (n may lie outside [0, 32]).
+// The lowest n bits (n may lie outside [0, 32]; shl.b32 gives 0 from 32 on).
 __device__ __forceinline__ uint32_t bits_below(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+  uint32_t x;
+  asm("shl.b32 %0, 1, %1;" : "=r"(x) : "r"(max(n, 0)));
+  return x - 1u;
+}
+// x as an int, where what lies outside [lo, hi] may as well lie on its border.
+__device__ __forceinline__ int clamped(long long x, int lo, int hi) {
+  return static_cast<int>(max(static_cast<long long>(lo), min(x, static_cast<long long>(hi))));
 }
 
 // The mask of a launch with Lk keys; false for window < 1 or a negative argument (window_fwd.cu).

@@ -620,10 +620,11 @@ __global__ void __launch_bounds__(512, 1)
         const bool edge = none || kstart + kTileN > p.Lk || kTileN - 1 > diag0 ||
                           (diag0 + kTileM - 1 - p.w.window + 1 > 0 && kstart + kTileN > p.w.snk);
         if (edge) {
-          const long long dg = diag0 + row_in_tile;
-          const int jhi = none ? -1 : static_cast<int>(max(-1ll, min(dg, static_cast<long long>(p.Lk) - 1 - kstart)));
-          const int jlo = static_cast<int>(max(0ll, min(128ll, dg - p.w.window + 1)));
-          const int js = max(0, p.w.snk - kstart);
+          // (64 bits for the whole warp, 32 for a row: a first row's key outside
+          // the block by a tile or more masks the same whatever the distance)
+          const int jhi = none ? -1 : min(clamped(diag0, -kTileM - 1, kTileN) + row_in_tile, p.Lk - 1 - kstart);
+          const int jlo = clamped(diag0 - p.w.window + 1, -kTileM, kTileN) + row_in_tile;
+          const int js = p.w.snk - kstart;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t bits = bits_below(jhi + 1 - 32 * c) & (~bits_below(jlo - 32 * c) | bits_below(js - 32 * c));

@@ -26,8 +26,8 @@ bool valid_kv_heads(int H, int Hkv);
 // Events of attn_bwd_time_main (both nullptr when off).
 void bwd_main_events(cudaEvent_t* begin, cudaEvent_t* end);
 
-// Tokens of a sequence in a paged cache: a step of keys past the last one still
-// counts in 32 bits.
+// Rows of a windowed call, tokens of a sequence in a paged cache: a tile past
+// the last one still counts in 32 bits.
 constexpr int kMaxTokens = 0x7FFFFF00;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

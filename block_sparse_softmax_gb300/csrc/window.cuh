@@ -44,20 +44,34 @@ struct WindowBlocks {
   }
 };
 
-__device__ __forceinline__ WindowBlocks window_blocks(const WindowMask& w, int r0, int Lq, int Lk) {
+// x as an int, where what lies outside [lo, hi] may as well lie on its border.
+__device__ __forceinline__ int clamped(long long x, int lo, int hi) {
+  return static_cast<int>(max(static_cast<long long>(lo), min(x, static_cast<long long>(hi))));
+}
+
+// The keys of a query tile: row r of it sees those from lo + r on up to own + r
+// (and sinks).  Limits before the first key or past the last one by more than a
+// tile's rows are taken as there: 32 bits do, and the softmax warps' 64-bit
+// arithmetic cost 4 %.
+struct WindowRows {
+  int own, lo;
+};
+__device__ __forceinline__ WindowRows window_rows(const WindowMask& w, int r0, int Lk) {
+  const long long own = static_cast<long long>(r0) + w.sh;
+  return WindowRows{clamped(own, -kTileM, Lk), clamped(own - w.window + 1, -kTileM, Lk)};
+}
+
+__device__ __forceinline__ WindowBlocks window_blocks(const WindowRows& t, int snk, int rows, int Lk) {
   WindowBlocks b{0, 0, 0, 0};
-  if (r0 >= Lq || Lk <= 0) return b;
-  const long long last = static_cast<long long>(min(r0 + kTileM, Lq) - 1) + w.sh;   // last row's own key
-  if (last < 0) return b;
-  const int kmax = static_cast<int>(min(last, static_cast<long long>(Lk) - 1));
-  const long long lo = max(0ll, static_cast<long long>(r0) + w.sh - w.window + 1);
-  const int s_end = min(w.snk, kmax + 1);
-  const int sink_blocks = (s_end + kTileN - 1) / kTileN;
+  const int kmax = min(t.own + rows, Lk) - 1;      // the last row's own key, or the last there is
+  if (rows <= 0 || kmax < 0) return b;
+  const int lo = max(t.lo, 0);
+  const int sink_blocks = (min(snk, kmax + 1) + kTileN - 1) / kTileN;
   if (lo > kmax) {               // the window lies past the last key: sinks alone
     b.nsb = sink_blocks;
     return b;
   }
-  b.wb0 = static_cast<int>(lo / kTileN);
+  b.wb0 = lo / kTileN;
   b.nwb = kmax / kTileN - b.wb0 + 1;
   b.nsb = min(sink_blocks, b.wb0);
   return b;
@@ -69,11 +83,6 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   asm("shl.b32 %0, 1, %1;" : "=r"(x) : "r"(max(n, 0)));
   return x - 1u;
 }
-// x as an int, where what lies outside [lo, hi] may as well lie on its border.
-__device__ __forceinline__ int clamped(long long x, int lo, int hi) {
-  return static_cast<int>(max(static_cast<long long>(lo), min(x, static_cast<long long>(hi))));
-}
-
 // The mask of a launch with Lk keys; false for window < 1 or a negative argument (window_fwd.cu).
 bool window_mask(WindowMask* w, int Lk, int64_t window, int64_t sinks, int64_t q_offset,
                  int64_t k_offset);

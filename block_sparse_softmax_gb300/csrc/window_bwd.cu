@@ -550,11 +550,12 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     int n = 0;                 // query tiles done (over all items)
     int kv = 0;                // items with query tiles done
     for (int x = static_cast<int>(blockIdx.x); x < p.n_items && ok; x += static_cast<int>(gridDim.x)) {
-    int key, n_it;
+    int key0, key, n_it;         // the tile's first key, this thread's
     {
     const WindowBwdCta cta = window_bwd_cta(x, p);
     const WindowQWalk walk = window_bwd_walk(cta, p);
-    key = cta.j * kTileN + kr;
+    key0 = cta.j * kTileN;
+    key = key0 + kr;
     n_it = walk.n_it;
     const int bhq0 = (cta.bh / p.Hkv) * p.H + (cta.bh % p.Hkv) * G;   // first query head of the group
     int g, i;
@@ -585,9 +586,10 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
       // (query >= Lq) has -lse2 = -inf, so P is 0 there already
       uint32_t seen[2];
       {
-        const long long own = static_cast<long long>(key) - p.w.sh - static_cast<long long>(i) * kTileM - 64 * X;
-        const int qlo = key < Lk ? static_cast<int>(max(0ll, min(64ll, own))) : 64;
-        const int end = key < p.w.snk ? 64 : static_cast<int>(max(0ll, min(64ll, own + p.w.window)));
+        const long long tile = static_cast<long long>(key0) - p.w.sh - static_cast<long long>(i) * kTileM;
+        const int own = clamped(tile, -kTileM, kTileM) + kr - 64 * X;
+        const int qlo = key < Lk ? own : 64;
+        const int end = key < p.w.snk ? 64 : clamped(tile + p.w.window, -kTileM, kTileM) + kr - 64 * X;
         seen[0] = bits_below(end) & ~bits_below(qlo);
         seen[1] = bits_below(end - 32) & ~bits_below(qlo - 32);
       }
@@ -1169,6 +1171,7 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   attn_status_t s = check_common(B, H, Lq, Lk, d, scale);
   if (s != ATTN_OK) return s;
   if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
+  if (Lq > kMaxTokens || Lk > kMaxTokens) return ATTN_ERR_UNSUPPORTED;
   WindowBwdParams p{};
   if (!window_mask(&p.w, Lk, window, sinks, q_offset, k_offset)) return ATTN_ERR_INVALID_ARG;
   const WindowBwdPlan pl = window_bwd_plan(B, H, H_kv, Lq, Lk, d, p.w);

@@ -133,7 +133,7 @@ __device__ __forceinline__ WindowItem window_item(int item, const WindowFwdParam
   it.h = it.bh - it.b * p.H;
   it.hkv = it.h / (p.H / p.Hkv);
   it.r0 = (n_tiles - 1 - rank) * kTileM;
-  it.kb = window_blocks(p.w, it.r0, p.Lq, p.Lk);
+  it.kb = window_blocks(window_rows(p.w, it.r0, p.Lk), p.w.snk, min(p.Lq - it.r0, kTileM), p.Lk);
   if (SPLIT) it.kb = it.kb.part(static_cast<int>(blockIdx.x) % p.split, p.split);
   return it;
 }
@@ -582,7 +582,8 @@ __global__ void __launch_bounds__(512, 1)
       // few registers are left beside the scores: of the item only its first
       // row and its blocks are kept
       const int r0 = (n_tiles - 1 - item / (p.B * p.H)) * kTileM;
-      WindowBlocks kb = window_blocks(p.w, r0, p.Lq, p.Lk);
+      const WindowRows t = window_rows(p.w, r0, p.Lk);
+      WindowBlocks kb = window_blocks(t, p.w.snk, min(p.Lq - r0, kTileM), p.Lk);
       if (SPLIT) kb = kb.part(static_cast<int>(blockIdx.x) % p.split, p.split);
       const int nb = kb.count();
       if (nb == 0) {
@@ -616,14 +617,13 @@ __global__ void __launch_bounds__(512, 1)
         // row (j <= jhi: diagonal and last key; j >= jlo: window; j < js:
         // sinks).  Most groups of an edge block are allowed or masked as a
         // whole for the warp's 32 rows; only the others go element by element
-        const long long diag0 = static_cast<long long>(r0) + p.w.sh - kstart;   // first row's own key
+        const int diag0 = t.own - kstart;           // first row's own key
+        const int low0 = t.lo - kstart;             // the first one its window holds
         const bool edge = none || kstart + kTileN > p.Lk || kTileN - 1 > diag0 ||
-                          (diag0 + kTileM - 1 - p.w.window + 1 > 0 && kstart + kTileN > p.w.snk);
+                          (low0 + kTileM - 1 > 0 && kstart + kTileN > p.w.snk);
         if (edge) {
-          // (64 bits for the whole warp, 32 for a row: a first row's key outside
-          // the block by a tile or more masks the same whatever the distance)
-          const int jhi = none ? -1 : min(clamped(diag0, -kTileM - 1, kTileN) + row_in_tile, p.Lk - 1 - kstart);
-          const int jlo = clamped(diag0 - p.w.window + 1, -kTileM, kTileN) + row_in_tile;
+          const int jhi = none ? -1 : min(diag0 + row_in_tile, p.Lk - 1 - kstart);
+          const int jlo = low0 + row_in_tile;
           const int js = p.w.snk - kstart;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -912,6 +912,7 @@ extern "C" attn_status_t attn_fwd_window(const void* q, const void* k, const voi
   attn_status_t s = check_common(B, H, Lq, Lk, d, scale);
   if (s != ATTN_OK) return s;
   if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
+  if (Lq > kMaxTokens || Lk > kMaxTokens) return ATTN_ERR_UNSUPPORTED;
   WindowFwdParams p{};
   if (!window_mask(&p.w, Lk, window, sinks, q_offset, k_offset)) return ATTN_ERR_INVALID_ARG;
   if (Lq == 0) return ATTN_OK;

@@ -30,6 +30,7 @@ def test_window_forward(lib):
                 dict(Lq=-1), dict(Lk=-1), dict(scale=0.0), dict(scale=float("inf")), dict(window=0),
                 dict(window=-5), dict(sinks=-1), dict(qo=-1), dict(ko=-1)):
         assert call(**bad) == INVALID, bad
+    assert call(Lk=2 ** 31 - 1) == call(Lq=2 ** 31 - 1) == UNSUPPORTED
     assert call(Lq=0, q=None, o=None, lse=None) == 0      # nothing to do
 
 

@@ -578,10 +578,19 @@ __global__ void __launch_bounds__(512, 1)
       ++nx;
       return w;
     };
-    for (int item = window_first<SPLIT>(p); item < p.n_items; item += window_stride<SPLIT>(p)) {
-      // few registers are left beside the scores: of the item only its first
-      // row and its blocks are kept
-      const int r0 = (n_tiles - 1 - item / (p.B * p.H)) * kTileM;
+    // the items again, as query tiles (from the last one up) and heads, stepped
+    // through without a division
+    const int BH = p.B * p.H;
+    int rank = window_first<SPLIT>(p) / BH;
+    int bh = window_first<SPLIT>(p) - rank * BH;
+    const int d_rank = SPLIT ? n_tiles : static_cast<int>(gridDim.x) / BH;
+    const int d_bh = SPLIT ? 0 : static_cast<int>(gridDim.x) - d_rank * BH;
+    for (; rank < n_tiles; rank += d_rank, bh += d_bh) {
+      if (bh >= BH) {
+        bh -= BH;
+        if (++rank >= n_tiles) break;
+      }
+      const int r0 = (n_tiles - 1 - rank) * kTileM;
       const WindowRows t = window_rows(p.w, r0, p.Lk);
       WindowBlocks kb = window_blocks(t, p.w.snk, min(p.Lq - r0, kTileM), p.Lk);
       if (SPLIT) kb = kb.part(static_cast<int>(blockIdx.x) % p.split, p.split);
@@ -758,10 +767,8 @@ __global__ void __launch_bounds__(512, 1)
         inv_s[row_in_tile] = lt == 0.f ? 0.f : 1.f / lt;
         mbar_arrive(bar(C::kBarLFull));
         const int row = r0 + row_in_tile;
-        int it = item;
-        asm volatile("" : "+r"(it));        // the head again from the item, rather than kept
         if (row < p.Lq)
-          p.lse[static_cast<size_t>(it % (p.B * p.H)) * p.Lq + row] =
+          p.lse[static_cast<size_t>(bh) * p.Lq + row] =
               lt == 0.f ? NEG_INF : (m2 + __log2f(lt)) * kLn2;
       }
       ++on;

@@ -25,7 +25,7 @@
 // (rounding them alone costs 1.7e-3).
 //
 // Measured, B1 H16(4) L16384 d128, window 1024, sinks 4: D and clearing 40 us
-// (HBM: 268 MB), main kernel 394 us (848 TFLOP/s of allowed pairs), dQ 27 us
+// (HBM: 268 MB), main kernel 391 us (855 TFLOP/s of allowed pairs), dQ 27 us
 // (HBM: 201 MB, part of it from L2).  What sets the main kernel's pace is the
 // chain of hand-offs of a query tile, dQ -> drain -> dP^T -> dS -> dQ, as in
 // the dense backward (tensor pipe 48 % busy while an SM has a CTA), and an

@@ -26,12 +26,13 @@
 //           O while the softmax works on the next item.
 // With the softmax warps writing O themselves an item of one pair took 12000
 // cycles and every further pair 3100: 410 us for B2 H16(4) L16384 d128, window
-// 1024, sinks 4.  So it takes 309 us: 866 TFLOP/s of allowed pairs, 1080 of
-// executed blocks (57 % of a large bf16 product's).  An item's 20700 cycles are
-// 14300 of MMAs (5 pairs); its two masked steps take 1600 and 900 more than a
-// plain one (3200), and the next item's Q comes 1500 late, after the last S
-// has freed its buffer (shared memory holds one at d=128; prefetching it into
-// L2 made everything 3 to 5 % slower).
+// 1024, sinks 4.  So it takes 287 us: 930 TFLOP/s of allowed pairs, 1160 of
+// executed blocks (61 % of a large bf16 product's).  An item's 20400 cycles are
+// 14300 of MMAs (5 pairs); a plain step takes 3300, the two masked ones 1200
+// and 600 more (with 64-bit limits in every row 1600 and 900: 310 us), an
+// item's end 1300, and the next item's Q comes late, after the last S has freed
+// its buffer (shared memory holds one at d=128; prefetching it into L2 made
+// everything 3 to 5 % slower).
 //
 // Where a launch has few items, a cluster of CTAs shares one (window_split).
 //

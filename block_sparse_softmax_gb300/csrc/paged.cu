@@ -34,6 +34,10 @@
 //     same two heads as its softmax state.  (tcgen05 tiles have at least 64
 //     rows and would be fed through shared memory twice; these products take a
 //     tenth of the time the bytes do.)
+//   * Over bf16 pages P enters its product in two bf16 parts, which together
+//     hold all but 2^-15 of it: one part alone put 1.4e-3 (in norm) on top of
+//     O's own rounding of 1.65e-3.  The bytes leave room for the second
+//     product: within 0.3 % on the first and third line below, 1 % on the last.
 //   * e4m3 pages are read as they are (half the bytes); a pair of elements
 //     becomes fp16 by one conversion, exactly, on the way into an fp16 MMA.
 //     (Going on to bf16 takes four instructions: 128 sequences of up to 16384
@@ -218,6 +222,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// A number in [0, 1] as two bf16 ones: its high half cut off (a pair of them
+// packed), and the rest, of which bf16 holds all but 2^-15 of the number.  The
+// rest is kept above 0: 0 times an infinity in V would turn it into a NaN.
+__device__ __forceinline__ uint32_t high_bf16(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float rest_bf16(float x) {
+  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u), 1.17549435e-38f);
 }
 
 // The running state of a unit in one warp: A^T fragments, and for the thread's
@@ -663,6 +677,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
       }
       // ---- mask and online softmax; rows g and g + 8 of a tile are its keys ----
       uint32_t pb[C::kRowTiles][NT][2];
+      uint32_t pb_lo[FP8 ? 1 : C::kRowTiles][NT][2];      // bf16 pages: P's remainders
 #pragma unroll
       for (int n8 = 0; n8 < NT; ++n8) {
         float al[2];
@@ -710,8 +725,15 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
         // P^T as the B operand: rows (keys) become the pairs of a thread
 #pragma unroll
         for (int m = 0; m < C::kRowTiles; ++m) {
-          pb[m][n8][0] = movm(FP8 ? pack_f16(pr[m][0], pr[m][1]) : pack_bf16(pr[m][0], pr[m][1]));
-          pb[m][n8][1] = movm(FP8 ? pack_f16(pr[m][2], pr[m][3]) : pack_bf16(pr[m][2], pr[m][3]));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if constexpr (FP8) {
+              pb[m][n8][u] = movm(pack_f16(pr[m][2 * u], pr[m][2 * u + 1]));
+            } else {
+              pb[m][n8][u] = movm(high_bf16(pr[m][2 * u], pr[m][2 * u + 1]));
+              pb_lo[m][n8][u] = movm(pack_bf16(rest_bf16(pr[m][2 * u]), rest_bf16(pr[m][2 * u + 1])));
+            }
+          }
         }
       }
       // ---- A^T += V^T P^T ----
@@ -724,8 +746,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
             uint32_t f[4];        // keys 0-7: d 0-7, d 8-15; keys 8-15: the same
             ldsm4t(vm + dec_off<C::kRowBytes>((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)), f);
 #pragma unroll
-            for (int n8 = 0; n8 < NT; ++n8)
+            for (int n8 = 0; n8 < NT; ++n8) {
               mma16816<FP8>(a.acc[n8][i], f[0], f[1], f[2], f[3], pb[m][n8][0], pb[m][n8][1]);
+              mma16816<FP8>(a.acc[n8][i], f[0], f[1], f[2], f[3], pb_lo[m][n8][0], pb_lo[m][n8][1]);
+            }
           }
         } else {
 #pragma unroll

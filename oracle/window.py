@@ -13,7 +13,7 @@ The bounds count the roundings that such a kernel makes, each by at most half a 
           delta = scale * sum|q||k| * d * 2^-23.
   P       exp(S - LSE): relative 2 delta (score and normaliser) + 2^-19 (the exponential's and
           the logarithm's own error, and the fp32 sum of the row), and 2^-8 as an operand of P V
-          or P^T dO.
+          or P^T dO (`p_round` where a kernel holds it in more bits).
   O       sum P |v| times P's error, + 2^-8 |O| for its own rounding.
   D       dO . O with the rounded O: sum |dO| (O's error), + fp32; for rows of at most 16 keys
           sum_j P_ij dP_ij in fp32: P's error before any rounding to bf16.
@@ -52,8 +52,9 @@ def forward(q, k, v, mask, scale):
     return P @ v, torch.where(seen, lse, -math.inf), P
 
 
-def forward_bounds(q, k, v, mask, scale):
-    """(bound of O, bound of LSE) element by element."""
+def forward_bounds(q, k, v, mask, scale, p_round=BF16, sums=0.0):
+    """(bound of O, bound of LSE) element by element.  p_round: what rounding P takes off it;
+    sums: the fp32 sums over the keys, relative to sum P |v| (beside a P in bf16 they vanish)."""
     H, d = q.shape[1], q.shape[-1]
     O, lse, P = forward(q, k, v, mask, scale)
     kk = _grouped(k, H).double()
@@ -61,8 +62,9 @@ def forward_bounds(q, k, v, mask, scale):
     delta = torch.where(mask, size, 0.0).amax(-1, keepdim=True) * d * 2.0 ** -23
     spread = P @ _grouped(v, H).double().abs()
     p_rel = 2 * delta + 2.0 ** -19
-    bound_o = spread * (BF16 * (1 + p_rel) + p_rel) + O.abs() * BF16 * (1 + BF16) + spread * BF16 * (
-        BF16 + p_rel) + 1e-30
+    p_rel = p_rel + sums
+    bound_o = spread * (p_round * (1 + p_rel) + p_rel) + O.abs() * BF16 * (1 + BF16) + spread * BF16 * (
+        p_round + p_rel) + 1e-30
     bound_l = delta[..., 0] + torch.nan_to_num(lse, neginf=0.0).abs() * 2.0 ** -22 + 2.0 ** -18
     return bound_o, bound_l
 

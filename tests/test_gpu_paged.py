@@ -580,3 +580,39 @@ def test_paged_refusals(bss):
         bss.attn_decode_paged(q, c.k, c.v, c.table.repeat(1, 50), c.lens, workspace=torch.empty(64, device="cuda"))
     with pytest.raises(bss.AttnError, match="UNSUPPORTED"):
         bss.attn_kv_reserve(c.table, c.lens, ints([0] * c.k.shape[0]), ints([1]), 24)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens,H,Hkv,d,page", [([300, 1, 64], 8, 2, 128, 16), ([700, 33], 16, 1, 64, 32),
+                                               ([2100, 900], 16, 4, 64, 64), ([3000, 70], 20, 1, 128, 128)])
+def test_decode_loses_nothing_to_P(bss, lens, H, Hkv, d, page, e4m3):
+    """P enters its product in two bf16 parts (all but 2^-15 of it) over bf16 pages, in fp16 (2^-11)
+    over e4m3 ones: what is left is the rounding of O itself, and fp32 sums of a term a key, off by
+    at most 2^-23 of sum P |v| each.  Where O is small beside the values it averages, a P in bf16
+    alone is 2^-8 of sum P |v| off."""
+    c = Cache(lens, Hkv, d, page, 7 * d + page, e4m3)
+    g = torch.Generator("cuda").manual_seed(d)
+    q = torch.randn(len(lens), H, d, generator=g, device="cuda").bfloat16()
+    for columns in (0, 1100 // page):
+        c.table = torch.cat([c.table, ints([[-1] * columns] * len(lens))], 1)
+        o, _ = check_decode(bss, c, q, lens, 0, 0)
+        for s, n in enumerate(lens):
+            mask = ref.window_mask(1, n, n, 0, n - 1, 0, "cuda")
+            args = q[s].reshape(1, H, 1, d), c.k64[s][None], c.v64[s][None], mask, d ** -0.5
+            bound, _ = ref.forward_bounds(*args, p_round=2.0 ** (-11 if e4m3 else -15), sums=n * 2.0 ** -23)
+            off = (o[s].double() - ref.forward(*args)[0][0, :, 0]).abs()
+            assert (off <= bound[0, :, 0]).all(), (s, n, (off / bound[0, :, 0]).max())
+
+
+def test_decode_of_an_infinite_value(bss):
+    """An infinity among the values that are seen comes out as one, in its own column alone."""
+    c = Cache([100, 40], 2, 64, 16, 5)
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    want, _ = bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens)
+    c.v[c.table[0, 1], 1, 3, 7] = float("inf")
+    c.v[c.table[0, 2], 0, 0, 9] = -float("inf")
+    got, _ = bss.attn_decode_paged(q, c.k, c.v, c.table, c.lens)
+    want[0, 2:, 7] = float("inf")
+    want[0, :2, 9] = -float("inf")
+    assert torch.equal(got, want)
+    assert bss.attn_poll_status() == 0

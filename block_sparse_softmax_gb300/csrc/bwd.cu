@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
   const bool tr = BSS_TRACE_ON(p, blockIdx.x);
   BSS_TRACE_EV(p, tr && tid == 0, 5, 0);             // kernel entry
   (void)tr;
-  if (*reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
+  const int status = status_at_entry(p.err);
 
   // CTA order (bwd_cta_tile): heads in groups of p.head_group, key tile major
   // inside a group.  A block-sparse launch may instead read its order from
@@ -293,9 +293,17 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(status == ATTN_ERR_TIMEOUT);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (gave_up) {
+    if (tid == 0) drain_bar(bar(C::kBarKV), 0);      // K and V are on their way
+    if (warp == 0) {
+      __syncwarp();
+      tmem_dealloc(tmem, C::kTmemCols);
+    }
+    return;
+  }
   BSS_TRACE_EV(p, tr && tid == 0, 5, 1);             // set-up done
 
   if (warp < 4) {

@@ -46,6 +46,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
 }
 
+// The status word as a block's first thread finds it (0 for the others).  A
+// launch whose earlier CTAs already gave up stops at once instead of timing out
+// CTA by CTA.  The block decides that as one, by this reading and a vote at its
+// set-up's barrier: another CTA may record the code at any moment, and a block
+// that loses some of its warps waits for them without end.
+__device__ __forceinline__ int status_at_entry(const int* err) {
+  return threadIdx.x == 0 ? *const_cast<const volatile int*>(err) : 0;
+}
+
 // Row-per-thread to line-coalesced stores.  In the epilogue lane l of a warp
 // holds row l of the warp's 32 rows; a store of 16 bytes per lane would touch
 // 32 cache lines per instruction.  An in-register 8x8 transpose of 16-byte

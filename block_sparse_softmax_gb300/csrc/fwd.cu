@@ -305,9 +305,7 @@ __global__ void __launch_bounds__(384, 1)
   const int tid = static_cast<int>(threadIdx.x);
   const bool tr = BSS_TRACE_ON(p, blockIdx.x);
   (void)tr;
-  // A launch whose earlier CTAs already timed out stops at once instead of
-  // timing out CTA by CTA.
-  if (*reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
+  const int status = status_at_entry(p.err);
 
   // ---- set-up: barriers, tensor memory, block-sparse bitmaps -------------
   // A block-sparse CTA builds its first item's bitmaps here.  The item's two
@@ -402,9 +400,18 @@ __global__ void __launch_bounds__(384, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(status == ATTN_ERR_TIMEOUT);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (gave_up) {
+    if (SPARSE && tid == 0)                          // the Q tiles are on their way
+      for (int t = 0; t < 2; ++t) drain_bar(bar(C::kBarQFull + t), 0);
+    if (warp == 0) {
+      __syncwarp();
+      tmem_dealloc(tmem, C::kTmemCols);
+    }
+    return;
+  }
 
   if (warp < 4) {
   regs_set<FwdRegs<SPARSE>::kLow, FwdRegs<SPARSE>::kLaunchRegs>();

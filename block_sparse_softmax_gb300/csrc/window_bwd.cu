@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
   const int tid = static_cast<int>(threadIdx.x);
-  if (*reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
+  const int status = status_at_entry(p.err);
 
   const int Lk = p.Lk, Lq = p.Lq;
   const int G = p.H / p.Hkv;
@@ -284,9 +284,16 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(status == ATTN_ERR_TIMEOUT);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (gave_up) {
+    if (warp == 0) {
+      __syncwarp();
+      tmem_dealloc(tmem, C::kTmemCols);
+    }
+    return;
+  }
 
   if (warp < 4) {
   regs_set<WinBwdRegs<D>::kLow, WinBwdRegs<D>::kLaunchRegs>();

@@ -203,9 +203,7 @@ __global__ void __launch_bounds__(512, 1)
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
   const int tid = static_cast<int>(threadIdx.x);
-  // A launch whose earlier CTAs already timed out stops at once (but not a
-  // cluster's CTAs, which would have to agree on it).
-  if (!SPLIT && *reinterpret_cast<volatile int*>(p.err) == ATTN_ERR_TIMEOUT) return;
+  const int status = status_at_entry(p.err);
   const int n_tiles = (p.Lq + kTileM - 1) / kTileM;
 
   if (tid == 0) {
@@ -240,9 +238,16 @@ __global__ void __launch_bounds__(512, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(!SPLIT && status == ATTN_ERR_TIMEOUT);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (gave_up) {                   // (a cluster's CTAs would have to agree on it)
+    if (warp == 0) {
+      __syncwarp();
+      tmem_dealloc(tmem, C::kTmemCols);
+    }
+    return;
+  }
 
   if (warp >= 12) {
     regs_set<kWinLow, kWinLaunchRegs>();

@@ -232,3 +232,29 @@ def test_gradients_of_few_keys(bss, L, window, sinks):
     terms = (want[3].abs().amax() + (do.double().abs() * v.double().abs().amax()).sum(-1).amax()) * 2.0 ** -16
     if L <= 64 or window + sinks <= 32:
         assert (got[3].double() - want[3]).abs().amax() <= terms
+
+
+def test_a_launch_after_a_timeout_stops(bss):
+    """With a timeout in the status word a launch stops at once, block by block, and returns; once
+    the word is read and cleared the same calls are right."""
+    q, k, v, do = inputs(1, 8, 2, 1000, 1000, 128, 12)
+    o, lse = bss.attn_fwd_window(q, k, v, 100, sinks=3)
+    bss.attn_watchdog_selftest(1 << 16)
+    held = torch.full_like(q, 7.0)
+    bss.attn_fwd_window(q, k, v, 100, sinks=3, out=held)
+    bss.attn_bwd_window(q, k, v, o, lse, do, 100, sinks=3)
+    bss.attn_bwd_window(*(t[..., :64].contiguous() for t in (q, k, v, o)), lse, do[..., :64].contiguous(), 100)
+    bss.attn_fwd(q, k, v, causal=True, out=held)
+    bss.attn_fwd(q[..., :64].contiguous(), k[..., :64].contiguous(), v[..., :64].contiguous())
+    bss.attn_bwd(q, k, v, o, lse, do, causal=True)
+    assert bss.attn_poll_status() == bss.ERR_TIMEOUT
+    assert torch.all(held == 7)
+    assert bss.attn_poll_status() == 0
+    mask = ref.window_mask(1000, 1000, 100, 3, device="cuda")
+    o, lse = bss.attn_fwd_window(q, k, v, 100, sinks=3, out=held)
+    got = bss.attn_bwd_window(q, k, v, o, lse, do, 100, sinks=3)
+    check_forward(o, lse, q, k, v, mask, 128 ** -0.5)
+    for a, w, b in zip(got, ref.backward(q, k, v, do, mask, 128 ** -0.5),
+                       ref.backward_bounds(q, k, v, do, mask, 128 ** -0.5)):
+        assert ((a.double() - w).abs() <= b).all()
+    assert bss.attn_poll_status() == 0

@@ -581,11 +581,10 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
         walk.advance(gn, in);
         load_stats(bhq0 + gn, in, l2n, dln);
       }
-      if (!wait_bar(bar(C::kBarSFull), n & 1, abort_flag, p.err) ||
-          !wait_bar(bar(C::kBarStat + (n & 1)), (n >> 1) & 1, abort_flag, p.err)) {
-        ok = false;
-        break;
-      }
+      // (a wait that runs out is noted, and at the tile's end the warp leaves as
+      // one; up to there it only spoils results that are lost already)
+      bool fine = wait_bar(bar(C::kBarSFull), n & 1, abort_flag, p.err) &&
+                  wait_bar(bar(C::kBarStat + (n & 1)), (n >> 1) & 1, abort_flag, p.err);
       tc_fence_after();
       // element mask: a bit for each of this half's 64 queries that sees the
       // key (those from its own position on, up to the window's end unless
@@ -639,10 +638,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(bar(C::kBarPReady));
       // ---- phase 2: dS = P o (dP - D), into shared memory ----
-      if (!wait_bar(bar(C::kBarDPFull + X), n & 1, abort_flag, p.err)) {
-        ok = false;
-        break;
-      }
+      fine = wait_bar(bar(C::kBarDPFull + X), n & 1, abort_flag, p.err) && fine;
       tc_fence_after();
       {
         uint32_t dv[2][16];
@@ -686,12 +682,16 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(bar(C::kBarDSReady));
       if (X == 0 && it + 1 < n_it) store_stats(n + 1, l2n, dln);
+      if (!__all_sync(0xFFFFFFFFu, fine)) {
+        ok = false;
+        break;
+      }
     }
     }
     // ---- an item's end: half 0 stores dK rows, half 1 stores dV rows ----
-    if (ok && n_it > 0) ok = wait_bar(bar(C::kBarDKVFull), kv & 1, abort_flag, p.err);
+    if (ok && n_it > 0)
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarDKVFull), kv & 1, abort_flag, p.err));
     tc_fence_after();
-    ok = __all_sync(0xFFFFFFFFu, ok);
     if (ok) {
       int xx = x;
       asm volatile("" : "+r"(xx));            // the item again, rather than kept in registers
@@ -774,10 +774,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
     int gq, i;                                    // query head of the group, query tile
     walk.start(gq, i);
     for (int it = 0; it < walk.n_it && ok; walk.advance(gq, i), ++it, ++n) {
-      if (!wait_bar_relaxed(bar(C::kBarDQFull), n & 1, abort_flag, p.err)) {
-        ok = false;
-        break;
-      }
+      bool fine = wait_bar_relaxed(bar(C::kBarDQFull), n & 1, abort_flag, p.err);
       tc_fence_after();
       for (int r = 0; r < kRounds; ++r, ++g) {
         uint32_t v0[32], v1[32];
@@ -798,10 +795,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
             bulk_wait_read_all();
             mbar_arrive(bar(C::kBarStageFree));
           }
-          if (!wait_bar(bar(C::kBarStageFree), (g - 1) & 1, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
+          fine = wait_bar(bar(C::kBarStageFree), (g - 1) & 1, abort_flag, p.err) && fine;
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {               // box column 0: columns 0..31 of the round
@@ -824,18 +818,19 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
           }
         } else {
           mbar_arrive(bar(C::kBarStaged));
-          if (qr == 0) {
-            if (!wait_bar(bar(C::kBarStaged), g & 1, abort_flag, p.err)) {
-              ok = false;
-              break;
-            }
+          if (qr == 0) fine = wait_bar(bar(C::kBarStaged), g & 1, abort_flag, p.err) && fine;
+          if (qr == 0 && fine) {
             const int row = i * kTileM;
             tma_reduce_add_4d(&tmDQ, stage, 64 * r, row, hq0 + gq, b);
             tma_reduce_add_4d(&tmDQ, stage + kBoxBytes, 64 * r + 32, row, hq0 + gq, b);
             bulk_commit_group();
           }
         }
-        __syncwarp();                               // reconverge before the next TMEM load
+        // reconverge before the next TMEM load, or leave as a warp
+        if (!__all_sync(0xFFFFFFFFu, fine)) {
+          ok = false;
+          break;
+        }
       }
     }
     }

@@ -574,8 +574,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
         walk.advance(gn, in);
         load_stats(gn, in, l2n, dln);
       }
-      if (!wait_bar(bar(C::kBarSFull), it & 1, abort_flag, p.err) ||
-          !wait_bar(bar(C::kBarStat + (it & 1)), (it >> 1) & 1, abort_flag, p.err)) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarSFull), it & 1, abort_flag, p.err) &&
+                                       wait_bar(bar(C::kBarStat + (it & 1)), (it >> 1) & 1, abort_flag, p.err))) {
         ok = false;
         break;
       }
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
       mbar_arrive(bar(C::kBarPReady));
       BSS_TRACE_EV(p, trw, 2, 4 * it + 1);
       // ---- phase 2: dS = P o (dP - D), into shared memory ----
-      if (!wait_bar(bar(C::kBarDPFull + X), it & 1, abort_flag, p.err)) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarDPFull + X), it & 1, abort_flag, p.err))) {
         ok = false;
         break;
       }
@@ -679,10 +679,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
       }
     }
     // ---- epilogue: half 0 stores dK rows, half 1 stores dV rows ----
-    if (ok) ok = wait_bar(bar(C::kBarDKVFull), 0, abort_flag, p.err);
+    if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarDKVFull), 0, abort_flag, p.err));
     BSS_TRACE_EV(p, tr && kr == 0 && X == 0, 5, 3);   // dK and dV complete
     tc_fence_after();
-    ok = __all_sync(0xFFFFFFFFu, ok);
     if (ok) {
       // one 128-byte line (64 columns as bf16 pairs) of this thread's key row
       // at a time; after the octet transpose every store writes whole lines
@@ -740,7 +739,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     int gq, i;                                    // query head of the group, query tile
     walk.start(gq, i);
     for (int it = 0; i >= 0 && ok; walk.advance(gq, i), ++it) {
-      if (!wait_bar_relaxed(bar(C::kBarDQFull), it & 1, abort_flag, p.err)) break;
+      // (a wait that runs out is noted, and at the round's end the warp leaves as
+      // one; up to there it only spoils results that are lost already)
+      bool fine = wait_bar_relaxed(bar(C::kBarDQFull), it & 1, abort_flag, p.err);
       BSS_TRACE_EV(p, tr && qr == 0, 3, 3 * it);
       tc_fence_after();
       for (int r = 0; r < kRounds; ++r, ++g) {
@@ -763,10 +764,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
             bulk_wait_read_all();
             mbar_arrive(bar(C::kBarStageFree));
           }
-          if (!wait_bar(bar(C::kBarStageFree), (g - 1) & 1, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
+          fine = wait_bar(bar(C::kBarStageFree), (g - 1) & 1, abort_flag, p.err) && fine;
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {               // box column 0: columns 0..31 of the round
@@ -789,18 +787,19 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
           }
         } else {
           mbar_arrive(bar(C::kBarStaged));
-          if (qr == 0) {
-            if (!wait_bar(bar(C::kBarStaged), g & 1, abort_flag, p.err)) {
-              ok = false;
-              break;
-            }
+          if (qr == 0) fine = wait_bar(bar(C::kBarStaged), g & 1, abort_flag, p.err) && fine;
+          if (qr == 0 && fine) {
             const int row = i * kTileM;
             tma_reduce_add_4d(&tmDQ, stage, 64 * r, row, hq0 + gq, b);
             tma_reduce_add_4d(&tmDQ, stage + kBoxBytes, 64 * r + 32, row, hq0 + gq, b);
             bulk_commit_group();
           }
         }
-        __syncwarp();                               // reconverge before the next TMEM load
+        // reconverge before the next TMEM load, or leave as a warp
+        if (!__all_sync(0xFFFFFFFFu, fine)) {
+          ok = false;
+          break;
+        }
       }
       BSS_TRACE_EV(p, tr && qr == 0, 3, 3 * it + 2);
     }

@@ -26,7 +26,8 @@ def test_a_block_reads_the_timeout_as_one(name):
 
 # where the roles of whole warps begin in each kernel (the others' waits are one lane's)
 WHOLE_WARPS = {"window_fwd.cu": "regs_set<kWinOut", "window_bwd.cu": "regs_set<WinBwdRegs<D>::kMid",
-               "fwd.cu": "regs_set<FwdRegs<SPARSE>::kHigh", "fwd_wide.cu": "regs_set<kWideHigh"}
+               "bwd.cu": "regs_set<BwdRegs<D>::kMid", "fwd.cu": "regs_set<FwdRegs<SPARSE>::kHigh",
+               "fwd_wide.cu": "regs_set<kWideHigh"}
 
 
 def votes(text):

@@ -1062,7 +1062,7 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   const long long nq = (static_cast<long long>(Lq) + kTileM - 1) / kTileM;
   const long long G = H / Hkv, BH = static_cast<long long>(B) * Hkv;
   pl.nk = static_cast<int>((static_cast<long long>(Lk) + kTileN - 1) / kTileN);
-  pl.nst = (w.snk + kTileN - 1) / kTileN;
+  pl.nst = static_cast<int>((static_cast<long long>(w.snk) + kTileN - 1) / kTileN);
   // query tiles that a tile without sinks meets at most, over its heads
   const long long share = std::min(nq, std::min<long long>(w.window, 1ll << 40) / kTileM + 2) * G;
   const long long rest = pl.nk - pl.nst;
@@ -1160,6 +1160,7 @@ extern "C" size_t attn_bwd_window_workspace_bytes(int B, int H, int H_kv, int Lq
                                                   int64_t k_offset) {
   WindowMask w;
   if (check_common(B, H, Lq, Lk, d, 1.f) != ATTN_OK || !valid_kv_heads(H, H_kv)) return 0;
+  if (Lq > kMaxTokens || Lk > kMaxTokens) return 0;      // as the call refuses them
   if (!window_mask(&w, Lk, window, sinks, q_offset, k_offset)) return 0;
   return window_bwd_plan(B, H, H_kv, Lq, Lk, d, w).bytes;
 }

@@ -140,3 +140,15 @@ def test_binding_refuses_cpu_tensors(lib):
         bss.attn_kv_reserve(t, n, n, n, 16)
     with pytest.raises(ValueError, match="CUDA"):
         bss.attn_kv_copy_pages(c, c, n, n)
+
+
+def test_no_workspace_for_lengths_that_are_refused(lib):
+    """Lengths that attn_bwd_window refuses get no size, whatever the sinks; the longest allowed do."""
+    size = lib.attn_bwd_window_workspace_bytes
+    most = 0x7FFFFF00
+    for Lq, Lk in ((128, 2 ** 31 - 1), (2 ** 31 - 1, 128), (128, most + 1), (2 ** 31 - 1, 2 ** 31 - 1)):
+        for sinks in (0, 4, 2 ** 31 - 1):
+            assert size(1, 1, 1, Lq, Lk, 64, 256, sinks, 0, 0) == 0, (Lq, Lk, sinks)
+    acc = 128 * 64 * 4
+    for sinks in (0, 4, most):
+        assert acc <= size(1, 1, 1, 128, most, 64, 256, sinks, 0, 0) <= acc + 152 * 8 * 2 * 128 * 64 * 4, sinks

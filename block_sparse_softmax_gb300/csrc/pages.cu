@@ -409,8 +409,7 @@ __global__ void __launch_bounds__(256) kv_remap_kernel(int* table, long long ent
                                                        const int* copy_src, const int* copy_dst,
                                                        const int* count, int* err) {
   const int n = *count;
-  if (n == 0) return;
-  const int first = copy_src[0];
+  const int first = n > 0 ? copy_src[0] : P;      // (nothing moves: entries out of range are still reported)
   for (long long x = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; x < entries;
        x += static_cast<long long>(gridDim.x) * blockDim.x) {
     const int e = table[x];

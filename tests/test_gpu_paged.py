@@ -616,3 +616,22 @@ def test_decode_of_an_infinite_value(bss):
     want[0, :2, 9] = -float("inf")
     assert torch.equal(got, want)
     assert bss.attn_poll_status() == 0
+
+
+@pytest.mark.parametrize("columns", [4, 70000])
+def test_compaction_reports_bad_entries(bss, columns):
+    """An entry past the last page is reported and left as it is, for small tables and for large
+    ones, which a launch of their own rewrites, whether or not a page moves."""
+    for refs, moved in (([1, 1, 0, 0], 0), ([0, 1, 1, 0], 1)):
+        table = torch.full((1, columns), -1, dtype=torch.int32, device="cuda")
+        table[0, -3:] = ints([9, 1, 2 if moved else 0])
+        r = ints(refs)
+        src, dst, count = bss.attn_kv_compact(table, r)
+        assert bss.attn_poll_status() == bss.ERR_BAD_PAGES
+        assert int(count) == moved and r.tolist() == [1, 1, 0, 0]
+        assert table[0, -3:].tolist() == [9, 1, 0] and torch.all(table[0, :-3] == -1)
+        assert src.tolist() == [2 if moved else -1, -1, -1, -1]
+        assert dst.tolist() == [0 if moved else -1, -1, -1, -1]
+        table[0, -3] = -1
+        bss.attn_kv_compact(table, r)
+        assert bss.attn_poll_status() == 0

@@ -5,7 +5,8 @@ head); its bookkeeping is three int32 tensors on the same device, changed in pla
 [S, max_pages] (-1 where a sequence holds no page), ``seq_lens`` [S] and ``refs`` [n_pages] (0 for
 a free page).  A fresh cache has -1 in every entry and 0 in every length and count.  What is wrong
 in them is found on the device: ``attn_poll_status`` then returns ``ERR_BAD_PAGES``, or
-``ERR_NO_PAGES`` where too few pages were free.
+``ERR_NO_PAGES`` where too few pages were free.  A call for an empty batch (no sequence, token,
+fork or copy) does nothing; outputs without rows are returned.
 """
 from __future__ import annotations
 
@@ -125,6 +126,8 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int 
     lp = _is(seq_lens, "seq_lens", _INT, (rows,), dev)
     out, op = _out(out, "out", _BF16, (S, H, d), q)
     lse, ep = _out(lse, "lse", _FP32, (S, H), q)
+    if S == 0:                                # no sequence asks for anything
+        return out, lse
     wp, nbytes = None, 0
     if workspace is None:
         nbytes = _decode_bytes(S, H, Hkv, d, M, page)
@@ -147,6 +150,8 @@ def attn_kv_reserve(page_table, seq_lens, refs, n_new, page_size: int, *, start=
     if n > S:
         raise ValueError(f"n_new has {n} entries for {S} sequences")
     start, sp = _out(start, "start", _INT, (n,), n_new)
+    if n == 0:
+        return start
     _run("attn_kv_reserve", dev, tp, lp, rp, np_, sp, n, M, P, int(page_size))
     return start
 
@@ -168,9 +173,11 @@ def attn_kv_write(k_new, v_new, k_cache, v_cache, page_table, start, cu_new, *, 
     S = start.numel()
     if rows < S:
         raise ValueError(f"page_table has {rows} rows for {S} sequences")
+    sp, cp = _is(start, "start", _INT, (S,), dev), _is(cu_new, "cu_new", _INT, (S + 1,), dev)
+    if S == 0:                                # every row is one of no sequence
+        return
     _run("attn_kv_write", dev, k_new.data_ptr(), v_new.data_ptr(), k_row, v_row, kp, vp, ks, vs, code,
-         ksp, vsp, tp, _is(start, "start", _INT, (S,), dev),
-         _is(cu_new, "cu_new", _INT, (S + 1,), dev), T, S, M, P, Hkv, d, page)
+         ksp, vsp, tp, sp, cp, T, S, M, P, Hkv, d, page)
 
 
 def attn_kv_fork(page_table, seq_lens, refs, parents, children, page_size: int, *, copy_src=None,

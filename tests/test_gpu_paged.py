@@ -635,3 +635,31 @@ def test_compaction_reports_bad_entries(bss, columns):
         table[0, -3] = -1
         bss.attn_kv_compact(table, r)
         assert bss.attn_poll_status() == 0
+
+
+def test_an_empty_batch(bss):
+    """No sequence, no token, no fork: nothing happens, and the outputs have no rows."""
+    c = Cache([40, 3], 2, 64, 16, 6)
+    before = [t.clone() for t in (c.k, c.v, c.table, c.lens)]
+    refs = torch.zeros(c.k.shape[0], dtype=torch.int32, device="cuda")
+    none, bf = ints([]), dict(dtype=torch.bfloat16, device="cuda")
+    for columns in (0, 100):                           # either route
+        wide = torch.cat([c.table, ints([[-1] * columns] * 2)], 1)
+        for table, lens in ((wide, c.lens), (wide[:0], c.lens[:0])):
+            o, lse = bss.attn_decode_paged(torch.empty(0, 4, 64, **bf), c.k, c.v, table, lens)
+            assert o.shape == (0, 4, 64) and o.dtype == torch.bfloat16
+            assert lse.shape == (0, 4) and lse.dtype == torch.float32
+    start = bss.attn_kv_reserve(c.table, c.lens, refs, none, 16)
+    assert start.shape == (0,) and start.dtype == torch.int32
+    rows = torch.randn(3, 2, 64, device="cuda").bfloat16()
+    bss.attn_kv_write(rows, rows, c.k, c.v, c.table, none, ints([3]))       # rows of no sequence
+    bss.attn_kv_write(rows[:0], rows[:0], c.k, c.v, c.table, ints([40, 3]), ints([0, 0, 0]))
+    src, dst = bss.attn_kv_fork(c.table, c.lens, refs, none, none, 16)
+    bss.attn_kv_copy_pages(c.k, c.v, src, dst)
+    bss.attn_kv_free(c.table, c.lens, refs, none, 16)
+    assert bss.attn_poll_status() == 0
+    assert all(torch.equal(a.view(torch.int16) if a.dtype == torch.bfloat16 else a,
+                           b.view(torch.int16) if b.dtype == torch.bfloat16 else b)
+               for a, b in zip(before, (c.k, c.v, c.table, c.lens)))
+    with pytest.raises(ValueError):
+        bss.attn_decode_paged(torch.empty(0, 4, 32, **bf), c.k, c.v, c.table, c.lens)

@@ -981,8 +981,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join_kernel(const
 constexpr int kDecMaxCtas = 152 * 3;
 
 constexpr int kDecWorkers = kDecMaxCtas * kDecWarps;
-constexpr int kSmallKeys = 1024;
-constexpr int kSmallUnits = 4096;
 
 // query heads of a part: what a K/V head's group has, at most 16
 int decode_rows(int G) { return G <= 8 ? 8 : 16; }
@@ -992,17 +990,42 @@ long long decode_workers(int S, int Hkv, int G, int max_pages, int page) {
   const long long steps = static_cast<long long>(max_pages) * (page / 16) * S * Hkv * ((G + 15) / 16);
   return std::min<long long>(kDecWorkers, (steps + kDecWarps - 1) / kDecWarps * kDecWarps);
 }
-// Whether a CTA a unit does: where a row of the table holds up to 1024 tokens,
-// one launch without a scan of the lengths and without parts is shorter than
-// sharing all steps evenly (us, d=128, 4 K/V heads, 300 tokens: 8.3 against
-// 12.3 for 1 sequence, 10.3 against 14.4 for 64; 1000 tokens: 16.5 and 16.4,
-// 26.6 and 32.6; one K/V head of 16 query heads, 1000 tokens: 22 and 18), and
-// the host has one launch and one allocation less (20 against 25 us).  Over
-// very many units the CTAs' set-up adds up (2048 units of 30 tokens: 18.5
-// against 12.3).
+// Whether a CTA a unit does: one launch without a scan of the lengths and
+// without parts, instead of sharing all steps evenly.  What that takes grows
+// with the longest unit, so it is for tables whose rows hold up to 1024 tokens
+// (us, a CTA a unit | shared evenly, rows as long as the table has room for,
+// d=128, bf16; S sequences of 16 query heads on 4 K/V heads):
+//      tokens    64           256          1024
+//      S = 1     6.1 | 10.2   8.2 | 12.2   16.4 | 16.6
+//      S = 64    6.2 | 12.3   12.0 | 18.5  27.8 | 33.0
+//      S = 512   24 | 29      51 | 58      161 | 173
+// A group of more than 8 query heads takes a warp longer over its keys; past
+// 512 tokens its few units do better shared by more CTAs (16 query heads on one
+// K/V head):
+//      tokens    256          512          768          1024
+//      S = 1     10.3 | 12.5  14.5 | 14.3  18.5 | 16.4  22.5 | 18.3
+//      S = 32    10.3 | 16.3  14.5 | 18.4  18.5 | 18.8  23.2 | 20.5
+//      S = 64    11.6 | 16.4  14.4 | 18.8  19.8 | 22.0  24.6 | 23.8
+//      S = 128   11.0 | 20.1  16.4 | 24.6  20.5 | 27.6  24.7 | 30.0
+// And over many units of few tokens the CTAs' set-up adds up (4 K/V heads; bf16,
+// e4m3):
+//      tokens    16                        32                        64
+//      S = 128   8.2 | 10.2, 10.3 | 11.9   8.9 | 12.7, 9.6 | 11.0    9.6 | 16.4, 10.2 | 13.2
+//      S = 512   15.8 | 14.4, 23.2 | 18.4  19.7 | 22.6, 18.5 | 16.4  24.3 | 28.7, 22.4 | 23.6
+//      S = 1024  32.5 | 21.9, 38.9 | 25.9  33.1 | 30.6, 35.1 | 24.6  39.1 | 41.0, 38.3 | 32.8
+// The host has one launch and one allocation less (20 against 25 us).  Rows that
+// are shorter than the table has room for take less by either way, a CTA a
+// unit's more so; the lengths are the device's.
+constexpr int kSmallKeys = 1024;
+constexpr int kSmallKeysLarge = 512;        // groups of more than 8 query heads in few units
+constexpr int kSmallUnitsLarge = 64;        // ... fewer than this
+constexpr int kSmallUnits = 4096;
+constexpr int kSmallUnitsAToken = 32;
 bool decode_small(int S, int Hkv, int G, int max_pages, int page) {
   const long long units = static_cast<long long>(S) * Hkv * ((G + 15) / 16);
-  return static_cast<long long>(max_pages) * page <= kSmallKeys && units <= kSmallUnits;
+  const long long tokens = static_cast<long long>(max_pages) * page;
+  if (tokens > kSmallKeys || units > std::min<long long>(kSmallUnits, tokens * kSmallUnitsAToken)) return false;
+  return G <= 8 || tokens <= kSmallKeysLarge || units >= kSmallUnitsLarge;
 }
 size_t decode_workspace(int d, int G, long long workers) {
   return static_cast<size_t>(workers) * 8 + static_cast<size_t>(workers) * 2 * decode_rows(G) * (d + 2) * 4;

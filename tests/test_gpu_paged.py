@@ -663,3 +663,20 @@ def test_an_empty_batch(bss):
                for a, b in zip(before, (c.k, c.v, c.table, c.lens)))
     with pytest.raises(ValueError):
         bss.attn_decode_paged(torch.empty(0, 4, 32, **bf), c.k, c.v, c.table, c.lens)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens,H,Hkv,d,page,window,sinks", [
+    ([1008], 16, 1, 128, 16, 0, 0),                # a tight table, units shared by several CTAs
+    ([700, 0, 1, 1023], 20, 1, 64, 32, 0, 0),
+    ([1024 - 64, 17], 66, 2, 128, 64, 300, 5),
+    ([13, 0, 16, 1] * 160, 4, 1, 64, 16, 0, 0),    # many units of one page
+])
+def test_decode_of_tight_tables_shared_evenly(bss, lens, H, Hkv, d, page, window, sinks, e4m3):
+    c = Cache(lens, Hkv, d, page, sum(lens) + d, e4m3, window=window, sinks=sinks)
+    c.table = c.table[:, :-(-max(lens) // page)].contiguous()       # no more room than the longest takes
+    assert bss.attn_decode_paged_workspace_bytes(len(lens), H, Hkv, d, c.table.shape[1], page) > 0
+    q = torch.randn(len(lens), H, d, generator=torch.Generator("cuda").manual_seed(H), device="cuda").bfloat16()
+    a = check_decode(bss, c, q, lens, window, sinks)
+    b = check_decode(bss, c, q, lens, window, sinks)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

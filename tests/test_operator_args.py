@@ -152,3 +152,19 @@ def test_no_workspace_for_lengths_that_are_refused(lib):
     acc = 128 * 64 * 4
     for sinks in (0, 4, most):
         assert acc <= size(1, 1, 1, 128, most, 64, 256, sinks, 0, 0) <= acc + 152 * 8 * 2 * 128 * 64 * 4, sinks
+
+
+def test_decode_takes_the_route_that_measured_faster(lib):
+    """A CTA a unit (no workspace) or the units' steps shared evenly, at sizes where the two were
+    timed 4 % or more apart (rows as long as the table)."""
+    def shared(S, H, Hkv, tokens):
+        return lib.attn_decode_paged_workspace_bytes(S, H, Hkv, 128, tokens // 16, 16) > 0
+    # S, H, H_kv, tokens a row: one CTA a unit is faster
+    for case in ((1, 16, 4, 64), (1, 16, 4, 256), (64, 16, 4, 1024), (512, 16, 4, 1024), (1, 16, 1, 256),
+                 (32, 16, 1, 512), (64, 16, 1, 768), (128, 16, 1, 1024), (16, 64, 2, 512), (128, 16, 4, 16),
+                 (512, 16, 4, 64), (1024, 16, 4, 512)):
+        assert not shared(*case), case
+    # ... sharing is
+    for case in ((1, 16, 1, 768), (1, 16, 1, 1024), (8, 16, 1, 1024), (32, 16, 1, 1024), (1, 64, 2, 1024),
+                 (512, 16, 4, 16), (1024, 16, 4, 16), (1024, 16, 4, 32)):
+        assert shared(*case), case

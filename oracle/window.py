@@ -15,8 +15,9 @@ The bounds count the roundings that such a kernel makes, each by at most half a 
           the logarithm's own error, and the fp32 sum of the row), and 2^-8 as an operand of P V
           or P^T dO (`p_round` where a kernel holds it in more bits).
   O       sum P |v| times P's error, + 2^-8 |O| for its own rounding.
-  D       dO . O with the rounded O: sum |dO| (O's error), + fp32; for rows of at most 16 keys
-          sum_j P_ij dP_ij in fp32: P's error before any rounding to bf16.
+  D       dO . O with the rounded O: sum |dO| (O's error), + fp32; for rows of few keys
+          sum_j P_ij dP_ij in fp32: P's error before any rounding to bf16.  Which rows those are
+          `few_keys` says; without it, the rows of at most 16 keys.
   dS      scale P (dP - D): P's error on |dS|, 2^-8 |dS| as an operand, scale P (D's error + dP's).
   dQ, dK  sums of dS's error times |k|, |q|, + 2^-8 of the result.
 """
@@ -34,6 +35,19 @@ def window_mask(Lq, Lk, window, sinks=0, q_offset=0, k_offset=0, device="cpu"):
     i = torch.arange(Lq, device=device)[:, None] + q_offset
     j = torch.arange(Lk, device=device)[None, :] + k_offset
     return (j <= i) & ((i - j < window) | (j < sinks))
+
+
+def few_keys(Lq, Lk, window, sinks=0, q_offset=0, k_offset=0, device="cpu"):
+    """Boolean [Lq]: the rows whose D attn_bwd_window takes from its definition.  They see at most
+    64 keys, and lie near the first key or past the last one (the window holds the first key, or
+    reaches past the last but 64), or window and sinks together are at most 32 keys."""
+    n = window_mask(Lq, Lk, window, sinks, q_offset, k_offset, device).sum(1)
+    own = torch.arange(Lq, device=device) + q_offset - k_offset
+    near = (own < 64) | (own - window + 1 >= Lk - 64)
+    held = max(0, min(sinks - k_offset, Lk))
+    if window + held <= 32 or Lk <= 64:
+        near = torch.ones_like(near)
+    return near & (n <= 64)
 
 
 def _grouped(x, H):
@@ -81,8 +95,8 @@ def backward(q, k, v, do, mask, scale):
     return (dS @ kk, fold(dS.transpose(-1, -2) @ qq), fold(P.transpose(-1, -2) @ do), D[..., 0])
 
 
-def backward_bounds(q, k, v, do, mask, scale):
-    """(bounds of dq, dk, dv, D) element by element."""
+def backward_bounds(q, k, v, do, mask, scale, few_rows=None):
+    """(bounds of dq, dk, dv, D) element by element; few_rows: `few_keys` of the call."""
     B, H, Lq, d = q.shape
     Hkv = k.shape[1]
     O, lse, P = forward(q, k, v, mask, scale)
@@ -99,7 +113,9 @@ def backward_bounds(q, k, v, do, mask, scale):
     D_err = (doa * bound_o).sum(-1, keepdim=True) + (doa * (O.abs() + bound_o)).sum(
         -1, keepdim=True) * d * 2.0 ** -23
     few = (P * (1 + p_rel) * (dP.abs() * p_rel + dP_size * d * 2.0 ** -23)).sum(-1, keepdim=True)
-    D_err = torch.where(mask.sum(-1, keepdim=True) <= 16, few + (P * dP.abs()).sum(
+    if few_rows is None:
+        few_rows = mask.sum(-1) <= 16
+    D_err = torch.where(few_rows[:, None], few + (P * dP.abs()).sum(
         -1, keepdim=True) * 2.0 ** -19, D_err)
     dS = (scale * P * (dP - D)).abs()
     dS_err = scale * P * (1 + p_rel) * (D_err + dP_size * d * 2.0 ** -23 + (dP.abs() + D.abs()) * 2.0 ** -22)

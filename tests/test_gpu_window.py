@@ -258,3 +258,69 @@ def test_a_launch_after_a_timeout_stops(bss):
                        ref.backward_bounds(q, k, v, do, mask, 128 ** -0.5)):
         assert ((a.double() - w).abs() <= b).all()
     assert bss.attn_poll_status() == 0
+
+
+@pytest.mark.parametrize("B,H,Hkv,Lq,Lk,d,window,sinks,qo,ko", [
+    # forward: more query tiles than the device has SMs, so that a CTA takes several, d=128
+    (1, 40, 8, 1100, 1100, 128, 100, 4, 0, 0),
+    (1, 48, 16, 1300, 1300, 128, 1, 0, 0, 0),      # one block each but for its neighbour's edge
+    (1, 64, 8, 1200, 700, 128, 300, 0, 0, 0),      # the last tiles see nothing
+    (2, 40, 40, 900, 900, 128, 513, 130, 0, 0),
+    (1, 50, 10, 1000, 900, 128, 200, 2, 0, 300),   # ... the first ones
+    (1, 70, 70, 1000, 1000, 128, 10 ** 12, 0, 0, 0),
+    (1, 64, 4, 1500, 800, 64, 260, 1, 100, 0),     # the same at d=64
+    # backward: walks of more than 20 tiles over at least 152 key tiles, a CTA each
+    (6, 16, 2, 1600, 1600, 128, 700, 4, 0, 0),
+    (6, 16, 2, 1600, 1600, 64, 700, 0, 0, 0),
+    (1, 8, 8, 2750, 2750, 64, 2500, 3, 0, 0),
+    (1, 8, 8, 2750, 2750, 128, 10 ** 12, 0, 0, 0),
+])
+def test_many_items_and_long_walks(bss, B, H, Hkv, Lq, Lk, d, window, sinks, qo, ko):
+    """What small shapes do not reach: a CTA that goes from query tile to query tile with one Q
+    buffer, and key tiles whose walks are long enough for a CTA of their own."""
+    test_forward_and_backward(bss, B, H, Hkv, Lq, Lk, d, window, sinks, qo, ko)
+
+
+@pytest.mark.parametrize("H,Hkv,Lq,Lk,d,window,sinks,qo,ko", [
+    (4, 4, 2, 2, 128, 50, 0, 0, 0),
+    (4, 2, 63, 63, 128, 47, 1, 0, 0),
+    (4, 1, 64, 64, 64, 1000, 0, 0, 0),
+    (4, 4, 300, 300, 128, 20, 1, 0, 0),            # every row sees at most 21 keys
+    (4, 2, 300, 300, 64, 28, 4, 0, 0),             # ... 32
+    (4, 2, 300, 300, 64, 29, 4, 0, 0),             # ... 33: the first 64 rows alone
+    (2, 2, 300, 300, 128, 150, 3, 0, 0),
+    (2, 1, 300, 300, 128, 64, 0, 0, 0),
+    (2, 2, 200, 300, 64, 50, 0, 320, 0),           # rows past the last key
+    (2, 2, 200, 300, 128, 100, 10, 250, 0),
+    (2, 1, 300, 200, 128, 64, 0, 0, 150),          # a later chunk of keys
+    (2, 1, 300, 200, 64, 300, 160, 0, 150),
+    (2, 2, 500, 40, 128, 50, 3, 5, 0),             # few keys there are
+    (2, 2, 100, 65, 64, 70, 0, 0, 0),
+])
+def test_rows_of_few_keys(bss, H, Hkv, Lq, Lk, d, window, sinks, qo, ko):
+    """Rows of up to 64 keys, of which a sink may have most of the weight, take D from its
+    definition: D is off by fp32 sums alone and dQ and dK by what rounding dS and the result leaves.
+    (D from the rounded O is up to 2^-8 |dO| |O| off, several times these bounds.)"""
+    g = torch.Generator("cuda").manual_seed(Lq + Lk + window)
+    q, do = (torch.randn(1, H, Lq, d, generator=g, device="cuda") for _ in range(2))
+    k, v = (torch.randn(1, Hkv, Lk, d, generator=g, device="cuda") for _ in range(2))
+    lead = 0.4 * torch.randn(1, Hkv, 1, d, generator=g, device="cuda")
+    q = q + lead.repeat_interleave(H // Hkv, 1)
+    k[:, :, :max(0, min(sinks - ko, Lk))] += 2 * lead
+    q, k, v, do = (t.bfloat16() for t in (q, k, v, do))
+    opt = dict(sinks=sinks, q_offset=qo, k_offset=ko)
+    o, lse = bss.attn_fwd_window(q, k, v, window, **opt)
+    got = bss.attn_bwd_window(q, k, v, o, lse, do, window, **opt)
+    assert bss.attn_poll_status() == 0
+    mask = ref.window_mask(Lq, Lk, window, sinks, qo, ko, "cuda")
+    few = ref.few_keys(Lq, Lk, window, sinks, qo, ko, "cuda")
+    want = ref.backward(q, k, v, do, mask, d ** -0.5)
+    bound = ref.backward_bounds(q, k, v, do, mask, d ** -0.5, few)
+    for name, a, w, b in zip(("dq", "dk", "dv", "delta"), got, want, bound):
+        off = (a.double() - w).abs()
+        assert (off <= b).all(), f"{name}: {(off / b).max().item():.3g} of its bound"
+    # the other way to take D would not be within them
+    seen = few & (mask.sum(1) > 1)
+    if seen.any():
+        rough = (do.double() * o.double()).sum(-1)
+        assert ((rough - want[3]).abs() > bound[3])[:, :, seen].any()

@@ -549,8 +549,9 @@ unsigned grid_256(long long work) {
   return static_cast<unsigned>(b < 1 ? 1 : (b > 152ll * 16 ? 152ll * 16 : b));
 }
 
-// Dynamic shared memory past 48 KB, once a device.
-attn_status_t allow_smem(const void* kernel, int bytes) {
+// The compaction's map in shared memory is past the 48 KB that a kernel has
+// without asking: asked for once a device.
+attn_status_t allow_compact_smem() {
   constexpr int kMaxDev = 64;
   static bool configured[kMaxDev] = {};
   int dev = 0;
@@ -558,7 +559,7 @@ attn_status_t allow_smem(const void* kernel, int bytes) {
   if (e != cudaSuccess) return cuda_status("cudaGetDevice", e);
   if (dev < 0 || dev >= kMaxDev) return ATTN_ERR_UNSUPPORTED;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(kv_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpan * 4);
     if (e != cudaSuccess) return cuda_status("cudaFuncSetAttribute", e);
     configured[dev] = true;
   }
@@ -723,7 +724,7 @@ attn_status_t attn_kv_compact(int32_t* page_table, int32_t* refs, int32_t* copy_
   const long long entries = static_cast<long long>(S) * max_pages;
   const bool inside = entries <= kSmallTable && n_pages <= kSpan;
   const int smem = inside ? n_pages * 4 : 0;
-  if ((s = allow_smem(reinterpret_cast<const void*>(kv_compact_kernel), kSpan * 4)) != ATTN_OK) return s;
+  if ((s = allow_compact_smem()) != ATTN_OK) return s;
   kv_compact_kernel<<<1, kBookThreads, smem, st>>>(refs, n_pages, copy_src, copy_dst, count, page_table,
                                                    inside ? static_cast<int>(entries) : 0, err);
   if ((s = cuda_status("attn_kv_compact launch", cudaGetLastError())) != ATTN_OK || inside) return s;

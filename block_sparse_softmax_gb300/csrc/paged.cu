@@ -58,6 +58,7 @@
 #include <algorithm>
 
 #include "host.cuh"
+#include "mma.cuh"
 
 namespace bss {
 namespace {
@@ -167,15 +168,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;       // 0: the 16 bytes are filled with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -183,28 +175,6 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t movm(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-// fp16 operands (F16) or bf16 ones, fp32 accumulators.
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Two e4m3 elements (the low 16 bits) as a pair of fp16, which holds them all.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
@@ -224,14 +194,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-// A number in [0, 1] as two bf16 ones: its high half cut off (a pair of them
-// packed), and the rest, of which bf16 holds all but 2^-15 of the number.  The
-// rest is kept above 0: 0 times an infinity in V would turn it into a NaN.
-__device__ __forceinline__ uint32_t high_bf16(float lo, float hi) {
-  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-}
-__device__ __forceinline__ float rest_bf16(float x) {
-  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u), 1.17549435e-38f);
+// P's rest beside its high half (high_bf16), of which bf16 holds all but 2^-15 of
+// P.  It is kept above 0: 0 times an infinity in V would turn it into a NaN.
+__device__ __forceinline__ float p_rest(float x) {
+  return fmaxf(low_part(x), 1.17549435e-38f);
 }
 
 // The running state of a unit in one warp: A^T fragments, and for the thread's
@@ -731,7 +697,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
               pb[m][n8][u] = movm(pack_f16(pr[m][2 * u], pr[m][2 * u + 1]));
             } else {
               pb[m][n8][u] = movm(high_bf16(pr[m][2 * u], pr[m][2 * u + 1]));
-              pb_lo[m][n8][u] = movm(pack_bf16(rest_bf16(pr[m][2 * u]), rest_bf16(pr[m][2 * u + 1])));
+              pb_lo[m][n8][u] = movm(pack_bf16(p_rest(pr[m][2 * u]), p_rest(pr[m][2 * u + 1])));
             }
           }
         }

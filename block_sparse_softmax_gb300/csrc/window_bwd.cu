@@ -12,9 +12,10 @@
 // in tensor memory, dQ added into an fp32 accumulator by bulk reduce-adds)
 // over the query tiles that the window lets the key tile meet.
 //
-// A tile with a sink key meets every later query tile, window / 128 + 1 tiles
-// would be its neighbours' share: its walk is cut into segments of about that
-// share, each a CTA of its own that leaves fp32 parts of dK and dV in the
+// Up to kFewSinks sinks have a kernel of their own, which also takes D.  With
+// more, a tile with a sink key meets every later query tile, where window / 128 +
+// 1 tiles would be its neighbours' share: its walk is cut into segments of about
+// that share, each a CTA of its own that leaves fp32 parts of dK and dV in the
 // workspace; a last kernel adds the parts in segment order and rounds once.
 // The other tiles' walks are cut the same way when there are too few tiles to
 // fill the GPU.  dK and dV come out the same in every run; dQ's fp32 additions
@@ -34,6 +35,7 @@
 #include <algorithm>
 
 #include "host.cuh"
+#include "mma.cuh"
 #include "window.cuh"
 
 namespace bss {
@@ -44,6 +46,9 @@ namespace {
 // together are at most kFewWindow keys.
 constexpr int kFewKeys = 64;
 constexpr int kFewWindow = 32;
+
+// Sinks that have a kernel of their own: up to an N tile of its products.
+constexpr int kFewSinks = 8;
 
 // Key tiles j0 .. j0 + n - 1 of every K/V head, their walks cut into `seg`
 // segments each; their first item, and the workspace slot of its part (cut
@@ -69,8 +74,11 @@ struct WindowBwdParams {
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   float* part;          // fp32 [slot][dK, dV][128][d]: parts of the cut walks
+  float* sink_part;     // fp32 [B H_kv][sink_ctas][dK, dV][kFewSinks][d]
+  int sink_ctas;        // CTAs of a K/V head in the sinks' kernel (0: the main kernel takes the sinks)
+  int first_key;        // the main kernel's first key (those below have the sinks' kernel)
   int nk;               // key tiles
-  int nst;              // the first of them, which hold a sink key
+  int nst;              // the first of them, which meet every later query tile for a sink key
   WindowTiles tiles[2]; // those, and the others, in the order of their items
   int n_items;          // key tiles, or segments of them, over all heads
   int* err;
@@ -588,13 +596,14 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
       tc_fence_after();
       // element mask: a bit for each of this half's 64 queries that sees the
       // key (those from its own position on, up to the window's end unless
-      // the key is a sink; none for a key past the last one).  The ragged tail
+      // the key is a sink; none for a key past the last one, or one of the sinks
+      // that have their own kernel).  The ragged tail
       // (query >= Lq) has -lse2 = -inf, so P is 0 there already
       uint32_t seen[2];
       {
         const long long tile = static_cast<long long>(key0) - p.w.sh - static_cast<long long>(i) * kTileM;
         const int own = clamped(tile, -kTileM, kTileM) + kr - 64 * X;
-        const int qlo = key < Lk ? own : 64;
+        const int qlo = key < Lk && key >= p.first_key ? own : 64;
         const int end = key < p.w.snk ? 64 : clamped(tile + p.w.window, -kTileM, kTileM) + kr - 64 * X;
         seen[0] = bits_below(end) & ~bits_below(qlo);
         seen[1] = bits_below(end - 32) & ~bits_below(qlo - 32);
@@ -993,22 +1002,335 @@ __global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBw
   }
 }
 
-// dQ (bf16) from the fp32 accumulator (the scale was applied to dS already),
-// and dK, dV of the cut walks: their parts added in segment order.
+// The same where up to kFewSinks keys are sinks (snk of them), and all that
+// comes of the pairs of a query with a sink: their dQ, which the accumulator
+// starts from, and parts of the sinks' dK and dV.
+//
+// A sink's dK and dV are sums over every later query of every head of its
+// group: elements of a hundred times the other keys', of which a P and a dS
+// rounded to bf16 leave 2e-3 uncertain.  (Taken by the main kernel, single
+// elements near 0 came out up to 0.4 of the rms of all dK off: 4 sinks of 16384
+// keys, window 1024, 4 heads a group.)  Here P and dS enter their products in
+// two bf16 parts each, which hold all but 2^-15 of them.
+//
+// A warp takes 16 rows at a time, as mma.m16n8k16 has them, with the sinks as its
+// 8 columns: S and dP = [Q; dO] [K; V]^T, then dQ = [dS, its rest] [K; K] (the
+// rest takes the 8 rows that 8 sinks leave of 16), dK^T += Q^T dS and dV^T +=
+// dO^T P with both parts.  A thread's 16 bytes of a row are 8 neighbouring
+// d's, of which the first 4 and the last 4 stand in two steps' columns 2c, 2c + 1,
+// 2c + 8 and 2c + 9.  sink_ctas CTAs of kSinkWarps warps share the rows of a
+// K/V head's group, and a lane's pieces of its warp's next rows are on their way
+// into its own places in shared memory (cp.async) while the warp computes.  D of
+// rows of few keys comes by the same products, 8 keys at a time (a row at a
+// time, as in the kernel above, the warp that meets the first rows ended 100 us
+// after the others).
+// Bound by HBM (Q, dO, O in, the accumulator out): 59 us for 336 MB, 5.7 TB/s, at
+// B1 H16(4) L16384 d128; three CTAs an SM with the pieces in registers took 69.
+// With the main kernel's walks of the sink tile gone, that call (window 1024, 4
+// sinks) took 474 us instead of 462 (435 with the last wave cut, below), B4 H16
+// L2000 d64 105 instead of 114, B2 H8(2) L300 29 instead of 43.
+constexpr int kSinkWarps = 4;
+constexpr int kSinkCtasPerSm = 2;
+
+// Rows g and g + 8 of a warp's unit, as a lane holds them.
+struct SinkRows {
+  size_t head;                    // first row of the query head
+  int i[2];                       // query rows
+  int seen[2];                    // sinks that they see (-1: no row)
+  float nl2[2];                   // minus the LSE in log2 units
+};
+template <int D>
+struct SinkSmem {
+  static constexpr int NJ = D / 32;                   // 16-byte pieces of a row a lane holds
+  union {
+    uint4 buf[kSinkWarps][2][3][2][NJ][32];           // [warp][stage][Q, dO, O][row][piece][lane]
+    float sum[2][kFewSinks][D];
+  };
+  uint4 ks[NJ][32], vs[NJ][32];                       // the sinks as B of S and dP
+  uint4 kt[NJ][32];                                   // K as B of dQ: tiles 4 j .. 4 j + 3
+};
+
+template <int D>
+__global__ void __launch_bounds__(kSinkWarps * 32, kSinkCtasPerSm)
+    attn_bwd_window_sink_kernel(const WindowBwdParams p, const FewRows fr) {
+  constexpr int NJ = D / 32;
+  extern __shared__ __align__(16) uint8_t sink_smem[];
+  SinkSmem<D>& sm = *reinterpret_cast<SinkSmem<D>*>(sink_smem);
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int g = lane >> 2, c = lane & 3;
+  const int snk = p.w.snk;
+  const int bh = static_cast<int>(blockIdx.x) / p.sink_ctas;
+  const int cta = static_cast<int>(blockIdx.x) - bh * p.sink_ctas;
+  const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
+  const int group = p.H / p.Hkv;
+  const int head0 = b * p.H + hkv * group;
+  // a unit: 16 rows of one of the group's heads
+  const uint32_t tiles = (static_cast<uint32_t>(p.Lq) + 15) / 16, units = group * tiles;
+  const uint32_t stride = p.sink_ctas * kSinkWarps;
+
+  auto locate = [&](uint32_t unit) {
+    SinkRows w;
+    const uint32_t h = unit / tiles;
+    w.head = static_cast<size_t>(head0 + h) * p.Lq;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      w.i[u] = static_cast<int>((unit - h * tiles) * 16) + g + 8 * u;
+      const bool in = w.i[u] < p.Lq;
+      w.seen[u] = in ? clamped(w.i[u] + p.w.sh + 1, 0, snk) : -1;
+      w.nl2[u] = in ? -(__ldg(p.lse + w.head + w.i[u]) * kLog2e) : 0.f;
+    }
+    return w;
+  };
+  auto fetch = [&](const SinkRows& w, int stage) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool in = w.seen[u] >= 0;
+      const size_t at = in ? (w.head + w.i[u]) * D + c * 8 : 0;
+      const uint32_t to = smem_u32(&sm.buf[warp][stage][0][u][0][lane]);
+#pragma unroll
+      for (int jj = 0; jj < NJ; ++jj) {
+        cp_async16(to + jj * 512, p.q + at + jj * 32, in);
+        cp_async16(to + (2 * NJ + jj) * 512, p.dout + at + jj * 32, in);
+        cp_async16(to + (4 * NJ + jj) * 512, p.o + at + jj * 32, in);
+      }
+    }
+  };
+  uint32_t unit = cta * kSinkWarps + warp;
+  SinkRows w;
+  if (unit < units) {
+    w = locate(unit);
+    fetch(w, 0);
+  }
+  cp_commit();
+
+  const __nv_bfloat16* kg = p.k + static_cast<size_t>(bh) * p.Lk * D;
+  const __nv_bfloat16* vg = p.v + static_cast<size_t>(bh) * p.Lk * D;
+  for (int x = static_cast<int>(threadIdx.x); x < NJ * 32; x += kSinkWarps * 32) {
+    const int jj = x >> 5, l = x & 31;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    const size_t at = static_cast<size_t>(l >> 2) * D + jj * 32 + (l & 3) * 8;
+    sm.ks[jj][l] = (l >> 2) < snk ? *reinterpret_cast<const uint4*>(kg + at) : none;
+    sm.vs[jj][l] = (l >> 2) < snk ? *reinterpret_cast<const uint4*>(vg + at) : none;
+    // dQ's tile 4 jj + e: columns n stand for d = 16 (2 jj + e / 2) + 4 (n / 2) + 2 (e % 2) + n % 2
+    uint32_t word[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = l >> 2, s0 = 2 * (l & 3);
+      const int d = 16 * (2 * jj + (e >> 1)) + 4 * (n >> 1) + 2 * (e & 1) + (n & 1);
+      const unsigned short* ku = reinterpret_cast<const unsigned short*>(kg) + d;
+      const uint32_t lo = s0 < snk ? ku[static_cast<size_t>(s0) * D] : 0u;
+      const uint32_t hi = s0 + 1 < snk ? ku[static_cast<size_t>(s0 + 1) * D] : 0u;
+      word[e] = lo | hi << 16;
+    }
+    sm.kt[jj][l] = make_uint4(word[0], word[1], word[2], word[3]);
+  }
+  __syncthreads();
+
+  float dk[D / 16][4], dv[D / 16][4];
+#pragma unroll
+  for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dk[t][e] = dv[t][e] = 0.f;
+  for (int stage = 0; unit < units; stage ^= 1) {
+    SinkRows next = w;
+    const bool more = units - unit > stride;
+    if (more) {
+      next = locate(unit + stride);
+      fetch(next, stage ^ 1);
+    }
+    cp_commit();
+    cp_wait<1>();                 // this unit's pieces (each lane reads what it copied)
+    const uint4* q = &sm.buf[warp][stage][0][0][0][lane];           // piece jj of row u: [(u NJ + jj) 32]
+    const uint4* d_o = q + 2 * NJ * 32;
+    const uint4* o = q + 4 * NJ * 32;
+    // ---- D: the diagonals of dO O^T, rows 0-7 and 8-15; row g's lies with c = g / 2 ----
+    float dd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) {
+      const uint4 d0 = d_o[jj * 32], d1 = d_o[(NJ + jj) * 32], o0 = o[jj * 32], o1 = o[(NJ + jj) * 32];
+      mma16816<false>(dd[0], d0.x, d1.x, d0.y, d1.y, o0.x, o0.y);
+      mma16816<false>(dd[1], d0.x, d1.x, d0.y, d1.y, o1.x, o1.y);
+      mma16816<false>(dd[0], d0.z, d1.z, d0.w, d1.w, o0.z, o0.w);
+      mma16816<false>(dd[1], d0.z, d1.z, d0.w, d1.w, o1.z, o1.w);
+    }
+    // ---- S and dP: rows g (0, 1) and g + 8 (2, 3), sinks 2 c and 2 c + 1 ----
+    auto products = [&](float (&sc)[4], float (&dp)[4], const uint4& kf, const uint4& vf, int jj) {
+      const uint4 q0 = q[jj * 32], q1 = q[(NJ + jj) * 32], d0 = d_o[jj * 32], d1 = d_o[(NJ + jj) * 32];
+      mma16816<false>(sc, q0.x, q1.x, q0.y, q1.y, kf.x, kf.y);
+      mma16816<false>(dp, d0.x, d1.x, d0.y, d1.y, vf.x, vf.y);
+      mma16816<false>(sc, q0.z, q1.z, q0.w, q1.w, kf.z, kf.w);
+      mma16816<false>(dp, d0.z, d1.z, d0.w, d1.w, vf.z, vf.w);
+    };
+    float sc[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) products(sc, dp, sm.ks[jj][lane], sm.vs[jj][lane], jj);
+    float pr[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      pr[e] = 2 * c + (e & 1) < w.seen[e >> 1] ? ex2(fmaf(sc[e], p.scale_log2, w.nl2[e >> 1])) : 0.f;
+    // ---- D of rows of few keys: the sum of P dP over the sinks and, 8 keys at a
+    // time, the others ----
+    float dl[2];
+    bool few[2];
+    int from = p.Lk, to = -1, lo[2], hi[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      dl[u] = __shfl_sync(0xFFFFFFFFu, (g & 1) ? dd[u][2 * u + 1] : dd[u][2 * u], (lane & 28) | (g >> 1));
+      few[u] = false;
+      if (w.seen[u] >= 0 && (w.i[u] < fr.first || w.i[u] >= fr.late)) {
+        const RowKeys rk = window_row_keys(p, w.i[u]);
+        few[u] = fr.has(rk, w.i[u]);
+        lo[u] = max(rk.lo, snk);
+        hi[u] = rk.lo + rk.nw - 1;
+        if (few[u] && lo[u] <= hi[u]) {
+          from = min(from, lo[u]);
+          to = max(to, hi[u]);
+        }
+      }
+    }
+    if (__any_sync(0xFFFFFFFFu, few[0] || few[1])) {
+      from = __reduce_min_sync(0xFFFFFFFFu, from);
+      to = __reduce_max_sync(0xFFFFFFFFu, to);
+      float y[2] = {pr[0] * dp[0] + pr[1] * dp[1], pr[2] * dp[2] + pr[3] * dp[3]};
+#pragma unroll 1
+      for (int k0 = from; k0 <= to; k0 += 8) {
+        const size_t at = static_cast<size_t>(min(k0 + g, p.Lk - 1)) * D + c * 8;
+        float sk[4] = {0.f, 0.f, 0.f, 0.f}, dk8[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int jj = 0; jj < NJ; ++jj)
+          products(sk, dk8, __ldg(reinterpret_cast<const uint4*>(kg + at + jj * 32)),
+                   __ldg(reinterpret_cast<const uint4*>(vg + at + jj * 32)), jj);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = k0 + 2 * c + (e & 1);
+          if (few[e >> 1] && key >= lo[e >> 1] && key <= hi[e >> 1])
+            y[e >> 1] = fmaf(ex2(fmaf(sk[e], p.scale_log2, w.nl2[e >> 1])), dk8[e], y[e >> 1]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        y[u] += __shfl_xor_sync(0xFFFFFFFFu, y[u], 1);
+        y[u] += __shfl_xor_sync(0xFFFFFFFFu, y[u], 2);
+        if (few[u]) dl[u] = y[u];
+      }
+    }
+    float4* acc[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (w.seen[u] >= 0 && c == 0) p.delta[w.head + w.i[u]] = dl[u];
+      acc[u] = reinterpret_cast<float4*>(p.dq_acc + (w.head + w.i[u]) * D) + c;
+    }
+    // ---- P and dS = scale P (dP - D), each as two bf16 parts ----
+    float ds[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      ds[e] = 2 * c + (e & 1) < w.seen[e >> 1] ? pr[e] * (dp[e] * p.scale - dl[e >> 1] * p.scale) : 0.f;
+    uint32_t ph[2], pl[2], sh[2], sl[2];              // rows g, g + 8
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      ph[u] = high_bf16(pr[2 * u], pr[2 * u + 1]);
+      pl[u] = pack_bf16(low_part(pr[2 * u]), low_part(pr[2 * u + 1]));
+      sh[u] = high_bf16(ds[2 * u], ds[2 * u + 1]);
+      sl[u] = pack_bf16(low_part(ds[2 * u]), low_part(ds[2 * u + 1]));
+    }
+    // ---- dQ: columns 4 c .. 4 c + 3 of every 16 ----
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) {
+      const uint4 kt = sm.kt[jj][lane];
+      const uint32_t kw[4] = {kt.x, kt.y, kt.z, kt.w};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816<false>(y0, sh[0], sh[1], sl[0], sl[1], kw[2 * x], kw[2 * x]);
+        mma16816<false>(y1, sh[0], sh[1], sl[0], sl[1], kw[2 * x + 1], kw[2 * x + 1]);
+        if (w.seen[0] >= 0) acc[0][4 * (2 * jj + x)] = make_float4(y0[0], y0[1], y1[0], y1[1]);
+        if (w.seen[1] >= 0) acc[1][4 * (2 * jj + x)] = make_float4(y0[2], y0[3], y1[2], y1[3]);
+      }
+    }
+    // ---- dK^T += Q^T dS, dV^T += dO^T P: 16 d's a tile, as S's steps have them ----
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      ph[u] = movm(ph[u]);
+      pl[u] = movm(pl[u]);
+      sh[u] = movm(sh[u]);
+      sl[u] = movm(sl[u]);
+    }
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) {
+      const uint4 q0 = q[jj * 32], q1 = q[(NJ + jj) * 32], d0 = d_o[jj * 32], d1 = d_o[(NJ + jj) * 32];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t a0 = movm(x ? q0.z : q0.x), a1 = movm(x ? q0.w : q0.y);
+        const uint32_t a2 = movm(x ? q1.z : q1.x), a3 = movm(x ? q1.w : q1.y);
+        const uint32_t b0 = movm(x ? d0.z : d0.x), b1 = movm(x ? d0.w : d0.y);
+        const uint32_t b2 = movm(x ? d1.z : d1.x), b3 = movm(x ? d1.w : d1.y);
+        mma16816<false>(dk[2 * jj + x], a0, a1, a2, a3, sh[0], sh[1]);
+        mma16816<false>(dv[2 * jj + x], b0, b1, b2, b3, ph[0], ph[1]);
+        mma16816<false>(dk[2 * jj + x], a0, a1, a2, a3, sl[0], sl[1]);
+        mma16816<false>(dv[2 * jj + x], b0, b1, b2, b3, pl[0], pl[1]);
+      }
+    }
+    if (!more) break;
+    w = next;
+    unit += stride;
+  }
+  __syncthreads();                // the buffers become the warps' sums
+  // ---- the warps' sums, added one warp after the other ----
+  for (int turn = 0; turn < kSinkWarps; ++turn) {
+    if (warp == turn) {
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // rows g (0, 1) and g + 8 (2, 3) of tile t
+          const int d = 32 * (t >> 1) + 8 * (g >> 1) + 4 * (t & 1) + (e & 2) + (g & 1);
+          const int s = 2 * c + (e & 1);
+          sm.sum[0][s][d] = (turn == 0 ? 0.f : sm.sum[0][s][d]) + dk[t][e];
+          sm.sum[1][s][d] = (turn == 0 ? 0.f : sm.sum[1][s][d]) + dv[t][e];
+        }
+    }
+    __syncthreads();
+  }
+  float* to = p.sink_part + static_cast<size_t>(blockIdx.x) * (2 * kFewSinks * D);
+  const float* from = &sm.sum[0][0][0];
+  for (int x = static_cast<int>(threadIdx.x); x < 2 * kFewSinks * D; x += kSinkWarps * 32) to[x] = from[x];
+}
+
+// dK and dV of the cut walks, their parts added in segment order, and of the
+// sinks that have a kernel of their own, its CTAs' parts added by a warp for
+// every 4 columns; and dQ (bf16) from the fp32 accumulator (the scale was applied
+// to dS already).
 template <int D>
 __global__ void __launch_bounds__(256) attn_bwd_window_post_kernel(const WindowBwdParams p) {
   const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long nthreads = static_cast<long long>(gridDim.x) * blockDim.x;
-  const long long n8 = static_cast<long long>(p.B) * p.H * p.Lq * D / 8;
-  for (long long x = tid; x < n8; x += nthreads) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p.dq_acc) + 2 * x);
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p.dq_acc) + 2 * x + 1);
-    uint4 w;
-    w.x = pack_bf16(a.x, a.y);
-    w.y = pack_bf16(a.z, a.w);
-    w.z = pack_bf16(b.x, b.y);
-    w.w = pack_bf16(b.z, b.w);
-    reinterpret_cast<uint4*>(p.dq)[x] = w;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const long long sink_cols = p.sink_ctas > 0 ? 2ll * p.B * p.Hkv * p.w.snk * (D / 4) : 0;
+  for (long long x = tid / 32; x < sink_cols; x += nthreads / 32) {
+    const int c4 = static_cast<int>(x % (D / 4));
+    const long long y = x / (D / 4);
+    const int key = static_cast<int>(y % p.w.snk);
+    const int which = static_cast<int>(y / p.w.snk % 2);     // 0: dK, 1: dV
+    const long long bh = y / p.w.snk / 2;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = lane; i < p.sink_ctas; i += 32) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p.sink_part) +
+                             (((bh * p.sink_ctas + i) * 2 + which) * kFewSinks + key) * (D / 4) + c4);
+      s.x += a.x;
+      s.y += a.y;
+      s.z += a.z;
+      s.w += a.w;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, off);
+      s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, off);
+      s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, off);
+      s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, off);
+    }
+    if (lane == 0)
+      *(reinterpret_cast<uint2*>((which ? p.dv : p.dk) + (bh * p.Lk + key) * D) + c4) =
+          make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
   }
   // one thread per 4 columns of a row of dK or dV of a cut tile
   const int BH = p.B * p.Hkv;
@@ -1030,7 +1352,7 @@ __global__ void __launch_bounds__(256) attn_bwd_window_post_kernel(const WindowB
       const int r = rest / (D / 4);
       const int c4 = rest - r * (D / 4);
       const int key = j * kTileN + r;
-      if (key >= p.Lk) continue;
+      if (key >= p.Lk || (p.sink_ctas > 0 && key < p.w.snk)) continue;     // (those sinks are written above)
       const float4* src = reinterpret_cast<const float4*>(p.part) +
                           (static_cast<size_t>(slot) * 2 + which) * (kTileN * D / 4) + rest;
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1047,6 +1369,17 @@ __global__ void __launch_bounds__(256) attn_bwd_window_post_kernel(const WindowB
       *(reinterpret_cast<uint2*>((which ? p.dv : p.dk) + (static_cast<size_t>(bh) * p.Lk + key) * D) + c4) = w;
     }
   }
+  const long long n8 = static_cast<long long>(p.B) * p.H * p.Lq * D / 8;
+  for (long long x = tid; x < n8; x += nthreads) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p.dq_acc) + 2 * x);
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p.dq_acc) + 2 * x + 1);
+    uint4 w;
+    w.x = pack_bf16(a.x, a.y);
+    w.y = pack_bf16(a.z, a.w);
+    w.z = pack_bf16(b.x, b.y);
+    w.w = pack_bf16(b.z, b.w);
+    reinterpret_cast<uint4*>(p.dq)[x] = w;
+  }
 }
 
 // How the walks are cut, and where the parts go.
@@ -1055,14 +1388,23 @@ struct WindowBwdPlan {
   WindowTiles tiles[2];
   long long slots, n_cta;
   bool persistent;
-  size_t part_off, bytes;
+  int sink_ctas;
+  size_t part_off, sink_off, bytes;
 };
 WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, const WindowMask& w) {
   WindowBwdPlan pl{};
   const long long nq = (static_cast<long long>(Lq) + kTileM - 1) / kTileM;
   const long long G = H / Hkv, BH = static_cast<long long>(B) * Hkv;
   pl.nk = static_cast<int>((static_cast<long long>(Lk) + kTileN - 1) / kTileN);
-  pl.nst = static_cast<int>((static_cast<long long>(w.snk) + kTileN - 1) / kTileN);
+  const long long sink_tiles = (static_cast<long long>(w.snk) + kTileN - 1) / kTileN;
+  // a few sinks have a kernel of their own; the main kernel walks their tile for
+  // the windows over its other keys alone
+  if (w.snk > 0 && w.snk <= kFewSinks && Lq - 1 + w.sh >= 0) {
+    const long long units = G * ((static_cast<long long>(Lq) + 15) / 16);
+    pl.sink_ctas = static_cast<int>(std::max(1ll, std::min((units + kSinkWarps - 1) / kSinkWarps,
+                                                           152ll * kSinkCtasPerSm / BH)));
+  }
+  pl.nst = pl.sink_ctas > 0 ? 0 : static_cast<int>(sink_tiles);
   // query tiles that a tile without sinks meets at most, over its heads
   const long long share = std::min(nq, std::min<long long>(w.window, 1ll << 40) / kTileM + 2) * G;
   const long long rest = pl.nk - pl.nst;
@@ -1089,6 +1431,18 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   // cost more than it gave there (104 items of 40 tiles on 152 SMs: 6 us more).
   pl.tiles[0] = WindowTiles{0, pl.nst, static_cast<int>(seg_s), 0, 0};
   pl.tiles[1] = WindowTiles{pl.nst, static_cast<int>(rest), static_cast<int>(seg_w), 0, 0};
+  // Without the sinks' segments, which filled the SMs beside a last wave of
+  // items that leaves some idle, its walks are cut to fill them (where they are
+  // not short already, at the sequence's end): 474 -> 436 us at B1 H16(4) L16384
+  // d128, window 1024.
+  if (pl.sink_ctas > 0 && seg_w == 1 && BH * rest > 152) {
+    const long long nt = (BH * rest % 152 + BH - 1) / BH;         // key tiles of the last wave
+    const long long cut = nt > 0 ? 152 / (nt * BH) : 1;
+    if (cut > 1 && share / G <= nt) {
+      pl.tiles[0] = WindowTiles{0, static_cast<int>(rest - nt), 1, 0, 0};
+      pl.tiles[1] = WindowTiles{static_cast<int>(rest - nt), static_cast<int>(nt), static_cast<int>(cut), 0, 0};
+    }
+  }
   for (WindowTiles& t : pl.tiles) {
     if (t.n == 0) t.seg = 1;
     t.item0 = static_cast<int>(std::min(pl.n_cta, 0x7FFFFFFFll));       // (a launch that passes it is refused)
@@ -1097,7 +1451,8 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
     if (t.seg > 1) pl.slots += BH * t.n * t.seg;
   }
   pl.part_off = (static_cast<size_t>(B) * H * Lq * d * 4 + 255) & ~static_cast<size_t>(255);
-  pl.bytes = pl.part_off + static_cast<size_t>(pl.slots) * 2 * kTileN * d * 4;
+  pl.sink_off = pl.part_off + static_cast<size_t>(pl.slots) * 2 * kTileN * d * 4;
+  pl.bytes = pl.sink_off + static_cast<size_t>(BH) * pl.sink_ctas * 2 * kFewSinks * d * 4;
   return pl;
 }
 
@@ -1123,17 +1478,30 @@ cudaError_t launch_window_bwd(const CUtensorMap& tq, const CUtensorMap& tk, cons
     if (fa.numRegs < static_cast<int>(WinBwdRegs<D>::kLaunchRegs)) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attn_bwd_window_sink_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sizeof(SinkSmem<D>)));
+    if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
   const long long rows = static_cast<long long>(p.B) * p.H * p.Lq;
   const FewRows few = window_few_rows(p);
-  const long long n_few = (few.first + p.Lq - few.late) * p.B * p.H;
-  const int few_blocks = n_few > 0 ? static_cast<int>(window_grid(n_few * 32)) : 0;
-  // (together no more than the two waves that either takes alone)
-  const int stream_blocks =
-      std::max(1, std::min(static_cast<int>(window_grid(rows * (D / 8))), std::max(152 * 8, 152 * 16 - few_blocks)));
-  attn_bwd_window_pre_kernel<D><<<stream_blocks + few_blocks, 256, 0, st>>>(p, few, few_blocks);
+  if (p.sink_ctas > 0) {
+    attn_bwd_window_sink_kernel<D><<<static_cast<unsigned>(p.B * p.Hkv * p.sink_ctas), kSinkWarps * 32,
+                                     sizeof(SinkSmem<D>), st>>>(p, few);
+  } else {
+    const long long n_few = (few.first + p.Lq - few.late) * p.B * p.H;
+    const int few_blocks = n_few > 0 ? static_cast<int>(window_grid(n_few * 32)) : 0;
+    // (together no more than the two waves that either takes alone)
+    const int stream_blocks =
+        std::max(1, std::min(static_cast<int>(window_grid(rows * (D / 8))), std::max(152 * 8, 152 * 16 - few_blocks)));
+    attn_bwd_window_pre_kernel<D><<<stream_blocks + few_blocks, 256, 0, st>>>(p, few, few_blocks);
+  }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  WindowBwdParams pm = p;
+  if (p.sink_ctas > 0) {
+    pm.first_key = p.w.snk;
+    pm.w.snk = 0;
+  }
   // optional timing of the main kernel alone (attn_bwd_time_main)
   cudaEvent_t begin, end;
   bwd_main_events(&begin, &end);
@@ -1142,7 +1510,7 @@ cudaError_t launch_window_bwd(const CUtensorMap& tq, const CUtensorMap& tk, cons
     int sms = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(persistent ? std::min<long long>(n_cta, sms) : n_cta);
-    kern<<<grid, C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, tdo, tdq, p);
+    kern<<<grid, C::kThreads, C::kSmemBytes, st>>>(tq, tk, tv, tdo, tdq, pm);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (end && (e = cudaEventRecord(end, st)) != cudaSuccess) return e;
@@ -1224,6 +1592,8 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.part_off);
+  p.sink_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.sink_off);
+  p.sink_ctas = pl.sink_ctas;
   p.nk = pl.nk;
   p.nst = pl.nst;
   for (int i = 0; i < 2; ++i) p.tiles[i] = pl.tiles[i];

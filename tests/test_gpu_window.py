@@ -324,3 +324,56 @@ def test_rows_of_few_keys(bss, H, Hkv, Lq, Lk, d, window, sinks, qo, ko):
     if seen.any():
         rough = (do.double() * o.double()).sum(-1)
         assert ((rough - want[3]).abs() > bound[3])[:, :, seen].any()
+
+
+@pytest.mark.parametrize("B,H,Hkv,Lq,Lk,d,window,sinks,qo,ko", [
+    (2, 12, 3, 1111, 1111, 64, 70, 8, 0, 0),       # as many sinks as share a kernel of their own
+    (2, 12, 3, 1111, 1111, 64, 70, 9, 0, 0),       # ... one more
+    (1, 16, 16, 37, 37, 128, 5, 8, 0, 0),
+    (3, 4, 1, 203, 203, 128, 1000, 5, 0, 0),       # a window past every length
+    (1, 6, 2, 100, 900, 128, 256, 7, 800, 0),      # a prompt's next chunk
+    (1, 4, 2, 500, 700, 64, 60, 7, 900, 4),        # three of seven sinks, queries past the window
+    (1, 2, 1, 300, 6, 128, 4, 8, 0, 0),            # nothing but sinks
+    (1, 2, 2, 400, 200, 64, 30, 130, 0, 123),      # seven of 130
+    (1, 200, 100, 40, 40, 64, 7, 2, 0, 0),
+    (1, 16, 4, 5000, 5000, 128, 300, 4, 0, 0),     # a last wave of key tiles that is cut
+])
+def test_few_sinks(bss, B, H, Hkv, Lq, Lk, d, window, sinks, qo, ko):
+    test_forward_and_backward(bss, B, H, Hkv, Lq, Lk, d, window, sinks, qo, ko)
+
+
+@pytest.mark.parametrize("H,Hkv,L,d,window,sinks", [(8, 2, 4000, 128, 24, 4), (4, 4, 3001, 64, 20, 8),
+                                                    (8, 1, 2500, 128, 700, 1), (6, 3, 2000, 64, 100, 5)])
+def test_gradients_of_sinks(bss, H, Hkv, L, d, window, sinks):
+    """A sink's dK and dV add up thousands of queries, so elements near 0 show what rounding P and dS
+    leaves: two bf16 parts hold all but 2^-15 of each, which over independent terms adds up to
+    2^-15 / sqrt(3) of the root of their squares' sum; 2^-12, 14 of those, covers every element and
+    the fp32 scores and sums.  (A single bf16 part leaves 2^-8 / sqrt(3).)  dK so where every row
+    takes D from its definition; else D's rounded O adds 2^-8 / sqrt(3) of the root of sum dO^2 O^2,
+    a row, and 6 of those count."""
+    g = torch.Generator("cuda").manual_seed(L)
+    q, do = (torch.randn(1, H, L, d, generator=g, device="cuda") for _ in range(2))
+    k, v = (torch.randn(1, Hkv, L, d, generator=g, device="cuda") for _ in range(2))
+    lead = 0.4 * torch.randn(1, Hkv, 1, d, generator=g, device="cuda")
+    q = q + lead.repeat_interleave(H // Hkv, 1)
+    k[:, :, :sinks] += 2 * lead
+    q, k, v, do = (t.bfloat16() for t in (q, k, v, do))
+    o, lse = bss.attn_fwd_window(q, k, v, window, sinks=sinks)
+    _, dk, dv, _ = bss.attn_bwd_window(q, k, v, o, lse, do, window, sinks=sinks)
+    assert bss.attn_poll_status() == 0
+    scale = d ** -0.5
+    O, _, P = ref.forward(q, k, v, ref.window_mask(L, L, window, sinks, device="cuda"), scale)
+    P, qq, dd = P[..., :sinks], q.double(), do.double()
+    vv = v[:, :, :sinks].double().repeat_interleave(H // Hkv, 1)
+    dS = scale * P * (dd @ vv.transpose(-1, -2) - (dd * O).sum(-1, keepdim=True))
+    fold = lambda x: x.reshape(1, Hkv, H // Hkv, sinks, d).sum(2)  # noqa: E731
+    each = lambda a, b: fold((a ** 2).transpose(-1, -2) @ b ** 2).sqrt()  # noqa: E731
+    for got, a, b in ((dv, P, dd), (dk, dS, qq)):
+        want = fold(a.transpose(-1, -2) @ b)
+        tail = 2.0 ** -12 * each(a, b)
+        if got is dk and window + sinks > 32:
+            off_d = 2.0 ** -8 / 3 ** 0.5 * ((dd * O) ** 2).sum(-1, keepdim=True).sqrt()
+            tail = tail + 6 * each(scale * P * off_d, qq)
+        off = (got[:, :, :sinks].double() - want).abs()
+        bound = 2.0 ** -8 * want.abs() + tail
+        assert (off <= bound).all(), (off / bound).max()

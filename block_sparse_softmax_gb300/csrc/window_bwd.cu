@@ -75,8 +75,8 @@ struct WindowBwdParams {
   __nv_bfloat16* dv;
   float* part;          // fp32 [slot][dK, dV][128][d]: parts of the cut walks
   float* sink_part;     // fp32 [B H_kv][sink_ctas][dK, dV][kFewSinks][d]
-  int sink_ctas;        // CTAs of a K/V head in the sinks' kernel (0: the main kernel takes the sinks)
-  int first_key;        // the main kernel's first key (those below have the sinks' kernel)
+  int sink_ctas;        // CTAs of a K/V head in the sinks' kernel (0: not launched)
+  int few_sinks;        // the first keys, which it takes and the main kernel leaves out
   int nk;               // key tiles
   int nst;              // the first of them, which meet every later query tile for a sink key
   WindowTiles tiles[2]; // those, and the others, in the order of their items
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(WinBwdCfg<D>::kThreads, 1)
       {
         const long long tile = static_cast<long long>(key0) - p.w.sh - static_cast<long long>(i) * kTileM;
         const int own = clamped(tile, -kTileM, kTileM) + kr - 64 * X;
-        const int qlo = key < Lk && key >= p.first_key ? own : 64;
+        const int qlo = key < Lk && key >= p.few_sinks ? own : 64;
         const int end = key < p.w.snk ? 64 : clamped(tile + p.w.window, -kTileM, kTileM) + kr - 64 * X;
         seen[0] = bits_below(end) & ~bits_below(qlo);
         seen[1] = bits_below(end - 32) & ~bits_below(qlo - 32);
@@ -890,10 +890,11 @@ struct FewRows {
     return (i < first || i >= late) && rk.nsk + rk.nw <= kFewKeys;
   }
 };
+bool every_row_few(const WindowMask& w, int Lk) { return w.window + w.snk <= kFewWindow || Lk <= kFewKeys; }
 FewRows window_few_rows(const WindowBwdParams& p) {
   FewRows f;
   const long long Lq = p.Lq;
-  if (p.w.window + p.w.snk <= kFewWindow || p.Lk <= kFewKeys) {
+  if (every_row_few(p.w, p.Lk)) {
     f.first = f.late = Lq;
   } else {
     f.first = std::max(0ll, std::min(Lq, kFewKeys - p.w.sh));
@@ -912,8 +913,9 @@ FewRows window_few_rows(const WindowBwdParams& p) {
 // which one is a heavy sink 5.2e-3 and 3.3e-3).  Rows of few keys therefore
 // take the definition, D_i = sum_j P_ij dP_ij, in fp32: a warp a row, two lanes
 // a key, 16 keys at a time.  Rows of a wide window have few keys only near the
-// first key and past the last; under a window of up to 32 keys every row takes
-// its time (at 16384 rows of 16 heads about as long as the main kernel).
+// first key and past the last.  Where every row has (under a window of up to 32
+// keys), the sinks' kernel takes them (B1 H16(4) L16384 d128, window 28: a call in
+// 255 us, a warp a row 1140).
 template <int D>
 __global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBwdParams p, const FewRows fr,
                                                                   int few_blocks) {
@@ -1002,9 +1004,9 @@ __global__ void __launch_bounds__(256) attn_bwd_window_pre_kernel(const WindowBw
   }
 }
 
-// The same where up to kFewSinks keys are sinks (snk of them), and all that
-// comes of the pairs of a query with a sink: their dQ, which the accumulator
-// starts from, and parts of the sinks' dK and dV.
+// The same where up to kFewSinks keys are sinks, and all that comes of the pairs
+// of a query with a sink: their dQ, which the accumulator starts from, and parts
+// of the sinks' dK and dV.  (few_sinks = 0: D alone, of rows of few keys.)
 //
 // A sink's dK and dV are sums over every later query of every head of its
 // group: elements of a hundred times the other keys', of which a P and a dS
@@ -1058,7 +1060,7 @@ __global__ void __launch_bounds__(kSinkWarps * 32, kSinkCtasPerSm)
   SinkSmem<D>& sm = *reinterpret_cast<SinkSmem<D>*>(sink_smem);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int g = lane >> 2, c = lane & 3;
-  const int snk = p.w.snk;
+  const int snk = p.few_sinks;
   const int bh = static_cast<int>(blockIdx.x) / p.sink_ctas;
   const int cta = static_cast<int>(blockIdx.x) - bh * p.sink_ctas;
   const int b = bh / p.Hkv, hkv = bh - b * p.Hkv;
@@ -1169,10 +1171,10 @@ __global__ void __launch_bounds__(kSinkWarps * 32, kSinkCtasPerSm)
     for (int e = 0; e < 4; ++e)
       pr[e] = 2 * c + (e & 1) < w.seen[e >> 1] ? ex2(fmaf(sc[e], p.scale_log2, w.nl2[e >> 1])) : 0.f;
     // ---- D of rows of few keys: the sum of P dP over the sinks and, 8 keys at a
-    // time, the others ----
+    // time, the others: sinks past those, then the window ----
     float dl[2];
     bool few[2];
-    int from = p.Lk, to = -1, lo[2], hi[2];
+    int from[2] = {snk, p.Lk}, to[2] = {-1, -1}, lo[2], hi[2], nsk[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       dl[u] = __shfl_sync(0xFFFFFFFFu, (g & 1) ? dd[u][2 * u + 1] : dd[u][2 * u], (lane & 28) | (g >> 1));
@@ -1182,29 +1184,33 @@ __global__ void __launch_bounds__(kSinkWarps * 32, kSinkCtasPerSm)
         few[u] = fr.has(rk, w.i[u]);
         lo[u] = max(rk.lo, snk);
         hi[u] = rk.lo + rk.nw - 1;
+        nsk[u] = rk.nsk;
+        if (few[u]) to[0] = max(to[0], nsk[u] - 1);
         if (few[u] && lo[u] <= hi[u]) {
-          from = min(from, lo[u]);
-          to = max(to, hi[u]);
+          from[1] = min(from[1], lo[u]);
+          to[1] = max(to[1], hi[u]);
         }
       }
     }
     if (__any_sync(0xFFFFFFFFu, few[0] || few[1])) {
-      from = __reduce_min_sync(0xFFFFFFFFu, from);
-      to = __reduce_max_sync(0xFFFFFFFFu, to);
       float y[2] = {pr[0] * dp[0] + pr[1] * dp[1], pr[2] * dp[2] + pr[3] * dp[3]};
 #pragma unroll 1
-      for (int k0 = from; k0 <= to; k0 += 8) {
-        const size_t at = static_cast<size_t>(min(k0 + g, p.Lk - 1)) * D + c * 8;
-        float sk[4] = {0.f, 0.f, 0.f, 0.f}, dk8[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int part = 0; part < 2; ++part) {
+        const int end = __reduce_max_sync(0xFFFFFFFFu, part ? to[1] : to[0]);
+#pragma unroll 1
+        for (int k0 = __reduce_min_sync(0xFFFFFFFFu, part ? from[1] : from[0]); k0 <= end; k0 += 8) {
+          const size_t at = static_cast<size_t>(min(k0 + g, p.Lk - 1)) * D + c * 8;
+          float sk[4] = {0.f, 0.f, 0.f, 0.f}, dk8[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int jj = 0; jj < NJ; ++jj)
-          products(sk, dk8, __ldg(reinterpret_cast<const uint4*>(kg + at + jj * 32)),
-                   __ldg(reinterpret_cast<const uint4*>(vg + at + jj * 32)), jj);
+          for (int jj = 0; jj < NJ; ++jj)
+            products(sk, dk8, __ldg(reinterpret_cast<const uint4*>(kg + at + jj * 32)),
+                     __ldg(reinterpret_cast<const uint4*>(vg + at + jj * 32)), jj);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = k0 + 2 * c + (e & 1);
-          if (few[e >> 1] && key >= lo[e >> 1] && key <= hi[e >> 1])
-            y[e >> 1] = fmaf(ex2(fmaf(sk[e], p.scale_log2, w.nl2[e >> 1])), dk8[e], y[e >> 1]);
+          for (int e = 0; e < 4; ++e) {
+            const int u = e >> 1, key = k0 + 2 * c + (e & 1);
+            if (few[u] && (part ? key >= lo[u] && key <= hi[u] : key < nsk[u]))
+              y[u] = fmaf(ex2(fmaf(sk[e], p.scale_log2, w.nl2[u])), dk8[e], y[u]);
+          }
         }
       }
 #pragma unroll
@@ -1219,6 +1225,17 @@ __global__ void __launch_bounds__(kSinkWarps * 32, kSinkCtasPerSm)
     for (int u = 0; u < 2; ++u) {
       if (w.seen[u] >= 0 && c == 0) p.delta[w.head + w.i[u]] = dl[u];
       acc[u] = reinterpret_cast<float4*>(p.dq_acc + (w.head + w.i[u]) * D) + c;
+    }
+    if (snk == 0) {               // D alone was wanted
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          if (w.seen[u] >= 0) acc[u][4 * x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!more) break;
+      w = next;
+      unit += stride;
+      continue;
     }
     // ---- P and dS = scale P (dP - D), each as two bf16 parts ----
     float ds[4];
@@ -1274,6 +1291,7 @@ __global__ void __launch_bounds__(kSinkWarps * 32, kSinkCtasPerSm)
     w = next;
     unit += stride;
   }
+  if (snk == 0) return;
   __syncthreads();                // the buffers become the warps' sums
   // ---- the warps' sums, added one warp after the other ----
   for (int turn = 0; turn < kSinkWarps; ++turn) {
@@ -1305,13 +1323,13 @@ __global__ void __launch_bounds__(256) attn_bwd_window_post_kernel(const WindowB
   const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long nthreads = static_cast<long long>(gridDim.x) * blockDim.x;
   const int lane = static_cast<int>(threadIdx.x & 31);
-  const long long sink_cols = p.sink_ctas > 0 ? 2ll * p.B * p.Hkv * p.w.snk * (D / 4) : 0;
+  const long long sink_cols = 2ll * p.B * p.Hkv * p.few_sinks * (D / 4);
   for (long long x = tid / 32; x < sink_cols; x += nthreads / 32) {
     const int c4 = static_cast<int>(x % (D / 4));
     const long long y = x / (D / 4);
-    const int key = static_cast<int>(y % p.w.snk);
-    const int which = static_cast<int>(y / p.w.snk % 2);     // 0: dK, 1: dV
-    const long long bh = y / p.w.snk / 2;
+    const int key = static_cast<int>(y % p.few_sinks);
+    const int which = static_cast<int>(y / p.few_sinks % 2);     // 0: dK, 1: dV
+    const long long bh = y / p.few_sinks / 2;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = lane; i < p.sink_ctas; i += 32) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(p.sink_part) +
@@ -1352,7 +1370,7 @@ __global__ void __launch_bounds__(256) attn_bwd_window_post_kernel(const WindowB
       const int r = rest / (D / 4);
       const int c4 = rest - r * (D / 4);
       const int key = j * kTileN + r;
-      if (key >= p.Lk || (p.sink_ctas > 0 && key < p.w.snk)) continue;     // (those sinks are written above)
+      if (key >= p.Lk || key < p.few_sinks) continue;          // (those sinks are written above)
       const float4* src = reinterpret_cast<const float4*>(p.part) +
                           (static_cast<size_t>(slot) * 2 + which) * (kTileN * D / 4) + rest;
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1388,7 +1406,7 @@ struct WindowBwdPlan {
   WindowTiles tiles[2];
   long long slots, n_cta;
   bool persistent;
-  int sink_ctas;
+  int sink_ctas, few_sinks;
   size_t part_off, sink_off, bytes;
 };
 WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, const WindowMask& w) {
@@ -1399,12 +1417,14 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   const long long sink_tiles = (static_cast<long long>(w.snk) + kTileN - 1) / kTileN;
   // a few sinks have a kernel of their own; the main kernel walks their tile for
   // the windows over its other keys alone
-  if (w.snk > 0 && w.snk <= kFewSinks && Lq - 1 + w.sh >= 0) {
+  if (w.snk <= kFewSinks && Lq - 1 + w.sh >= 0) pl.few_sinks = w.snk;
+  // ... which also takes D where every row has it from its definition
+  if (pl.few_sinks > 0 || every_row_few(w, Lk)) {
     const long long units = G * ((static_cast<long long>(Lq) + 15) / 16);
     pl.sink_ctas = static_cast<int>(std::max(1ll, std::min((units + kSinkWarps - 1) / kSinkWarps,
                                                            152ll * kSinkCtasPerSm / BH)));
   }
-  pl.nst = pl.sink_ctas > 0 ? 0 : static_cast<int>(sink_tiles);
+  pl.nst = pl.few_sinks > 0 ? 0 : static_cast<int>(sink_tiles);
   // query tiles that a tile without sinks meets at most, over its heads
   const long long share = std::min(nq, std::min<long long>(w.window, 1ll << 40) / kTileM + 2) * G;
   const long long rest = pl.nk - pl.nst;
@@ -1435,7 +1455,7 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   // items that leaves some idle, its walks are cut to fill them (where they are
   // not short already, at the sequence's end): 474 -> 436 us at B1 H16(4) L16384
   // d128, window 1024.
-  if (pl.sink_ctas > 0 && seg_w == 1 && BH * rest > 152) {
+  if (pl.few_sinks > 0 && seg_w == 1 && BH * rest > 152) {
     const long long nt = (BH * rest % 152 + BH - 1) / BH;         // key tiles of the last wave
     const long long cut = nt > 0 ? 152 / (nt * BH) : 1;
     if (cut > 1 && share / G <= nt) {
@@ -1452,7 +1472,7 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   }
   pl.part_off = (static_cast<size_t>(B) * H * Lq * d * 4 + 255) & ~static_cast<size_t>(255);
   pl.sink_off = pl.part_off + static_cast<size_t>(pl.slots) * 2 * kTileN * d * 4;
-  pl.bytes = pl.sink_off + static_cast<size_t>(BH) * pl.sink_ctas * 2 * kFewSinks * d * 4;
+  pl.bytes = pl.sink_off + (pl.few_sinks > 0 ? static_cast<size_t>(BH) * pl.sink_ctas * 2 * kFewSinks * d * 4 : 0);
   return pl;
 }
 
@@ -1498,10 +1518,7 @@ cudaError_t launch_window_bwd(const CUtensorMap& tq, const CUtensorMap& tk, cons
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   WindowBwdParams pm = p;
-  if (p.sink_ctas > 0) {
-    pm.first_key = p.w.snk;
-    pm.w.snk = 0;
-  }
+  if (p.few_sinks > 0) pm.w.snk = 0;
   // optional timing of the main kernel alone (attn_bwd_time_main)
   cudaEvent_t begin, end;
   bwd_main_events(&begin, &end);
@@ -1594,6 +1611,7 @@ extern "C" attn_status_t attn_bwd_window(const void* q, const void* k, const voi
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.part_off);
   p.sink_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.sink_off);
   p.sink_ctas = pl.sink_ctas;
+  p.few_sinks = pl.few_sinks;
   p.nk = pl.nk;
   p.nst = pl.nst;
   for (int i = 0; i < 2; ++i) p.tiles[i] = pl.tiles[i];

@@ -337,6 +337,10 @@ def test_rows_of_few_keys(bss, H, Hkv, Lq, Lk, d, window, sinks, qo, ko):
     (1, 2, 2, 400, 200, 64, 30, 130, 0, 123),      # seven of 130
     (1, 200, 100, 40, 40, 64, 7, 2, 0, 0),
     (1, 16, 4, 5000, 5000, 128, 300, 4, 0, 0),     # a last wave of key tiles that is cut
+    (1, 4, 2, 700, 700, 128, 20, 12, 0, 0),        # every row of few keys: more sinks than share a kernel
+    (1, 4, 4, 700, 700, 64, 32, 0, 0, 0),          # ... none
+    (2, 4, 1, 500, 40, 128, 50, 13, 5, 0),         # ... no more keys than that
+    (1, 4, 2, 300, 64, 64, 10, 40, 0, 0),
 ])
 def test_few_sinks(bss, B, H, Hkv, Lq, Lk, d, window, sinks, qo, ko):
     test_forward_and_backward(bss, B, H, Hkv, Lq, Lk, d, window, sinks, qo, ko)
@@ -377,3 +381,20 @@ def test_gradients_of_sinks(bss, H, Hkv, L, d, window, sinks):
         off = (got[:, :, :sinks].double() - want).abs()
         bound = 2.0 ** -8 * want.abs() + tail
         assert (off <= bound).all(), (off / bound).max()
+
+
+def test_rows_of_few_keys_with_more_sinks(bss):
+    """The rows' D where every row takes it from its definition and the sinks are too many for a
+    kernel of their own."""
+    for args in ((4, 2, 700, 700, 128, 20, 12, 0, 0), (4, 4, 500, 40, 64, 50, 13, 5, 0),
+                 (2, 1, 300, 64, 128, 10, 40, 0, 0), (4, 4, 600, 600, 64, 32, 0, 0, 0)):
+        test_rows_of_few_keys(bss, *args)
+
+
+def test_sinks_without_a_key(bss):
+    q, k, v, do = inputs(1, 2, 1, 90, 0, 128, 1)
+    o, lse = bss.attn_fwd_window(q, k, v, 10, sinks=4)
+    dq, dk, dv, delta = bss.attn_bwd_window(q, k, v, o, lse, do, 10, sinks=4)
+    assert bss.attn_poll_status() == 0
+    assert torch.all(o == 0) and torch.all(torch.isneginf(lse))
+    assert torch.all(dq == 0) and torch.all(delta == 0) and dk.numel() == dv.numel() == 0

@@ -41,17 +41,17 @@
 //   * e4m3 pages are read as they are (half the bytes); a pair of elements
 //     becomes fp16 by one conversion, exactly, on the way into an fp16 MMA.
 //     (Going on to bf16 takes four instructions: 128 sequences of up to 16384
-//     tokens took 174 us that way, 148 so.)  So that Q and P lose nothing
+//     tokens took 174 us that way, 150 so.)  So that Q and P lose nothing
 //     there that bf16 holds, a head's Q is scaled by a power of two (largest
 //     element in [128, 256)) and P by 2^12: fp16 then rounds by at most 2^-32
 //     of Q's largest element, 2^-37 of P's.  The caches' scales multiply the
 //     score and the output.
 // Measured (GPU time, d=128, 4 K/V heads of 4 query heads where not said):
-//   2 sequences of 131071 tokens, 8 heads    159 us, 6.7 TB/s (99 % of a copy's)
-//   128 of up to 16384 tokens, e4m3          148 us, 6.2 TB/s (92 %)
+//   2 sequences of 131071 tokens, 8 heads    161 us, 6.7 TB/s (98 % of a copy's)
+//   128 of up to 16384 tokens, e4m3          150 us, 6.1 TB/s (91 %)
 //   32 of up to 8192 tokens                   50 us, 4.7 TB/s (69 %)
 //   64 of up to 16384 tokens, window 1000,
-//     4 sinks, d=64, 16 heads                 46 us, 4.7 TB/s (70 %)
+//     4 sinks, d=64, 16 heads                 46 us, 4.7 TB/s (69 %)
 // What the last two lose is about 6 us until the first keys land (lengths,
 // table and data, one after the other), 4 us between the first and the last
 // warp's end, 5 us for the join and 4 us for the two launches.

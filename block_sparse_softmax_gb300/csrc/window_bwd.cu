@@ -22,16 +22,17 @@
 // come in the order the CTAs reach them, so its last bit may differ.
 //
 // P and dS are rounded to bf16 as the operands of their products, all else is
-// fp32 until the results: dQ and dK come out 2.4e-3 to 2.7e-3 off in norm
-// (rounding them alone costs 1.7e-3).
+// fp32 until the results: dQ and dK come out 2.4e-3 off in norm, dV 2.3e-3
+// (rounding them alone costs 1.65e-3).  The pairs with up to kFewSinks sinks take
+// two bf16 parts: 2.0e-3, 2.0e-3 and 1.7e-3 off in the first case below.
 //
-// Measured, B1 H16(4) L16384 d128, window 1024, sinks 4: D and clearing 40 us
-// (HBM: 268 MB), main kernel 391 us (855 TFLOP/s of allowed pairs), dQ 27 us
-// (HBM: 201 MB, part of it from L2).  What sets the main kernel's pace is the
-// chain of hand-offs of a query tile, dQ -> drain -> dP^T -> dS -> dQ, as in
-// the dense backward (tensor pipe 48 % busy while an SM has a CTA), and an
+// Measured, B1 H16(4) L16384 d128, window 1024, sinks 4: D and the sinks 59 us
+// (HBM: 336 MB), main kernel 343 us (970 TFLOP/s of allowed pairs), dQ and parts
+// 30 us (HBM: 220 MB, part of it from L2).  What sets the main kernel's pace is
+// the chain of hand-offs of a query tile, dQ -> drain -> dP^T -> dS -> dQ, as in
+// the dense backward (tensor pipe 49 % busy while an SM has a CTA), and an
 // item's set-up and epilogue over walks of 10 tiles a head.
-// B4 H16 L2000 d64, window 256: 16, 67 and 8.5 us.
+// B4 H16 L2000 d64, window 256: D and clearing 16, main kernel 67, dQ 9.5 us.
 #include <algorithm>
 
 #include "host.cuh"

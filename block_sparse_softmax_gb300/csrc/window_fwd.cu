@@ -26,8 +26,9 @@
 //           O while the softmax works on the next item.
 // With the softmax warps writing O themselves an item of one pair took 12000
 // cycles and every further pair 3100: 410 us for B2 H16(4) L16384 d128, window
-// 1024, sinks 4.  So it takes 287 us: 930 TFLOP/s of allowed pairs, 1160 of
-// executed blocks (61 % of a large bf16 product's).  An item's 20400 cycles are
+// 1024, sinks 4.  So it takes 287 us in a graph (290 to 293 called from Python):
+// 930 TFLOP/s of allowed pairs, 1160 of executed blocks (61 % of a large bf16
+// product's).  An item's 20400 cycles are
 // 14300 of MMAs (5 pairs); a plain step takes 3300, the two masked ones 1200
 // and 600 more (with 64-bit limits in every row 1600 and 900: 310 us), an
 // item's end 1300, and the next item's Q comes late, after the last S has freed
@@ -38,6 +39,10 @@
 //
 // The element mask is applied in the blocks that the diagonal, the window's
 // lower edge or the last sink crosses; all others run without it.
+//
+// P is rounded to bf16, V's type, which one tcgen05.mma wants of both operands
+// (its rest as a second product would add half of an item's MMAs): O is 1.9e-3
+// off in norm, of which its own rounding is 1.65e-3.
 #include <algorithm>
 #include <mutex>
 

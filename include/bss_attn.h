@@ -351,6 +351,9 @@ attn_status_t attn_bwd_noalloc(const void* q, const void* k, const void* v, cons
  *   128-query tile's window, and the sink blocks.
  *   Keys and values are taken as finite: a NaN or infinity in v reaches the
  *   queries of every 128-query tile that reads its block.
+ *   Scores, maxima, sums and O are fp32; the probabilities are rounded to bf16
+ *   for their product with v, as in attn_fwd (O comes out about 1.9e-3 off in
+ *   norm, of which rounding O itself is 1.65e-3).
  */
 attn_status_t attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse,
                               int B, int H, int H_kv, int Lq, int Lk, int d, float scale,
@@ -370,12 +373,18 @@ attn_status_t attn_fwd_window(const void* q, const void* k, const void* v, void*
  *   the same without O's rounding.  A query that sees no key gets dq = 0; a
  *   key that no query sees gets dk = dv = 0.  Inputs are taken as finite, as in
  *   attn_fwd_window.
+ *   P and dS are rounded to bf16 for their products, as in attn_bwd, all else
+ *   is fp32 (gradients about 2.4e-3 off in norm, of which rounding them is
+ *   1.65e-3; more where one key has most of a query's weight, by the rounding
+ *   of O in delta).  With up to 8 sinks in the call, whose dk and dv add up
+ *   every later query, the pairs with a sink take P and dS in two bf16 parts
+ *   (2^-15).
  *   dk and dv are the same in every run.  dq is accumulated in fp32 in the
  *   order the key tiles finish, so its last bit may differ from run to run.
  *   workspace: device, 16-byte aligned, >= attn_bwd_window_workspace_bytes
- *   bytes (0 for invalid arguments): the fp32 dQ accumulator, and fp32 parts
- *   of dK and dV of key tiles whose queries several CTAs share; contents on
- *   entry irrelevant.  Calls that can overlap need a workspace each.
+ *   bytes (0 for invalid arguments and for lengths that the call refuses): the
+ *   fp32 dQ accumulator, and fp32 parts of dK and dV of sinks and of key tiles
+ *   whose queries several CTAs share; contents on entry irrelevant.  Calls that can overlap need a workspace each.
  */
 size_t attn_bwd_window_workspace_bytes(int B, int H, int H_kv, int Lq, int Lk, int d,
                                        int64_t window, int64_t sinks, int64_t q_offset,
@@ -420,16 +429,18 @@ enum { ATTN_KV_BF16 = 0, ATTN_KV_E4M3 = 1 };
  *   seq_lens[s] - window or j < sinks; window = 0: every key (sinks must be
  *   0).  H_kv divides H; query head h reads K/V head h / (H / H_kv).  A
  *   sequence of length 0 gets O = 0, LSE = -inf.
- *   Table entries of keys that are not seen are not read, and neither are the
- *   rows of the last page past the length: they may hold anything.  A seen
- *   page outside [0, n_pages) is skipped and reported, a length past
+ *   What the table's entries of unseen keys and the caches' rows that are not
+ *   seen (past the length, or outside window and sinks) hold does not matter.
+ *   A seen page outside [0, n_pages) is skipped and reported, a length past
  *   max_pages * page_size (or 0x7FFFFF00) is cut to it and reported.
  *   workspace: device, 16-byte aligned, >= attn_decode_paged_workspace_bytes
  *   (it does not depend on the lengths: 0 for invalid arguments and for small
  *   calls, which take NULL; at most 16 MB for groups of up to 8 query heads,
  *   31 MB for larger ones), contents on entry irrelevant.  Calls that can
  *   overlap need a workspace each.
- *   The same lengths give the same bits in every run.
+ *   S >= 1.  The same lengths give the same bits in every run.
+ *   Scores, maxima, sums and O are fp32; the probabilities enter their product
+ *   in two bf16 parts (2^-15) over bf16 pages, as fp16 (2^-11) over e4m3 ones.
  */
 size_t attn_decode_paged_workspace_bytes(int S, int H, int H_kv, int d, int max_pages,
                                          int page_size);
@@ -446,6 +457,7 @@ attn_status_t attn_decode_paged(const void* q, int64_t q_stride, const void* k_c
  * pages enter the table, seq_lens grows.  start [S] out: the position of the
  * first new token, or -1 for every sequence when the call was refused (too
  * few free pages, or a sequence past max_pages * page_size or 0x7FFFFF00).
+ * S >= 1.
  */
 attn_status_t attn_kv_reserve(int32_t* page_table, int32_t* seq_lens, int32_t* refs,
                               const int32_t* n_new, int32_t* start, int S, int max_pages,

@@ -739,9 +739,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     int gq, i;                                    // query head of the group, query tile
     walk.start(gq, i);
     for (int it = 0; i >= 0 && ok; walk.advance(gq, i), ++it) {
-      // (a wait that runs out is noted, and at the round's end the warp leaves as
-      // one; up to there it only spoils results that are lost already)
+      // The warp leaves a wait that ran out as one: per-warp drains by a vote here,
+      // CTA-wide ones at the round's end, where it costs less at d=64 (up to there
+      // it only spoils results that are lost already).
       bool fine = wait_bar_relaxed(bar(C::kBarDQFull), it & 1, abort_flag, p.err);
+      if (kPerWarp && !__all_sync(0xFFFFFFFFu, fine)) break;
       BSS_TRACE_EV(p, tr && qr == 0, 3, 3 * it);
       tc_fence_after();
       for (int r = 0; r < kRounds; ++r, ++g) {
@@ -796,7 +798,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
           }
         }
         // reconverge before the next TMEM load, or leave as a warp
-        if (!__all_sync(0xFFFFFFFFu, fine)) {
+        if (kPerWarp) {
+          __syncwarp();
+        } else if (!__all_sync(0xFFFFFFFFu, fine)) {
           ok = false;
           break;
         }

@@ -1458,7 +1458,7 @@ WindowBwdPlan window_bwd_plan(int B, int H, int Hkv, int Lq, int Lk, int d, cons
   // d128, window 1024.
   if (pl.few_sinks > 0 && seg_w == 1 && BH * rest > 152) {
     const long long nt = (BH * rest % 152 + BH - 1) / BH;         // key tiles of the last wave
-    const long long cut = nt > 0 ? 152 / (nt * BH) : 1;
+    const long long cut = nt > 0 ? std::min(share, 152 / (nt * BH)) : 1;
     if (cut > 1 && share / G <= nt) {
       pl.tiles[0] = WindowTiles{0, static_cast<int>(rest - nt), 1, 0, 0};
       pl.tiles[1] = WindowTiles{static_cast<int>(rest - nt), static_cast<int>(nt), static_cast<int>(cut), 0, 0};

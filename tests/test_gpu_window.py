@@ -336,7 +336,11 @@ def test_rows_of_few_keys(bss, H, Hkv, Lq, Lk, d, window, sinks, qo, ko):
     (1, 2, 1, 300, 6, 128, 4, 8, 0, 0),            # nothing but sinks
     (1, 2, 2, 400, 200, 64, 30, 130, 0, 123),      # seven of 130
     (1, 200, 100, 40, 40, 64, 7, 2, 0, 0),
-    (1, 16, 4, 5000, 5000, 128, 300, 4, 0, 0),     # a last wave of key tiles that is cut
+    (1, 16, 4, 5300, 5300, 128, 300, 4, 0, 0),     # a last wave of key tiles that is cut, in 9
+    (1, 16, 4, 5000, 5000, 64, 100, 1, 0, 0),      # ... a query tile each
+    (1, 8, 8, 2500, 2500, 128, 50, 8, 0, 0),       # ... not, its walks being short
+    (20, 16, 1, 1100, 1100, 64, 100, 4, 0, 0),     # ... of a launch of a CTA an item
+    (2, 6, 2, 5200, 5200, 64, 130, 3, 0, 0),
     (1, 4, 2, 700, 700, 128, 20, 12, 0, 0),        # every row of few keys: more sinks than share a kernel
     (1, 4, 4, 700, 700, 64, 32, 0, 0, 0),          # ... none
     (2, 4, 1, 500, 40, 128, 50, 13, 5, 0),         # ... no more keys than that

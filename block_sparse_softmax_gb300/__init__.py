@@ -12,7 +12,8 @@ Functions carry the C names: ``attn_fwd``, ``attn_fwd_partial``,
 ``attn_bwd``, ``attn_bwd_blocksparse``, ``attn_bwd_noalloc``, ``attn_poll_status``,
 ``attn_bwd_time_main``, ``attn_watchdog_selftest``, ``attn_probe_ex2_rate``; with a sliding
 window and sinks ``attn_fwd_window``, ``attn_bwd_window``; over a paged cache
-``attn_decode_paged``, ``attn_kv_reserve``, ``attn_kv_write``, ``attn_kv_fork``,
+``attn_decode_paged``, ``attn_fwd_paged``, ``attn_select_pages``, ``attn_decode_selected``,
+``attn_kv_pool``, ``attn_kv_reserve``, ``attn_kv_write``, ``attn_kv_fork``,
 ``attn_kv_free``, ``attn_kv_evict``, ``attn_kv_compact``, ``attn_kv_copy_pages``.  Each
 call runs on the
 device of its tensors and on that device's current stream.
@@ -37,6 +38,8 @@ __all__ = [
     "attn_fwd_window", "attn_bwd_window", "attn_bwd_window_workspace_bytes",
     "attn_decode_paged", "attn_decode_paged_workspace_bytes", "attn_kv_reserve", "attn_kv_write",
     "attn_kv_fork", "attn_kv_free", "attn_kv_evict", "attn_kv_compact", "attn_kv_copy_pages",
+    "attn_fwd_paged", "attn_fwd_paged_workspace_bytes", "attn_kv_pool", "attn_select_pages",
+    "attn_select_pages_workspace_bytes", "attn_decode_selected",
 ]
 
 OK = 0
@@ -440,5 +443,7 @@ def attn_watchdog_selftest(timeout_cycles: int = 1 << 20, device=None) -> None:
 from ._window import (attn_bwd_window, attn_bwd_window_workspace_bytes,  # noqa: E402
                       attn_fwd_window)
 from ._paged import (attn_decode_paged, attn_decode_paged_workspace_bytes,  # noqa: E402
+                     attn_decode_selected, attn_fwd_paged, attn_fwd_paged_workspace_bytes,
                      attn_kv_compact, attn_kv_copy_pages, attn_kv_evict, attn_kv_fork,
-                     attn_kv_free, attn_kv_reserve, attn_kv_write)
+                     attn_kv_free, attn_kv_pool, attn_kv_reserve, attn_kv_write,
+                     attn_select_pages, attn_select_pages_workspace_bytes)

@@ -84,6 +84,31 @@ _SIGNATURES = {
                                      _C.c_size_t, _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
                                      _C.c_int, _C.c_int, _C.c_float, _C.c_int64, _C.c_int64,
                                      _C.c_void_p]),
+    "attn_fwd_paged_workspace_bytes": (_C.c_size_t, [_C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                                     _C.c_int, _C.c_int, _C.c_int]),
+    "attn_fwd_paged": (_C.c_int, [_C.c_void_p, _C.c_int64, _C.c_void_p, _C.c_void_p, _C.c_int64,
+                                  _C.c_int64, _C.c_int, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                  _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                  _C.c_size_t, _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                  _C.c_int, _C.c_int, _C.c_int, _C.c_float, _C.c_int64, _C.c_int64,
+                                  _C.c_void_p]),
+    "attn_kv_pool": (_C.c_int, [_C.c_void_p, _C.c_int64, _C.c_int, _C.c_void_p, _C.c_void_p,
+                                _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_int, _C.c_int, _C.c_int,
+                                _C.c_int, _C.c_int, _C.c_int, _C.c_void_p]),
+    "attn_select_pages_workspace_bytes": (_C.c_size_t, [_C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                                        _C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                                        _C.c_int, _C.c_int]),
+    "attn_select_pages": (_C.c_int, [_C.c_void_p, _C.c_int64, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                     _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                     _C.c_size_t, _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                     _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_int,
+                                     _C.c_void_p]),
+    "attn_decode_selected": (_C.c_int, [_C.c_void_p, _C.c_int64, _C.c_void_p, _C.c_void_p,
+                                        _C.c_int64, _C.c_int64, _C.c_int, _C.c_void_p, _C.c_void_p,
+                                        _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
+                                        _C.c_void_p, _C.c_size_t, _C.c_int, _C.c_int, _C.c_int,
+                                        _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_float,
+                                        _C.c_void_p]),
     "attn_kv_reserve": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p, _C.c_void_p,
                                    _C.c_int, _C.c_int, _C.c_int, _C.c_int, _C.c_void_p]),
     "attn_kv_write": (_C.c_int, [_C.c_void_p, _C.c_void_p, _C.c_int64, _C.c_int64, _C.c_void_p,

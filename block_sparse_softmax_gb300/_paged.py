@@ -1,4 +1,5 @@
-"""Paged key/value caches: ``attn_decode_paged`` and the ``attn_kv_*`` calls.
+"""Paged key/value caches: ``attn_decode_paged``, ``attn_fwd_paged``, ``attn_select_pages``,
+``attn_decode_selected`` and the ``attn_kv_*`` calls.
 
 A cache is a pair of tensors [n_pages, H_kv, page_size, d] (bf16, or e4m3 with a scale per K/V
 head); its bookkeeping is three int32 tensors on the same device, changed in place: ``page_table``
@@ -136,6 +137,157 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, window: int 
         wp, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _run("attn_decode_paged", dev, q.data_ptr(), q_stride, kp, vp, ks, vs, code, ksp, vsp, tp, lp,
          op, ep, wp, nbytes, S, H, Hkv, d, M, P, page, _scale(scale, d), int(window), int(sinks))
+    return out, lse
+
+
+def attn_fwd_paged_workspace_bytes(T: int, S: int, H: int, H_kv: int, d: int, max_pages: int,
+                                   page_size: int) -> int:
+    return int(_lib.load().attn_fwd_paged_workspace_bytes(T, S, H, H_kv, d, max_pages, page_size))
+
+
+_chunk_bytes = functools.lru_cache(maxsize=256)(attn_fwd_paged_workspace_bytes)
+
+
+def _rows_of(q, page_table, seq_lens, cu_q, dev: int):
+    """(T, H, d, S, max_pages, table, lengths and cu_q addresses) of a ragged batch of new tokens."""
+    if len(q.shape) != 3:
+        raise ValueError("q must have 3 dimensions [T, H, d]")
+    T, H, d = q.shape
+    tp, rows, M = _table(page_table, dev)
+    S = cu_q.numel() - 1
+    if not 0 <= S <= rows:
+        raise ValueError(f"page_table has {rows} rows, cu_q {S + 1} entries for one less sequences")
+    return (T, H, d, S, M, tp, _is(seq_lens, "seq_lens", _INT, (rows,), dev),
+            _is(cu_q, "cu_q", _INT, (S + 1,), dev))
+
+
+def attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu_q, *, window: int = 0,
+                   sinks: int = 0, scale: Optional[float] = None, k_scale=None, v_scale=None,
+                   workspace: Optional[torch.Tensor] = None, out=None, lse=None):
+    """Attention of a chunk of new tokens per sequence over a paged cache: O [T,H,d] bf16 and LSE
+    [T,H] fp32.  Rows cu_q[s] .. cu_q[s+1]-1 of q [T,H,d] bf16 (rows may be strided) are the last
+    tokens of sequence s, their keys already in the cache: row t stands at position i =
+    seq_lens[s] - (cu_q[s+1] - t) and sees the keys j <= i, with ``window`` > 0 only those with
+    j > i - window or j < sinks.  Rows before cu_q[0] or from cu_q[S] on belong to no sequence:
+    their rows of ``out`` and ``lse`` are left as they were.  At most 128 query heads share a K/V
+    head.  The table may have more rows than cu_q names sequences: they are ignored."""
+    dev = q.get_device()
+    kp, vp, ks, vs, code = _cache(k_cache, v_cache, dev)
+    P, Hkv, page, d = k_cache.shape
+    T, H, _, S, M, tp, lp, cp = _rows_of(q, page_table, seq_lens, cu_q, dev)
+    q_stride = _rows(q, "q", (T, H, d), dev)
+    ksp, vsp = _scales(code, k_scale, v_scale, Hkv, dev)
+    out, op = _out(out, "out", _BF16, (T, H, d), q)
+    lse, ep = _out(lse, "lse", _FP32, (T, H), q)
+    if T == 0 or S == 0:                      # no row of a sequence
+        return out, lse
+    ws = _workspace(workspace, 0 if workspace is not None else _chunk_bytes(
+        T, S, H, Hkv, d, M, page), q)
+    _run("attn_fwd_paged", dev, q.data_ptr(), q_stride, kp, vp, ks, vs, code, ksp, vsp, tp, lp, cp,
+         op, ep, ws.data_ptr(), ws.numel() * ws.element_size(), T, S, H, Hkv, d, M, P, page,
+         _scale(scale, d), int(window), int(sinks))
+    return out, lse
+
+
+def attn_kv_pool(k_cache, k_means, page_table, start, seq_lens, *, k_scale=None) -> None:
+    """The mean keys of the pages that became full between start[s] and seq_lens[s] tokens (start
+    as attn_kv_reserve returns it; 0 for all of a sequence's full pages) go to ``k_means``
+    [n_pages,H_kv,d] fp32; other pages' stay as they are.  start may be shorter than the table."""
+    dev = k_cache.get_device()
+    # (one cache alone: the second one's place is taken by the first)
+    kp, _, ks, _, code = _cache(k_cache, k_cache, dev)
+    P, Hkv, page, d = k_cache.shape
+    mp = _is(k_means, "k_means", _FP32, (P, Hkv, d), dev)
+    tp, rows, M = _table(page_table, dev)
+    S = start.numel()
+    if rows < S:
+        raise ValueError(f"page_table has {rows} rows for {S} sequences")
+    sp, lp = _is(start, "start", _INT, (S,), dev), _is(seq_lens, "seq_lens", _INT, (rows,), dev)
+    if (code == KV_E4M3) != (k_scale is not None):
+        raise ValueError("k_scale belongs to an e4m3 cache and to no other")
+    ksp = None if k_scale is None else _is(k_scale, "k_scale", _FP32, (Hkv,), dev)
+    if S == 0:
+        return
+    _run("attn_kv_pool", dev, kp, ks, code, ksp, mp, tp, sp, lp, S, M, P, Hkv, d, page)
+
+
+def attn_select_pages_workspace_bytes(T: int, S: int, H: int, H_kv: int, d: int, max_pages: int,
+                                      page_size: int, top_r: int, local_pages: int = 1,
+                                      first_pages: int = 0) -> int:
+    return int(_lib.load().attn_select_pages_workspace_bytes(
+        T, S, H, H_kv, d, max_pages, page_size, top_r, local_pages, first_pages))
+
+
+_select_bytes = functools.lru_cache(maxsize=256)(attn_select_pages_workspace_bytes)
+
+
+def attn_select_pages(q, k_means, page_table, seq_lens, cu_q, top_r: int, page_size: int, *,
+                      local_pages: int = 1, first_pages: int = 0,
+                      workspace: Optional[torch.Tensor] = None, pages=None, lens=None):
+    """For each new token and K/V head the pages it reads: the first ``first_pages`` of its
+    sequence, the last ``local_pages`` up to its own, and the ``top_r`` others whose mean keys
+    (``k_means`` [n_pages,H_kv,d] fp32, attn_kv_pool) score highest against the sum of the query
+    heads that share the K/V head, ties to the lower place.  q, page_table, seq_lens and cu_q as
+    for attn_fwd_paged.  Returns pages [T,H_kv,first+local+top] int32 (in ascending order of their
+    place, then -1) and lens [T] int32, the tokens in them (-1 for a row of no sequence), as
+    attn_decode_selected takes them."""
+    dev = q.get_device()
+    T, H, d, S, M, tp, lp, cp = _rows_of(q, page_table, seq_lens, cu_q, dev)
+    if len(k_means.shape) != 3:
+        raise ValueError("k_means must have 3 dimensions [n_pages, H_kv, d]")
+    P, Hkv, _ = k_means.shape
+    mp = _is(k_means, "k_means", _FP32, (P, Hkv, d), dev)
+    q_stride = _rows(q, "q", (T, H, d), dev)
+    top_r, local_pages, first_pages = int(top_r), int(local_pages), int(first_pages)
+    R = top_r + local_pages + first_pages
+    if top_r < 0 or local_pages < 1 or first_pages < 0:
+        raise ValueError("top_r and first_pages must be at least 0, local_pages at least 1")
+    if T * Hkv * R >= 1 << 31:
+        raise ValueError(f"pages would have {T * Hkv * R} entries; at most 2^31 - 1 are supported")
+    pages, pp = _out(pages, "pages", _INT, (T, Hkv, R), q)
+    lens, np_ = _out(lens, "lens", _INT, (T,), q)
+    if T == 0:
+        return pages, lens
+    if S == 0:                                # every row is one of no sequence
+        return pages.fill_(-1), lens.fill_(-1)
+    page_size = int(page_size)
+    ws = _workspace(workspace, 0 if workspace is not None else _select_bytes(
+        T, S, H, Hkv, d, M, page_size, top_r, local_pages, first_pages), q)
+    _run("attn_select_pages", dev, q.data_ptr(), q_stride, mp, tp, lp, cp, pp, np_, ws.data_ptr(),
+         ws.numel() * ws.element_size(), T, S, H, Hkv, d, M, P, page_size, top_r, local_pages,
+         first_pages)
+    return pages, lens
+
+
+def attn_decode_selected(q, k_cache, v_cache, pages, lens, *, scale: Optional[float] = None,
+                         k_scale=None, v_scale=None, workspace: Optional[torch.Tensor] = None,
+                         out=None, lse=None):
+    """Attention of rows that read pages of their own per K/V head: O [T,H,d] bf16 and LSE [T,H]
+    fp32.  Row t's query heads of K/V head h see the first lens[t] tokens of the pages
+    pages[t,h,:] (attn_select_pages); a row with lens[t] < 0 is of no sequence, its rows of ``out``
+    and ``lse`` are left as they were.  q [T,H,d] bf16 (rows may be strided), T <= 65536."""
+    dev = q.get_device()
+    kp, vp, ks, vs, code = _cache(k_cache, v_cache, dev)
+    P, Hkv, page, d = k_cache.shape
+    if len(q.shape) != 3 or len(pages.shape) != 3:
+        raise ValueError("q must have 3 dimensions [T, H, d], pages 3 [T, H_kv, max_pages]")
+    T, H, _ = q.shape
+    M = pages.shape[2]
+    q_stride = _rows(q, "q", (T, H, d), dev)
+    ksp, vsp = _scales(code, k_scale, v_scale, Hkv, dev)
+    pp, lp = _is(pages, "pages", _INT, (T, Hkv, M), dev), _is(lens, "lens", _INT, (T,), dev)
+    out, op = _out(out, "out", _BF16, (T, H, d), q)
+    lse, ep = _out(lse, "lse", _FP32, (T, H), q)
+    if T == 0:
+        return out, lse
+    wp, nbytes = None, 0
+    if workspace is None:
+        nbytes = _decode_bytes(T, H, Hkv, d, M, page)
+    if workspace is not None or nbytes:       # small calls need none
+        workspace = _workspace(workspace, nbytes, q)
+        wp, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _run("attn_decode_selected", dev, q.data_ptr(), q_stride, kp, vp, ks, vs, code, ksp, vsp, pp, lp,
+         op, ep, wp, nbytes, T, H, Hkv, d, M, P, page, _scale(scale, d))
     return out, lse
 
 

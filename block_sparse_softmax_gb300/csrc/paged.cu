@@ -76,6 +76,8 @@ struct DecodeParams {
   const float* k_scale;
   const float* v_scale;
   const int* table;
+  int t_row, t_head;             // its entries from sequence to sequence, from K/V head to K/V head
+  bool selected;                 // attn_decode_selected: a row of negative length is nobody's
   const int* lens;
   __nv_bfloat16* o;
   float* lse;
@@ -320,6 +322,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     un.s = cta / units;
     un.r = cta - un.s * units;
     const int n = __ldg(p.lens + un.s);
+    if (p.selected && n < 0) return;                // (the whole block)
     if (tid == 0 && un.r == 0 && (n < 0 || n > most_tokens(p)))
       record_error(p.err, ATTN_ERR_BAD_PAGES);
     un.st = seq_steps<KEYS>(n, p);
@@ -350,6 +353,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     // sequences that see no key, and lengths out of range
     for (int s = cta; s < p.S; s += n_cta) {
       const int n = __ldg(p.lens + s);
+      if (p.selected && n < 0) continue;
       if (tid == 0 && (n < 0 || n > most_tokens(p)))
         record_error(p.err, ATTN_ERR_BAD_PAGES);
       if (seq_steps<KEYS>(n, p).total > 0) continue;
@@ -426,7 +430,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
 #pragma unroll
     for (int m = 0; m < C::kRowTiles; ++m) {
       const int key = in ? u.st.key(t) + 16 * m : 0;
-      pages[m] = in && key < u.st.n ? __ldg(p.table + static_cast<size_t>(u.s) * p.M + (key >> p.page_log2)) : -1;
+      pages[m] = in && key < u.st.n ? __ldg(p.table + static_cast<size_t>(u.s) * p.t_row +
+                                            u.r / p.q_tiles * p.t_head + (key >> p.page_log2)) : -1;
     }
   };
   auto valid_page = [&](int pg) { return pg >= 0 && pg < p.P; };
@@ -1066,17 +1071,20 @@ extern "C" size_t attn_decode_paged_workspace_bytes(int S, int H, int H_kv, int 
   return decode_workspace(d, H / H_kv, decode_workers(S, H_kv, H / H_kv, max_pages, page_size));
 }
 
-extern "C" attn_status_t attn_decode_paged(
-    const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int64_t k_page_stride,
-    int64_t v_page_stride, int kv_dtype, const float* k_scale, const float* v_scale,
-    const int32_t* page_table, const int32_t* seq_lens, void* o, float* lse, void* workspace,
-    size_t workspace_bytes, int S, int H, int H_kv, int d, int max_pages, int n_pages, int page_size,
-    float scale, int64_t window, int64_t sinks, void* stream) {
+namespace {
+// Both entry points: a row of the table per sequence, or per sequence and K/V head (`selected`).
+attn_status_t decode(const char* name, const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                     int64_t k_page_stride, int64_t v_page_stride, int kv_dtype, const float* k_scale,
+                     const float* v_scale, const int32_t* page_table, const int32_t* seq_lens, void* o,
+                     float* lse, void* workspace, size_t workspace_bytes, int S, int H, int H_kv, int d,
+                     int max_pages, int n_pages, int page_size, float scale, int64_t window, int64_t sinks,
+                     bool selected, void* stream) {
   attn_status_t s = check_common(S, H, 1, 1, d, scale);
   if (s != ATTN_OK) return s;
   if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
   if (S > kMaxSeqs) return ATTN_ERR_UNSUPPORTED;
   if (max_pages < 1 || n_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if (selected && static_cast<long long>(H_kv) * max_pages > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return ATTN_ERR_UNSUPPORTED;
   if (kv_dtype != ATTN_KV_BF16 && kv_dtype != ATTN_KV_E4M3) return ATTN_ERR_UNSUPPORTED;
   if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return ATTN_ERR_INVALID_ARG;
@@ -1119,6 +1127,9 @@ extern "C" attn_status_t attn_decode_paged(
   p.Hkv = H_kv;
   p.G = H / H_kv;
   p.M = max_pages;
+  p.t_head = selected ? max_pages : 0;
+  p.t_row = selected ? H_kv * max_pages : max_pages;
+  p.selected = selected;
   p.P = n_pages;
   while ((1 << p.page_log2) < page_size) ++p.page_log2;
   p.q_tiles = (p.G + 15) / 16;
@@ -1147,5 +1158,27 @@ extern "C" attn_status_t attn_decode_paged(
   BSS_DECODE_CASES(128, true)
 #undef BSS_DECODE_CASES
 #undef BSS_DECODE_CASE
-  return cuda_status("attn_decode_paged launch", e);
+  return cuda_status(name, e);
+}
+}  // namespace
+
+extern "C" attn_status_t attn_decode_paged(
+    const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int64_t k_page_stride,
+    int64_t v_page_stride, int kv_dtype, const float* k_scale, const float* v_scale,
+    const int32_t* page_table, const int32_t* seq_lens, void* o, float* lse, void* workspace,
+    size_t workspace_bytes, int S, int H, int H_kv, int d, int max_pages, int n_pages, int page_size,
+    float scale, int64_t window, int64_t sinks, void* stream) {
+  return decode("attn_decode_paged launch", q, q_stride, k_cache, v_cache, k_page_stride, v_page_stride, kv_dtype,
+                k_scale, v_scale, page_table, seq_lens, o, lse, workspace, workspace_bytes, S, H, H_kv, d,
+                max_pages, n_pages, page_size, scale, window, sinks, false, stream);
+}
+
+extern "C" attn_status_t attn_decode_selected(
+    const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int64_t k_page_stride,
+    int64_t v_page_stride, int kv_dtype, const float* k_scale, const float* v_scale, const int32_t* pages,
+    const int32_t* lens, void* o, float* lse, void* workspace, size_t workspace_bytes, int T, int H, int H_kv,
+    int d, int max_pages, int n_pages, int page_size, float scale, void* stream) {
+  return decode("attn_decode_selected launch", q, q_stride, k_cache, v_cache, k_page_stride, v_page_stride,
+                kv_dtype, k_scale, v_scale, pages, lens, o, lse, workspace, workspace_bytes, T, H, H_kv, d,
+                max_pages, n_pages, page_size, scale, 0, 0, true, stream);
 }

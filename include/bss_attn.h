@@ -396,7 +396,8 @@ attn_status_t attn_bwd_window(const void* q, const void* k, const void* v, const
                               int64_t sinks, int64_t q_offset, int64_t k_offset, void* stream);
 
 /*
- * Paged key/value caches (attn_decode_paged and the attn_kv_ calls).
+ * Paged key/value caches (attn_decode_paged, attn_fwd_paged, attn_select_pages,
+ * attn_decode_selected and the attn_kv_ calls).
  *   - k_cache, v_cache [n_pages][H_kv][page_size][d], bf16 (ATTN_KV_BF16) or
  *     e4m3 (ATTN_KV_E4M3); a page is contiguous, pages lie k_page_stride /
  *     v_page_stride elements apart (a multiple of 16 bytes, at least a page).
@@ -451,6 +452,106 @@ attn_status_t attn_decode_paged(const void* q, int64_t q_stride, const void* k_c
                                 float* lse, void* workspace, size_t workspace_bytes, int S, int H,
                                 int H_kv, int d, int max_pages, int n_pages, int page_size,
                                 float scale, int64_t window, int64_t sinks, void* stream);
+
+/*
+ * attn_fwd_paged - attention of a chunk of new tokens per sequence over a paged
+ * cache ("Exact Blocks, Rings, and Sparsity", section 4: the new tokens'
+ * queries against key chunks, cached ones and their own): a prompt's next
+ * chunk, a few tokens to verify, or both beside single tokens in one batch.
+ *   q [T][H][d] bf16, rows q_stride elements apart (a multiple of 8, at least
+ *   H*d); o [T][H][d] bf16 and lse [T][H] fp32 out, contiguous.  Rows cu_q[s] ..
+ *   cu_q[s+1]-1 (cu_q [S+1] int32, ascending) are the last tokens of sequence s,
+ *   whose keys are in the cache: row t stands at position
+ *       i = seq_lens[s] - (cu_q[s+1] - t)
+ *   and sees the keys j <= i, with window > 0 only those with j > i - window or
+ *   j < sinks; window = 0: every key (sinks must be 0).  H_kv divides H, at most
+ *   128 query heads share a K/V head; query head h reads K/V head h / (H / H_kv).
+ *   Rows before cu_q[0] or from cu_q[S] on belong to no sequence: their o and
+ *   lse are left as they were.  A row before its sequence's first token (more
+ *   new tokens than the sequence has) gets O = 0, LSE = -inf and is reported.
+ *   What the table's entries of keys that no row of a sequence sees hold does
+ *   not matter, nor what the caches hold past a sequence's length.  A seen page
+ *   outside [0, n_pages) is reported (its keys are left out), a length past
+ *   max_pages * page_size (or 0x7FFFFF00) is cut to it and reported.  As in
+ *   attn_fwd_window, a V that is infinite or NaN reaches every row whose block of
+ *   128 keys it lies in.
+ *   workspace: device, 16-byte aligned, >= attn_fwd_paged_workspace_bytes (it
+ *   depends on none of the device's arrays; 0 for invalid arguments), contents
+ *   on entry irrelevant.  Calls that can overlap need a workspace each.
+ *   T >= 0, S >= 1.  The same lengths give the same bits in every run.
+ */
+size_t attn_fwd_paged_workspace_bytes(int T, int S, int H, int H_kv, int d, int max_pages,
+                                      int page_size);
+attn_status_t attn_fwd_paged(const void* q, int64_t q_stride, const void* k_cache,
+                             const void* v_cache, int64_t k_page_stride, int64_t v_page_stride,
+                             int kv_dtype, const float* k_scale, const float* v_scale,
+                             const int32_t* page_table, const int32_t* seq_lens,
+                             const int32_t* cu_q, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, int T, int S, int H, int H_kv, int d,
+                             int max_pages, int n_pages, int page_size, float scale,
+                             int64_t window, int64_t sinks, void* stream);
+
+/*
+ * attn_kv_pool - the mean keys that attn_select_pages scores ("Exact Blocks,
+ * Rings, and Sparsity", section 5, 'Fixed pooling').  k_means
+ * [n_pages][H_kv][d] fp32, contiguous: of every page of sequence s that became
+ * full between start[s] and seq_lens[s] tokens (start as attn_kv_reserve gives
+ * it), the mean over its page_size keys, times k_scale[h] over an e4m3 cache, is
+ * written, rounded once; other pages' are left as they are.  Sequences with
+ * start[s] < 0 and pages given back (-1) are passed over.  With start[s] = 0 all
+ * of a sequence's pages are pooled, as after attn_kv_copy_pages has moved pages
+ * (attn_kv_compact; what attn_kv_fork copies is not full).  S >= 1.
+ */
+attn_status_t attn_kv_pool(const void* k_cache, int64_t k_page_stride, int kv_dtype,
+                           const float* k_scale, float* k_means, const int32_t* page_table,
+                           const int32_t* start, const int32_t* seq_lens, int S, int max_pages,
+                           int n_pages, int H_kv, int d, int page_size, void* stream);
+
+/*
+ * attn_select_pages - for each new token and K/V head the pages it reads: the
+ * first first_pages pages of its sequence, the last local_pages (its own among
+ * them, so local_pages >= 1), and of the others the top_r with the highest score
+ *   (sum of the query heads that share the K/V head) . k_means[page]
+ * ("Exact Blocks, Rings, and Sparsity", sections 5 and 6, as attn_select_blocks
+ * scores blocks; exact: a score's rounding decides nothing; ties to the lower
+ * place, a NaN last).  q, cu_q, seq_lens and page_table as for attn_fwd_paged; a
+ * row sees the pages of the tokens up to its own.  Pages given back (-1) are
+ * left out.
+ *   pages [T][H_kv][R] int32 out, R = first_pages + local_pages + top_r: the pages
+ *   in ascending order of their place, then -1.  lens [T] int32 out: the tokens
+ *   in them (every page but the row's own counts whole); -1 for a row of no
+ *   sequence, 0 for one before its sequence's first token (reported).
+ *   workspace: as for attn_fwd_paged (attn_select_pages_workspace_bytes).
+ *   max_pages <= 32768, T * H_kv * R < 2^31.  T >= 0, S >= 1.
+ */
+size_t attn_select_pages_workspace_bytes(int T, int S, int H, int H_kv, int d, int max_pages,
+                                         int page_size, int top_r, int local_pages,
+                                         int first_pages);
+attn_status_t attn_select_pages(const void* q, int64_t q_stride, const float* k_means,
+                                const int32_t* page_table, const int32_t* seq_lens,
+                                const int32_t* cu_q, int32_t* pages, int32_t* lens,
+                                void* workspace, size_t workspace_bytes, int T, int S, int H,
+                                int H_kv, int d, int max_pages, int n_pages, int page_size,
+                                int top_r, int local_pages, int first_pages, void* stream);
+
+/*
+ * attn_decode_selected - attn_decode_paged for rows that read pages of their own
+ * per K/V head: row t's query heads of K/V head h see the first lens[t] tokens of
+ * the pages pages[t][h][0 .. max_pages-1] ([T][H_kv][max_pages] int32, as
+ * attn_select_pages gives them), in fp32 and bf16 parts as there.  q [T][H][d], o,
+ * lse, caches, scales, workspace (attn_decode_paged_workspace_bytes(T, H, H_kv,
+ * d, max_pages, page_size)) and errors as for attn_decode_paged with S = T; a row
+ * with lens[t] < 0 is of no sequence, its o and lse are left as they were.
+ * 1 <= T <= 65536.
+ */
+attn_status_t attn_decode_selected(const void* q, int64_t q_stride, const void* k_cache,
+                                   const void* v_cache, int64_t k_page_stride,
+                                   int64_t v_page_stride, int kv_dtype, const float* k_scale,
+                                   const float* v_scale, const int32_t* pages,
+                                   const int32_t* lens, void* o, float* lse, void* workspace,
+                                   size_t workspace_bytes, int T, int H, int H_kv, int d,
+                                   int max_pages, int n_pages, int page_size, float scale,
+                                   void* stream);
 
 /*
  * attn_kv_reserve - room for n_new[s] >= 0 more tokens in every sequence: new

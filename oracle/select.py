@@ -111,3 +111,48 @@ def block_mass(q, k, scale, block: int = 128):
             m = blk.max()
             out[a, c] = m + np.log(np.exp(blk - m).sum())
     return out
+
+
+def page_means(k, page: int):
+    """Mean keys [n // page, Hkv, d] of the full pages of a sequence's keys [Hkv, n, d] (torch, fp64)."""
+    Hkv, n, d = k.shape
+    full = n // page
+    return k[:, :full * page].reshape(Hkv, full, page, d).mean(2).transpose(0, 1)
+
+
+def select_pages(q, means, table, lens, cu, news, top, page, local, first):
+    """(pages [T,Hkv,first+local+top], lens [T]) of attn_select_pages, int32 on the host: for each
+    new token and K/V head the first pages, the last ones up to its own and the `top` others by the
+    sum of the group's queries times the mean key, each score summed exactly (math.fsum of products
+    that 64 bits hold), ties to the lower place, a NaN last; pages of -1 are left out.  Rows of no
+    sequence have lens -1."""
+    import math
+
+    import torch
+    T, H, d = q.shape
+    Hkv = means.shape[1]
+    most = first + local + top
+    pages = torch.full((T, Hkv, most), -1, dtype=torch.int32)
+    out = torch.full((T,), -1, dtype=torch.int32)
+    qs = q.double().reshape(T, Hkv, H // Hkv, d).sum(2).cpu().numpy()
+    for s, (n, new) in enumerate(zip(lens, news)):
+        slots = table[s].tolist()
+        for i in range(new):
+            t, sees = cu[s] + i, n - new + i + 1
+            held = -(-sees // page)
+            kept = [m for m in range(held) if m < first or m >= held - local]
+            rest = [m for m in range(held) if m not in set(kept) and slots[m] >= 0]
+            kept = [m for m in kept if slots[m] >= 0]
+            for h in range(Hkv):
+                picked = rest
+                if len(rest) > top:
+                    x = means[[slots[m] for m in rest], h].double().cpu().numpy() * qs[t, h]
+                    score = ([math.fsum(row) for row in x.tolist()] if np.isfinite(x).all()
+                             else x.sum(1).tolist())
+                    order = sorted(range(len(rest)), key=lambda j: (
+                        score[j] != score[j], -score[j] if score[j] == score[j] else 0.0, j))
+                    picked = [rest[j] for j in order[:top]]
+                chosen = sorted(kept + picked)
+                pages[t, h, :len(chosen)] = torch.tensor([slots[m] for m in chosen], dtype=torch.int32)
+                out[t] = sees - (held - len(chosen)) * page
+    return pages, out

@@ -168,3 +168,95 @@ def test_decode_takes_the_route_that_measured_faster(lib):
     for case in ((1, 16, 1, 768), (1, 16, 1, 1024), (8, 16, 1, 1024), (32, 16, 1, 1024), (1, 64, 2, 1024),
                  (512, 16, 4, 16), (1024, 16, 4, 16), (1024, 16, 4, 32)):
         assert shared(*case), case
+
+
+def test_chunk(lib):
+    size = lib.attn_fwd_paged_workspace_bytes
+    full = size(500, 3, 8, 2, 128, 400, 16)
+    assert full > 0
+    for bad in ((500, 3, 8, 3, 128, 400, 16), (500, 3, 8, 2, 96, 400, 16), (0, 3, 8, 2, 128, 400, 16),
+                (500, 0, 8, 2, 128, 400, 16), (500, 3, 8, 2, 128, 0, 16), (500, 3, 8, 2, 128, 400, 24),
+                (500, 70000, 8, 2, 128, 400, 16), (500, 3, 129, 1, 128, 400, 16), (2 ** 28, 3, 8, 2, 128, 400, 16)):
+        assert size(*bad) == 0, bad
+
+    def call(q=P, qs=8 * 128, ks=2 * 16 * 128, vs=2 * 16 * 128, kind=0, kscale=None, vscale=None, table=P, cu=P,
+             o=P, lse=P, ws=P, nbytes=full, T=500, S=3, H=8, Hkv=2, d=128, M=400, n=20, page=16, scale=0.1,
+             window=0, sinks=0):
+        return lib.attn_fwd_paged(q, qs, P, P, ks, vs, kind, kscale, vscale, table, P, cu, o, lse, ws, nbytes,
+                                  T, S, H, Hkv, d, M, n, page, scale, window, sinks, None)
+    assert call(nbytes=full - 1) == WORKSPACE
+    for bad in (dict(d=96), dict(kind=2), dict(page=8), dict(page=24), dict(page=2048),
+                dict(S=70000, nbytes=1 << 40), dict(H=258, Hkv=2, qs=258 * 128, nbytes=1 << 40)):
+        assert call(**bad) == UNSUPPORTED, bad
+    for bad in (dict(q=None), dict(q=ODD), dict(table=None), dict(cu=None), dict(cu=ODD), dict(o=ODD),
+                dict(lse=None), dict(ws=None), dict(T=-1), dict(S=0), dict(Hkv=3), dict(M=0), dict(n=0),
+                dict(qs=8 * 128 - 8), dict(qs=8 * 128 + 4), dict(ks=2 * 16 * 128 - 8), dict(vs=2 * 16 * 128 + 4),
+                dict(scale=-1.0), dict(scale=float("nan")), dict(window=-1), dict(sinks=-1), dict(sinks=4),
+                dict(kscale=P), dict(kind=1), dict(kind=1, kscale=P),
+                dict(kind=1, kscale=P, vscale=P, ks=2 * 16 * 128 + 8)):
+        assert call(**bad) == INVALID, bad
+    assert call(T=0, q=None, o=None, lse=None, ws=None) == 0       # nothing to do
+
+
+def test_selection(lib):
+    def pool(k=P, ks=2 * 16 * 128, kind=0, scale=None, means=P, table=P, start=P, S=3, M=4, n=20, Hkv=2, d=128,
+             page=16):
+        return lib.attn_kv_pool(k, ks, kind, scale, means, table, start, P, S, M, n, Hkv, d, page, None)
+    for bad in (dict(k=None), dict(k=ODD), dict(means=ODD), dict(means=None), dict(table=None), dict(start=ODD),
+                dict(S=0), dict(M=0), dict(n=0), dict(Hkv=0), dict(ks=2 * 16 * 128 - 8), dict(ks=2 * 16 * 128 + 4),
+                dict(kind=1), dict(scale=P), dict(kind=1, scale=P, ks=2 * 16 * 128 + 8)):
+        assert pool(**bad) == INVALID, bad
+    for bad in (dict(S=70000), dict(d=96), dict(page=24), dict(page=2048), dict(kind=2)):
+        assert pool(**bad) == UNSUPPORTED, bad
+
+    size = lib.attn_select_pages_workspace_bytes
+    full = size(500, 3, 8, 2, 128, 400, 16, 5, 1, 0)
+    assert full > 0
+    for bad in ((500, 3, 8, 3, 128, 400, 16, 5, 1, 0), (500, 3, 8, 2, 96, 400, 16, 5, 1, 0),
+                (500, 3, 8, 2, 128, 32769, 16, 5, 1, 0), (500, 3, 8, 2, 128, 400, 16, -1, 1, 0),
+                (500, 3, 8, 2, 128, 400, 16, 5, 0, 0), (500, 3, 8, 2, 128, 400, 16, 5, 1, -1),
+                (500, 3, 8, 2, 128, 400, 16, 2 ** 31 - 1, 1, 0), (0, 3, 8, 2, 128, 400, 16, 5, 1, 0)):
+        assert size(*bad) == 0, bad
+    # however many rows there are, their scores go through in turns
+    assert size(10 ** 6, 3, 8, 2, 128, 32768, 16, 5, 1, 0) < 1e9
+
+    def select(q=P, qs=8 * 128, means=P, table=P, cu=P, pages=P, lens=P, ws=P, nbytes=full, T=500, S=3, H=8, Hkv=2,
+               d=128, M=400, n=20, page=16, top=5, local=1, first=0):
+        return lib.attn_select_pages(q, qs, means, table, P, cu, pages, lens, ws, nbytes, T, S, H, Hkv, d, M, n, page,
+                                     top, local, first, None)
+    assert select(nbytes=full - 1) == WORKSPACE
+    for bad in (dict(q=None), dict(q=ODD), dict(means=ODD), dict(table=None), dict(cu=ODD), dict(pages=None),
+                dict(lens=None), dict(ws=ODD), dict(T=-1), dict(S=0), dict(Hkv=3), dict(M=0), dict(n=0),
+                dict(qs=8 * 128 - 8), dict(qs=8 * 128 + 4), dict(top=-1), dict(local=0), dict(first=-1)):
+        assert select(**bad) == INVALID, bad
+    for bad in (dict(d=96), dict(page=24), dict(S=70000), dict(M=32769), dict(top=2 ** 31 - 1), dict(top=10 ** 9)):
+        assert select(**bad) == UNSUPPORTED, bad
+    assert select(T=0, q=None, pages=None, ws=None) == 0
+
+    full = lib.attn_decode_paged_workspace_bytes(300, 8, 2, 128, 400, 16)
+
+    def decode(q=P, pages=P, lens=P, ws=P, nbytes=full, T=300, H=8, Hkv=2, d=128, M=400, n=20, page=16, kind=0):
+        return lib.attn_decode_selected(q, H * d, P, P, Hkv * page * d, Hkv * page * d, kind, None, None, pages, lens,
+                                        P, P, ws, nbytes, T, H, Hkv, d, M, n, page, 0.1, None)
+    assert decode(nbytes=full - 1) == WORKSPACE
+    for bad in (dict(q=None), dict(pages=ODD), dict(lens=None), dict(ws=None), dict(T=0), dict(Hkv=3), dict(M=0),
+                dict(kind=1)):
+        assert decode(**bad) == INVALID, bad
+    for bad in (dict(d=96), dict(page=24), dict(T=70000, nbytes=1 << 40), dict(M=2 ** 31 - 1, nbytes=1 << 40)):
+        assert decode(**bad) == UNSUPPORTED, bad
+
+
+def test_binding_of_the_paged_calls_refuses(lib):
+    import block_sparse_softmax_gb300 as bss
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    c = torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16)
+    t, n, cu = (torch.zeros(x, dtype=torch.int32) for x in ((1, 2), 1, 2))
+    means = torch.zeros(4, 1, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        bss.attn_fwd_paged(q, c, c, t, n, cu)
+    with pytest.raises(ValueError, match="CUDA"):
+        bss.attn_kv_pool(c, means, t, n, n)
+    with pytest.raises(ValueError, match="CUDA"):
+        bss.attn_select_pages(q, means, t, n, cu, 3, 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        bss.attn_decode_selected(q, c, c, torch.zeros(3, 1, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))

@@ -4,135 +4,1505 @@
 // Mathematics: row t of sequence s stands at pos = n - (cu[s+1] - t), n the
 // sequence's length; over the keys j <= pos (with a window only those with j >
 // pos - window or j < sinks)
-//     O = sum_j p_j V_j / l,  p_j = exp(scale q . k_j - m),  l = sum_j p_j.
+//     O = sum_j p_j V_j / l,  p_j = exp(scale q . k_j - m),  l = sum_j p_j,
+// kept as the running state (m, l, A) of the online softmax, so that any cut of
+// the keys can be joined afterwards: with m* = max m_c,
+//     l* = sum_c e^{m_c - m*} l_c,   A* = sum_c e^{m_c - m*} A_c.
 //
-// The simplest form: a warp a row and query head, a key a lane.
+// What bounds it: with few new tokens a K/V head HBM, which every key and value
+// comes from once; with many the tensor pipe.  Both ask for full 128-row tiles:
+//   * A tile's rows are the (token, query head) pairs of 128 / G tokens, G the
+//     query heads of a K/V head: one box of TMA, and a group's heads share every
+//     key that is read.
+//   * Its keys are blocks of 128, two at a time: S of a pair by M128 N256 MMAs, S
+//     (256 columns) | P | O in tensor memory, P V block by block, as in
+//     window_fwd.cu; a block is gathered from its pages by boxes of min(page, 128)
+//     rows, a lane of the producer warp each.
+//   * The work is cut on the GPU, from the lengths (chunk_plan_kernel): pieces
+//     are parts of a tile's keys, of about equal length, and CTAs take them by a
+//     counter.  A sequence's pieces are numbered so that those that run at the
+//     same time share their keys (tiles first, then key parts): L2 serves all but
+//     one of them.  The parts of a tile leave (m, l, A) in the workspace, and a
+//     last kernel joins them in order (so the counter does not show in a bit).
+//   * e4m3 pages are read as they are.  One MMA wants the same 16-bit type of both
+//     operands, so a warpgroup turns a tile into fp16, exactly, on its way through
+//     shared memory; Q is scaled row by row by a power of two (largest element in
+//     [128, 256)) and P by 2^7, so that fp16 rounds them by at most 2^-32 of a
+//     row's largest element (Q) or 2^-11 of the element (P, and 2^-31 of the
+//     largest).  Over bf16 pages P is rounded to bf16, V's type.
+// Rows of the caches that hold no token may hold anything: V's are set to zero in
+// shared memory, S's are masked.
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "host.cuh"
+#include "window.cuh"
 
 namespace bss {
 namespace {
 
 constexpr int kMaxSeqs = 65536;
+constexpr int kMaxGroup = 128;             // query heads of a K/V head: rows of a tile
+constexpr int kMaxParts = 152 * 8;         // parts that wait to be joined
+constexpr int kLeastPairs = 4;             // pairs of key blocks of a part at least
+
+// What the plan leaves for the other kernels.
+struct ChunkPlan {
+  int pieces1, pieces;       // of the long kind, in all
+  int next;                  // pieces taken, past each CTA's first
+  int joins;                 // (tile, K/V head)s that are joined
+  int pad[4];
+};
+struct ChunkSeq {            // of a sequence: pieces of either kind, slots and joins before it,
+  int before1, before2, slot0, join0;
+};
 
 struct ChunkParams {
-  const __nv_bfloat16* q;
-  long long q_stride;
-  const uint8_t* k;
-  const uint8_t* v;
-  size_t k_stride, v_stride;     // bytes from page to page
-  const float* k_scale;
-  const float* v_scale;
   const int* table;
   const int* lens;
   const int* cu;
+  const float* k_scale;
+  const float* v_scale;
   __nv_bfloat16* o;
   float* lse;
-  int T, S, H, Hkv, G, M, P;
+  ChunkPlan* plan;
+  ChunkSeq* seq;             // [S]
+  int* cuts;                 // [S] parts of a tile's keys
+  float* part;               // [slots]: A as [d / 4][128 rows][4], m (log2 units) [128], l [128]
+  int slots;
+  int T, S, H, Hkv, G, tpt, M, P;     // tpt: tokens of a tile
   int page_log2;
+  int ctas;
   float scale_log2;
-  long long window;
+  int window;                // no window: more than any position
   int sinks;
   int* err;
 };
 
-template <bool FP8>
-__device__ __forceinline__ float element(const uint8_t* x, int i) {
-  if constexpr (FP8) {
-    uint32_t y;
-    asm("{\n\t.reg .b16 v;\n\tcvt.u16.u32 v, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, v;\n\t}" : "=r"(y)
-        : "r"(static_cast<uint32_t>(x[i])));
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(y & 0xFFFFu)));
-  } else {
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x)[i]);
+// A sequence's new tokens: rows [a, b) of the batch, row t at position t + shift.
+struct SeqRows {
+  int a, b, n;
+  long long shift;
+  bool bad;                  // its length is out of range
+};
+__device__ __forceinline__ SeqRows seq_rows(const ChunkParams& p, int s) {
+  SeqRows r;
+  const int c0 = __ldg(p.cu + s), c1 = __ldg(p.cu + s + 1);
+  const int len = __ldg(p.lens + s);
+  r.a = min(max(c0, 0), p.T);
+  r.b = max(r.a, min(c1, p.T));
+  const long long most = min(static_cast<long long>(p.M) << p.page_log2, static_cast<long long>(kMaxTokens));
+  r.n = static_cast<int>(max(0ll, min(static_cast<long long>(len), most)));
+  r.bad = len < 0 || len > most;
+  r.shift = static_cast<long long>(r.n) - c1;
+  return r;
+}
+// Tile i of a sequence: rows [t0, t0 + ntok) of the batch, the first at position
+// p0 (before the first token: at most 128 before it).
+struct Tile {
+  int t0, ntok, p0;
+};
+__device__ __forceinline__ Tile seq_tile(const SeqRows& r, int i, int tpt) {
+  Tile t;
+  t.t0 = r.a + i * tpt;
+  t.ntok = min(tpt, r.b - t.t0);
+  t.p0 = clamped(t.t0 + r.shift, -kTileM, kMaxTokens);
+  return t;
+}
+__device__ __forceinline__ WindowBlocks tile_blocks(const ChunkParams& p, const Tile& t, int n) {
+  return window_blocks(WindowRows{t.p0, t.p0 - p.window + 1}, min(p.sinks, n), t.ntok, n);
+}
+
+// ----------------------------------------------------------------------------
+// the plan: one CTA
+// ----------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanCuts = 10;              // lengths of parts that are weighed
+struct SeqWork {
+  int nt, longest;           // tiles; pairs of key blocks of its longest tile
+  float mean;                // ... of a tile
+};
+__device__ __forceinline__ SeqWork seq_work(const ChunkParams& p, const SeqRows& r) {
+  SeqWork w{(r.b - r.a + p.tpt - 1) / p.tpt, 0, 0.f};
+  if (w.nt == 0) return w;
+  const int first = (tile_blocks(p, seq_tile(r, 0, p.tpt), r.n).count() + 1) / 2;
+  const int last = (tile_blocks(p, seq_tile(r, w.nt - 1, p.tpt), r.n).count() + 1) / 2;
+  w.longest = max(first, last);
+  w.mean = 0.5f * static_cast<float>(first + last);
+  return w;
+}
+// Parts of the tiles of a sequence, where a part has about `len` pairs at most.
+__device__ __forceinline__ int seq_cuts(const SeqWork& w, int len) {
+  return w.longest <= len ? 1 : (w.longest + len - 1) / len;
+}
+// ... whether those are long pieces, which go first.
+__device__ __forceinline__ bool long_pieces(const SeqWork& w, int cuts, int len) {
+  return 2ll * w.longest > static_cast<long long>(len) * cuts;
+}
+
+// Exclusive prefix sums of four numbers a thread over the block; *total gets the sums.
+__device__ __forceinline__ int4 plan_scan(int4 v, int4* warp_sums, int4* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int4 x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int4 y = make_int4(__shfl_up_sync(0xFFFFFFFFu, x.x, o), __shfl_up_sync(0xFFFFFFFFu, x.y, o),
+                             __shfl_up_sync(0xFFFFFFFFu, x.z, o), __shfl_up_sync(0xFFFFFFFFu, x.w, o));
+    if (lane >= o) x = make_int4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
   }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int4 before = make_int4(x.x - v.x, x.y - v.y, x.z - v.z, x.w - v.w), sum = make_int4(0, 0, 0, 0);
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const int4 y = warp_sums[w];
+    if (w < warp) before = make_int4(before.x + y.x, before.y + y.y, before.z + y.z, before.w + y.w);
+    sum = make_int4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
+  }
+  *total = sum;
+  return before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
+  __shared__ float sums[kPlanThreads / 32][4 * kPlanCuts];
+  __shared__ float all[4 * kPlanCuts];
+  __shared__ int4 scan[kPlanThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int warps = min(kPlanThreads / 32, (p.S + 31) / 32);         // with a sequence of their own
+  SeqWork mine{0, 0, 0.f};
+  if (tid < p.S) {
+    const SeqRows r = seq_rows(p, tid);
+    mine = seq_work(p, r);
+    if (r.bad) record_error(p.err, ATTN_ERR_BAD_PAGES);
+  }
+  auto work = [&](int s) { return s == tid ? mine : seq_work(p, seq_rows(p, s)); };
+  auto reduce = [&](float (&v)[4 * kPlanCuts], int n) {               // sums (the first: a maximum) to `all`
+#pragma unroll
+    for (int i = 0; i < 4 * kPlanCuts; ++i) {
+      if (i >= n) break;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float y = __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+        v[i] = n == 2 && i == 0 ? fmaxf(v[i], y) : v[i] + y;
+      }
+      if (lane == 0) sums[warp][i] = v[i];
+    }
+    __syncthreads();
+    if (tid < n) {
+      float x = 0.f;
+      for (int w = 0; w < warps; ++w) x = n == 2 && tid == 0 ? fmaxf(x, sums[w][tid]) : x + sums[w][tid];
+      all[tid] = x;
+    }
+    __syncthreads();
+  };
+  // all pairs, and the longest tile's
+  float v[4 * kPlanCuts];
+#pragma unroll
+  for (int i = 0; i < 4 * kPlanCuts; ++i) v[i] = 0.f;
+  for (int s = tid; s < p.S; s += kPlanThreads) {
+    const SeqWork w = work(s);
+    v[0] = fmaxf(v[0], static_cast<float>(w.longest));
+    v[1] += w.mean * static_cast<float>(w.nt);
+  }
+  reduce(v, 2);
+  const int longest = static_cast<int>(all[0]);
+  const float per_cta = all[1] * static_cast<float>(p.Hkv) / static_cast<float>(p.ctas);
+  __syncthreads();
+  // lengths of parts: a whole tile, and the fair share of a CTA cut into 1, 1.25, ...
+  auto length = [&](int i) {
+    const float turns[kPlanCuts - 1] = {1.f, 1.25f, 1.5f, 2.f, 2.5f, 3.f, 4.f, 5.f, 8.f};
+    float t = 1.f;
+#pragma unroll
+    for (int j = 0; j < kPlanCuts - 1; ++j)
+      if (i == j + 1) t = turns[j];
+    return i == 0 ? max(1, longest) : max(kLeastPairs, static_cast<int>(ceilf(per_cta / t)));
+  };
+  // long pieces (their number, their pairs with what a piece costs beside them), the
+  // others' pairs, slots
+#pragma unroll
+  for (int i = 0; i < 4 * kPlanCuts; ++i) v[i] = 0.f;
+  for (int s = tid; s < p.S; s += kPlanThreads) {
+    const SeqWork w = work(s);
+    const float tiles = static_cast<float>(w.nt) * static_cast<float>(p.Hkv);
+#pragma unroll
+    for (int i = 0; i < kPlanCuts; ++i) {
+      const int len = length(i);
+      const int cuts = seq_cuts(w, len);
+      // about a pair's time to begin and end a piece, as much again to leave a part
+      const float cost = tiles * (w.mean + static_cast<float>(cuts) * (cuts > 1 ? 2.f : 1.f));
+      if (long_pieces(w, cuts, len)) {
+        v[4 * i] += tiles * static_cast<float>(cuts);
+        v[4 * i + 1] += cost;
+      } else {
+        v[4 * i + 2] += cost;
+      }
+      if (cuts > 1) v[4 * i + 3] += tiles * static_cast<float>(cuts);
+    }
+  }
+  reduce(v, 4 * kPlanCuts);
+  int best = 0;
+  float least = 3.4e38f;
+#pragma unroll
+  for (int i = 0; i < kPlanCuts; ++i) {
+    const float n = all[4 * i], each = n > 0.f ? all[4 * i + 1] / n : 0.f;
+    const float ctas = static_cast<float>(p.ctas), turns = ceilf(n / ctas);
+    const float idle = (turns * ctas - n) * each;
+    // the long pieces' turns, what does not fit beside the last of them, and the join
+    const float t = turns * each + fmaxf(0.f, all[4 * i + 2] - idle) / ctas + (all[4 * i + 3] > 0.f ? 2.f : 0.f);
+    if (i > 0 && all[4 * i + 3] > static_cast<float>(p.slots)) continue;
+    if (t < least) {
+      least = t;
+      best = i;
+    }
+  }
+  const int len = length(best);
+  int4 base = make_int4(0, 0, 0, 0);
+  for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int4 x = make_int4(0, 0, 0, 0);
+    int cuts = 1;
+    if (s < p.S) {
+      const SeqWork w = work(s);
+      cuts = seq_cuts(w, len);
+      const int tiles = w.nt * p.Hkv;
+      (long_pieces(w, cuts, len) ? x.x : x.y) = tiles * cuts;
+      if (cuts > 1) {
+        x.z = tiles * cuts;
+        x.w = tiles;
+      }
+    }
+    int4 total;
+    const int4 y = plan_scan(x, scan, &total);
+    if (s < p.S) {
+      p.seq[s] = ChunkSeq{base.x + y.x, base.y + y.y, base.z + y.z, base.w + y.w};
+      p.cuts[s] = cuts;
+    }
+    base = make_int4(base.x + total.x, base.y + total.y, base.z + total.z, base.w + total.w);
+  }
+  if (tid == 0) {
+    p.plan->pieces1 = base.x;
+    p.plan->pieces = base.x + base.y;
+    p.plan->next = 0;
+    p.plan->joins = base.w;
+  }
+}
+
+// The last sequence with at most x before it, by a whole warp; `before` of it.
+template <class Before>
+__device__ __forceinline__ int find_seq(int S, int x, int lane, const Before& before) {
+  int lo = 0, hi = S;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, lane == 0 || (i < hi && before(i) <= x));
+    lo += (31 - __clz(yes)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// ----------------------------------------------------------------------------
+// the main kernel
+// ----------------------------------------------------------------------------
+// What the roles need of a piece.
+struct Piece {
+  int t0, ntok, p0, n, hkv;
+  int slot;                  // -1: the whole tile's keys
+  WindowBlocks kb;
+};
+
+// ... and the producer: its sequence, the first key that some row of the sequence
+// has in its window.
+struct Work : Piece {
+  int s, low;
+};
+// Rows of a V block that some row of the sequence sees: [low, rows) and below
+// `sinks`, in the groups of 16 that have a page.  What the others hold (rows past
+// the last token above all) becomes zeros before a product meets it.
+struct BlockRows {
+  int rows, low, sinks;
+  uint32_t groups;
+  __device__ __forceinline__ bool all() const {
+    return rows == kTileN && groups == 255u && (low == 0 || sinks >= low);
+  }
+  __device__ __forceinline__ bool has(int r) const {
+    return r < rows && (r >= low || r < sinks) && (groups >> (r >> 4) & 1u);
+  }
+  __device__ __forceinline__ uint32_t packed() const {
+    return static_cast<uint32_t>(rows) << 24 | static_cast<uint32_t>(low) << 16 | static_cast<uint32_t>(sinks) << 8 |
+           groups;
+  }
+};
+__device__ __forceinline__ BlockRows block_rows(uint32_t x) {
+  return BlockRows{static_cast<int>(x >> 24), static_cast<int>(x >> 16 & 255u), static_cast<int>(x >> 8 & 255u),
+                   x & 255u};
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(128) attn_fwd_paged_kernel(const ChunkParams p) {
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const long long x = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (x >= static_cast<long long>(p.T) * p.H) return;
-  const int t = static_cast<int>(x / p.H), h = static_cast<int>(x % p.H), hkv = h / p.G;
-  int s = 0, hi = p.S;
-  while (s < hi) {
-    const int mid = (s + hi + 1) >> 1;
-    if (__ldg(p.cu + mid) <= t) s = mid;
-    else hi = mid - 1;
-  }
-  if (s >= p.S || __ldg(p.cu + s) > t) return;               // a row of no sequence
-  const long long most = min(static_cast<long long>(p.M) << p.page_log2, static_cast<long long>(kMaxTokens));
-  const int len = __ldg(p.lens + s);
-  const long long n = max(0ll, min(static_cast<long long>(len), most));
-  const long long pos = min(n, n - (static_cast<long long>(__ldg(p.cu + s + 1)) - t) + 1) - 1;
-  if (lane == 0 && (len < 0 || len > most || pos < 0)) record_error(p.err, ATTN_ERR_BAD_PAGES);
-  float q[D];
-  const __nv_bfloat16* qp = p.q + t * p.q_stride + static_cast<long long>(h) * D;
-#pragma unroll
-  for (int i = 0; i < D; ++i) q[i] = __bfloat162float(qp[i]);
-  const float sl2 = p.scale_log2 * (FP8 ? __ldg(p.k_scale + hkv) : 1.f);
-  const float NEG_INF = -__int_as_float(0x7f800000);
-  float m = NEG_INF, l = 0.f, acc[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-  const long long lo = p.window > 0 ? max(0ll, pos + 1 - p.window) : 0;
-  for (long long j0 = 0; j0 <= pos; j0 += 32) {
-    if (j0 + 32 <= lo && j0 >= p.sinks) continue;
-    const long long j = j0 + lane;
-    bool seen = j <= pos && (j >= lo || j < p.sinks);
-    int pg = 0;
-    if (seen) {
-      pg = __ldg(p.table + static_cast<size_t>(s) * p.M + (j >> p.page_log2));
-      if (pg < 0 || pg >= p.P) {
-        record_error(p.err, ATTN_ERR_BAD_PAGES);
-        seen = false;
-        pg = 0;
-      }
-    }
-    const size_t off = ((static_cast<size_t>(hkv) << p.page_log2) + (j & ((1 << p.page_log2) - 1))) * D * (FP8 ? 1 : 2);
-    float y = NEG_INF;
-    if (seen) {
-      const uint8_t* kp = p.k + pg * p.k_stride + off;
-      float d = 0.f;
-      for (int i = 0; i < D; ++i) d = fmaf(q[i], element<FP8>(kp, i), d);
-      y = d * sl2;
-    }
-    float mx = y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    const float mn = fmaxf(m, mx);
-    const float mu = mn == NEG_INF ? 0.f : mn;
-    const float al = exp2f(m - mu), pr = seen ? exp2f(y - mu) : 0.f;
-    m = mn;
-    l = l * al + pr;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] *= al;
-    for (int u = 0; u < 32; ++u) {
-      if (!__shfl_sync(0xFFFFFFFFu, seen ? 1 : 0, u)) continue;
-      const float pu = __shfl_sync(0xFFFFFFFFu, pr, u);
-      const uint8_t* vp = p.v + __shfl_sync(0xFFFFFFFFu, pg, u) * p.v_stride + __shfl_sync(0xFFFFFFFFu, off, u);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(pu, element<FP8>(vp, i * 32 + lane), acc[i]);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-  const float inv = l == 0.f ? 0.f : (FP8 ? __ldg(p.v_scale + hkv) : 1.f) / l;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) p.o[x * D + i * 32 + lane] = __float2bfloat16(acc[i] * inv);
-  if (lane == 0) p.lse[x] = l == 0.f ? NEG_INF : (m + __log2f(l)) * kLn2;
+struct ChunkCfg {
+  static constexpr int kChunks = D / 64;                   // 128-byte swizzle atoms across d
+  static constexpr int kChunkBytes = kTileM * 128;
+  static constexpr int kTileBytes = kTileM * D * 2;
+  static constexpr int kRawBytes = kTileM * D;             // 128 rows of e4m3
+  static constexpr int kStagesQ = D == 64 ? 2 : 1;
+  // K: pairs of blocks, side by side for an N = 256 MMA; e4m3: single blocks
+  static constexpr int kKBytes = FP8 ? kTileBytes : 2 * kTileBytes;
+  static constexpr int kStagesK = FP8 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
+  static constexpr int kStagesV = D == 64 ? 4 : 2;
+  static constexpr int kStagesR = FP8 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kQOff + kStagesQ * kTileBytes;
+  static constexpr int kVOff = kKOff + kStagesK * kKBytes;
+  static constexpr int kROff = kVOff + kStagesV * kTileBytes;
+  static constexpr int kBarOff = kROff + kStagesR * kRawBytes;
+  static constexpr int kBarQFull = 0;
+  static constexpr int kBarQEmpty = kBarQFull + kStagesQ;
+  static constexpr int kBarKFull = kBarQEmpty + kStagesQ;
+  static constexpr int kBarKEmpty = kBarKFull + kStagesK;
+  static constexpr int kBarVFull = kBarKEmpty + kStagesK;
+  static constexpr int kBarVEmpty = kBarVFull + kStagesV;
+  static constexpr int kBarSFull = kBarVEmpty + kStagesV;  // a pair's S in TMEM
+  static constexpr int kBarSFree = kBarSFull + 1;          // ... read into registers by both warpgroups
+  // [2] P of key block X written by warpgroup X; block 0's also waits for
+  // warpgroup 1's rescale of its half of O
+  static constexpr int kBarPFull = kBarSFree + 1;
+  static constexpr int kBarPvDone = kBarPFull + 2;         // [2] a pair's P V of block X completed
+  static constexpr int kBarXch = kBarPvDone + 2;           // [2] row values exchanged, by parity
+  static constexpr int kBarOFull = kBarXch + 2;            // a piece's last P V completed
+  static constexpr int kBarOEmpty = kBarOFull + 1;         // ... O and the row factors read
+  static constexpr int kBarLFull = kBarOEmpty + 1;         // a piece's row factors written
+  static constexpr int kBarMmaDone = kBarLFull + 1;
+  static constexpr int kBarPieceFull = kBarMmaDone + 1;    // [2] a piece's description written
+  static constexpr int kBarPieceEmpty = kBarPieceFull + 2; // [2] ... read by every role
+  // bf16: a V block that is cleaned has landed; e4m3: Q has landed, by stage
+  static constexpr int kBarLand = kBarPieceEmpty + 2;
+  static constexpr int kBarRFull = kBarLand + kStagesQ;    // raw tiles: landed
+  static constexpr int kBarREmpty = kBarRFull + kStagesR;  // ... converted
+  static constexpr int kNumBars = kBarREmpty + kStagesR;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kTmemSlotOff = kMiscOff;
+  static constexpr int kAbortOff = kMiscOff + 4;
+  // [kRing] which groups of 16 keys of a pair have a page; a pair's entry is
+  // written when its K is asked for, and read before its S is given back: at
+  // most the K stages and raw tiles, and one, lie between
+  static constexpr int kRing = D == 64 ? 16 : 8;
+  static_assert(kRing > kStagesK + kStagesR + 1, "a pair's entry is read before it is written again");
+  static constexpr int kValidOff = kMiscOff + 8;
+  static constexpr int kRawInfoOff = kValidOff + kRing * 2;        // [stages] BlockRows of a raw tile
+  static constexpr int kPieceOff = kRawInfoOff + ((kStagesR * 4 + 7) / 8) * 8;
+  static constexpr int kUpOff = kPieceOff + 2 * static_cast<int>(sizeof(Piece));  // exponents of Q's factors
+  static constexpr int kXchOff = (kUpOff + (FP8 ? kTileM : 0) + 15) / 16 * 16;
+  static constexpr int kInvOff = kXchOff + 2 * 2 * kTileM * 4;
+  static constexpr int kSmemBytes = kInvOff + kTileM * 4;
+  static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(kBarOff % 8 == 0 && kPieceOff % 8 == 0, "alignment");
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS = 0;      // S: 256 fp32 columns (key block X at 128 X)
+  static constexpr uint32_t kColP = 256;    // P: 256 keys, 16-bit pairs (block X at 256 + 64 X)
+  static constexpr uint32_t kColO = 384;    // O: D fp32 columns
+  static constexpr int kThreads = 512;
+  static constexpr int kPartFloats = kTileM * (D + 2);
+};
+
+// Register split per warpgroup (setmaxnreg): output and conversion (warps 0-3),
+// softmax (4-7, 8-11), TMA and MMA (12, 13; two idle warps).
+constexpr uint32_t kChunkOut = 48;
+constexpr uint32_t kChunkSoft = 192;
+constexpr uint32_t kChunkLow = 80;
+constexpr uint32_t kChunkLaunchRegs = 128;
+static_assert(kChunkOut + 2 * kChunkSoft + kChunkLow <= 4 * kChunkLaunchRegs, "register split exceeds the launch");
+constexpr float kP2 = 7.f;                  // e4m3: P carries 2^7
+
+// kind::f16 with fp16 operands: A and B formats 0.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                            int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {        // the low 16 bits
+  uint32_t y;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+template <int D, bool FP8>
+__global__ void __launch_bounds__(512, 1)
+    attn_fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const ChunkParams p) {
+  using C = ChunkCfg<D, FP8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {                      // the swizzle needs it: report, touch nothing
+    if (threadIdx.x == 0) record_error(p.err, ATTN_ERR_UNSUPPORTED);
+    return;
+  }
+  auto bar = [&](int i) { return sbase + C::kBarOff + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kTmemSlotOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbortOff);
+  volatile uint16_t* valid_ring = reinterpret_cast<volatile uint16_t*>(smem + C::kValidOff);
+  volatile uint32_t* raw_info = reinterpret_cast<volatile uint32_t*>(smem + C::kRawInfoOff);
+  const float NEG_INF = -__int_as_float(0x7f800000);
+
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  const int tid = static_cast<int>(threadIdx.x);
+  const int status = status_at_entry(p.err);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStagesQ; ++s) {
+      mbar_init(bar(C::kBarQFull + s), FP8 ? kTileM : 1);
+      mbar_init(bar(C::kBarQEmpty + s), 1);
+      mbar_init(bar(C::kBarLand + s), 1);
+    }
+    for (int s = 0; s < C::kStagesK; ++s) {
+      mbar_init(bar(C::kBarKFull + s), FP8 ? kTileM : 1);
+      mbar_init(bar(C::kBarKEmpty + s), 1);
+    }
+    for (int s = 0; s < C::kStagesV; ++s) {
+      mbar_init(bar(C::kBarVFull + s), FP8 ? kTileM : 1);
+      mbar_init(bar(C::kBarVEmpty + s), 1);
+    }
+    for (int s = 0; s < C::kStagesR; ++s) {
+      mbar_init(bar(C::kBarRFull + s), 1);
+      mbar_init(bar(C::kBarREmpty + s), kTileM);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(C::kBarXch + s), 2 * 4 * 32);
+      mbar_init(bar(C::kBarPvDone + s), 1);
+      mbar_init(bar(C::kBarPieceFull + s), 1);
+      mbar_init(bar(C::kBarPieceEmpty + s), 1 + 2 * 4 + 4);      // MMA thread, softmax and output warps
+    }
+    mbar_init(bar(C::kBarSFull), 1);
+    mbar_init(bar(C::kBarSFree), 2 * 4 * 32);
+    mbar_init(bar(C::kBarPFull + 0), 2 * 4 * 32);
+    mbar_init(bar(C::kBarPFull + 1), 4 * 32);
+    mbar_init(bar(C::kBarOFull), 1);
+    mbar_init(bar(C::kBarOEmpty), 4 * 32);
+    mbar_init(bar(C::kBarLFull), 4 * 32);
+    mbar_init(bar(C::kBarMmaDone), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(sbase + C::kTmemSlotOff, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const bool gave_up = __syncthreads_or(status == ATTN_ERR_TIMEOUT);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (gave_up) {
+    if (warp == 0) {
+      __syncwarp();
+      tmem_dealloc(tmem, C::kTmemCols);
+    }
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the plan is there, and all before it
+
+  // A role's next piece (slot `i & 1` of the ring holds piece i); false at the end
+  // or when a wait ran out.  `whole`: all lanes of a warp ask.
+  auto piece_slot = [&](int i) { return reinterpret_cast<volatile Piece*>(smem + C::kPieceOff) + (i & 1); };
+  auto read_piece = [&](int i, Piece& x) {
+    const volatile Piece* src = piece_slot(i);
+    x.t0 = src->t0;
+    x.ntok = src->ntok;
+    x.p0 = src->p0;
+    x.n = src->n;
+    x.hkv = src->hkv;
+    x.slot = src->slot;
+    x.kb.nsb = src->kb.nsb;
+    x.kb.wb0 = src->kb.wb0;
+    x.kb.nwb = src->kb.nwb;
+    x.kb.sb0 = src->kb.sb0;
+  };
+
+  if (warp >= 12) {
+    regs_set<kChunkLow, kChunkLaunchRegs>();
+    if (warp == 12) {
+      // =================== TMA producer (a whole warp) ===================
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
+      const int total = p.plan->pieces, total1 = p.plan->pieces1;
+      const int page = 1 << p.page_log2;
+      const int br = min(page, kTileN);                    // rows of a box
+      const int subs = kTileN / br;                        // boxes of a block, a chunk of d each
+      constexpr int kAcross = FP8 ? 1 : C::kChunks;
+      const int c_of = lane % kAcross;
+      const int sub = lane / kAcross % subs;
+      const int t_of = lane / kAcross / subs;              // block of the pair (2 and more: none)
+      const uint32_t box_bytes = static_cast<uint32_t>(br) * (FP8 ? D : 128);
+      int ik = 0, iv = 0, ir = 0;    // K stages, V tiles, raw tiles filled (over all pieces)
+      int qn = 0, np = 0, pairs = 0, landed = 0;
+      auto wait = [&](int b, uint32_t parity) -> bool {
+        return __all_sync(0xFFFFFFFFu, wait_bar(bar(b), parity, abort_flag, p.err));
+      };
+
+      // The next piece that has keys, from piece `index` on; pieces without are
+      // seen to here.  index moves on to the piece after it.
+      int index = static_cast<int>(blockIdx.x);
+      auto take = [&]() {
+        int x = 0;
+        if (lane == 0) x = atomicAdd(&p.plan->next, 1);
+        return static_cast<int>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, x, 0);
+      };
+      auto next_piece = [&](Work& x) -> bool {
+        while (index >= 0 && index < total) {
+          int s, in;
+          if (index < total1) {
+            s = find_seq(p.S, index, lane, [&](int i) { return p.seq[i].before1; });
+            in = index - p.seq[s].before1;
+          } else {
+            s = find_seq(p.S, index - total1, lane, [&](int i) { return p.seq[i].before2; });
+            in = index - total1 - p.seq[s].before2;
+          }
+          index = take();
+          const SeqRows r = seq_rows(p, s);
+          const int cuts = p.cuts[s];
+          const int nt = (r.b - r.a + p.tpt - 1) / p.tpt;
+          // tiles first (the last ones, which see most keys, lead), then parts, then heads
+          const int cut = in / nt % cuts;
+          x.hkv = in / nt / cuts;
+          const Tile t = seq_tile(r, nt - 1 - in % nt, p.tpt);
+          x.t0 = t.t0;
+          x.ntok = t.ntok;
+          x.p0 = t.p0;
+          x.n = r.n;
+          x.kb = tile_blocks(p, t, r.n);
+          if (cuts > 1) x.kb = x.kb.part(cut, cuts);
+          x.slot = cuts > 1 ? p.seq[s].slot0 + in : -1;
+          if (t.p0 < 0 && lane == 0) record_error(p.err, ATTN_ERR_BAD_PAGES);
+          x.s = s;
+          x.low = clamped(r.a + r.shift - p.window + 1, 0, r.n);
+          if (x.kb.count() > 0) return true;
+          if (x.slot >= 0) {                               // a part without keys
+            float* l = p.part + static_cast<size_t>(x.slot) * C::kPartFloats + kTileM * (D + 1);
+            for (int i = lane; i < kTileM; i += 32) l[i] = 0.f;
+          } else {                                         // rows that see nothing
+            for (int i = 0; i < x.ntok * p.G; ++i) {
+              const size_t row = static_cast<size_t>(x.t0 + i / p.G) * p.H + x.hkv * p.G + i % p.G;
+              for (int e = lane; e < D; e += 32) p.o[row * D + e] = __float2bfloat16(0.f);
+              if (lane == 0) p.lse[row] = NEG_INF;
+            }
+          }
+        }
+        return false;
+      };
+      // Hand a piece (or, with no key blocks, the end) to the other roles.
+      auto publish = [&](const Piece& x) -> bool {
+        if (np >= 2 && !wait(C::kBarPieceEmpty + (np & 1), ((np >> 1) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          volatile Piece* dst = piece_slot(np);
+          dst->t0 = x.t0;
+          dst->ntok = x.ntok;
+          dst->p0 = x.p0;
+          dst->n = x.n;
+          dst->hkv = x.hkv;
+          dst->slot = x.slot;
+          dst->kb.nsb = x.kb.nsb;
+          dst->kb.wb0 = x.kb.wb0;
+          dst->kb.nwb = x.kb.nwb;
+          dst->kb.sb0 = x.kb.sb0;
+          mbar_arrive(bar(C::kBarPieceFull + (np & 1)));
+        }
+        ++np;
+        return true;
+      };
+
+      // This lane's box of a pair of key blocks: its page (-1: none is copied).
+      struct Box {
+        int page, key;               // page, first key
+        bool seen;                   // a page that some row of the piece sees
+      };
+      auto fetch = [&](const Work& x, int k) {
+        Box b{-1, 0, false};
+        if (t_of < 2 && 2 * k + t_of < x.kb.count()) {
+          b.key = x.kb.at(2 * k + t_of) * kTileN + sub * br;
+          if (b.key < x.n) {
+            b.page = __ldg(p.table + static_cast<size_t>(x.s) * p.M + (b.key >> p.page_log2));
+            const int last = b.key + br - 1;
+            b.seen = b.key <= x.p0 + x.ntok - 1 && (last > x.p0 - p.window || b.key < p.sinks);
+          }
+        }
+        return b;
+      };
+      auto check = [&](Box& b) {
+        if (b.page >= 0 && b.page < p.P) return;
+        b.page = -1;
+        if (b.seen) record_error(p.err, ATTN_ERR_BAD_PAGES);
+      };
+      auto groups = [&](const Box& b) -> uint32_t {        // of the pair's 16 groups of 16 keys, those with a page
+        const uint32_t g = b.page >= 0 ? ((1u << (br / 16)) - 1u) << (t_of * 8 + sub * (br / 16)) : 0u;
+        return __reduce_or_sync(0xFFFFFFFFu, g);
+      };
+      auto copy = [&](const CUtensorMap* map, uint32_t dst, int b, const Box& x, int hkv) {
+        tma_load_3d(dst, map, bar(b), c_of * 64, (hkv << p.page_log2) + (x.key & (page - 1)), x.page);
+      };
+      auto rows_of = [&](const Work& x, int k, int t, uint32_t ok) {
+        const int k0 = x.kb.at(2 * k + t) * kTileN;
+        return BlockRows{min(kTileN, x.n - k0), max(0, min(x.low - k0, kTileN)), max(0, min(p.sinks - k0, kTileN)),
+                         ok >> (8 * t) & 255u};
+      };
+      // e4m3: block t of a pair into the next raw tile
+      auto load_raw = [&](const CUtensorMap* map, const Work& x, int k, int t, const Box& b, uint32_t ok) -> bool {
+        const int s = ir % max(1, C::kStagesR);
+        if (ir >= C::kStagesR && !wait(C::kBarREmpty + s, ((ir / max(1, C::kStagesR)) & 1) ^ 1)) return false;
+        const bool mine = t_of == t && b.page >= 0;
+        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        if (lane == 0) {
+          raw_info[s] = rows_of(x, k, t, ok).packed();
+          mbar_arrive_expect_tx(bar(C::kBarRFull + s), boxes * box_bytes);
+        }
+        __syncwarp();
+        if (mine) copy(map, sbase + C::kROff + s * C::kRawBytes + sub * br * D, C::kBarRFull + s, b, x.hkv);
+        ++ir;
+        return true;
+      };
+      auto load_k = [&](const Work& x, int k, Box& b) -> bool {
+        check(b);
+        const uint32_t ok = groups(b);
+        if (lane == 0) valid_ring[pairs % C::kRing] = static_cast<uint16_t>(ok);
+        ++pairs;
+        if constexpr (FP8) {
+          if (!load_raw(&tmK, x, k, 0, b, ok)) return false;
+          return 2 * k + 1 >= x.kb.count() || load_raw(&tmK, x, k, 1, b, ok);
+        } else {
+          const int s = ik % C::kStagesK;
+          if (ik >= C::kStagesK && !wait(C::kBarKEmpty + s, ((ik / C::kStagesK) & 1) ^ 1)) return false;
+          const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, b.page >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarKFull + s), boxes * box_bytes);
+          __syncwarp();
+          if (b.page >= 0)
+            copy(&tmK, sbase + C::kKOff + s * C::kKBytes + (c_of * 2 + t_of) * C::kChunkBytes + sub * br * 128,
+                 C::kBarKFull + s, b, x.hkv);
+          ++ik;
+          return true;
+        }
+      };
+      auto load_v = [&](const Work& x, int k, const Box& b) -> bool {
+        const uint32_t ok = groups(b);
+        for (int t = 0; t < 2 && 2 * k + t < x.kb.count(); ++t) {
+          if constexpr (FP8) {
+            if (!load_raw(&tmV, x, k, t, b, ok)) return false;
+          } else {
+            const int s = iv % C::kStagesV;
+            if (iv >= C::kStagesV && !wait(C::kBarVEmpty + s, ((iv / C::kStagesV) & 1) ^ 1)) return false;
+            const uint32_t vs = sbase + C::kVOff + s * C::kTileBytes;
+            const BlockRows rows = rows_of(x, k, t, ok);
+            const bool clean = rows.all();
+            const int full = clean ? C::kBarVFull + s : C::kBarLand;
+            const bool mine = t_of == t && b.page >= 0;
+            const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+            if (lane == 0) mbar_arrive_expect_tx(bar(full), boxes * box_bytes);
+            __syncwarp();
+            if (mine) copy(&tmV, vs + c_of * C::kChunkBytes + sub * br * 128, full, b, x.hkv);
+            ++iv;
+            if (!clean) {
+              // (the next K and Q are on their way already)
+              ++landed;
+              if (!wait(C::kBarLand, (landed - 1) & 1)) return false;
+              for (int r = 0; r < kTileN; ++r) {
+                if (rows.has(r)) continue;
+                if (lane < C::kChunks * 8)
+                  sts128(vs + (lane >> 3) * C::kChunkBytes + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(C::kBarVFull + s));
+            }
+          }
+        }
+        return true;
+      };
+      auto load_q = [&](const Piece& x) -> bool {
+        const int s = qn % C::kStagesQ;
+        // the last S that read this Q buffer must have completed
+        if (qn >= C::kStagesQ && !wait(C::kBarQEmpty + s, ((qn / C::kStagesQ) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          const int full = (FP8 ? C::kBarLand : C::kBarQFull) + s;
+          mbar_arrive_expect_tx(bar(full), static_cast<uint32_t>(C::kChunks * 128 * p.G * p.tpt));
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_3d(sbase + C::kQOff + s * C::kTileBytes + c * C::kChunkBytes, &tmQ, bar(full), c * 64,
+                        x.hkv * p.G, x.t0);
+        }
+        __syncwarp();
+        ++qn;
+        return true;
+      };
+
+      Work x, y;
+      Box now{-1, 0, false}, first{-1, 0, false};
+      auto look_ahead = [&]() -> bool {
+        if (!next_piece(y)) return false;
+        first = fetch(y, 0);
+        return true;
+      };
+      bool more = look_ahead();
+      bool ok = true;
+      if (more) {
+        x = y;
+        now = first;
+        ok = publish(x) && load_k(x, 0, now) && load_q(x);
+      }
+      while (ok && more) {
+        const int ns = (x.kb.count() + 1) / 2;
+        Box then{-1, 0, false};
+        if (ns > 1) then = fetch(x, 1);
+        for (int k = 0; k < ns && ok; ++k) {
+          // V of this pair goes after K of the next one
+          const Box cur = now;
+          if (k + 1 < ns) {
+            now = then;
+            if (k + 2 < ns) then = fetch(x, k + 2);
+            ok = load_k(x, k + 1, now);
+          } else {
+            if (ns == 1) more = look_ahead();
+            if (more) {
+              now = first;
+              ok = publish(y) && load_k(y, 0, now) && load_q(y);
+            } else {
+              y.kb = WindowBlocks{0, 0, 0, 0};
+              ok = publish(y);
+            }
+          }
+          ok = ok && load_v(x, k, cur);
+          // the next piece is looked up while there is something to compute
+          if (k == 0 && ns > 1 && ok) more = look_ahead();
+        }
+        x = y;
+      }
+      if (np == 0) {                          // nothing for this CTA: the others are told
+        x.kb = WindowBlocks{0, 0, 0, 0};
+        publish(x);
+      }
+      // every copy issued has landed before the CTA may exit
+      for (int j = max(0, ik - C::kStagesK); j < ik; ++j)
+        drain_bar(bar(C::kBarKFull + j % C::kStagesK), (j / C::kStagesK) & 1);
+      for (int j = max(0, iv - C::kStagesV); j < iv; ++j)
+        drain_bar(bar(C::kBarVFull + j % C::kStagesV), (j / C::kStagesV) & 1);
+      if constexpr (FP8) {
+        for (int j = max(0, ir - C::kStagesR); j < ir; ++j)
+          drain_bar(bar(C::kBarRFull + j % C::kStagesR), (j / C::kStagesR) & 1);
+      } else {
+        if (landed > 0) drain_bar(bar(C::kBarLand), (landed - 1) & 1);
+      }
+      for (int j = max(0, qn - C::kStagesQ); j < qn; ++j)
+        drain_bar(bar((FP8 ? C::kBarLand : C::kBarQFull) + j % C::kStagesQ), (j / C::kStagesQ) & 1);
+    } else if (warp == 13) {
+      // =================== MMA issuer (one thread) ===================
+      // For every pair: S of the next pair (of the next piece at a piece's end),
+      // as soon as both softmax warpgroups hold this pair's S in registers, then
+      // this pair's P V.
+      if (lane == 0) {
+        constexpr uint32_t kIdescS = FP8 ? idesc_f16_f32(kTileM, 2 * kTileN, false)
+                                         : idesc_bf16_f32(kTileM, 2 * kTileN, false, false);
+        constexpr uint32_t kIdescS1 = FP8 ? idesc_f16_f32(kTileM, kTileN, false)
+                                          : idesc_bf16_f32(kTileM, kTileN, false, false);   // a block alone
+        constexpr uint32_t kIdescPV = FP8 ? idesc_f16_f32(kTileM, D, true) : idesc_bf16_f32(kTileM, D, false, true);
+        int ik = 0, iv = 0;     // K stages and V tiles consumed
+        int qn = 0;             // Q tiles consumed
+        int sn = 0;             // S tiles issued
+        int pn = 0;             // P tiles consumed
+        int on = 0;             // O results handed to the output warps
+        int np = 0;             // pieces read
+        // S of pair k of a piece with nb blocks
+        auto issue_s = [&](int k, int nb) -> bool {
+          if (k == 0) {
+            if (!wait_bar(bar(C::kBarQFull + qn % C::kStagesQ), (qn / C::kStagesQ) & 1, abort_flag, p.err))
+              return false;
+            ++qn;
+          }
+          if (sn > 0 && !wait_bar(bar(C::kBarSFree), (sn - 1) & 1, abort_flag, p.err)) return false;
+          const int qs = (qn - 1) % C::kStagesQ;
+          const uint64_t dq = sdesc_sw128(sbase + C::kQOff + qs * C::kTileBytes, 16, 1024);
+          if constexpr (FP8) {
+            for (int t = 0; t < 2 && 2 * k + t < nb; ++t) {
+              const int s = ik % C::kStagesK;
+              if (!wait_bar(bar(C::kBarKFull + s), (ik / C::kStagesK) & 1, abort_flag, p.err)) return false;
+              tc_fence_after();
+              const uint64_t dk = sdesc_sw128(sbase + C::kKOff + s * C::kKBytes, 16, 1024);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+                mma_ss(tmem + C::kColS + t * kTileN, sdesc_add(dq, off), sdesc_add(dk, off), kIdescS1, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(bar(C::kBarKEmpty + s));
+              ++ik;
+            }
+          } else {
+            const int s = ik % C::kStagesK;
+            if (!wait_bar(bar(C::kBarKFull + s), (ik / C::kStagesK) & 1, abort_flag, p.err)) return false;
+            tc_fence_after();
+            const uint64_t dk = sdesc_sw128(sbase + C::kKOff + s * C::kKBytes, 16, 1024);
+            const uint32_t idesc = 2 * k + 1 < nb ? kIdescS : kIdescS1;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t qoff = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
+              const uint32_t koff = (kk >> 2) * 2 * C::kChunkBytes + (kk & 3) * 32;
+              mma_ss(tmem + C::kColS, sdesc_add(dq, qoff), sdesc_add(dk, koff), idesc, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(C::kBarKEmpty + s));
+            ++ik;
+          }
+          mma_commit(bar(C::kBarSFull));
+          if (2 * k + 2 >= nb) mma_commit(bar(C::kBarQEmpty + qs));   // Q's buffer is free for a later piece
+          ++sn;
+          return true;
+        };
+        // P V block by block: block X's MMAs go as soon as warpgroup X has
+        // written its P, and their completion frees that block's P columns
+        auto issue_pv = [&](int k, int nb) -> bool {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!wait_bar(bar(C::kBarPFull + t), pn & 1, abort_flag, p.err)) return false;
+            tc_fence_after();
+            if (t == 0 && k == 0 && on > 0) {
+              // O still holds the previous piece's result until the output warps read it
+              if (!wait_bar(bar(C::kBarOEmpty), (on - 1) & 1, abort_flag, p.err)) return false;
+              tc_fence_after();
+            }
+            if (2 * k + t < nb) {
+              const int s = iv % C::kStagesV;
+              if (!wait_bar(bar(C::kBarVFull + s), (iv / C::kStagesV) & 1, abort_flag, p.err)) return false;
+              tc_fence_after();
+              const uint64_t dv = sdesc_sw128(sbase + C::kVOff + s * C::kTileBytes, C::kChunkBytes, 1024);
+#pragma unroll
+              for (int kk = 0; kk < kTileN / 16; ++kk)
+                mma_ts(tmem + C::kColO, tmem + C::kColP + (t * 8 + kk) * 8, sdesc_add(dv, kk * 16 * 128),
+                       kIdescPV, (k > 0 || t > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(bar(C::kBarVEmpty + s));
+              ++iv;
+            }
+            mma_commit(bar(C::kBarPvDone + t));
+          }
+          ++pn;
+          return true;
+        };
+        // blocks of the next piece (0: none is left)
+        auto next_blocks = [&](int& nb) -> bool {
+          if (!wait_bar(bar(C::kBarPieceFull + (np & 1)), (np >> 1) & 1, abort_flag, p.err)) return false;
+          const volatile Piece* x = piece_slot(np);
+          nb = x->kb.nsb + x->kb.nwb;
+          mbar_arrive(bar(C::kBarPieceEmpty + (np & 1)));
+          ++np;
+          return true;
+        };
+        int nb = 0;
+        bool ok = next_blocks(nb) && (nb == 0 || issue_s(0, nb));
+        while (ok && nb > 0) {
+          int nb2 = 0;
+          const int ns = (nb + 1) / 2;
+          for (int k = 0; k < ns && ok; ++k) {
+            if (k + 1 < ns) ok = issue_s(k + 1, nb);
+            else ok = next_blocks(nb2) && (nb2 == 0 || issue_s(0, nb2));
+            if (ok) ok = issue_pv(k, nb);
+          }
+          if (!ok) break;
+          mma_commit(bar(C::kBarOFull));
+          ++on;
+          nb = nb2;
+        }
+        // every MMA issued has completed before tensor memory is released
+        mma_commit(bar(C::kBarMmaDone));
+        drain_bar(bar(C::kBarMmaDone), 0);
+      }
+    }
+  } else if (warp < 4) {
+    regs_set<kChunkOut, kChunkLaunchRegs>();
+    // =================== output (and e4m3's conversion): thread = row ===================
+    const int row = warp * 32 + lane;
+    const int tok = row / p.G, head = row - tok * p.G;
+    const uint32_t tO = tmem + (static_cast<uint32_t>(warp * 32) << 16) + C::kColO;
+    const volatile float* inv_s = reinterpret_cast<const volatile float*>(smem + C::kInvOff);
+    int on = 0;             // O results read
+    int np = 0;             // pieces read
+    auto wait = [&](int b, uint32_t parity) -> bool {
+      return __all_sync(0xFFFFFFFFu, wait_bar_relaxed(bar(b), parity, abort_flag, p.err));
+    };
+    auto next_piece = [&](Piece& x) -> bool {
+      if (!wait(C::kBarPieceFull + (np & 1), (np >> 1) & 1)) return false;
+      read_piece(np, x);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kBarPieceEmpty + (np & 1)));
+      ++np;
+      return x.kb.count() > 0;
+    };
+    // the piece's O: scaled and rounded, or as it is to its part
+    auto output = [&](const Piece& x) -> bool {
+      if (!wait(C::kBarLFull, on & 1)) return false;
+      const float inv = inv_s[row];
+      if (!wait(C::kBarOFull, on & 1)) return false;
+      tc_fence_after();
+      const bool inb = tok < x.ntok;
+      const size_t at = static_cast<size_t>(x.t0 + tok) * p.H + x.hkv * p.G + head;
+      uint4* dst = reinterpret_cast<uint4*>(p.o + at * D);
+      float4* part = reinterpret_cast<float4*>(p.part + static_cast<size_t>(max(x.slot, 0)) * C::kPartFloats) + row;
+      // 16 columns at a time (the warpgroup has few registers); a row without a
+      // key (inv = 0) is 0 whatever the masked keys held
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(tO + c * 16, o);
+        tmem_ld_wait16(o);
+        if (c == D / 16 - 1) {
+          tc_fence_before();
+          mbar_arrive(bar(C::kBarOEmpty));      // the next piece's P V may overwrite O
+        }
+        if (!inb) continue;
+        if (x.slot >= 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            part[(4 * c + e) * kTileM] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w[e] = inv == 0.f ? 0u : pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          dst[2 * c] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[2 * c + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      ++on;
+      return true;
+    };
+    if constexpr (!FP8) {
+      Piece x;
+      while (next_piece(x) && output(x)) {
+      }
+    } else {
+      int ir = 0, ik = 0, iv = 0, qn = 0;
+      // the next raw tile becomes fp16 tile `dst`, its row `row` by this thread
+      // (rows without a token become zeros), once that tile is free
+      auto convert = [&](uint32_t dst, int full, int empty, bool used, uint32_t parity) -> bool {
+        const int s = ir % C::kStagesR;
+        if (!wait(C::kBarRFull + s, (ir / C::kStagesR) & 1)) return false;
+        if (used && !wait(empty, parity)) return false;
+        const bool there = block_rows(raw_info[s]).has(row);
+        const uint32_t src = sbase + C::kROff + s * C::kRawBytes + row * D;
+        const uint32_t to = dst + row * 128;
+#pragma unroll 2
+        for (int u = 0; u < D / 16; ++u) {          // 16 elements
+          const int su = D == 128 ? u ^ (row & 7) : u ^ ((row >> 1) & 3);
+          const uint4 w = lds128(src + su * 16);
+          uint32_t f[8];
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = there ? e4m3x2_f16x2(in[e]) : 0u;
+            f[2 * e + 1] = there ? e4m3x2_f16x2(in[e] >> 16) : 0u;
+          }
+          const uint32_t at = to + (u >> 2) * C::kChunkBytes;
+          const int u2 = (2 * u) & 7;
+          sts128(at + ((u2 ^ (row & 7)) << 4), f[0], f[1], f[2], f[3]);
+          sts128(at + (((u2 + 1) ^ (row & 7)) << 4), f[4], f[5], f[6], f[7]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(full));
+        mbar_arrive(bar(C::kBarREmpty + s));
+        ++ir;
+        return true;
+      };
+      auto convert_k = [&](const Piece& x, int k) -> bool {
+        for (int t = 0; t < 2 && 2 * k + t < x.kb.count(); ++t) {
+          const int s = ik % C::kStagesK;
+          if (!convert(sbase + C::kKOff + s * C::kKBytes, C::kBarKFull + s, C::kBarKEmpty + s, ik >= C::kStagesK,
+                       ((ik / C::kStagesK) & 1) ^ 1))
+            return false;
+          ++ik;
+        }
+        return true;
+      };
+      auto convert_v = [&](const Piece& x, int k) -> bool {
+        for (int t = 0; t < 2 && 2 * k + t < x.kb.count(); ++t) {
+          const int s = iv % C::kStagesV;
+          if (!convert(sbase + C::kVOff + s * C::kTileBytes, C::kBarVFull + s, C::kBarVEmpty + s,
+                       iv >= C::kStagesV, ((iv / C::kStagesV) & 1) ^ 1))
+            return false;
+          ++iv;
+        }
+        return true;
+      };
+      // this thread's row of Q, in place: bf16 to fp16, by a power of two that
+      // puts its largest element in [128, 256)
+      auto convert_q = [&]() -> bool {
+        const int s = qn % C::kStagesQ;
+        if (!wait(C::kBarLand + s, (qn / C::kStagesQ) & 1)) return false;
+        // the softmax has read the previous piece's factors
+        if (qn > 0 && !wait(C::kBarPieceEmpty + ((qn - 1) & 1), ((qn - 1) >> 1) & 1)) return false;
+        const uint32_t at = sbase + C::kQOff + s * C::kTileBytes + row * 128;
+        float top = 0.f;
+#pragma unroll 2
+        for (int u = 0; u < D / 8; ++u) {
+          const uint4 w = lds128(at + (u >> 3) * C::kChunkBytes + (((u & 7) ^ (row & 7)) << 4));
+          top = fmax3(top, fabsf(bf16lo(w.x)), fabsf(bf16hi(w.x)));
+          top = fmax3(top, fabsf(bf16lo(w.y)), fabsf(bf16hi(w.y)));
+          top = fmax3(top, fabsf(bf16lo(w.z)), fabsf(bf16hi(w.z)));
+          top = fmax3(top, fabsf(bf16lo(w.w)), fabsf(bf16hi(w.w)));
+        }
+        // 2^(134 - e) for a top of exponent field e, kept a normal number (an
+        // infinity or NaN stays one, whatever it is multiplied by)
+        int field = max(1, min(253, 127 + 134 - static_cast<int>(__float_as_uint(top) >> 23)));
+        if (top == 0.f) field = 127;
+        const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+#pragma unroll 2
+        for (int u = 0; u < D / 8; ++u) {
+          const uint32_t a = at + (u >> 3) * C::kChunkBytes + (((u & 7) ^ (row & 7)) << 4);
+          const uint4 w = lds128(a);
+          sts128(a, pack_f16(bf16lo(w.x) * up, bf16hi(w.x) * up), pack_f16(bf16lo(w.y) * up, bf16hi(w.y) * up),
+                 pack_f16(bf16lo(w.z) * up, bf16hi(w.z) * up), pack_f16(bf16lo(w.w) * up, bf16hi(w.w) * up));
+        }
+        *reinterpret_cast<volatile uint8_t*>(smem + C::kUpOff + row) = static_cast<uint8_t>(field);
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::kBarQFull + s));
+        ++qn;
+        return true;
+      };
+      // in the producer's order: V of a pair after K of the next one, which at a
+      // piece's end is the next piece's first, with its Q
+      Piece x, y;
+      bool more = next_piece(x);
+      bool ok = !more || (convert_k(x, 0) && convert_q());
+      while (ok && more) {
+        const int ns = (x.kb.count() + 1) / 2;
+        for (int k = 0; k < ns && ok; ++k) {
+          if (k + 1 < ns) {
+            ok = convert_k(x, k + 1);
+          } else {
+            more = next_piece(y);
+            ok = !more || (convert_k(y, 0) && convert_q());
+          }
+          ok = ok && convert_v(x, k);
+        }
+        ok = ok && output(x);
+        x = y;
+      }
+    }
+  } else {
+    regs_set<kChunkSoft, kChunkLaunchRegs>();
+    // =================== softmax warpgroups: X = 0 (warps 4-7), 1 (warps 8-11) ===================
+    const int X = (warp - 4) >> 2;                // key block X of every pair
+    const int wq = warp & 3;                      // TMEM lane quarter of this warp
+    const int row_in_tile = wq * 32 + lane;
+    const int tok = row_in_tile / p.G;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_base + C::kColS + X * 128;
+    const uint32_t tP = tmem + lane_base + C::kColP + X * 64;
+    const uint32_t tO = tmem + lane_base + C::kColO + X * (D / 2);
+    float* xch = reinterpret_cast<float*>(smem + C::kXchOff);
+    float* inv_s = reinterpret_cast<float*>(smem + C::kInvOff);
+
+    int cnt = 0;        // S tiles consumed (over all pieces)
+    int nx = 0;         // row values exchanged
+    int on = 0;         // pieces finished
+    bool ok = true;
+    // hand this row's value to the other warpgroup and take its value back
+    auto exchange = [&](float v, float& other) -> bool {
+      float* xb = xch + (nx & 1) * 2 * kTileM;
+      xb[X * kTileM + row_in_tile] = v;
+      mbar_arrive(bar(C::kBarXch + (nx & 1)));
+      const bool w = __all_sync(0xFFFFFFFFu,
+                                wait_bar(bar(C::kBarXch + (nx & 1)), (nx >> 1) & 1, abort_flag, p.err));
+      other = xb[(1 - X) * kTileM + row_in_tile];
+      ++nx;
+      return w;
+    };
+    for (int np = 0;; ++np) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarPieceFull + (np & 1)), (np >> 1) & 1, abort_flag, p.err)))
+        break;
+      Piece x;
+      read_piece(np, x);
+      const int nb = x.kb.count();
+      // (e4m3: given back with the first S, when Q's factors have been read, too)
+      if (!FP8 || nb == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarPieceEmpty + (np & 1)));
+      }
+      if (nb == 0) break;                         // the end
+      const int ns = (nb + 1) / 2;
+      const int own = x.p0 + tok;                 // this row's own key, and the first its window holds
+      const int low = own - p.window + 1;
+      const int low_last = x.p0 + x.ntok - p.window;
+      float sl2 = p.scale_log2;
+      if constexpr (FP8) sl2 *= __ldg(p.k_scale + x.hkv);
+      float m2 = NEG_INF;     // reference max (log2 units), moved only by > 8
+      float l = 0.f;          // this warpgroup's part of the row sum
+      for (int k = 0; k < ns; ++k) {
+        const bool none = 2 * k + X >= nb;        // the pair's second block is missing
+        const int kstart = none ? 0 : x.kb.at(2 * k + X) * kTileN;
+        if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarSFull), cnt & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+        if constexpr (FP8) {
+          if (k == 0) {                           // Q's factor, written before this S was
+            const uint32_t f = *reinterpret_cast<volatile uint8_t*>(smem + C::kUpOff + row_in_tile);
+            sl2 *= __uint_as_float((254u - f) << 23);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kBarPieceEmpty + (np & 1)));
+          }
+        }
+        const uint32_t valid = (valid_ring[cnt % C::kRing] >> (8 * X)) & 255u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
+        // S is in registers: the next pair's S may overwrite its columns
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarSFree));
+
+        // element mask, 32 columns at a time: a bit for each allowed key of this
+        // row (j <= own, which is before the last key; j >= low: window; j < sinks;
+        // and the key has a page)
+        const bool edge = none || valid != 255u || kTileN - 1 > x.p0 - kstart ||
+                          (low_last - kstart > 0 && kstart + kTileN > p.sinks);
+        if (edge) {
+          const int jhi = none ? -1 : own - kstart;
+          const int jlo = low - kstart;
+          const int js = p.sinks - kstart;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t bits = bits_below(jhi + 1 - 32 * c) & (~bits_below(jlo - 32 * c) | bits_below(js - 32 * c));
+            bits &= (valid >> (2 * c) & 1u ? 0x0000FFFFu : 0u) | (valid >> (2 * c) & 2u ? 0xFFFF0000u : 0u);
+            if (!__all_sync(0xFFFFFFFFu, bits == 0xFFFFFFFFu)) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((bits >> j) & 1u)) s[c][j] = __float_as_uint(NEG_INF);
+            }
+          }
+        }
+        // row max of this block over 8 chains of three-input max
+        float mx[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mx[u] = __uint_as_float(s[0][u]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = (c == 0 ? 8 : 0); j < 32; j += 16)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (j + 8 + u < 32)
+                mx[u] = fmax3(mx[u], __uint_as_float(s[c][j + u]), __uint_as_float(s[c][j + 8 + u]));
+              else
+                mx[u] = fmaxf(mx[u], __uint_as_float(s[c][j + u]));
+        const float mmine = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
+        // the pair's row max: both warpgroups take the same decisions below
+        float mothr;
+        if (!exchange(mmine, mothr)) {
+          ok = false;
+          break;
+        }
+        const float mblk = fmaxf(mmine, mothr);
+        float alpha = 1.f;
+        bool moved = false;
+        if (mblk > m2 + 8.f) {
+          alpha = ex2(m2 - mblk);
+          m2 = mblk;
+          moved = true;
+        }
+        const float mu = ((m2 == NEG_INF) ? 0.f : m2) - (FP8 ? kP2 : 0.f);
+        // Where the reference max moved, this warpgroup's half of O is
+        // rescaled: after the previous pair's whole P V (both blocks write
+        // all of O).  Warpgroup 1 does it first and then releases block 0's
+        // P V; warpgroup 0 after writing its P, before releasing it.
+        const bool fix = moved && k > 0;
+        const bool any_fix = __any_sync(0xFFFFFFFFu, fix);
+        auto rescale_o = [&]() -> bool {
+          if (!__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarPvDone + 1), (cnt - 1) & 1, abort_flag, p.err)))
+            return false;
+          tc_fence_after();
+          const float a = fix ? alpha : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+            tmem_st32(tO + c * 32, o);
+          }
+          return true;
+        };
+        if (X == 1) {
+          if (any_fix && !rescale_o()) {
+            ok = false;
+            break;
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar(C::kBarPFull + 0));
+        }
+        // P block X is written below: the previous pair's P V of block X
+        // (which reads it) must have completed
+        if (cnt > 0 &&
+            !__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarPvDone + X), (cnt - 1) & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float rs[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) rs[u] = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            const int c = half * 2 + c2;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float x0, x1;
+              ffma2(x0, x1, __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]), sl2, sl2, -mu,
+                    -mu);
+              const float p0 = ex2(x0);
+              const float p1 = ex2(x1);
+              const int u = (j >> 1) & 3;
+              fadd2(rs[2 * u], rs[2 * u + 1], rs[2 * u], rs[2 * u + 1], p0, p1);
+              pk[c2 * 16 + j / 2] = FP8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+            }
+          }
+          tmem_st32(tP + half * 32, pk);
+        }
+        l = l * alpha + (((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7])));
+        if (X == 0 && any_fix && !rescale_o()) {
+          ok = false;
+          break;
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarPFull + X));
+        ++cnt;
+      }
+      if (!ok) break;
+
+      // ---- the row sum is the two warpgroups' parts; warpgroup 0 hands its
+      // inverse to the output warps, which must have read the previous piece's
+      float lo;
+      if (!exchange(l, lo)) break;
+      if (X == 0) {
+        if (on > 0 &&
+            !__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarOEmpty), (on - 1) & 1, abort_flag, p.err)))
+          break;
+        // a row that saw no key has l = 0; a NaN score makes l NaN and goes through
+        const float lt = l + lo;
+        const float m = FP8 ? m2 - kP2 : m2;      // the max that goes with l
+        float vs = 1.f;
+        if constexpr (FP8) vs = __ldg(p.v_scale + x.hkv);
+        inv_s[row_in_tile] = lt == 0.f ? 0.f : vs / lt;
+        mbar_arrive(bar(C::kBarLFull));
+        if (tok < x.ntok) {
+          if (x.slot >= 0) {
+            float* part = p.part + static_cast<size_t>(x.slot) * C::kPartFloats + kTileM * D + row_in_tile;
+            part[0] = m;
+            part[kTileM] = lt;
+          } else {
+            p.lse[static_cast<size_t>(x.t0 + tok) * p.H + x.hkv * p.G + row_in_tile - tok * p.G] =
+                lt == 0.f ? NEG_INF : (m + __log2f(lt)) * kLn2;
+          }
+        }
+      }
+      ++on;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// the join: a CTA a (tile, K/V head) and 32 columns, a thread a row and 16 of them
+// ----------------------------------------------------------------------------
+constexpr int kJoinThreads = 2 * kTileM;
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkParams p) {
+  constexpr int kPart = kTileM * (D + 2);
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int row = static_cast<int>(threadIdx.x) & (kTileM - 1);
+  const int col = static_cast<int>(blockIdx.y) * 32 + static_cast<int>(threadIdx.x >> 7) * 16;
+  const int tok = row / p.G;
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // the parts are complete
+  const int joins = p.plan->joins;
+  for (int j = static_cast<int>(blockIdx.x); j < joins; j += static_cast<int>(gridDim.x)) {
+    const int s = find_seq(p.S, j, lane, [&](int i) { return p.seq[i].join0; });
+    const ChunkSeq q = p.seq[s];
+    const SeqRows r = seq_rows(p, s);
+    const int cuts = p.cuts[s], nt = (r.b - r.a + p.tpt - 1) / p.tpt;
+    const int in = j - q.join0;
+    const int hkv = in / nt, i = in % nt;                 // the tile's number among its pieces'
+    const Tile t = seq_tile(r, nt - 1 - i, p.tpt);
+    if (tok >= t.ntok) continue;
+    const float* part = p.part + static_cast<size_t>(q.slot0 + hkv * cuts * nt + i) * kPart;
+    const size_t step = static_cast<size_t>(nt) * kPart;  // from part to part
+    float m = NEG_INF, l = 0.f, y[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = 0.f;
+    for (int c = 0; c < cuts; ++c) {
+      const float lc = part[c * step + kTileM * (D + 1) + row];
+      if (lc != 0.f) m = fmaxf(m, part[c * step + kTileM * D + row]);
+    }
+    for (int c = 0; c < cuts; ++c) {
+      const float lc = part[c * step + kTileM * (D + 1) + row];
+      if (lc == 0.f) continue;                            // this part saw no key
+      const float w = ex2(part[c * step + kTileM * D + row] - m);
+      l = fmaf(w, lc, l);
+      const float4* a = reinterpret_cast<const float4*>(part + c * step) + col / 4 * kTileM + row;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 v = a[e * kTileM];
+        y[4 * e] = fmaf(w, v.x, y[4 * e]);
+        y[4 * e + 1] = fmaf(w, v.y, y[4 * e + 1]);
+        y[4 * e + 2] = fmaf(w, v.z, y[4 * e + 2]);
+        y[4 * e + 3] = fmaf(w, v.w, y[4 * e + 3]);
+      }
+    }
+    float inv = l == 0.f ? 0.f : 1.f / l;
+    if constexpr (FP8) inv *= __ldg(p.v_scale + hkv);
+    const size_t at = static_cast<size_t>(t.t0 + tok) * p.H + hkv * p.G + row - tok * p.G;
+    uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + col);
+    dst[0] = make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
+                        pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
+    dst[1] = make_uint4(pack_bf16(y[8] * inv, y[9] * inv), pack_bf16(y[10] * inv, y[11] * inv),
+                        pack_bf16(y[12] * inv, y[13] * inv), pack_bf16(y[14] * inv, y[15] * inv));
+    if (col == 0) p.lse[at] = l == 0.f ? NEG_INF : (m + __log2f(l)) * kLn2;
+  }
+}
+
+// ----------------------------------------------------------------------------
+// host
+// ----------------------------------------------------------------------------
 bool chunk_sizes(int T, int S, int H, int Hkv, int d, int max_pages, int page) {
   if (T < 1 || S < 1 || S > kMaxSeqs || max_pages < 1) return false;
   if (page < 16 || page > 1024 || (page & (page - 1))) return false;
-  return valid_kv_heads(H, Hkv) && H / Hkv <= 128 && (d == 64 || d == 128) && static_cast<long long>(T) * H <= 0x7FFFFFFFll;
+  return valid_kv_heads(H, Hkv) && H / Hkv <= kMaxGroup && (d == 64 || d == 128) && static_cast<long long>(T) * H <= 0x7FFFFFFFll;
 }
 
-size_t chunk_workspace(int, int, int, int, int, int, int) { return 16; }
+// Tiles of all sequences at most, of one K/V head.
+long long most_tiles(int T, int S, int G) {
+  const int tpt = kTileM / G;
+  return std::min<long long>(T, (static_cast<long long>(T) + tpt - 1) / tpt + S);
+}
+// Parts that the plan may leave to be joined: none where no tile has enough keys
+// for two of them.
+int most_slots(int T, int S, int Hkv, int G, int M, int page) {
+  const long long keys = std::min<long long>(static_cast<long long>(M) * page, kMaxTokens);
+  const long long pairs = (keys + 2 * kTileN - 1) / (2 * kTileN) + 1;      // (a window and its sinks: one more)
+  if (pairs <= kLeastPairs) return 0;
+  const long long cuts = (pairs + kLeastPairs - 1) / kLeastPairs;
+  const long long tiles = most_tiles(T, S, G) * Hkv;
+  return static_cast<int>(tiles >= kMaxParts ? kMaxParts : std::min<long long>(kMaxParts, tiles * cuts));
+}
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+// plan | sequences | cuts | parts
+size_t chunk_workspace(int T, int S, int H, int Hkv, int d, int M, int page) {
+  return up256(sizeof(ChunkPlan)) + up256(static_cast<size_t>(S) * sizeof(ChunkSeq)) +
+         up256(static_cast<size_t>(S) * 4) +
+         static_cast<size_t>(most_slots(T, S, Hkv, H / Hkv, M, page)) * kTileM * (d + 2) * 4;
+}
+
+// K or V pages as a 3-D tensor (d, H_kv * page_size, pages) with boxes of up to 128
+// rows of a page and 128 bytes.
+attn_status_t pages_map(CUtensorMap* map, const void* ptr, int d, bool fp8, long long rows, int P,
+                        size_t page_bytes, int page) {
+  const int item = fp8 ? 1 : 2;
+  const int box = std::min(d * item, 128);
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows), static_cast<uint64_t>(P)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * item, page_bytes};
+  const uint32_t boxes[3] = {static_cast<uint32_t>(box / item), static_cast<uint32_t>(std::min(page, kTileN)), 1};
+  return make_map_tiled(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr,
+                        dims, strides, boxes, box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// The kernels' attributes, set once a device; its multiprocessors.
+template <int D, bool FP8>
+cudaError_t chunk_device(int* sms) {
+  constexpr int kMaxDev = 64;
+  static int known[kMaxDev] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (known[dev] == 0) {
+    const void* k = reinterpret_cast<const void*>(attn_fwd_paged_kernel<D, FP8>);
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
+    if (fa.numRegs < static_cast<int>(kChunkLaunchRegs)) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<D, FP8>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&known[dev], cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  }
+  *sms = known[dev];
+  return cudaSuccess;
+}
+
+template <int D, bool FP8>
+cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, ChunkParams& p,
+                         cudaStream_t st) {
+  int sms = 0;
+  cudaError_t e = chunk_device<D, FP8>(&sms);
+  if (e != cudaSuccess) return e;
+  p.ctas = sms;
+  chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // the next kernels are set up while the ones before them run; they wait for
+  // their ends themselves
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  const long long pieces = std::max<long long>(most_tiles(p.T, p.S, p.G) * p.Hkv, p.slots);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(sms, pieces)));
+  cfg.blockDim = dim3(ChunkCfg<D, FP8>::kThreads);
+  cfg.dynamicSmemBytes = ChunkCfg<D, FP8>::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, attn_fwd_paged_kernel<D, FP8>, tq, tk, tv, p)) != cudaSuccess) return e;
+  if (p.slots == 0) return cudaSuccess;
+  cfg.gridDim = dim3(std::min(p.slots, 2 * sms), D / 32);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, FP8>, p);
+}
 
 }  // namespace
 }  // namespace bss
@@ -178,12 +1548,6 @@ extern "C" attn_status_t attn_fwd_paged(
   if (workspace_bytes < chunk_workspace(T, S, H, H_kv, d, max_pages, page_size)) return ATTN_ERR_WORKSPACE;
   ChunkParams p{};
   if ((s = status_word(&p.err)) != ATTN_OK) return s;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.q_stride = q_stride;
-  p.k = static_cast<const uint8_t*>(k_cache);
-  p.v = static_cast<const uint8_t*>(v_cache);
-  p.k_stride = static_cast<size_t>(k_page_stride) * (fp8 ? 1 : 2);
-  p.v_stride = static_cast<size_t>(v_page_stride) * (fp8 ? 1 : 2);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.table = page_table;
@@ -199,17 +1563,41 @@ extern "C" attn_status_t attn_fwd_paged(
   p.M = max_pages;
   p.P = n_pages;
   while ((1 << p.page_log2) < page_size) ++p.page_log2;
+  p.tpt = kTileM / p.G;
+  p.slots = most_slots(T, S, H_kv, p.G, max_pages, page_size);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.plan = reinterpret_cast<ChunkPlan*>(ws);
+  ws += up256(sizeof(ChunkPlan));
+  p.seq = reinterpret_cast<ChunkSeq*>(ws);
+  ws += up256(static_cast<size_t>(S) * sizeof(ChunkSeq));
+  p.cuts = reinterpret_cast<int*>(ws);
+  ws += up256(static_cast<size_t>(S) * 4);
+  p.part = reinterpret_cast<float*>(ws);
   p.scale_log2 = scale * kLog2e;
-  p.window = std::min<int64_t>(window, int64_t(1) << 60);
-  p.sinks = static_cast<int>(std::min<int64_t>(sinks, 0x7FFFFFF0));
+  // no position reaches kMaxTokens
+  p.window = window == 0 ? kMaxTokens : static_cast<int>(std::min<int64_t>(window, kMaxTokens));
+  p.sinks = static_cast<int>(std::min<int64_t>(sinks, kMaxTokens));
+  if ((s = get_encoder()) != ATTN_OK) return s;
+  const long long rows = static_cast<long long>(H_kv) * page_size;
+  if (rows > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;     // a copy's row is an int
+  CUtensorMap tq, tk, tv;
+  // Q as (d, H, T), a box the query heads of a K/V head of a tile's tokens
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(H), static_cast<uint64_t>(T)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(q_stride) * 2};
+  const uint32_t boxes[3] = {64, static_cast<uint32_t>(p.G), static_cast<uint32_t>(p.tpt)};
+  if ((s = make_map_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, boxes,
+                          CU_TENSOR_MAP_SWIZZLE_128B)) != ATTN_OK)
+    return s;
+  const size_t item = fp8 ? 1 : 2;
+  if ((s = pages_map(&tk, k_cache, d, fp8, rows, n_pages, static_cast<size_t>(k_page_stride) * item, page_size)) !=
+      ATTN_OK)
+    return s;
+  if ((s = pages_map(&tv, v_cache, d, fp8, rows, n_pages, static_cast<size_t>(v_page_stride) * item, page_size)) !=
+      ATTN_OK)
+    return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(T) * H + 3) / 4);
-  if (d == 64) {
-    if (fp8) attn_fwd_paged_kernel<64, true><<<grid, 128, 0, st>>>(p);
-    else attn_fwd_paged_kernel<64, false><<<grid, 128, 0, st>>>(p);
-  } else {
-    if (fp8) attn_fwd_paged_kernel<128, true><<<grid, 128, 0, st>>>(p);
-    else attn_fwd_paged_kernel<128, false><<<grid, 128, 0, st>>>(p);
-  }
-  return cuda_status("attn_fwd_paged launch", cudaGetLastError());
+  cudaError_t e;
+  if (d == 64) e = fp8 ? launch_chunk<64, true>(tq, tk, tv, p, st) : launch_chunk<64, false>(tq, tk, tv, p, st);
+  else e = fp8 ? launch_chunk<128, true>(tq, tk, tv, p, st) : launch_chunk<128, false>(tq, tk, tv, p, st);
+  return cuda_status("attn_fwd_paged launch", e);
 }

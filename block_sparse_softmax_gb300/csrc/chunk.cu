@@ -53,10 +53,14 @@ struct ChunkPlan {
   int pieces1, pieces;       // of the long kind, in all
   int next;                  // pieces taken, past each CTA's first
   int joins;                 // (tile, K/V head)s that are joined
-  int pad[4];
 };
-struct ChunkSeq {            // of a sequence: pieces of either kind, slots and joins before it,
+// Of a sequence: pieces of either kind, slots and joins before it; its rows
+// (SeqRows); the parts that its tiles' keys are cut into; its work (SeqWork).
+struct __align__(16) ChunkSeq {
   int before1, before2, slot0, join0;
+  int a, b, n, cuts;
+  long long shift;
+  int nt, longest;
 };
 
 struct ChunkParams {
@@ -68,8 +72,8 @@ struct ChunkParams {
   __nv_bfloat16* o;
   float* lse;
   ChunkPlan* plan;
+  int* first;                // [ctas] the sequence of each CTA's first piece
   ChunkSeq* seq;             // [S]
-  int* cuts;                 // [S] parts of a tile's keys
   float* part;               // [slots]: A as [d / 4][128 rows][4], m (log2 units) [128], l [128]
   int slots;
   int T, S, H, Hkv, G, tpt, M, P;     // tpt: tokens of a tile
@@ -116,10 +120,12 @@ __device__ __forceinline__ WindowBlocks tile_blocks(const ChunkParams& p, const 
 }
 
 // ----------------------------------------------------------------------------
-// the plan: one CTA
+// the plan: one CTA, which the main kernel waits for: what counts is the chain of
+// its steps (4 us with one instruction stream for all lengths of parts, 13 with
+// every thread weighing all of them)
 // ----------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCuts = 10;              // lengths of parts that are weighed
+constexpr int kPlanCuts = 16;              // lengths of parts that are weighed
 struct SeqWork {
   int nt, longest;           // tiles; pairs of key blocks of its longest tile
   float mean;                // ... of a tile
@@ -127,23 +133,25 @@ struct SeqWork {
 __device__ __forceinline__ SeqWork seq_work(const ChunkParams& p, const SeqRows& r) {
   SeqWork w{(r.b - r.a + p.tpt - 1) / p.tpt, 0, 0.f};
   if (w.nt == 0) return w;
-  const int first = (tile_blocks(p, seq_tile(r, 0, p.tpt), r.n).count() + 1) / 2;
   const int last = (tile_blocks(p, seq_tile(r, w.nt - 1, p.tpt), r.n).count() + 1) / 2;
+  int first = last;
+  if (w.nt > 1) first = (tile_blocks(p, seq_tile(r, 0, p.tpt), r.n).count() + 1) / 2;
   w.longest = max(first, last);
   w.mean = 0.5f * static_cast<float>(first + last);
   return w;
 }
 // Parts of the tiles of a sequence, where a part has about `len` pairs at most.
-__device__ __forceinline__ int seq_cuts(const SeqWork& w, int len) {
-  return w.longest <= len ? 1 : (w.longest + len - 1) / len;
+__device__ __forceinline__ int seq_cuts(int longest, int len) {
+  return longest <= len ? 1 : (longest + len - 1) / len;
 }
 // ... whether those are long pieces, which go first.
-__device__ __forceinline__ bool long_pieces(const SeqWork& w, int cuts, int len) {
-  return 2ll * w.longest > static_cast<long long>(len) * cuts;
+__device__ __forceinline__ bool long_pieces(int longest, int cuts, int len) {
+  return 2ll * longest > static_cast<long long>(len) * cuts;
 }
 
-// Exclusive prefix sums of four numbers a thread over the block; *total gets the sums.
-__device__ __forceinline__ int4 plan_scan(int4 v, int4* warp_sums, int4* total) {
+// Exclusive prefix sums of four numbers a thread over the block's first `warps`
+// warps; *total gets the sums.
+__device__ __forceinline__ int4 plan_scan(int4 v, int4* warp_sums, int warps, int4* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int4 x = v;
 #pragma unroll
@@ -156,7 +164,7 @@ __device__ __forceinline__ int4 plan_scan(int4 v, int4* warp_sums, int4* total) 
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   int4 before = make_int4(x.x - v.x, x.y - v.y, x.z - v.z, x.w - v.w), sum = make_int4(0, 0, 0, 0);
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < warps; ++w) {
     const int4 y = warp_sums[w];
     if (w < warp) before = make_int4(before.x + y.x, before.y + y.y, before.z + y.z, before.w + y.w);
     sum = make_int4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
@@ -166,121 +174,142 @@ __device__ __forceinline__ int4 plan_scan(int4 v, int4* warp_sums, int4* total) 
 }
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p) {
-  __shared__ float sums[kPlanThreads / 32][4 * kPlanCuts];
-  __shared__ float all[4 * kPlanCuts];
+  __shared__ float4 sums[kPlanThreads / 32][kPlanCuts];
+  __shared__ float2 tops[kPlanThreads / 32];
   __shared__ int4 scan[kPlanThreads / 32];
+  __shared__ SeqWork works[kPlanThreads];
+  __shared__ int chosen;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int warps = min(kPlanThreads / 32, (p.S + 31) / 32);         // with a sequence of their own
-  SeqWork mine{0, 0, 0.f};
-  if (tid < p.S) {
-    const SeqRows r = seq_rows(p, tid);
-    mine = seq_work(p, r);
+  const bool few = p.S <= kPlanThreads;                              // `works` holds them all
+
+  // ---- the sequences' rows and work; all pairs, and the longest tile's ----
+  float2 top = make_float2(0.f, 0.f);
+  for (int s = tid; s < p.S; s += kPlanThreads) {
+    const SeqRows r = seq_rows(p, s);
+    const SeqWork w = seq_work(p, r);
     if (r.bad) record_error(p.err, ATTN_ERR_BAD_PAGES);
+    ChunkSeq* q = p.seq + s;
+    q->a = r.a;
+    q->b = r.b;
+    q->n = r.n;
+    q->shift = r.shift;
+    q->nt = w.nt;
+    q->longest = w.longest;
+    if (few) works[s] = w;
+    top.x = fmaxf(top.x, static_cast<float>(w.longest));
+    top.y += w.mean * static_cast<float>(w.nt);
   }
-  auto work = [&](int s) { return s == tid ? mine : seq_work(p, seq_rows(p, s)); };
-  auto reduce = [&](float (&v)[4 * kPlanCuts], int n) {               // sums (the first: a maximum) to `all`
 #pragma unroll
-    for (int i = 0; i < 4 * kPlanCuts; ++i) {
-      if (i >= n) break;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float y = __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-        v[i] = n == 2 && i == 0 ? fmaxf(v[i], y) : v[i] + y;
-      }
-      if (lane == 0) sums[warp][i] = v[i];
-    }
-    __syncthreads();
-    if (tid < n) {
-      float x = 0.f;
-      for (int w = 0; w < warps; ++w) x = n == 2 && tid == 0 ? fmaxf(x, sums[w][tid]) : x + sums[w][tid];
-      all[tid] = x;
-    }
-    __syncthreads();
-  };
-  // all pairs, and the longest tile's
-  float v[4 * kPlanCuts];
-#pragma unroll
-  for (int i = 0; i < 4 * kPlanCuts; ++i) v[i] = 0.f;
-  for (int s = tid; s < p.S; s += kPlanThreads) {
-    const SeqWork w = work(s);
-    v[0] = fmaxf(v[0], static_cast<float>(w.longest));
-    v[1] += w.mean * static_cast<float>(w.nt);
+  for (int o = 16; o > 0; o >>= 1) {
+    top.x = fmaxf(top.x, __shfl_xor_sync(0xFFFFFFFFu, top.x, o));
+    top.y += __shfl_xor_sync(0xFFFFFFFFu, top.y, o);
   }
-  reduce(v, 2);
-  const int longest = static_cast<int>(all[0]);
-  const float per_cta = all[1] * static_cast<float>(p.Hkv) / static_cast<float>(p.ctas);
+  if (lane == 0) tops[warp] = top;
   __syncthreads();
-  // lengths of parts: a whole tile, and the fair share of a CTA cut into 1, 1.25, ...
-  auto length = [&](int i) {
-    const float turns[kPlanCuts - 1] = {1.f, 1.25f, 1.5f, 2.f, 2.5f, 3.f, 4.f, 5.f, 8.f};
-    float t = 1.f;
-#pragma unroll
-    for (int j = 0; j < kPlanCuts - 1; ++j)
-      if (i == j + 1) t = turns[j];
-    return i == 0 ? max(1, longest) : max(kLeastPairs, static_cast<int>(ceilf(per_cta / t)));
-  };
-  // long pieces (their number, their pairs with what a piece costs beside them), the
-  // others' pairs, slots
-#pragma unroll
-  for (int i = 0; i < 4 * kPlanCuts; ++i) v[i] = 0.f;
-  for (int s = tid; s < p.S; s += kPlanThreads) {
-    const SeqWork w = work(s);
+  top = tops[0];
+  for (int w = 1; w < warps; ++w) {
+    top.x = fmaxf(top.x, tops[w].x);
+    top.y += tops[w].y;
+  }
+  const int longest = static_cast<int>(top.x);
+  const float ctas = static_cast<float>(p.ctas);
+  const float share = top.y * static_cast<float>(p.Hkv) / ctas;      // a CTA's fair share of the pairs
+
+  // ---- what lengths of parts cost: a whole tile, and the share cut into 1, 1.17, ..., 12;
+  // a thread weighs one of them for every 64th sequence ----
+  const int cand = tid & (kPlanCuts - 1);
+  const float turns = cand <= 6 ? 1.f + static_cast<float>(cand - 1) / 6.f
+                                : exp2f(static_cast<float>(cand - 6) * 0.3f + 0.9f);
+  const int my_len = cand == 0 ? max(1, longest) : max(kLeastPairs, static_cast<int>(ceilf(share / turns)));
+  // long pieces, their pairs with what a piece costs beside them; the others' pairs; slots
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = tid / kPlanCuts; s < p.S; s += kPlanThreads / kPlanCuts) {
+    const SeqWork w = few ? works[s] : seq_work(p, seq_rows(p, s));
     const float tiles = static_cast<float>(w.nt) * static_cast<float>(p.Hkv);
-#pragma unroll
-    for (int i = 0; i < kPlanCuts; ++i) {
-      const int len = length(i);
-      const int cuts = seq_cuts(w, len);
-      // about a pair's time to begin and end a piece, as much again to leave a part
-      const float cost = tiles * (w.mean + static_cast<float>(cuts) * (cuts > 1 ? 2.f : 1.f));
-      if (long_pieces(w, cuts, len)) {
-        v[4 * i] += tiles * static_cast<float>(cuts);
-        v[4 * i + 1] += cost;
-      } else {
-        v[4 * i + 2] += cost;
-      }
-      if (cuts > 1) v[4 * i + 3] += tiles * static_cast<float>(cuts);
+    const int cuts = seq_cuts(w.longest, my_len);
+    // about a pair's time to begin and end a piece, as much again to leave a part
+    const float cost = tiles * (w.mean + static_cast<float>(cuts) * (cuts > 1 ? 2.f : 1.f));
+    if (long_pieces(w.longest, cuts, my_len)) {
+      v.x += tiles * static_cast<float>(cuts);
+      v.y += cost;
+    } else {
+      v.z += cost;
     }
+    if (cuts > 1) v.w += tiles * static_cast<float>(cuts);
   }
-  reduce(v, 4 * kPlanCuts);
-  int best = 0;
-  float least = 3.4e38f;
-#pragma unroll
-  for (int i = 0; i < kPlanCuts; ++i) {
-    const float n = all[4 * i], each = n > 0.f ? all[4 * i + 1] / n : 0.f;
-    const float ctas = static_cast<float>(p.ctas), turns = ceilf(n / ctas);
-    const float idle = (turns * ctas - n) * each;
+  v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, 16);
+  v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, 16);
+  v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, 16);
+  v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, 16);
+  if (lane < kPlanCuts) sums[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0) {
+    const int used = min(kPlanThreads / 32, (p.S + 1) / 2);
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < used; ++w) {
+      const float4 y = sums[w][cand];
+      v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+    }
+    const float each = v.x > 0.f ? v.y / v.x : 0.f, rounds = ceilf(v.x / ctas);
+    const float idle = (rounds * ctas - v.x) * each;
     // the long pieces' turns, what does not fit beside the last of them, and the join
-    const float t = turns * each + fmaxf(0.f, all[4 * i + 2] - idle) / ctas + (all[4 * i + 3] > 0.f ? 2.f : 0.f);
-    if (i > 0 && all[4 * i + 3] > static_cast<float>(p.slots)) continue;
-    if (t < least) {
-      least = t;
-      best = i;
+    float t = rounds * each + fmaxf(0.f, v.z - idle) / ctas + (v.w > 0.f ? 2.f : 0.f);
+    if (cand > 0 && v.w > static_cast<float>(p.slots)) t = 3.4e38f;
+    int best = cand;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      const float t2 = __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      const int b2 = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+      if (t2 < t || (t2 == t && b2 < best)) {
+        t = t2;
+        best = b2;
+      }
     }
+    const int len = __shfl_sync(0xFFFFFFFFu, my_len, best);
+    if (lane == 0) chosen = len;
   }
-  const int len = length(best);
+  __syncthreads();
+  const int len = chosen;
+
+  // ---- where each sequence's pieces, slots and joins begin ----
   int4 base = make_int4(0, 0, 0, 0);
   for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
     const int s = s0 + tid;
     int4 x = make_int4(0, 0, 0, 0);
     int cuts = 1;
+    bool first = false;
     if (s < p.S) {
-      const SeqWork w = work(s);
-      cuts = seq_cuts(w, len);
-      const int tiles = w.nt * p.Hkv;
-      (long_pieces(w, cuts, len) ? x.x : x.y) = tiles * cuts;
+      const int nt = few ? works[s].nt : p.seq[s].nt, most = few ? works[s].longest : p.seq[s].longest;
+      cuts = seq_cuts(most, len);
+      const int tiles = nt * p.Hkv;
+      first = long_pieces(most, cuts, len);
+      if (first) x.x = tiles * cuts;
+      else x.y = tiles * cuts;
       if (cuts > 1) {
         x.z = tiles * cuts;
         x.w = tiles;
       }
     }
     int4 total;
-    const int4 y = plan_scan(x, scan, &total);
+    const int4 y = plan_scan(x, scan, warps, &total);
     if (s < p.S) {
-      p.seq[s] = ChunkSeq{base.x + y.x, base.y + y.y, base.z + y.z, base.w + y.w};
-      p.cuts[s] = cuts;
+      ChunkSeq* q = p.seq + s;
+      *reinterpret_cast<int4*>(q) = make_int4(base.x + y.x, base.y + y.y, base.z + y.z, base.w + y.w);
+      q->cuts = cuts;
+      if (first)
+        for (int i = base.x + y.x; i < min(base.x + y.x + x.x, p.ctas); ++i) p.first[i] = s;
     }
     base = make_int4(base.x + total.x, base.y + total.y, base.z + total.z, base.w + total.w);
+  }
+  if (base.x < p.ctas && base.y > 0) {                      // CTAs that begin with another piece
+    for (int s = tid; s < p.S; s += kPlanThreads) {
+      const int b2 = p.seq[s].before2, nt = few ? works[s].nt : p.seq[s].nt;
+      const int cuts = p.seq[s].cuts;
+      if (long_pieces(few ? works[s].longest : p.seq[s].longest, cuts, len)) continue;
+      for (int i = base.x + b2; i < min(base.x + b2 + nt * p.Hkv * cuts, p.ctas); ++i) p.first[i] = s;
+    }
   }
   if (tid == 0) {
     p.plan->pieces1 = base.x;
@@ -309,15 +338,19 @@ __device__ __forceinline__ int find_seq(int S, int x, int lane, const Before& be
 // ----------------------------------------------------------------------------
 // What the roles need of a piece.
 struct Piece {
-  int t0, ntok, p0, n, hkv;
+  int t0, p0;                // its tile's first row and that one's position
+  int heads;                 // K/V head << 8 | tokens of the tile
   int slot;                  // -1: the whole tile's keys
   WindowBlocks kb;
+  __device__ __forceinline__ int ntok() const { return heads & 255; }
+  __device__ __forceinline__ int hkv() const { return heads >> 8; }
 };
+static_assert(sizeof(Piece) == 32, "two pieces fit beside the tiles");
 
-// ... and the producer: its sequence, the first key that some row of the sequence
-// has in its window.
+// ... and the producer: its sequence, that one's length, and the first key that
+// some row of the sequence has in its window.
 struct Work : Piece {
-  int s, low;
+  int s, n, low;
 };
 // Rows of a V block that some row of the sequence sees: [low, rows) and below
 // `sinks`, in the groups of 16 that have a page.  What the others hold (rows past
@@ -350,9 +383,9 @@ struct ChunkCfg {
   static constexpr int kStagesQ = D == 64 ? 2 : 1;
   // K: pairs of blocks, side by side for an N = 256 MMA; e4m3: single blocks
   static constexpr int kKBytes = FP8 ? kTileBytes : 2 * kTileBytes;
-  static constexpr int kStagesK = FP8 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
+  static constexpr int kStagesK = FP8 ? (D == 64 ? 4 : 2) : (D == 64 ? 3 : 2);
   static constexpr int kStagesV = D == 64 ? 4 : 2;
-  static constexpr int kStagesR = FP8 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int kStagesR = FP8 ? (D == 64 ? 6 : 4) : 0;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + kStagesQ * kTileBytes;
   static constexpr int kVOff = kKOff + kStagesK * kKBytes;
@@ -531,10 +564,8 @@ __global__ void __launch_bounds__(512, 1)
   auto read_piece = [&](int i, Piece& x) {
     const volatile Piece* src = piece_slot(i);
     x.t0 = src->t0;
-    x.ntok = src->ntok;
     x.p0 = src->p0;
-    x.n = src->n;
-    x.hkv = src->hkv;
+    x.heads = src->heads;
     x.slot = src->slot;
     x.kb.nsb = src->kb.nsb;
     x.kb.wb0 = src->kb.wb0;
@@ -566,39 +597,34 @@ __global__ void __launch_bounds__(512, 1)
         return __all_sync(0xFFFFFFFFu, wait_bar(bar(b), parity, abort_flag, p.err));
       };
 
-      // The next piece that has keys, from piece `index` on; pieces without are
-      // seen to here.  index moves on to the piece after it.
-      int index = static_cast<int>(blockIdx.x);
-      auto take = [&]() {
-        int x = 0;
-        if (lane == 0) x = atomicAdd(&p.plan->next, 1);
-        return static_cast<int>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, x, 0);
-      };
+      // The next piece that has keys; pieces without are seen to here.  The number
+      // of the one after it is asked for ahead of time (lane 0 has it).
+      int taken = static_cast<int>(blockIdx.x);
+      bool begun = false;
       auto next_piece = [&](Work& x) -> bool {
-        while (index >= 0 && index < total) {
-          int s, in;
-          if (index < total1) {
-            s = find_seq(p.S, index, lane, [&](int i) { return p.seq[i].before1; });
-            in = index - p.seq[s].before1;
-          } else {
-            s = find_seq(p.S, index - total1, lane, [&](int i) { return p.seq[i].before2; });
-            in = index - total1 - p.seq[s].before2;
-          }
-          index = take();
-          const SeqRows r = seq_rows(p, s);
-          const int cuts = p.cuts[s];
-          const int nt = (r.b - r.a + p.tpt - 1) / p.tpt;
+        while (true) {
+          const int index = begun ? static_cast<int>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, taken, 0) : taken;
+          if (index < 0 || index >= total) return false;
+          int s;
+          if (!begun) s = p.first[index];
+          else if (index < total1) s = find_seq(p.S, index, lane, [&](int i) { return p.seq[i].before1; });
+          else s = find_seq(p.S, index - total1, lane, [&](int i) { return p.seq[i].before2; });
+          begun = true;
+          if (lane == 0) taken = atomicAdd(&p.plan->next, 1);
+          const ChunkSeq q = p.seq[s];
+          const int in = index < total1 ? index - q.before1 : index - total1 - q.before2;
           // tiles first (the last ones, which see most keys, lead), then parts, then heads
-          const int cut = in / nt % cuts;
-          x.hkv = in / nt / cuts;
-          const Tile t = seq_tile(r, nt - 1 - in % nt, p.tpt);
+          const int cut = in / q.nt % q.cuts;
+          const int hkv = in / q.nt / q.cuts;
+          const SeqRows r{q.a, q.b, q.n, q.shift, false};
+          const Tile t = seq_tile(r, q.nt - 1 - in % q.nt, p.tpt);
           x.t0 = t.t0;
-          x.ntok = t.ntok;
           x.p0 = t.p0;
+          x.heads = hkv << 8 | t.ntok;
           x.n = r.n;
           x.kb = tile_blocks(p, t, r.n);
-          if (cuts > 1) x.kb = x.kb.part(cut, cuts);
-          x.slot = cuts > 1 ? p.seq[s].slot0 + in : -1;
+          if (q.cuts > 1) x.kb = x.kb.part(cut, q.cuts);
+          x.slot = q.cuts > 1 ? q.slot0 + in : -1;
           if (t.p0 < 0 && lane == 0) record_error(p.err, ATTN_ERR_BAD_PAGES);
           x.s = s;
           x.low = clamped(r.a + r.shift - p.window + 1, 0, r.n);
@@ -607,14 +633,13 @@ __global__ void __launch_bounds__(512, 1)
             float* l = p.part + static_cast<size_t>(x.slot) * C::kPartFloats + kTileM * (D + 1);
             for (int i = lane; i < kTileM; i += 32) l[i] = 0.f;
           } else {                                         // rows that see nothing
-            for (int i = 0; i < x.ntok * p.G; ++i) {
-              const size_t row = static_cast<size_t>(x.t0 + i / p.G) * p.H + x.hkv * p.G + i % p.G;
+            for (int i = 0; i < x.ntok() * p.G; ++i) {
+              const size_t row = static_cast<size_t>(x.t0 + i / p.G) * p.H + x.hkv() * p.G + i % p.G;
               for (int e = lane; e < D; e += 32) p.o[row * D + e] = __float2bfloat16(0.f);
               if (lane == 0) p.lse[row] = NEG_INF;
             }
           }
         }
-        return false;
       };
       // Hand a piece (or, with no key blocks, the end) to the other roles.
       auto publish = [&](const Piece& x) -> bool {
@@ -622,10 +647,8 @@ __global__ void __launch_bounds__(512, 1)
         if (lane == 0) {
           volatile Piece* dst = piece_slot(np);
           dst->t0 = x.t0;
-          dst->ntok = x.ntok;
           dst->p0 = x.p0;
-          dst->n = x.n;
-          dst->hkv = x.hkv;
+          dst->heads = x.heads;
           dst->slot = x.slot;
           dst->kb.nsb = x.kb.nsb;
           dst->kb.wb0 = x.kb.wb0;
@@ -649,7 +672,7 @@ __global__ void __launch_bounds__(512, 1)
           if (b.key < x.n) {
             b.page = __ldg(p.table + static_cast<size_t>(x.s) * p.M + (b.key >> p.page_log2));
             const int last = b.key + br - 1;
-            b.seen = b.key <= x.p0 + x.ntok - 1 && (last > x.p0 - p.window || b.key < p.sinks);
+            b.seen = b.key <= x.p0 + x.ntok() - 1 && (last > x.p0 - p.window || b.key < p.sinks);
           }
         }
         return b;
@@ -682,7 +705,7 @@ __global__ void __launch_bounds__(512, 1)
           mbar_arrive_expect_tx(bar(C::kBarRFull + s), boxes * box_bytes);
         }
         __syncwarp();
-        if (mine) copy(map, sbase + C::kROff + s * C::kRawBytes + sub * br * D, C::kBarRFull + s, b, x.hkv);
+        if (mine) copy(map, sbase + C::kROff + s * C::kRawBytes + sub * br * D, C::kBarRFull + s, b, x.hkv());
         ++ir;
         return true;
       };
@@ -702,7 +725,7 @@ __global__ void __launch_bounds__(512, 1)
           __syncwarp();
           if (b.page >= 0)
             copy(&tmK, sbase + C::kKOff + s * C::kKBytes + (c_of * 2 + t_of) * C::kChunkBytes + sub * br * 128,
-                 C::kBarKFull + s, b, x.hkv);
+                 C::kBarKFull + s, b, x.hkv());
           ++ik;
           return true;
         }
@@ -723,16 +746,20 @@ __global__ void __launch_bounds__(512, 1)
             const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
             if (lane == 0) mbar_arrive_expect_tx(bar(full), boxes * box_bytes);
             __syncwarp();
-            if (mine) copy(&tmV, vs + c_of * C::kChunkBytes + sub * br * 128, full, b, x.hkv);
+            if (mine) copy(&tmV, vs + c_of * C::kChunkBytes + sub * br * 128, full, b, x.hkv());
             ++iv;
             if (!clean) {
               // (the next K and Q are on their way already)
               ++landed;
               if (!wait(C::kBarLand, (landed - 1) & 1)) return false;
-              for (int r = 0; r < kTileN; ++r) {
+              const uint32_t held = (2u << ((rows.rows - 1) >> 4)) - 1u;
+              const bool tail = (rows.groups & held) == held && rows.low == 0;   // the last rows alone lack
+#pragma unroll 4
+              for (int r = (tail ? rows.rows & ~3 : 0) + (lane >> 3); r < kTileN; r += 4) {
                 if (rows.has(r)) continue;
-                if (lane < C::kChunks * 8)
-                  sts128(vs + (lane >> 3) * C::kChunkBytes + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c)
+                  sts128(vs + c * C::kChunkBytes + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
               }
               fence_proxy_async_smem();
               __syncwarp();
@@ -752,7 +779,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_3d(sbase + C::kQOff + s * C::kTileBytes + c * C::kChunkBytes, &tmQ, bar(full), c * 64,
-                        x.hkv * p.G, x.t0);
+                        x.hkv() * p.G, x.t0);
         }
         __syncwarp();
         ++qn;
@@ -962,8 +989,8 @@ __global__ void __launch_bounds__(512, 1)
       const float inv = inv_s[row];
       if (!wait(C::kBarOFull, on & 1)) return false;
       tc_fence_after();
-      const bool inb = tok < x.ntok;
-      const size_t at = static_cast<size_t>(x.t0 + tok) * p.H + x.hkv * p.G + head;
+      const bool inb = tok < x.ntok();
+      const size_t at = static_cast<size_t>(x.t0 + tok) * p.H + x.hkv() * p.G + head;
       uint4* dst = reinterpret_cast<uint4*>(p.o + at * D);
       float4* part = reinterpret_cast<float4*>(p.part + static_cast<size_t>(max(x.slot, 0)) * C::kPartFloats) + row;
       // 16 columns at a time (the warpgroup has few registers); a row without a
@@ -1007,24 +1034,28 @@ __global__ void __launch_bounds__(512, 1)
         const int s = ir % C::kStagesR;
         if (!wait(C::kBarRFull + s, (ir / C::kStagesR) & 1)) return false;
         if (used && !wait(empty, parity)) return false;
-        const bool there = block_rows(raw_info[s]).has(row);
         const uint32_t src = sbase + C::kROff + s * C::kRawBytes + row * D;
         const uint32_t to = dst + row * 128;
-#pragma unroll 2
-        for (int u = 0; u < D / 16; ++u) {          // 16 elements
-          const int su = D == 128 ? u ^ (row & 7) : u ^ ((row >> 1) & 3);
-          const uint4 w = lds128(src + su * 16);
-          uint32_t f[8];
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        if (block_rows(raw_info[s]).has(row)) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[2 * e] = there ? e4m3x2_f16x2(in[e]) : 0u;
-            f[2 * e + 1] = there ? e4m3x2_f16x2(in[e] >> 16) : 0u;
+          for (int u0 = 0; u0 < D / 16; u0 += 4) {
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)               // 16 elements each
+              w[i] = lds128(src + ((D == 128 ? (u0 + i) ^ (row & 7) : (u0 + i) ^ ((row >> 1) & 3)) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int u = u0 + i, u2 = (2 * u) & 7;
+              const uint32_t at = to + (u >> 2) * C::kChunkBytes;
+              sts128(at + ((u2 ^ (row & 7)) << 4), e4m3x2_f16x2(w[i].x), e4m3x2_f16x2(w[i].x >> 16),
+                     e4m3x2_f16x2(w[i].y), e4m3x2_f16x2(w[i].y >> 16));
+              sts128(at + (((u2 + 1) ^ (row & 7)) << 4), e4m3x2_f16x2(w[i].z), e4m3x2_f16x2(w[i].z >> 16),
+                     e4m3x2_f16x2(w[i].w), e4m3x2_f16x2(w[i].w >> 16));
+            }
           }
-          const uint32_t at = to + (u >> 2) * C::kChunkBytes;
-          const int u2 = (2 * u) & 7;
-          sts128(at + ((u2 ^ (row & 7)) << 4), f[0], f[1], f[2], f[3]);
-          sts128(at + (((u2 + 1) ^ (row & 7)) << 4), f[4], f[5], f[6], f[7]);
+        } else {
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) sts128(to + (u >> 3) * C::kChunkBytes + (u & 7) * 16, 0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(full));
@@ -1151,9 +1182,9 @@ __global__ void __launch_bounds__(512, 1)
       const int ns = (nb + 1) / 2;
       const int own = x.p0 + tok;                 // this row's own key, and the first its window holds
       const int low = own - p.window + 1;
-      const int low_last = x.p0 + x.ntok - p.window;
+      const int low_last = x.p0 + x.ntok() - p.window;
       float sl2 = p.scale_log2;
-      if constexpr (FP8) sl2 *= __ldg(p.k_scale + x.hkv);
+      if constexpr (FP8) sl2 *= __ldg(p.k_scale + x.hkv());
       float m2 = NEG_INF;     // reference max (log2 units), moved only by > 8
       float l = 0.f;          // this warpgroup's part of the row sum
       for (int k = 0; k < ns; ++k) {
@@ -1319,16 +1350,16 @@ __global__ void __launch_bounds__(512, 1)
         const float lt = l + lo;
         const float m = FP8 ? m2 - kP2 : m2;      // the max that goes with l
         float vs = 1.f;
-        if constexpr (FP8) vs = __ldg(p.v_scale + x.hkv);
+        if constexpr (FP8) vs = __ldg(p.v_scale + x.hkv());
         inv_s[row_in_tile] = lt == 0.f ? 0.f : vs / lt;
         mbar_arrive(bar(C::kBarLFull));
-        if (tok < x.ntok) {
+        if (tok < x.ntok()) {
           if (x.slot >= 0) {
             float* part = p.part + static_cast<size_t>(x.slot) * C::kPartFloats + kTileM * D + row_in_tile;
             part[0] = m;
             part[kTileM] = lt;
           } else {
-            p.lse[static_cast<size_t>(x.t0 + tok) * p.H + x.hkv * p.G + row_in_tile - tok * p.G] =
+            p.lse[static_cast<size_t>(x.t0 + tok) * p.H + x.hkv() * p.G + row_in_tile - tok * p.G] =
                 lt == 0.f ? NEG_INF : (m + __log2f(lt)) * kLn2;
           }
         }
@@ -1347,7 +1378,7 @@ __global__ void __launch_bounds__(512, 1)
 }
 
 // ----------------------------------------------------------------------------
-// the join: a CTA a (tile, K/V head) and 32 columns, a thread a row and 16 of them
+// the join: a CTA a (tile, K/V head) and 16 columns, a thread a row and 8 of them
 // ----------------------------------------------------------------------------
 constexpr int kJoinThreads = 2 * kTileM;
 template <int D, bool FP8>
@@ -1356,51 +1387,66 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
   const float NEG_INF = -__int_as_float(0x7f800000);
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int row = static_cast<int>(threadIdx.x) & (kTileM - 1);
-  const int col = static_cast<int>(blockIdx.y) * 32 + static_cast<int>(threadIdx.x >> 7) * 16;
+  const int col = static_cast<int>(blockIdx.y) * 16 + static_cast<int>(threadIdx.x >> 7) * 8;
   const int tok = row / p.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");      // the parts are complete
   const int joins = p.plan->joins;
   for (int j = static_cast<int>(blockIdx.x); j < joins; j += static_cast<int>(gridDim.x)) {
     const int s = find_seq(p.S, j, lane, [&](int i) { return p.seq[i].join0; });
     const ChunkSeq q = p.seq[s];
-    const SeqRows r = seq_rows(p, s);
-    const int cuts = p.cuts[s], nt = (r.b - r.a + p.tpt - 1) / p.tpt;
+    const SeqRows r{q.a, q.b, q.n, q.shift, false};
+    const int cuts = q.cuts, nt = q.nt;
     const int in = j - q.join0;
     const int hkv = in / nt, i = in % nt;                 // the tile's number among its pieces'
     const Tile t = seq_tile(r, nt - 1 - i, p.tpt);
     if (tok >= t.ntok) continue;
     const float* part = p.part + static_cast<size_t>(q.slot0 + hkv * cuts * nt + i) * kPart;
     const size_t step = static_cast<size_t>(nt) * kPart;  // from part to part
-    float m = NEG_INF, l = 0.f, y[16];
+    float m = NEG_INF, l = 0.f, y[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) y[e] = 0.f;
-    for (int c = 0; c < cuts; ++c) {
-      const float lc = part[c * step + kTileM * (D + 1) + row];
-      if (lc != 0.f) m = fmaxf(m, part[c * step + kTileM * D + row]);
+    for (int e = 0; e < 8; ++e) y[e] = 0.f;
+    // four parts' loads are in flight together (past the last one the last is read
+    // again, and not counted)
+    constexpr int kBatch = 4;
+    for (int c0 = 0; c0 < cuts; c0 += kBatch) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float* x = part + min(c0 + u, cuts - 1) * step + kTileM * D + row;
+        if (x[kTileM] != 0.f) m = fmaxf(m, x[0]);
+      }
     }
-    for (int c = 0; c < cuts; ++c) {
-      const float lc = part[c * step + kTileM * (D + 1) + row];
-      if (lc == 0.f) continue;                            // this part saw no key
-      const float w = ex2(part[c * step + kTileM * D + row] - m);
-      l = fmaf(w, lc, l);
-      const float4* a = reinterpret_cast<const float4*>(part + c * step) + col / 4 * kTileM + row;
+    for (int c0 = 0; c0 < cuts; c0 += kBatch) {
+      float lc[kBatch], mc[kBatch];
+      float4 v[kBatch][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 v = a[e * kTileM];
-        y[4 * e] = fmaf(w, v.x, y[4 * e]);
-        y[4 * e + 1] = fmaf(w, v.y, y[4 * e + 1]);
-        y[4 * e + 2] = fmaf(w, v.z, y[4 * e + 2]);
-        y[4 * e + 3] = fmaf(w, v.w, y[4 * e + 3]);
+      for (int u = 0; u < kBatch; ++u) {
+        const float* x = part + min(c0 + u, cuts - 1) * step;
+        mc[u] = x[kTileM * D + row];
+        lc[u] = c0 + u < cuts ? x[kTileM * (D + 1) + row] : 0.f;
+        const float4* a = reinterpret_cast<const float4*>(x) + col / 4 * kTileM + row;
+        v[u][0] = a[0];
+        v[u][1] = a[kTileM];
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (lc[u] == 0.f) continue;                       // this part saw no key
+        const float w = ex2(mc[u] - m);
+        l = fmaf(w, lc[u], l);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[4 * e] = fmaf(w, v[u][e].x, y[4 * e]);
+          y[4 * e + 1] = fmaf(w, v[u][e].y, y[4 * e + 1]);
+          y[4 * e + 2] = fmaf(w, v[u][e].z, y[4 * e + 2]);
+          y[4 * e + 3] = fmaf(w, v[u][e].w, y[4 * e + 3]);
+        }
       }
     }
     float inv = l == 0.f ? 0.f : 1.f / l;
     if constexpr (FP8) inv *= __ldg(p.v_scale + hkv);
     const size_t at = static_cast<size_t>(t.t0 + tok) * p.H + hkv * p.G + row - tok * p.G;
     uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + col);
-    dst[0] = make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
-                        pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
-    dst[1] = make_uint4(pack_bf16(y[8] * inv, y[9] * inv), pack_bf16(y[10] * inv, y[11] * inv),
-                        pack_bf16(y[12] * inv, y[13] * inv), pack_bf16(y[14] * inv, y[15] * inv));
+    *dst = make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
+                      pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
     if (col == 0) p.lse[at] = l == 0.f ? NEG_INF : (m + __log2f(l)) * kLn2;
   }
 }
@@ -1430,10 +1476,10 @@ int most_slots(int T, int S, int Hkv, int G, int M, int page) {
   return static_cast<int>(tiles >= kMaxParts ? kMaxParts : std::min<long long>(kMaxParts, tiles * cuts));
 }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-// plan | sequences | cuts | parts
+// plan | first pieces | sequences | parts
+constexpr int kMaxSms = 256;
 size_t chunk_workspace(int T, int S, int H, int Hkv, int d, int M, int page) {
-  return up256(sizeof(ChunkPlan)) + up256(static_cast<size_t>(S) * sizeof(ChunkSeq)) +
-         up256(static_cast<size_t>(S) * 4) +
+  return up256(sizeof(ChunkPlan)) + kMaxSms * 4 + up256(static_cast<size_t>(S) * sizeof(ChunkSeq)) +
          static_cast<size_t>(most_slots(T, S, Hkv, H / Hkv, M, page)) * kTileM * (d + 2) * 4;
 }
 
@@ -1468,7 +1514,9 @@ cudaError_t chunk_device(int* sms) {
     if (fa.numRegs < static_cast<int>(kChunkLaunchRegs)) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<D, FP8>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&known[dev], cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    int n = 0;
+    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    known[dev] = std::min(n, kMaxSms);
   }
   *sms = known[dev];
   return cudaSuccess;
@@ -1480,7 +1528,8 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   int sms = 0;
   cudaError_t e = chunk_device<D, FP8>(&sms);
   if (e != cudaSuccess) return e;
-  p.ctas = sms;
+  const long long pieces = std::max<long long>(most_tiles(p.T, p.S, p.G) * p.Hkv, p.slots);
+  p.ctas = static_cast<int>(std::min<long long>(sms, pieces));
   chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the next kernels are set up while the ones before them run; they wait for
@@ -1489,8 +1538,7 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  const long long pieces = std::max<long long>(most_tiles(p.T, p.S, p.G) * p.Hkv, p.slots);
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(sms, pieces)));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
   cfg.blockDim = dim3(ChunkCfg<D, FP8>::kThreads);
   cfg.dynamicSmemBytes = ChunkCfg<D, FP8>::kSmemBytes;
   cfg.stream = st;
@@ -1498,7 +1546,7 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, attn_fwd_paged_kernel<D, FP8>, tq, tk, tv, p)) != cudaSuccess) return e;
   if (p.slots == 0) return cudaSuccess;
-  cfg.gridDim = dim3(std::min(p.slots, 2 * sms), D / 32);
+  cfg.gridDim = dim3(std::min(p.slots, 2 * sms), D / 16);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, FP8>, p);
@@ -1568,10 +1616,10 @@ extern "C" attn_status_t attn_fwd_paged(
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.plan = reinterpret_cast<ChunkPlan*>(ws);
   ws += up256(sizeof(ChunkPlan));
+  p.first = reinterpret_cast<int*>(ws);
+  ws += kMaxSms * 4;
   p.seq = reinterpret_cast<ChunkSeq*>(ws);
   ws += up256(static_cast<size_t>(S) * sizeof(ChunkSeq));
-  p.cuts = reinterpret_cast<int*>(ws);
-  ws += up256(static_cast<size_t>(S) * 4);
   p.part = reinterpret_cast<float*>(ws);
   p.scale_log2 = scale * kLog2e;
   // no position reaches kMaxTokens

@@ -24,12 +24,16 @@
 //     same time share their keys (tiles first, then key parts): L2 serves all but
 //     one of them.  The parts of a tile leave (m, l, A) in the workspace, and a
 //     last kernel joins them in order (so the counter does not show in a bit).
-//   * e4m3 pages are read as they are.  One MMA wants the same 16-bit type of both
-//     operands, so a warpgroup turns a tile into fp16, exactly, on its way through
-//     shared memory; Q is scaled row by row by a power of two (largest element in
-//     [128, 256)) and P by 2^7, so that fp16 rounds them by at most 2^-32 of a
-//     row's largest element (Q) or 2^-11 of the element (P, and 2^-31 of the
-//     largest).  Over bf16 pages P is rounded to bf16, V's type.
+//   * e4m3 pages are read as they are.  K stays so: Q, scaled row by row by a power
+//     of two (largest element in [128, 256)), is held as two 8-bit parts, e4m3 and
+//     the rest in e5m2.  A bf16 element's 8 bits less the first part's 4 leave 3
+//     and a sign, which e5m2 holds: the parts are exact down to 2^-13 of a row's
+//     largest element, below it off by at most 2^-21 of that.  P has to keep more
+//     bits than two such parts could over its range, so V is turned into fp16,
+//     exactly, on its way through shared memory, and P carries 2^7 and is rounded
+//     to fp16, by 2^-11 (and 2^-32 of a row's largest).  With K turned into fp16,
+//     too, the turning took 5800 cycles a pair, twice the MMAs.
+//     Over bf16 pages P is rounded to bf16, V's type.
 // Rows of the caches that hold no token may hold anything: V's are set to zero in
 // shared memory, S's are masked.
 #include <cuda_fp16.h>
@@ -381,9 +385,9 @@ struct ChunkCfg {
   static constexpr int kTileBytes = kTileM * D * 2;
   static constexpr int kRawBytes = kTileM * D;             // 128 rows of e4m3
   static constexpr int kStagesQ = D == 64 ? 2 : 1;
-  // K: pairs of blocks, side by side for an N = 256 MMA; e4m3: single blocks
-  static constexpr int kKBytes = FP8 ? kTileBytes : 2 * kTileBytes;
-  static constexpr int kStagesK = FP8 ? (D == 64 ? 4 : 2) : (D == 64 ? 3 : 2);
+  // K: pairs of blocks, side by side for an N = 256 MMA
+  static constexpr int kKBytes = 2 * (FP8 ? kRawBytes : kTileBytes);
+  static constexpr int kStagesK = FP8 && D == 64 ? 4 : (D == 64 ? 3 : 2);
   static constexpr int kStagesV = D == 64 ? 4 : 2;
   static constexpr int kStagesR = FP8 ? (D == 64 ? 6 : 4) : 0;
   static constexpr int kQOff = 0;
@@ -412,7 +416,7 @@ struct ChunkCfg {
   static constexpr int kBarPieceEmpty = kBarPieceFull + 2; // [2] ... read by every role
   // bf16: a V block that is cleaned has landed; e4m3: Q has landed, by stage
   static constexpr int kBarLand = kBarPieceEmpty + 2;
-  static constexpr int kBarRFull = kBarLand + kStagesQ;    // raw tiles: landed
+  static constexpr int kBarRFull = kBarLand + kStagesQ;    // e4m3's V tiles: landed
   static constexpr int kBarREmpty = kBarRFull + kStagesR;  // ... converted
   static constexpr int kNumBars = kBarREmpty + kStagesR;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
@@ -420,9 +424,9 @@ struct ChunkCfg {
   static constexpr int kAbortOff = kMiscOff + 4;
   // [kRing] which groups of 16 keys of a pair have a page; a pair's entry is
   // written when its K is asked for, and read before its S is given back: at
-  // most the K stages and raw tiles, and one, lie between
-  static constexpr int kRing = D == 64 ? 16 : 8;
-  static_assert(kRing > kStagesK + kStagesR + 1, "a pair's entry is read before it is written again");
+  // most the K stages, and one, lie between
+  static constexpr int kRing = 8;
+  static_assert(kRing > kStagesK + 1, "a pair's entry is read before it is written again");
   static constexpr int kValidOff = kMiscOff + 8;
   static constexpr int kRawInfoOff = kValidOff + kRing * 2;        // [stages] BlockRows of a raw tile
   static constexpr int kPieceOff = kRawInfoOff + ((kStagesR * 4 + 7) / 8) * 8;
@@ -449,10 +453,26 @@ constexpr uint32_t kChunkLaunchRegs = 128;
 static_assert(kChunkOut + 2 * kChunkSoft + kChunkLow <= 4 * kChunkLaunchRegs, "register split exceeds the launch");
 constexpr float kP2 = 7.f;                  // e4m3: P carries 2^7
 
-// kind::f16 with fp16 operands: A and B formats 0.
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+// kind::f16 with fp16 operands, kind::f8f6f4 with e4m3 ones: formats 0; A in
+// e5m2: format 1 in bits 7-9.
+__host__ __device__ constexpr uint32_t idesc_f32(int M, int N, bool b_mn_major, uint32_t a_format = 0u) {
+  return (1u << 4) | (a_format << 7) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D[tmem] (+)= A[smem desc] * B[smem desc], 32 8-bit elements deep
+__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Shared-memory matrix descriptor of rows of 64 bytes with the 64-byte swizzle
+// (mode 4): 8 rows are 512 bytes.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
+  return (sdesc_sw128(saddr, 16, 512) & ~(static_cast<uint64_t>(7) << 61)) | static_cast<uint64_t>(4) << 61;
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
                                             int c2) {
@@ -466,6 +486,17 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {        // the low
   uint32_t y;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
   return y;
+}
+// x and y in e4m3 (the low 16 bits) and what that leaves of them in e5m2 (the high).
+__device__ __forceinline__ uint32_t two_parts(float x, float y) {
+  uint32_t h, a, b;
+  asm("{\n\t.reg .b16 q;\n\tcvt.rn.satfinite.e4m3x2.f32 q, %3, %2;\n\tcvt.u32.u16 %0, q;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, q;\n\t}"
+      : "=r"(a), "=r"(h) : "f"(x), "f"(y));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  asm("{\n\t.reg .b16 q;\n\tcvt.rn.satfinite.e5m2x2.f32 q, %2, %1;\n\tcvt.u32.u16 %0, q;\n\t}"
+      : "=r"(b) : "f"(x - f.x), "f"(y - f.y));
+  return a | b << 16;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -512,7 +543,7 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(bar(C::kBarLand + s), 1);
     }
     for (int s = 0; s < C::kStagesK; ++s) {
-      mbar_init(bar(C::kBarKFull + s), FP8 ? kTileM : 1);
+      mbar_init(bar(C::kBarKFull + s), 1);
       mbar_init(bar(C::kBarKEmpty + s), 1);
     }
     for (int s = 0; s < C::kStagesV; ++s) {
@@ -694,7 +725,7 @@ __global__ void __launch_bounds__(512, 1)
         return BlockRows{min(kTileN, x.n - k0), max(0, min(x.low - k0, kTileN)), max(0, min(p.sinks - k0, kTileN)),
                          ok >> (8 * t) & 255u};
       };
-      // e4m3: block t of a pair into the next raw tile
+      // e4m3: V's block t of a pair into the next raw tile
       auto load_raw = [&](const CUtensorMap* map, const Work& x, int k, int t, const Box& b, uint32_t ok) -> bool {
         const int s = ir % max(1, C::kStagesR);
         if (ir >= C::kStagesR && !wait(C::kBarREmpty + s, ((ir / max(1, C::kStagesR)) & 1) ^ 1)) return false;
@@ -714,21 +745,18 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t ok = groups(b);
         if (lane == 0) valid_ring[pairs % C::kRing] = static_cast<uint16_t>(ok);
         ++pairs;
-        if constexpr (FP8) {
-          if (!load_raw(&tmK, x, k, 0, b, ok)) return false;
-          return 2 * k + 1 >= x.kb.count() || load_raw(&tmK, x, k, 1, b, ok);
-        } else {
-          const int s = ik % C::kStagesK;
-          if (ik >= C::kStagesK && !wait(C::kBarKEmpty + s, ((ik / C::kStagesK) & 1) ^ 1)) return false;
-          const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, b.page >= 0));
-          if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarKFull + s), boxes * box_bytes);
-          __syncwarp();
-          if (b.page >= 0)
-            copy(&tmK, sbase + C::kKOff + s * C::kKBytes + (c_of * 2 + t_of) * C::kChunkBytes + sub * br * 128,
-                 C::kBarKFull + s, b, x.hkv());
-          ++ik;
-          return true;
+        const int s = ik % C::kStagesK;
+        if (ik >= C::kStagesK && !wait(C::kBarKEmpty + s, ((ik / C::kStagesK) & 1) ^ 1)) return false;
+        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, b.page >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarKFull + s), boxes * box_bytes);
+        __syncwarp();
+        if (b.page >= 0) {
+          const uint32_t at = FP8 ? t_of * C::kRawBytes + sub * br * D
+                                  : (c_of * 2 + t_of) * C::kChunkBytes + sub * br * 128;
+          copy(&tmK, sbase + C::kKOff + s * C::kKBytes + at, C::kBarKFull + s, b, x.hkv());
         }
+        ++ik;
+        return true;
       };
       auto load_v = [&](const Work& x, int k, const Box& b) -> bool {
         const uint32_t ok = groups(b);
@@ -850,11 +878,12 @@ __global__ void __launch_bounds__(512, 1)
       // as soon as both softmax warpgroups hold this pair's S in registers, then
       // this pair's P V.
       if (lane == 0) {
-        constexpr uint32_t kIdescS = FP8 ? idesc_f16_f32(kTileM, 2 * kTileN, false)
+        constexpr uint32_t kIdescS = FP8 ? idesc_f32(kTileM, 2 * kTileN, false)
                                          : idesc_bf16_f32(kTileM, 2 * kTileN, false, false);
-        constexpr uint32_t kIdescS1 = FP8 ? idesc_f16_f32(kTileM, kTileN, false)
+        constexpr uint32_t kIdescS1 = FP8 ? idesc_f32(kTileM, kTileN, false)
                                           : idesc_bf16_f32(kTileM, kTileN, false, false);   // a block alone
-        constexpr uint32_t kIdescPV = FP8 ? idesc_f16_f32(kTileM, D, true) : idesc_bf16_f32(kTileM, D, false, true);
+        constexpr uint32_t kE5m2 = 1u << 7;
+        constexpr uint32_t kIdescPV = FP8 ? idesc_f32(kTileM, D, true) : idesc_bf16_f32(kTileM, D, false, true);
         int ik = 0, iv = 0;     // K stages and V tiles consumed
         int qn = 0;             // Q tiles consumed
         int sn = 0;             // S tiles issued
@@ -871,35 +900,31 @@ __global__ void __launch_bounds__(512, 1)
           if (sn > 0 && !wait_bar(bar(C::kBarSFree), (sn - 1) & 1, abort_flag, p.err)) return false;
           const int qs = (qn - 1) % C::kStagesQ;
           const uint64_t dq = sdesc_sw128(sbase + C::kQOff + qs * C::kTileBytes, 16, 1024);
+          const int s = ik % C::kStagesK;
+          if (!wait_bar(bar(C::kBarKFull + s), (ik / C::kStagesK) & 1, abort_flag, p.err)) return false;
+          tc_fence_after();
+          const uint32_t idesc = 2 * k + 1 < nb ? kIdescS : kIdescS1;
+          const uint32_t ks = sbase + C::kKOff + s * C::kKBytes;
           if constexpr (FP8) {
-            for (int t = 0; t < 2 && 2 * k + t < nb; ++t) {
-              const int s = ik % C::kStagesK;
-              if (!wait_bar(bar(C::kBarKFull + s), (ik / C::kStagesK) & 1, abort_flag, p.err)) return false;
-              tc_fence_after();
-              const uint64_t dk = sdesc_sw128(sbase + C::kKOff + s * C::kKBytes, 16, 1024);
+            // Q's parts: d=128 a tile of 128-byte rows each, d=64 the halves of one
+            const uint64_t dk = D == 128 ? sdesc_sw128(ks, 16, 1024) : sdesc_sw64(ks);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
-                mma_ss(tmem + C::kColS + t * kTileN, sdesc_add(dq, off), sdesc_add(dk, off), kIdescS1, kk > 0 ? 1u : 0u);
-              }
-              mma_commit(bar(C::kBarKEmpty + s));
-              ++ik;
-            }
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_ss_f8(tmem + C::kColS, sdesc_add(dq, part * (D == 128 ? C::kChunkBytes : 64) + kk * 32),
+                          sdesc_add(dk, kk * 32), part == 0 ? idesc : idesc | kE5m2, part > 0 || kk > 0 ? 1u : 0u);
           } else {
-            const int s = ik % C::kStagesK;
-            if (!wait_bar(bar(C::kBarKFull + s), (ik / C::kStagesK) & 1, abort_flag, p.err)) return false;
-            tc_fence_after();
-            const uint64_t dk = sdesc_sw128(sbase + C::kKOff + s * C::kKBytes, 16, 1024);
-            const uint32_t idesc = 2 * k + 1 < nb ? kIdescS : kIdescS1;
+            const uint64_t dk = sdesc_sw128(ks, 16, 1024);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t qoff = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
               const uint32_t koff = (kk >> 2) * 2 * C::kChunkBytes + (kk & 3) * 32;
               mma_ss(tmem + C::kColS, sdesc_add(dq, qoff), sdesc_add(dk, koff), idesc, kk > 0 ? 1u : 0u);
             }
-            mma_commit(bar(C::kBarKEmpty + s));
-            ++ik;
           }
+          mma_commit(bar(C::kBarKEmpty + s));
+          ++ik;
           mma_commit(bar(C::kBarSFull));
           if (2 * k + 2 >= nb) mma_commit(bar(C::kBarQEmpty + qs));   // Q's buffer is free for a later piece
           ++sn;
@@ -1027,7 +1052,7 @@ __global__ void __launch_bounds__(512, 1)
       while (next_piece(x) && output(x)) {
       }
     } else {
-      int ir = 0, ik = 0, iv = 0, qn = 0;
+      int ir = 0, iv = 0, qn = 0;
       // the next raw tile becomes fp16 tile `dst`, its row `row` by this thread
       // (rows without a token become zeros), once that tile is free
       auto convert = [&](uint32_t dst, int full, int empty, bool used, uint32_t parity) -> bool {
@@ -1063,16 +1088,6 @@ __global__ void __launch_bounds__(512, 1)
         ++ir;
         return true;
       };
-      auto convert_k = [&](const Piece& x, int k) -> bool {
-        for (int t = 0; t < 2 && 2 * k + t < x.kb.count(); ++t) {
-          const int s = ik % C::kStagesK;
-          if (!convert(sbase + C::kKOff + s * C::kKBytes, C::kBarKFull + s, C::kBarKEmpty + s, ik >= C::kStagesK,
-                       ((ik / C::kStagesK) & 1) ^ 1))
-            return false;
-          ++ik;
-        }
-        return true;
-      };
       auto convert_v = [&](const Piece& x, int k) -> bool {
         for (int t = 0; t < 2 && 2 * k + t < x.kb.count(); ++t) {
           const int s = iv % C::kStagesV;
@@ -1083,34 +1098,80 @@ __global__ void __launch_bounds__(512, 1)
         }
         return true;
       };
-      // this thread's row of Q, in place: bf16 to fp16, by a power of two that
-      // puts its largest element in [128, 256)
+      // this thread's row of Q, in place: bf16 to two 8-bit parts, by a power of two
+      // that puts its largest element in [128, 256)
       auto convert_q = [&]() -> bool {
         const int s = qn % C::kStagesQ;
         if (!wait(C::kBarLand + s, (qn / C::kStagesQ) & 1)) return false;
         // the softmax has read the previous piece's factors
         if (qn > 0 && !wait(C::kBarPieceEmpty + ((qn - 1) & 1), ((qn - 1) >> 1) & 1)) return false;
         const uint32_t at = sbase + C::kQOff + s * C::kTileBytes + row * 128;
+        auto unit = [&](int c, int u) { return at + c * C::kChunkBytes + ((u ^ (row & 7)) << 4); };
         float top = 0.f;
 #pragma unroll 2
         for (int u = 0; u < D / 8; ++u) {
-          const uint4 w = lds128(at + (u >> 3) * C::kChunkBytes + (((u & 7) ^ (row & 7)) << 4));
+          const uint4 w = lds128(unit(u >> 3, u & 7));
           top = fmax3(top, fabsf(bf16lo(w.x)), fabsf(bf16hi(w.x)));
           top = fmax3(top, fabsf(bf16lo(w.y)), fabsf(bf16hi(w.y)));
           top = fmax3(top, fabsf(bf16lo(w.z)), fabsf(bf16hi(w.z)));
           top = fmax3(top, fabsf(bf16lo(w.w)), fabsf(bf16hi(w.w)));
         }
-        // 2^(134 - e) for a top of exponent field e, kept a normal number (an
-        // infinity or NaN stays one, whatever it is multiplied by)
-        int field = max(1, min(253, 127 + 134 - static_cast<int>(__float_as_uint(top) >> 23)));
-        if (top == 0.f) field = 127;
-        const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-#pragma unroll 2
-        for (int u = 0; u < D / 8; ++u) {
-          const uint32_t a = at + (u >> 3) * C::kChunkBytes + (((u & 7) ^ (row & 7)) << 4);
-          const uint4 w = lds128(a);
-          sts128(a, pack_f16(bf16lo(w.x) * up, bf16hi(w.x) * up), pack_f16(bf16lo(w.y) * up, bf16hi(w.y) * up),
-                 pack_f16(bf16lo(w.z) * up, bf16hi(w.z) * up), pack_f16(bf16lo(w.w) * up, bf16hi(w.w) * up));
+        // 2^(134 - e) for a top of exponent field e, kept a normal number; a row
+        // with an infinity becomes NaN, as its scores would be
+        const int e = static_cast<int>(__float_as_uint(top) >> 23);
+        const int field = top == 0.f ? 127 : max(1, min(253, 127 + 134 - e));
+        const float up = e == 255 ? __int_as_float(0x7fffffff) : __uint_as_float(static_cast<uint32_t>(field) << 23);
+        // 16 elements from units 2 u and 2 u + 1 of chunk c
+        auto parts = [&](int c, int u, uint32_t (&a)[4], uint32_t (&b)[4]) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 w = lds128(unit(c, 2 * u + i));
+            const uint32_t x0 = two_parts(bf16lo(w.x) * up, bf16hi(w.x) * up);
+            const uint32_t x1 = two_parts(bf16lo(w.y) * up, bf16hi(w.y) * up);
+            const uint32_t x2 = two_parts(bf16lo(w.z) * up, bf16hi(w.z) * up);
+            const uint32_t x3 = two_parts(bf16lo(w.w) * up, bf16hi(w.w) * up);
+            a[2 * i] = __byte_perm(x0, x1, 0x5410);
+            b[2 * i] = __byte_perm(x0, x1, 0x7632);
+            a[2 * i + 1] = __byte_perm(x2, x3, 0x5410);
+            b[2 * i + 1] = __byte_perm(x2, x3, 0x7632);
+          }
+        };
+        // the second parts wait in registers until their place has been read: they
+        // go to the row's second half (d=64) or second chunk (d=128)
+        uint32_t rest[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t a[4];
+          parts(0, u, a, rest[u]);
+          sts128(unit(0, u), a[0], a[1], a[2], a[3]);       // units 2 u + 1 and below have been read
+        }
+        if constexpr (D == 64) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) sts128(unit(0, 4 + u), rest[u][0], rest[u][1], rest[u][2], rest[u][3]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t a[4], b[4];
+            parts(1, u, a, b);
+            sts128(unit(0, 4 + u), a[0], a[1], a[2], a[3]);
+            // units 2 u and 2 u + 1 of the second chunk are free
+            if (u < 2) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                sts128(unit(1, 2 * u + i), rest[2 * u + i][0], rest[2 * u + i][1], rest[2 * u + i][2],
+                       rest[2 * u + i][3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rest[u][i] = b[i];  // (rest[0] and [1] went out with u = 0, [2], [3] with 1)
+            if (u == 2) {
+              sts128(unit(1, 4), rest[0][0], rest[0][1], rest[0][2], rest[0][3]);
+              sts128(unit(1, 5), rest[1][0], rest[1][1], rest[1][2], rest[1][3]);
+            }
+            if (u == 3) {
+              sts128(unit(1, 6), rest[2][0], rest[2][1], rest[2][2], rest[2][3]);
+              sts128(unit(1, 7), rest[3][0], rest[3][1], rest[3][2], rest[3][3]);
+            }
+          }
         }
         *reinterpret_cast<volatile uint8_t*>(smem + C::kUpOff + row) = static_cast<uint8_t>(field);
         fence_proxy_async_smem();
@@ -1118,19 +1179,16 @@ __global__ void __launch_bounds__(512, 1)
         ++qn;
         return true;
       };
-      // in the producer's order: V of a pair after K of the next one, which at a
-      // piece's end is the next piece's first, with its Q
+      // in the producer's order: at a piece's end the next one's Q before the last V
       Piece x, y;
       bool more = next_piece(x);
-      bool ok = !more || (convert_k(x, 0) && convert_q());
+      bool ok = !more || convert_q();
       while (ok && more) {
         const int ns = (x.kb.count() + 1) / 2;
         for (int k = 0; k < ns && ok; ++k) {
-          if (k + 1 < ns) {
-            ok = convert_k(x, k + 1);
-          } else {
+          if (k + 1 == ns) {
             more = next_piece(y);
-            ok = !more || (convert_k(y, 0) && convert_q());
+            ok = !more || convert_q();
           }
           ok = ok && convert_v(x, k);
         }

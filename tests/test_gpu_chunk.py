@@ -32,16 +32,22 @@ def ragged(news, H, d, seed, before=0, after=0):
     return torch.randn(cu[-1] + after, H, d, generator=g, device="cuda").bfloat16(), cu
 
 
-def check_rows(q, o, lse, c, lens, news, cu, window=0, sinks=0, skip=()):
+def check_rows(q, o, lse, c, lens, news, cu, window=0, sinks=0, skip=(), scale=None):
     H, d = q.shape[1:]
+    scale = scale or 1.0 / math.sqrt(d)
     for s, (n, new) in enumerate(zip(lens, news)):
         if new == 0 or s in skip:
             continue
         a, b = cu[s], cu[s + 1]
         mask = ref.window_mask(new, n, window or n, sinks, n - new, 0, "cuda")
-        args = (q[a:b].transpose(0, 1)[None], c.k64[s][None], c.v64[s][None], mask, 1.0 / math.sqrt(d))
+        args = (q[a:b].transpose(0, 1)[None], c.k64[s][None], c.v64[s][None], mask, scale)
         O, L, _ = ref.forward(*args)
         bo, bl = ref.forward_bounds(*args)
+        if getattr(c, "k_scale", None) is not None:
+            # over e4m3 pages P enters its product as fp16, 2^7 times itself relative to a maximum
+            # that the row's largest reaches: what is below 2^-14 there is off by at most half of
+            # fp16's last step, 2^-25, so a P_j by 2^-32 of the largest, which l holds whole
+            bo = bo + 2.0 ** -32 * (mask.double() @ c.v64[s].abs().repeat_interleave(H // c.v64[s].shape[0], 0))
         off = (o[a:b].transpose(0, 1)[None].double() - O).abs()
         assert (off <= bo).all(), (s, n, new, (off / bo).max())
         off = (lse[a:b].transpose(0, 1)[None].double() - L).abs()
@@ -53,7 +59,7 @@ def check_chunk(bss, c, q, cu, lens, news, window=0, sinks=0, **kw):
                                 k_scale=c.k_scale, v_scale=c.v_scale, **kw)
     torch.cuda.synchronize()
     assert bss.attn_poll_status() == 0
-    check_rows(q, o, lse, c, lens, news, cu, window, sinks)
+    check_rows(q, o, lse, c, lens, news, cu, window, sinks, scale=kw.get("scale"))
     return o, lse
 
 
@@ -229,12 +235,51 @@ def test_chunk_in_a_graph_and_on_streams(bss, e4m3):
             check_rows(q, o, lse, c, lens, news, cu)
 
 
-def test_chunk_of_large_scores(bss):
-    """Scores of some thousands, rows whose keys all score far below 0, zeros."""
-    c = Cache([500, 64], 2, 128, 16, 3)
-    q, cu = ragged([100, 64], 4, 128, 2)
-    for f in (60.0, -60.0, 0.0):
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_of_large_scores(bss, d, e4m3):
+    """Scores of some thousands, rows whose keys all score far below 0, zeros; the smallest and the
+    largest numbers; rows with an element that is hundreds of times the others."""
+    c = Cache([500, 64], 2, d, 16, 3, e4m3)
+    q, cu = ragged([100, 64], 4, d, 2)
+    for f in (60.0, -60.0, 0.0, 2.0 ** -130, 2.0 ** -100):
         check_chunk(bss, c, (q.float() * f).bfloat16(), cu, [500, 64], [100, 64])
+    check_chunk(bss, c, (q.float() * 2.0 ** 100).bfloat16(), cu, [500, 64], [100, 64], scale=2.0 ** -103)
+    for at in (0, d - 1):
+        far = q.clone()
+        far[::2, :, at] = 700.0
+        far[1::4, :, at] = -90.0
+        check_chunk(bss, c, far, cu, [500, 64], [100, 64])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_numbers_that_are_not_finite(bss, d, e4m3):
+    """A NaN among the keys reaches the rows that see it, one among the values its own column of the
+    rows of its 128 keys' block and later; other sequences are as they were."""
+    lens, news = [300, 200], [40, 60]
+    c = Cache(lens, 2, d, 16, 7, e4m3)
+    q, cu = ragged(news, 8, d, 1)
+    args = dict(k_scale=c.k_scale, v_scale=c.v_scale)
+    kind = c.k.dtype
+    bits = torch.tensor([0xFF if e4m3 else 0x7FC0], device="cuda", dtype=torch.int32)
+    nan = bits.to(torch.uint8 if e4m3 else torch.int16).view(kind)[0]
+    page = c.table[1, 50 // 16].item()
+
+    def planted(x, h, col):
+        y = x.view(torch.uint8 if e4m3 else torch.int16).clone()
+        y[page, h, 50 % 16, col] = nan.view(torch.uint8 if e4m3 else torch.int16)
+        return y.view(kind)
+
+    o, lse = bss.attn_fwd_paged(q, c.k, planted(c.v, 0, 5), c.table, c.lens, ints(cu), **args)
+    check_rows(q, o, lse, c, lens, news, cu, skip=(1,))
+    hit = o[cu[1]:].isnan()
+    assert hit[:, :4, 5].all() and hit.sum() == hit[:, :4, 5].numel() and lse.isfinite().all()
+    o, lse = bss.attn_fwd_paged(q, planted(c.k, 1, d - 1), c.v, c.table, c.lens, ints(cu), **args)
+    check_rows(q, o, lse, c, lens, news, cu, skip=(1,))
+    assert o[cu[1]:, 4:].isnan().all() and lse[cu[1]:, 4:].isnan().all()
+    assert o[cu[1]:, :4].isfinite().all()
+    assert bss.attn_poll_status() == 0
 
 
 def test_far_pages(bss):

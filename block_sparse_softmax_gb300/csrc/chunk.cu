@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const int cand = tid & (kPlanCuts - 1);
   const float turns = cand <= 6 ? 1.f + static_cast<float>(cand - 1) / 6.f
                                 : exp2f(static_cast<float>(cand - 6) * 0.3f + 0.9f);
-  const int my_len = cand == 0 ? max(1, longest) : max(kLeastPairs, static_cast<int>(ceilf(share / turns)));
+  const int whole = max(1, longest);
+  const int my_len = cand == 0 ? whole : min(whole, max(kLeastPairs, static_cast<int>(ceilf(share / turns))));
   // long pieces, their pairs with what a piece costs beside them; the others' pairs; slots
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = tid / kPlanCuts; s < p.S; s += kPlanThreads / kPlanCuts) {

@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     }
     const float each = v.x > 0.f ? v.y / v.x : 0.f, rounds = ceilf(v.x / ctas);
     const float idle = (rounds * ctas - v.x) * each;
-    // the long pieces' turns, what does not fit beside the last of them, and the join
-    float t = rounds * each + fmaxf(0.f, v.z - idle) / ctas + (v.w > 0.f ? 2.f : 0.f);
+    // the long pieces' turns, what does not fit beside the last of them, and the
+    // join: 6 us and 7 ns a part, in the 1.75 us that a pair takes
+    float t = rounds * each + fmaxf(0.f, v.z - idle) / ctas + (v.w > 0.f ? 3.5f + 0.004f * v.w : 0.f);
     if (cand > 0 && v.w > static_cast<float>(p.slots)) t = 3.4e38f;
     int best = cand;
 #pragma unroll
@@ -343,6 +344,7 @@ __device__ __forceinline__ int find_seq(int S, int x, int lane, const Before& be
 // ----------------------------------------------------------------------------
 // What the roles need of a piece.
 struct Piece {
+  int s;                     // its sequence
   int t0, p0;                // its tile's first row and that one's position
   int heads;                 // K/V head << 8 | tokens of the tile
   int slot;                  // -1: the whole tile's keys
@@ -350,12 +352,12 @@ struct Piece {
   __device__ __forceinline__ int ntok() const { return heads & 255; }
   __device__ __forceinline__ int hkv() const { return heads >> 8; }
 };
-static_assert(sizeof(Piece) == 32, "two pieces fit beside the tiles");
+static_assert(sizeof(Piece) == 36, "two pieces fit beside the tiles");
 
-// ... and the producer: its sequence, that one's length, and the first key that
-// some row of the sequence has in its window.
+// ... and the producer: the sequence's length, and the first key that some row of
+// the sequence has in its window.
 struct Work : Piece {
-  int s, n, low;
+  int n, low;
 };
 // Rows of a V block that some row of the sequence sees: [low, rows) and below
 // `sinks`, in the groups of 16 that have a page.  What the others hold (rows past
@@ -412,31 +414,35 @@ struct ChunkCfg {
   static constexpr int kBarOFull = kBarXch + 2;            // a piece's last P V completed
   static constexpr int kBarOEmpty = kBarOFull + 1;         // ... O and the row factors read
   static constexpr int kBarLFull = kBarOEmpty + 1;         // a piece's row factors written
-  static constexpr int kBarMmaDone = kBarLFull + 1;
-  static constexpr int kBarPieceFull = kBarMmaDone + 1;    // [2] a piece's description written
+  static constexpr int kBarWant = kBarLFull + 1;           // the next piece may be chosen
+  static constexpr int kBarPieceFull = kBarWant + 1;       // [2] a piece's description written
   static constexpr int kBarPieceEmpty = kBarPieceFull + 2; // [2] ... read by every role
-  // bf16: a V block that is cleaned has landed; e4m3: Q has landed, by stage
+  // [stages] bf16: a V block that wants cleaning has landed (VFull: it is clean); e4m3: Q has
   static constexpr int kBarLand = kBarPieceEmpty + 2;
-  static constexpr int kBarRFull = kBarLand + kStagesQ;    // e4m3's V tiles: landed
+  static constexpr int kLands = FP8 ? kStagesQ : kStagesV;
+  static constexpr int kBarRFull = kBarLand + kLands;      // e4m3's V tiles: landed
   static constexpr int kBarREmpty = kBarRFull + kStagesR;  // ... converted
-  static constexpr int kNumBars = kBarREmpty + kStagesR;
+  static constexpr int kReqs = FP8 ? 0 : 8;                // V blocks to be cleaned: at most the stages', and the end
+  static constexpr int kBarReq = kBarREmpty + kStagesR;
+  static constexpr int kNumBars = kBarReq + kReqs;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kTmemSlotOff = kMiscOff;
   static constexpr int kAbortOff = kMiscOff + 4;
   // [kRing] which groups of 16 keys of a pair have a page; a pair's entry is
   // written when its K is asked for, and read before its S is given back: at
   // most the K stages, and one, lie between
-  static constexpr int kRing = 8;
+  static constexpr int kRing = D == 64 ? 8 : 4;
   static_assert(kRing > kStagesK + 1, "a pair's entry is read before it is written again");
   static constexpr int kValidOff = kMiscOff + 8;
-  static constexpr int kRawInfoOff = kValidOff + kRing * 2;        // [stages] BlockRows of a raw tile
-  static constexpr int kPieceOff = kRawInfoOff + ((kStagesR * 4 + 7) / 8) * 8;
+  static constexpr int kInfoOff = kValidOff + kRing * 2;           // [stages] BlockRows of a V block that has landed
+  static constexpr int kReqOff = kInfoOff + (FP8 ? kStagesR : kStagesV) * 4;   // [requests] stages
+  static constexpr int kPieceOff = kReqOff + kReqs * 4;
   static constexpr int kUpOff = kPieceOff + 2 * static_cast<int>(sizeof(Piece));  // exponents of Q's factors
   static constexpr int kXchOff = (kUpOff + (FP8 ? kTileM : 0) + 15) / 16 * 16;
   static constexpr int kInvOff = kXchOff + 2 * 2 * kTileM * 4;
   static constexpr int kSmemBytes = kInvOff + kTileM * 4;
   static_assert(kSmemBytes <= 232448, "shared memory");
-  static_assert(kBarOff % 8 == 0 && kPieceOff % 8 == 0, "alignment");
+  static_assert(kBarOff % 8 == 0 && kInfoOff % 4 == 0, "alignment");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;      // S: 256 fp32 columns (key block X at 128 X)
   static constexpr uint32_t kColP = 256;    // P: 256 keys, 16-bit pairs (block X at 256 + 64 X)
@@ -446,12 +452,13 @@ struct ChunkCfg {
 };
 
 // Register split per warpgroup (setmaxnreg): output and conversion (warps 0-3),
-// softmax (4-7, 8-11), TMA and MMA (12, 13; two idle warps).
+// softmax (4-7, 8-11), K and Q, MMA, pieces and V (12 to 15).
 constexpr uint32_t kChunkOut = 48;
 constexpr uint32_t kChunkSoft = 192;
 constexpr uint32_t kChunkLow = 80;
 constexpr uint32_t kChunkLaunchRegs = 128;
 static_assert(kChunkOut + 2 * kChunkSoft + kChunkLow <= 4 * kChunkLaunchRegs, "register split exceeds the launch");
+constexpr int kWantPairs = 6;               // pairs of a piece that are left when the next one is chosen
 constexpr float kP2 = 7.f;                  // e4m3: P carries 2^7
 
 // kind::f16 with fp16 operands, kind::f8f6f4 with e4m3 ones: formats 0; A in
@@ -474,6 +481,9 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint
 // (mode 4): 8 rows are 512 bytes.
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
   return (sdesc_sw128(saddr, 16, 512) & ~(static_cast<uint64_t>(7) << 61)) | static_cast<uint64_t>(4) << 61;
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
                                             int c2) {
@@ -529,7 +539,7 @@ __global__ void __launch_bounds__(512, 1)
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kTmemSlotOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbortOff);
   volatile uint16_t* valid_ring = reinterpret_cast<volatile uint16_t*>(smem + C::kValidOff);
-  volatile uint32_t* raw_info = reinterpret_cast<volatile uint32_t*>(smem + C::kRawInfoOff);
+  volatile uint32_t* block_info = reinterpret_cast<volatile uint32_t*>(smem + C::kInfoOff);
   const float NEG_INF = -__int_as_float(0x7f800000);
 
   const int warp = static_cast<int>(warp_id());
@@ -541,16 +551,17 @@ __global__ void __launch_bounds__(512, 1)
     for (int s = 0; s < C::kStagesQ; ++s) {
       mbar_init(bar(C::kBarQFull + s), FP8 ? kTileM : 1);
       mbar_init(bar(C::kBarQEmpty + s), 1);
-      mbar_init(bar(C::kBarLand + s), 1);
     }
     for (int s = 0; s < C::kStagesK; ++s) {
       mbar_init(bar(C::kBarKFull + s), 1);
       mbar_init(bar(C::kBarKEmpty + s), 1);
     }
     for (int s = 0; s < C::kStagesV; ++s) {
-      mbar_init(bar(C::kBarVFull + s), FP8 ? kTileM : 1);
+      mbar_init(bar(C::kBarVFull + s), FP8 ? kTileM : 4);        // (bf16: a clean block's copy counts for four warps)
       mbar_init(bar(C::kBarVEmpty + s), 1);
     }
+    for (int s = 0; s < C::kLands; ++s) mbar_init(bar(C::kBarLand + s), 1);
+    for (int s = 0; s < C::kReqs; ++s) mbar_init(bar(C::kBarReq + s), 1);
     for (int s = 0; s < C::kStagesR; ++s) {
       mbar_init(bar(C::kBarRFull + s), 1);
       mbar_init(bar(C::kBarREmpty + s), kTileM);
@@ -559,7 +570,7 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(bar(C::kBarXch + s), 2 * 4 * 32);
       mbar_init(bar(C::kBarPvDone + s), 1);
       mbar_init(bar(C::kBarPieceFull + s), 1);
-      mbar_init(bar(C::kBarPieceEmpty + s), 1 + 2 * 4 + 4);      // MMA thread, softmax and output warps
+      mbar_init(bar(C::kBarPieceEmpty + s), 3 + 2 * 4 + 4);      // the warps that read it: K, V, MMA, softmax, output
     }
     mbar_init(bar(C::kBarSFull), 1);
     mbar_init(bar(C::kBarSFree), 2 * 4 * 32);
@@ -568,7 +579,7 @@ __global__ void __launch_bounds__(512, 1)
     mbar_init(bar(C::kBarOFull), 1);
     mbar_init(bar(C::kBarOEmpty), 4 * 32);
     mbar_init(bar(C::kBarLFull), 4 * 32);
-    mbar_init(bar(C::kBarMmaDone), 1);
+    mbar_init(bar(C::kBarWant), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -595,6 +606,7 @@ __global__ void __launch_bounds__(512, 1)
   auto piece_slot = [&](int i) { return reinterpret_cast<volatile Piece*>(smem + C::kPieceOff) + (i & 1); };
   auto read_piece = [&](int i, Piece& x) {
     const volatile Piece* src = piece_slot(i);
+    x.s = src->s;
     x.t0 = src->t0;
     x.p0 = src->p0;
     x.heads = src->heads;
@@ -607,14 +619,19 @@ __global__ void __launch_bounds__(512, 1)
 
   if (warp >= 12) {
     regs_set<kChunkLow, kChunkLaunchRegs>();
-    if (warp == 12) {
-      // =================== TMA producer (a whole warp) ===================
+    if (warp == 12 || warp == 15) {
+      // =================== TMA producers: K and Q (warp 12), V (warp 15) ===================
+      // Two warps, for V has no time to lose at d=128: with two stages a block can be
+      // asked for when the one two before it has been used, and is wanted 2200 cycles
+      // later.  What one warp had to do for K and V between that and the copy cost up
+      // to a third of everything (1024 tokens at 131071: 413 to 540 us).  So all that
+      // a copy needs is computed before the wait for its stage.
+      const bool is_v = warp == 15;
+      const CUtensorMap* map = is_v ? &tmV : &tmK;
       if (lane == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(map);
+        if (!is_v) tma_prefetch_desc(&tmQ);
       }
-      const int total = p.plan->pieces, total1 = p.plan->pieces1;
       const int page = 1 << p.page_log2;
       const int br = min(page, kTileN);                    // rows of a box
       const int subs = kTileN / br;                        // boxes of a block, a chunk of d each
@@ -623,75 +640,33 @@ __global__ void __launch_bounds__(512, 1)
       const int sub = lane / kAcross % subs;
       const int t_of = lane / kAcross / subs;              // block of the pair (2 and more: none)
       const uint32_t box_bytes = static_cast<uint32_t>(br) * (FP8 ? D : 128);
-      int ik = 0, iv = 0, ir = 0;    // K stages, V tiles, raw tiles filled (over all pieces)
-      int qn = 0, np = 0, pairs = 0, landed = 0;
+      int used = 0;                  // K stages, V tiles or raw tiles filled (over all pieces)
+      int qn = 0, np = 0, reqs = 0;
       auto wait = [&](int b, uint32_t parity) -> bool {
         return __all_sync(0xFFFFFFFFu, wait_bar(bar(b), parity, abort_flag, p.err));
       };
-
-      // The next piece that has keys; pieces without are seen to here.  The number
-      // of the one after it is asked for ahead of time (lane 0 has it).
-      int taken = static_cast<int>(blockIdx.x);
-      bool begun = false;
-      auto next_piece = [&](Work& x) -> bool {
-        while (true) {
-          const int index = begun ? static_cast<int>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, taken, 0) : taken;
-          if (index < 0 || index >= total) return false;
-          int s;
-          if (!begun) s = p.first[index];
-          else if (index < total1) s = find_seq(p.S, index, lane, [&](int i) { return p.seq[i].before1; });
-          else s = find_seq(p.S, index - total1, lane, [&](int i) { return p.seq[i].before2; });
-          begun = true;
-          if (lane == 0) taken = atomicAdd(&p.plan->next, 1);
-          const ChunkSeq q = p.seq[s];
-          const int in = index < total1 ? index - q.before1 : index - total1 - q.before2;
-          // tiles first (the last ones, which see most keys, lead), then parts, then heads
-          const int cut = in / q.nt % q.cuts;
-          const int hkv = in / q.nt / q.cuts;
-          const SeqRows r{q.a, q.b, q.n, q.shift, false};
-          const Tile t = seq_tile(r, q.nt - 1 - in % q.nt, p.tpt);
-          x.t0 = t.t0;
-          x.p0 = t.p0;
-          x.heads = hkv << 8 | t.ntok;
-          x.n = r.n;
-          x.kb = tile_blocks(p, t, r.n);
-          if (q.cuts > 1) x.kb = x.kb.part(cut, q.cuts);
-          x.slot = q.cuts > 1 ? q.slot0 + in : -1;
-          if (t.p0 < 0 && lane == 0) record_error(p.err, ATTN_ERR_BAD_PAGES);
-          x.s = s;
-          x.low = clamped(r.a + r.shift - p.window + 1, 0, r.n);
-          if (x.kb.count() > 0) return true;
-          if (x.slot >= 0) {                               // a part without keys
-            float* l = p.part + static_cast<size_t>(x.slot) * C::kPartFloats + kTileM * (D + 1);
-            for (int i = lane; i < kTileM; i += 32) l[i] = 0.f;
-          } else {                                         // rows that see nothing
-            for (int i = 0; i < x.ntok() * p.G; ++i) {
-              const size_t row = static_cast<size_t>(x.t0 + i / p.G) * p.H + x.hkv() * p.G + i % p.G;
-              for (int e = lane; e < D; e += 32) p.o[row * D + e] = __float2bfloat16(0.f);
-              if (lane == 0) p.lse[row] = NEG_INF;
-            }
-          }
-        }
-      };
-      // Hand a piece (or, with no key blocks, the end) to the other roles.
-      auto publish = [&](const Piece& x) -> bool {
-        if (np >= 2 && !wait(C::kBarPieceEmpty + (np & 1), ((np >> 1) & 1) ^ 1)) return false;
+      // bf16: V stage s has to be cleaned when it has landed (-1: no more of this piece)
+      auto request = [&](int s) {
         if (lane == 0) {
-          volatile Piece* dst = piece_slot(np);
-          dst->t0 = x.t0;
-          dst->p0 = x.p0;
-          dst->heads = x.heads;
-          dst->slot = x.slot;
-          dst->kb.nsb = x.kb.nsb;
-          dst->kb.wb0 = x.kb.wb0;
-          dst->kb.nwb = x.kb.nwb;
-          dst->kb.sb0 = x.kb.sb0;
-          mbar_arrive(bar(C::kBarPieceFull + (np & 1)));
+          reinterpret_cast<volatile int*>(smem + C::kReqOff)[reqs % max(1, C::kReqs)] = s;
+          mbar_arrive(bar(C::kBarReq + reqs % max(1, C::kReqs)));
         }
+        ++reqs;
+      };
+      // The next piece, with what the producers alone need of it; false at the end
+      // (or where the wait ran out).
+      auto next_piece = [&](Work& x) -> bool {
+        if (!wait(C::kBarPieceFull + (np & 1), (np >> 1) & 1)) return false;
+        read_piece(np, x);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarPieceEmpty + (np & 1)));
         ++np;
+        if (x.kb.count() == 0) return false;
+        const ChunkSeq* q = p.seq + x.s;
+        x.n = q->n;
+        x.low = clamped(q->a + q->shift - p.window + 1, 0, x.n);
         return true;
       };
-
       // This lane's box of a pair of key blocks: its page (-1: none is copied).
       struct Box {
         int page, key;               // page, first key
@@ -709,92 +684,55 @@ __global__ void __launch_bounds__(512, 1)
         }
         return b;
       };
-      auto check = [&](Box& b) {
-        if (b.page >= 0 && b.page < p.P) return;
-        b.page = -1;
-        if (b.seen) record_error(p.err, ATTN_ERR_BAD_PAGES);
-      };
-      auto groups = [&](const Box& b) -> uint32_t {        // of the pair's 16 groups of 16 keys, those with a page
-        const uint32_t g = b.page >= 0 ? ((1u << (br / 16)) - 1u) << (t_of * 8 + sub * (br / 16)) : 0u;
-        return __reduce_or_sync(0xFFFFFFFFu, g);
-      };
-      auto copy = [&](const CUtensorMap* map, uint32_t dst, int b, const Box& x, int hkv) {
-        tma_load_3d(dst, map, bar(b), c_of * 64, (hkv << p.page_log2) + (x.key & (page - 1)), x.page);
-      };
-      auto rows_of = [&](const Work& x, int k, int t, uint32_t ok) {
-        const int k0 = x.kb.at(2 * k + t) * kTileN;
-        return BlockRows{min(kTileN, x.n - k0), max(0, min(x.low - k0, kTileN)), max(0, min(p.sinks - k0, kTileN)),
-                         ok >> (8 * t) & 255u};
-      };
-      // e4m3: V's block t of a pair into the next raw tile
-      auto load_raw = [&](const CUtensorMap* map, const Work& x, int k, int t, const Box& b, uint32_t ok) -> bool {
-        const int s = ir % max(1, C::kStagesR);
-        if (ir >= C::kStagesR && !wait(C::kBarREmpty + s, ((ir / max(1, C::kStagesR)) & 1) ^ 1)) return false;
-        const bool mine = t_of == t && b.page >= 0;
-        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-        if (lane == 0) {
-          raw_info[s] = rows_of(x, k, t, ok).packed();
-          mbar_arrive_expect_tx(bar(C::kBarRFull + s), boxes * box_bytes);
-        }
-        __syncwarp();
-        if (mine) copy(map, sbase + C::kROff + s * C::kRawBytes + sub * br * D, C::kBarRFull + s, b, x.hkv());
-        ++ir;
-        return true;
-      };
-      auto load_k = [&](const Work& x, int k, Box& b) -> bool {
-        check(b);
-        const uint32_t ok = groups(b);
-        if (lane == 0) valid_ring[pairs % C::kRing] = static_cast<uint16_t>(ok);
-        ++pairs;
-        const int s = ik % C::kStagesK;
-        if (ik >= C::kStagesK && !wait(C::kBarKEmpty + s, ((ik / C::kStagesK) & 1) ^ 1)) return false;
-        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, b.page >= 0));
-        if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarKFull + s), boxes * box_bytes);
-        __syncwarp();
-        if (b.page >= 0) {
-          const uint32_t at = FP8 ? t_of * C::kRawBytes + sub * br * D
-                                  : (c_of * 2 + t_of) * C::kChunkBytes + sub * br * 128;
-          copy(&tmK, sbase + C::kKOff + s * C::kKBytes + at, C::kBarKFull + s, b, x.hkv());
-        }
-        ++ik;
-        return true;
-      };
-      auto load_v = [&](const Work& x, int k, const Box& b) -> bool {
-        const uint32_t ok = groups(b);
-        for (int t = 0; t < 2 && 2 * k + t < x.kb.count(); ++t) {
-          if constexpr (FP8) {
-            if (!load_raw(&tmV, x, k, t, b, ok)) return false;
-          } else {
-            const int s = iv % C::kStagesV;
-            if (iv >= C::kStagesV && !wait(C::kBarVEmpty + s, ((iv / C::kStagesV) & 1) ^ 1)) return false;
-            const uint32_t vs = sbase + C::kVOff + s * C::kTileBytes;
-            const BlockRows rows = rows_of(x, k, t, ok);
-            const bool clean = rows.all();
-            const int full = clean ? C::kBarVFull + s : C::kBarLand;
-            const bool mine = t_of == t && b.page >= 0;
-            const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-            if (lane == 0) mbar_arrive_expect_tx(bar(full), boxes * box_bytes);
-            __syncwarp();
-            if (mine) copy(&tmV, vs + c_of * C::kChunkBytes + sub * br * 128, full, b, x.hkv());
-            ++iv;
-            if (!clean) {
-              // (the next K and Q are on their way already)
-              ++landed;
-              if (!wait(C::kBarLand, (landed - 1) & 1)) return false;
-              const uint32_t held = (2u << ((rows.rows - 1) >> 4)) - 1u;
-              const bool tail = (rows.groups & held) == held && rows.low == 0;   // the last rows alone lack
-#pragma unroll 4
-              for (int r = (tail ? rows.rows & ~3 : 0) + (lane >> 3); r < kTileN; r += 4) {
-                if (rows.has(r)) continue;
-#pragma unroll
-                for (int c = 0; c < C::kChunks; ++c)
-                  sts128(vs + c * C::kChunkBytes + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(C::kBarVFull + s));
-            }
+      // The copies of a pair; `b` was fetched a pair before.
+      auto load = [&](const Work& x, int k, const Box& b) -> bool {
+        const bool mine = b.page >= 0 && b.page < p.P;
+        if (!mine && b.seen && !is_v) record_error(p.err, ATTN_ERR_BAD_PAGES);
+        // of the pair's 16 groups of 16 keys, those with a page
+        const uint32_t ok = __reduce_or_sync(
+            0xFFFFFFFFu, mine ? ((1u << (br / 16)) - 1u) << (t_of * 8 + sub * (br / 16)) : 0u);
+        const uint32_t boxes = __ballot_sync(0xFFFFFFFFu, mine);
+        const int row = (x.hkv() << p.page_log2) + (b.key & (page - 1));
+        if (!is_v) {
+          const int s = used % C::kStagesK;
+          const uint32_t at = sbase + C::kKOff + s * C::kKBytes +
+                              (FP8 ? t_of * C::kRawBytes + sub * br * D
+                                   : (c_of * 2 + t_of) * C::kChunkBytes + sub * br * 128);
+          const uint32_t bytes = __popc(boxes) * box_bytes;
+          if (used >= C::kStagesK && !wait(C::kBarKEmpty + s, ((used / C::kStagesK) & 1) ^ 1)) return false;
+          // (a box's bytes may count before they are expected: the arrival is one of them)
+          if (lane == 0) {
+            valid_ring[used % C::kRing] = static_cast<uint16_t>(ok);
+            mbar_arrive_expect_tx(bar(C::kBarKFull + s), bytes);
           }
+          if (mine) tma_load_3d(at, map, bar(C::kBarKFull + s), c_of * 64, row, b.page);
+          ++used;
+          return true;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (2 * k + t >= x.kb.count()) break;
+          const int k0 = x.kb.at(2 * k + t) * kTileN;
+          const BlockRows rows{min(kTileN, x.n - k0), max(0, min(x.low - k0, kTileN)),
+                               max(0, min(p.sinks - k0, kTileN)), ok >> (8 * t) & 255u};
+          constexpr int kStages = FP8 ? C::kStagesR : C::kStagesV;
+          const int s = used % kStages;
+          const bool clean = FP8 || rows.all();
+          const int full = (FP8 ? C::kBarRFull : clean ? C::kBarVFull : C::kBarLand) + s;
+          const int empty = (FP8 ? C::kBarREmpty : C::kBarVEmpty) + s;
+          const uint32_t at = sbase + (FP8 ? C::kROff + s * C::kRawBytes + sub * br * D
+                                           : C::kVOff + s * C::kTileBytes + c_of * C::kChunkBytes + sub * br * 128);
+          const bool go = mine && t_of == t;
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, go)) * box_bytes;
+          if (used >= kStages && !wait(empty, ((used / kStages) & 1) ^ 1)) return false;
+          if (lane == 0) {
+            block_info[s] = rows.packed();
+            mbar_arrive_expect_tx(bar(full), bytes);
+            if (!FP8 && clean) mbar_arrive_n(bar(full), 3);
+          }
+          if (go) tma_load_3d(at, map, bar(full), c_of * 64, row, b.page);
+          if (!clean) request(s);
+          ++used;
         }
         return true;
       };
@@ -815,62 +753,26 @@ __global__ void __launch_bounds__(512, 1)
         return true;
       };
 
-      Work x, y;
-      Box now{-1, 0, false}, first{-1, 0, false};
-      auto look_ahead = [&]() -> bool {
-        if (!next_piece(y)) return false;
-        first = fetch(y, 0);
-        return true;
-      };
-      bool more = look_ahead();
+      Work x;
       bool ok = true;
-      if (more) {
-        x = y;
-        now = first;
-        ok = publish(x) && load_k(x, 0, now) && load_q(x);
-      }
-      while (ok && more) {
+      while (ok && next_piece(x)) {
         const int ns = (x.kb.count() + 1) / 2;
-        Box then{-1, 0, false};
-        if (ns > 1) then = fetch(x, 1);
+        const bool q_first = !is_v && np == 1;             // (later ones wait for the piece before)
+        if (q_first) ok = load_q(x);
+        Box now = fetch(x, 0);
         for (int k = 0; k < ns && ok; ++k) {
-          // V of this pair goes after K of the next one
-          const Box cur = now;
-          if (k + 1 < ns) {
-            now = then;
-            if (k + 2 < ns) then = fetch(x, k + 2);
-            ok = load_k(x, k + 1, now);
-          } else {
-            if (ns == 1) more = look_ahead();
-            if (more) {
-              now = first;
-              ok = publish(y) && load_k(y, 0, now) && load_q(y);
-            } else {
-              y.kb = WindowBlocks{0, 0, 0, 0};
-              ok = publish(y);
-            }
-          }
-          ok = ok && load_v(x, k, cur);
-          // the next piece is looked up while there is something to compute
-          if (k == 0 && ns > 1 && ok) more = look_ahead();
+          if (!is_v && k == max(0, ns - kWantPairs) && lane == 0) mbar_arrive(bar(C::kBarWant));
+          const Box then = fetch(x, k + 1);
+          ok = load(x, k, now);
+          if (k == 0 && !is_v && !q_first && ok) ok = load_q(x);
+          now = then;
         }
-        x = y;
-      }
-      if (np == 0) {                          // nothing for this CTA: the others are told
-        x.kb = WindowBlocks{0, 0, 0, 0};
-        publish(x);
+        if (!FP8 && is_v) request(-1);
       }
       // every copy issued has landed before the CTA may exit
-      for (int j = max(0, ik - C::kStagesK); j < ik; ++j)
-        drain_bar(bar(C::kBarKFull + j % C::kStagesK), (j / C::kStagesK) & 1);
-      for (int j = max(0, iv - C::kStagesV); j < iv; ++j)
-        drain_bar(bar(C::kBarVFull + j % C::kStagesV), (j / C::kStagesV) & 1);
-      if constexpr (FP8) {
-        for (int j = max(0, ir - C::kStagesR); j < ir; ++j)
-          drain_bar(bar(C::kBarRFull + j % C::kStagesR), (j / C::kStagesR) & 1);
-      } else {
-        if (landed > 0) drain_bar(bar(C::kBarLand), (landed - 1) & 1);
-      }
+      const int stages = !is_v ? C::kStagesK : FP8 ? C::kStagesR : C::kStagesV;
+      const int full = !is_v ? C::kBarKFull : FP8 ? C::kBarRFull : C::kBarVFull;
+      for (int j = max(0, used - stages); j < used; ++j) drain_bar(bar(full + j % stages), (j / stages) & 1);
       for (int j = max(0, qn - C::kStagesQ); j < qn; ++j)
         drain_bar(bar((FP8 ? C::kBarLand : C::kBarQFull) + j % C::kStagesQ), (j / C::kStagesQ) & 1);
     } else if (warp == 13) {
@@ -984,9 +886,89 @@ __global__ void __launch_bounds__(512, 1)
           ++on;
           nb = nb2;
         }
-        // every MMA issued has completed before tensor memory is released
-        mma_commit(bar(C::kBarMmaDone));
-        drain_bar(bar(C::kBarMmaDone), 0);
+        // every MMA issued has completed before tensor memory is released (one phase
+        // more of a barrier that nobody waits for by now)
+        mma_commit(bar(C::kBarPvDone + 1));
+        drain_bar(bar(C::kBarPvDone + 1), pn & 1);
+      }
+    } else if (warp == 14) {
+      // =================== pieces (a whole warp) ===================
+      const int total = p.plan->pieces, total1 = p.plan->pieces1;
+      int np = 0;
+      // The next piece that has keys; pieces without are seen to here.
+      int taken = static_cast<int>(blockIdx.x);
+      bool begun = false;
+      auto next_piece = [&](Piece& x) -> bool {
+        while (true) {
+          if (begun && lane == 0) taken = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
+          const int index = __shfl_sync(0xFFFFFFFFu, taken, 0);
+          if (index < 0 || index >= total) return false;
+          int s;
+          if (!begun) s = p.first[index];
+          else if (index < total1) s = find_seq(p.S, index, lane, [&](int i) { return p.seq[i].before1; });
+          else s = find_seq(p.S, index - total1, lane, [&](int i) { return p.seq[i].before2; });
+          begun = true;
+          const ChunkSeq q = p.seq[s];
+          const int in = index < total1 ? index - q.before1 : index - total1 - q.before2;
+          // tiles first (the last ones, which see most keys, lead), then parts, then heads
+          const int cut = in / q.nt % q.cuts;
+          const int hkv = in / q.nt / q.cuts;
+          const SeqRows r{q.a, q.b, q.n, q.shift, false};
+          const Tile t = seq_tile(r, q.nt - 1 - in % q.nt, p.tpt);
+          x.s = s;
+          x.t0 = t.t0;
+          x.p0 = t.p0;
+          x.heads = hkv << 8 | t.ntok;
+          x.kb = tile_blocks(p, t, r.n);
+          if (q.cuts > 1) x.kb = x.kb.part(cut, q.cuts);
+          x.slot = q.cuts > 1 ? q.slot0 + in : -1;
+          if (t.p0 < 0 && lane == 0) record_error(p.err, ATTN_ERR_BAD_PAGES);
+          if (x.kb.count() > 0) return true;
+          if (x.slot >= 0) {                               // a part without keys
+            float* l = p.part + static_cast<size_t>(x.slot) * C::kPartFloats + kTileM * (D + 1);
+            for (int i = lane; i < kTileM; i += 32) l[i] = 0.f;
+          } else {                                         // rows that see nothing
+            for (int i = 0; i < x.ntok() * p.G; ++i) {
+              const size_t row = static_cast<size_t>(x.t0 + i / p.G) * p.H + x.hkv() * p.G + i % p.G;
+              for (int e = lane; e < D; e += 32) p.o[row * D + e] = __float2bfloat16(0.f);
+              if (lane == 0) p.lse[row] = NEG_INF;
+            }
+          }
+        }
+      };
+      // Hand a piece (or, with no key blocks, the end) to the other roles.
+      auto publish = [&](const Piece& x) -> bool {
+        if (np >= 2 && !__all_sync(0xFFFFFFFFu, wait_bar(bar(C::kBarPieceEmpty + (np & 1)), ((np >> 1) & 1) ^ 1,
+                                                         abort_flag, p.err)))
+          return false;
+        if (lane == 0) {
+          volatile Piece* dst = piece_slot(np);
+          dst->s = x.s;
+          dst->t0 = x.t0;
+          dst->p0 = x.p0;
+          dst->heads = x.heads;
+          dst->slot = x.slot;
+          dst->kb.nsb = x.kb.nsb;
+          dst->kb.wb0 = x.kb.wb0;
+          dst->kb.nwb = x.kb.nwb;
+          dst->kb.sb0 = x.kb.sb0;
+          mbar_arrive(bar(C::kBarPieceFull + (np & 1)));
+        }
+        ++np;
+        return true;
+      };
+
+      // A piece is chosen late, when few pairs of the one before it are left to be
+      // asked for: chosen a piece ahead, the last ones waited behind others while
+      // CTAs had nothing to do (1024 tokens at 131071: 557 us, so 4xx).
+      Piece x;
+      bool more = true;
+      while (more) {
+        if (np > 0 && !__all_sync(0xFFFFFFFFu, wait_bar_relaxed(bar(C::kBarWant), (np - 1) & 1, abort_flag, p.err)))
+          break;
+        more = next_piece(x);
+        if (!more) x.kb = WindowBlocks{0, 0, 0, 0};
+        if (!publish(x)) break;
       }
     }
   } else if (warp < 4) {
@@ -1049,8 +1031,32 @@ __global__ void __launch_bounds__(512, 1)
       return true;
     };
     if constexpr (!FP8) {
+      // V blocks with rows that no row of the sequence sees are handed on when those
+      // are zeros.  (A piece's first P V waits for these warps anyway: it overwrites
+      // the O that they read.)
+      uint32_t phases = 0;           // of the stages' landings
+      int reqs = 0;
+      auto clean = [&]() -> bool {
+        for (;; ++reqs) {
+          if (!wait(C::kBarReq + reqs % C::kReqs, (reqs / C::kReqs) & 1)) return false;
+          const int s = reinterpret_cast<volatile int*>(smem + C::kReqOff)[reqs % C::kReqs];
+          if (s < 0) break;
+          if (!wait(C::kBarLand + s, (phases >> s) & 1u)) return false;
+          phases ^= 1u << s;
+          if (!block_rows(block_info[s]).has(row)) {
+            const uint32_t at = sbase + C::kVOff + s * C::kTileBytes + row * 128;
+#pragma unroll
+            for (int u = 0; u < D / 8; ++u) sts128(at + (u >> 3) * C::kChunkBytes + (u & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBarVFull + s));
+        }
+        ++reqs;
+        return true;
+      };
       Piece x;
-      while (next_piece(x) && output(x)) {
+      while (next_piece(x) && clean() && output(x)) {
       }
     } else {
       int ir = 0, iv = 0, qn = 0;
@@ -1062,7 +1068,7 @@ __global__ void __launch_bounds__(512, 1)
         if (used && !wait(empty, parity)) return false;
         const uint32_t src = sbase + C::kROff + s * C::kRawBytes + row * D;
         const uint32_t to = dst + row * 128;
-        if (block_rows(raw_info[s]).has(row)) {
+        if (block_rows(block_info[s]).has(row)) {
 #pragma unroll
           for (int u0 = 0; u0 < D / 16; u0 += 4) {
             uint4 w[4];
@@ -1471,7 +1477,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const float* x = part + min(c0 + u, cuts - 1) * step + kTileM * D + row;
-        if (x[kTileM] != 0.f) m = fmaxf(m, x[0]);
+        const float mc = x[0], lc = x[kTileM];
+        m = lc != 0.f ? fmaxf(m, mc) : m;
       }
     }
     for (int c0 = 0; c0 < cuts; c0 += kBatch) {
@@ -1605,7 +1612,7 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, attn_fwd_paged_kernel<D, FP8>, tq, tk, tv, p)) != cudaSuccess) return e;
   if (p.slots == 0) return cudaSuccess;
-  cfg.gridDim = dim3(std::min(p.slots, 2 * sms), D / 16);
+  cfg.gridDim = dim3(std::min(p.slots / 2, 2 * sms), D / 16);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, FP8>, p);

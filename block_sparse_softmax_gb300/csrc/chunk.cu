@@ -699,15 +699,17 @@ __global__ void __launch_bounds__(512, 1)
                               (FP8 ? t_of * C::kRawBytes + sub * br * D
                                    : (c_of * 2 + t_of) * C::kChunkBytes + sub * br * 128);
           const uint32_t bytes = __popc(boxes) * box_bytes;
-          if (used >= C::kStagesK && !wait(C::kBarKEmpty + s, ((used / C::kStagesK) & 1) ^ 1)) return false;
-          // (a box's bytes may count before they are expected: the arrival is one of them)
+          const bool fine = used < C::kStagesK || wait_bar(bar(C::kBarKEmpty + s), ((used / C::kStagesK) & 1) ^ 1,
+                                                           abort_flag, p.err);
+          // the copies first; the warp agrees on the wait afterwards (bytes may arrive
+          // before they are expected: the phase waits for the arrival)
+          if (fine && mine) tma_load_3d(at, map, bar(C::kBarKFull + s), c_of * 64, row, b.page);
           if (lane == 0) {
             valid_ring[used % C::kRing] = static_cast<uint16_t>(ok);
             mbar_arrive_expect_tx(bar(C::kBarKFull + s), bytes);
           }
-          if (mine) tma_load_3d(at, map, bar(C::kBarKFull + s), c_of * 64, row, b.page);
           ++used;
-          return true;
+          return __all_sync(0xFFFFFFFFu, fine);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -724,15 +726,16 @@ __global__ void __launch_bounds__(512, 1)
                                            : C::kVOff + s * C::kTileBytes + c_of * C::kChunkBytes + sub * br * 128);
           const bool go = mine && t_of == t;
           const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, go)) * box_bytes;
-          if (used >= kStages && !wait(empty, ((used / kStages) & 1) ^ 1)) return false;
+          const bool fine = used < kStages || wait_bar(bar(empty), ((used / kStages) & 1) ^ 1, abort_flag, p.err);
+          if (fine && go) tma_load_3d(at, map, bar(full), c_of * 64, row, b.page);
           if (lane == 0) {
             block_info[s] = rows.packed();
             mbar_arrive_expect_tx(bar(full), bytes);
             if (!FP8 && clean) mbar_arrive_n(bar(full), 3);
           }
-          if (go) tma_load_3d(at, map, bar(full), c_of * 64, row, b.page);
-          if (!clean) request(s);
           ++used;
+          if (!__all_sync(0xFFFFFFFFu, fine)) return false;
+          if (!clean) request(s);
         }
         return true;
       };

@@ -14,10 +14,10 @@
 //     exact), then summed as an unevaluated pair of fp32 numbers by Knuth's
 //     two-sum, which leaves one rounding, the mean's own to fp32;
 //   * scores: in fp32 first, each off by at most
-//         e = (G + 16) 2^-24 sum_i A_i max_mi |mean_mi|,   A = sum_h |q_h|
-//     (G roundings of the group's sum at most, d / 32 of a lane's chain and 5 of
-//     the lanes' tree, of products whose absolute values add up to at most that
-//     sum).  The top_r-th largest of numbers that are off by e is off by e, so
+//         e = (G + r + 2) 2^-24 sum_i A_i max_mi |mean_mi|,   A = sum_h |q_h|
+//     (G roundings of the group's sum at most and r of a product's, on terms whose
+//     absolute values add up to at most that sum; r = d / 32 + 5 for a lane's chain
+//     and the tree over the lanes, d for one chain).  The top_r-th largest of numbers that are off by e is off by e, so
 //     what lies more than 2 e above it is taken and more than 2 e below is not;
 //     only what lies between (as a rule, that one page) is scored again, in 64
 //     bits.
@@ -169,6 +169,7 @@ struct SelectParams {
   int page_log2;
   int top, local, first, R;
   int parts;                // score CTAs along a row
+  int rounds;               // roundings of a score's sum
   float* score;             // [rows][Hkv][M]
   double* exact;            // [rows][Hkv][M], written where needed
   float* norm;              // [rows][Hkv][parts]: the largest |mean| element met
@@ -183,12 +184,14 @@ struct SelectRow {
   int n;                    // tokens, its own among them (0: none)
   int held;                 // pages they lie in
 };
-__device__ __forceinline__ SelectRow select_row(const SelectParams& p, int t) {
-  int lo = 0, hi = p.S;
-  while (lo < hi) {                           // the last s with cu[s] <= t
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.cu + mid) <= t) lo = mid;
-    else hi = mid - 1;
+__device__ __forceinline__ SelectRow select_row(const SelectParams& p, int t, int lane) {
+  int lo = 0, hi = p.S + 1;                   // the last s with cu[s] <= t, by a whole warp
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const uint32_t yes = __ballot_sync(0xFFFFFFFFu, lane == 0 || (i < hi && __ldg(p.cu + i) <= t));
+    lo += (31 - __clz(yes)) * step;
+    hi = min(hi, lo + step);
   }
   SelectRow r{-1, 0, 0};
   if (lo >= p.S || __ldg(p.cu + lo) > t) return r;
@@ -211,111 +214,190 @@ __device__ __forceinline__ float larger_or_nan(float a, float b) { return b > a 
 constexpr int kScoreWarps = 4;
 constexpr int kScorePages = 8;                // pages of a warp's turn
 
-// RT rows (consecutive, scored together where they belong to one sequence) and
-// a K/V head: CTA x of `parts` takes every parts-th group of pages.
-template <int D, int RT>
+// Row by row (a token a sequence): bound by reading the means.  CTA x of `parts`
+// takes every parts-th group of pages, a warp 8 at a time, a row of means a load.
+template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) select_score_kernel(const SelectParams p) {
   constexpr int E = D / 32;                   // elements a lane
-  __shared__ float qsum[RT][D];
-  __shared__ float top[kScoreWarps][RT];
+  __shared__ float top[kScoreWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = static_cast<int>(threadIdx.x);
+  const int warp = tid >> 5, lane = tid & 31;
+  const int r = static_cast<int>(blockIdx.y), h = static_cast<int>(blockIdx.z);
+  const int t = p.t0 + r;
+  float q[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) q[e] = 0.f;
+  const __nv_bfloat16* src = p.q + t * p.q_stride + static_cast<long long>(h) * p.G * D + lane * E;
+  for (int g = 0; g < p.G; ++g, src += D) {
+    if constexpr (E == 4) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+      q[0] += bf16lo(x.x), q[1] += bf16hi(x.x), q[2] += bf16lo(x.y), q[3] += bf16hi(x.y);
+    } else {
+      const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(src));
+      q[0] += bf16lo(x), q[1] += bf16hi(x);
+    }
+  }
+  const SelectRow row = select_row(p, t, lane);
+  const int end = row.s < 0 ? 0 : scored_end(p, row);
+  const int* tab = p.table + static_cast<size_t>(max(row.s, 0)) * p.M;
+  float* score = p.score + (static_cast<size_t>(r) * p.Hkv + h) * p.M;
+  float most = 0.f;
+  for (long long g = static_cast<long long>(blockIdx.x) * kScoreWarps + warp; p.first + g * kScorePages < end;
+       g += static_cast<long long>(p.parts) * kScoreWarps) {
+    const int m0 = p.first + static_cast<int>(g) * kScorePages;
+    int pg = lane < kScorePages && m0 + lane < end ? __ldg(tab + m0 + lane) : -1;
+    if (pg >= p.P || pg < -1) {
+      record_error(p.err, ATTN_ERR_BAD_PAGES);
+      pg = -1;
+    }
+    float v[kScorePages][E];
+#pragma unroll
+    for (int u = 0; u < kScorePages; ++u) {
+      const int x = __shfl_sync(0xFFFFFFFFu, pg, u);
+      const float* from = p.means + (static_cast<size_t>(max(x, 0)) * p.Hkv + h) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+      if (x >= 0) {
+        if constexpr (E == 4) {
+          const float4 y = __ldg(reinterpret_cast<const float4*>(from));
+          v[u][0] = y.x, v[u][1] = y.y, v[u][2] = y.z, v[u][3] = y.w;
+        } else {
+          const float2 y = __ldg(reinterpret_cast<const float2*>(from));
+          v[u][0] = y.x, v[u][1] = y.y;
+        }
+      }
+    }
+    float mine = 0.f;
+#pragma unroll
+    for (int u = 0; u < kScorePages; ++u) {
+      float d = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        most = larger_or_nan(most, fabsf(v[u][e]));
+        d = fmaf(q[e], v[u][e], d);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+      if (lane == u) mine = d;
+    }
+    if (lane < kScorePages && m0 + lane < end) score[m0 + lane] = mine;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = larger_or_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  if (lane == 0) top[warp] = most;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kScoreWarps; ++w) most = larger_or_nan(most, top[w]);
+    p.norm[(static_cast<size_t>(r) * p.Hkv + h) * p.parts + blockIdx.x] = most;
+  }
+}
+
+// Chunks: 16 rows share the means of 128 pages of their sequence in shared memory
+// (read from L2 once for 16 rows), a thread a page: a dot product is a chain of d
+// fused multiply-adds in four interleaved parts.  With a warp a page and sums over
+// its lanes, 8 rows at a time, 500 rows of 1024 pages took 142 us.
+constexpr int kTileRows = 16;
+constexpr int kTilePages = 128;
+template <int D>
+struct ScoreTile {
+  static constexpr int kRow = D + 4;          // floats from page to page: 16 bytes of 8 pages hit 8 different banks
+  static constexpr int kSmem = (kTilePages * kRow + kTileRows * D) * 4;
+};
+template <int D>
+__global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const SelectParams p) {
+  using C = ScoreTile<D>;
+  extern __shared__ __align__(16) float score_smem[];
+  float* means = score_smem;                  // [pages][kRow]
+  float* qsum = score_smem + kTilePages * C::kRow;             // [rows][D]
+  __shared__ int row_s[kTileRows], row_end[kTileRows];
+  __shared__ float top[kTilePages / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
   const int h = static_cast<int>(blockIdx.z);
-  const int r0 = static_cast<int>(blockIdx.y) * RT;
-  const int nr = min(RT, p.rows - r0);
-  for (int i = tid; i < RT * D; i += kScoreWarps * 32) {
+  const int r0 = static_cast<int>(blockIdx.y) * kTileRows;
+  const int nr = min(kTileRows, p.rows - r0);
+  for (int r = warp; r < kTileRows; r += kTilePages / 32) {
+    SelectRow row{-1, 0, 0};
+    if (r < nr) row = select_row(p, p.t0 + r0 + r, lane);
+    if (lane == 0) {
+      row_s[r] = row.s;
+      row_end[r] = row.s < 0 ? 0 : scored_end(p, row);
+    }
+  }
+  for (int i = tid; i < kTileRows * D; i += kTilePages) {
     const int r = i / D, e = i % D;
     float sum = 0.f;
     if (r < nr) {
       const __nv_bfloat16* q = p.q + (p.t0 + r0 + r) * p.q_stride + static_cast<long long>(h) * p.G * D + e;
       for (int g = 0; g < p.G; ++g) sum += __bfloat162float(q[static_cast<long long>(g) * D]);
     }
-    qsum[r][e] = sum;
+    qsum[i] = sum;
   }
   __syncthreads();
-  float most[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) most[r] = 0.f;
+  float seen = 0.f;                           // the largest element met, for any of the rows
   for (int a = 0; a < nr;) {                  // runs of rows of one sequence
-    const SelectRow row = select_row(p, p.t0 + r0 + a);
-    int b = a + 1;
-    SelectRow last = row;
-    while (b < nr) {
-      const SelectRow x = select_row(p, p.t0 + r0 + b);
-      if (x.s != row.s) break;
-      last = x;
-      ++b;
-    }
-    // the run's last row sees the most
-    const int end = row.s < 0 ? 0 : scored_end(p, last);
-    float q[RT][E];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int e = 0; e < E; ++e) q[r][e] = r >= a && r < b ? qsum[r][lane * E + e] : 0.f;
-    const int* tab = p.table + static_cast<size_t>(max(row.s, 0)) * p.M;
-    for (long long g = static_cast<long long>(blockIdx.x) * kScoreWarps + warp; p.first + g * kScorePages < end;
-         g += static_cast<long long>(p.parts) * kScoreWarps) {
-      const int m0 = p.first + static_cast<int>(g) * kScorePages;
-      int pg = lane < kScorePages && m0 + lane < end ? __ldg(tab + m0 + lane) : -1;
+    const int s = row_s[a];
+    int b = a + 1, end = row_end[a];
+    while (b < nr && row_s[b] == s) end = max(end, row_end[b++]);
+    const int* tab = p.table + static_cast<size_t>(max(s, 0)) * p.M;
+    for (long long m1 = p.first + static_cast<long long>(blockIdx.x) * kTilePages; s >= 0 && m1 < end;
+         m1 += static_cast<long long>(p.parts) * kTilePages) {
+      const int m0 = static_cast<int>(m1);
+      int pg = m0 + tid < end ? __ldg(tab + m0 + tid) : -1;
       if (pg >= p.P || pg < -1) {
         record_error(p.err, ATTN_ERR_BAD_PAGES);
         pg = -1;
       }
-      float v[kScorePages][E];
+      __syncthreads();                        // the tile before has been read
+      // a warp its 32 pages, 8 rows of means in flight
+#pragma unroll 1
+      for (int u0 = 0; u0 < 32; u0 += 8) {
+        float4 v[8];
 #pragma unroll
-      for (int u = 0; u < kScorePages; ++u) {
-        const int x = __shfl_sync(0xFFFFFFFFu, pg, u);
-        if (x >= 0) {
-          const float* src = p.means + (static_cast<size_t>(x) * p.Hkv + h) * D + lane * E;
-          if constexpr (E == 4) {
-            const float4 y = __ldg(reinterpret_cast<const float4*>(src));
-            v[u][0] = y.x, v[u][1] = y.y, v[u][2] = y.z, v[u][3] = y.w;
-          } else {
-            const float2 y = __ldg(reinterpret_cast<const float2*>(src));
-            v[u][0] = y.x, v[u][1] = y.y;
-          }
-        } else {
+        for (int u = 0; u < 8; ++u) {
+          const int x = __shfl_sync(0xFFFFFFFFu, pg, u0 + u);
+          const float* from = p.means + (static_cast<size_t>(max(x, 0)) * p.Hkv + h) * D + lane * 4;
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (x >= 0 && lane * 4 < D) v[u] = __ldg(reinterpret_cast<const float4*>(from));
+        }
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+        for (int u = 0; u < 8; ++u) {
+          seen = larger_or_nan(larger_or_nan(seen, fabsf(v[u].x)), fabsf(v[u].y));
+          seen = larger_or_nan(larger_or_nan(seen, fabsf(v[u].z)), fabsf(v[u].w));
+          if (lane * 4 < D)
+            *reinterpret_cast<float4*>(means + (warp * 32 + u0 + u) * C::kRow + lane * 4) = v[u];
         }
       }
-      float norm = 0.f;
+      __syncthreads();
+      float acc[kTileRows];
 #pragma unroll
-      for (int u = 0; u < kScorePages; ++u) {
+      for (int r = 0; r < kTileRows; ++r) acc[r] = 0.f;
+#pragma unroll 2
+      for (int e = 0; e < D; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(means + tid * C::kRow + e);
 #pragma unroll
-        for (int e = 0; e < E; ++e) norm = larger_or_nan(norm, fabsf(v[u][e]));
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (r < a || r >= b) continue;
-        most[r] = larger_or_nan(most[r], norm);
-        float mine = 0.f;
-#pragma unroll
-        for (int u = 0; u < kScorePages; ++u) {
-          float d = 0.f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) d = fmaf(q[r][e], v[u][e], d);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-          if (lane == u) mine = d;
+        for (int r = 0; r < kTileRows; ++r) {
+          const float4 q = *reinterpret_cast<const float4*>(qsum + r * D + e);
+          acc[r] = fmaf(q.x, v.x, fmaf(q.y, v.y, fmaf(q.z, v.z, fmaf(q.w, v.w, acc[r]))));
         }
-        if (lane < kScorePages && m0 + lane < end)
-          p.score[(static_cast<size_t>(r0 + r) * p.Hkv + h) * p.M + m0 + lane] = mine;
+      }
+      if (m0 + tid < end) {
+#pragma unroll
+        for (int r = 0; r < kTileRows; ++r)
+          if (r >= a && r < b) p.score[(static_cast<size_t>(r0 + r) * p.Hkv + h) * p.M + m0 + tid] = acc[r];
       }
     }
     a = b;
   }
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most[r] = larger_or_nan(most[r], __shfl_xor_sync(0xFFFFFFFFu, most[r], o));
-    if (lane == 0) top[warp][r] = most[r];
-  }
+  for (int o = 16; o > 0; o >>= 1) seen = larger_or_nan(seen, __shfl_xor_sync(0xFFFFFFFFu, seen, o));
+  if (lane == 0) top[warp] = seen;
   __syncthreads();
   if (tid < nr) {
     float x = 0.f;
-    for (int w = 0; w < kScoreWarps; ++w) x = larger_or_nan(x, top[w][tid]);
+    for (int w = 0; w < kTilePages / 32; ++w) x = larger_or_nan(x, top[w]);
     p.norm[(static_cast<size_t>(r0 + tid) * p.Hkv + h) * p.parts + blockIdx.x] = x;
   }
 }
@@ -323,9 +405,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) select_score_kernel(const Se
 // ----------------------------------------------------------------------------
 // the pick
 // ----------------------------------------------------------------------------
-// Numbers in an order of whole ones; a NaN comes last, below every other.
+// Numbers in an order of whole ones; a NaN comes last, below every other (0 is for
+// no number at all).
 __device__ __forceinline__ uint32_t order_of(float x) {
-  if (x != x) return 0u;
+  if (x != x) return 1u;
   const uint32_t b = __float_as_uint(x + 0.f);          // -0 as 0
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
@@ -335,7 +418,7 @@ __device__ __forceinline__ unsigned long long order_of(double x) {
   return b >> 63 ? ~b : b | (1ull << 63);
 }
 __device__ __forceinline__ float value_of(uint32_t k) {
-  return k == 0u ? __int_as_float(0x7fffffff) : __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+  return k <= 1u ? __int_as_float(0x7fffffff) : __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
 constexpr int kPickThreads = 256;
@@ -393,15 +476,31 @@ __device__ K nth_largest(int lo, int hi, int want, const In& in, const Key& key,
 template <int D>
 __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectParams p) {
   extern __shared__ uint32_t keys[];                     // [M], then a bit for each slot taken
-  __shared__ int hist[256];
+  __shared__ __align__(16) int hist[256];
   __shared__ int sums[kPickThreads / 32];
   __shared__ float fsums[2][kPickThreads / 32];
   __shared__ double qd[D];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
   const int r = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y);
   const int t = p.t0 + r;
-  const SelectRow row = select_row(p, t);
+  // what does not need the scores comes before the wait for them: A = sum_h |q_h|
+  // and the group's sum, the table
+  float a1 = 0.f, mn = 0.f;
+  for (int e = tid; e < D; e += kPickThreads) {
+    float a = 0.f;
+    double x = 0.0;
+    const __nv_bfloat16* q = p.q + t * p.q_stride + static_cast<long long>(h) * p.G * D + e;
+    for (int g = 0; g < p.G; ++g) {
+      const float y = __bfloat162float(q[static_cast<long long>(g) * D]);
+      a += fabsf(y);
+      x += static_cast<double>(y);
+    }
+    a1 += a;
+    qd[e] = x;
+  }
+  const SelectRow row = select_row(p, t, lane);
   int* out = p.pages + (static_cast<size_t>(t) * p.Hkv + h) * p.R;
   if (row.n == 0) {                                      // nobody's row (-1), or one that sees nothing
     for (int i = tid; i < p.R; i += kPickThreads) out[i] = -1;
@@ -423,35 +522,22 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
   double* exact = p.exact + at * p.M;
   uint32_t* taken = keys + p.M;
   const int words = (row.held + 31) / 32;
-  auto held_page = [&](int m) {
-    const int pg = __ldg(tab + m);
-    return pg >= 0 && pg < p.P;
-  };
-
-  // the candidates' keys (0 for those without a page, as for a NaN: told apart by `held_page`)
+  // a warp a word: what is taken anyway; the candidates are marked (1: a page, 0: none)
   int mine = 0;
-  for (int m = begin + tid; m < end; m += kPickThreads) {
-    const bool is = held_page(m);
-    keys[m] = is ? order_of(score[m]) : 0u;
-    mine += is;
+  for (int w = warp; w < words; w += kPickThreads / 32) {
+    const int m = 32 * w + lane;
+    const int pg = m < row.held ? __ldg(tab + m) : -1;
+    const bool is = pg >= 0 && pg < p.P, scored = m >= begin && m < end;
+    if (!is && pg != -1 && !scored) record_error(p.err, ATTN_ERR_BAD_PAGES);
+    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, is && !scored);
+    if (lane == 0) taken[w] = bits;
+    if (scored) keys[m] = is ? 1u : 0u;
+    mine += is && scored;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // the scores are there
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
   if (lane == 0) sums[warp] = mine;
-  // the sum of A = sum_h |q_h| and the largest mean, for the bound
-  float a1 = 0.f, mn = 0.f;
-  for (int e = tid; e < D; e += kPickThreads) {
-    float a = 0.f;
-    double x = 0.0;
-    const __nv_bfloat16* q = p.q + t * p.q_stride + static_cast<long long>(h) * p.G * D + e;
-    for (int g = 0; g < p.G; ++g) {
-      const float y = __bfloat162float(q[static_cast<long long>(g) * D]);
-      a += fabsf(y);
-      x += static_cast<double>(y);
-    }
-    a1 += a;
-    qd[e] = x;
-  }
   for (int i = tid; i < p.parts; i += kPickThreads) mn = larger_or_nan(mn, p.norm[at * p.parts + i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -462,18 +548,6 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
     fsums[0][warp] = a1;
     fsums[1][warp] = mn;
   }
-  for (int w = tid; w < words; w += kPickThreads) {      // what is taken anyway
-    uint32_t bits = 0u;
-    for (int i = 0; i < 32; ++i) {
-      const int m = 32 * w + i;
-      if (m < row.held && (m < begin || m >= end)) {
-        const int pg = __ldg(tab + m);
-        if (pg >= 0 && pg < p.P) bits |= 1u << i;
-        else if (pg != -1) record_error(p.err, ATTN_ERR_BAD_PAGES);
-      }
-    }
-    taken[w] = bits;
-  }
   __syncthreads();
   int nc = 0;
   a1 = mn = 0.f;
@@ -482,7 +556,20 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
     a1 += fsums[0][w];
     mn = larger_or_nan(mn, fsums[1][w]);
   }
+  if (nc > p.top && p.top > 0)
+    for (int m = begin + tid; m < end; m += kPickThreads)
+      if (keys[m] != 0u) keys[m] = order_of(score[m]);
   __syncthreads();
+  auto held_page = [&](int m) { return keys[m] != 0u; };
+  // slot m's score in 64 bits, by a warp
+  auto score_again = [&](int m) {
+    const float* src = p.means + (static_cast<size_t>(__ldg(tab + m)) * p.Hkv + h) * D;
+    double d = 0.0;
+    for (int e = lane; e < D; e += 32) d = fma(qd[e], static_cast<double>(__ldg(src + e)), d);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+    return d;
+  };
   auto take = [&](int m) { atomicOr(taken + (m >> 5), 1u << (m & 31)); };
   if (nc <= p.top) {
     for (int m = begin + tid; m < end; m += kPickThreads)
@@ -493,7 +580,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
                                                &larger, hist);
     const float tval = value_of(kth);
     // (1 % and the smallest normal number cover this product's own roundings)
-    const float e2 = 2.02f * static_cast<float>(p.G + 16) * 5.9604645e-8f * a1 * mn + 1.17549435e-38f;
+    const float e2 = 2.02f * static_cast<float>(p.G + p.rounds + 2) * 5.9604645e-8f * a1 * mn + 1.17549435e-38f;
     const float hi = tval + e2, lo = tval - e2;          // a NaN or infinity in either: all are undecided
     const bool clear = isfinite(hi) && isfinite(lo);
     int sure = 0, open = 0;
@@ -530,17 +617,36 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
     if (open <= want) {
       for (int m = begin + tid; m < end; m += kPickThreads)
         if (is_open(m)) take(m);
+    } else if (want > 0 && open <= 32) {
+      // scored again, a warp an open page, and ranked by one warp
+      if (tid == 0) sums[0] = 0;
+      __syncthreads();
+      for (int m = begin + tid; m < end; m += kPickThreads)
+        if (is_open(m)) hist[atomicAdd(sums, 1)] = m;
+      __syncthreads();
+      double* again = reinterpret_cast<double*>(hist + 32);
+      for (int i = warp; i < open; i += kPickThreads / 32) {
+        const double d = score_again(hist[i]);
+        if (lane == 0) again[i] = d;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        const int m = lane < open ? hist[lane] : 0;
+        const unsigned long long k = lane < open ? order_of(again[lane]) : 0ull;
+        int better = 0;
+        for (int i = 0; i < open; ++i) {
+          const unsigned long long k2 = __shfl_sync(0xFFFFFFFFu, k, i);
+          const int m2 = __shfl_sync(0xFFFFFFFFu, m, i);
+          better += k2 > k || (k2 == k && m2 < m);
+        }
+        if (lane < open && better < want) take(m);
+      }
     } else if (want > 0) {
-      // scored again: a warp an open page
       for (int m0 = begin + warp * 32; m0 < end; m0 += kPickThreads) {
         uint32_t todo = __ballot_sync(0xFFFFFFFFu, m0 + lane < end && is_open(m0 + lane));
         for (; todo != 0u; todo &= todo - 1) {
           const int m = m0 + __ffs(todo) - 1;
-          const float* src = p.means + (static_cast<size_t>(__ldg(tab + m)) * p.Hkv + h) * D;
-          double d = 0.0;
-          for (int e = lane; e < D; e += 32) d = fma(qd[e], static_cast<double>(__ldg(src + e)), d);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+          const double d = score_again(m);
           if (lane == 0) exact[m] = d;
         }
       }
@@ -595,7 +701,8 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
   for (int i = base + tid; i < p.R; i += kPickThreads) out[i] = -1;
   if (tid == 0 && h == 0) {
     // every page listed is whole, but for the row's own
-    const bool own = held_page(row.held - 1);
+    const int last = __ldg(tab + row.held - 1);
+    const bool own = last >= 0 && last < p.P;
     if (!own) record_error(p.err, ATTN_ERR_BAD_PAGES);
     p.out_lens[t] = own ? ((base - 1) << p.page_log2) + row.n - ((row.held - 1) << p.page_log2)
                         : base << p.page_log2;
@@ -603,7 +710,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
 }
 
 // Rows scored together: a chunk's share their sequence's means.
-int score_rows(int T, int S) { return T >= 4ll * S ? 8 : 1; }
+int score_rows(int T, int S) { return T >= 4ll * S ? kTileRows : 1; }
 // Rows of a launch: at most 2^26 scores (768 MB with the second ones), and a grid's 65535.
 long long select_chunk(int T, int Hkv, int M) {
   const long long rows = (1ll << 26) / (static_cast<long long>(Hkv) * M) / 8 * 8;
@@ -611,7 +718,8 @@ long long select_chunk(int T, int Hkv, int M) {
 }
 int score_parts(long long rows, int RT, int Hkv, int M) {
   const long long tiles = (rows + RT - 1) / RT * Hkv;
-  const long long most = (M + kScoreWarps * kScorePages - 1) / (kScoreWarps * kScorePages);
+  const int pages = RT == 1 ? kScoreWarps * kScorePages : kTilePages;
+  const long long most = (M + pages - 1) / pages;
   return static_cast<int>(std::max<long long>(1, std::min<long long>(most, 152ll * 16 / tiles)));
 }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -647,6 +755,9 @@ cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
     e = cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMaxSelectPages * 4 + kMaxSelectPages / 8);
     if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(select_score_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ScoreTile<D>::kSmem);
+    if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
   const int chunk = static_cast<int>(select_chunk(p.T, p.Hkv, p.M));
@@ -654,11 +765,21 @@ cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
     p.t0 = t0;
     p.rows = std::min(chunk, p.T - t0);
     const dim3 grid(p.parts, (p.rows + RT - 1) / RT, p.Hkv);
-    if (RT == 1) select_score_kernel<D, 1><<<grid, kScoreWarps * 32, 0, st>>>(p);
-    else select_score_kernel<D, 8><<<grid, kScoreWarps * 32, 0, st>>>(p);
+    if (RT == 1) select_score_kernel<D><<<grid, kScoreWarps * 32, 0, st>>>(p);
+    else select_score_tile_kernel<D><<<grid, kTilePages, ScoreTile<D>::kSmem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    pick<<<dim3(p.rows, p.Hkv), kPickThreads, smem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // the pick is set up while the scores are made, and waits for them itself
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.rows, p.Hkv);
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, pick, p)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -769,6 +890,7 @@ extern "C" attn_status_t attn_select_pages(const void* q, int64_t q_stride, cons
   const long long rows = select_chunk(T, H_kv, max_pages);
   const int RT = score_rows(T, S);
   p.parts = score_parts(rows, RT, H_kv, max_pages);
+  p.rounds = RT == 1 ? d / 32 + 5 : d;
   const size_t slots = static_cast<size_t>(rows) * H_kv;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.score = reinterpret_cast<float*>(ws);

@@ -436,18 +436,20 @@ def test_every_page_selected_is_decoding(bss):
     assert (lse - ld[[0, 1, 3]]).abs().max() <= 1e-5
 
 
-def test_ties_and_near_ties(bss):
+@pytest.mark.parametrize("rows,n", [(3, 40), (70, 40), (2, 300), (20, 300)])
+def test_ties_and_near_ties(bss, rows, n):
     """Equal scores go to the lower place; scores that 32 bits cannot tell apart are told apart."""
-    page, d, n = 16, 128, 40
-    g = torch.Generator("cuda").manual_seed(1)
+    page, d = 16, 128
+    g = torch.Generator("cuda").manual_seed(rows + n)
     table = torch.randperm(n, generator=g, device="cuda").int()[None]
     base = torch.randn(1, d, generator=g, device="cuda")
     means = base.repeat(n, 1)[:, None].contiguous()                  # all alike
-    q = torch.randn(3, 4, d, generator=g, device="cuda").bfloat16()
-    args = ([n * page], [0, 3], [3])
+    q = torch.randn(rows, 4, d, generator=g, device="cuda").bfloat16()
+    # the first token of the last page and those after it, or before it
+    args = ([n * page - 15 + rows % 16], [0, rows], [rows])
     pages, _ = select_and_check(bss, q, means, table, *args, 5, page, 1, 0)
-    assert torch.equal(pages[0, 0], table[0, [0, 1, 2, 3, 4, n - 1]])
-    for step in (2.0 ** -23, 2.0 ** -22, 2.0 ** -18):
+    assert torch.equal(pages[-1, 0], table[0, [0, 1, 2, 3, 4, n - 1]])
+    for step in (2.0 ** -23, 2.0 ** -22, 2.0 ** -18, 2.0 ** -12):
         # one element of each differs by a few units of its last place: sums that round alike
         near = means.clone()
         units = torch.randint(-3, 4, (n,), generator=g, device="cuda")

@@ -405,34 +405,23 @@ __global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const Sel
 // ----------------------------------------------------------------------------
 // the pick
 // ----------------------------------------------------------------------------
-// Numbers in an order of whole ones; a NaN comes last, below every other (0 is for
-// no number at all).
-__device__ __forceinline__ uint32_t order_of(float x) {
-  if (x != x) return 1u;
-  const uint32_t b = __float_as_uint(x + 0.f);          // -0 as 0
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
+// Numbers in an order of whole ones; a NaN comes last, below every other.
 __device__ __forceinline__ unsigned long long order_of(double x) {
   if (x != x) return 0ull;
   const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
   return b >> 63 ? ~b : b | (1ull << 63);
 }
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return k <= 1u ? __int_as_float(0x7fffffff) : __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-}
-
-constexpr int kPickThreads = 256;
-
-// The want-th largest (want >= 1) of the keys key(i), i in [lo, hi), of those that
-// in(i) admits, and how many are larger: eight bits a turn, from the top.
-template <class K, class In, class Key>
-__device__ K nth_largest(int lo, int hi, int want, const In& in, const Key& key, int* larger, int* hist) {
+// The want-th largest (want >= 1) of the keys key(i) of `bits` bits, i in [lo, hi),
+// of those that in(i) admits, and how many are larger: eight bits a turn, from the
+// top.
+template <int NT, class K, class In, class Key>
+__device__ K nth_largest(int bits, int lo, int hi, int want, const In& in, const Key& key, int* larger, int* hist) {
   K prefix = 0, mask = 0;
   int above = 0;
-  for (int shift = static_cast<int>(sizeof(K)) * 8 - 8; shift >= 0; shift -= 8) {
-    for (int i = static_cast<int>(threadIdx.x); i < 256; i += kPickThreads) hist[i] = 0;
+  for (int shift = bits - 8; shift >= 0; shift -= 8) {
+    for (int i = static_cast<int>(threadIdx.x); i < 256; i += NT) hist[i] = 0;
     __syncthreads();
-    for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += kPickThreads) {
+    for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += NT) {
       if (!in(i)) continue;
       const K k = key(i);
       if ((k & mask) == prefix) atomicAdd(hist + static_cast<int>((k >> shift) & 255), 1);
@@ -472,13 +461,15 @@ __device__ K nth_largest(int lo, int hi, int want, const In& in, const Key& key,
   return prefix;
 }
 
+constexpr uint32_t kNoScore = 0xFFFFFFFFu;               // (a NaN that no sum gives)
+
 // A CTA a row and K/V head.
-template <int D>
-__global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectParams p) {
+template <int D, int NT>
+__global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
   extern __shared__ uint32_t keys[];                     // [M], then a bit for each slot taken
   __shared__ __align__(16) int hist[256];
-  __shared__ int sums[kPickThreads / 32];
-  __shared__ float fsums[2][kPickThreads / 32];
+  __shared__ int sums[NT / 32];
+  __shared__ float fsums[2][NT / 32], range[2][NT / 32];
   __shared__ double qd[D];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x);
@@ -488,7 +479,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
   // what does not need the scores comes before the wait for them: A = sum_h |q_h|
   // and the group's sum, the table
   float a1 = 0.f, mn = 0.f;
-  for (int e = tid; e < D; e += kPickThreads) {
+  for (int e = tid; e < D; e += NT) {
     float a = 0.f;
     double x = 0.0;
     const __nv_bfloat16* q = p.q + t * p.q_stride + static_cast<long long>(h) * p.G * D + e;
@@ -503,7 +494,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
   const SelectRow row = select_row(p, t, lane);
   int* out = p.pages + (static_cast<size_t>(t) * p.Hkv + h) * p.R;
   if (row.n == 0) {                                      // nobody's row (-1), or one that sees nothing
-    for (int i = tid; i < p.R; i += kPickThreads) out[i] = -1;
+    for (int i = tid; i < p.R; i += NT) out[i] = -1;
     if (tid == 0 && h == 0) {
       p.out_lens[t] = row.s < 0 ? -1 : 0;
       if (row.s >= 0) record_error(p.err, ATTN_ERR_BAD_PAGES);        // fewer tokens than new ones
@@ -524,7 +515,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
   const int words = (row.held + 31) / 32;
   // a warp a word: what is taken anyway; the candidates are marked (1: a page, 0: none)
   int mine = 0;
-  for (int w = warp; w < words; w += kPickThreads / 32) {
+  for (int w = warp; w < words; w += NT / 32) {
     const int m = 32 * w + lane;
     const int pg = m < row.held ? __ldg(tab + m) : -1;
     const bool is = pg >= 0 && pg < p.P, scored = m >= begin && m < end;
@@ -538,7 +529,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
   if (lane == 0) sums[warp] = mine;
-  for (int i = tid; i < p.parts; i += kPickThreads) mn = larger_or_nan(mn, p.norm[at * p.parts + i]);
+  for (int i = tid; i < p.parts; i += NT) mn = larger_or_nan(mn, p.norm[at * p.parts + i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     a1 += __shfl_xor_sync(0xFFFFFFFFu, a1, o);
@@ -551,14 +542,59 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
   __syncthreads();
   int nc = 0;
   a1 = mn = 0.f;
-  for (int w = 0; w < kPickThreads / 32; ++w) {
+  for (int w = 0; w < NT / 32; ++w) {
     nc += sums[w];
     a1 += fsums[0][w];
     mn = larger_or_nan(mn, fsums[1][w]);
   }
-  if (nc > p.top && p.top > 0)
-    for (int m = begin + tid; m < end; m += kPickThreads)
-      if (keys[m] != 0u) keys[m] = order_of(score[m]);
+  const bool choose = nc > p.top && p.top > 0;
+  // the candidates' scores and their range (a NaN spreads into it)
+  float lo = __int_as_float(0x7f800000), hi = -lo;
+  bool odd = false;
+  if (choose)
+    for (int m = begin + tid; m < end; m += NT) {
+      if (keys[m] == 0u) {
+        keys[m] = kNoScore;
+        continue;
+      }
+      const float x = score[m];
+      odd = odd || x != x;
+      lo = fminf(lo, x);
+      hi = fmaxf(hi, x);
+      keys[m] = __float_as_uint(x);
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+  }
+  if (lane == 0) {
+    range[0][warp] = lo;
+    range[1][warp] = hi;
+  }
+  odd = __syncthreads_or(odd);
+  for (int w = 0; w < NT / 32; ++w) {
+    lo = fminf(lo, range[0][w]);
+    hi = fmaxf(hi, range[1][w]);
+  }
+  // Keys of 24 bits, their steps alike over the range: digits that spread, where
+  // the scores' own bits would crowd into a few binades.  A score's key is off by
+  // less than 3 of its steps (the subtraction's, the product's and the cut's), so
+  // with 2 e in steps, and 6, on either side a page's place is certain.  (1 % and
+  // the smallest normal number cover the bound's own roundings.)
+  const float e2 = 2.02f * static_cast<float>(p.G + p.rounds + 2) * 5.9604645e-8f * a1 * mn + 1.17549435e-38f;
+  const float steps = 16777215.f / fmaxf(hi - lo, 1.17549435e-38f);
+  const float wide = e2 * steps * 1.01f + 7.f;
+  // an infinity or NaN anywhere, or a bound as wide as the range: nothing is certain
+  const bool clear = choose && !odd && isfinite(hi) && isfinite(lo) && isfinite(steps) && wide < 16777216.f;
+  const int band = clear ? static_cast<int>(wide) : 0;
+  if (choose)
+    for (int m = begin + tid; m < end; m += NT) {
+      const uint32_t x = keys[m];
+      keys[m] = x == kNoScore ? 0u
+                : clear       ? 1u + min(static_cast<uint32_t>((__uint_as_float(x) - lo) * steps), 16777215u)
+                              : 1u;
+    }
   __syncthreads();
   auto held_page = [&](int m) { return keys[m] != 0u; };
   // slot m's score in 64 bits, by a warp
@@ -572,23 +608,19 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
   };
   auto take = [&](int m) { atomicOr(taken + (m >> 5), 1u << (m & 31)); };
   if (nc <= p.top) {
-    for (int m = begin + tid; m < end; m += kPickThreads)
+    for (int m = begin + tid; m < end; m += NT)
       if (held_page(m)) take(m);
   } else if (p.top > 0) {
     int larger;
-    const uint32_t kth = nth_largest<uint32_t>(begin, end, p.top, held_page, [&](int m) { return keys[m]; },
-                                               &larger, hist);
-    const float tval = value_of(kth);
-    // (1 % and the smallest normal number cover this product's own roundings)
-    const float e2 = 2.02f * static_cast<float>(p.G + p.rounds + 2) * 5.9604645e-8f * a1 * mn + 1.17549435e-38f;
-    const float hi = tval + e2, lo = tval - e2;          // a NaN or infinity in either: all are undecided
-    const bool clear = isfinite(hi) && isfinite(lo);
+    const int kth = clear ? static_cast<int>(nth_largest<NT, uint32_t>(
+                                24, begin, end, p.top, held_page, [&](int m) { return keys[m] - 1u; }, &larger, hist)) + 1
+                          : 1;
+    auto is_sure = [&](int m) { return clear && static_cast<int>(keys[m]) > kth + band; };
+    auto is_open = [&](int m) { return held_page(m) && !is_sure(m) && static_cast<int>(keys[m]) >= kth - band; };
     int sure = 0, open = 0;
-    for (int m = begin + tid; m < end; m += kPickThreads) {
-      if (!held_page(m)) continue;
-      const float x = value_of(keys[m]);
-      if (clear && x > hi) ++sure;
-      else if (!(clear && x < lo)) ++open;
+    for (int m = begin + tid; m < end; m += NT) {
+      sure += is_sure(m);
+      open += is_open(m);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -601,31 +633,26 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
     }
     __syncthreads();
     sure = open = 0;
-    for (int w = 0; w < kPickThreads / 32; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
       sure += sums[w];
       open += hist[w];
     }
     __syncthreads();
     const int want = p.top - sure;                       // of the open ones
-    auto is_open = [&](int m) {
-      if (!held_page(m)) return false;
-      const float x = value_of(keys[m]);
-      return !(clear && (x > hi || x < lo));
-    };
-    for (int m = begin + tid; m < end; m += kPickThreads)
-      if (held_page(m) && clear && value_of(keys[m]) > hi) take(m);
+    for (int m = begin + tid; m < end; m += NT)
+      if (is_sure(m)) take(m);
     if (open <= want) {
-      for (int m = begin + tid; m < end; m += kPickThreads)
+      for (int m = begin + tid; m < end; m += NT)
         if (is_open(m)) take(m);
     } else if (want > 0 && open <= 32) {
       // scored again, a warp an open page, and ranked by one warp
       if (tid == 0) sums[0] = 0;
       __syncthreads();
-      for (int m = begin + tid; m < end; m += kPickThreads)
+      for (int m = begin + tid; m < end; m += NT)
         if (is_open(m)) hist[atomicAdd(sums, 1)] = m;
       __syncthreads();
       double* again = reinterpret_cast<double*>(hist + 32);
-      for (int i = warp; i < open; i += kPickThreads / 32) {
+      for (int i = warp; i < open; i += NT / 32) {
         const double d = score_again(hist[i]);
         if (lane == 0) again[i] = d;
       }
@@ -642,7 +669,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
         if (lane < open && better < want) take(m);
       }
     } else if (want > 0) {
-      for (int m0 = begin + warp * 32; m0 < end; m0 += kPickThreads) {
+      for (int m0 = begin + warp * 32; m0 < end; m0 += NT) {
         uint32_t todo = __ballot_sync(0xFFFFFFFFu, m0 + lane < end && is_open(m0 + lane));
         for (; todo != 0u; todo &= todo - 1) {
           const int m = m0 + __ffs(todo) - 1;
@@ -652,11 +679,11 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
       }
       __syncthreads();
       int more;
-      const unsigned long long kd = nth_largest<unsigned long long>(
-          begin, end, want, is_open, [&](int m) { return order_of(exact[m]); }, &more, hist);
+      const unsigned long long kd = nth_largest<NT, unsigned long long>(
+          64, begin, end, want, is_open, [&](int m) { return order_of(exact[m]); }, &more, hist);
       // those above it, and of those that equal it the first ones
       int equal = want - more;
-      for (int m0 = begin; m0 < end; m0 += kPickThreads) {
+      for (int m0 = begin; m0 < end; m0 += NT) {
         const int m = m0 + tid;
         unsigned long long k = 0;
         const bool is = m < end && is_open(m);
@@ -667,7 +694,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
         if (lane == 0) sums[warp] = __popc(votes);
         __syncthreads();
         int before = __popc(votes & ((1u << lane) - 1u)), total = 0;
-        for (int w = 0; w < kPickThreads / 32; ++w) {
+        for (int w = 0; w < NT / 32; ++w) {
           if (w < warp) before += sums[w];
           total += sums[w];
         }
@@ -680,7 +707,7 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
   __syncthreads();
   // the list, in ascending order
   int base = 0;
-  for (int w0 = 0; w0 < words; w0 += kPickThreads) {
+  for (int w0 = 0; w0 < words; w0 += NT) {
     const int w = w0 + tid;
     uint32_t bits = w < words ? taken[w] : 0u;
     int x = __popc(bits);
@@ -695,10 +722,10 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const SelectP
     for (int v = 0; v < warp; ++v) place += sums[v];
     for (; bits != 0u; bits &= bits - 1, ++place)
       if (place < p.R) out[place] = __ldg(tab + 32 * w + __ffs(bits) - 1);
-    for (int v = 0; v < kPickThreads / 32; ++v) base += sums[v];
+    for (int v = 0; v < NT / 32; ++v) base += sums[v];
     __syncthreads();
   }
-  for (int i = base + tid; i < p.R; i += kPickThreads) out[i] = -1;
+  for (int i = base + tid; i < p.R; i += NT) out[i] = -1;
   if (tid == 0 && h == 0) {
     // every page listed is whole, but for the row's own
     const int last = __ldg(tab + row.held - 1);
@@ -741,9 +768,12 @@ size_t select_workspace(int T, int S, int Hkv, int M) {
 
 bool valid_page_size(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 
+// A CTA of 256 threads a row and K/V head, of 1024 where the rows of the table are long.
+constexpr int kLongRow = 2048;
 template <int D>
 cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
-  auto pick = select_pick_kernel<D>;
+  const bool many = p.M > kLongRow;
+  auto pick = many ? select_pick_kernel<D, 1024> : select_pick_kernel<D, 256>;
   const int smem = p.M * 4 + (p.M + 31) / 32 * 4;
   constexpr int kMaxDev = 64;
   static bool configured[kMaxDev] = {};
@@ -752,7 +782,7 @@ cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(select_pick_kernel<D, 1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMaxSelectPages * 4 + kMaxSelectPages / 8);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(select_score_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -774,7 +804,7 @@ cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.rows, p.Hkv);
-    cfg.blockDim = dim3(kPickThreads);
+    cfg.blockDim = dim3(many ? 1024 : 256);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;

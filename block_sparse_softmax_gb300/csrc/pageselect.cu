@@ -12,7 +12,8 @@
 // Which page is taken must not hang on a rounding, so a pick is the exact one:
 //   * means: each element is divided by the page size first (a power of two:
 //     exact), then summed as an unevaluated pair of fp32 numbers by Knuth's
-//     two-sum, which leaves one rounding, the mean's own to fp32;
+//     two-sum, which leaves one rounding, the mean's own to fp32 (over e4m3 pages
+//     with their scale's product, off by 2^-24 and 2^-46 at most);
 //   * scores: in fp32 first, each off by at most
 //         e = (G + r + 2) 2^-24 sum_i A_i max_mi |mean_mi|,   A = sum_h |q_h|
 //     (G roundings of the group's sum at most and r of a product's, on terms whose
@@ -45,6 +46,7 @@ struct PoolParams {
   const int* start;
   const int* lens;
   int S, M, P, Hkv, page_log2;
+  int warps;                // of a (page, head)
   int* err;
 };
 
@@ -62,19 +64,24 @@ __device__ __forceinline__ float2 e4m3x2_f32x2(uint32_t x) {
   return __half22float2(*reinterpret_cast<const __half2*>(&y));
 }
 
-// A warp a (page, head): 16 bytes a lane and load, so that 32 * 16 / (bytes of a
-// row) rows arrive at once.
+// `W` warps a (page, head), each with all of its part's loads in flight (up to 8 of
+// 16 bytes a lane; 32 * 16 / (bytes of a row) rows arrive with each), joined in
+// order in shared memory.  A page's part is what a warp waits for once: with a warp
+// a page of 64 tokens, four times, a prompt of 16384 took 10.8 us.
 constexpr int kPoolWarps = 8;
-constexpr int kPoolBatch = 8;                 // loads in flight
+constexpr int kPoolBatch = 8;
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kPoolWarps * 32) kv_pool_kernel(const PoolParams p) {
   constexpr int kEl = FP8 ? 16 : 8;           // elements of 16 bytes
   constexpr int kLanes = D / kEl;             // lanes of a row
   constexpr int kRows = 32 / kLanes;          // rows of a load
-  const int s = static_cast<int>(blockIdx.y);
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const int page = 1 << p.page_log2;
-  for (int sq = s; sq < p.S; sq += static_cast<int>(gridDim.y)) {
+  __shared__ float2 parts[kPoolWarps][D];
+  const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
+  const int loads = (1 << p.page_log2) / kRows;            // of a page (16 rows at least, 8 a load at most)
+  const int W = p.warps, each = loads / W;                 // warps of an item, loads of a warp
+  const int items_cta = kPoolWarps / W;
+  const float share = 1.f / static_cast<float>(1 << p.page_log2);
+  for (int sq = static_cast<int>(blockIdx.y); sq < p.S; sq += static_cast<int>(gridDim.y)) {
     const int a = __ldg(p.start + sq), n = __ldg(p.lens + sq);
     if (a < 0) continue;                      // nothing was reserved
     const long long most = static_cast<long long>(p.M) << p.page_log2;
@@ -82,74 +89,97 @@ __global__ void __launch_bounds__(kPoolWarps * 32) kv_pool_kernel(const PoolPara
       if (threadIdx.x == 0 && blockIdx.x == 0) record_error(p.err, ATTN_ERR_BAD_PAGES);
       continue;
     }
-    const int m0 = a >> p.page_log2, m1 = n >> p.page_log2;
-    const long long items = static_cast<long long>(max(0, m1 - m0)) * p.Hkv;
-    for (long long x = static_cast<long long>(blockIdx.x) * kPoolWarps + (threadIdx.x >> 5); x < items;
-         x += static_cast<long long>(gridDim.x) * kPoolWarps) {
-      const int m = m0 + static_cast<int>(x / p.Hkv);
-      const int h = static_cast<int>(x % p.Hkv);
-      const int pg = __ldg(p.table + static_cast<size_t>(sq) * p.M + m);
-      if (pg < 0 || pg >= p.P) {              // -1: given back already
-        if (pg != -1 && lane == 0) record_error(p.err, ATTN_ERR_BAD_PAGES);
-        continue;
+    const int m0 = a >> p.page_log2, pages = max(0, (n >> p.page_log2) - m0);
+    // items (a page and head each) in rounds of the whole CTA, whose warps meet in each
+    const long long items = static_cast<long long>(pages) * p.Hkv;
+    for (long long x = static_cast<long long>(blockIdx.x) * items_cta; x < items;
+         x += static_cast<long long>(gridDim.x) * items_cta) {
+      const long long item = x + warp / W;
+      const int i = item < items ? static_cast<int>(item / p.Hkv) : pages;
+      const int h = static_cast<int>(item - static_cast<long long>(i) * p.Hkv);
+      int pg = i < pages ? __ldg(p.table + static_cast<size_t>(sq) * p.M + m0 + i) : -1;
+      if (pg < -1 || pg >= p.P) {             // (-1: given back already)
+        if (lane == 0) record_error(p.err, ATTN_ERR_BAD_PAGES);
+        pg = -1;
       }
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.k + pg * p.k_stride + ((static_cast<size_t>(h) << p.page_log2) * D) * (FP8 ? 1 : 2)) + lane;
-      const float part = 1.f / static_cast<float>(page);
       float hi[kEl], lo[kEl];
 #pragma unroll
       for (int e = 0; e < kEl; ++e) hi[e] = lo[e] = 0.f;
-      const int loads = page / kRows;         // page >= 16 >= kRows
-      for (int i0 = 0; i0 < loads; i0 += kPoolBatch) {
-        uint4 v[kPoolBatch];
+      if (pg >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.k + pg * p.k_stride + ((static_cast<size_t>(h) << p.page_log2) * D) * (FP8 ? 1 : 2)) + lane +
+            warp % W * each * 32;
+        for (int i0 = 0; i0 < each; i0 += kPoolBatch) {
+          uint4 v[kPoolBatch];
 #pragma unroll
-        for (int u = 0; u < kPoolBatch; ++u)
-          v[u] = i0 + u < loads ? src[(i0 + u) * 32] : make_uint4(0u, 0u, 0u, 0u);
+          for (int u = 0; u < kPoolBatch; ++u)
+            v[u] = i0 + u < each ? __ldg(src + (i0 + u) * 32) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int u = 0; u < kPoolBatch; ++u) {
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          for (int u = 0; u < kPoolBatch; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (FP8) {
-              const float2 c0 = e4m3x2_f32x2(w[e]), c1 = e4m3x2_f32x2(w[e] >> 16);
-              two_sum(hi[4 * e], lo[4 * e], c0.x * part);
-              two_sum(hi[4 * e + 1], lo[4 * e + 1], c0.y * part);
-              two_sum(hi[4 * e + 2], lo[4 * e + 2], c1.x * part);
-              two_sum(hi[4 * e + 3], lo[4 * e + 3], c1.y * part);
-            } else {
-              two_sum(hi[2 * e], lo[2 * e], bf16lo(w[e]) * part);
-              two_sum(hi[2 * e + 1], lo[2 * e + 1], bf16hi(w[e]) * part);
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (FP8) {
+                const float2 c0 = e4m3x2_f32x2(w[e]), c1 = e4m3x2_f32x2(w[e] >> 16);
+                two_sum(hi[4 * e], lo[4 * e], c0.x * share);
+                two_sum(hi[4 * e + 1], lo[4 * e + 1], c0.y * share);
+                two_sum(hi[4 * e + 2], lo[4 * e + 2], c1.x * share);
+                two_sum(hi[4 * e + 3], lo[4 * e + 3], c1.y * share);
+              } else {
+                two_sum(hi[2 * e], lo[2 * e], bf16lo(w[e]) * share);
+                two_sum(hi[2 * e + 1], lo[2 * e + 1], bf16hi(w[e]) * share);
+              }
             }
           }
         }
-      }
-      // the lanes that hold the same columns of other rows
+        // the lanes that hold the same columns of other rows
 #pragma unroll
-      for (int o = kLanes; o < 32; o <<= 1) {
+        for (int o = kLanes; o < 32; o <<= 1) {
 #pragma unroll
-        for (int e = 0; e < kEl; ++e) {
-          const float oh = __shfl_xor_sync(0xFFFFFFFFu, hi[e], o);
-          const float ol = __shfl_xor_sync(0xFFFFFFFFu, lo[e], o);
-          two_sum(hi[e], lo[e], oh);
-          lo[e] = __fadd_rn(lo[e], ol);
+          for (int e = 0; e < kEl; ++e) {
+            const float oh = __shfl_xor_sync(0xFFFFFFFFu, hi[e], o);
+            const float ol = __shfl_xor_sync(0xFFFFFFFFu, lo[e], o);
+            two_sum(hi[e], lo[e], oh);
+            lo[e] = __fadd_rn(lo[e], ol);
+          }
         }
       }
-      if (lane < kLanes) {
-        const double f = FP8 ? static_cast<double>(__ldg(p.k_scale + h)) : 1.0;
+      if (W > 1) {
+        if (lane < kLanes) {
+#pragma unroll
+          for (int e = 0; e < kEl; ++e) parts[warp][lane * kEl + e] = make_float2(hi[e], lo[e]);
+        }
+        __syncthreads();
+        if (warp % W == 0 && lane < kLanes)
+          for (int w = 1; w < W; ++w)
+#pragma unroll
+            for (int e = 0; e < kEl; ++e) {
+              const float2 y = parts[warp + w][lane * kEl + e];
+              two_sum(hi[e], lo[e], y.x);
+              lo[e] = __fadd_rn(lo[e], y.y);
+            }
+      }
+      if (pg >= 0 && warp % W == 0 && lane < kLanes) {
+        const float f = FP8 ? __ldg(p.k_scale + h) : 1.f;
         float* dst = p.means + (static_cast<size_t>(pg) * p.Hkv + h) * D + lane * kEl;
 #pragma unroll
         for (int e = 0; e < kEl; e += 4) {
           float y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float hh = hi[e + i];       // an infinity's or NaN's lo is a NaN
-            const double sum = isfinite(hh) ? static_cast<double>(hh) + static_cast<double>(lo[e + i])
-                                            : static_cast<double>(hh);
-            y[i] = static_cast<float>(sum * f);
+          for (int i4 = 0; i4 < 4; ++i4) {
+            // the pair (times the scale: with the product's own rest), rounded once; in
+            // fp32, for a multiprocessor has two fp64 lanes.  An infinity's or NaN's lo
+            // is a NaN, and left out.
+            const float hh = hi[e + i4], ll = lo[e + i4];
+            const float pr = hh * f;
+            y[i4] = !isfinite(hh) ? pr
+                    : FP8         ? __fadd_rn(pr, fmaf(hh, f, -pr) + ll * f)
+                                  : __fadd_rn(hh, ll);
           }
           *reinterpret_cast<float4*>(dst + e) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
+      if (W > 1) __syncthreads();             // the parts have been read
     }
   }
 }
@@ -318,22 +348,48 @@ __global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const Sel
   const int h = static_cast<int>(blockIdx.z);
   const int r0 = static_cast<int>(blockIdx.y) * kTileRows;
   const int nr = min(kTileRows, p.rows - r0);
-  for (int r = warp; r < kTileRows; r += kTilePages / 32) {
-    SelectRow row{-1, 0, 0};
-    if (r < nr) row = select_row(p, p.t0 + r0 + r, lane);
-    if (lane == 0) {
-      row_s[r] = row.s;
-      row_end[r] = row.s < 0 ? 0 : scored_end(p, row);
-    }
-  }
-  for (int i = tid; i < kTileRows * D; i += kTilePages) {
-    const int r = i / D, e = i % D;
-    float sum = 0.f;
+  // the group's sums, 8 columns a thread
+  for (int i = tid; i < kTileRows * D / 8; i += kTilePages) {
+    const int r = i / (D / 8), e = i % (D / 8) * 8;
+    float sum[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) sum[u] = 0.f;
     if (r < nr) {
       const __nv_bfloat16* q = p.q + (p.t0 + r0 + r) * p.q_stride + static_cast<long long>(h) * p.G * D + e;
-      for (int g = 0; g < p.G; ++g) sum += __bfloat162float(q[static_cast<long long>(g) * D]);
+#pragma unroll 4
+      for (int g = 0; g < p.G; ++g) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + static_cast<long long>(g) * D));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          sum[2 * u] += bf16lo(w[u]);
+          sum[2 * u + 1] += bf16hi(w[u]);
+        }
+      }
     }
-    qsum[i] = sum;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) qsum[r * D + e + u] = sum[u];
+  }
+  // the first row's sequence by search, a later row's mostly the same one
+  if (warp == 0) {
+    const SelectRow first = select_row(p, p.t0 + r0, lane);
+    SelectRow row = first;
+    const int t = p.t0 + r0 + lane;
+    bool other = false;
+    if (lane < nr) {
+      other = first.s < 0 || __ldg(p.cu + first.s + 1) <= t;
+      row.n = first.n + lane;                 // (in the same sequence)
+      row.held = static_cast<int>((static_cast<long long>(row.n) + (1 << p.page_log2) - 1) >> p.page_log2);
+    }
+    for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, other); todo != 0u; todo &= todo - 1) {
+      const int r = __ffs(todo) - 1;
+      const SelectRow x = select_row(p, p.t0 + r0 + r, lane);
+      if (lane == r) row = x;
+    }
+    if (lane < kTileRows) {
+      row_s[lane] = lane < nr ? row.s : -1;
+      row_end[lane] = lane < nr && row.s >= 0 ? scored_end(p, row) : 0;
+    }
   }
   __syncthreads();
   float seen = 0.f;                           // the largest element met, for any of the rows
@@ -768,12 +824,12 @@ size_t select_workspace(int T, int S, int Hkv, int M) {
 
 bool valid_page_size(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 
-// A CTA of 256 threads a row and K/V head, of 1024 where the rows of the table are long.
+// A CTA of 128 threads a row and K/V head, of 1024 where the rows of the table are long.
 constexpr int kLongRow = 2048;
 template <int D>
 cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
   const bool many = p.M > kLongRow;
-  auto pick = many ? select_pick_kernel<D, 1024> : select_pick_kernel<D, 256>;
+  auto pick = many ? select_pick_kernel<D, 1024> : select_pick_kernel<D, 128>;
   const int smem = p.M * 4 + (p.M + 31) / 32 * 4;
   constexpr int kMaxDev = 64;
   static bool configured[kMaxDev] = {};
@@ -804,7 +860,7 @@ cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.rows, p.Hkv);
-    cfg.blockDim = dim3(many ? 1024 : 256);
+    cfg.blockDim = dim3(many ? 1024 : 128);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
@@ -849,11 +905,17 @@ extern "C" attn_status_t attn_kv_pool(const void* k_cache, int64_t k_page_stride
   p.P = n_pages;
   p.Hkv = H_kv;
   while ((1 << p.page_log2) < page_size) ++p.page_log2;
+  // loads of 32 lanes a page: a warp for 8 of them
+  const int loads = page_size * d * (fp8 ? 1 : 2) / 512;
+  p.warps = 1;
+  while (p.warps < kPoolWarps && loads > p.warps * kPoolBatch) p.warps *= 2;
   // the pages that became full are known on the device alone: CTAs enough for all
-  // of a few sequences, and few a sequence where there are many
+  // of a few sequences, and one a sequence where there are many (each takes its
+  // pages in turns; four a sequence, of which three found nothing, took 25 us
+  // instead of POOL256 for 256 sequences with two full pages each)
   const int gy = std::min(S, 65535);
-  const long long most = (static_cast<long long>(max_pages) * H_kv + kPoolWarps - 1) / kPoolWarps;
-  const dim3 grid(static_cast<unsigned>(std::max<long long>(1, std::min<long long>(most, 152 * 8 / gy))), gy);
+  const long long rounds = (static_cast<long long>(max_pages) * p.warps + kPoolWarps - 1) / kPoolWarps * H_kv;
+  const dim3 grid(static_cast<unsigned>(std::max<long long>(1, std::min<long long>(rounds, 152 * 4 / gy))), gy);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (d == 64) {
     if (fp8) kv_pool_kernel<64, true><<<grid, kPoolWarps * 32, 0, st>>>(p);

@@ -323,11 +323,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32) select_score_kernel(const Se
   }
 }
 
-// Chunks: 16 rows share the means of 128 pages of their sequence in shared memory
-// (read from L2 once for 16 rows), a thread a page: a dot product is a chain of d
-// fused multiply-adds in four interleaved parts.  With a warp a page and sums over
-// its lanes, 8 rows at a time, 500 rows of 1024 pages took 142 us.
-constexpr int kTileRows = 16;
+// Chunks: 32 rows share the means of 128 pages of their sequence in shared memory
+// (read from L2 once for 32 rows), a thread two pages and 16 rows: a dot product is
+// a chain of d fused multiply-adds.  500 rows of 1024 pages, 4 K/V heads: 34 us;
+// with a warp a page and sums over its lanes, 8 rows at a time, 142, with a page and
+// 16 rows a thread 42.
+constexpr int kTileRows = 32;
 constexpr int kTilePages = 128;
 template <int D>
 struct ScoreTile {
@@ -427,22 +428,30 @@ __global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const Sel
         }
       }
       __syncthreads();
-      float acc[kTileRows];
+      constexpr int kHalf = kTileRows / 2;
+      const int x0 = tid & 63, rh = tid / 64 * kHalf;      // pages x0 and x0 + 64, rows rh ..
+      float acc[2][kHalf];
 #pragma unroll
-      for (int r = 0; r < kTileRows; ++r) acc[r] = 0.f;
+      for (int r = 0; r < kHalf; ++r) acc[0][r] = acc[1][r] = 0.f;
 #pragma unroll 2
       for (int e = 0; e < D; e += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(means + tid * C::kRow + e);
+        const float4 v0 = *reinterpret_cast<const float4*>(means + x0 * C::kRow + e);
+        const float4 v1 = *reinterpret_cast<const float4*>(means + (x0 + 64) * C::kRow + e);
 #pragma unroll
-        for (int r = 0; r < kTileRows; ++r) {
-          const float4 q = *reinterpret_cast<const float4*>(qsum + r * D + e);
-          acc[r] = fmaf(q.x, v.x, fmaf(q.y, v.y, fmaf(q.z, v.z, fmaf(q.w, v.w, acc[r]))));
+        for (int r = 0; r < kHalf; ++r) {
+          const float4 q = *reinterpret_cast<const float4*>(qsum + (rh + r) * D + e);
+          acc[0][r] = fmaf(q.x, v0.x, fmaf(q.y, v0.y, fmaf(q.z, v0.z, fmaf(q.w, v0.w, acc[0][r]))));
+          acc[1][r] = fmaf(q.x, v1.x, fmaf(q.y, v1.y, fmaf(q.z, v1.z, fmaf(q.w, v1.w, acc[1][r]))));
         }
       }
-      if (m0 + tid < end) {
 #pragma unroll
-        for (int r = 0; r < kTileRows; ++r)
-          if (r >= a && r < b) p.score[(static_cast<size_t>(r0 + r) * p.Hkv + h) * p.M + m0 + tid] = acc[r];
+      for (int u = 0; u < 2; ++u) {
+        const int m = m0 + x0 + 64 * u;
+        if (m >= end) continue;
+#pragma unroll
+        for (int r = 0; r < kHalf; ++r)
+          if (rh + r >= a && rh + r < b)
+            p.score[(static_cast<size_t>(r0 + rh + r) * p.Hkv + h) * p.M + m] = acc[u][r];
       }
     }
     a = b;
@@ -532,20 +541,13 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
   const int warp = tid >> 5, lane = tid & 31;
   const int r = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y);
   const int t = p.t0 + r;
-  // what does not need the scores comes before the wait for them: A = sum_h |q_h|
-  // and the group's sum, the table
+  // what does not need the scores comes before the wait for them: the sum of A =
+  // sum_h |q_h|, the table
+  const __nv_bfloat16* q_row = p.q + t * p.q_stride + static_cast<long long>(h) * p.G * D;
   float a1 = 0.f, mn = 0.f;
   for (int e = tid; e < D; e += NT) {
-    float a = 0.f;
-    double x = 0.0;
-    const __nv_bfloat16* q = p.q + t * p.q_stride + static_cast<long long>(h) * p.G * D + e;
-    for (int g = 0; g < p.G; ++g) {
-      const float y = __bfloat162float(q[static_cast<long long>(g) * D]);
-      a += fabsf(y);
-      x += static_cast<double>(y);
-    }
-    a1 += a;
-    qd[e] = x;
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g) a1 += fabsf(__bfloat162float(q_row[static_cast<long long>(g) * D + e]));
   }
   const SelectRow row = select_row(p, t, lane);
   int* out = p.pages + (static_cast<size_t>(t) * p.Hkv + h) * p.R;
@@ -662,6 +664,14 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
     return d;
   };
+  // ... and the group's sum, for those
+  auto sum_again = [&]() {
+    for (int e = tid; e < D; e += NT) {
+      double x = 0.0;
+      for (int g = 0; g < p.G; ++g) x += static_cast<double>(__bfloat162float(q_row[static_cast<long long>(g) * D + e]));
+      qd[e] = x;
+    }
+  };
   auto take = [&](int m) { atomicOr(taken + (m >> 5), 1u << (m & 31)); };
   if (nc <= p.top) {
     for (int m = begin + tid; m < end; m += NT)
@@ -703,6 +713,7 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
     } else if (want > 0 && open <= 32) {
       // scored again, a warp an open page, and ranked by one warp
       if (tid == 0) sums[0] = 0;
+      sum_again();
       __syncthreads();
       for (int m = begin + tid; m < end; m += NT)
         if (is_open(m)) hist[atomicAdd(sums, 1)] = m;
@@ -725,6 +736,9 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
         if (lane < open && better < want) take(m);
       }
     } else if (want > 0) {
+      // scored again, a warp an open page
+      sum_again();
+      __syncthreads();
       for (int m0 = begin + warp * 32; m0 < end; m0 += NT) {
         uint32_t todo = __ballot_sync(0xFFFFFFFFu, m0 + lane < end && is_open(m0 + lane));
         for (; todo != 0u; todo &= todo - 1) {
@@ -912,7 +926,7 @@ extern "C" attn_status_t attn_kv_pool(const void* k_cache, int64_t k_page_stride
   // the pages that became full are known on the device alone: CTAs enough for all
   // of a few sequences, and one a sequence where there are many (each takes its
   // pages in turns; four a sequence, of which three found nothing, took 25 us
-  // instead of POOL256 for 256 sequences with two full pages each)
+  // instead of 10 for 256 sequences with two full pages each)
   const int gy = std::min(S, 65535);
   const long long rounds = (static_cast<long long>(max_pages) * p.warps + kPoolWarps - 1) / kPoolWarps * H_kv;
   const dim3 grid(static_cast<unsigned>(std::max<long long>(1, std::min<long long>(rounds, 152 * 4 / gy))), gy);

@@ -273,6 +273,7 @@ __device__ __forceinline__ void decode_merge(const DecodeParams& p, const DecSta
 template <int KEYS>
 struct DecUnit {
   int s, r, ta, tb;
+  const int* table;            // its row
   long long x0;
   SeqSteps<KEYS> st;
 };
@@ -313,6 +314,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     fence_barrier_init();
   }
 
+  // (the division is for rows that belong to a K/V head, and done once a unit)
+  auto table_row = [&](int s, int r) {
+    const int* row = p.table + static_cast<size_t>(s) * p.t_row;
+    return p.t_head != 0 ? row + static_cast<size_t>(r / p.q_tiles) * p.t_head : row;
+  };
   DecUnit<KEYS> un;
   int2 meta = make_int2(-1, -1);
   const int worker = cta * kDecWarps + warp;
@@ -321,6 +327,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
   if constexpr (SMALL) {
     un.s = cta / units;
     un.r = cta - un.s * units;
+    un.table = table_row(un.s, un.r);
     const int n = __ldg(p.lens + un.s);
     if (p.selected && n < 0) return;                // (the whole block)
     if (tid == 0 && un.r == 0 && (n < 0 || n > most_tokens(p)))
@@ -406,6 +413,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
       un.r = un.st.total > 0 ? static_cast<int>((x0 - before) / un.st.total) : units;
       un.x0 = before + static_cast<long long>(un.r) * un.st.total;
       any = un.r < units;
+      un.table = table_row(un.s, un.r);
     }
     if (!any) {
       if (lane == 0) p.meta[worker] = meta;
@@ -430,8 +438,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
 #pragma unroll
     for (int m = 0; m < C::kRowTiles; ++m) {
       const int key = in ? u.st.key(t) + 16 * m : 0;
-      pages[m] = in && key < u.st.n ? __ldg(p.table + static_cast<size_t>(u.s) * p.t_row +
-                                            u.r / p.q_tiles * p.t_head + (key >> p.page_log2)) : -1;
+      pages[m] = in && key < u.st.n ? __ldg(u.table + (key >> p.page_log2)) : -1;
     }
   };
   auto valid_page = [&](int pg) { return pg >= 0 && pg < p.P; };
@@ -507,6 +514,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D, FP8, NT>::kCtas)
     }
     u.ta = 0;
     u.tb = static_cast<int>(min(static_cast<long long>(u.st.total), x1 - u.x0));
+    u.table = table_row(u.s, u.r);
     return true;
   };
   // The first steps of a unit.

@@ -221,11 +221,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const float ctas = static_cast<float>(p.ctas);
   const float share = top.y * static_cast<float>(p.Hkv) / ctas;      // a CTA's fair share of the pairs
 
-  // ---- what lengths of parts cost: a whole tile, and the share cut into 1, 1.17, ..., 12;
-  // a thread weighs one of them for every 64th sequence ----
+  // ---- what lengths of parts cost: a whole tile, and 2 to 1/9 of the share; a thread
+  // weighs one of them for every 64th sequence ----
   const int cand = tid & (kPlanCuts - 1);
-  const float turns = cand <= 6 ? 1.f + static_cast<float>(cand - 1) / 6.f
-                                : exp2f(static_cast<float>(cand - 6) * 0.3f + 0.9f);
+  const float turns = 0.5f * exp2f(static_cast<float>(cand - 1) * 0.3f);
   const int whole = max(1, longest);
   const int my_len = cand == 0 ? whole : min(whole, max(kLeastPairs, static_cast<int>(ceilf(share / turns))));
   // long pieces, their pairs with what a piece costs beside them; the others' pairs; slots
@@ -822,7 +821,7 @@ __global__ void __launch_bounds__(512, 1)
                           sdesc_add(dk, kk * 32), part == 0 ? idesc : idesc | kE5m2, part > 0 || kk > 0 ? 1u : 0u);
           } else {
             const uint64_t dk = sdesc_sw128(ks, 16, 1024);
-#pragma unroll
+#pragma unroll (D == 64 ? 2 : 8)
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t qoff = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
               const uint32_t koff = (kk >> 2) * 2 * C::kChunkBytes + (kk & 3) * 32;
@@ -853,7 +852,7 @@ __global__ void __launch_bounds__(512, 1)
               if (!wait_bar(bar(C::kBarVFull + s), (iv / C::kStagesV) & 1, abort_flag, p.err)) return false;
               tc_fence_after();
               const uint64_t dv = sdesc_sw128(sbase + C::kVOff + s * C::kTileBytes, C::kChunkBytes, 1024);
-#pragma unroll
+#pragma unroll (D == 64 ? 2 : 8)
               for (int kk = 0; kk < kTileN / 16; ++kk)
                 mma_ts(tmem + C::kColO, tmem + C::kColP + (t * 8 + kk) * 8, sdesc_add(dv, kk * 16 * 128),
                        kIdescPV, (k > 0 || t > 0 || kk > 0) ? 1u : 0u);

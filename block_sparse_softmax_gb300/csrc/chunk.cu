@@ -94,6 +94,7 @@ struct SeqRows {
   int a, b, n;
   long long shift;
   bool bad;                  // its length is out of range
+  bool disorder;             // its offsets do not ascend
 };
 __device__ __forceinline__ SeqRows seq_rows(const ChunkParams& p, int s) {
   SeqRows r;
@@ -104,6 +105,7 @@ __device__ __forceinline__ SeqRows seq_rows(const ChunkParams& p, int s) {
   const long long most = min(static_cast<long long>(p.M) << p.page_log2, static_cast<long long>(kMaxTokens));
   r.n = static_cast<int>(max(0ll, min(static_cast<long long>(len), most)));
   r.bad = len < 0 || len > most;
+  r.disorder = c0 > c1;
   r.shift = static_cast<long long>(r.n) - c1;
   return r;
 }
@@ -189,11 +191,15 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const bool few = p.S <= kPlanThreads;                              // `works` holds them all
 
   // ---- the sequences' rows and work; all pairs, and the longest tile's ----
+  // (Where the offsets ascend, no row is two sequences', and no sum below passes T
+  // H; where they do not, nothing is done.)
   float2 top = make_float2(0.f, 0.f);
+  bool disorder = false;
   for (int s = tid; s < p.S; s += kPlanThreads) {
     const SeqRows r = seq_rows(p, s);
     const SeqWork w = seq_work(p, r);
-    if (r.bad) record_error(p.err, ATTN_ERR_BAD_PAGES);
+    if (r.bad || r.disorder) record_error(p.err, ATTN_ERR_BAD_PAGES);
+    disorder = disorder || r.disorder;
     ChunkSeq* q = p.seq + s;
     q->a = r.a;
     q->b = r.b;
@@ -211,7 +217,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     top.y += __shfl_xor_sync(0xFFFFFFFFu, top.y, o);
   }
   if (lane == 0) tops[warp] = top;
-  __syncthreads();
+  if (__syncthreads_or(disorder)) {
+    if (tid == 0) *p.plan = ChunkPlan{0, 0, 0, 0};
+    return;
+  }
   top = tops[0];
   for (int w = 1; w < warps; ++w) {
     top.x = fmaxf(top.x, tops[w].x);
@@ -460,10 +469,11 @@ static_assert(kChunkOut + 2 * kChunkSoft + kChunkLow <= 4 * kChunkLaunchRegs, "r
 constexpr int kWantPairs = 6;               // pairs of a piece that are left when the next one is chosen
 constexpr float kP2 = 7.f;                  // e4m3: P carries 2^7
 
-// kind::f16 with fp16 operands, kind::f8f6f4 with e4m3 ones: formats 0; A in
-// e5m2: format 1 in bits 7-9.
-__host__ __device__ constexpr uint32_t idesc_f32(int M, int N, bool b_mn_major, uint32_t a_format = 0u) {
-  return (1u << 4) | (a_format << 7) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+// kind::f16 with fp16 operands, kind::f8f6f4 with e4m3 ones: formats 0 (A in e5m2:
+// kAIsE5m2, format 1 in bits 7-9).
+constexpr uint32_t kAIsE5m2 = 1u << 7;
+__host__ __device__ constexpr uint32_t idesc_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 // D[tmem] (+)= A[smem desc] * B[smem desc], 32 8-bit elements deep
@@ -531,6 +541,7 @@ __global__ void __launch_bounds__(512, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {                      // the swizzle needs it: report, touch nothing
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) record_error(p.err, ATTN_ERR_UNSUPPORTED);
     return;
   }
@@ -591,6 +602,9 @@ __global__ void __launch_bounds__(512, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the plan is there, and all before it (who gives up waits, too: the join reads
+  // the plan when this kernel has ended)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (gave_up) {
     if (warp == 0) {
       __syncwarp();
@@ -598,7 +612,6 @@ __global__ void __launch_bounds__(512, 1)
     }
     return;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // the plan is there, and all before it
 
   // A role's next piece (slot `i & 1` of the ring holds piece i); false at the end
   // or when a wait ran out.  `whole`: all lanes of a warp ask.
@@ -787,7 +800,6 @@ __global__ void __launch_bounds__(512, 1)
                                          : idesc_bf16_f32(kTileM, 2 * kTileN, false, false);
         constexpr uint32_t kIdescS1 = FP8 ? idesc_f32(kTileM, kTileN, false)
                                           : idesc_bf16_f32(kTileM, kTileN, false, false);   // a block alone
-        constexpr uint32_t kE5m2 = 1u << 7;
         constexpr uint32_t kIdescPV = FP8 ? idesc_f32(kTileM, D, true) : idesc_bf16_f32(kTileM, D, false, true);
         int ik = 0, iv = 0;     // K stages and V tiles consumed
         int qn = 0;             // Q tiles consumed
@@ -818,7 +830,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
                 mma_ss_f8(tmem + C::kColS, sdesc_add(dq, part * (D == 128 ? C::kChunkBytes : 64) + kk * 32),
-                          sdesc_add(dk, kk * 32), part == 0 ? idesc : idesc | kE5m2, part > 0 || kk > 0 ? 1u : 0u);
+                          sdesc_add(dk, kk * 32), part == 0 ? idesc : idesc | kAIsE5m2, part > 0 || kk > 0 ? 1u : 0u);
           } else {
             const uint64_t dk = sdesc_sw128(ks, 16, 1024);
 #pragma unroll (D == 64 ? 2 : 8)
@@ -915,7 +927,7 @@ __global__ void __launch_bounds__(512, 1)
           // tiles first (the last ones, which see most keys, lead), then parts, then heads
           const int cut = in / q.nt % q.cuts;
           const int hkv = in / q.nt / q.cuts;
-          const SeqRows r{q.a, q.b, q.n, q.shift, false};
+          const SeqRows r{q.a, q.b, q.n, q.shift, false, false};
           const Tile t = seq_tile(r, q.nt - 1 - in % q.nt, p.tpt);
           x.s = s;
           x.t0 = t.t0;
@@ -962,7 +974,7 @@ __global__ void __launch_bounds__(512, 1)
 
       // A piece is chosen late, when few pairs of the one before it are left to be
       // asked for: chosen a piece ahead, the last ones waited behind others while
-      // CTAs had nothing to do (1024 tokens at 131071: 557 us, so 4xx).
+      // CTAs had nothing to do (1024 tokens at 131071: 557 us, so 425).
       Piece x;
       bool more = true;
       while (more) {
@@ -1269,6 +1281,7 @@ __global__ void __launch_bounds__(512, 1)
           if (k == 0) {                           // Q's factor, written before this S was
             const uint32_t f = *reinterpret_cast<volatile uint8_t*>(smem + C::kUpOff + row_in_tile);
             sl2 *= __uint_as_float((254u - f) << 23);
+            if (sl2 == 0.f) sl2 = __uint_as_float(1u);    // 0 times a masked score would be a NaN
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kBarPieceEmpty + (np & 1)));
           }
@@ -1461,7 +1474,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
   for (int j = static_cast<int>(blockIdx.x); j < joins; j += static_cast<int>(gridDim.x)) {
     const int s = find_seq(p.S, j, lane, [&](int i) { return p.seq[i].join0; });
     const ChunkSeq q = p.seq[s];
-    const SeqRows r{q.a, q.b, q.n, q.shift, false};
+    const SeqRows r{q.a, q.b, q.n, q.shift, false, false};
     const int cuts = q.cuts, nt = q.nt;
     const int in = j - q.join0;
     const int hkv = in / nt, i = in % nt;                 // the tile's number among its pieces'

@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
       p.out_lens[t] = row.s < 0 ? -1 : 0;
       if (row.s >= 0) record_error(p.err, ATTN_ERR_BAD_PAGES);        // fewer tokens than new ones
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // no launch ends before the scores' does
     return;
   }
   if (tid == 0 && h == 0) {

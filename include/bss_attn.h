@@ -467,7 +467,8 @@ attn_status_t attn_decode_paged(const void* q, int64_t q_stride, const void* k_c
  *   j < sinks; window = 0: every key (sinks must be 0).  H_kv divides H, at most
  *   128 query heads share a K/V head; query head h reads K/V head h / (H / H_kv).
  *   Rows before cu_q[0] or from cu_q[S] on belong to no sequence: their o and
- *   lse are left as they were.  A row before its sequence's first token (more
+ *   lse are left as they were (all rows' where cu_q does not ascend, which is
+ *   reported).  A row before its sequence's first token (more
  *   new tokens than the sequence has) gets O = 0, LSE = -inf and is reported.
  *   What the table's entries of keys that no row of a sequence sees hold does
  *   not matter, nor what the caches hold past a sequence's length.  A seen page
@@ -479,6 +480,13 @@ attn_status_t attn_decode_paged(const void* q, int64_t q_stride, const void* k_c
  *   depends on none of the device's arrays; 0 for invalid arguments), contents
  *   on entry irrelevant.  Calls that can overlap need a workspace each.
  *   T >= 0, S >= 1.  The same lengths give the same bits in every run.
+ *   With a window, attn_kv_evict is for after this call: a chunk's first tokens
+ *   still see what its last one does not.
+ *   Scores, maxima, sums and O are fp32, parts are joined in fp32.  The
+ *   probabilities enter their product as bf16 (2^-9) over bf16 pages, as fp16
+ *   (2^-11, and 2^-32 of the row's largest) over e4m3 ones, where q enters its
+ *   own as two 8-bit parts (all of an element down to 2^-13 of its row's largest,
+ *   below that off by 2^-21 of that one at most).
  */
 size_t attn_fwd_paged_workspace_bytes(int T, int S, int H, int H_kv, int d, int max_pages,
                                       int page_size);

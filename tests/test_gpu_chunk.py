@@ -187,13 +187,24 @@ def test_chunk_reports_bad_lengths(bss):
         check_rows(q, o, lse, c, lens, news, cu, skip=(1,))
 
 
-def test_offsets_in_disorder_stay_in_range(bss):
+def test_offsets_in_disorder_are_refused(bss):
+    """... on the device: nothing is written, and it is reported; the selection's rows each find some
+    sequence or none."""
     c = Cache([300, 40, 50], 2, 128, 16, 7)
     q, _ = ragged([40, 40, 50], 8, 128, 1)
+    o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 3.0, device="cuda")
     means = torch.zeros(c.k.shape[0], 2, 128, device="cuda")
     for cu in ([0, 90, 40, 130], [130, 90, 40, 0], [-5, 40, 80, 10 ** 6], [0, 0, 0, 0],
                [-2 ** 31, 2 ** 31 - 1, -1, 7]):
-        bss.attn_fwd_paged(q, c.k, c.v, c.table, c.lens, ints(cu))
+        bss.attn_fwd_paged(q, c.k, c.v, c.table, c.lens, ints(cu), out=o, lse=lse)
+        if cu != sorted(cu):
+            assert bss.attn_poll_status() == BAD_PAGES
+            assert (o == 7.0).all() and (lse == 3.0).all()
+        elif cu == [0, 0, 0, 0]:
+            assert bss.attn_poll_status() == 0 and (o == 7.0).all()
+        else:                                            # more new tokens than there are
+            assert bss.attn_poll_status() == BAD_PAGES
+            o.fill_(7.0), lse.fill_(3.0)
         pages, lens = bss.attn_select_pages(q, means, c.table, c.lens, ints(cu), 3, 16)
         bss.attn_decode_selected(q, c.k, c.v, pages, lens)
         torch.cuda.synchronize()
@@ -245,6 +256,7 @@ def test_chunk_of_large_scores(bss, d, e4m3):
     for f in (60.0, -60.0, 0.0, 2.0 ** -130, 2.0 ** -100):
         check_chunk(bss, c, (q.float() * f).bfloat16(), cu, [500, 64], [100, 64])
     check_chunk(bss, c, (q.float() * 2.0 ** 100).bfloat16(), cu, [500, 64], [100, 64], scale=2.0 ** -103)
+    check_chunk(bss, c, (q.float() * 2.0 ** -100).bfloat16(), cu, [500, 64], [100, 64], scale=2.0 ** -120)
     for at in (0, d - 1):
         far = q.clone()
         far[::2, :, at] = 700.0

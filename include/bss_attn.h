@@ -483,7 +483,7 @@ attn_status_t attn_decode_paged(const void* q, int64_t q_stride, const void* k_c
  *   With a window, attn_kv_evict is for after this call: a chunk's first tokens
  *   still see what its last one does not.
  *   Scores, maxima, sums and O are fp32, parts are joined in fp32.  The
- *   probabilities enter their product as bf16 (2^-9) over bf16 pages, as fp16
+ *   probabilities enter their product as bf16 (2^-8) over bf16 pages, as fp16
  *   (2^-11, and 2^-32 of the row's largest) over e4m3 ones, where q enters its
  *   own as two 8-bit parts (all of an element down to 2^-13 of its row's largest,
  *   below that off by 2^-21 of that one at most).

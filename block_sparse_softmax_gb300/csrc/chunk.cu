@@ -502,6 +502,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {     // to L2
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {        // the low 16 bits
   uint32_t y;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
@@ -823,13 +828,13 @@ __global__ void __launch_bounds__(512, 1)
           const uint32_t idesc = 2 * k + 1 < nb ? kIdescS : kIdescS1;
           const uint32_t ks = sbase + C::kKOff + s * C::kKBytes;
           if constexpr (FP8) {
-            // Q's parts: d=128 a tile of 128-byte rows each, d=64 the halves of one
+            // Q's parts: 32 bytes each, side by side
             const uint64_t dk = D == 128 ? sdesc_sw128(ks, 16, 1024) : sdesc_sw64(ks);
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
-                mma_ss_f8(tmem + C::kColS, sdesc_add(dq, part * (D == 128 ? C::kChunkBytes : 64) + kk * 32),
+                mma_ss_f8(tmem + C::kColS, sdesc_add(dq, (kk >> 1) * C::kChunkBytes + (kk & 1) * 64 + part * 32),
                           sdesc_add(dk, kk * 32), part == 0 ? idesc : idesc | kAIsE5m2, part > 0 || kk > 0 ? 1u : 0u);
           } else {
             const uint64_t dk = sdesc_sw128(ks, 16, 1024);
@@ -892,12 +897,15 @@ __global__ void __launch_bounds__(512, 1)
           const int ns = (nb + 1) / 2;
           for (int k = 0; k < ns && ok; ++k) {
             if (k + 1 < ns) ok = issue_s(k + 1, nb);
-            else ok = next_blocks(nb2) && (nb2 == 0 || issue_s(0, nb2));
+            else if (!FP8) ok = next_blocks(nb2) && (nb2 == 0 || issue_s(0, nb2));
             if (ok) ok = issue_pv(k, nb);
           }
           if (!ok) break;
           mma_commit(bar(C::kBarOFull));
           ++on;
+          // e4m3: the next Q has to be turned, too, which this piece's last V is not to
+          // wait for
+          if (FP8) ok = next_blocks(nb2) && (nb2 == 0 || issue_s(0, nb2));
           nb = nb2;
         }
         // every MMA issued has completed before tensor memory is released (one phase
@@ -967,6 +975,11 @@ __global__ void __launch_bounds__(512, 1)
           dst->kb.nwb = x.kb.nwb;
           dst->kb.sb0 = x.kb.sb0;
           mbar_arrive(bar(C::kBarPieceFull + (np & 1)));
+          // its Q is wanted when the piece before it has had its last S, and not earlier
+          if (x.kb.count() > 0) {
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c) prefetch_3d(&tmQ, c * 64, x.hkv() * p.G, x.t0);
+          }
         }
         ++np;
         return true;
@@ -1129,7 +1142,7 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t at = sbase + C::kQOff + s * C::kTileBytes + row * 128;
         auto unit = [&](int c, int u) { return at + c * C::kChunkBytes + ((u ^ (row & 7)) << 4); };
         float top = 0.f;
-#pragma unroll 2
+#pragma unroll 4
         for (int u = 0; u < D / 8; ++u) {
           const uint4 w = lds128(unit(u >> 3, u & 7));
           top = fmax3(top, fabsf(bf16lo(w.x)), fabsf(bf16hi(w.x)));
@@ -1142,11 +1155,14 @@ __global__ void __launch_bounds__(512, 1)
         const int e = static_cast<int>(__float_as_uint(top) >> 23);
         const int field = top == 0.f ? 127 : max(1, min(253, 127 + 134 - e));
         const float up = e == 255 ? __int_as_float(0x7fffffff) : __uint_as_float(static_cast<uint32_t>(field) << 23);
-        // 16 elements from units 2 u and 2 u + 1 of chunk c
-        auto parts = [&](int c, int u, uint32_t (&a)[4], uint32_t (&b)[4]) {
+        // 32 elements, which an MMA takes, and their parts have the same 64 bytes (one
+        // turn of a loop: this runs once a piece, and what it takes is reading its code)
+#pragma unroll 1
+        for (int g = 0; g < D / 32; ++g) {
+          uint32_t a[8], b[8];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 w = lds128(unit(c, 2 * u + i));
+          for (int i = 0; i < 4; ++i) {
+            const uint4 w = lds128(unit(g >> 1, (g & 1) * 4 + i));
             const uint32_t x0 = two_parts(bf16lo(w.x) * up, bf16hi(w.x) * up);
             const uint32_t x1 = two_parts(bf16lo(w.y) * up, bf16hi(w.y) * up);
             const uint32_t x2 = two_parts(bf16lo(w.z) * up, bf16hi(w.z) * up);
@@ -1156,42 +1172,10 @@ __global__ void __launch_bounds__(512, 1)
             a[2 * i + 1] = __byte_perm(x2, x3, 0x5410);
             b[2 * i + 1] = __byte_perm(x2, x3, 0x7632);
           }
-        };
-        // the second parts wait in registers until their place has been read: they
-        // go to the row's second half (d=64) or second chunk (d=128)
-        uint32_t rest[4][4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t a[4];
-          parts(0, u, a, rest[u]);
-          sts128(unit(0, u), a[0], a[1], a[2], a[3]);       // units 2 u + 1 and below have been read
-        }
-        if constexpr (D == 64) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) sts128(unit(0, 4 + u), rest[u][0], rest[u][1], rest[u][2], rest[u][3]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t a[4], b[4];
-            parts(1, u, a, b);
-            sts128(unit(0, 4 + u), a[0], a[1], a[2], a[3]);
-            // units 2 u and 2 u + 1 of the second chunk are free
-            if (u < 2) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                sts128(unit(1, 2 * u + i), rest[2 * u + i][0], rest[2 * u + i][1], rest[2 * u + i][2],
-                       rest[2 * u + i][3]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rest[u][i] = b[i];  // (rest[0] and [1] went out with u = 0, [2], [3] with 1)
-            if (u == 2) {
-              sts128(unit(1, 4), rest[0][0], rest[0][1], rest[0][2], rest[0][3]);
-              sts128(unit(1, 5), rest[1][0], rest[1][1], rest[1][2], rest[1][3]);
-            }
-            if (u == 3) {
-              sts128(unit(1, 6), rest[2][0], rest[2][1], rest[2][2], rest[2][3]);
-              sts128(unit(1, 7), rest[3][0], rest[3][1], rest[3][2], rest[3][3]);
-            }
+          for (int i = 0; i < 2; ++i) {
+            sts128(unit(g >> 1, (g & 1) * 4 + i), a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+            sts128(unit(g >> 1, (g & 1) * 4 + 2 + i), b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
           }
         }
         *reinterpret_cast<volatile uint8_t*>(smem + C::kUpOff + row) = static_cast<uint8_t>(field);
@@ -1200,20 +1184,16 @@ __global__ void __launch_bounds__(512, 1)
         ++qn;
         return true;
       };
-      // in the producer's order: at a piece's end the next one's Q before the last V
+      // (a piece's last V before the next one's Q: the MMAs come in that order)
       Piece x, y;
       bool more = next_piece(x);
       bool ok = !more || convert_q();
       while (ok && more) {
         const int ns = (x.kb.count() + 1) / 2;
-        for (int k = 0; k < ns && ok; ++k) {
-          if (k + 1 == ns) {
-            more = next_piece(y);
-            ok = !more || convert_q();
-          }
-          ok = ok && convert_v(x, k);
-        }
-        ok = ok && output(x);
+        for (int k = 0; k < ns && ok; ++k) ok = convert_v(x, k);
+        if (!ok) break;
+        more = next_piece(y);
+        ok = (!more || convert_q()) && output(x);
         x = y;
       }
     }
@@ -1489,14 +1469,6 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
     // again, and not counted)
     constexpr int kBatch = 4;
     for (int c0 = 0; c0 < cuts; c0 += kBatch) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const float* x = part + min(c0 + u, cuts - 1) * step + kTileM * D + row;
-        const float mc = x[0], lc = x[kTileM];
-        m = lc != 0.f ? fmaxf(m, mc) : m;
-      }
-    }
-    for (int c0 = 0; c0 < cuts; c0 += kBatch) {
       float lc[kBatch], mc[kBatch];
       float4 v[kBatch][2];
 #pragma unroll
@@ -1507,6 +1479,16 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
         const float4* a = reinterpret_cast<const float4*>(x) + col / 4 * kTileM + row;
         v[u][0] = a[0];
         v[u][1] = a[kTileM];
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) top = lc[u] != 0.f ? fmaxf(top, mc[u]) : top;
+      if (top != m) {                                     // (of the first four: from -inf, 0 to 0)
+        const float w = ex2(m - top);
+        l *= w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= w;
+        m = top;
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
@@ -1627,7 +1609,7 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, attn_fwd_paged_kernel<D, FP8>, tq, tk, tv, p)) != cudaSuccess) return e;
   if (p.slots == 0) return cudaSuccess;
-  cfg.gridDim = dim3(std::min(p.slots / 2, 2 * sms), D / 16);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(p.slots / 2, most_tiles(p.T, p.S, p.G) * p.Hkv)), D / 16);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, FP8>, p);

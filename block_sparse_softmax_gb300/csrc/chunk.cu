@@ -52,14 +52,17 @@ constexpr int kMaxGroup = 128;             // query heads of a K/V head: rows of
 constexpr int kMaxParts = 152 * 8;         // parts that wait to be joined
 constexpr int kLeastPairs = 4;             // pairs of key blocks of a part at least
 
-// What the plan leaves for the other kernels.
+// What the plan leaves for the other kernels.  Pieces of the long kind from `tail`
+// on are cut once more, into `fine` each; their parts' slots begin at tail_slot.
 struct ChunkPlan {
-  int pieces1, pieces;       // of the long kind, in all
+  int pieces1, pieces;       // of the long kind, in all (before they are cut once more)
   int next;                  // pieces taken, past each CTA's first
-  int joins;                 // (tile, K/V head)s that are joined
+  int joins;                 // (tile, K/V head)s that are joined: those of cut sequences, then the tail's pieces
+  int tail, fine, tail_slot, tail_join;
 };
 // Of a sequence: pieces of either kind, slots and joins before it; its rows
-// (SeqRows); the parts that its tiles' keys are cut into; its work (SeqWork).
+// (SeqRows); the parts that its tiles' keys are cut into; its work (SeqWork; 0 for
+// `longest` says that its pieces are not long ones).
 struct __align__(16) ChunkSeq {
   int before1, before2, slot0, join0;
   int a, b, n, cuts;
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   __shared__ float2 tops[kPlanThreads / 32];
   __shared__ int4 scan[kPlanThreads / 32];
   __shared__ SeqWork works[kPlanThreads];
-  __shared__ int chosen;
+  __shared__ int chosen, chosen_tail, chosen_fine;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int warps = min(kPlanThreads / 32, (p.S + 31) / 32);         // with a sequence of their own
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   }
   if (lane == 0) tops[warp] = top;
   if (__syncthreads_or(disorder)) {
-    if (tid == 0) *p.plan = ChunkPlan{0, 0, 0, 0};
+    if (tid == 0) *p.plan = ChunkPlan{0, 0, 0, 0, 0, 1, 0, 0};
     return;
   }
   top = tops[0];
@@ -267,13 +270,25 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     }
     const float each = v.x > 0.f ? v.y / v.x : 0.f, rounds = ceilf(v.x / ctas);
     const float idle = (rounds * ctas - v.x) * each;
-    // the long pieces' turns, what does not fit beside the last of them, and the
-    // join: 6 us and 7 ns a part, in the 1.75 us that a pair takes
-    float t = rounds * each + fmaxf(0.f, v.z - idle) / ctas + (v.w > 0.f ? 3.5f + 0.004f * v.w : 0.f);
-    if (cand > 0 && v.w > static_cast<float>(p.slots)) t = 3.4e38f;
-    int best = cand;
+    // the long pieces' turns, and what does not fit beside the last of them
+    float t = rounds * each + fmaxf(0.f, v.z - idle) / ctas;
+    // ... or, as the second half of the warp weighs it, the last turn's pieces and some
+    // more cut once more: all CTAs end together but for half a piece of those
+    float tail = 0.f, fine = 1.f;
+    if (lane >= kPlanCuts) {
+      tail = v.x - floorf(v.x / ctas) * ctas;
+      if (2.f * tail < ctas) tail += floorf(0.5f * ctas);
+      fine = each >= 32.f ? 4.f : each >= 12.f ? 3.f : 2.f;
+      t = (v.y + v.z + tail * (2.f * fine - 1.f)) / ctas + 0.5f * each / fine;
+      v.w += tail * fine;
+      if (v.x - tail < ctas || each < 6.f || p.slots == 0) t = 3.4e38f;
+    }
+    // the join: 6 us and 7 ns a part, in the 1.75 us that a pair takes
+    t += v.w > 0.f ? 3.5f + 0.004f * v.w : 0.f;
+    if (lane > 0 && v.w > static_cast<float>(p.slots)) t = 3.4e38f;
+    int best = lane;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
+    for (int o = 16; o > 0; o >>= 1) {
       const float t2 = __shfl_xor_sync(0xFFFFFFFFu, t, o);
       const int b2 = __shfl_xor_sync(0xFFFFFFFFu, best, o);
       if (t2 < t || (t2 == t && b2 < best)) {
@@ -281,8 +296,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         best = b2;
       }
     }
-    const int len = __shfl_sync(0xFFFFFFFFu, my_len, best);
-    if (lane == 0) chosen = len;
+    if (lane == best) {
+      chosen = my_len;
+      chosen_tail = static_cast<int>(tail);
+      chosen_fine = static_cast<int>(fine);
+    }
   }
   __syncthreads();
   const int len = chosen;
@@ -312,6 +330,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       ChunkSeq* q = p.seq + s;
       *reinterpret_cast<int4*>(q) = make_int4(base.x + y.x, base.y + y.y, base.z + y.z, base.w + y.w);
       q->cuts = cuts;
+      if (!first) q->longest = 0;
       if (first)
         for (int i = base.x + y.x; i < min(base.x + y.x + x.x, p.ctas); ++i) p.first[i] = s;
     }
@@ -321,15 +340,14 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     for (int s = tid; s < p.S; s += kPlanThreads) {
       const int b2 = p.seq[s].before2, nt = few ? works[s].nt : p.seq[s].nt;
       const int cuts = p.seq[s].cuts;
-      if (long_pieces(few ? works[s].longest : p.seq[s].longest, cuts, len)) continue;
+      if (p.seq[s].longest > 0) continue;
       for (int i = base.x + b2; i < min(base.x + b2 + nt * p.Hkv * cuts, p.ctas); ++i) p.first[i] = s;
     }
   }
   if (tid == 0) {
-    p.plan->pieces1 = base.x;
-    p.plan->pieces = base.x + base.y;
-    p.plan->next = 0;
-    p.plan->joins = base.w;
+    // (the sums above are exact where a tail is chosen: fewer parts than slots)
+    const int tail = min(chosen_tail, base.x);
+    *p.plan = ChunkPlan{base.x, base.x + base.y, 0, base.w + tail, base.x - tail, chosen_fine, base.z, base.w};
   }
 }
 
@@ -490,6 +508,14 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint
 // (mode 4): 8 rows are 512 bytes.
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
   return (sdesc_sw128(saddr, 16, 512) & ~(static_cast<uint64_t>(7) << 61)) | static_cast<uint64_t>(4) << 61;
+}
+// One thread of a converged warp, and the compiler knows it: an MMA's operands are
+// the warp's, and behind `lane == 0` each MMA's code has to find whose they are (23
+// KB of code for the MMA thread instead of 15).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0u;
 }
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
@@ -800,7 +826,7 @@ __global__ void __launch_bounds__(512, 1)
       // For every pair: S of the next pair (of the next piece at a piece's end),
       // as soon as both softmax warpgroups hold this pair's S in registers, then
       // this pair's P V.
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t kIdescS = FP8 ? idesc_f32(kTileM, 2 * kTileN, false)
                                          : idesc_bf16_f32(kTileM, 2 * kTileN, false, false);
         constexpr uint32_t kIdescS1 = FP8 ? idesc_f32(kTileM, kTileN, false)
@@ -838,7 +864,7 @@ __global__ void __launch_bounds__(512, 1)
                           sdesc_add(dk, kk * 32), part == 0 ? idesc : idesc | kAIsE5m2, part > 0 || kk > 0 ? 1u : 0u);
           } else {
             const uint64_t dk = sdesc_sw128(ks, 16, 1024);
-#pragma unroll (D == 64 ? 2 : 8)
+#pragma unroll 2
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t qoff = (kk >> 2) * C::kChunkBytes + (kk & 3) * 32;
               const uint32_t koff = (kk >> 2) * 2 * C::kChunkBytes + (kk & 3) * 32;
@@ -869,7 +895,7 @@ __global__ void __launch_bounds__(512, 1)
               if (!wait_bar(bar(C::kBarVFull + s), (iv / C::kStagesV) & 1, abort_flag, p.err)) return false;
               tc_fence_after();
               const uint64_t dv = sdesc_sw128(sbase + C::kVOff + s * C::kTileBytes, C::kChunkBytes, 1024);
-#pragma unroll (D == 64 ? 2 : 8)
+#pragma unroll 2
               for (int kk = 0; kk < kTileN / 16; ++kk)
                 mma_ts(tmem + C::kColO, tmem + C::kColP + (t * 8 + kk) * 8, sdesc_add(dv, kk * 16 * 128),
                        kIdescPV, (k > 0 || t > 0 || kk > 0) ? 1u : 0u);
@@ -915,7 +941,9 @@ __global__ void __launch_bounds__(512, 1)
       }
     } else if (warp == 14) {
       // =================== pieces (a whole warp) ===================
-      const int total = p.plan->pieces, total1 = p.plan->pieces1;
+      const ChunkPlan plan = *p.plan;
+      const int tail = plan.pieces1 - plan.tail;           // pieces that are cut once more
+      const int total1 = plan.tail + tail * plan.fine, total = total1 + plan.pieces - plan.pieces1;
       int np = 0;
       // The next piece that has keys; pieces without are seen to here.
       int taken = static_cast<int>(blockIdx.x);
@@ -925,35 +953,50 @@ __global__ void __launch_bounds__(512, 1)
           if (begun && lane == 0) taken = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
           const int index = __shfl_sync(0xFFFFFFFFu, taken, 0);
           if (index < 0 || index >= total) return false;
+          // the piece among its kind's, and which of its cuts (each for all pieces in turn)
+          const bool is_long = index < total1;
+          const int over = index - plan.tail;
+          const int sub = is_long && over >= 0 ? over / tail : 0;
+          const int piece = is_long ? index - sub * tail : index - total1;
+          const int* before = &p.seq->before1 + (is_long ? 0 : 1);
+          constexpr int kStep = sizeof(ChunkSeq) / sizeof(int);
           int s;
           if (!begun) s = p.first[index];
-          else if (index < total1) s = find_seq(p.S, index, lane, [&](int i) { return p.seq[i].before1; });
-          else s = find_seq(p.S, index - total1, lane, [&](int i) { return p.seq[i].before2; });
+          else s = find_seq(p.S, piece, lane, [&](int i) { return before[static_cast<size_t>(i) * kStep]; });
           begun = true;
           const ChunkSeq q = p.seq[s];
-          const int in = index < total1 ? index - q.before1 : index - total1 - q.before2;
+          const int in = piece - (is_long ? q.before1 : q.before2);
           // tiles first (the last ones, which see most keys, lead), then parts, then heads
-          const int cut = in / q.nt % q.cuts;
-          const int hkv = in / q.nt / q.cuts;
+          const int u = in / q.nt, hkv = u / q.cuts;
+          int cut = u - hkv * q.cuts, cuts = q.cuts;
           const SeqRows r{q.a, q.b, q.n, q.shift, false, false};
-          const Tile t = seq_tile(r, q.nt - 1 - in % q.nt, p.tpt);
+          const Tile t = seq_tile(r, q.nt - 1 - (in - u * q.nt), p.tpt);
           x.s = s;
           x.t0 = t.t0;
           x.p0 = t.p0;
           x.heads = hkv << 8 | t.ntok;
-          x.kb = tile_blocks(p, t, r.n);
-          if (q.cuts > 1) x.kb = x.kb.part(cut, q.cuts);
-          x.slot = q.cuts > 1 ? q.slot0 + in : -1;
+          x.slot = cuts > 1 ? q.slot0 + in : -1;
+          if (is_long && over >= 0) {
+            cut = cut * plan.fine + sub;
+            cuts *= plan.fine;
+            x.slot = plan.tail_slot + (piece - plan.tail) * plan.fine + sub;
+          }
+          x.kb = tile_blocks(p, t, r.n).part(cut, cuts);
           if (t.p0 < 0 && lane == 0) record_error(p.err, ATTN_ERR_BAD_PAGES);
           if (x.kb.count() > 0) return true;
           if (x.slot >= 0) {                               // a part without keys
             float* l = p.part + static_cast<size_t>(x.slot) * C::kPartFloats + kTileM * (D + 1);
+#pragma unroll 1
             for (int i = lane; i < kTileM; i += 32) l[i] = 0.f;
           } else {                                         // rows that see nothing
-            for (int i = 0; i < x.ntok() * p.G; ++i) {
-              const size_t row = static_cast<size_t>(x.t0 + i / p.G) * p.H + x.hkv() * p.G + i % p.G;
-              for (int e = lane; e < D; e += 32) p.o[row * D + e] = __float2bfloat16(0.f);
-              if (lane == 0) p.lse[row] = NEG_INF;
+#pragma unroll 1
+            for (int i = 0; i < x.ntok(); ++i) {
+              const size_t row = static_cast<size_t>(x.t0 + i) * p.H + x.hkv() * p.G;
+#pragma unroll 1
+              for (int e = lane; e < p.G * (D / 8); e += 32)
+                reinterpret_cast<uint4*>(p.o + row * D)[e] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+              for (int g = lane; g < p.G; g += 32) p.lse[row + g] = NEG_INF;
             }
           }
         }
@@ -1450,60 +1493,73 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
   const int col = static_cast<int>(blockIdx.y) * 16 + static_cast<int>(threadIdx.x >> 7) * 8;
   const int tok = row / p.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");      // the parts are complete
-  const int joins = p.plan->joins;
-  for (int j = static_cast<int>(blockIdx.x); j < joins; j += static_cast<int>(gridDim.x)) {
-    const int s = find_seq(p.S, j, lane, [&](int i) { return p.seq[i].join0; });
+  const ChunkPlan plan = *p.plan;
+  for (int j = static_cast<int>(blockIdx.x); j < plan.joins; j += static_cast<int>(gridDim.x)) {
+    // a tile of a sequence whose tiles are cut; or a piece of the tail (a tile), if its
+    // sequence's are not
+    const bool whole = j >= plan.tail_join;
+    const int piece = plan.tail + j - plan.tail_join;
+    const int s = whole ? find_seq(p.S, piece, lane, [&](int i) { return p.seq[i].before1; })
+                        : find_seq(p.S, j, lane, [&](int i) { return p.seq[i].join0; });
     const ChunkSeq q = p.seq[s];
+    if (whole && q.cuts > 1) continue;
     const SeqRows r{q.a, q.b, q.n, q.shift, false, false};
-    const int cuts = q.cuts, nt = q.nt;
-    const int in = j - q.join0;
+    const int nt = q.nt;
+    const int in = whole ? piece - q.before1 : j - q.join0;
     const int hkv = in / nt, i = in % nt;                 // the tile's number among its pieces'
     const Tile t = seq_tile(r, nt - 1 - i, p.tpt);
+    // its pieces are numbers first, first + nt ..: `plain` of them have one part, those in
+    // the tail `fine` each
+    const int first = hkv * q.cuts * nt + i;
+    const int plain = q.longest == 0 ? q.cuts : max(0, min(q.cuts, (plan.tail - q.before1 - first + nt - 1) / nt));
     if (tok >= t.ntok) continue;
-    const float* part = p.part + static_cast<size_t>(q.slot0 + hkv * cuts * nt + i) * kPart;
-    const size_t step = static_cast<size_t>(nt) * kPart;  // from part to part
     float m = NEG_INF, l = 0.f, y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = 0.f;
-    // four parts' loads are in flight together (past the last one the last is read
-    // again, and not counted)
-    constexpr int kBatch = 4;
-    for (int c0 = 0; c0 < cuts; c0 += kBatch) {
-      float lc[kBatch], mc[kBatch];
-      float4 v[kBatch][2];
+    // parts `slot`, slot + step .. are added, four's loads in flight together (past the
+    // last one the last is read again, and not counted)
+    auto add = [&](int slot, int step, int parts) {
+      constexpr int kBatch = 4;
+      for (int c0 = 0; c0 < parts; c0 += kBatch) {
+        float lc[kBatch], mc[kBatch];
+        float4 v[kBatch][2];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const float* x = part + min(c0 + u, cuts - 1) * step;
-        mc[u] = x[kTileM * D + row];
-        lc[u] = c0 + u < cuts ? x[kTileM * (D + 1) + row] : 0.f;
-        const float4* a = reinterpret_cast<const float4*>(x) + col / 4 * kTileM + row;
-        v[u][0] = a[0];
-        v[u][1] = a[kTileM];
-      }
-      float top = m;
+        for (int u = 0; u < kBatch; ++u) {
+          const float* x = p.part + static_cast<size_t>(slot + min(c0 + u, parts - 1) * step) * kPart;
+          mc[u] = x[kTileM * D + row];
+          lc[u] = c0 + u < parts ? x[kTileM * (D + 1) + row] : 0.f;
+          const float4* a = reinterpret_cast<const float4*>(x) + col / 4 * kTileM + row;
+          v[u][0] = a[0];
+          v[u][1] = a[kTileM];
+        }
+        float top = m;
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) top = lc[u] != 0.f ? fmaxf(top, mc[u]) : top;
-      if (top != m) {                                     // (of the first four: from -inf, 0 to 0)
-        const float w = ex2(m - top);
-        l *= w;
+        for (int u = 0; u < kBatch; ++u) top = lc[u] != 0.f ? fmaxf(top, mc[u]) : top;
+        if (top != m) {                                   // (at first: from -inf, 0 stays 0)
+          const float w = ex2(m - top);
+          l *= w;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= w;
-        m = top;
-      }
+          for (int e = 0; e < 8; ++e) y[e] *= w;
+          m = top;
+        }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (lc[u] == 0.f) continue;                       // this part saw no key
-        const float w = ex2(mc[u] - m);
-        l = fmaf(w, lc[u], l);
+        for (int u = 0; u < kBatch; ++u) {
+          if (lc[u] == 0.f) continue;                     // this part saw no key
+          const float w = ex2(mc[u] - m);
+          l = fmaf(w, lc[u], l);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          y[4 * e] = fmaf(w, v[u][e].x, y[4 * e]);
-          y[4 * e + 1] = fmaf(w, v[u][e].y, y[4 * e + 1]);
-          y[4 * e + 2] = fmaf(w, v[u][e].z, y[4 * e + 2]);
-          y[4 * e + 3] = fmaf(w, v[u][e].w, y[4 * e + 3]);
+          for (int e = 0; e < 2; ++e) {
+            y[4 * e] = fmaf(w, v[u][e].x, y[4 * e]);
+            y[4 * e + 1] = fmaf(w, v[u][e].y, y[4 * e + 1]);
+            y[4 * e + 2] = fmaf(w, v[u][e].z, y[4 * e + 2]);
+            y[4 * e + 3] = fmaf(w, v[u][e].w, y[4 * e + 3]);
+          }
         }
       }
-    }
+    };
+    add(q.slot0 + first, nt, plain);
+    for (int c = plain; c < q.cuts; ++c)
+      add(plan.tail_slot + (q.before1 + first + c * nt - plan.tail) * plan.fine, 1, plan.fine);
     float inv = l == 0.f ? 0.f : 1.f / l;
     if constexpr (FP8) inv *= __ldg(p.v_scale + hkv);
     const size_t at = static_cast<size_t>(t.t0 + tok) * p.H + hkv * p.G + row - tok * p.G;

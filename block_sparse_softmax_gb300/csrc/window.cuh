@@ -38,7 +38,9 @@ struct WindowBlocks {
   // Part `rank` of `split` parts of about as many pairs of blocks each.
   __device__ __forceinline__ WindowBlocks part(int rank, int split) const {
     const int pairs = (count() + 1) / 2;
-    const int b0 = 2 * (pairs * rank / split), b1 = min(count(), 2 * (pairs * (rank + 1) / split));
+    const int each = pairs / split, rest = pairs % split;      // (pairs * rank may need more than 32 bits)
+    const int b0 = 2 * (each * rank + rest * rank / split);
+    const int b1 = min(count(), 2 * (each * (rank + 1) + rest * (rank + 1) / split));
     const int w0 = max(b0 - nsb, 0);
     return WindowBlocks{max(min(b1, nsb) - b0, 0), wb0 + w0, max(b1 - nsb, 0) - w0, b0};
   }

@@ -27,7 +27,7 @@ def test_a_warp_of_the_chunk_kernel_leaves_a_wait_as_one():
         text = re.sub(r"//[^\n]*", "", f.read())
     begin = text.index("attn_fwd_paged_kernel(")
     text = text[begin:text.index("chunk_join_kernel(")]
-    mma = text.index("if (lane == 0) {", text.index("warp == 13")), text.index("warp == 14")   # one thread
+    mma = text.index("if (elect_one()) {", text.index("warp == 13")), text.index("warp == 14")   # one thread
     votes = list(spans(text, "__all_sync"))
     waits = [m.start() for m in re.finditer(r"\bwait_bar(_relaxed)?\(", text)]
     assert len(waits) >= 15

@@ -608,3 +608,21 @@ def test_selection_in_a_graph(bss):
         for x, y in zip(out[2:], want[2:]):
             assert torch.equal(x[cu[0]:cu[2]], y[cu[0]:cu[2]])
     assert bss.attn_poll_status() == 0
+
+
+# (equal prompts: the last turn's tiles are cut once more; 60 tiles a K/V head of whole ones, of ones
+# that are cut already, and beside sequences of a few keys; with and without a window)
+TAIL = [
+    ([9000] * 3, [1900, 1920, 1900], 8, 2, 128, 0, 0),
+    ([4200] * 4 + [3, 900, 0], [1024] * 4 + [1, 1, 0], 16, 4, 128, 0, 0),
+    ([6000] * 5, [1100] * 5, 8, 8, 64, 2500, 3),
+    ([20000], [2600], 8, 2, 64, 0, 0),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens,news,H,Hkv,d,window,sinks", TAIL)
+def test_chunk_of_equal_tiles(bss, lens, news, H, Hkv, d, window, sinks, e4m3):
+    c = Cache(lens, Hkv, d, 64, d + Hkv, e4m3)
+    q, cu = ragged(news, H, d, 4)
+    check_chunk(bss, c, q, cu, lens, news, window=window, sinks=sinks)

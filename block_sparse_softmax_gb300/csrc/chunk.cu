@@ -479,9 +479,9 @@ struct ChunkCfg {
 
 // Register split per warpgroup (setmaxnreg): output and conversion (warps 0-3),
 // softmax (4-7, 8-11), K and Q, MMA, pieces and V (12 to 15).
-constexpr uint32_t kChunkOut = 48;
+constexpr uint32_t kChunkOut = 64;
 constexpr uint32_t kChunkSoft = 192;
-constexpr uint32_t kChunkLow = 80;
+constexpr uint32_t kChunkLow = 64;
 constexpr uint32_t kChunkLaunchRegs = 128;
 static_assert(kChunkOut + 2 * kChunkSoft + kChunkLow <= 4 * kChunkLaunchRegs, "register split exceeds the launch");
 constexpr int kWantPairs = 6;               // pairs of a piece that are left when the next one is chosen
@@ -1071,30 +1071,29 @@ __global__ void __launch_bounds__(512, 1)
       const size_t at = static_cast<size_t>(x.t0 + tok) * p.H + x.hkv() * p.G + head;
       uint4* dst = reinterpret_cast<uint4*>(p.o + at * D);
       float4* part = reinterpret_cast<float4*>(p.part + static_cast<size_t>(max(x.slot, 0)) * C::kPartFloats) + row;
-      // 16 columns at a time (the warpgroup has few registers); a row without a
+      // 32 columns at a time (the warpgroup has few registers); a row without a
       // key (inv = 0) is 0 whatever the masked keys held
 #pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t o[16];
-        tmem_ld16(tO + c * 16, o);
-        tmem_ld_wait16(o);
-        if (c == D / 16 - 1) {
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_ld_wait(o);
+        if (c == D / 32 - 1) {
           tc_fence_before();
           mbar_arrive(bar(C::kBarOEmpty));      // the next piece's P V may overwrite O
         }
         if (!inb) continue;
         if (x.slot >= 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            part[(4 * c + e) * kTileM] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+          for (int e = 0; e < 8; ++e)
+            part[(8 * c + e) * kTileM] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                                      __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
         } else {
-          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[e] = inv == 0.f ? 0u : pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          dst[2 * c] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[2 * c + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int e = 0; e < 16; ++e)
+            o[e] = inv == 0.f ? 0u : pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[4 * c + e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       ++on;

@@ -22,8 +22,11 @@
 //     are parts of a tile's keys, of about equal length, and CTAs take them by a
 //     counter.  A sequence's pieces are numbered so that those that run at the
 //     same time share their keys (tiles first, then key parts): L2 serves all but
-//     one of them.  The parts of a tile leave (m, l, A) in the workspace, and a
-//     last kernel joins them in order (so the counter does not show in a bit).
+//     one of them.  Where pieces are whole tiles, or few a CTA, those of the last
+//     turn are cut once more (4 x 1000 tokens at 16384: 473 us with all tiles in two
+//     parts, 424 with whole ones and the last 132 of 512 in four).  The parts of a
+//     tile leave (m, l, A) in the workspace, and a last kernel joins them in order
+//     (so the counter does not show in a bit).
 //   * e4m3 pages are read as they are.  K stays so: Q, scaled row by row by a power
 //     of two (largest element in [128, 256)), is held as two 8-bit parts, e4m3 and
 //     the rest in e5m2.  A bf16 element's 8 bits less the first part's 4 leave 3
@@ -36,6 +39,18 @@
 //     Over bf16 pages P is rounded to bf16, V's type.
 // Rows of the caches that hold no token may hold anything: V's are set to zero in
 // shared memory, S's are masked.
+//
+// Measured (GB300, d=128, 16 query heads on 4 K/V heads where not said; of the
+// bf16 GEMM's 1929 TFLOP/s): 500 tokens at 8191 45 us; 32 sequences of up to 8192,
+// every fourth with 512 tokens 139 us, 44 %; 1024 tokens at 131071, 8 heads of their
+// own 376 us, 75 %, and every key from HBM once; 4 x 1000 at 16384 over e4m3 428 us,
+// 63 %; d=64, window 1000, 16 heads of their own, 6 x <= 700 64 us.  A pair of blocks
+// takes 2900 to 3050 cycles (e4m3 3350) for 2048 of MMAs at their peak rate: the
+// softmax warps' 570 for the mask and maximum, 320 to exchange it, 1350 for the
+// exponentials (1024 at their unit's rate) and the rest in hand-offs.  Of
+// short pieces (d=64 with a window: 6 pairs) their beginning and end, 6000 cycles,
+// take a third.  Few rows: plan 4 us, then lengths, table, pages, 2 pairs and O, one
+// after the other (8 x 5 tokens of 300: 16.5 us).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -130,7 +145,7 @@ __device__ __forceinline__ WindowBlocks tile_blocks(const ChunkParams& p, const 
 
 // ----------------------------------------------------------------------------
 // the plan: one CTA, which the main kernel waits for: what counts is the chain of
-// its steps (4 us with one instruction stream for all lengths of parts, 13 with
+// its steps (4 to 6 us with one instruction stream for all lengths of parts, 13 with
 // every thread weighing all of them)
 // ----------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
@@ -283,7 +298,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
       v.w += tail * fine;
       if (v.x - tail < ctas || each < 6.f || p.slots == 0) t = 3.4e38f;
     }
-    // the join: 6 us and 7 ns a part, in the 1.75 us that a pair takes
+    // the join: 5.4 us and 6 ns a part, in the 1.55 us that a pair takes
     t += v.w > 0.f ? 3.5f + 0.004f * v.w : 0.f;
     if (lane > 0 && v.w > static_cast<float>(p.slots)) t = 3.4e38f;
     int best = lane;
@@ -479,6 +494,7 @@ struct ChunkCfg {
 
 // Register split per warpgroup (setmaxnreg): output and conversion (warps 0-3),
 // softmax (4-7, 8-11), K and Q, MMA, pieces and V (12 to 15).
+// (Output 48 and producers 80, O by 16 columns: bf16 1 to 3 % slower, e4m3 1 % faster.)
 constexpr uint32_t kChunkOut = 64;
 constexpr uint32_t kChunkSoft = 192;
 constexpr uint32_t kChunkLow = 64;
@@ -511,7 +527,7 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
 }
 // One thread of a converged warp, and the compiler knows it: an MMA's operands are
 // the warp's, and behind `lane == 0` each MMA's code has to find whose they are (23
-// KB of code for the MMA thread instead of 15).
+// KB of code for the MMA thread instead of 15: 1024 tokens at 131071 412 us, so 378).
 __device__ __forceinline__ bool elect_one() {
   uint32_t yes;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
@@ -667,8 +683,8 @@ __global__ void __launch_bounds__(512, 1)
       // Two warps, for V has no time to lose at d=128: with two stages a block can be
       // asked for when the one two before it has been used, and is wanted 2200 cycles
       // later.  What one warp had to do for K and V between that and the copy cost up
-      // to a third of everything (1024 tokens at 131071: 413 to 540 us).  So all that
-      // a copy needs is computed before the wait for its stage.
+      // to a third of everything (1024 tokens at 131071, at the time: 413 to 540 us).  So
+      // all that a copy needs is computed before the wait for its stage.
       const bool is_v = warp == 15;
       const CUtensorMap* map = is_v ? &tmV : &tmK;
       if (lane == 0) {
@@ -1030,7 +1046,7 @@ __global__ void __launch_bounds__(512, 1)
 
       // A piece is chosen late, when few pairs of the one before it are left to be
       // asked for: chosen a piece ahead, the last ones waited behind others while
-      // CTAs had nothing to do (1024 tokens at 131071: 557 us, so 425).
+      // CTAs had nothing to do (1024 tokens at 131071, at the time: 557 us, so 425).
       Piece x;
       bool more = true;
       while (more) {

@@ -573,16 +573,26 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
   uint32_t* taken = keys + p.M;
   const int words = (row.held + 31) / 32;
   // a warp a word: what is taken anyway; the candidates are marked (1: a page, 0: none)
+  constexpr int kAhead = 4;                              // loads in flight
   int mine = 0;
-  for (int w = warp; w < words; w += NT / 32) {
-    const int m = 32 * w + lane;
-    const int pg = m < row.held ? __ldg(tab + m) : -1;
-    const bool is = pg >= 0 && pg < p.P, scored = m >= begin && m < end;
-    if (!is && pg != -1 && !scored) record_error(p.err, ATTN_ERR_BAD_PAGES);
-    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, is && !scored);
-    if (lane == 0) taken[w] = bits;
-    if (scored) keys[m] = is ? 1u : 0u;
-    mine += is && scored;
+  for (int w0 = warp; w0 < words; w0 += kAhead * (NT / 32)) {
+    int pg[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int m = 32 * (w0 + u * (NT / 32)) + lane;
+      pg[u] = m < row.held ? __ldg(tab + m) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int w = w0 + u * (NT / 32), m = 32 * w + lane;
+      if (w >= words) break;
+      const bool is = pg[u] >= 0 && pg[u] < p.P, scored = m >= begin && m < end;
+      if (!is && pg[u] != -1 && !scored) record_error(p.err, ATTN_ERR_BAD_PAGES);
+      const uint32_t bits = __ballot_sync(0xFFFFFFFFu, is && !scored);
+      if (lane == 0) taken[w] = bits;
+      if (scored) keys[m] = is ? 1u : 0u;
+      mine += is && scored;
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");      // the scores are there
 #pragma unroll
@@ -611,16 +621,23 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
   float lo = __int_as_float(0x7f800000), hi = -lo;
   bool odd = false;
   if (choose)
-    for (int m = begin + tid; m < end; m += NT) {
-      if (keys[m] == 0u) {
-        keys[m] = kNoScore;
-        continue;
+    for (int m0 = begin + tid; m0 < end; m0 += kAhead * NT) {
+      float x[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) x[u] = m0 + u * NT < end ? score[m0 + u * NT] : 0.f;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int m = m0 + u * NT;
+        if (m >= end) break;
+        if (keys[m] == 0u) {
+          keys[m] = kNoScore;
+          continue;
+        }
+        odd = odd || x[u] != x[u];
+        lo = fminf(lo, x[u]);
+        hi = fmaxf(hi, x[u]);
+        keys[m] = __float_as_uint(x[u]);
       }
-      const float x = score[m];
-      odd = odd || x != x;
-      lo = fminf(lo, x);
-      hi = fmaxf(hi, x);
-      keys[m] = __float_as_uint(x);
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -776,12 +793,13 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
     }
   }
   __syncthreads();
-  // the list, in ascending order
+  // the list, in ascending order: where each word's pages begin (in keys' place), then
+  // a warp a word, so that the table's entries come together
   int base = 0;
   for (int w0 = 0; w0 < words; w0 += NT) {
     const int w = w0 + tid;
-    uint32_t bits = w < words ? taken[w] : 0u;
-    int x = __popc(bits);
+    const int count = w < words ? __popc(taken[w]) : 0;
+    int x = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
@@ -789,12 +807,17 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
     }
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    int place = base + x - __popc(bits);
+    int place = base + x - count;
     for (int v = 0; v < warp; ++v) place += sums[v];
-    for (; bits != 0u; bits &= bits - 1, ++place)
-      if (place < p.R) out[place] = __ldg(tab + 32 * w + __ffs(bits) - 1);
+    if (w < words) keys[w] = static_cast<uint32_t>(place);
     for (int v = 0; v < NT / 32; ++v) base += sums[v];
     __syncthreads();
+  }
+#pragma unroll 4
+  for (int w = warp; w < words; w += NT / 32) {
+    const uint32_t bits = taken[w];
+    const int place = static_cast<int>(keys[w]) + __popc(bits & ((1u << lane) - 1u));
+    if ((bits >> lane & 1u) && place < p.R) out[place] = __ldg(tab + 32 * w + lane);
   }
   for (int i = base + tid; i < p.R; i += NT) out[i] = -1;
   if (tid == 0 && h == 0) {

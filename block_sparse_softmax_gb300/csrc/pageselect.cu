@@ -324,25 +324,26 @@ __global__ void __launch_bounds__(kScoreWarps * 32) select_score_kernel(const Se
 }
 
 // Chunks: 32 rows share the means of 128 pages of their sequence in shared memory
-// (read from L2 once for 32 rows), a thread two pages and 16 rows: a dot product is
-// a chain of d fused multiply-adds.  500 rows of 1024 pages, 4 K/V heads: 34 us;
-// with a warp a page and sums over its lanes, 8 rows at a time, 142, with a page and
-// 16 rows a thread 42.
+// (read from L2 once for 32 rows), a thread two pages and 8 rows: a dot product is
+// a chain of d fused multiply-adds.  500 rows of 1024 pages, 4 K/V heads: 31 us; half
+// the threads, 16 rows each 34; a warp a page and sums over its lanes, 8 rows at a
+// time, 142.
 constexpr int kTileRows = 32;
 constexpr int kTilePages = 128;
+constexpr int kTileThreads = 256;
 template <int D>
 struct ScoreTile {
   static constexpr int kRow = D + 4;          // floats from page to page: 16 bytes of 8 pages hit 8 different banks
   static constexpr int kSmem = (kTilePages * kRow + kTileRows * D) * 4;
 };
 template <int D>
-__global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kTileThreads) select_score_tile_kernel(const SelectParams p) {
   using C = ScoreTile<D>;
   extern __shared__ __align__(16) float score_smem[];
   float* means = score_smem;                  // [pages][kRow]
   float* qsum = score_smem + kTilePages * C::kRow;             // [rows][D]
   __shared__ int row_s[kTileRows], row_end[kTileRows];
-  __shared__ float top[kTilePages / 32];
+  __shared__ float top[kTileThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const Sel
   const int r0 = static_cast<int>(blockIdx.y) * kTileRows;
   const int nr = min(kTileRows, p.rows - r0);
   // the group's sums, 8 columns a thread
-  for (int i = tid; i < kTileRows * D / 8; i += kTilePages) {
+  for (int i = tid; i < kTileRows * D / 8; i += kTileThreads) {
     const int r = i / (D / 8), e = i % (D / 8) * 8;
     float sum[8];
 #pragma unroll
@@ -393,6 +394,7 @@ __global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const Sel
     }
   }
   __syncthreads();
+  constexpr int kWarpPages = kTilePages / (kTileThreads / 32);
   float seen = 0.f;                           // the largest element met, for any of the rows
   for (int a = 0; a < nr;) {                  // runs of rows of one sequence
     const int s = row_s[a];
@@ -402,15 +404,16 @@ __global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const Sel
     for (long long m1 = p.first + static_cast<long long>(blockIdx.x) * kTilePages; s >= 0 && m1 < end;
          m1 += static_cast<long long>(p.parts) * kTilePages) {
       const int m0 = static_cast<int>(m1);
-      int pg = m0 + tid < end ? __ldg(tab + m0 + tid) : -1;
+      const int mine = warp * kWarpPages + lane;           // of its warp's pages
+      int pg = lane < kWarpPages && m0 + mine < end ? __ldg(tab + m0 + mine) : -1;
       if (pg >= p.P || pg < -1) {
         record_error(p.err, ATTN_ERR_BAD_PAGES);
         pg = -1;
       }
       __syncthreads();                        // the tile before has been read
-      // a warp its 32 pages, 8 rows of means in flight
+      // a warp its pages, 8 rows of means in flight
 #pragma unroll 1
-      for (int u0 = 0; u0 < 32; u0 += 8) {
+      for (int u0 = 0; u0 < kWarpPages; u0 += 8) {
         float4 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -424,11 +427,11 @@ __global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const Sel
           seen = larger_or_nan(larger_or_nan(seen, fabsf(v[u].x)), fabsf(v[u].y));
           seen = larger_or_nan(larger_or_nan(seen, fabsf(v[u].z)), fabsf(v[u].w));
           if (lane * 4 < D)
-            *reinterpret_cast<float4*>(means + (warp * 32 + u0 + u) * C::kRow + lane * 4) = v[u];
+            *reinterpret_cast<float4*>(means + (warp * kWarpPages + u0 + u) * C::kRow + lane * 4) = v[u];
         }
       }
       __syncthreads();
-      constexpr int kHalf = kTileRows / 2;
+      constexpr int kHalf = kTileRows / (kTileThreads / 64);
       const int x0 = tid & 63, rh = tid / 64 * kHalf;      // pages x0 and x0 + 64, rows rh ..
       float acc[2][kHalf];
 #pragma unroll
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kTilePages) select_score_tile_kernel(const Sel
   __syncthreads();
   if (tid < nr) {
     float x = 0.f;
-    for (int w = 0; w < kTilePages / 32; ++w) x = larger_or_nan(x, top[w]);
+    for (int w = 0; w < kTileThreads / 32; ++w) x = larger_or_nan(x, top[w]);
     p.norm[(static_cast<size_t>(r0 + tid) * p.Hkv + h) * p.parts + blockIdx.x] = x;
   }
 }
@@ -917,7 +920,7 @@ cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
     p.rows = std::min(chunk, p.T - t0);
     const dim3 grid(p.parts, (p.rows + RT - 1) / RT, p.Hkv);
     if (RT == 1) select_score_kernel<D><<<grid, kScoreWarps * 32, 0, st>>>(p);
-    else select_score_tile_kernel<D><<<grid, kTilePages, ScoreTile<D>::kSmem, st>>>(p);
+    else select_score_tile_kernel<D><<<grid, kTileThreads, ScoreTile<D>::kSmem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // the pick is set up while the scores are made, and waits for them itself
     cudaLaunchAttribute attr{};

@@ -1509,6 +1509,9 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
   const int tok = row / p.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");      // the parts are complete
   const ChunkPlan plan = *p.plan;
+  if (static_cast<int>(blockIdx.x) >= plan.joins) return;
+  // (a launch that gave up left parts unwritten)
+  if (__syncthreads_or(status_at_entry(p.err) == ATTN_ERR_TIMEOUT)) return;
   for (int j = static_cast<int>(blockIdx.x); j < plan.joins; j += static_cast<int>(gridDim.x)) {
     // a tile of a sequence whose tiles are cut; or a piece of the tail (a tile), if its
     // sequence's are not

@@ -626,3 +626,20 @@ def test_chunk_of_equal_tiles(bss, lens, news, H, Hkv, d, window, sinks, e4m3):
     c = Cache(lens, Hkv, d, 64, d + Hkv, e4m3)
     q, cu = ragged(news, H, d, 4)
     check_chunk(bss, c, q, cu, lens, news, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_launch_after_a_timeout_stops(bss, e4m3):
+    """With a timeout in the status word a launch stops, block by block, with parts to be joined or
+    without, and leaves its outputs; once the word is read and cleared the same call is right."""
+    for lens, news in (([300, 40], [5, 40]), ([9000], [300])):
+        c = Cache(lens, 2, 128, 16, 9, e4m3)
+        q, cu = ragged(news, 8, 128, 2)
+        o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 3.0, device="cuda")
+        bss.attn_watchdog_selftest(1 << 16)
+        for _ in range(2):
+            bss.attn_fwd_paged(q, c.k, c.v, c.table, c.lens, ints(cu), k_scale=c.k_scale, v_scale=c.v_scale,
+                               out=o, lse=lse)
+        assert bss.attn_poll_status() == bss.ERR_TIMEOUT
+        assert (o == 7.0).all() and (lse == 3.0).all()
+        check_chunk(bss, c, q, cu, lens, news)

@@ -20,9 +20,10 @@
 //     rows, a lane of the producer warp each.
 //   * The work is cut on the GPU, from the lengths (chunk_plan_kernel): pieces
 //     are parts of a tile's keys, of about equal length, and CTAs take them by a
-//     counter.  A sequence's pieces are numbered so that those that run at the
-//     same time share their keys (tiles first, then key parts): L2 serves all but
-//     one of them.  Where pieces are whole tiles, or few a CTA, those of the last
+//     counter, longest first (32 sequences of up to 8192, every fourth with 512
+//     tokens: 140 us with two kinds of pieces in no order otherwise, 122 so).  A
+//     sequence's pieces are numbered so that those that run at the same time share
+//     their keys (tiles first, then key parts): L2 serves all but one of them.  Where pieces are whole tiles, or few a CTA, those of the last
 //     turn are cut once more (4 x 1000 tokens at 16384: 473 us with all tiles in two
 //     parts, 424 with whole ones and the last 132 of 512 in four).  The parts of a
 //     tile leave (m, l, A) in the workspace, and a last kernel joins them in order
@@ -42,7 +43,7 @@
 //
 // Measured (GB300, d=128, 16 query heads on 4 K/V heads where not said; of the
 // bf16 GEMM's 1929 TFLOP/s): 500 tokens at 8191 45 us; 32 sequences of up to 8192,
-// every fourth with 512 tokens 139 us, 44 %; 1024 tokens at 131071, 8 heads of their
+// every fourth with 512 tokens 122 us, 50 %; 1024 tokens at 131071, 8 heads of their
 // own 376 us, 75 %, and every key from HBM once; 4 x 1000 at 16384 over e4m3 428 us,
 // 63 %; d=64, window 1000, 16 heads of their own, 6 x <= 700 64 us.  A pair of blocks
 // takes 2900 to 3050 cycles (e4m3 3350) for 2048 of MMAs at their peak rate: the
@@ -75,14 +76,14 @@ struct ChunkPlan {
   int joins;                 // (tile, K/V head)s that are joined: those of cut sequences, then the tail's pieces
   int tail, fine, tail_slot, tail_join;
 };
-// Of a sequence: pieces of either kind, slots and joins before it; its rows
-// (SeqRows); the parts that its tiles' keys are cut into; its work (SeqWork; 0 for
-// `longest` says that its pieces are not long ones).
+// Of a sequence, in the order of their pieces' lengths, longest first: pieces, slots
+// and joins before it; its number and rows (SeqRows); the parts that its tiles' keys
+// are cut into; its tiles; whether its pieces are long ones (1) or others (0).
 struct __align__(16) ChunkSeq {
-  int before1, before2, slot0, join0;
+  int before, slot0, join0, s;
   int a, b, n, cuts;
   long long shift;
-  int nt, longest;
+  int nt, kind;
 };
 
 struct ChunkParams {
@@ -150,6 +151,7 @@ __device__ __forceinline__ WindowBlocks tile_blocks(const ChunkParams& p, const 
 // ----------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCuts = 16;              // lengths of parts that are weighed
+constexpr int kPlanSorted = 256;           // sequences that are sorted
 struct SeqWork {
   int nt, longest;           // tiles; pairs of key blocks of its longest tile
   float mean;                // ... of a tile
@@ -168,7 +170,7 @@ __device__ __forceinline__ SeqWork seq_work(const ChunkParams& p, const SeqRows&
 __device__ __forceinline__ int seq_cuts(int longest, int len) {
   return longest <= len ? 1 : (longest + len - 1) / len;
 }
-// ... whether those are long pieces, which go first.
+// ... whether those are long pieces: more than half of it.
 __device__ __forceinline__ bool long_pieces(int longest, int cuts, int len) {
   return 2ll * longest > static_cast<long long>(len) * cuts;
 }
@@ -202,6 +204,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   __shared__ float2 tops[kPlanThreads / 32];
   __shared__ int4 scan[kPlanThreads / 32];
   __shared__ SeqWork works[kPlanThreads];
+  __shared__ float keys[kPlanSorted];
+  __shared__ int4 sorted[kPlanSorted];
   __shared__ int chosen, chosen_tail, chosen_fine;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -213,18 +217,12 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   // H; where they do not, nothing is done.)
   float2 top = make_float2(0.f, 0.f);
   bool disorder = false;
+  SeqRows mine{0, 0, 0, 0, false, false};          // (the last one's: the only one's, of few)
   for (int s = tid; s < p.S; s += kPlanThreads) {
-    const SeqRows r = seq_rows(p, s);
-    const SeqWork w = seq_work(p, r);
-    if (r.bad || r.disorder) record_error(p.err, ATTN_ERR_BAD_PAGES);
-    disorder = disorder || r.disorder;
-    ChunkSeq* q = p.seq + s;
-    q->a = r.a;
-    q->b = r.b;
-    q->n = r.n;
-    q->shift = r.shift;
-    q->nt = w.nt;
-    q->longest = w.longest;
+    mine = seq_rows(p, s);
+    const SeqWork w = seq_work(p, mine);
+    if (mine.bad || mine.disorder) record_error(p.err, ATTN_ERR_BAD_PAGES);
+    disorder = disorder || mine.disorder;
     if (few) works[s] = w;
     top.x = fmaxf(top.x, static_cast<float>(w.longest));
     top.y += w.mean * static_cast<float>(w.nt);
@@ -254,47 +252,44 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   const float turns = 0.5f * exp2f(static_cast<float>(cand - 1) * 0.3f);
   const int whole = max(1, longest);
   const int my_len = cand == 0 ? whole : min(whole, max(kLeastPairs, static_cast<int>(ceilf(share / turns))));
-  // long pieces, their pairs with what a piece costs beside them; the others' pairs; slots
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  // long pieces; all pairs, with what a piece costs beside them; the shortest long
+  // piece; slots
+  float4 v = make_float4(0.f, 0.f, 3.4e38f, 0.f);
   for (int s = tid / kPlanCuts; s < p.S; s += kPlanThreads / kPlanCuts) {
     const SeqWork w = few ? works[s] : seq_work(p, seq_rows(p, s));
     const float tiles = static_cast<float>(w.nt) * static_cast<float>(p.Hkv);
     const int cuts = seq_cuts(w.longest, my_len);
     // about a pair's time to begin and end a piece, as much again to leave a part
-    const float cost = tiles * (w.mean + static_cast<float>(cuts) * (cuts > 1 ? 2.f : 1.f));
+    const float beside = cuts > 1 ? 2.f : 1.f;
+    v.y += tiles * (w.mean + static_cast<float>(cuts) * beside);
     if (long_pieces(w.longest, cuts, my_len)) {
       v.x += tiles * static_cast<float>(cuts);
-      v.y += cost;
-    } else {
-      v.z += cost;
+      v.z = fminf(v.z, w.mean / static_cast<float>(cuts) + beside);
     }
     if (cuts > 1) v.w += tiles * static_cast<float>(cuts);
   }
-  v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, 16);
-  v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, 16);
-  v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, 16);
-  v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, 16);
+  auto add = [](const float4& a, const float4& b) {
+    return make_float4(a.x + b.x, a.y + b.y, fminf(a.z, b.z), a.w + b.w);
+  };
+  v = add(v, make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, 16), __shfl_xor_sync(0xFFFFFFFFu, v.y, 16),
+                         __shfl_xor_sync(0xFFFFFFFFu, v.z, 16), __shfl_xor_sync(0xFFFFFFFFu, v.w, 16)));
   if (lane < kPlanCuts) sums[warp][lane] = v;
   __syncthreads();
   if (warp == 0) {
     const int used = min(kPlanThreads / 32, (p.S + 1) / 2);
-    v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = 0; w < used; ++w) {
-      const float4 y = sums[w][cand];
-      v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
-    }
-    const float each = v.x > 0.f ? v.y / v.x : 0.f, rounds = ceilf(v.x / ctas);
-    const float idle = (rounds * ctas - v.x) * each;
-    // the long pieces' turns, and what does not fit beside the last of them
-    float t = rounds * each + fmaxf(0.f, v.z - idle) / ctas;
-    // ... or, as the second half of the warp weighs it, the last turn's pieces and some
-    // more cut once more: all CTAs end together but for half a piece of those
+    v = sums[0][cand];
+    for (int w = 1; w < used; ++w) v = add(v, sums[w][cand]);
+    const float each = v.x > 0.f ? v.z : 0.f;
+    // everybody's share, where the long pieces' turns do not take longer
+    float t = fmaxf(v.y / ctas, ceilf(v.x / ctas) * each);
+    // ... or, as the second half of the warp weighs it, the last turn's long pieces and
+    // some more cut once more: all CTAs end together but for half a piece of those
     float tail = 0.f, fine = 1.f;
     if (lane >= kPlanCuts) {
       tail = v.x - floorf(v.x / ctas) * ctas;
       if (2.f * tail < ctas) tail += floorf(0.5f * ctas);
       fine = each >= 32.f ? 4.f : each >= 12.f ? 3.f : 2.f;
-      t = (v.y + v.z + tail * (2.f * fine - 1.f)) / ctas + 0.5f * each / fine;
+      t = (v.y + tail * (2.f * fine - 1.f)) / ctas + 0.5f * each / fine;
       v.w += tail * fine;
       if (v.x - tail < ctas || each < 6.f || p.slots == 0) t = 3.4e38f;
     }
@@ -320,49 +315,85 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
   __syncthreads();
   const int len = chosen;
 
-  // ---- where each sequence's pieces, slots and joins begin ----
-  int4 base = make_int4(0, 0, 0, 0);
-  for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    int4 x = make_int4(0, 0, 0, 0);
+  // ---- the sequences in the order of their pieces' lengths, and where each one's
+  // pieces, slots and joins begin ----
+  auto put = [&](int at, int s, const SeqRows& r, int nt, int cuts, bool is_long) {
+    ChunkSeq* q = p.seq + at;
+    q->s = s;
+    *reinterpret_cast<int4*>(&q->a) = make_int4(r.a, r.b, r.n, cuts);
+    q->shift = r.shift;
+    q->nt = nt;
+    q->kind = is_long;
+  };
+  auto begin = [&](int at, int before, int slot0, int join0, int pieces) {
+    ChunkSeq* q = p.seq + at;
+    q->before = before;
+    q->slot0 = slot0;
+    q->join0 = join0;
+    for (int i = before; i < min(before + pieces, p.ctas); ++i) p.first[i] = at;
+  };
+  int4 base = make_int4(0, 0, 0, 0);         // long pieces (or sequences); pieces, slots, joins
+  int pieces1 = 0;
+  if (p.S <= kPlanSorted) {
+    // a rank each, by comparing with all (long pieces before the others whatever the
+    // rounding; ties by number)
     int cuts = 1;
-    bool first = false;
-    if (s < p.S) {
-      const int nt = few ? works[s].nt : p.seq[s].nt, most = few ? works[s].longest : p.seq[s].longest;
-      cuts = seq_cuts(most, len);
-      const int tiles = nt * p.Hkv;
-      first = long_pieces(most, cuts, len);
-      if (first) x.x = tiles * cuts;
-      else x.y = tiles * cuts;
-      if (cuts > 1) {
-        x.z = tiles * cuts;
-        x.w = tiles;
+    bool is_long = false;
+    SeqWork w{0, 0, 0.f};
+    if (tid < p.S) {
+      w = works[tid];
+      cuts = seq_cuts(w.longest, len);
+      is_long = long_pieces(w.longest, cuts, len);
+      const float pairs = static_cast<float>(w.longest) / static_cast<float>(cuts);
+      keys[tid] = is_long ? pairs : -1.f / (pairs + 1.f);
+    }
+    __syncthreads();
+    if (tid < p.S) {
+      const float key = keys[tid];
+      int rank = 0;
+      for (int i = 0; i < p.S; ++i) rank += keys[i] > key || (keys[i] == key && i < tid);
+      put(rank, tid, mine, w.nt, cuts, is_long);
+      const int tiles = w.nt * p.Hkv, n = tiles * cuts;
+      sorted[rank] = make_int4(is_long ? n : 0, n, cuts > 1 ? n : 0, cuts > 1 ? tiles : 0);
+    }
+    __syncthreads();
+    const int4 x = tid < p.S ? sorted[tid] : make_int4(0, 0, 0, 0);
+    const int4 y = plan_scan(x, scan, warps, &base);
+    if (tid < p.S) begin(tid, y.y, y.z, y.w, x.y);
+    pieces1 = base.x;
+  } else {
+    // (many: the long ones, then the others)
+    for (int kind = 1; kind >= 0; --kind) {
+      for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int4 x = make_int4(0, 0, 0, 0);
+        int cuts = 1;
+        SeqRows r{0, 0, 0, 0, false, false};
+        SeqWork w{0, 0, 0.f};
+        if (s < p.S) {
+          r = seq_rows(p, s);
+          w = few ? works[s] : seq_work(p, r);
+          cuts = seq_cuts(w.longest, len);
+          if (long_pieces(w.longest, cuts, len) == (kind == 1)) {
+            const int tiles = w.nt * p.Hkv, n = tiles * cuts;
+            x = make_int4(1, n, cuts > 1 ? n : 0, cuts > 1 ? tiles : 0);
+          }
+        }
+        int4 total;
+        const int4 y = plan_scan(x, scan, warps, &total);
+        if (x.x) {
+          put(base.x + y.x, s, r, w.nt, cuts, kind == 1);
+          begin(base.x + y.x, base.y + y.y, base.z + y.z, base.w + y.w, x.y);
+        }
+        base = make_int4(base.x + total.x, base.y + total.y, base.z + total.z, base.w + total.w);
       }
-    }
-    int4 total;
-    const int4 y = plan_scan(x, scan, warps, &total);
-    if (s < p.S) {
-      ChunkSeq* q = p.seq + s;
-      *reinterpret_cast<int4*>(q) = make_int4(base.x + y.x, base.y + y.y, base.z + y.z, base.w + y.w);
-      q->cuts = cuts;
-      if (!first) q->longest = 0;
-      if (first)
-        for (int i = base.x + y.x; i < min(base.x + y.x + x.x, p.ctas); ++i) p.first[i] = s;
-    }
-    base = make_int4(base.x + total.x, base.y + total.y, base.z + total.z, base.w + total.w);
-  }
-  if (base.x < p.ctas && base.y > 0) {                      // CTAs that begin with another piece
-    for (int s = tid; s < p.S; s += kPlanThreads) {
-      const int b2 = p.seq[s].before2, nt = few ? works[s].nt : p.seq[s].nt;
-      const int cuts = p.seq[s].cuts;
-      if (p.seq[s].longest > 0) continue;
-      for (int i = base.x + b2; i < min(base.x + b2 + nt * p.Hkv * cuts, p.ctas); ++i) p.first[i] = s;
+      if (kind == 1) pieces1 = base.y;
     }
   }
   if (tid == 0) {
     // (the sums above are exact where a tail is chosen: fewer parts than slots)
-    const int tail = min(chosen_tail, base.x);
-    *p.plan = ChunkPlan{base.x, base.x + base.y, 0, base.w + tail, base.x - tail, chosen_fine, base.z, base.w};
+    const int tail = min(chosen_tail, pieces1);
+    *p.plan = ChunkPlan{pieces1, base.y, 0, base.w + tail, pieces1 - tail, chosen_fine, base.z, base.w};
   }
 }
 
@@ -385,7 +416,7 @@ __device__ __forceinline__ int find_seq(int S, int x, int lane, const Before& be
 // ----------------------------------------------------------------------------
 // What the roles need of a piece.
 struct Piece {
-  int s;                     // its sequence
+  int s;                     // its sequence's place in the plan
   int t0, p0;                // its tile's first row and that one's position
   int heads;                 // K/V head << 8 | tokens of the tile
   int slot;                  // -1: the whole tile's keys
@@ -398,7 +429,7 @@ static_assert(sizeof(Piece) == 36, "two pieces fit beside the tiles");
 // ... and the producer: the sequence's length, and the first key that some row of
 // the sequence has in its window.
 struct Work : Piece {
-  int n, low;
+  int n, low, row;           // (and its row of the table)
 };
 // Rows of a V block that some row of the sequence sees: [low, rows) and below
 // `sinks`, in the groups of 16 that have a page.  What the others hold (rows past
@@ -723,6 +754,7 @@ __global__ void __launch_bounds__(512, 1)
         if (x.kb.count() == 0) return false;
         const ChunkSeq* q = p.seq + x.s;
         x.n = q->n;
+        x.row = q->s;
         x.low = clamped(q->a + q->shift - p.window + 1, 0, x.n);
         return true;
       };
@@ -736,7 +768,7 @@ __global__ void __launch_bounds__(512, 1)
         if (t_of < 2 && 2 * k + t_of < x.kb.count()) {
           b.key = x.kb.at(2 * k + t_of) * kTileN + sub * br;
           if (b.key < x.n) {
-            b.page = __ldg(p.table + static_cast<size_t>(x.s) * p.M + (b.key >> p.page_log2));
+            b.page = __ldg(p.table + static_cast<size_t>(x.row) * p.M + (b.key >> p.page_log2));
             const int last = b.key + br - 1;
             b.seen = b.key <= x.p0 + x.ntok() - 1 && (last > x.p0 - p.window || b.key < p.sinks);
           }
@@ -969,19 +1001,17 @@ __global__ void __launch_bounds__(512, 1)
           if (begun && lane == 0) taken = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
           const int index = __shfl_sync(0xFFFFFFFFu, taken, 0);
           if (index < 0 || index >= total) return false;
-          // the piece among its kind's, and which of its cuts (each for all pieces in turn)
+          // the piece, and which of its cuts (each for all pieces in turn)
           const bool is_long = index < total1;
           const int over = index - plan.tail;
           const int sub = is_long && over >= 0 ? over / tail : 0;
-          const int piece = is_long ? index - sub * tail : index - total1;
-          const int* before = &p.seq->before1 + (is_long ? 0 : 1);
-          constexpr int kStep = sizeof(ChunkSeq) / sizeof(int);
+          const int piece = is_long ? index - sub * tail : index - (total1 - plan.pieces1);
           int s;
           if (!begun) s = p.first[index];
-          else s = find_seq(p.S, piece, lane, [&](int i) { return before[static_cast<size_t>(i) * kStep]; });
+          else s = find_seq(p.S, piece, lane, [&](int i) { return p.seq[i].before; });
           begun = true;
           const ChunkSeq q = p.seq[s];
-          const int in = piece - (is_long ? q.before1 : q.before2);
+          const int in = piece - q.before;
           // tiles first (the last ones, which see most keys, lead), then parts, then heads
           const int u = in / q.nt, hkv = u / q.cuts;
           int cut = u - hkv * q.cuts, cuts = q.cuts;
@@ -1517,19 +1547,19 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
     // sequence's are not
     const bool whole = j >= plan.tail_join;
     const int piece = plan.tail + j - plan.tail_join;
-    const int s = whole ? find_seq(p.S, piece, lane, [&](int i) { return p.seq[i].before1; })
+    const int s = whole ? find_seq(p.S, piece, lane, [&](int i) { return p.seq[i].before; })
                         : find_seq(p.S, j, lane, [&](int i) { return p.seq[i].join0; });
     const ChunkSeq q = p.seq[s];
     if (whole && q.cuts > 1) continue;
     const SeqRows r{q.a, q.b, q.n, q.shift, false, false};
     const int nt = q.nt;
-    const int in = whole ? piece - q.before1 : j - q.join0;
+    const int in = whole ? piece - q.before : j - q.join0;
     const int hkv = in / nt, i = in % nt;                 // the tile's number among its pieces'
     const Tile t = seq_tile(r, nt - 1 - i, p.tpt);
     // its pieces are numbers first, first + nt ..: `plain` of them have one part, those in
     // the tail `fine` each
     const int first = hkv * q.cuts * nt + i;
-    const int plain = q.longest == 0 ? q.cuts : max(0, min(q.cuts, (plan.tail - q.before1 - first + nt - 1) / nt));
+    const int plain = q.kind == 0 ? q.cuts : max(0, min(q.cuts, (plan.tail - q.before - first + nt - 1) / nt));
     if (tok >= t.ntok) continue;
     float m = NEG_INF, l = 0.f, y[8];
 #pragma unroll
@@ -1577,7 +1607,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
     };
     add(q.slot0 + first, nt, plain);
     for (int c = plain; c < q.cuts; ++c)
-      add(plan.tail_slot + (q.before1 + first + c * nt - plan.tail) * plan.fine, 1, plan.fine);
+      add(plan.tail_slot + (q.before + first + c * nt - plan.tail) * plan.fine, 1, plan.fine);
     float inv = l == 0.f ? 0.f : 1.f / l;
     if constexpr (FP8) inv *= __ldg(p.v_scale + hkv);
     const size_t at = static_cast<size_t>(t.t0 + tok) * p.H + hkv * p.G + row - tok * p.G;

@@ -628,6 +628,19 @@ def test_chunk_of_equal_tiles(bss, lens, news, H, Hkv, d, window, sinks, e4m3):
     check_chunk(bss, c, q, cu, lens, news, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("S", [257, 1300])
+def test_chunk_of_many_sequences(bss, S):
+    """More sequences than the plan sorts, and than it has threads; a few of them long."""
+    rng = random.Random(S)
+    lens = [rng.choice([0, 1, 17, 40]) for _ in range(S)]
+    news = [min(n, rng.choice([0, 1, 1, 3])) for n in lens]
+    for s, n, new in ((5, 9000, 70), (S // 2, 2500, 300), (S - 1, 9000, 1)):
+        lens[s], news[s] = n, new
+    c = Cache(lens, 2, 64, 32, S)
+    q, cu = ragged(news, 8, 64, 5)
+    check_chunk(bss, c, q, cu, lens, news)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_a_launch_after_a_timeout_stops(bss, e4m3):
     """With a timeout in the status word a launch stops, block by block, with parts to be joined or

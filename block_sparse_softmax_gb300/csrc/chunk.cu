@@ -21,7 +21,7 @@
 //   * The work is cut on the GPU, from the lengths (chunk_plan_kernel): pieces
 //     are parts of a tile's keys, of about equal length, and CTAs take them by a
 //     counter, longest first (32 sequences of up to 8192, every fourth with 512
-//     tokens: 140 us with two kinds of pieces in no order otherwise, 122 so).  A
+//     tokens: 140 us with two kinds of pieces in no order otherwise, 120 so).  A
 //     sequence's pieces are numbered so that those that run at the same time share
 //     their keys (tiles first, then key parts): L2 serves all but one of them.  Where pieces are whole tiles, or few a CTA, those of the last
 //     turn are cut once more (4 x 1000 tokens at 16384: 473 us with all tiles in two
@@ -43,9 +43,9 @@
 //
 // Measured (GB300, d=128, 16 query heads on 4 K/V heads where not said; of the
 // bf16 GEMM's 1929 TFLOP/s): 500 tokens at 8191 45 us; 32 sequences of up to 8192,
-// every fourth with 512 tokens 122 us, 50 %; 1024 tokens at 131071, 8 heads of their
+// every fourth with 512 tokens 120 us, 51 %; 1024 tokens at 131071, 8 heads of their
 // own 376 us, 75 %, and every key from HBM once; 4 x 1000 at 16384 over e4m3 428 us,
-// 63 %; d=64, window 1000, 16 heads of their own, 6 x <= 700 64 us.  A pair of blocks
+// 63 %; d=64, window 1000, 16 heads of their own, 6 x <= 700 62 us.  A pair of blocks
 // takes 2900 to 3050 cycles (e4m3 3350) for 2048 of MMAs at their peak rate: the
 // softmax warps' 570 for the mask and maximum, 320 to exchange it, 1350 for the
 // exponentials (1024 at their unit's rate) and the rest in hand-offs.  Of
@@ -1713,7 +1713,10 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, attn_fwd_paged_kernel<D, FP8>, tq, tk, tv, p)) != cudaSuccess) return e;
   if (p.slots == 0) return cudaSuccess;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(p.slots / 2, most_tiles(p.T, p.S, p.G) * p.Hkv)), D / 16);
+  // (as many as run at once: what is joined is known on the device alone, and 4576
+  // CTAs that find nothing took 4.4 us)
+  const long long joins = std::min<long long>(p.slots / 2, most_tiles(p.T, p.S, p.G) * p.Hkv);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(joins, sms)), D / 16);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, FP8>, p);

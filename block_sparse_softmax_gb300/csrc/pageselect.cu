@@ -10,10 +10,13 @@
 // the top_r others by score, ties to the lower slot, listed in ascending order.
 //
 // Which page is taken must not hang on a rounding, so a pick is the exact one:
-//   * means: each element is divided by the page size first (a power of two:
-//     exact), then summed as an unevaluated pair of fp32 numbers by Knuth's
-//     two-sum, which leaves one rounding, the mean's own to fp32 (over e4m3 pages
-//     with their scale's product, off by 2^-24 and 2^-46 at most);
+//   * means: the elements are summed as an unevaluated pair of fp32 numbers by
+//     Knuth's two-sum.  The pair is the exact sum where the largest element is at
+//     most 2^34 / page times the smallest that is not 0 (kPoolSpread); a column of
+//     others, or one past fp32's range, is summed again in whole numbers.  The page
+//     size is a power of two, so there is one rounding, the mean's own to fp32.
+//     (1024 e4m3 elements are a pair in any order; with their scale's product a mean
+//     is off by 2^-24 and 2^-46 at most.)
 //   * scores: in fp32 first, each off by at most
 //         e = (G + r + 2) 2^-24 sum_i A_i max_mi |mean_mi|,   A = sum_h |q_h|
 //     (G roundings of the group's sum at most and r of a product's, on terms whose
@@ -58,6 +61,77 @@ __device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
   hi = s;
 }
 
+// When lo rounds.  With fields f of bf16 exponents between f0 (of an element other
+// than 0) and f1, every sum is a multiple of u = 2^(f0 - 134), an element less than A
+// = 2^(f1 - 126).  A lane adds up 64 elements at most, two levels of lanes and then
+// 8 warps join: over all additions the sums' absolute values come to less than
+// 39 page A, and their errors, each at most 2^-24 of its sum, to 2^-18 page A.  That
+// is less than 2^24 u, so that lo has bits for all of them, where f1 - f0 <= 34 -
+// log2(page).
+constexpr int kPoolSpread = 34;
+
+// The means of the eight columns at `src` (rows `stride` apart, bf16) by a warp, a
+// lane's in lane / 4, rounded once: a finite element is an 8-bit number times
+// 2^(s - 133), s < 254, and counts in the s / 32-th of eight 64-bit sums, shifted by
+// s % 32 (8 + 31 bits, a sign and 2^10 rows).  Their carries settled, the sums are
+// the 32-bit digits of the whole.
+__device__ __noinline__ float exact_mean(const uint16_t* src, int stride, int page_log2) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  long long sum[8];
+  float odd = 0.f;                            // infinities and NaN, as they add up
+#pragma unroll
+  for (int w = 0; w < 8; ++w) sum[w] = 0;
+#pragma unroll 8
+  for (int r = lane & 3; r < 1 << page_log2; r += 4) {
+    const uint32_t x = __ldg(src + static_cast<size_t>(r) * stride + (lane >> 2));
+    const int field = static_cast<int>(x >> 7 & 255u);
+    if (field == 255) odd += __uint_as_float(x << 16);
+    const int s = max(field, 1) - 1;
+    long long v = static_cast<long long>((x & 127u) | (field != 0 ? 128u : 0u)) << (s & 31);
+    if (x >> 15) v = -v;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum[w] += s >> 5 == w ? v : 0;
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum[w] += __shfl_xor_sync(0xFFFFFFFFu, sum[w], o);
+  }
+  if (odd != 0.f) return odd;
+  // the digits of the sum's absolute value; the ninth takes what eight sums carry over
+  long long carry = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) carry = (sum[w] + carry) >> 32;
+  const bool negative = carry < 0;
+  uint32_t digit[9];
+  carry = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    carry += negative ? -sum[w] : sum[w];
+    digit[w] = static_cast<uint32_t>(carry);
+    carry >>= 32;
+  }
+  digit[8] = static_cast<uint32_t>(carry);
+  // the highest digit and the one below it, and a bit for all that lies lower: the
+  // rounding to fp32 is the only one (a mean below fp32's normal numbers is a
+  // multiple of their last place)
+  unsigned long long top = static_cast<unsigned long long>(digit[0]) << 32;
+  int at = 0;
+#pragma unroll
+  for (int w = 1; w < 9; ++w) {
+    if (digit[w] != 0u) {
+      top = static_cast<unsigned long long>(digit[w]) << 32 | digit[w - 1];
+      at = w;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 7; ++w)
+    if (w < at - 1 && digit[w] != 0u) top |= 1ull;
+  const float f = ldexpf(__ull2float_rn(top), 32 * (at - 1) - 133 - page_log2);
+  return negative ? -f : f;
+}
+
 __device__ __forceinline__ float2 e4m3x2_f32x2(uint32_t x) {
   uint32_t y;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
@@ -67,7 +141,9 @@ __device__ __forceinline__ float2 e4m3x2_f32x2(uint32_t x) {
 // `W` warps a (page, head), each with all of its part's loads in flight (up to 8 of
 // 16 bytes a lane; 32 * 16 / (bytes of a row) rows arrive with each), joined in
 // order in shared memory.  A page's part is what a warp waits for once: with a warp
-// a page of 64 tokens, four times, a prompt of 16384 took 10.8 us.
+// a page of 64 tokens, four times, a prompt of 16384 took 10.8 us.  (The
+// same with more warps, from L2 and among others: 8.8 us, 7.8 without the span of the
+// elements' magnitudes; a test of every addition to lo instead took 1 to 2 more.)
 constexpr int kPoolWarps = 8;
 constexpr int kPoolBatch = 8;
 template <int D, bool FP8>
@@ -76,6 +152,7 @@ __global__ void __launch_bounds__(kPoolWarps * 32) kv_pool_kernel(const PoolPara
   constexpr int kLanes = D / kEl;             // lanes of a row
   constexpr int kRows = 32 / kLanes;          // rows of a load
   __shared__ float2 parts[kPoolWarps][D];
+  __shared__ uint2 spans[kPoolWarps][FP8 ? 1 : D / 2];
   const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
   const int loads = (1 << p.page_log2) / kRows;            // of a page (16 rows at least, 8 a load at most)
   const int W = p.warps, each = loads / W;                 // warps of an item, loads of a warp
@@ -103,8 +180,24 @@ __global__ void __launch_bounds__(kPoolWarps * 32) kv_pool_kernel(const PoolPara
         pg = -1;
       }
       float hi[kEl], lo[kEl];
+      // bf16: two columns' largest magnitudes, bit 15 set, and the smallest less 1, bit
+      // 15 set before (as signed numbers: 0 becomes the largest there is)
+      uint32_t big[kEl / 2], small[kEl / 2];
 #pragma unroll
       for (int e = 0; e < kEl; ++e) hi[e] = lo[e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kEl / 2; ++e) {
+        big[e] = 0x80008000u;
+        small[e] = 0x7FFF7FFFu;
+      }
+      auto join = [&](int e, float oh, float ol) {
+        two_sum(hi[e], lo[e], oh);
+        lo[e] = __fadd_rn(lo[e], ol);
+      };
+      auto widen = [&](int e, uint32_t other_big, uint32_t other_small) {
+        big[e] = __vmaxu2(big[e], other_big);
+        small[e] = __vmins2(small[e], other_small);
+      };
       if (pg >= 0) {
         const uint4* src = reinterpret_cast<const uint4*>(
             p.k + pg * p.k_stride + ((static_cast<size_t>(h) << p.page_log2) * D) * (FP8 ? 1 : 2)) + lane +
@@ -121,13 +214,15 @@ __global__ void __launch_bounds__(kPoolWarps * 32) kv_pool_kernel(const PoolPara
             for (int e = 0; e < 4; ++e) {
               if constexpr (FP8) {
                 const float2 c0 = e4m3x2_f32x2(w[e]), c1 = e4m3x2_f32x2(w[e] >> 16);
-                two_sum(hi[4 * e], lo[4 * e], c0.x * share);
-                two_sum(hi[4 * e + 1], lo[4 * e + 1], c0.y * share);
-                two_sum(hi[4 * e + 2], lo[4 * e + 2], c1.x * share);
-                two_sum(hi[4 * e + 3], lo[4 * e + 3], c1.y * share);
+                two_sum(hi[4 * e], lo[4 * e], c0.x);
+                two_sum(hi[4 * e + 1], lo[4 * e + 1], c0.y);
+                two_sum(hi[4 * e + 2], lo[4 * e + 2], c1.x);
+                two_sum(hi[4 * e + 3], lo[4 * e + 3], c1.y);
               } else {
-                two_sum(hi[2 * e], lo[2 * e], bf16lo(w[e]) * share);
-                two_sum(hi[2 * e + 1], lo[2 * e + 1], bf16hi(w[e]) * share);
+                two_sum(hi[2 * e], lo[2 * e], bf16lo(w[e]));
+                two_sum(hi[2 * e + 1], lo[2 * e + 1], bf16hi(w[e]));
+                const uint32_t magnitude = w[e] | 0x80008000u;
+                widen(e, magnitude, magnitude - 0x00010001u);
               }
             }
           }
@@ -139,8 +234,12 @@ __global__ void __launch_bounds__(kPoolWarps * 32) kv_pool_kernel(const PoolPara
           for (int e = 0; e < kEl; ++e) {
             const float oh = __shfl_xor_sync(0xFFFFFFFFu, hi[e], o);
             const float ol = __shfl_xor_sync(0xFFFFFFFFu, lo[e], o);
-            two_sum(hi[e], lo[e], oh);
-            lo[e] = __fadd_rn(lo[e], ol);
+            join(e, oh, ol);
+          }
+#pragma unroll
+          for (int e = 0; e < (FP8 ? 0 : kEl / 2); ++e) {
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, big[e], o);
+            widen(e, other, __shfl_xor_sync(0xFFFFFFFFu, small[e], o));
           }
         }
       }
@@ -148,35 +247,62 @@ __global__ void __launch_bounds__(kPoolWarps * 32) kv_pool_kernel(const PoolPara
         if (lane < kLanes) {
 #pragma unroll
           for (int e = 0; e < kEl; ++e) parts[warp][lane * kEl + e] = make_float2(hi[e], lo[e]);
+#pragma unroll
+          for (int e = 0; e < (FP8 ? 0 : kEl / 2); ++e)
+            spans[warp][lane * (kEl / 2) + e] = make_uint2(big[e], small[e]);
         }
         __syncthreads();
         if (warp % W == 0 && lane < kLanes)
-          for (int w = 1; w < W; ++w)
+          for (int w = 1; w < W; ++w) {
 #pragma unroll
             for (int e = 0; e < kEl; ++e) {
               const float2 y = parts[warp + w][lane * kEl + e];
-              two_sum(hi[e], lo[e], y.x);
-              lo[e] = __fadd_rn(lo[e], y.y);
+              join(e, y.x, y.y);
             }
-      }
-      if (pg >= 0 && warp % W == 0 && lane < kLanes) {
-        const float f = FP8 ? __ldg(p.k_scale + h) : 1.f;
-        float* dst = p.means + (static_cast<size_t>(pg) * p.Hkv + h) * D + lane * kEl;
 #pragma unroll
-        for (int e = 0; e < kEl; e += 4) {
-          float y[4];
-#pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            // the pair (times the scale: with the product's own rest), rounded once; in
-            // fp32, for a multiprocessor has two fp64 lanes.  An infinity's or NaN's lo
-            // is a NaN, and left out.
-            const float hh = hi[e + i4], ll = lo[e + i4];
-            const float pr = hh * f;
-            y[i4] = !isfinite(hh) ? pr
-                    : FP8         ? __fadd_rn(pr, fmaf(hh, f, -pr) + ll * f)
-                                  : __fadd_rn(hh, ll);
+            for (int e = 0; e < (FP8 ? 0 : kEl / 2); ++e) {
+              const uint2 y = spans[warp + w][lane * (kEl / 2) + e];
+              widen(e, y.x, y.y);
+            }
           }
-          *reinterpret_cast<float4*>(dst + e) = make_float4(y[0], y[1], y[2], y[3]);
+      }
+      if (pg >= 0 && warp % W == 0) {          // (a whole warp)
+        float* dst = p.means + (static_cast<size_t>(pg) * p.Hkv + h) * D;
+        bool again = false;                   // bf16: one of this lane's pairs may not be its sum
+        if (lane < kLanes) {
+          const float f = FP8 ? __ldg(p.k_scale + h) : 1.f;
+#pragma unroll
+          for (int e = 0; e < kEl; e += 4) {
+            float y[4];
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              // the pair (times the scale: with the product's own rest), rounded once; in
+              // fp32, for a multiprocessor has two fp64 lanes.  A NaN's lo is a NaN, and
+              // left out.
+              const float hh = hi[e + i4] * share, ll = lo[e + i4] * share;
+              const float pr = hh * f;
+              if constexpr (FP8) {
+                y[i4] = !isfinite(hh) ? pr : __fadd_rn(pr, fmaf(hh, f, -pr) + ll * f);
+              } else {
+                y[i4] = __fadd_rn(hi[e + i4], lo[e + i4]) * share;
+                const int half = 16 * (i4 & 1), c = (e + i4) / 2;
+                const int f1 = static_cast<int>(big[c] >> half >> 7 & 255u);
+                const int f0 = static_cast<int>(((small[c] >> half) + 1u) >> 7 & 255u);  // (0, too, where all are 0)
+                again = again || f1 - max(f0, 1) > kPoolSpread - p.page_log2 || !isfinite(hi[e + i4]);
+              }
+            }
+            *reinterpret_cast<float4*>(dst + lane * kEl + e) = make_float4(y[0], y[1], y[2], y[3]);
+          }
+        }
+        if constexpr (!FP8) {
+          uint32_t todo = __ballot_sync(0xFFFFFFFFu, again);
+          if (todo != 0u) __syncwarp();       // (after the stores above)
+          for (; todo != 0u; todo &= todo - 1) {
+            const int c = (__ffs(todo) - 1) * kEl;
+            const float y = exact_mean(reinterpret_cast<const uint16_t*>(p.k + pg * p.k_stride) +
+                                           (static_cast<size_t>(h) << p.page_log2) * D + c, D, p.page_log2);
+            if ((lane & 3) == 0) dst[c + lane / 4] = y;
+          }
         }
       }
       if (W > 1) __syncthreads();             // the parts have been read

@@ -1,0 +1,64 @@
+"""Mean keys and selected pages where they are hardest, on the GPU: sums that cancel."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_paged import ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bss():
+    import block_sparse_softmax_gb300 as m
+    m.library()
+    return m
+
+
+# ----------------------------------------------------------------------------
+# mean keys
+# ----------------------------------------------------------------------------
+
+def check_means(bss, k):
+    """`k` [pages, heads, page, d] bf16: every mean is the exact sum's, rounded once.  (The sum itself
+    is rounded to 64 bits by math.fsum, by 2^-53 of it.)"""
+    P, Hkv, page, d = k.shape
+    means = torch.full((P, Hkv, d), 5.0, device="cuda")
+    bss.attn_kv_pool(k, means, ints([list(range(P))]), ints([0]), ints([P * page]))
+    assert bss.attn_poll_status() == 0
+    columns = k.double().transpose(2, 3).reshape(-1, page).tolist()
+    want = torch.tensor([math.fsum(c) / page for c in columns], dtype=torch.float64).view(P, Hkv, d)
+    off = (means.double().cpu() - want).abs()
+    assert (off <= (2.0 ** -24 + 2.0 ** -50) * want.abs()).all(), (off / want.abs().clamp_min(1e-300)).max()
+
+
+def test_pool_of_three_magnitudes(bss):
+    """Numbers that cancel down to one that neither the sum nor its rest holds beside them."""
+    k = torch.zeros(4, 1, 16, 64, device="cuda", dtype=torch.bfloat16)
+    # rows that one warp's lanes of different rows hold, in either order
+    for p, order in enumerate(((0, 4, 8, 12, 1), (12, 8, 4, 0, 3), (0, 1, 2, 3, 4), (15, 0, 7, 9, 2))):
+        for r, x in zip(order, (2.0 ** 51, 2.0 ** 26, 1.0, -(2.0 ** 51), -(2.0 ** 26))):
+            k[p, 0, r] = x
+    check_means(bss, k)
+    k[1, 0, :, 5:9] *= -(2.0 ** -70)
+    k[2, 0, :, 40] *= 2.0 ** 70
+    k[3, 0, 5, 63] = 2.0 ** -133                          # the smallest number there is
+    check_means(bss, k)
+
+
+@pytest.mark.parametrize("page,d,Hkv", [(16, 64, 2), (64, 128, 3), (128, 64, 1), (1024, 128, 1), (1024, 64, 2)])
+def test_pool_of_wide_ranges(bss, page, d, Hkv):
+    """Elements spread over some or all binades, half of them cancelling the other half but for little."""
+    g = torch.Generator("cuda").manual_seed(page + d)
+    P = 3
+    x = torch.randn(P, Hkv, page, d, generator=g, device="cuda")
+    e = torch.randint(-20, 21, x.shape, generator=g, device="cuda")
+    e[1] = torch.randint(-60, 61, e[1].shape, generator=g, device="cuda")
+    e[2] = torch.randint(-132, 116, e[2].shape, generator=g, device="cuda")
+    k = torch.ldexp(x, e).clamp(-3e38, 3e38).bfloat16()
+    half = page // 2
+    perm = torch.randperm(half, generator=g, device="cuda")
+    k[:, :, half:, ::2] = -k[:, :, perm, ::2]             # every other column: sums of 0 but for
+    k[:, :, page - 1, ::4] = torch.ldexp(x[:, :, 0, ::4], e[:, :, 1, ::4]).clamp(-3e38, 3e38).bfloat16()
+    check_means(bss, k)

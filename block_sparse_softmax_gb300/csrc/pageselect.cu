@@ -278,11 +278,11 @@ __global__ void __launch_bounds__(kPoolWarps * 32) kv_pool_kernel(const PoolPara
             for (int i4 = 0; i4 < 4; ++i4) {
               // the pair (times the scale: with the product's own rest), rounded once; in
               // fp32, for a multiprocessor has two fp64 lanes.  A NaN's lo is a NaN, and
-              // left out.
+              // left out, as is what a product past fp32's range leaves.
               const float hh = hi[e + i4] * share, ll = lo[e + i4] * share;
               const float pr = hh * f;
               if constexpr (FP8) {
-                y[i4] = !isfinite(hh) ? pr : __fadd_rn(pr, fmaf(hh, f, -pr) + ll * f);
+                y[i4] = !isfinite(pr) ? pr : __fadd_rn(pr, fmaf(hh, f, -pr) + ll * f);
               } else {
                 y[i4] = __fadd_rn(hi[e + i4], lo[e + i4]) * share;
                 const int half = 16 * (i4 & 1), c = (e + i4) / 2;

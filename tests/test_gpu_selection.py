@@ -62,3 +62,14 @@ def test_pool_of_wide_ranges(bss, page, d, Hkv):
     k[:, :, half:, ::2] = -k[:, :, perm, ::2]             # every other column: sums of 0 but for
     k[:, :, page - 1, ::4] = torch.ldexp(x[:, :, 0, ::4], e[:, :, 1, ::4]).clamp(-3e38, 3e38).bfloat16()
     check_means(bss, k)
+
+
+def test_pool_of_scales_past_the_range(bss):
+    """A mean times its scale that leaves fp32's range is infinite, not a NaN."""
+    k = torch.full((1, 3, 16, 64), 448.0, device="cuda").to(torch.float8_e4m3fn)
+    k[0, 1] = torch.full((16, 64), -448.0, device="cuda").to(torch.float8_e4m3fn)
+    means = torch.zeros(1, 3, 64, device="cuda")
+    bss.attn_kv_pool(k, means, ints([[0]]), ints([0]), ints([16]),
+                     k_scale=torch.tensor([2.0 ** 120, 2.0 ** 120, 2.0 ** 110], device="cuda"))
+    assert (means[0, 0] == math.inf).all() and (means[0, 1] == -math.inf).all()
+    assert (means[0, 2] == 448.0 * 2.0 ** 110).all()

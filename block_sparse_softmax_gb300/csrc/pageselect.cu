@@ -21,10 +21,15 @@
 //         e = (G + r + 2) 2^-24 sum_i A_i max_mi |mean_mi|,   A = sum_h |q_h|
 //     (G roundings of the group's sum at most and r of a product's, on terms whose
 //     absolute values add up to at most that sum; r = d / 32 + 5 for a lane's chain
-//     and the tree over the lanes, d for one chain).  The top_r-th largest of numbers that are off by e is off by e, so
-//     what lies more than 2 e above it is taken and more than 2 e below is not;
-//     only what lies between (as a rule, that one page) is scored again, in 64
-//     bits.
+//     and the tree over the lanes, d for one chain).  The top_r-th largest of numbers
+//     that are off by e is off by e, so what lies more than 2 e above it is taken and
+//     more than 2 e below is not.  What lies between (as a rule, that one page) is
+//     scored again, in whole numbers of 128 bits, of which the last stands for at
+//     most 2^-110 times sum_i A_i max_mi |mean_mi|; each product's bits below that are
+//     dropped.  A product of a query's element and a mean's that is not below 2^-60
+//     times the largest of both keeps all of its 32 bits, and scores of the same
+//     products are the same in any order.  (Pairs of fp64 numbers, which a
+//     multiprocessor has two lanes for, took 16 times as long.)
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -326,8 +331,7 @@ struct SelectParams {
   int top, local, first, R;
   int parts;                // score CTAs along a row
   int rounds;               // roundings of a score's sum
-  float* score;             // [rows][Hkv][M]
-  double* exact;            // [rows][Hkv][M], written where needed
+  float* score;             // [rows][Hkv][M]; then words of what is scored again
   float* norm;              // [rows][Hkv][parts]: the largest |mean| element met
   int* pages;               // [T][Hkv][R]
   int* out_lens;            // [T]
@@ -599,26 +603,29 @@ __global__ void __launch_bounds__(kTileThreads) select_score_tile_kernel(const S
 // ----------------------------------------------------------------------------
 // the pick
 // ----------------------------------------------------------------------------
-// Numbers in an order of whole ones; a NaN comes last, below every other.
-__device__ __forceinline__ unsigned long long order_of(double x) {
-  if (x != x) return 0ull;
-  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
-  return b >> 63 ? ~b : b | (1ull << 63);
-}
+// A column's sum over the group's query heads, in units of 2^(Q - 94); `odd` adds up
+// its infinities and NaN (0: there are none).
+struct __align__(16) FixedSum {
+  unsigned long long lo;
+  int hi;
+  float odd;
+  __device__ __forceinline__ __int128 value() const { return static_cast<__int128>(hi) << 64 | lo; }
+};
+
 // The want-th largest (want >= 1) of the keys key(i) of `bits` bits, i in [lo, hi),
 // of those that in(i) admits, and how many are larger: eight bits a turn, from the
 // top, until at most 32 keys are left, which every warp ranks (three turns for 8192
 // keys took 5.8 us, a turn and the ranking 3.4).
-template <int NT, class K, class In, class Key>
-__device__ K nth_largest(int bits, int lo, int hi, int want, const In& in, const Key& key, int* larger, int* hist) {
-  K prefix = 0, mask = 0;
+template <int NT, class In, class Key>
+__device__ uint32_t nth_largest(int bits, int lo, int hi, int want, const In& in, const Key& key, int* larger, int* hist) {
+  uint32_t prefix = 0, mask = 0;
   int above = 0;
   for (int shift = bits - 8; shift >= 0; shift -= 8) {
     for (int i = static_cast<int>(threadIdx.x); i < 256; i += NT) hist[i] = 0;
     __syncthreads();
     for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += NT) {
       if (!in(i)) continue;
-      const K k = key(i);
+      const uint32_t k = key(i);
       if ((k & mask) == prefix) atomicAdd(hist + static_cast<int>((k >> shift) & 255), 1);
     }
     __syncthreads();
@@ -649,24 +656,24 @@ __device__ K nth_largest(int bits, int lo, int hi, int want, const In& in, const
     const int from = who ? __ffs(who) - 1 : 0;           // (who is 0 only where fewer than `want` are in)
     digit = max(0, __shfl_sync(0xFFFFFFFFu, digit, from));
     above += __shfl_sync(0xFFFFFFFFu, more, from);
-    prefix |= static_cast<K>(digit) << shift;
-    mask |= static_cast<K>(255) << shift;
+    prefix |= static_cast<uint32_t>(digit) << shift;
+    mask |= 255u << shift;
     same = __shfl_sync(0xFFFFFFFFu, same, from);
     __syncthreads();
     if (shift == 0 || same == 0 || same > 32) continue;
-    K* list = reinterpret_cast<K*>(hist);
+    uint32_t* list = reinterpret_cast<uint32_t*>(hist);
     if (threadIdx.x == 0) hist[255] = 0;
     __syncthreads();
     for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += NT) {
       if (!in(i)) continue;
-      const K k = key(i);
+      const uint32_t k = key(i);
       if ((k & mask) == prefix) list[atomicAdd(hist + 255, 1)] = k;
     }
     __syncthreads();
-    const K mine = lane < same ? list[lane] : 0;
+    const uint32_t mine = lane < same ? list[lane] : 0;
     int larger_ones = 0, equal = 0;
     for (int i = 0; i < same; ++i) {
-      const K k = __shfl_sync(0xFFFFFFFFu, mine, i);
+      const uint32_t k = __shfl_sync(0xFFFFFFFFu, mine, i);
       larger_ones += k > mine;
       equal += k == mine;
     }
@@ -691,7 +698,7 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
   __shared__ __align__(16) int hist[256];
   __shared__ int sums[NT / 32];
   __shared__ float fsums[2][NT / 32], range[2][NT / 32];
-  __shared__ double qd[D];
+  __shared__ FixedSum qsum[D];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31;
@@ -724,8 +731,7 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
   const int* tab = p.table + static_cast<size_t>(row.s) * p.M;
   const int begin = min(p.first, row.held), end = scored_end(p, row);
   const size_t at = static_cast<size_t>(r) * p.Hkv + h;
-  const float* score = p.score + at * p.M;
-  double* exact = p.exact + at * p.M;
+  float* score = p.score + at * p.M;
   uint32_t* taken = keys + p.M;
   const int words = (row.held + 31) / 32;
   // a warp a word: what is taken anyway; the candidates are marked (1: a page, 0: none)
@@ -829,22 +835,94 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
     }
   __syncthreads();
   auto held_page = [&](int m) { return keys[m] != 0u; };
-  // slot m's score in 64 bits, by a warp
+  // What follows is for pages that are scored again.  A column's sum of queries is less
+  // than 2^q_exp = 2^Q, a mean than 2^(mean_field - 126) = 2^M, a score then than 2^125
+  // units of 2^(Q + M - 118).
+  int q_exp = 0, mean_field = 0;
+  auto sum_again = [&]() {
+    float qm = a1, mm = mn;
+    if (!isfinite(a1) || !isfinite(mn)) {                // the largest ones that are finite
+      qm = mm = 0.f;
+      for (int i = tid; i < p.G * D; i += NT) {
+        const float x = fabsf(__bfloat162float(q_row[i]));
+        if (isfinite(x)) qm = fmaxf(qm, x);
+      }
+      for (int m0 = begin + warp; m0 < end; m0 += NT / 32) {
+        if (!held_page(m0)) continue;
+        const float* src = p.means + (static_cast<size_t>(__ldg(tab + m0)) * p.Hkv + h) * D;
+        for (int e = lane; e < D; e += 32) {
+          const float x = fabsf(__ldg(src + e));
+          if (isfinite(x)) mm = fmaxf(mm, x);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        qm = fmaxf(qm, __shfl_xor_sync(0xFFFFFFFFu, qm, o));
+        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+      }
+      if (lane == 0) {
+        fsums[0][warp] = qm;
+        fsums[1][warp] = mm;
+      }
+      __syncthreads();
+      for (int w = 0; w < NT / 32; ++w) {
+        qm = fmaxf(qm, fsums[0][w]);
+        mm = fmaxf(mm, fsums[1][w]);
+      }
+    }
+    // (twice the sum of all magnitudes, for its own rounding; or G times the largest)
+    q_exp = static_cast<int>(__float_as_uint(qm) >> 23) - 125 + (qm == a1 ? 0 : 32 - __clz(p.G));
+    mean_field = max(1, static_cast<int>(__float_as_uint(mm) >> 23));
+    for (int e = tid; e < D; e += NT) {
+      __int128 sum = 0;
+      float odd = 0.f;
+      for (int g = 0; g < p.G; ++g) {
+        const float x = __bfloat162float(q_row[static_cast<long long>(g) * D + e]);
+        const uint32_t bits = __float_as_uint(x);
+        const int field = static_cast<int>(bits >> 23 & 255u);
+        if (field == 255) {
+          odd += x;
+          continue;
+        }
+        // 8 bits times 2^(field - 134)
+        const long long digits = static_cast<long long>((bits >> 16 & 127u) | (field != 0 ? 128u : 0u));
+        const int shift = max(field, 1) - 40 - q_exp;
+        const __int128 y = shift >= 0 ? static_cast<__int128>(digits) << shift : digits >> min(-shift, 63);
+        sum += bits >> 31 ? -y : y;
+      }
+      qsum[e] = FixedSum{static_cast<unsigned long long>(sum), static_cast<int>(sum >> 64), odd};
+    }
+  };
+  // slot m's score in those units, past 2^126 of them, by a warp; -inf is 1, a NaN 0
   auto score_again = [&](int m) {
     const float* src = p.means + (static_cast<size_t>(__ldg(tab + m)) * p.Hkv + h) * D;
-    double d = 0.0;
-    for (int e = lane; e < D; e += 32) d = fma(qd[e], static_cast<double>(__ldg(src + e)), d);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-    return d;
-  };
-  // ... and the group's sum, for those
-  auto sum_again = [&]() {
-    for (int e = tid; e < D; e += NT) {
-      double x = 0.0;
-      for (int g = 0; g < p.G; ++g) x += static_cast<double>(__bfloat162float(q_row[static_cast<long long>(g) * D + e]));
-      qd[e] = x;
+    __int128 sum = 0;
+    float odd = 0.f;
+    for (int e = lane; e < D; e += 32) {
+      const float mean = __ldg(src + e);
+      const uint32_t bits = __float_as_uint(mean);
+      const int field = static_cast<int>(bits >> 23 & 255u);
+      const FixedSum q = qsum[e];
+      const __int128 x = q.value();
+      if (q.odd != 0.f) {
+        odd += q.odd * mean;
+      } else if (field == 255) {
+        odd += mean * (x > 0 ? 1.f : x < 0 ? -1.f : 0.f);
+      } else {
+        // 24 bits times 2^(field - 150)
+        const int digits = static_cast<int>((bits & 0x7FFFFFu) | (field != 0 ? 0x800000u : 0u));
+        sum += x * (bits >> 31 ? -digits : digits) >> min(mean_field - max(field, 1), 127);
+      }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long lo = __shfl_xor_sync(0xFFFFFFFFu, static_cast<unsigned long long>(sum), o);
+      const long long hi = __shfl_xor_sync(0xFFFFFFFFu, static_cast<long long>(sum >> 64), o);
+      sum += static_cast<__int128>(hi) << 64 | lo;
+      odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
+    }
+    const unsigned __int128 key = static_cast<unsigned __int128>(sum) + (static_cast<unsigned __int128>(1) << 126);
+    return odd == 0.f ? key : odd > 0.f ? ~static_cast<unsigned __int128>(0) : static_cast<unsigned __int128>(odd < 0.f);
   };
   auto take = [&](int m) { atomicOr(taken + (m >> 5), 1u << (m & 31)); };
   if (nc <= p.top) {
@@ -852,7 +930,7 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
       if (held_page(m)) take(m);
   } else if (p.top > 0) {
     int larger;
-    const int kth = clear ? static_cast<int>(nth_largest<NT, uint32_t>(
+    const int kth = clear ? static_cast<int>(nth_largest<NT>(
                                 24, begin, end, p.top, held_page, [&](int m) { return keys[m] - 1u; }, &larger, hist)) + 1
                           : 1;
     auto is_sure = [&](int m) { return clear && static_cast<int>(keys[m]) > kth + band; };
@@ -892,49 +970,86 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
       for (int m = begin + tid; m < end; m += NT)
         if (is_open(m)) hist[atomicAdd(sums, 1)] = m;
       __syncthreads();
-      double* again = reinterpret_cast<double*>(hist + 32);
+      ulonglong2* again = reinterpret_cast<ulonglong2*>(hist + 32);
       for (int i = warp; i < open; i += NT / 32) {
-        const double d = score_again(hist[i]);
-        if (lane == 0) again[i] = d;
+        const unsigned __int128 k = score_again(hist[i]);
+        if (lane == 0)
+          again[i] = make_ulonglong2(static_cast<unsigned long long>(k), static_cast<unsigned long long>(k >> 64));
       }
       __syncthreads();
       if (warp == 0) {
         const int m = lane < open ? hist[lane] : 0;
-        const unsigned long long k = lane < open ? order_of(again[lane]) : 0ull;
+        const ulonglong2 k = lane < open ? again[lane] : make_ulonglong2(0ull, 0ull);
         int better = 0;
         for (int i = 0; i < open; ++i) {
-          const unsigned long long k2 = __shfl_sync(0xFFFFFFFFu, k, i);
+          const unsigned long long lo = __shfl_sync(0xFFFFFFFFu, k.x, i), hi = __shfl_sync(0xFFFFFFFFu, k.y, i);
           const int m2 = __shfl_sync(0xFFFFFFFFu, m, i);
-          better += k2 > k || (k2 == k && m2 < m);
+          better += hi > k.y || (hi == k.y && (lo > k.x || (lo == k.x && m2 < m)));
         }
         if (lane < open && better < want) take(m);
       }
     } else if (want > 0) {
-      // scored again, a warp an open page
+      // Scored again, a warp an open page, 32 bits of the number at a time (where the
+      // score was): what is larger than the want-th word is taken, what is smaller
+      // is no longer open, and so on with those that equal it.
       sum_again();
-      __syncthreads();
-      for (int m0 = begin + warp * 32; m0 < end; m0 += NT) {
-        uint32_t todo = __ballot_sync(0xFFFFFFFFu, m0 + lane < end && is_open(m0 + lane));
-        for (; todo != 0u; todo &= todo - 1) {
-          const int m = m0 + __ffs(todo) - 1;
-          const double d = score_again(m);
-          if (lane == 0) exact[m] = d;
+      int left = want, same = open;
+      uint32_t* word = reinterpret_cast<uint32_t*>(score);
+      ulonglong2* firsts = reinterpret_cast<ulonglong2*>(hist);
+      for (int part = 0; part < 4 && same > left; ++part) {
+        __syncthreads();
+        unsigned __int128 first = 0;
+        int met = 0;                                     // 1: a page, 3: and one of another score
+        for (int m0 = begin + warp * 32; m0 < end; m0 += NT) {
+          uint32_t todo = __ballot_sync(0xFFFFFFFFu, m0 + lane < end && is_open(m0 + lane));
+          for (; todo != 0u; todo &= todo - 1) {
+            const int m = m0 + __ffs(todo) - 1;
+            const unsigned __int128 k = score_again(m);
+            if (lane == 0) word[m] = static_cast<uint32_t>(k >> (96 - 32 * part));
+            if (met == 0) first = k;
+            met |= k == first ? 1 : 3;
+          }
         }
+        if (lane == 0) {
+          sums[warp] = met;
+          firsts[warp] = make_ulonglong2(static_cast<unsigned long long>(first),
+                                         static_cast<unsigned long long>(first >> 64));
+        }
+        __syncthreads();
+        bool alike = true;                               // all of them: nothing more to tell apart
+        int one = -1;
+        for (int w = 0; w < NT / 32; ++w) {
+          if (sums[w] == 0) continue;
+          if (one < 0) one = w;
+          alike = alike && sums[w] == 1 && firsts[w].x == firsts[one].x && firsts[w].y == firsts[one].y;
+        }
+        __syncthreads();
+        if (alike) break;
+        int more;
+        const uint32_t kw = nth_largest<NT>(32, begin, end, left, is_open, [&](int m) { return word[m]; },
+                                                      &more, hist);
+        int count = 0;
+        for (int m = begin + tid; m < end; m += NT) {
+          if (!is_open(m)) continue;
+          const uint32_t k = word[m];
+          if (k > kw) take(m);
+          if (k != kw) keys[m] = 0u;
+          count += k == kw;
+        }
+        left -= more;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xFFFFFFFFu, count, o);
+        if (lane == 0) sums[warp] = count;
+        __syncthreads();
+        same = 0;
+        for (int w = 0; w < NT / 32; ++w) same += sums[w];
+        __syncthreads();
       }
-      __syncthreads();
-      int more;
-      const unsigned long long kd = nth_largest<NT, unsigned long long>(
-          64, begin, end, want, is_open, [&](int m) { return order_of(exact[m]); }, &more, hist);
-      // those above it, and of those that equal it the first ones
-      int equal = want - more;
-      for (int m0 = begin; m0 < end; m0 += NT) {
+      // of those that are equal the first ones
+      for (int m0 = begin; m0 < end && left > 0; m0 += NT) {
         const int m = m0 + tid;
-        unsigned long long k = 0;
         const bool is = m < end && is_open(m);
-        if (is) k = order_of(exact[m]);
-        if (is && k > kd) take(m);
-        const bool same = is && k == kd;
-        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, same);
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, is);
         if (lane == 0) sums[warp] = __popc(votes);
         __syncthreads();
         int before = __popc(votes & ((1u << lane) - 1u)), total = 0;
@@ -942,8 +1057,8 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
           if (w < warp) before += sums[w];
           total += sums[w];
         }
-        if (same && before < equal) take(m);
-        equal -= total;
+        if (is && before < left) take(m);
+        left -= total;
         __syncthreads();
       }
     }
@@ -988,7 +1103,7 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
 
 // Rows scored together: a chunk's share their sequence's means.
 int score_rows(int T, int S) { return T >= 4ll * S ? kTileRows : 1; }
-// Rows of a launch: at most 2^26 scores (768 MB with the second ones), and a grid's 65535.
+// Rows of a launch: at most 2^26 scores (256 MB), and a grid's 65535.
 long long select_chunk(int T, int Hkv, int M) {
   const long long rows = (1ll << 26) / (static_cast<long long>(Hkv) * M) / 8 * 8;
   return std::min<long long>(T, std::max<long long>(8, std::min<long long>(rows, 65528)));
@@ -1013,7 +1128,7 @@ size_t select_workspace(int T, int S, int Hkv, int M) {
   const long long rows = select_chunk(T, Hkv, M);
   const size_t slots = static_cast<size_t>(rows) * Hkv;
   const int parts = score_parts(rows, score_rows(T, S), Hkv, M);
-  return up256(slots * M * 4) + up256(slots * M * 8) + slots * parts * 4;
+  return up256(slots * M * 4) + slots * parts * 4;
 }
 
 bool valid_page_size(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
@@ -1180,8 +1295,7 @@ extern "C" attn_status_t attn_select_pages(const void* q, int64_t q_stride, cons
   const size_t slots = static_cast<size_t>(rows) * H_kv;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.score = reinterpret_cast<float*>(ws);
-  p.exact = reinterpret_cast<double*>(ws + up256(slots * max_pages * 4));
-  p.norm = reinterpret_cast<float*>(ws + up256(slots * max_pages * 4) + up256(slots * max_pages * 8));
+  p.norm = reinterpret_cast<float*>(ws + up256(slots * max_pages * 4));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = d == 64 ? launch_select_pages<64>(p, RT, st) : launch_select_pages<128>(p, RT, st);
   return cuda_status("attn_select_pages launch", e);

@@ -521,10 +521,12 @@ attn_status_t attn_kv_pool(const void* k_cache, int64_t k_page_stride, int kv_dt
  * them, so local_pages >= 1), and of the others the top_r with the highest score
  *   (sum of the query heads that share the K/V head) . k_means[page]
  * ("Exact Blocks, Rings, and Sparsity", sections 5 and 6, as attn_select_blocks
- * scores blocks; exact: a score's rounding decides nothing; ties to the lower
- * place, a NaN last).  q, cu_q, seq_lens and page_table as for attn_fwd_paged; a
- * row sees the pages of the tokens up to its own.  Pages given back (-1) are
- * left out.
+ * scores blocks; ties to the lower place, a NaN last).  What fp32 cannot decide is
+ * decided in whole numbers of 128 bits: a score is exact where no product of a
+ * query's element and a mean's is below 2^-60 times the largest of both, but 0 (what
+ * is lower may be left out of it), and the same products score alike in any order.
+ * q, cu_q, seq_lens and page_table as for attn_fwd_paged; a row sees the pages of
+ * the tokens up to its own.  Pages given back (-1) are left out.
  *   pages [T][H_kv][R] int32 out, R = first_pages + local_pages + top_r: the pages
  *   in ascending order of their place, then -1.  lens [T] int32 out: the tokens
  *   in them (every page but the row's own counts whole); -1 for a row of no

@@ -124,8 +124,9 @@ def select_pages(q, means, table, lens, cu, news, top, page, local, first):
     """(pages [T,Hkv,first+local+top], lens [T]) of attn_select_pages, int32 on the host: for each
     new token and K/V head the first pages, the last ones up to its own and the `top` others by the
     sum of the group's queries times the mean key, each score summed exactly (math.fsum of products
-    that 64 bits hold), ties to the lower place, a NaN last; pages of -1 are left out.  Rows of no
-    sequence have lens -1."""
+    that 64 bits hold, and of its own rest), ties to the lower place, a NaN last; pages of -1 are left
+    out.  Rows of no sequence have lens -1."""
+    import collections
     import math
 
     import torch
@@ -134,7 +135,7 @@ def select_pages(q, means, table, lens, cu, news, top, page, local, first):
     most = first + local + top
     pages = torch.full((T, Hkv, most), -1, dtype=torch.int32)
     out = torch.full((T,), -1, dtype=torch.int32)
-    qs = q.double().reshape(T, Hkv, H // Hkv, d).sum(2).cpu().numpy()
+    qs = q.double().reshape(T, Hkv, H // Hkv, d).cpu().numpy()
     for s, (n, new) in enumerate(zip(lens, news)):
         slots = table[s].tolist()
         for i in range(new):
@@ -146,11 +147,20 @@ def select_pages(q, means, table, lens, cu, news, top, page, local, first):
             for h in range(Hkv):
                 picked = rest
                 if len(rest) > top:
-                    x = means[[slots[m] for m in rest], h].double().cpu().numpy() * qs[t, h]
-                    score = ([math.fsum(row) for row in x.tolist()] if np.isfinite(x).all()
-                             else x.sum(1).tolist())
+                    mean = means[[slots[m] for m in rest], h].double().cpu().numpy()
+                    x = (mean[:, None] * qs[t, h]).reshape(len(rest), -1)
+                    if np.isfinite(x).all():
+                        # the sum, rounded, and what that leaves of it where sums are alike
+                        rows = x.tolist()
+                        score = [(math.fsum(row), 0.0) for row in rows]
+                        alike = collections.Counter(score)
+                        score = [(y, math.fsum(row + [-y]) if alike[y, 0.0] > 1 else 0.0)
+                                 for row, (y, _) in zip(rows, score)]
+                    else:
+                        score = [(y, 0.0) for y in (mean * qs[t, h].sum(0)).sum(1).tolist()]
                     order = sorted(range(len(rest)), key=lambda j: (
-                        score[j] != score[j], -score[j] if score[j] == score[j] else 0.0, j))
+                        score[j][0] != score[j][0],
+                        (-score[j][0], -score[j][1]) if score[j][0] == score[j][0] else (0.0, 0.0), j))
                     picked = [rest[j] for j in order[:top]]
                 chosen = sorted(kept + picked)
                 pages[t, h, :len(chosen)] = torch.tensor([slots[m] for m in chosen], dtype=torch.int32)

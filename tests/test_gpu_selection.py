@@ -1,9 +1,11 @@
-"""Mean keys and selected pages where they are hardest, on the GPU: sums that cancel."""
+"""Mean keys and selected pages where they are hardest, on the GPU: sums that cancel, scores
+that tie."""
 import math
 
 import pytest
 import torch
 
+from oracle.select import select_pages
 from test_gpu_paged import ints
 
 pytestmark = pytest.mark.gpu
@@ -73,3 +75,76 @@ def test_pool_of_scales_past_the_range(bss):
                      k_scale=torch.tensor([2.0 ** 120, 2.0 ** 120, 2.0 ** 110], device="cuda"))
     assert (means[0, 0] == math.inf).all() and (means[0, 1] == -math.inf).all()
     assert (means[0, 2] == 448.0 * 2.0 ** 110).all()
+
+
+# ----------------------------------------------------------------------------
+# selection
+# ----------------------------------------------------------------------------
+
+def check_selected(bss, q, means, table, lens, cu, news, top, page, local=1, first=0):
+    pages, got = bss.attn_select_pages(q, means, table, ints(lens), ints(cu), top, page, local_pages=local,
+                                       first_pages=first)
+    assert bss.attn_poll_status() == 0
+    want, n = select_pages(q, means, table, lens, cu, news, top, page, local, first)
+    assert torch.equal(pages.cpu(), want) and torch.equal(got.cpu(), n)
+    return pages
+
+
+# pages of a row: few and many that are undecided (32 are ranked at once), and more columns than a
+# table whose rows are short has
+@pytest.mark.parametrize("rows", [1, 9])
+@pytest.mark.parametrize("n", [25, 300, 2500])
+def test_products_that_cancel(bss, n, rows):
+    """Scores that only what 64 bits lose beside 2^60 tells apart."""
+    page, d = 16, 128
+    g = torch.Generator("cuda").manual_seed(n)
+    table = torch.randperm(n, generator=g, device="cuda").int()[None]
+    q = torch.zeros(rows, 2, d, device="cuda", dtype=torch.bfloat16)
+    q[:, 0, 0], q[:, 0, 32], q[:, 0, 64] = 2.0 ** 60, 1.0, -(2.0 ** 60)       # a lane's three
+    means = torch.zeros(n, 1, d, device="cuda")
+    means[:, 0, 0] = means[:, 0, 64] = 1.0
+    means[:, 0, 32] = torch.randint(-63, 64, (n,), generator=g, device="cuda").float()
+    args = [n * page - rows // 2], [0, rows], [rows]
+    for top in (1, 7, 20):
+        check_selected(bss, q, means, table, *args, top, page)
+    q = q.roll(5, -1)
+    q[:, 0, 37] = 0.0                                     # ... and lanes' sums of them
+    q[:, 1, 21] = 1.0
+    means = means.roll(5, -1)
+    means[:, 0, 21] = means[:, 0, 37]
+    for top in (1, 7):
+        check_selected(bss, q, means, table, *args, top, page)
+    # the same in the group's sum: heads of 2^60, 1 and -2^60
+    q = torch.zeros(rows, 3, d, device="cuda", dtype=torch.bfloat16)
+    q[:, 0, 3], q[:, 1, 3], q[:, 2, 3] = 2.0 ** 60, 1.0, -(2.0 ** 60)
+    means = torch.zeros(n, 1, d, device="cuda")
+    means[:, 0, 3] = torch.randint(-63, 64, (n,), generator=g, device="cuda").float()
+    for top in (1, 7):
+        check_selected(bss, q, means, table, *args, top, page)
+
+
+@pytest.mark.parametrize("rows", [1, 9])
+@pytest.mark.parametrize("n", [25, 300, 2500])
+@pytest.mark.parametrize("d,spread", [(128, 0), (128, 12), (64, 20), (128, 20)])
+def test_sums_of_the_same_numbers_tie(bss, d, spread, n, rows):
+    """Means that are one another's permutations score alike under a query of one value, in whatever
+    order they are added; the lower places are taken."""
+    page = 16
+    g = torch.Generator("cuda").manual_seed(n + d + spread)
+    table = torch.randperm(n, generator=g, device="cuda").int()[None]
+    q = torch.full((rows, 2, d), 1.375, device="cuda", dtype=torch.bfloat16)
+    x = torch.randn(d, generator=g, device="cuda")
+    x = torch.ldexp(x, torch.randint(-spread // 2, spread // 2 + 1, (d,), generator=g, device="cuda"))
+    means = torch.stack([x[torch.randperm(d, generator=g, device="cuda")] for _ in range(n)])[:, None].contiguous()
+    # (the rows end in the last page: all see the same others)
+    args = [n * page - 1], [0, rows], [rows]
+    for top in (1, 7, 20):
+        pages = check_selected(bss, q, means, table, *args, top, page)
+        assert torch.equal(pages[:, 0, :top], table[:, :top].expand(rows, -1))
+    # one of them is larger by a unit of its smallest element's last place
+    at = table[0, n * 2 // 3].item()
+    col = means[at, 0].abs().argmin()
+    means[at, 0, col] = torch.nextafter(means[at, 0, col], means.new_tensor(math.inf))
+    for top in (1, 20):
+        pages = check_selected(bss, q, means, table, *args, top, page)
+        assert (pages[:, 0, :-1] == at).any(-1).all()

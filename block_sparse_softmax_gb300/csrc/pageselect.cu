@@ -1103,10 +1103,11 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
 
 // Rows scored together: a chunk's share their sequence's means.
 int score_rows(int T, int S) { return T >= 4ll * S ? kTileRows : 1; }
-// Rows of a launch: at most 2^26 scores (256 MB), and a grid's 65535.
+// Rows of a launch: at most 2^26 scores (256 MB), or those of one row of very many
+// heads, and a grid's 65535.
 long long select_chunk(int T, int Hkv, int M) {
-  const long long rows = (1ll << 26) / (static_cast<long long>(Hkv) * M) / 8 * 8;
-  return std::min<long long>(T, std::max<long long>(8, std::min<long long>(rows, 65528)));
+  const long long rows = std::max<long long>(1, (1ll << 26) / (static_cast<long long>(Hkv) * M));
+  return std::min<long long>(T, std::min<long long>(rows < 8 ? rows : rows / 8 * 8, 65528));
 }
 int score_parts(long long rows, int RT, int Hkv, int M) {
   const long long tiles = (rows + RT - 1) / RT * Hkv;

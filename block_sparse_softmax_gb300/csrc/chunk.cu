@@ -1741,8 +1741,10 @@ extern "C" attn_status_t attn_fwd_paged(
     const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_q, void* o, float* lse,
     void* workspace, size_t workspace_bytes, int T, int S, int H, int H_kv, int d, int max_pages,
     int n_pages, int page_size, float scale, int64_t window, int64_t sinks, void* stream) {
-  attn_status_t s = check_common(S, H, T, 1, d, scale);
+  // (the sequences' rows are the batch's: one "batch" of T rows)
+  attn_status_t s = check_common(1, H, T, 1, d, scale);
   if (s != ATTN_OK) return s;
+  if (S < 1) return ATTN_ERR_INVALID_ARG;
   if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
   if (max_pages < 1 || n_pages < 1) return ATTN_ERR_INVALID_ARG;
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) || S > kMaxSeqs)

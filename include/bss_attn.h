@@ -479,8 +479,8 @@ attn_status_t attn_decode_paged(const void* q, int64_t q_stride, const void* k_c
  *   workspace: device, 16-byte aligned, >= attn_fwd_paged_workspace_bytes (it
  *   depends on none of the device's arrays; 0 for invalid arguments), contents
  *   on entry irrelevant.  Calls that can overlap need a workspace each.
- *   T >= 0, S >= 1.  The same lengths give the same bits in every run.
- *   With a window, attn_kv_evict is for after this call: a chunk's first tokens
+ *   T >= 0, S >= 1, T * H < 2^31.  The same lengths give the same bits in every
+ *   run.  With a window, attn_kv_evict is for after this call: a chunk's first tokens
  *   still see what its last one does not.
  *   Scores, maxima, sums and O are fp32, parts are joined in fp32.  The
  *   probabilities enter their product as bf16 (2^-8) over bf16 pages, as fp16

@@ -712,6 +712,10 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
 #pragma unroll 4
     for (int g = 0; g < p.G; ++g) a1 += fabsf(__bfloat162float(q_row[static_cast<long long>(g) * D + e]));
   }
+  // offsets that do not ascend (a share of them a row; no index depends on their order)
+  if (h == 0)
+    for (long long s = static_cast<long long>(r) * NT + tid; s < p.S; s += static_cast<long long>(p.rows) * NT)
+      if (__ldg(p.cu + s) > __ldg(p.cu + s + 1)) record_error(p.err, ATTN_ERR_BAD_PAGES);
   const SelectRow row = select_row(p, t, lane);
   int* out = p.pages + (static_cast<size_t>(t) * p.Hkv + h) * p.R;
   if (row.n == 0) {                                      // nobody's row (-1), or one that sees nothing

@@ -526,7 +526,8 @@ attn_status_t attn_kv_pool(const void* k_cache, int64_t k_page_stride, int kv_dt
  * query's element and a mean's is below 2^-60 times the largest of both, but 0 (what
  * is lower may be left out of it), and the same products score alike in any order.
  * q, cu_q, seq_lens and page_table as for attn_fwd_paged; a row sees the pages of
- * the tokens up to its own.  Pages given back (-1) are left out.
+ * the tokens up to its own.  Pages given back (-1) are left out.  Where cu_q does not
+ * ascend, which is reported, a row is one of some sequence or of none.
  *   pages [T][H_kv][R] int32 out, R = first_pages + local_pages + top_r: the pages
  *   in ascending order of their place, then -1.  lens [T] int32 out: the tokens
  *   in them (every page but the row's own counts whole); -1 for a row of no

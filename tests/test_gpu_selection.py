@@ -1,5 +1,5 @@
 """Mean keys and selected pages where they are hardest, on the GPU: sums that cancel, scores
-that tie."""
+that tie, offsets in disorder."""
 import math
 
 import pytest
@@ -9,6 +9,8 @@ from oracle.select import select_pages
 from test_gpu_paged import ints
 
 pytestmark = pytest.mark.gpu
+
+BAD_PAGES = 7
 
 
 @pytest.fixture(scope="module")
@@ -148,3 +150,24 @@ def test_sums_of_the_same_numbers_tie(bss, d, spread, n, rows):
     for top in (1, 20):
         pages = check_selected(bss, q, means, table, *args, top, page)
         assert (pages[:, 0, :-1] == at).any(-1).all()
+
+
+def test_selection_reports_offsets_in_disorder(bss):
+    """... as the dense layer's call does; what it writes may be handed on."""
+    page, d = 16, 64
+    table = ints([[0, 1, 2, 3]] * 4)
+    means = torch.zeros(4, 1, d, device="cuda")
+    lens = ints([60, 60, 60, 60])
+    k = torch.zeros(4, 1, page, d, device="cuda", dtype=torch.bfloat16)
+    for T in (3, 40):
+        q = torch.zeros(T, 2, d, device="cuda", dtype=torch.bfloat16)
+        for cu in ([0, 2, 1, 2, 3], [3, 2, 1, 0, 0], [0, 1, 2, 3, 2]):
+            pages, n = bss.attn_select_pages(q, means, table, lens, ints(cu), 2, page)
+            assert bss.attn_poll_status() == BAD_PAGES, cu
+            assert ((pages >= -1) & (pages < 4)).all() and ((n >= -1) & (n <= 64)).all()
+            bss.attn_decode_selected(q, k, k, pages, n)
+            torch.cuda.synchronize()
+            bss.attn_poll_status()
+        # (three of the four pages: two whole ones and the 12 tokens of the last)
+        pages, n = bss.attn_select_pages(q, means, table, lens, ints([0, 1, 1, 2, 3]), 2, page)
+        assert bss.attn_poll_status() == 0 and n[:3].tolist() == [44, 44, 44] and (n[3:] == -1).all()

@@ -1,10 +1,13 @@
-"""Mean keys and selected pages where they are hardest, on the GPU: sums that cancel, scores
-that tie, offsets in disorder."""
+"""Mean keys and selected pages where they are hardest, on the GPU: sums that cancel, scores that tie,
+the widest tables, offsets in disorder, and the attention of a sparse layer in a cache whose pages are
+shared and moved."""
 import math
+import random
 
 import pytest
 import torch
 
+from oracle import window as ref
 from oracle.select import select_pages
 from test_gpu_paged import ints
 
@@ -152,6 +155,50 @@ def test_sums_of_the_same_numbers_tie(bss, d, spread, n, rows):
         assert (pages[:, 0, :-1] == at).any(-1).all()
 
 
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("d,n", [(128, 2049), (64, 4000), (128, 4500)])
+def test_wide_tables(bss, d, n, rows):
+    """Tables of more columns than a small block picks from: ordinary scores, pages given back, ties
+    and near ties, scores that are not finite."""
+    page, top = 16, 60
+    g = torch.Generator("cuda").manual_seed(n + rows)
+    table = torch.randperm(n, generator=g, device="cuda").int()[None]
+    q = torch.randn(rows, 4, d, generator=g, device="cuda").bfloat16()
+    means = torch.randn(n, 2, d, generator=g, device="cuda")
+    few = slice(0, 1) if rows == 1 else slice(18, 21)     # rows that are looked at
+    picked = list(range(rows))[few]
+
+    def check(means, table, top, local=1, first=0, q=q):
+        pages, got = bss.attn_select_pages(q, means, table, ints([n * page - 3]), ints([0, rows]), top, page,
+                                           local_pages=local, first_pages=first)
+        assert bss.attn_poll_status() == 0
+        for r in picked:
+            end = n * page - 3 - rows + r + 1
+            want, m = select_pages(q[r:r + 1], means, table, [end], [0, 1], [1], top, page, local, first)
+            assert torch.equal(pages[r].cpu(), want[0]) and got[r].item() == m[0].item()
+
+    check(means, table, top)
+    holes = table.clone()
+    holes[0, torch.randperm(n - 9, generator=g, device="cuda")[:n // 3]] = -1
+    check(means, holes, top, 3, 2)
+    check(means, holes, n, 3, 2)                          # more than there are
+    alike = means[:1].repeat(n, 1, 1)
+    check(alike, table, top)
+    for step in (2.0 ** -23, 2.0 ** -18):
+        near = alike.clone()
+        col = torch.randint(0, d, (n,), generator=g, device="cuda")
+        near[torch.arange(n), 0, col] *= 1 + step * torch.randint(-3, 4, (n,), generator=g, device="cuda")
+        check(near, table, 1)
+        check(near, table, top)
+    check(alike, table, 7, q=q * 0)
+    odd = means.clone()
+    for x in (math.nan, math.inf, -math.inf):
+        odd[torch.randperm(n, generator=g, device="cuda")[:30], :, 3] = x
+    check(odd, table, top)
+    odd[:, :, 5] = math.nan                               # nothing but NaN: the lower places
+    check(odd, table, top)
+
+
 def test_selection_reports_offsets_in_disorder(bss):
     """... as the dense layer's call does; what it writes may be handed on."""
     page, d = 16, 64
@@ -171,3 +218,74 @@ def test_selection_reports_offsets_in_disorder(bss):
         # (three of the four pages: two whole ones and the 12 tokens of the last)
         pages, n = bss.attn_select_pages(q, means, table, lens, ints([0, 1, 1, 2, 3]), 2, page)
         assert bss.attn_poll_status() == 0 and n[:3].tolist() == [44, 44, 44] and (n[3:] == -1).all()
+
+
+# ----------------------------------------------------------------------------
+# a sparse layer
+# ----------------------------------------------------------------------------
+
+def test_a_sparse_layer_of_a_server(bss):
+    """Step after step in one cache, over forks, compaction and freed sequences: the attention of each
+    row is that over the tokens of its chosen pages, the last of them not whole."""
+    S, H, Hkv, d, page, P = 6, 8, 2, 64, 16, 300
+    G = H // Hkv
+    g = torch.Generator("cuda").manual_seed(11)
+    kc = torch.full((P, Hkv, page, d), float("nan"), device="cuda", dtype=torch.bfloat16)
+    vc = kc.clone()
+    means = torch.full((P, Hkv, d), float("nan"), device="cuda")
+    table = torch.full((S, 40), -1, dtype=torch.int32, device="cuda")
+    lens, refs = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (S, P))
+    keys = [torch.zeros(Hkv, 0, d, device="cuda", dtype=torch.float64) for _ in range(S)]
+    values = [x.clone() for x in keys]
+    rng = random.Random(6)
+    for step in range(8):
+        if step in (3, 6):                                # the second goes on as the sixth, too
+            bss.attn_kv_free(table, lens, refs, ints([5]), page)
+            src, dst = bss.attn_kv_fork(table, lens, refs, ints([1]), ints([5]), page)
+            bss.attn_kv_copy_pages(kc, vc, src, dst)
+            keys[5], values[5] = keys[1], values[1]
+        if step in (4, 7):
+            bss.attn_kv_free(table, lens, refs, ints([0]), page)
+            keys[0], values[0] = keys[0][:, :0], values[0][:, :0]
+            src, dst, count = bss.attn_kv_compact(table, refs)
+            bss.attn_kv_copy_pages(kc, vc, src, dst, count)
+            means.fill_(float("nan"))
+            bss.attn_kv_pool(kc, means, table, torch.zeros_like(lens), lens)
+        news = [rng.choice([0, 1, 5, 40, 70]) for _ in range(S)]
+        cu = [0]
+        for n in news:
+            cu.append(cu[-1] + n)
+        T = cu[-1]
+        if T == 0:
+            continue
+        q = torch.randn(T, H, d, generator=g, device="cuda").bfloat16()
+        k, v = (torch.randn(T, Hkv, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+        start = bss.attn_kv_reserve(table, lens, refs, ints(news), page)
+        bss.attn_kv_write(k, v, kc, vc, table, start, ints(cu))
+        bss.attn_kv_pool(kc, means, table, start, lens)
+        for s in range(S):
+            keys[s] = torch.cat([keys[s], k[cu[s]:cu[s + 1]].transpose(0, 1).double()], 1)
+            values[s] = torch.cat([values[s], v[cu[s]:cu[s + 1]].transpose(0, 1).double()], 1)
+        have = [x.shape[1] for x in keys]
+        pages = check_selected(bss, q, means, table, have, cu, news, 2, page, 2, 1)
+        pages, n = bss.attn_select_pages(q, means, table, lens, ints(cu), 2, page, local_pages=2, first_pages=1)
+        o, lse = bss.attn_decode_selected(q, kc, vc, pages, n)
+        assert bss.attn_poll_status() == 0
+        slots = table.tolist()
+        for t in rng.sample(range(T), min(T, 25)):
+            s = max(i for i in range(S) if cu[i] <= t)
+            own = have[s] - (cu[s + 1] - t)
+            for h in range(Hkv):
+                seen = []
+                for x in pages[t, h].tolist():
+                    if x >= 0:
+                        m = slots[s].index(x)
+                        seen += [j for j in range(m * page, (m + 1) * page) if j <= own]
+                assert len(seen) == n[t].item()
+                args = (q[t, h * G:(h + 1) * G][None, :, None], keys[s][h, seen][None, None],
+                        values[s][h, seen][None, None],
+                        torch.ones(1, len(seen), dtype=torch.bool, device="cuda"), 1.0 / math.sqrt(d))
+                O, L, _ = ref.forward(*args)
+                bo, bl = ref.forward_bounds(*args)
+                assert ((o[t, h * G:(h + 1) * G].double() - O[0, :, 0]).abs() <= bo[0, :, 0]).all(), (step, t, h)
+                assert ((lse[t, h * G:(h + 1) * G].double() - L[0, :, 0]).abs() <= bl[0, :, 0]).all(), (step, t, h)

@@ -148,7 +148,9 @@ def select_pages(q, means, table, lens, cu, news, top, page, local, first):
                 picked = rest
                 if len(rest) > top:
                     mean = means[[slots[m] for m in rest], h].double().cpu().numpy()
-                    x = (mean[:, None] * qs[t, h]).reshape(len(rest), -1)
+                    with np.errstate(invalid="ignore"):
+                        x = (mean[:, None] * qs[t, h]).reshape(len(rest), -1)
+                        total = (mean * qs[t, h].sum(0)).sum(1)
                     if np.isfinite(x).all():
                         # the sum, rounded, and what that leaves of it where sums are alike
                         rows = x.tolist()
@@ -157,7 +159,7 @@ def select_pages(q, means, table, lens, cu, news, top, page, local, first):
                         score = [(y, math.fsum(row + [-y]) if alike[y, 0.0] > 1 else 0.0)
                                  for row, (y, _) in zip(rows, score)]
                     else:
-                        score = [(y, 0.0) for y in (mean * qs[t, h].sum(0)).sum(1).tolist()]
+                        score = [(y, 0.0) for y in total.tolist()]
                     order = sorted(range(len(rest)), key=lambda j: (
                         score[j][0] != score[j][0],
                         (-score[j][0], -score[j][1]) if score[j][0] == score[j][0] else (0.0, 0.0), j))

@@ -199,6 +199,34 @@ def test_wide_tables(bss, d, n, rows):
     check(odd, table, top)
 
 
+@pytest.mark.parametrize("rows", [1, 9])
+@pytest.mark.parametrize("n", [25, 300, 2500])
+def test_scores_past_the_range(bss, n, rows):
+    """Scores that 32 bits make infinite or 0 are told apart; a query that is not finite has scores
+    that are infinite or no numbers."""
+    page, d = 16, 128
+    g = torch.Generator("cuda").manual_seed(n)
+    table = torch.randperm(n, generator=g, device="cuda").int()[None]
+    q = torch.randn(rows, 2, d, generator=g, device="cuda").bfloat16()
+    means = torch.randn(n, 1, d, generator=g, device="cuda")
+    args = [n * page - rows // 2], [0, rows], [rows]
+    for a, b in ((100, 60), (-100, -45), (-20, -120), (120, -100)):
+        for top in (1, 20):
+            check_selected(bss, torch.ldexp(q.float(), torch.tensor(a, device="cuda")).bfloat16(),
+                           torch.ldexp(means, torch.tensor(b, device="cuda")), table, *args, top, page)
+    for x in (math.inf, -math.inf, math.nan):
+        far = q.clone()
+        far[:, 1, 7] = x
+        check_selected(bss, far, means, table, *args, 20, page)
+        few = means.clone()
+        few[::3, 0, 7] = 0.0                              # infinity times 0
+        few[1::5, 0, 90] = math.inf
+        check_selected(bss, far, few, table, *args, 20, page)
+        check_selected(bss, q, few, table, *args, 20, page)
+    far[:, 1, 7], far[:, 0, 7] = math.inf, -math.inf      # ... and their sum
+    check_selected(bss, far, means, table, *args, 20, page)
+
+
 def test_selection_reports_offsets_in_disorder(bss):
     """... as the dense layer's call does; what it writes may be handed on."""
     page, d = 16, 64

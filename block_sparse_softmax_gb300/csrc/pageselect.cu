@@ -1105,8 +1105,20 @@ __global__ void __launch_bounds__(NT) select_pick_kernel(const SelectParams p) {
   }
 }
 
-// Rows scored together: a chunk's share their sequence's means.
-int score_rows(int T, int S) { return T >= 4ll * S ? kTileRows : 1; }
+// Rows scored together: those of chunks, which share their sequence's means.  (A tile
+// takes its rows' sequences one after the other.  Selections in us, row by row | tiles;
+// S sequences with `new` rows each, 4 K/V heads, d=128:
+//      pages         128              512              1024
+//      S = 1,  8     7.7 | 13.5       13.0 | 17.8      16.6 | 18.6
+//      S = 1,  32    10.7 | 17.8      17.2 | 19.4      23.6 | 20.9
+//      S = 8,  5     12.2 | 60.4      19.9 | 62.1      27.3 | 64.0
+//      S = 8,  16    17.1 | 28.8      30.4 | 30.9      47.6 | 33.0
+//      S = 8,  32    20.7 | 19.6      46.3 | 22.7      78.9 | 29.1
+//      S = 64, 5     25.8 | 76.3      58.4 | 100.3     125.9 | 169.7
+//      S = 64, 8     33.4 | 52.4      84.8 | 72.0      167.8 | 138.3
+//      S = 64, 16    60.7 | 48.8      159.6 | 95.4     293.4 | 172.8)
+constexpr int kTileRowsASeq = 16;
+int score_rows(int T, int S) { return T >= static_cast<long long>(kTileRowsASeq) * S ? kTileRows : 1; }
 // Rows of a launch: at most 2^26 scores (256 MB), or those of one row of very many
 // heads, and a grid's 65535.
 long long select_chunk(int T, int Hkv, int M) {
@@ -1138,12 +1150,21 @@ size_t select_workspace(int T, int S, int Hkv, int M) {
 
 bool valid_page_size(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 
-// A CTA of 128 threads a row and K/V head, of 1024 where the rows of the table are long.
+// Threads of a row and K/V head's CTA: 128, or 1024 where the table's rows are long and
+// either the CTAs are one a multiprocessor at most or the keys of 128 threads' CTAs
+// would fill its shared memory.  (Selections in us, 128 | 1024; `ctas` rows times heads:
+//      columns       1024            2048            4096            8192            16384
+//      ctas = 4      11.1 | 12.5     16.0 | 14.4     24.0 | 16.0     42.3 | 21.7     72.1 | 28.0
+//      ctas = 32     19.7 | 21.4     22.2 | 22.0     28.2 | 23.8     52.5 | 29.4     86.7 | 45.0
+//      ctas = 152    -               25.0 | 25.4     35.2 | 30.5     64.5 | 45.1     109 | 69
+//      ctas = 200    -               25.1 | 34.3     36.1 | 41.3     68.4 | 59.0     115 | 90
+//      ctas = 512    23.3 | 51.7     33.1 | 58.8     50.8 | 78.7     94.5 | 110      217 | 175
+//      ctas = 2000   52.2 | 163      83.2 | 196      142 | 261       275 | 377       650 | 598)
 constexpr int kLongRow = 2048;
+constexpr int kLongRowOfMany = 8192;
+constexpr int kFewPicks = 152;
 template <int D>
 cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
-  const bool many = p.M > kLongRow;
-  auto pick = many ? select_pick_kernel<D, 1024> : select_pick_kernel<D, 128>;
   const int smem = p.M * 4 + (p.M + 31) / 32 * 4;
   constexpr int kMaxDev = 64;
   static bool configured[kMaxDev] = {};
@@ -1168,18 +1189,20 @@ cudaError_t launch_select_pages(SelectParams p, int RT, cudaStream_t st) {
     if (RT == 1) select_score_kernel<D><<<grid, kScoreWarps * 32, 0, st>>>(p);
     else select_score_tile_kernel<D><<<grid, kTileThreads, ScoreTile<D>::kSmem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const bool wide = p.M > (static_cast<long long>(p.rows) * p.Hkv <= kFewPicks ? kLongRow : kLongRowOfMany);
     // the pick is set up while the scores are made, and waits for them itself
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.rows, p.Hkv);
-    cfg.blockDim = dim3(many ? 1024 : 128);
+    cfg.blockDim = dim3(wide ? 1024 : 128);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, pick, p)) != cudaSuccess) return e;
+    e = cudaLaunchKernelEx(&cfg, wide ? select_pick_kernel<D, 1024> : select_pick_kernel<D, 128>, p);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

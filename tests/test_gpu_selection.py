@@ -248,6 +248,31 @@ def test_selection_reports_offsets_in_disorder(bss):
         assert bss.attn_poll_status() == 0 and n[:3].tolist() == [44, 44, 44] and (n[3:] == -1).all()
 
 
+@pytest.mark.parametrize("news", [[100, 60], [1, 1, 70, 2, 1, 60, 3, 0, 40, 1]])
+def test_wide_tables_of_many_rows(bss, news):
+    """... and of more rows and heads than multiprocessors, of one chunk or of chunks beside single
+    tokens."""
+    page, d, n = 16, 64, 2600
+    g = torch.Generator("cuda").manual_seed(len(news))
+    S, T = len(news), sum(news)
+    table = torch.stack([torch.randperm(n, generator=g, device="cuda") for _ in range(S)]).int()
+    table[:, 5:900:7] = -1
+    means = torch.randn(n, 2, d, generator=g, device="cuda")
+    means[1::2] = means[::2]                              # ties
+    q = torch.randn(T, 2, d, generator=g, device="cuda").bfloat16()
+    cu = [0]
+    for x in news:
+        cu.append(cu[-1] + x)
+    lens = [n * page - 37 * s for s in range(S)]
+    pages, got = bss.attn_select_pages(q, means, table, ints(lens), ints(cu), 21, page, local_pages=2, first_pages=1)
+    assert bss.attn_poll_status() == 0
+    for s, new in enumerate(news):
+        for i in {0, new // 2, new - 1} if new else ():
+            t, end = cu[s] + i, lens[s] - new + i + 1
+            want, m = select_pages(q[t:t + 1], means, table[s:s + 1], [end], [0, 1], [1], 21, page, 2, 1)
+            assert torch.equal(pages[t].cpu(), want[0]) and got[t].item() == m[0].item(), (s, i)
+
+
 # ----------------------------------------------------------------------------
 # a sparse layer
 # ----------------------------------------------------------------------------

@@ -23,11 +23,12 @@
 //     counter, longest first (32 sequences of up to 8192, every fourth with 512
 //     tokens: 140 us with two kinds of pieces in no order otherwise, 120 so).  A
 //     sequence's pieces are numbered so that those that run at the same time share
-//     their keys (tiles first, then key parts): L2 serves all but one of them.  Where pieces are whole tiles, or few a CTA, those of the last
-//     turn are cut once more (4 x 1000 tokens at 16384: 473 us with all tiles in two
-//     parts, 424 with whole ones and the last 132 of 512 in four).  The parts of a
-//     tile leave (m, l, A) in the workspace, and a last kernel joins them in order
-//     (so the counter does not show in a bit).
+//     their keys (tiles first, then key parts): L2 serves all but one of them.  Where
+//     pieces are whole tiles, or few a CTA, those of the last turn are cut once more
+//     (4 x 1000 tokens at 16384: 473 us with all tiles in two parts, 424 with whole
+//     ones and the last 132 of 512 in four).  The parts of a tile leave (m, l, A) in
+//     the workspace, and a last kernel joins them in order (so the counter does not
+//     show in a bit).
 //   * e4m3 pages are read as they are.  K stays so: Q, scaled row by row by a power
 //     of two (largest element in [128, 256)), is held as two 8-bit parts, e4m3 and
 //     the rest in e5m2.  A bf16 element's 8 bits less the first part's 4 leave 3
@@ -37,11 +38,14 @@
 //     exactly, on its way through shared memory, and P carries 2^7 and is rounded
 //     to fp16, by 2^-11 (and 2^-32 of a row's largest).  With K turned into fp16,
 //     too, the turning took 5800 cycles a pair, twice the MMAs.
-//     Over bf16 pages P is rounded to bf16, V's type.
+//   * Over bf16 pages P is rounded to bf16, V's type: by 2^-8 at most (O is off from 64
+//     bits by 2.2e-3 of its rms, by its own rounding alone it would be 1.7e-3).  A
+//     second part, as attn_decode_paged has, would need 128 columns of tensor memory,
+//     which is full at d=128, and half as many MMAs again, 1024 cycles a pair.
 // Rows of the caches that hold no token may hold anything: V's are set to zero in
 // shared memory, S's are masked.
 //
-// Measured (GB300, d=128, 16 query heads on 4 K/V heads where not said; of the
+// Measured (GB300, in a graph, d=128, 16 query heads on 4 K/V heads where not said; of the
 // bf16 GEMM's 1929 TFLOP/s): 500 tokens at 8191 45 us; 32 sequences of up to 8192,
 // every fourth with 512 tokens 120 us, 51 %; 1024 tokens at 131071, 8 heads of their
 // own 376 us, 75 %, and every key from HBM once; 4 x 1000 at 16384 over e4m3 428 us,
@@ -1715,8 +1719,9 @@ cudaError_t launch_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, attn_fwd_paged_kernel<D, FP8>, tq, tk, tv, p)) != cudaSuccess) return e;
   if (p.slots == 0) return cudaSuccess;
-  // (as many as run at once: what is joined is known on the device alone, and 4576
-  // CTAs that find nothing took 4.4 us)
+  // (a tile and 16 columns a CTA, as many tiles at a time as there are multiprocessors:
+  // what is joined is known on the device alone, and 4576 CTAs that find nothing took
+  // 4.4 us)
   const long long joins = std::min<long long>(p.slots / 2, most_tiles(p.T, p.S, p.G) * p.Hkv);
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(joins, sms)), D / 16);
   cfg.blockDim = dim3(kJoinThreads);

@@ -21,6 +21,7 @@ from ._window import _is, _out, _run, _workspace
 
 KV_BF16 = 0
 KV_E4M3 = 1
+_DECODE_ROWS = 65536
 _INT, _BF16, _FP32, _E4M3 = torch.int32, torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
@@ -265,7 +266,8 @@ def attn_decode_selected(q, k_cache, v_cache, pages, lens, *, scale: Optional[fl
     """Attention of rows that read pages of their own per K/V head: O [T,H,d] bf16 and LSE [T,H]
     fp32.  Row t's query heads of K/V head h see the first lens[t] tokens of the pages
     pages[t,h,:] (attn_select_pages); a row with lens[t] < 0 is of no sequence, its rows of ``out``
-    and ``lse`` are left as they were.  q [T,H,d] bf16 (rows may be strided), T <= 65536."""
+    and ``lse`` are left as they were.  q [T,H,d] bf16 (rows may be strided).  The library takes
+    65536 rows at a time; longer batches go to it in parts, and a ``workspace`` is one for a part."""
     dev = q.get_device()
     kp, vp, ks, vs, code = _cache(k_cache, v_cache, dev)
     P, Hkv, page, d = k_cache.shape
@@ -279,6 +281,15 @@ def attn_decode_selected(q, k_cache, v_cache, pages, lens, *, scale: Optional[fl
     out, op = _out(out, "out", _BF16, (T, H, d), q)
     lse, ep = _out(lse, "lse", _FP32, (T, H), q)
     if T == 0:
+        return out, lse
+    if T > _DECODE_ROWS:
+        if workspace is None:
+            workspace = _workspace(None, _decode_bytes(_DECODE_ROWS, H, Hkv, d, M, page), q)
+        for a in range(0, T, _DECODE_ROWS):
+            b = min(T, a + _DECODE_ROWS)
+            attn_decode_selected(q[a:b], k_cache, v_cache, pages[a:b], lens[a:b], scale=scale,
+                                 k_scale=k_scale, v_scale=v_scale, workspace=workspace,
+                                 out=out[a:b], lse=lse[a:b])
         return out, lse
     wp, nbytes = None, 0
     if workspace is None:

@@ -553,7 +553,7 @@ attn_status_t attn_select_pages(const void* q, int64_t q_stride, const float* k_
  * lse, caches, scales, workspace (attn_decode_paged_workspace_bytes(T, H, H_kv,
  * d, max_pages, page_size)) and errors as for attn_decode_paged with S = T; a row
  * with lens[t] < 0 is of no sequence, its o and lse are left as they were.
- * 1 <= T <= 65536.
+ * 1 <= T <= 65536 (a longer batch, which attn_select_pages takes, in parts of rows).
  */
 attn_status_t attn_decode_selected(const void* q, int64_t q_stride, const void* k_cache,
                                    const void* v_cache, int64_t k_page_stride,

@@ -61,13 +61,12 @@
 #include <algorithm>
 #include <mutex>
 
-#include "host.cuh"
+#include "paged.cuh"
 #include "window.cuh"
 
 namespace bss {
 namespace {
 
-constexpr int kMaxSeqs = 65536;
 constexpr int kMaxGroup = 128;             // query heads of a K/V head: rows of a tile
 constexpr int kMaxParts = 152 * 8;         // parts that wait to be joined
 constexpr int kLeastPairs = 4;             // pairs of key blocks of a part at least
@@ -573,23 +572,10 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
-                                            int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
 __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {     // to L2
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
                    reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {        // the low 16 bits
-  uint32_t y;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
-  return y;
 }
 // x and y in e4m3 (the low 16 bits) and what that leaves of them in e5m2 (the high).
 __device__ __forceinline__ uint32_t two_parts(float x, float y) {
@@ -601,11 +587,6 @@ __device__ __forceinline__ uint32_t two_parts(float x, float y) {
   asm("{\n\t.reg .b16 q;\n\tcvt.rn.satfinite.e5m2x2.f32 q, %2, %1;\n\tcvt.u32.u16 %0, q;\n\t}"
       : "=r"(b) : "f"(x - f.x), "f"(y - f.y));
   return a | b << 16;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -1629,8 +1610,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
 // ----------------------------------------------------------------------------
 bool chunk_sizes(int T, int S, int H, int Hkv, int d, int max_pages, int page) {
   if (T < 1 || S < 1 || S > kMaxSeqs || max_pages < 1) return false;
-  if (page < 16 || page > 1024 || (page & (page - 1))) return false;
-  return valid_kv_heads(H, Hkv) && H / Hkv <= kMaxGroup && (d == 64 || d == 128) && static_cast<long long>(T) * H <= 0x7FFFFFFFll;
+  if (!valid_page_size(page) || !valid_kv_heads(H, Hkv) || H / Hkv > kMaxGroup) return false;
+  return (d == 64 || d == 128) && static_cast<long long>(T) * H <= 0x7FFFFFFFll;
 }
 
 // Tiles of all sequences at most, of one K/V head.
@@ -1648,25 +1629,11 @@ int most_slots(int T, int S, int Hkv, int G, int M, int page) {
   const long long tiles = most_tiles(T, S, G) * Hkv;
   return static_cast<int>(tiles >= kMaxParts ? kMaxParts : std::min<long long>(kMaxParts, tiles * cuts));
 }
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // plan | first pieces | sequences | parts
 constexpr int kMaxSms = 256;
 size_t chunk_workspace(int T, int S, int H, int Hkv, int d, int M, int page) {
   return up256(sizeof(ChunkPlan)) + kMaxSms * 4 + up256(static_cast<size_t>(S) * sizeof(ChunkSeq)) +
          static_cast<size_t>(most_slots(T, S, Hkv, H / Hkv, M, page)) * kTileM * (d + 2) * 4;
-}
-
-// K or V pages as a 3-D tensor (d, H_kv * page_size, pages) with boxes of up to 128
-// rows of a page and 128 bytes.
-attn_status_t pages_map(CUtensorMap* map, const void* ptr, int d, bool fp8, long long rows, int P,
-                        size_t page_bytes, int page) {
-  const int item = fp8 ? 1 : 2;
-  const int box = std::min(d * item, 128);
-  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows), static_cast<uint64_t>(P)};
-  const uint64_t strides[2] = {static_cast<uint64_t>(d) * item, page_bytes};
-  const uint32_t boxes[3] = {static_cast<uint32_t>(box / item), static_cast<uint32_t>(std::min(page, kTileN)), 1};
-  return make_map_tiled(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr,
-                        dims, strides, boxes, box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // The kernels' attributes, set once a device; its multiprocessors.
@@ -1752,8 +1719,7 @@ extern "C" attn_status_t attn_fwd_paged(
   if (S < 1) return ATTN_ERR_INVALID_ARG;
   if (!valid_kv_heads(H, H_kv)) return ATTN_ERR_INVALID_ARG;
   if (max_pages < 1 || n_pages < 1) return ATTN_ERR_INVALID_ARG;
-  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) || S > kMaxSeqs)
-    return ATTN_ERR_UNSUPPORTED;
+  if (!valid_page_size(page_size) || S > kMaxSeqs) return ATTN_ERR_UNSUPPORTED;
   if (kv_dtype != ATTN_KV_BF16 && kv_dtype != ATTN_KV_E4M3) return ATTN_ERR_UNSUPPORTED;
   if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return ATTN_ERR_INVALID_ARG;
   const bool fp8 = kv_dtype == ATTN_KV_E4M3;
@@ -1816,10 +1782,11 @@ extern "C" attn_status_t attn_fwd_paged(
                           CU_TENSOR_MAP_SWIZZLE_128B)) != ATTN_OK)
     return s;
   const size_t item = fp8 ? 1 : 2;
-  if ((s = pages_map(&tk, k_cache, d, fp8, rows, n_pages, static_cast<size_t>(k_page_stride) * item, page_size)) !=
+  const int box_rows = std::min(page_size, kTileN);
+  if ((s = cache_map(&tk, k_cache, d, fp8, rows, n_pages, static_cast<size_t>(k_page_stride) * item, box_rows)) !=
       ATTN_OK)
     return s;
-  if ((s = pages_map(&tv, v_cache, d, fp8, rows, n_pages, static_cast<size_t>(v_page_stride) * item, page_size)) !=
+  if ((s = cache_map(&tv, v_cache, d, fp8, rows, n_pages, static_cast<size_t>(v_page_stride) * item, box_rows)) !=
       ATTN_OK)
     return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

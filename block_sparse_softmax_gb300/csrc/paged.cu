@@ -57,15 +57,14 @@
 // warp's end, 5 us for the join and 4 us for the two launches.
 #include <algorithm>
 
-#include "host.cuh"
 #include "mma.cuh"
+#include "paged.cuh"
 
 namespace bss {
 namespace {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kMaxSeqs = 65536;
 
 struct DecodeParams {
   const __nv_bfloat16* q;
@@ -162,14 +161,6 @@ __device__ __forceinline__ int dec_off(int r, int u) {
   else return r * ROW + ((u ^ ((r >> 1) & 3)) << 4);
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
-                                            int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -178,22 +169,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// Two e4m3 elements (the low 16 bits) as a pair of fp16, which holds them all.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
-  return y;
-}
-// ... of the high 16 bits.
+// e4m3x2_f16x2 of the high 16 bits.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t x) {
   uint32_t y;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(y) : "r"(x));
   return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // P's rest beside its high half (high_bf16), of which bf16 holds all but 2^-15 of
@@ -1010,19 +990,6 @@ size_t decode_workspace(int d, int G, long long workers) {
   return static_cast<size_t>(workers) * 8 + static_cast<size_t>(workers) * 2 * decode_rows(G) * (d + 2) * 4;
 }
 
-// K or V pages as a 3-D tensor (d, H_kv * page_size, pages) with boxes of 16
-// rows of up to 128 bytes.
-attn_status_t cache_map(CUtensorMap* map, const void* ptr, int d, bool fp8, long long rows, int P,
-                        size_t page_bytes) {
-  const int item = fp8 ? 1 : 2;
-  const int box = std::min(d * item, 128);
-  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows), static_cast<uint64_t>(P)};
-  const uint64_t strides[2] = {static_cast<uint64_t>(d) * item, page_bytes};
-  const uint32_t boxes[3] = {static_cast<uint32_t>(box / item), 16, 1};
-  return make_map_tiled(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr,
-                        dims, strides, boxes, box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
 template <int D, bool FP8, int NT, bool SMALL>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, cudaStream_t st) {
   using C = DecCfg<D, FP8, NT>;
@@ -1062,7 +1029,7 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
 }
 
 bool decode_sizes(int S, int H, int Hkv, int d, int max_pages, int page) {
-  if (max_pages < 1 || page < 16 || page > 1024 || (page & (page - 1))) return false;
+  if (max_pages < 1 || !valid_page_size(page)) return false;
   if (S < 1 || H < 1 || !valid_kv_heads(H, Hkv) || (d != 64 && d != 128)) return false;
   return S <= kMaxSeqs && static_cast<long long>(S) * H <= 0x7FFFFFFFll;
 }
@@ -1093,7 +1060,7 @@ attn_status_t decode(const char* name, const void* q, int64_t q_stride, const vo
   if (S > kMaxSeqs) return ATTN_ERR_UNSUPPORTED;
   if (max_pages < 1 || n_pages < 1) return ATTN_ERR_INVALID_ARG;
   if (selected && static_cast<long long>(H_kv) * max_pages > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
-  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return ATTN_ERR_UNSUPPORTED;
+  if (!valid_page_size(page_size)) return ATTN_ERR_UNSUPPORTED;
   if (kv_dtype != ATTN_KV_BF16 && kv_dtype != ATTN_KV_E4M3) return ATTN_ERR_UNSUPPORTED;
   if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return ATTN_ERR_INVALID_ARG;
   const bool small = decode_small(S, H_kv, H / H_kv, max_pages, page_size);
@@ -1150,8 +1117,8 @@ attn_status_t decode(const char* name, const void* q, int64_t q_stride, const vo
   CUtensorMap tk, tv;
   const long long rows = static_cast<long long>(H_kv) * page_size;
   if (rows > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;     // a copy's row is an int
-  if ((s = cache_map(&tk, k_cache, d, fp8, rows, n_pages, p.k_stride)) != ATTN_OK) return s;
-  if ((s = cache_map(&tv, v_cache, d, fp8, rows, n_pages, p.v_stride)) != ATTN_OK) return s;
+  if ((s = cache_map(&tk, k_cache, d, fp8, rows, n_pages, p.k_stride, 16)) != ATTN_OK) return s;
+  if ((s = cache_map(&tv, v_cache, d, fp8, rows, n_pages, p.v_stride, 16)) != ATTN_OK) return s;
   cudaError_t e = cudaErrorInvalidValue;
 #define BSS_DECODE_CASE(DD, FP, NN, SM) \
   if (d == DD && fp8 == FP && one == (NN == 1) && small == SM) e = launch_decode<DD, FP, NN, SM>(tk, tv, p, st);

@@ -26,12 +26,11 @@
 // 2.1 TB/s, 31 %).
 #include <cuda_fp8.h>
 
-#include "host.cuh"
+#include "paged.cuh"
 
 namespace bss {
 namespace {
 
-constexpr int kMaxSeqs = 65536;      // rows of a page table (the fork kernel keeps a bit for each)
 constexpr int kMaxPages = 1 << 30;   // pages of a cache
 constexpr int kBookThreads = 1024;
 
@@ -571,7 +570,6 @@ attn_status_t allow_compact_smem() {
   return ATTN_OK;
 }
 
-bool valid_page_size(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 
 attn_status_t page_state(PageState* st, int32_t* table, int32_t* lens, int32_t* refs, int S, int M,
                          int P, int page) {

@@ -34,12 +34,11 @@
 
 #include <algorithm>
 
-#include "host.cuh"
+#include "paged.cuh"
 
 namespace bss {
 namespace {
 
-constexpr int kMaxSeqs = 65536;
 constexpr int kMaxSelectPages = 32768;        // slots of a table row: their keys fill 128 KB
 
 // ----------------------------------------------------------------------------
@@ -137,9 +136,8 @@ __device__ __noinline__ float exact_mean(const uint16_t* src, int stride, int pa
   return negative ? -f : f;
 }
 
-__device__ __forceinline__ float2 e4m3x2_f32x2(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
+__device__ __forceinline__ float2 e4m3x2_f32x2(uint32_t x) {        // the low 16 bits
+  const uint32_t y = e4m3x2_f16x2(x);
   return __half22float2(*reinterpret_cast<const __half2*>(&y));
 }
 
@@ -1131,12 +1129,11 @@ int score_parts(long long rows, int RT, int Hkv, int M) {
   const long long most = (M + pages - 1) / pages;
   return static_cast<int>(std::max<long long>(1, std::min<long long>(most, 152ll * 16 / tiles)));
 }
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 bool select_sizes(int T, int S, int H, int Hkv, int d, int M, int page, int top, int local, int first) {
   if (T < 1 || S < 1 || M < 1 || top < 0 || local < 1 || first < 0) return false;
   if (!valid_kv_heads(H, Hkv) || (d != 64 && d != 128) || S > kMaxSeqs || M > kMaxSelectPages) return false;
-  if (page < 16 || page > 1024 || (page & (page - 1))) return false;
+  if (!valid_page_size(page)) return false;
   if (H > 65535) return false;
   const long long R = static_cast<long long>(top) + local + first;
   return R <= 0x7FFFFFFFll && static_cast<long long>(T) * Hkv <= 0x7FFFFFFFll / std::max<long long>(R, 1);
@@ -1147,8 +1144,6 @@ size_t select_workspace(int T, int S, int Hkv, int M) {
   const int parts = score_parts(rows, score_rows(T, S), Hkv, M);
   return up256(slots * M * 4) + slots * parts * 4;
 }
-
-bool valid_page_size(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
 
 // Threads of a row and K/V head's CTA: 128, or 1024 where the table's rows are long and
 // either the CTAs are one a multiprocessor at most or the keys of 128 threads' CTAs

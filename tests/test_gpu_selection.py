@@ -273,6 +273,44 @@ def test_wide_tables_of_many_rows(bss, news):
             assert torch.equal(pages[t].cpu(), want[0]) and got[t].item() == m[0].item(), (s, i)
 
 
+def test_selections_on_two_streams(bss):
+    """Pooling, selection and its attention on two streams at once, in caches of their own, are what they
+    are one after the other."""
+    H, Hkv, d, page = 8, 2, 128, 16
+    steps = []
+    for i, (lens, news) in enumerate((([5000, 300, 41], [1, 200, 3]), ([2000] * 40, [1] * 40))):
+        g = torch.Generator("cuda").manual_seed(i)
+        held = [-(-n // page) for n in lens]
+        P, S = sum(held), len(lens)
+        table = torch.full((S, max(held)), -1, dtype=torch.int32, device="cuda")
+        order = torch.randperm(P, generator=g, device="cuda").int()
+        for s in range(S):
+            table[s, :held[s]] = order[sum(held[:s]):sum(held[:s + 1])]
+        k, v = (torch.randn(P, Hkv, page, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+        q = torch.randn(sum(news), H, d, generator=g, device="cuda").bfloat16()
+        cu = ints([sum(news[:s]) for s in range(S + 1)])
+        steps.append((q, k, v, torch.zeros(P, Hkv, d, device="cuda"), table, ints(lens), cu, ints([0] * S)))
+
+    def step(q, k, v, means, table, lens, cu, start):
+        bss.attn_kv_pool(k, means, table, start, lens)
+        pages, n = bss.attn_select_pages(q, means, table, lens, cu, 12, page, local_pages=2, first_pages=1)
+        return (means.clone(), pages, n) + bss.attn_decode_selected(q, k, v, pages, n)
+
+    want = [step(*x) for x in steps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(10):
+        got = []
+        for x, stream in zip(steps, streams):
+            with torch.cuda.stream(stream):
+                got.append(step(*x))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+    assert bss.attn_poll_status() == 0
+
+
 # ----------------------------------------------------------------------------
 # a sparse layer
 # ----------------------------------------------------------------------------
